@@ -284,6 +284,140 @@ msda_status msda_backward_static_workspace(msda_dtype dt, unsigned flags, int64_
                                            const void* grad_out, void* grad_value, void* grad_sampling_locations,
                                            void* grad_attention_weights, msda_stream_t stream);
 
+/*
+ * Rotary positions with several axes, alone or behind the norm of queries and
+ * keys per head, in one pass over the rows.
+ *
+ * Pair j of a row's channels turns by t_j = position[b, s, axis(j)] * frequency[j]
+ * (section[0] pairs by axis 0, then section[1] by axis 1, ...; P pairs in all):
+ *
+ *   (u, v) -> (u cos t - v sin t, v cos t + u sin t)
+ *
+ * with (u, v) = channels (j, j + P), or (2j, 2j + 1) with
+ * MSDA_ROTARY_INTERLEAVED; channels from 2P on pass through.  Angles are good
+ * to about 2^-24 at any position (the product and its reduction are carried
+ * in two binary32 numbers, or in binary64 where these do not hold it).
+ * With weights, a row x is first normed: z = x w / sqrt(mean(x^2) + eps).
+ * Sums and the rotation are in fp32, rounded once.
+ *
+ *   query [B, S, M, D], key [B, S, N, D]: rows of D contiguous elements at the
+ *       given strides (elements; batch, token, head).  N = 0: no keys.
+ *   query_weight, key_weight [D], both NULL: no norm
+ *   positions [B or 1, S, axes] dense rows of position_type (0 float32,
+ *       1 int32, 2 int64); position_stride: elements between batch items, 0 for
+ *       positions that all share.  frequencies [P] float32.
+ *   outputs [B, S, M, D] and [B, S, N, D], dense; an output may be its own input
+ *       where that is dense.
+ *
+ * Empty tensors enqueue nothing.  Requirements: D <= 256; 1..4 axes; 2P <= D.
+ * Rows of whole 16-byte vectors (and P too, in halves) at 16-byte aligned
+ * addresses and strides take the vector path, anything else the element path,
+ * with the same results up to the order of a row's sum.  The forward needs no workspace.
+ */
+typedef struct {
+    int64_t B, S, M, N, D;
+    int64_t axes, section[4];
+    int64_t query_stride[3], key_stride[3];
+    int64_t position_type, position_stride;
+} msda_rotary_problem;
+
+#define MSDA_ROTARY_INTERLEAVED 1u
+#define MSDA_ROTARY_INVERSE 2u /* turn by -t: the gradient of the rotation alone (forward entry only) */
+
+msda_status msda_norm_rotary_forward(msda_dtype dt, unsigned flags, const msda_rotary_problem* problem, double eps,
+                                     const void* positions, const float* frequencies, const void* query,
+                                     const void* key, const void* query_weight, const void* key_weight,
+                                     void* query_out, void* key_out, msda_stream_t stream);
+
+/*
+ * Gradients of the norm with rotation (weights needed).  With dz the output's
+ * gradient turned back, r = 1 / sqrt(mean(x^2) + eps) and n = x r:
+ *
+ *   grad_x = r (w dz - n mean(n w dz)),   grad_w = sum over rows of n dz
+ *
+ * grad_query_out, grad_key_out: dense, like the outputs; so are grad_query and
+ * grad_key.  The weights' gradients are summed in fp32 in an order that the
+ * sizes fix (no atomics: the same bits every run) and rounded once.
+ * workspace: msda_norm_rotary_backward_workspace_size() bytes, 16-byte aligned.
+ */
+size_t msda_norm_rotary_backward_workspace_size(const msda_rotary_problem* problem);
+msda_status msda_norm_rotary_backward(msda_dtype dt, unsigned flags, const msda_rotary_problem* problem, double eps,
+                                      const void* positions, const float* frequencies, const void* query,
+                                      const void* key, const void* query_weight, const void* key_weight,
+                                      const void* grad_query_out, const void* grad_key_out, void* grad_query,
+                                      void* grad_key, void* grad_query_weight, void* grad_key_weight, void* workspace,
+                                      size_t workspace_bytes, msda_stream_t stream);
+
+/*
+ * Dense softmax attention, the layer's attention among queries beside the
+ * sampled one:
+ *
+ *   s[i, j] = scale <query_i, key_j>   (-inf where the pair takes no part)
+ *   lse_i = log sum_j exp s[i, j],   out_i = sum_j exp(s[i, j] - lse_i) value_j
+ *
+ *   query [B, Q, M, D], key and value [B, S, N, D]: rows of D contiguous
+ *       elements at the given strides (elements; batch, row, head); M / N query
+ *       heads share a key head
+ *   key_mask [B, S] bytes, 0: the key takes no part (MSDA_ATTENTION_KEY_MASK);
+ *       rows S contiguous, key_mask_stride between batch items
+ *   mask [B or 1, M or 1, Q, S] bytes, 0: the pair takes no part
+ *       (MSDA_ATTENTION_MASK); keys contiguous, strides of batch, head, query
+ *       (0: shared)
+ *   MSDA_ATTENTION_CAUSAL: query i sees keys j <= i + S - Q
+ *   out [B, Q, M * D], lse [B, M, Q] float32 (natural logarithm), dense
+ *
+ * A row that sees no key gives out = 0 and lse = -inf and takes no part in the
+ * gradients.  A key that no query sees through key_mask or mask, and in the
+ * backward a row without keys, may hold anything, NaN included.  A NaN or
+ * infinity in a value that some query sees reaches every query whose tile of
+ * 128 keys holds it, masked or not (0 * NaN), as it does in the matrix form.
+ *
+ * Statistics, sums and products accumulate in fp32.  For fp16 / bf16 the
+ * probabilities, and in the backward the scores' gradients, are rounded to the
+ * dtype before their matrix product, as tensor-core products need.  No atomics
+ * take part in any sum: results are the same bits every run.
+ * 16-bit tensors with D a multiple of 8 and 16-byte aligned addresses and
+ * strides run on the tensor cores, others (and fp32) on the FMA pipe.
+ *
+ * Requirements: D <= 128; N divides M; scale > 0.  Q == 0 or B == 0 enqueue
+ * nothing; S == 0 writes zeros and -inf.
+ * workspace: msda_attention_forward_workspace_size() bytes (0 for many sizes:
+ * then it may be NULL), 256-byte aligned; not shared by calls that can overlap.
+ */
+typedef struct {
+    int64_t B, Q, S, M, N, D;
+    int64_t query_stride[3], key_stride[3], value_stride[3];
+    int64_t key_mask_stride, mask_stride[3];
+} msda_attention_problem;
+
+#define MSDA_ATTENTION_CAUSAL 1u
+#define MSDA_ATTENTION_KEY_MASK 2u
+#define MSDA_ATTENTION_MASK 4u
+
+size_t msda_attention_forward_workspace_size(msda_dtype dt, unsigned flags, const msda_attention_problem* problem);
+msda_status msda_attention_forward(msda_dtype dt, unsigned flags, const msda_attention_problem* problem, double scale,
+                                   const void* query, const void* key, const void* value, const uint8_t* key_mask,
+                                   const uint8_t* mask, void* out, float* lse, void* workspace, size_t workspace_bytes,
+                                   msda_stream_t stream);
+
+/*
+ * Gradients of the attention, the probabilities recomputed from lse:
+ *
+ *   p = exp(s - lse),  delta_i = <grad_out_i, out_i>,  ds = p (<grad_out_i, value_j> - delta_i)
+ *   grad_value_j = sum_i p grad_out_i,  grad_query_i = scale sum_j ds key_j,  grad_key_j = scale sum_i ds query_i
+ *
+ * out and lse: the forward's.  grad_out [B, Q, M * D] dense.  grad_query
+ * [B, Q, M, D], grad_key and grad_value [B, S, N, D], dense, overwritten; the
+ * heads that share a key head are summed in fp32.
+ * Masks and requirements as msda_attention_forward.
+ */
+size_t msda_attention_backward_workspace_size(msda_dtype dt, unsigned flags, const msda_attention_problem* problem);
+msda_status msda_attention_backward(msda_dtype dt, unsigned flags, const msda_attention_problem* problem, double scale,
+                                    const void* query, const void* key, const void* value, const uint8_t* key_mask,
+                                    const uint8_t* mask, const void* out, const float* lse, const void* grad_out,
+                                    void* grad_query, void* grad_key, void* grad_value, void* workspace,
+                                    size_t workspace_bytes, msda_stream_t stream);
+
 /* Message for the last non-OK status returned on the calling thread ("" if none). */
 const char* msda_last_error(void);
 
@@ -341,7 +475,10 @@ typedef struct {
 
 enum { MSDA_KERNEL_FORWARD = 0, MSDA_KERNEL_BACKWARD = 1, MSDA_KERNEL_ZERO = 2, MSDA_KERNEL_CONVERT = 3,
        MSDA_KERNEL_TILE_COUNT = 4, MSDA_KERNEL_TILE_SCAN = 5, MSDA_KERNEL_TILE_PLACE = 6,
-       MSDA_KERNEL_TILE_ACCUM = 7, MSDA_KERNEL_TOUCH = 8, MSDA_KERNEL_COUNT = 9 };
+       MSDA_KERNEL_TILE_ACCUM = 7, MSDA_KERNEL_TOUCH = 8,
+       MSDA_KERNEL_ROTARY = 9, MSDA_KERNEL_ROTARY_BACKWARD = 10, MSDA_KERNEL_ATTENTION = 11,
+       MSDA_KERNEL_ATTENTION_JOIN = 12, MSDA_KERNEL_ATTENTION_MASK = 13, MSDA_KERNEL_ATTENTION_PREPARE = 14,
+       MSDA_KERNEL_ATTENTION_GRAD_KEY = 15, MSDA_KERNEL_ATTENTION_GRAD_QUERY = 16, MSDA_KERNEL_COUNT = 17 };
 
 msda_status msda_trace_enable(int capacity);
 /* Pause (paused != 0) or resume recording without destroying the events:

@@ -17,6 +17,12 @@ Entry points:
 * ``multi_scale_deformable_attention_fused(...)``, ``forward_fused(...)`` /
   ``backward_fused(...)`` -- the fused operator (softmax of the attention
   logits and reference point + offset / (W, H) inside the kernels);
+* ``attention(query, key, value, mask, key_mask, causal, scale)``,
+  ``attention_forward`` / ``attention_backward`` -- dense softmax attention, a
+  layer's attention among its queries;
+* ``rotary(...)``, ``norm_rotary(...)`` and their ``_forward`` / ``_backward``
+  -- rotary positions with several axes, alone and behind the norm of queries
+  and keys per head;
 * ``device_errors()``, ``trace_enable()`` / ``trace_read()`` -- diagnostics;
 * ``reduction_ceiling()`` -- the L2's rate for the backward's reduction
   traffic, for roofline reporting.
@@ -31,10 +37,14 @@ from typing import Optional, Tuple
 import torch
 
 from . import _lib
+from ._attention import attention, attention_backward, attention_forward
 from ._lib import ACCUM, BWD_ACCUMULATE, BWD_WORKSPACE_ZEROED, MsdaError
+from ._rotary import norm_rotary, norm_rotary_backward, norm_rotary_forward, rotary, rotary_backward, rotary_forward
 
 __all__ = ["multi_scale_deformable_attention", "multi_scale_deformable_attention_fused", "forward", "backward",
            "forward_fused", "backward_fused", "workspace_size", "resolve_accum",
+           "attention", "attention_forward", "attention_backward", "rotary", "rotary_forward", "rotary_backward",
+           "norm_rotary", "norm_rotary_forward", "norm_rotary_backward",
            "device_errors", "trace_enable", "trace_pause", "trace_read", "MsdaError", "DTYPE_CODE"]
 
 DTYPE_CODE = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}

@@ -21,7 +21,17 @@ ACCUM_NAMES = {v: k for k, v in ACCUM.items()}
 BWD_ACCUMULATE = 1
 BWD_WORKSPACE_ZEROED = 2
 KERNEL_NAMES = {0: "forward", 1: "backward", 2: "zero", 3: "convert", 4: "tile_count", 5: "tile_scan",
-                6: "tile_place", 7: "tile_accum", 8: "touch_count"}
+                6: "tile_place", 7: "tile_accum", 8: "touch_count", 9: "rotary", 10: "rotary_backward", 11: "attention",
+                12: "attention_join", 13: "attention_mask", 14: "attention_prepare", 15: "attention_grad_key",
+                16: "attention_grad_query"}
+ROTARY_INTERLEAVED = 1
+ROTARY_INVERSE = 2
+ATTENTION_CAUSAL = 1
+ATTENTION_KEY_MASK = 2
+ATTENTION_MASK = 4
+# the problem structs of include/msda.h: nothing but int64 members, so a flat array lays them out
+RotaryProblem = ctypes.c_int64 * 18
+AttentionProblem = ctypes.c_int64 * 19
 
 
 class MsdaError(RuntimeError):
@@ -57,6 +67,20 @@ def _declare(lib):
     lib.msda_backward_workspace_size.restype = sz
     lib.msda_resolve_accum.argtypes = [c_int, c_int] + dims
     lib.msda_resolve_accum.restype = c_int
+    f64 = ctypes.c_double
+    lib.msda_norm_rotary_forward.argtypes = [c_int, c_uint, vp, f64] + [vp] * 9
+    lib.msda_norm_rotary_forward.restype = c_int
+    lib.msda_norm_rotary_backward.argtypes = [c_int, c_uint, vp, f64] + [vp] * 13 + [sz, vp]
+    lib.msda_norm_rotary_backward.restype = c_int
+    lib.msda_norm_rotary_backward_workspace_size.argtypes = [vp]
+    lib.msda_norm_rotary_backward_workspace_size.restype = sz
+    lib.msda_attention_forward.argtypes = [c_int, c_uint, vp, f64] + [vp] * 8 + [sz, vp]
+    lib.msda_attention_forward.restype = c_int
+    lib.msda_attention_backward.argtypes = [c_int, c_uint, vp, f64] + [vp] * 12 + [sz, vp]
+    lib.msda_attention_backward.restype = c_int
+    for f in (lib.msda_attention_forward_workspace_size, lib.msda_attention_backward_workspace_size):
+        f.argtypes = [c_int, c_uint, vp]
+        f.restype = sz
     lib.msda_last_error.restype = ctypes.c_char_p
     lib.msda_status_string.argtypes = [c_int]
     lib.msda_status_string.restype = ctypes.c_char_p

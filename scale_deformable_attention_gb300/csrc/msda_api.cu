@@ -13,7 +13,7 @@
 #include <mutex>
 #include <vector>
 
-#include "msda_internal.h"
+#include "msda_host.cuh"
 #include "msda_launch.cuh"
 
 using msda::KernelArgs;
@@ -643,6 +643,26 @@ namespace msda {
 msda_status set_error(msda_status s, const char* message) { return fail(s, "%s", message); }
 void clear_error() { g_msg[0] = 0; }
 
+int trace_begin(cudaStream_t st) { return TraceScope(st).slot; }
+void trace_end(int slot, cudaStream_t st, int kernel, int64_t work) {
+    std::lock_guard<std::mutex> lk(g_trace_mu);
+    if (slot >= (int)g_trace.kernel.size()) return;  // the trace was changed meanwhile
+    cudaEventRecord(g_trace.ev[2 * slot + 1], st);
+    g_trace.kernel[slot] = kernel;
+    g_trace.work[slot] = work;
+}
+
+msda_status device_facts(unsigned** err, int* sms) {
+    DeviceInfo* di = nullptr;
+    msda_status s = device_info(&di);
+    if (s != MSDA_OK) return s;
+    *err = di->err;
+    *sms = di->sms;
+    return MSDA_OK;
+}
+
+void* tensor_map_encoder() { return reinterpret_cast<void*>(encode_tiled()); }
+
 size_t fp32_workspace_bytes(msda_dtype dt, int64_t B, int64_t S, int64_t M, int64_t D, int64_t L, int64_t K,
                             int64_t Q, bool touch) {
     Dims d{B, S, M, D, L, K, Q, 0, 0, 0};
@@ -793,6 +813,14 @@ const char* msda_kernel_name(int k) {
     case MSDA_KERNEL_TILE_PLACE: return "tile_place";
     case MSDA_KERNEL_TILE_ACCUM: return "tile_accum";
     case MSDA_KERNEL_TOUCH: return "touch_count";
+    case MSDA_KERNEL_ROTARY: return "rotary";
+    case MSDA_KERNEL_ROTARY_BACKWARD: return "rotary_backward";
+    case MSDA_KERNEL_ATTENTION: return "attention";
+    case MSDA_KERNEL_ATTENTION_JOIN: return "attention_join";
+    case MSDA_KERNEL_ATTENTION_MASK: return "attention_mask";
+    case MSDA_KERNEL_ATTENTION_PREPARE: return "attention_prepare";
+    case MSDA_KERNEL_ATTENTION_GRAD_KEY: return "attention_grad_key";
+    case MSDA_KERNEL_ATTENTION_GRAD_QUERY: return "attention_grad_query";
     }
     return "unknown";
 }

@@ -1,0 +1,54 @@
+// msda_attention.cuh -- arguments that the attention kernels share, and the
+// element-wise tests that say which (query, key) pairs take part.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+namespace msda {
+
+constexpr int kAttnMaxChannels = 128;
+
+struct AttentionArgs {
+    const void *q, *k, *v;
+    long long q_sb, q_ss, q_sh, k_sb, k_ss, k_sh, v_sb, v_ss, v_sh;  // strides in elements: batch, row, head
+    const uint8_t* key_mask;  // [B, S] (under a mask [B|1, N|1, S]) or null: 0 = the key takes no part
+    long long km_sb, km_sh;
+    const uint8_t* mask;  // [B|1, M|1, Q, S] or null: 0 = the pair takes no part
+    long long mk_sb, mk_sh, mk_sq;
+    int B, Q, S, M, N, D;
+    int G;        // M / N query heads share a key head
+    int causal;   // query i sees keys up to i + S - Q
+    float scale;  // natural units
+    float c2;     // scale * log2(e)
+    void* out;    // [B, Q, M, D]
+    float* lse;   // [B, M, Q]
+    // a long key axis split between blocks: partial rows, then joined
+    float* part_o;    // [splits][B, M, Q][D] normalised rows
+    float* part_lse;  // [splits][B, M, Q], log2 units
+    int splits, tiles_per_split;
+    // backward
+    const void* dout;     // [B, Q, M, D]
+    const float* row_l2;  // lse * log2(e) of the kernels' rows, +inf where a row takes no part
+    const float* row_dl;  // delta = sum_d dout * out of the kernels' rows
+    const float* amax;    // fp16: largest squared norms of dout rows and of value rows (else null)
+    void *dq, *dk, *dv;   // [B, Q, M, D], [B, S, N, D], [B, S, N, D]
+    unsigned* err;
+};
+
+// Rows of the backward's per-row statistics: tiles of `rt` rows, the G query
+// heads of a key head beside one another (row = (q - tile's first) * G + g).
+struct AttentionRows {
+    int rt, qpt, tiles;  // rows a tile, queries a tile, tiles
+    int N, G;            // heads with rows of their own, heads sharing them
+};
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+__device__ __forceinline__ float attn_inf() { return __int_as_float(0x7f800000); }
+
+}  // namespace msda

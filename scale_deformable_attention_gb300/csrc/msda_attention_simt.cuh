@@ -1,0 +1,566 @@
+// msda_attention_simt.cuh -- softmax attention and its gradients on the FMA
+// pipe: every dtype, every D up to 128, every alignment.
+//
+// binary32 tensors run here whatever their size (the tensor pipe has no
+// binary32 product: its tf32 form keeps 11 bits), and 16-bit tensors whose
+// rows or strides are not made of 16-byte vectors.
+//
+// A block takes 64 rows against tiles of 64 others; 128 threads, each 8 x 4
+// scores and 8 x D/16 outputs in registers.  Per 4 channels a thread reads
+// 8 + 4 vectors of shared memory for 128 FMA: 16 shared-memory wavefronts a
+// warp against 32 FMA-pipe cycles, so the FMA pipe bounds it.  Rows are padded
+// by 4 floats: the 16 lanes that read 16 rows at one channel then hit each
+// bank once a phase.
+#pragma once
+
+#include "msda_attention.cuh"
+
+namespace msda {
+
+constexpr int kSimtThreads = 128;
+constexpr int kSimtRows = 64;
+
+template <typename T>
+__device__ __forceinline__ float attn_f32(T v) { return (float)v; }
+template <typename T>
+__device__ __forceinline__ T attn_round(float v);
+template <>
+__device__ __forceinline__ float attn_round<float>(float v) { return v; }
+template <>
+__device__ __forceinline__ __half attn_round<__half>(float v) { return __float2half_rn(v); }
+template <>
+__device__ __forceinline__ __nv_bfloat16 attn_round<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
+
+// 64 rows of D channels (rows at or above `rows`, and those `alive` says no
+// for, as zeros) into dst[64][DP + 4]; channels from D to DP are zeros.
+template <typename T, int DP>
+__device__ __forceinline__ void simt_load(float* dst, const T* src, long long stride, int rows, int D, bool vec,
+                                          const uint8_t* alive) {
+    constexpr int LD = DP + 4;
+    if constexpr (sizeof(T) == 4) {
+        if (vec) {
+            for (int i = threadIdx.x; i < kSimtRows * (DP / 4); i += kSimtThreads) {
+                const int r = i / (DP / 4), c = (i - r * (DP / 4)) * 4;
+                float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (r < rows && c < D && (!alive || alive[r])) v = *reinterpret_cast<const float4*>(src + r * stride + c);
+                *reinterpret_cast<float4*>(dst + r * LD + c) = v;
+            }
+            return;
+        }
+    }
+    for (int i = threadIdx.x; i < kSimtRows * DP; i += kSimtThreads) {
+        const int r = i / DP, c = i - r * DP;
+        dst[r * LD + c] = r < rows && c < D && (!alive || alive[r]) ? attn_f32(src[r * stride + c]) : 0.f;
+    }
+}
+
+// acc[i][c] += sum_d A[ty*8+i][d] B[tx+16c][d]
+template <int DP>
+__device__ __forceinline__ void simt_nt(float (&acc)[8][4], const float* A, const float* B, int tx, int ty) {
+    constexpr int LD = DP + 4;
+#pragma unroll 2
+    for (int d = 0; d < DP; d += 4) {
+        float4 a[8], b[4];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) a[i] = *reinterpret_cast<const float4*>(A + (ty * 8 + i) * LD + d);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) b[c] = *reinterpret_cast<const float4*>(B + (tx + 16 * c) * LD + d);
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                acc[i][c] = fmaf(a[i].x, b[c].x, acc[i][c]);
+                acc[i][c] = fmaf(a[i].y, b[c].y, acc[i][c]);
+                acc[i][c] = fmaf(a[i].z, b[c].z, acc[i][c]);
+                acc[i][c] = fmaf(a[i].w, b[c].w, acc[i][c]);
+            }
+    }
+}
+
+constexpr int kSimtLdP = 64 + 4;
+
+// acc[i][c] += sum_k P[ty*8+i][k] X[k][tx+16c]
+template <int DP>
+__device__ __forceinline__ void simt_nn(float (&acc)[8][DP / 16], const float* P, const float* X, int tx, int ty) {
+    constexpr int LD = DP + 4;
+#pragma unroll 2
+    for (int k = 0; k < 64; k += 4) {
+        float4 p[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) p[i] = *reinterpret_cast<const float4*>(P + (ty * 8 + i) * kSimtLdP + k);
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk) {
+            float x[DP / 16];
+#pragma unroll
+            for (int c = 0; c < DP / 16; ++c) x[c] = X[(k + kk) * LD + tx + 16 * c];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float pv = kk == 0 ? p[i].x : kk == 1 ? p[i].y : kk == 2 ? p[i].z : p[i].w;
+#pragma unroll
+                for (int c = 0; c < DP / 16; ++c) acc[i][c] = fmaf(pv, x[c], acc[i][c]);
+            }
+        }
+    }
+}
+
+// acc[i][c] += sum_q P[q][ty*8+i] X[q][tx+16c]
+template <int DP>
+__device__ __forceinline__ void simt_tn(float (&acc)[8][DP / 16], const float* P, const float* X, int tx, int ty) {
+    constexpr int LD = DP + 4;
+#pragma unroll 4
+    for (int q = 0; q < 64; ++q) {
+        const float4 p0 = *reinterpret_cast<const float4*>(P + q * kSimtLdP + ty * 8);
+        const float4 p1 = *reinterpret_cast<const float4*>(P + q * kSimtLdP + ty * 8 + 4);
+        const float p[8] = {p0.x, p0.y, p0.z, p0.w, p1.x, p1.y, p1.z, p1.w};
+#pragma unroll
+        for (int c = 0; c < DP / 16; ++c) {
+            const float x = X[q * LD + tx + 16 * c];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) acc[i][c] = fmaf(p[i], x, acc[i][c]);
+        }
+    }
+}
+
+// Scores in log2 units of the block's rows q0 + ty*8 + i and keys j0 + tx + 16c; -inf where the pair takes no part.
+__device__ __forceinline__ void simt_mask(float (&s)[8][4], const AttentionArgs& a, int b, int m, int q0, int j0, int tx,
+                                          int ty) {
+    const uint8_t* km = a.key_mask ? a.key_mask + b * a.km_sb + (m / a.G) * a.km_sh : nullptr;
+    const uint8_t* mk = a.mask ? a.mask + b * a.mk_sb + m * a.mk_sh : nullptr;
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+        const int j = j0 + tx + 16 * c;
+        const bool in = j < a.S && (!km || km[j]);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int q = q0 + ty * 8 + i;
+            bool ok = in && q < a.Q;
+            if (a.causal) ok = ok && j <= q + (a.S - a.Q);
+            if (mk && ok) ok = mk[q * a.mk_sq + j] != 0;
+            s[i][c] = ok ? s[i][c] * a.c2 : -attn_inf();
+        }
+    }
+}
+
+__device__ __forceinline__ float half_warp_max(float v) {
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+    return v;
+}
+__device__ __forceinline__ float half_warp_sum(float v) {
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+}
+
+// Tiles of 64 keys that rows q0 .. q0+63 can see.
+__device__ __forceinline__ int simt_key_tiles(const AttentionArgs& a, int q0) {
+    long long last = a.S;
+    if (a.causal) {
+        const long long see = (long long)min(q0 + kSimtRows, a.Q) + (a.S - a.Q);
+        last = see < 0 ? 0 : see < a.S ? see : a.S;
+    }
+    return (int)((last + 63) / 64);
+}
+
+// Forward: running maximum m and sum l of each row, O rescaled when m grows.
+template <typename T, int DP>
+__global__ void __launch_bounds__(kSimtThreads) msda_attention_simt_kernel(const AttentionArgs a, bool vec) {
+    extern __shared__ __align__(16) float simt_smem[];
+    constexpr int LD = DP + 4;
+    float* Qs = simt_smem;
+    float* Xs = Qs + kSimtRows * LD;  // keys, then values
+    float* Ps = Xs + kSimtRows * LD;
+    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+    const int qtiles = (a.Q + kSimtRows - 1) / kSimtRows;
+    long long id = blockIdx.x;
+    const int split = (int)(id % a.splits);
+    id /= a.splits;
+    const int q0 = (int)(id % qtiles) * kSimtRows;
+    id /= qtiles;
+    const int m = (int)(id % a.M), b = (int)(id / a.M), n = m / a.G;
+    const T* q = static_cast<const T*>(a.q) + b * a.q_sb + m * a.q_sh + q0 * a.q_ss;
+    const T* k = static_cast<const T*>(a.k) + b * a.k_sb + n * a.k_sh;
+    const T* v = static_cast<const T*>(a.v) + b * a.v_sb + n * a.v_sh;
+    const uint8_t* km = a.key_mask ? a.key_mask + b * a.km_sb + n * a.km_sh : nullptr;
+    simt_load<T, DP>(Qs, q, a.q_ss, a.Q - q0, a.D, vec, nullptr);
+    float o[8][DP / 16], mx[8], l[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        mx[i] = -attn_inf(), l[i] = 0.f;
+#pragma unroll
+        for (int c = 0; c < DP / 16; ++c) o[i][c] = 0.f;
+    }
+    const int t0 = split * a.tiles_per_split;
+    const int t1 = min(simt_key_tiles(a, q0), t0 + a.tiles_per_split);
+    for (int t = t0; t < t1; ++t) {
+        const int j0 = t * 64;
+        __syncthreads();
+        simt_load<T, DP>(Xs, k + j0 * a.k_ss, a.k_ss, a.S - j0, a.D, vec, km ? km + j0 : nullptr);
+        __syncthreads();
+        float s[8][4] = {};
+        simt_nt<DP>(s, Qs, Xs, tx, ty);
+        simt_mask(s, a, b, m, q0, j0, tx, ty);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float top = fmaxf(mx[i], half_warp_max(fmaxf(fmaxf(s[i][0], s[i][1]), fmaxf(s[i][2], s[i][3]))));
+            const float ref = top == -attn_inf() ? 0.f : top;  // a row that has seen nothing yet
+            const float f = exp2f(mx[i] - ref);
+            float sum = 0.f;
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                const float p = exp2f(s[i][c] - ref);
+                sum += p;
+                Ps[(ty * 8 + i) * kSimtLdP + tx + 16 * c] = p;
+            }
+            l[i] = l[i] * f + half_warp_sum(sum);
+            mx[i] = top;
+#pragma unroll
+            for (int c = 0; c < DP / 16; ++c) o[i][c] *= f;
+        }
+        __syncthreads();
+        simt_load<T, DP>(Xs, v + j0 * a.v_ss, a.v_ss, a.S - j0, a.D, vec, km ? km + j0 : nullptr);
+        __syncthreads();
+        simt_nn<DP>(o, Ps, Xs, tx, ty);
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int qi = q0 + ty * 8 + i;
+        if (qi >= a.Q) continue;
+        const float inv = l[i] == 0.f ? 0.f : 1.f / l[i];
+        const float l2 = l[i] == 0.f ? -attn_inf() : mx[i] + log2f(l[i]);
+        const long long row = ((long long)b * a.M + m) * a.Q + qi;
+        if (a.splits > 1) {
+            const long long at = (long long)split * a.B * a.M * a.Q + row;
+#pragma unroll
+            for (int c = 0; c < DP / 16; ++c) {
+                const int d = tx + 16 * c;
+                if (d < a.D) a.part_o[at * a.D + d] = o[i][c] * inv;
+            }
+            if (tx == 0) a.part_lse[at] = l2;
+        } else {
+            T* out = static_cast<T*>(a.out) + (((long long)b * a.Q + qi) * a.M + m) * a.D;
+#pragma unroll
+            for (int c = 0; c < DP / 16; ++c) {
+                const int d = tx + 16 * c;
+                if (d < a.D) out[d] = attn_round<T>(o[i][c] * inv);
+            }
+            if (tx == 0) a.lse[row] = l2 * kLn2;
+        }
+    }
+}
+
+// p and ds of a tile: s in, on return s = p and dp = p (dp - delta), each 0
+// where the pair takes no part.  Rows' statistics: l2 (+inf: no part), dl.
+__device__ __forceinline__ void simt_prob_grad(float (&s)[8][4], float (&dp)[8][4], const float* l2, const float* dl) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            const float p = s[i][c] == -attn_inf() ? 0.f : exp2f(s[i][c] - l2[i]);
+            s[i][c] = p;
+            dp[i][c] = p == 0.f ? 0.f : p * (dp[i][c] - dl[i]);
+        }
+}
+
+// Gradients of 64 keys and values of one key head: over all queries of the
+// heads that share it, so the sums over shared heads stay in registers.
+template <typename T, int DP>
+__global__ void __launch_bounds__(kSimtThreads) msda_attention_simt_grad_key_kernel(const AttentionArgs a,
+                                                                                    const AttentionRows rw, bool vec) {
+    extern __shared__ __align__(16) float simt_smem[];
+    constexpr int LD = DP + 4;
+    float* Ks = simt_smem;
+    float* Vs = Ks + kSimtRows * LD;
+    float* Qs = Vs + kSimtRows * LD;
+    float* Gs = Qs + kSimtRows * LD;
+    float* Ps = Gs + kSimtRows * LD;  // p, then ds
+    uint8_t* live = reinterpret_cast<uint8_t*>(Ps + kSimtRows * kSimtLdP);  // rows of the query tile that take part
+    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+    const int ktiles = (a.S + 63) / 64;
+    long long id = blockIdx.x;
+    const int j0 = (int)(id % ktiles) * 64;
+    id /= ktiles;
+    const int n = (int)(id % a.N), b = (int)(id / a.N);
+    const T* k = static_cast<const T*>(a.k) + b * a.k_sb + n * a.k_sh + j0 * a.k_ss;
+    const T* v = static_cast<const T*>(a.v) + b * a.v_sb + n * a.v_sh + j0 * a.v_ss;
+    const uint8_t* km = a.key_mask ? a.key_mask + b * a.km_sb + n * a.km_sh + j0 : nullptr;
+    simt_load<T, DP>(Ks, k, a.k_ss, a.S - j0, a.D, vec, km);
+    simt_load<T, DP>(Vs, v, a.v_ss, a.S - j0, a.D, vec, km);
+    float dk[8][DP / 16] = {}, dv[8][DP / 16] = {};
+    // causal: queries below j0 - (S - Q) see none of these keys
+    long long first = a.causal ? (long long)j0 - (a.S - a.Q) : 0;
+    if (first < 0) first = 0;
+    for (int g = 0; g < a.G; ++g) {
+        const int m = n * a.G + g;
+        for (int q0 = (int)(first / 64) * 64; q0 < a.Q; q0 += 64) {
+            const float* l2p = a.row_l2 + ((long long)(b * rw.N + m) * rw.tiles + q0 / 64) * 64;
+            const float* dlp = a.row_dl + ((long long)(b * rw.N + m) * rw.tiles + q0 / 64) * 64;
+            __syncthreads();
+            if (threadIdx.x < 64) live[threadIdx.x] = l2p[threadIdx.x] != attn_inf();
+            __syncthreads();
+            simt_load<T, DP>(Qs, static_cast<const T*>(a.q) + b * a.q_sb + m * a.q_sh + q0 * a.q_ss, a.q_ss, a.Q - q0,
+                             a.D, vec, live);
+            simt_load<T, DP>(Gs, static_cast<const T*>(a.dout) + (((long long)b * a.Q + q0) * a.M + m) * a.D,
+                             (long long)a.M * a.D, a.Q - q0, a.D, vec, live);
+            __syncthreads();
+            float s[8][4] = {}, dp[8][4] = {}, l2[8], dl[8];
+            simt_nt<DP>(s, Qs, Ks, tx, ty);
+            simt_nt<DP>(dp, Gs, Vs, tx, ty);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) l2[i] = l2p[ty * 8 + i], dl[i] = dlp[ty * 8 + i];
+            simt_mask(s, a, b, m, q0, j0, tx, ty);
+            simt_prob_grad(s, dp, l2, dl);
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+#pragma unroll
+                for (int c = 0; c < 4; ++c) Ps[(ty * 8 + i) * kSimtLdP + tx + 16 * c] = s[i][c];
+            __syncthreads();
+            simt_tn<DP>(dv, Ps, Gs, tx, ty);
+            __syncthreads();
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+#pragma unroll
+                for (int c = 0; c < 4; ++c) Ps[(ty * 8 + i) * kSimtLdP + tx + 16 * c] = dp[i][c];
+            __syncthreads();
+            simt_tn<DP>(dk, Ps, Qs, tx, ty);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int j = j0 + ty * 8 + i;
+        if (j >= a.S) continue;
+        const long long at = (((long long)b * a.S + j) * a.N + n) * a.D;
+#pragma unroll
+        for (int c = 0; c < DP / 16; ++c) {
+            const int d = tx + 16 * c;
+            if (d < a.D) {
+                static_cast<T*>(a.dk)[at + d] = attn_round<T>(dk[i][c] * a.scale);
+                static_cast<T*>(a.dv)[at + d] = attn_round<T>(dv[i][c]);
+            }
+        }
+    }
+}
+
+// Gradient of 64 queries of one head: over the keys that they see.
+template <typename T, int DP>
+__global__ void __launch_bounds__(kSimtThreads) msda_attention_simt_grad_query_kernel(const AttentionArgs a,
+                                                                                      const AttentionRows rw, bool vec) {
+    extern __shared__ __align__(16) float simt_smem[];
+    constexpr int LD = DP + 4;
+    float* Qs = simt_smem;
+    float* Gs = Qs + kSimtRows * LD;
+    float* Ks = Gs + kSimtRows * LD;
+    float* Vs = Ks + kSimtRows * LD;
+    float* Ps = Vs + kSimtRows * LD;
+    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+    const int qtiles = (a.Q + 63) / 64;
+    long long id = blockIdx.x;
+    const int q0 = (int)(id % qtiles) * 64;
+    id /= qtiles;
+    const int m = (int)(id % a.M), b = (int)(id / a.M), n = m / a.G;
+    const T* k = static_cast<const T*>(a.k) + b * a.k_sb + n * a.k_sh;
+    const T* v = static_cast<const T*>(a.v) + b * a.v_sb + n * a.v_sh;
+    const uint8_t* km = a.key_mask ? a.key_mask + b * a.km_sb + n * a.km_sh : nullptr;
+    simt_load<T, DP>(Qs, static_cast<const T*>(a.q) + b * a.q_sb + m * a.q_sh + q0 * a.q_ss, a.q_ss, a.Q - q0, a.D, vec,
+                     nullptr);
+    simt_load<T, DP>(Gs, static_cast<const T*>(a.dout) + (((long long)b * a.Q + q0) * a.M + m) * a.D,
+                     (long long)a.M * a.D, a.Q - q0, a.D, vec, nullptr);
+    float l2[8], dl[8], dq[8][DP / 16] = {};
+    const long long at0 = ((long long)(b * rw.N + m) * rw.tiles + q0 / 64) * 64;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) l2[i] = a.row_l2[at0 + ty * 8 + i], dl[i] = a.row_dl[at0 + ty * 8 + i];
+    const int tiles = simt_key_tiles(a, q0);
+    for (int t = 0; t < tiles; ++t) {
+        const int j0 = t * 64;
+        __syncthreads();
+        simt_load<T, DP>(Ks, k + j0 * a.k_ss, a.k_ss, a.S - j0, a.D, vec, km ? km + j0 : nullptr);
+        simt_load<T, DP>(Vs, v + j0 * a.v_ss, a.v_ss, a.S - j0, a.D, vec, km ? km + j0 : nullptr);
+        __syncthreads();
+        float s[8][4] = {}, dp[8][4] = {};
+        simt_nt<DP>(s, Qs, Ks, tx, ty);
+        simt_nt<DP>(dp, Gs, Vs, tx, ty);
+        simt_mask(s, a, b, m, q0, j0, tx, ty);
+        simt_prob_grad(s, dp, l2, dl);
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) Ps[(ty * 8 + i) * kSimtLdP + tx + 16 * c] = dp[i][c];
+        __syncthreads();
+        simt_nn<DP>(dq, Ps, Ks, tx, ty);
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int qi = q0 + ty * 8 + i;
+        if (qi >= a.Q) continue;
+        T* out = static_cast<T*>(a.dq) + (((long long)b * a.Q + qi) * a.M + m) * a.D;
+#pragma unroll
+        for (int c = 0; c < DP / 16; ++c) {
+            const int d = tx + 16 * c;
+            if (d < a.D) out[d] = attn_round<T>(dq[i][c] * a.scale);
+        }
+    }
+}
+
+// Joins the rows of a split key axis: out = sum_i 2^(lse_i - lse) o_i.  A warp a row.
+template <typename T>
+__global__ void __launch_bounds__(128) msda_attention_join_kernel(const AttentionArgs a) {
+    const long long rows = (long long)a.B * a.M * a.Q;
+    const long long row = (long long)blockIdx.x * 4 + (threadIdx.x >> 5);
+    if (row >= rows) return;
+    const int lane = threadIdx.x & 31;
+    float top = -attn_inf();
+    for (int i = lane; i < a.splits; i += 32) {
+        const float x = a.part_lse[i * rows + row];
+        top = x != x ? x : fmaxf(top, x);
+    }
+    for (int o = 16; o > 0; o >>= 1) {
+        const float x = __shfl_xor_sync(0xffffffffu, top, o);
+        top = x != x ? x : top != top ? top : fmaxf(top, x);
+    }
+    const float ref = top == -attn_inf() ? 0.f : top;
+    float sum = 0.f, o[kAttnMaxChannels / 32] = {};
+    for (int i = 0; i < a.splits; ++i) {
+        const float w = exp2f(a.part_lse[i * rows + row] - ref);
+        sum += w;
+        const float* p = a.part_o + (i * rows + row) * a.D;
+#pragma unroll
+        for (int c = 0; c < kAttnMaxChannels / 32; ++c)
+            if (lane + 32 * c < a.D) o[c] = fmaf(w, p[lane + 32 * c], o[c]);
+    }
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    const long long bm = row / a.Q;
+    const int q = (int)(row - bm * a.Q);
+    const long long b = bm / a.M;
+    const int m = (int)(bm - b * a.M);
+    T* out = static_cast<T*>(a.out) + ((b * a.Q + q) * a.M + m) * a.D;
+#pragma unroll
+    for (int c = 0; c < kAttnMaxChannels / 32; ++c)
+        if (lane + 32 * c < a.D) out[lane + 32 * c] = attn_round<T>(o[c] * inv);
+    if (lane == 0) a.lse[row] = sum == 0.f ? -attn_inf() : (ref + log2f(sum)) * kLn2;
+}
+
+// Statistics of the backward's rows: lse in log2 units (+inf where the row
+// takes no part or is padding) and delta = <dout, out>.  Eight lanes a row.
+template <typename T>
+__global__ void __launch_bounds__(256) msda_attention_prepare_kernel(const AttentionArgs a, const AttentionRows rw,
+                                                                     const void* out_, const float* lse, float* l2,
+                                                                     float* dl) {
+    const long long total = (long long)a.B * rw.N * rw.tiles * rw.rt;
+    const int lane = threadIdx.x & 7;
+    for (long long i = (long long)blockIdx.x * 32 + (threadIdx.x >> 3); i < (total + 3) / 4 * 4; i += (long long)gridDim.x * 32) {
+        const long long bt = i / rw.rt;
+        const int r = (int)(i - bt * rw.rt);
+        const long long bn = bt / rw.tiles;
+        const int q = (int)(bt - bn * rw.tiles) * rw.qpt + r / rw.G;
+        const int b = (int)(bn / rw.N), m = (int)(bn - (long long)b * rw.N) * rw.G + r % rw.G;
+        bool on = i < total && r < rw.qpt * rw.G && q < a.Q;
+        float x = on ? lse[((long long)b * a.M + m) * a.Q + q] : -attn_inf();
+        on = on && x != -attn_inf();
+        float d = 0.f;
+        if (on) {
+            const long long at = (((long long)b * a.Q + q) * a.M + m) * a.D;
+            const T* g = static_cast<const T*>(a.dout) + at;
+            const T* o = static_cast<const T*>(out_) + at;
+            for (int c = lane; c < a.D; c += 8) d = fmaf(attn_f32(g[c]), attn_f32(o[c]), d);
+        }
+        for (int s = 4; s > 0; s >>= 1) d += __shfl_xor_sync(0xffffffffu, d, s);
+        if (lane == 0 && i < total) {
+            l2[i] = on ? x * kLog2e : attn_inf();
+            dl[i] = on ? d : 0.f;
+        }
+    }
+}
+
+// Launches for dtype T (each in its own translation unit).
+template <typename T>
+cudaError_t launch_attention_simt(const AttentionArgs& a, bool vec, cudaStream_t st);
+template <typename T>
+cudaError_t launch_attention_simt_grad_key(const AttentionArgs& a, const AttentionRows& rw, bool vec, cudaStream_t st);
+template <typename T>
+cudaError_t launch_attention_simt_grad_query(const AttentionArgs& a, const AttentionRows& rw, bool vec, cudaStream_t st);
+template <typename T>
+cudaError_t launch_attention_join(const AttentionArgs& a, cudaStream_t st);
+template <typename T>
+cudaError_t launch_attention_prepare(const AttentionArgs& a, const AttentionRows& rw, const void* out, const float* lse,
+                                     float* l2, float* dl, cudaStream_t st);
+
+#ifdef MSDA_ATTENTION_SIMT_INSTANTIATE
+// head channels padded to a multiple of the 16 lanes that share a row
+#define MSDA_SIMT_BY_D(D, GO) \
+    do {                      \
+        if ((D) <= 32) GO(32); \
+        else if ((D) <= 48) GO(48); \
+        else if ((D) <= 64) GO(64); \
+        else if ((D) <= 96) GO(96); \
+        else GO(128);         \
+    } while (0)
+
+template <typename T, int DP>
+static cudaError_t simt_go(const AttentionArgs& a, bool vec, cudaStream_t st) {
+    const size_t smem = (size_t)(2 * kSimtRows * (DP + 4) + kSimtRows * kSimtLdP) * 4;
+    cudaError_t e = cudaFuncSetAttribute(msda_attention_simt_kernel<T, DP>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    const long long grid = (long long)a.B * a.M * ((a.Q + 63) / 64) * a.splits;
+    msda_attention_simt_kernel<T, DP><<<(unsigned)grid, kSimtThreads, smem, st>>>(a, vec);
+    return cudaGetLastError();
+}
+template <typename T, int DP>
+static cudaError_t simt_grad_key_go(const AttentionArgs& a, const AttentionRows& rw, bool vec, cudaStream_t st) {
+    const size_t smem = (size_t)(4 * kSimtRows * (DP + 4) + kSimtRows * kSimtLdP + 16) * 4;
+    cudaError_t e = cudaFuncSetAttribute(msda_attention_simt_grad_key_kernel<T, DP>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    const long long grid = (long long)a.B * a.N * ((a.S + 63) / 64);
+    msda_attention_simt_grad_key_kernel<T, DP><<<(unsigned)grid, kSimtThreads, smem, st>>>(a, rw, vec);
+    return cudaGetLastError();
+}
+template <typename T, int DP>
+static cudaError_t simt_grad_query_go(const AttentionArgs& a, const AttentionRows& rw, bool vec, cudaStream_t st) {
+    const size_t smem = (size_t)(4 * kSimtRows * (DP + 4) + kSimtRows * kSimtLdP) * 4;
+    cudaError_t e = cudaFuncSetAttribute(msda_attention_simt_grad_query_kernel<T, DP>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    const long long grid = (long long)a.B * a.M * ((a.Q + 63) / 64);
+    msda_attention_simt_grad_query_kernel<T, DP><<<(unsigned)grid, kSimtThreads, smem, st>>>(a, rw, vec);
+    return cudaGetLastError();
+}
+template <typename T>
+cudaError_t launch_attention_simt(const AttentionArgs& a, bool vec, cudaStream_t st) {
+#define MSDA_GO(DP) return simt_go<T, DP>(a, vec, st)
+    MSDA_SIMT_BY_D(a.D, MSDA_GO);
+#undef MSDA_GO
+}
+template <typename T>
+cudaError_t launch_attention_simt_grad_key(const AttentionArgs& a, const AttentionRows& rw, bool vec, cudaStream_t st) {
+#define MSDA_GO(DP) return simt_grad_key_go<T, DP>(a, rw, vec, st)
+    MSDA_SIMT_BY_D(a.D, MSDA_GO);
+#undef MSDA_GO
+}
+template <typename T>
+cudaError_t launch_attention_simt_grad_query(const AttentionArgs& a, const AttentionRows& rw, bool vec, cudaStream_t st) {
+#define MSDA_GO(DP) return simt_grad_query_go<T, DP>(a, rw, vec, st)
+    MSDA_SIMT_BY_D(a.D, MSDA_GO);
+#undef MSDA_GO
+}
+template <typename T>
+cudaError_t launch_attention_join(const AttentionArgs& a, cudaStream_t st) {
+    const long long rows = (long long)a.B * a.M * a.Q;
+    msda_attention_join_kernel<T><<<(unsigned)((rows + 3) / 4), 128, 0, st>>>(a);
+    return cudaGetLastError();
+}
+template <typename T>
+cudaError_t launch_attention_prepare(const AttentionArgs& a, const AttentionRows& rw, const void* out, const float* lse,
+                                     float* l2, float* dl, cudaStream_t st) {
+    const long long blocks = ((long long)a.B * rw.N * rw.tiles * rw.rt + 31) / 32;
+    const unsigned grid = (unsigned)(blocks < 152 * 32 ? blocks : 152 * 32);
+    msda_attention_prepare_kernel<T><<<grid, 256, 0, st>>>(a, rw, out, lse, l2, dl);
+    return cudaGetLastError();
+}
+#define MSDA_SIMT_INSTANCES(T)                                                                                          \
+    template cudaError_t launch_attention_simt<T>(const AttentionArgs&, bool, cudaStream_t);                            \
+    template cudaError_t launch_attention_simt_grad_key<T>(const AttentionArgs&, const AttentionRows&, bool, cudaStream_t); \
+    template cudaError_t launch_attention_simt_grad_query<T>(const AttentionArgs&, const AttentionRows&, bool, cudaStream_t); \
+    template cudaError_t launch_attention_join<T>(const AttentionArgs&, cudaStream_t);                                  \
+    template cudaError_t launch_attention_prepare<T>(const AttentionArgs&, const AttentionRows&, const void*,           \
+                                                     const float*, float*, float*, cudaStream_t);
+#endif
+
+}  // namespace msda
