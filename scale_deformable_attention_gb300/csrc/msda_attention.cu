@@ -1,5 +1,7 @@
 // msda_attention.cu -- host side of msda_attention_forward / _backward:
 // checks, workspace layout, choice of kernels, launches.
+#include <cuda.h>
+#include <cudaTypedefs.h>
 #include <cuda_runtime.h>
 
 #include <cmath>
@@ -7,31 +9,48 @@
 
 #include "msda_attention.cuh"
 #include "msda_attention_simt.cuh"
+#include "msda_attention_tc_host.cuh"
 #include "msda_host.cuh"
 
 namespace msda {
 
-// Keys that some query of the heads sharing them may see, as bytes
-// [LB][LN][S] (cleared before): a key outside it may hold anything, NaN too.
-// Blocks of 256 keys and 64 queries; every writer writes the same 1.
-__global__ void __launch_bounds__(256) msda_attention_live_kernel(const uint8_t* mask, long long mk_sb, long long mk_sh,
+// One pass over a mask of bytes [Bm, Mm, Q, S].  Writes
+//   live [LB, LN, S] bytes (cleared before): 1 where some query of the heads that
+//     share the key sees it; a key outside it may hold anything, NaN too (every
+//     writer of a byte writes the same 1);
+//   bits [Bm, Mm, Q, W] and bits_t [Bm, Mm, S, Wq] (tensor-core kernels; may be
+//     null): the mask and its transpose, 32 pairs a word, zeros behind S and Q.
+// A warp takes 32 queries and 32 keys: lane j reads byte j of each row, the
+// row's word is a ballot, and the lane's own column of the transpose builds up.
+__global__ void __launch_bounds__(128) msda_attention_mask_kernel(const uint8_t* mask, long long mk_sb, long long mk_sh,
                                                                   long long mk_sq, const uint8_t* key_mask,
-                                                                  long long km_sb, int Q, int S, int G, int LB, int LN,
-                                                                  int heads, uint8_t* live) {
-    const int j = blockIdx.x * 256 + threadIdx.x;
-    if (j >= S) return;
-    for (int z = blockIdx.z; z < LB * LN; z += gridDim.z) {
-        const int lb = z / LN, ln = z - lb * LN;
-        bool any = false;
-        for (int q0 = blockIdx.y * 64; q0 < Q && !any; q0 += gridDim.y * 64) {
-            const int q1 = min(Q, q0 + 64);
-            for (int h = 0; h < heads && !any; ++h) {
-                const uint8_t* p = mask + lb * mk_sb + (long long)(ln * G + h) * mk_sh + q0 * mk_sq + j;
+                                                                  long long km_sb, int Q, int S, int G, int Bm, int Mm,
+                                                                  int LB, int LN, int B, uint8_t* live, uint32_t* bits,
+                                                                  uint32_t* bits_t, int W, int Wq) {
+    const int lane = threadIdx.x & 31, word = blockIdx.x * 4 + (threadIdx.x >> 5), j = word * 32 + lane;
+    for (int z = blockIdx.z; z < Bm * Mm; z += gridDim.z) {
+        const int bm = z / Mm, mm = z - bm * Mm;
+        const uint8_t* src = mask + bm * mk_sb + mm * mk_sh + j;
+        for (int qw = blockIdx.y; qw < Wq; qw += gridDim.y) {
+            const int q0 = qw * 32;
+            uint32_t row = 0, col = 0;
 #pragma unroll 8
-                for (int q = q0; q < q1; ++q, p += mk_sq) any |= *p != 0;
+            for (int r = 0; r < 32; ++r) {
+                const bool on = j < S && q0 + r < Q && src[(q0 + r) * mk_sq] != 0;
+                const uint32_t w = __ballot_sync(0xffffffffu, on);
+                if (lane == r) row = w;
+                col |= (on ? 1u : 0u) << r;
+            }
+            if (bits && q0 + lane < Q) bits[((long long)z * Q + q0 + lane) * W + word] = row;
+            if (bits_t && j < S) bits_t[((long long)z * S + j) * Wq + qw] = col;
+            if (col) {
+                const int ln = LN > 1 ? mm / G : 0;
+                // a mask that all batch items share meets the key_mask of each
+                const int b0 = Bm > 1 ? bm : 0, b1 = Bm > 1 ? bm + 1 : LB;
+                for (int b = b0; b < b1; ++b)
+                    if (!key_mask || key_mask[b * km_sb + j]) live[((long long)(LB > 1 ? b : 0) * LN + ln) * S + j] = 1;
             }
         }
-        if (any && (!key_mask || key_mask[lb * km_sb + j])) live[(long long)z * S + j] = 1;
     }
 }
 
@@ -48,6 +67,13 @@ constexpr int kSms = 152;  // SMs that a grid is sized for
 constexpr unsigned kFlags = MSDA_ATTENTION_CAUSAL | MSDA_ATTENTION_KEY_MASK | MSDA_ATTENTION_MASK;
 
 size_t up(size_t n) { return (n + 255) / 256 * 256; }
+
+// Tensors that the tensor-core kernels take where their addresses and strides
+// are made of 16 bytes: 16-bit, channels in whole 16-byte vectors, a group of
+// shared heads that fits a tile, some key.
+bool tc_type(msda_dtype dt, const msda_attention_problem* p) {
+    return dt != MSDA_F32 && p->D % 8 == 0 && p->M / p->N <= 128 && p->S > 0;
+}
 
 msda_status check(msda_dtype dt, unsigned flags, const msda_attention_problem* p) {
     if (dt != MSDA_F32 && dt != MSDA_F16 && dt != MSDA_BF16) return failf(MSDA_ERR_INVALID_ARG, "unknown dtype %d", (int)dt);
@@ -81,18 +107,26 @@ msda_status check(msda_dtype dt, unsigned flags, const msda_attention_problem* p
     return MSDA_OK;
 }
 
-// Workspace of the liveness of keys under a mask: [LB][LN][S] bytes.
-struct Live {
-    int LB = 1, LN = 1, heads = 1;
-    size_t bytes = 0;
+// What the mask becomes in the workspace: the liveness of keys [LB][LN][S]
+// bytes and, for the tensor-core kernels, the pairs as bits by query and by key.
+struct MaskSpace {
+    int Bm = 1, Mm = 1, LB = 1, LN = 1, W = 0, Wq = 0;
+    size_t bits = 0, bits_t = 0, bytes = 0;  // offsets of the bits behind the liveness
 };
-Live live_of(unsigned flags, const msda_attention_problem* p) {
-    Live l;
+MaskSpace mask_space(msda_dtype dt, unsigned flags, const msda_attention_problem* p) {
+    MaskSpace l;
     if (!(flags & MSDA_ATTENTION_MASK)) return l;
-    l.LB = (flags & MSDA_ATTENTION_KEY_MASK) || (p->B > 1 && p->mask_stride[0] != 0) ? (int)p->B : 1;
-    l.LN = p->M > 1 && p->mask_stride[1] != 0 ? (int)p->N : 1;
-    l.heads = l.LN > 1 || (p->N == 1 && p->M > 1 && p->mask_stride[1] != 0) ? (int)(p->M / p->N) : 1;
-    l.bytes = up((size_t)l.LB * l.LN * (size_t)p->S);
+    l.Bm = p->B > 1 && p->mask_stride[0] != 0 ? (int)p->B : 1;
+    l.Mm = p->M > 1 && p->mask_stride[1] != 0 ? (int)p->M : 1;
+    l.LB = (flags & MSDA_ATTENTION_KEY_MASK) || l.Bm > 1 ? (int)p->B : 1;
+    l.LN = l.Mm > 1 ? (int)p->N : 1;
+    l.W = (int)((p->S + 127) / 128 * 4);
+    l.Wq = (int)((p->Q + 127) / 128 * 4);
+    l.bits = up((size_t)l.LB * l.LN * (size_t)p->S);
+    l.bits_t = l.bits;
+    if (tc_type(dt, p)) l.bits_t += up((size_t)l.Bm * l.Mm * p->Q * l.W * 4);
+    l.bytes = l.bits_t;
+    if (tc_type(dt, p)) l.bytes += up((size_t)l.Bm * l.Mm * p->S * l.Wq * 4);
     return l;
 }
 
@@ -147,25 +181,92 @@ AttentionArgs args_of(unsigned flags, const msda_attention_problem* p, double sc
     return a;
 }
 
-// Replaces key_mask by the keys that some pair of the mask leaves.
-msda_status make_live(AttentionArgs& a, const Live& l, void* ws, cudaStream_t st) {
-    if (!a.mask || a.S == 0 || a.B == 0) return MSDA_OK;
+// Replaces key_mask by the keys that some pair of the mask leaves, and brings
+// the mask's bits up where `t` is given.
+msda_status make_mask(AttentionArgs& a, const MaskSpace& l, void* ws, msda::TcArgs* t, cudaStream_t st) {
+    if (!a.mask) return MSDA_OK;
     uint8_t* live = static_cast<uint8_t*>(ws);
-    msda::TraceSpan ts(st);
-    cudaError_t e = cudaMemsetAsync(live, 0, (size_t)l.LB * l.LN * a.S, st);
-    if (e == cudaSuccess && a.Q > 0) {
-        const int64_t z = (int64_t)l.LB * l.LN, y = (a.Q + 63) / 64;
-        const dim3 grid((unsigned)((a.S + 255) / 256), (unsigned)(y < 65535 ? y : 65535), (unsigned)(z < 65535 ? z : 65535));
-        msda::msda_attention_live_kernel<<<grid, 256, 0, st>>>(a.mask, a.mk_sb, a.mk_sh, a.mk_sq, a.key_mask, a.km_sb, a.Q,
-                                                               a.S, a.G, l.LB, l.LN, l.heads, live);
-        e = cudaGetLastError();
+    uint32_t* bits = t ? reinterpret_cast<uint32_t*>(live + l.bits) : nullptr;
+    uint32_t* bits_t = t ? reinterpret_cast<uint32_t*>(live + l.bits_t) : nullptr;
+    if (a.S > 0) {
+        msda::TraceSpan ts(st);
+        cudaError_t e = cudaMemsetAsync(live, 0, (size_t)l.LB * l.LN * a.S, st);
+        if (e == cudaSuccess) {
+            const int64_t z = (int64_t)l.Bm * l.Mm;
+            const dim3 grid((unsigned)((a.S + 127) / 128), (unsigned)(l.Wq < 65535 ? l.Wq : 65535),
+                            (unsigned)(z < 65535 ? z : 65535));
+            msda::msda_attention_mask_kernel<<<grid, 128, 0, st>>>(a.mask, a.mk_sb, a.mk_sh, a.mk_sq, a.key_mask, a.km_sb, a.Q,
+                                                                   a.S, a.G, l.Bm, l.Mm, l.LB, l.LN, a.B, live, bits, bits_t,
+                                                                   l.W, l.Wq);
+            e = cudaGetLastError();
+        }
+        ts.end(MSDA_KERNEL_ATTENTION_MASK, (int64_t)a.Q * a.S);
+        if (e != cudaSuccess) return failf(MSDA_ERR_CUDA, "mask kernel launch: %s", cudaGetErrorString(e));
     }
-    ts.end(MSDA_KERNEL_ATTENTION_MASK, (int64_t)a.Q * a.S);
-    if (e != cudaSuccess) return failf(MSDA_ERR_CUDA, "mask kernel launch: %s", cudaGetErrorString(e));
     a.key_mask = live;
     a.km_sb = l.LB > 1 ? (long long)l.LN * a.S : 0;
     a.km_sh = l.LN > 1 ? a.S : 0;
+    if (t) {
+        t->bits = bits, t->bits_t = bits_t, t->W = l.W, t->Wq = l.Wq;
+        t->bits_sh = l.Mm > 1 ? (long long)a.Q * l.W : 0;
+        t->bits_sb = l.Bm > 1 ? (long long)l.Mm * a.Q * l.W : 0;
+        t->bits_t_sh = l.Mm > 1 ? (long long)a.S * l.Wq : 0;
+        t->bits_t_sb = l.Bm > 1 ? (long long)l.Mm * a.S * l.Wq : 0;
+    }
     return MSDA_OK;
+}
+
+using EncodeTiled = PFN_cuTensorMapEncodeTiled_v12000;
+
+// Rows of a [B, rows, heads, D] tensor as (channel, head of the group, row,
+// key head, batch); boxes of 64 channels x G heads x `rows` rows with the
+// 128-byte swizzle; zeros outside.
+bool rows_map(msda_dtype dt, const void* base, int64_t D, int64_t G, int64_t rows, int64_t N, int64_t B, int64_t sb,
+              int64_t ss, int64_t sh, int box_rows, CUtensorMap* map) {
+    EncodeTiled f = reinterpret_cast<EncodeTiled>(msda::tensor_map_encoder());
+    if (!f) return false;
+    // the stride of a dimension of one element is never used, and need not be a whole number of vectors
+    auto bytes = [](int64_t n, int64_t stride) { return (cuuint64_t)(n > 1 ? stride * 2 : 16); };
+    const cuuint64_t dims[5] = {(cuuint64_t)D, (cuuint64_t)G, (cuuint64_t)rows, (cuuint64_t)N, (cuuint64_t)B};
+    const cuuint64_t strides[4] = {bytes(G, sh), bytes(rows, ss), bytes(N, G * sh), bytes(B, sb)};
+    const cuuint32_t box[5] = {64u, (cuuint32_t)G, (cuuint32_t)box_rows, 1u, 1u};
+    const cuuint32_t one[5] = {1u, 1u, 1u, 1u, 1u};
+    return f(map, dt == MSDA_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5,
+             const_cast<void*>(base), dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Whether TMA can read a tensor: 16-byte address, strides of whole vectors below 2^40 bytes.
+bool tma_rows(const void* p, const int64_t* stride, int64_t B, int64_t rows, int64_t heads) {
+    const int64_t n[3] = {B, rows, heads};
+    for (int i = 0; i < 3; ++i)
+        if (n[i] > 1 && (stride[i] % 8 || stride[i] <= 0 || stride[i] >= (1ll << 38) / heads)) return false;
+    return msda::aligned_to(p, 16);
+}
+
+// Row blocks and split of the tensor-core forward.  Two row tiles a block
+// overlap one's products with the other's exponentials; one tile where two
+// would leave SMs without a block.  A key axis of many tiles is split until
+// every SM has a block, but not into pieces of less than four tiles: a piece
+// costs a launch's start and the joining of its rows.
+struct ForwardPlan {
+    int G, qpt, nq, qblocks, splits, per;
+};
+ForwardPlan forward_plan(const msda_attention_problem* p) {
+    ForwardPlan f;
+    f.G = (int)(p->M / p->N);
+    f.qpt = msda::kTcRows / f.G;
+    const int64_t one = (p->Q + f.qpt - 1) / f.qpt, two = (p->Q + 2 * f.qpt - 1) / (2 * f.qpt);
+    f.nq = p->B * p->N * two >= kSms ? 2 : 1;
+    f.qblocks = (int)(f.nq == 2 ? two : one);
+    const int64_t blocks = p->B * p->N * f.qblocks, tiles = (p->S + msda::kTcRows - 1) / msda::kTcRows;
+    int64_t n = blocks > 0 ? kSms / blocks : 1;
+    if (n > tiles / 4) n = tiles / 4;
+    if (n < 1) n = 1;
+    const int64_t each = tiles > 0 ? (tiles + n - 1) / n : 1;
+    f.per = (int)each;
+    f.splits = tiles > 0 ? (int)((tiles + each - 1) / each) : 1;
+    return f;
 }
 
 bool simt_vec(const AttentionArgs& a) {  // binary32 rows read as 16-byte vectors
@@ -188,15 +289,15 @@ msda_status launched(cudaError_t e, const char* what) {
 // Workspace of the backward: the rows' statistics, then the keys' liveness.
 struct BackwardLayout {
     AttentionRows rows;
-    size_t l2 = 0, dl = 0, live = 0, bytes = 0;
+    size_t l2 = 0, dl = 0, mask = 0, bytes = 0;
 };
-BackwardLayout backward_layout(unsigned flags, const msda_attention_problem* p) {
+BackwardLayout backward_layout(msda_dtype dt, unsigned flags, const msda_attention_problem* p) {
     BackwardLayout w;
     w.rows = {64, 64, (int)((p->Q + 63) / 64), (int)p->M, 1};
     const size_t n = up((size_t)p->B * w.rows.N * w.rows.tiles * w.rows.rt * 4);
     w.dl = n;
-    w.live = 2 * n;
-    w.bytes = 2 * n + live_of(flags, p).bytes;
+    w.mask = 2 * n;
+    w.bytes = 2 * n + mask_space(dt, flags, p).bytes;
     return w;
 }
 
@@ -208,12 +309,17 @@ size_t msda_attention_forward_workspace_size(msda_dtype dt, unsigned flags, cons
     if (check(dt, flags, p) != MSDA_OK) return 0;
     int splits, per;
     simt_splits(p, &splits, &per);
-    return part_bytes(p, splits) + live_of(flags, p).bytes;
+    size_t part = part_bytes(p, splits);
+    if (tc_type(dt, p)) {  // which of the two runs depends on the addresses
+        const size_t tc = part_bytes(p, forward_plan(p).splits);
+        if (tc > part) part = tc;
+    }
+    return part + mask_space(dt, flags, p).bytes;
 }
 
 size_t msda_attention_backward_workspace_size(msda_dtype dt, unsigned flags, const msda_attention_problem* p) {
     if (check(dt, flags, p) != MSDA_OK) return 0;
-    return backward_layout(flags, p).bytes;
+    return backward_layout(dt, flags, p).bytes;
 }
 
 msda_status msda_attention_forward(msda_dtype dt, unsigned flags, const msda_attention_problem* p, double scale,
@@ -237,14 +343,38 @@ msda_status msda_attention_forward(msda_dtype dt, unsigned flags, const msda_att
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     AttentionArgs a = args_of(flags, p, scale, query, key, value, key_mask, mask);
     a.out = out, a.lse = lse;
-    if ((s = make_live(a, live_of(flags, p), workspace, st)) != MSDA_OK) return s;
-    unsigned char* part = static_cast<unsigned char*>(workspace) + live_of(flags, p).bytes;
-    simt_splits(p, &a.splits, &a.tiles_per_split);
+    const bool tc = tc_type(dt, p) && tma_rows(query, p->query_stride, p->B, p->Q, p->M) &&
+                    tma_rows(key, p->key_stride, p->B, p->S, p->N) && tma_rows(value, p->value_stride, p->B, p->S, p->N) &&
+                    msda::aligned_to(out, 16);
+    const MaskSpace ms = mask_space(dt, flags, p);
+    msda::TcArgs t{};
+    if ((s = make_mask(a, ms, workspace, tc ? &t : nullptr, st)) != MSDA_OK) return s;
+    ForwardPlan f{};
+    if (tc) {
+        f = forward_plan(p);
+        a.splits = f.splits, a.tiles_per_split = f.per;
+    } else {
+        simt_splits(p, &a.splits, &a.tiles_per_split);
+    }
     if (a.splits > 1) {
+        unsigned char* part = static_cast<unsigned char*>(workspace) + ms.bytes;
         a.part_o = reinterpret_cast<float*>(part);
         a.part_lse = reinterpret_cast<float*>(part + up((size_t)a.splits * p->B * p->M * p->Q * p->D * 4));
     }
-    {
+    if (tc) {
+        int sms;
+        if ((s = msda::device_facts(&a.err, &sms)) != MSDA_OK) return s;
+        CUtensorMap mq, mk, mv;
+        if (!rows_map(dt, query, p->D, f.G, p->Q, p->N, p->B, a.q_sb, a.q_ss, a.q_sh, f.qpt, &mq) ||
+            !rows_map(dt, key, p->D, 1, p->S, p->N, p->B, a.k_sb, a.k_ss, a.k_sh, msda::kTcRows, &mk) ||
+            !rows_map(dt, value, p->D, 1, p->S, p->N, p->B, a.v_sb, a.v_ss, a.v_sh, msda::kTcRows, &mv))
+            return failf(MSDA_ERR_CUDA, "cuTensorMapEncodeTiled failed");
+        t.a = a;
+        t.G = f.G, t.qpt = f.qpt, t.rows = f.G * f.qpt, t.qblocks = f.qblocks;
+        msda::TraceSpan ts(st);
+        s = launched(msda::launch_attention_tc_forward(t, dt == MSDA_BF16, f.nq, mq, mk, mv, st), "attention kernel launch");
+        ts.end(MSDA_KERNEL_ATTENTION, p->B * p->M * p->Q);
+    } else {
         msda::TraceSpan ts(st);
         s = launched(MSDA_BY_DTYPE(dt, launch_attention_simt, a, simt_vec(a), st), "attention kernel launch");
         ts.end(MSDA_KERNEL_ATTENTION, p->B * p->M * p->Q);
@@ -283,7 +413,7 @@ msda_status msda_attention_backward(msda_dtype dt, unsigned flags, const msda_at
         if (keys && e == cudaSuccess) e = cudaMemsetAsync(grad_value, 0, (size_t)p->B * p->S * p->N * p->D * es, st);
         return launched(e, "cudaMemsetAsync");
     }
-    const BackwardLayout w = backward_layout(flags, p);
+    const BackwardLayout w = backward_layout(dt, flags, p);
     if (!workspace || workspace_bytes < w.bytes || !msda::aligned_to(workspace, 256))
         return failf(MSDA_ERR_WORKSPACE, "workspace of %zu bytes, 256-byte aligned, needed (got %zu)", w.bytes,
                      workspace_bytes);
@@ -293,7 +423,7 @@ msda_status msda_attention_backward(msda_dtype dt, unsigned flags, const msda_at
     float* l2 = reinterpret_cast<float*>(ws + w.l2);
     float* dl = reinterpret_cast<float*>(ws + w.dl);
     a.row_l2 = l2, a.row_dl = dl;
-    if ((s = make_live(a, live_of(flags, p), ws + w.live, st)) != MSDA_OK) return s;
+    if ((s = make_mask(a, mask_space(dt, flags, p), ws + w.mask, nullptr, st)) != MSDA_OK) return s;
     {
         msda::TraceSpan ts(st);
         s = launched(MSDA_BY_DTYPE(dt, launch_attention_prepare, a, w.rows, out, lse, l2, dl, st),

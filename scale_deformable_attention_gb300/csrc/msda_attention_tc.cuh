@@ -1,0 +1,90 @@
+// msda_attention_tc.cuh -- what the tensor-core attention kernels share:
+// arguments, tile geometry, masks of a tile's pairs as bits, the warp that
+// clears rows which take no part.
+#pragma once
+
+#include "msda_attention.cuh"
+#include "msda_tcgen05.cuh"
+
+namespace msda {
+
+constexpr int kTcRows = 128;            // rows and keys a tile
+constexpr uint32_t kTcTile = 128 * 128; // bytes of 128 rows of 64 channels
+
+struct TcArgs {
+    AttentionArgs a;
+    int G, qpt, rows;     // heads side by side in a row tile, queries a tile, rows used (G * qpt)
+    int qblocks;          // row blocks of a key head (forward), row tiles of a head (backward)
+    const uint32_t* bits;   // pairs of the mask as bits [Bm, Mm, Q, W] (W = words a row, a multiple of 4) or null
+    const uint32_t* bits_t; // the same with keys as rows: [Bm, Mm, S, Wq]
+    long long bits_sb, bits_sh, bits_t_sb, bits_t_sh;
+    int W, Wq;
+    int fix_rows;         // backward: rows without keys may occur, and are cleared
+    const float* scale_in; // f16: the largest squared norms (see attention_amax), else null
+};
+
+// Largest query-to-key limit: query q sees keys j < tc_seen(q).
+__device__ __forceinline__ int tc_seen(const AttentionArgs& a, int q) {
+    if (!a.causal) return a.S;
+    const long long n = (long long)q + 1 + (a.S - a.Q);
+    return n < 0 ? 0 : n < a.S ? (int)n : a.S;
+}
+
+// the lowest n bits, n clamped to 0..32
+__device__ __forceinline__ uint32_t tc_low_bits(int n) { return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u; }
+
+// First and last + 1 key tile of [t0, t1) that hold a key which `km` leaves
+// (all threads of the block; they see the same bytes).
+__device__ __forceinline__ void tc_trim(const uint8_t* km, int S, int* t0, int* t1) {
+    while (*t0 < *t1) {
+        const int lo = *t0 * kTcRows;
+        bool any = false;
+        const int n = min(S, *t1 * kTcRows) - lo;
+        // one tile at a time until one holds a key: padding lies at the end as a rule
+        any = (int)threadIdx.x < min(n, kTcRows) && km[lo + threadIdx.x] != 0;
+        if (__syncthreads_or(any)) break;
+        ++*t0;
+    }
+    while (*t0 < *t1) {
+        // 8 tiles at a time from the end
+        const int hi = min(S, *t1 * kTcRows), lo = max(*t0, *t1 - 8) * kTcRows;
+        bool any = false;
+        for (int j = lo + threadIdx.x; j < hi; j += blockDim.x) any |= km[j] != 0;
+        if (__syncthreads_or(any)) break;
+        *t1 = max(*t0, *t1 - 8);
+    }
+    while (*t0 < *t1) {
+        const int hi = min(S, *t1 * kTcRows), lo = (*t1 - 1) * kTcRows;
+        const bool any = (int)threadIdx.x < hi - lo && km[lo + threadIdx.x] != 0;
+        if (__syncthreads_or(any)) break;
+        --*t1;
+    }
+}
+
+// Clears the rows of a tile (NC blocks of 128 rows of 128 bytes) whose bit in
+// w[4] is 0: one warp, eight lanes a row.  A cleared row gives scores of 0 and
+// products of 0 whatever it held.
+template <int NC>
+__device__ __forceinline__ void tc_clear_rows(unsigned char* tile, const uint32_t (&w)[4], int lane) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        if (w[k] == 0xffffffffu) continue;
+        for (int r = lane >> 3; r < 32; r += 4) {
+            if ((w[k] >> r) & 1u) continue;
+#pragma unroll
+            for (int c = 0; c < NC; ++c)
+                *reinterpret_cast<uint4*>(tile + c * kTcTile + (k * 32 + r) * 128 + (lane & 7) * 16) = make_uint4(0, 0, 0, 0);
+        }
+    }
+}
+
+// Bits of 128 keys from `km` (bytes; beyond `n` keys: 0), the same in all lanes.
+__device__ __forceinline__ void tc_key_words(const uint8_t* km, int n, int lane, uint32_t (&w)[4]) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const int j = k * 32 + lane;
+        w[k] = __ballot_sync(0xffffffffu, j < n && km[j] != 0);
+    }
+}
+
+}  // namespace msda

@@ -1,0 +1,363 @@
+// msda_attention_tc_forward.cu -- softmax attention on the tensor cores
+// (tcgen05, sm_103a), fp16 and bf16, D a multiple of 8 up to 128.
+//
+//   S = Q K^T,  m = running row maximum,  P = 2^(c S - m),  l += row sums,  O = 2^(m_old - m) O + P V
+//
+// A block takes NQ tiles of 128 rows of one key head (the G query heads that
+// share it lie side by side in a tile, so keys and values are read once for
+// all of them) and walks the tiles of 128 keys.  Warps:
+//   - one warpgroup a row tile: a thread owns a row, so its maximum and sum need
+//     no exchange; it reads S from tensor memory, writes P (16 bits) over it;
+//   - one warp issues the TMA copies (a ring of K and V tiles), one the
+//     products, one clears keys that key_mask leaves out.
+// With two row tiles the products of one run while the other's exponentials
+// are worked out.  O stays in tensor memory; it is rescaled only when a row's
+// maximum has grown by more than 2^8 since the last time (P is then at most
+// 2^8, which f16 and the binary32 sums hold), in practice in the first tiles.
+//
+// The product S(j+1) is issued behind P(j) V(j) by the same thread, and the
+// barrier that hands S(j+1) over covers both: at that point O holds all tiles
+// up to j, so the rescaling needs no barrier of its own.
+#include "msda_attention_tc.cuh"
+#include "msda_attention_tc_host.cuh"
+
+namespace msda {
+
+template <int NQ, int NC>
+struct TcForwardCfg {
+    static constexpr int kStages = NC == 1 ? (NQ == 2 ? 8 : 4) : 4;  // ring of K and V tiles
+    static constexpr int kThreads = NQ * 128 + 128;
+    static constexpr uint32_t kTileBytes = NC * kTcTile;
+    static constexpr uint32_t kCols = NQ == 2 ? 512 : 256;  // tensor memory: NQ * (128 for S and P, up to 128 for O)
+    static constexpr size_t kSmem = (size_t)(NQ + kStages) * kTileBytes + 1024 + 512;
+};
+
+struct TcForwardSync {
+    uint64_t full[8], empty[8], ready[8];
+    uint64_t q_full, s_full[2], p_full[2], o_full[2];
+    uint32_t tmem, abort;
+    uint32_t words[8][4];
+};
+
+template <bool BF16, int NQ, int NC>
+__global__ void __launch_bounds__(TcForwardCfg<NQ, NC>::kThreads, 1)
+    msda_attention_tc_forward_kernel(const TcArgs p, const __grid_constant__ CUtensorMap map_q,
+                                     const __grid_constant__ CUtensorMap map_k,
+                                     const __grid_constant__ CUtensorMap map_v) {
+    using Cfg = TcForwardCfg<NQ, NC>;
+    constexpr int ST = Cfg::kStages;
+    const AttentionArgs& a = p.a;
+    extern __shared__ unsigned char tc_smem_raw[];
+    unsigned char* smem = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(tc_smem_raw) + 1023) & ~(uintptr_t)1023);
+    unsigned char* q_tiles = smem;
+    unsigned char* ring = smem + NQ * Cfg::kTileBytes;
+    __shared__ TcForwardSync sy;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+    long long id = blockIdx.x;
+    const int split = (int)(id % a.splits);
+    id /= a.splits;
+    int qb = (int)(id % p.qblocks);
+    id /= p.qblocks;
+    const int n = (int)(id % a.N), b = (int)(id / a.N);
+    if (a.causal) qb = p.qblocks - 1 - qb;  // the rows that see most first
+    const int q0 = qb * NQ * p.qpt;         // first query of the block
+
+    // key tiles of this block
+    const uint8_t* km = a.key_mask ? a.key_mask + b * a.km_sb + n * a.km_sh : nullptr;
+    int t0 = split * a.tiles_per_split;
+    int t1 = min(t0 + a.tiles_per_split, (tc_seen(a, min(q0 + NQ * p.qpt, a.Q) - 1) + kTcRows - 1) / kTcRows);
+    if (km) tc_trim(km, a.S, &t0, &t1);
+    const int nt = max(0, t1 - t0);
+
+    if (warp == NQ * 4) {
+        if (lane == 0) {
+            for (int i = 0; i < ST; ++i) {
+                tc_bar_init(tc_smem(&sy.full[i]), 1);
+                tc_bar_init(tc_smem(&sy.empty[i]), 1);
+                tc_bar_init(tc_smem(&sy.ready[i]), 1);
+            }
+            tc_bar_init(tc_smem(&sy.q_full), 1);
+            for (int i = 0; i < 2; ++i) {
+                tc_bar_init(tc_smem(&sy.s_full[i]), 1);
+                tc_bar_init(tc_smem(&sy.p_full[i]), 4);
+                tc_bar_init(tc_smem(&sy.o_full[i]), 1);
+            }
+            sy.abort = 0;
+            asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+            tc_prefetch_map(&map_q);
+            tc_prefetch_map(&map_k);
+            tc_prefetch_map(&map_v);
+        }
+    } else if (warp == NQ * 4 + 1) {
+        tmem_alloc(tc_smem(&sy.tmem), Cfg::kCols);
+    }
+    if (p.rows < kTcRows) {  // rows that no query fills hold zeros, not what was there
+        const uint32_t words = (kTcRows - p.rows) * 8;
+        for (uint32_t i = tid; i < NQ * NC * words; i += Cfg::kThreads) {
+            const uint32_t c = i / words, w = i - c * words;
+            *reinterpret_cast<uint4*>(q_tiles + c * kTcTile + p.rows * 128 + w * 16) = make_uint4(0, 0, 0, 0);
+        }
+        tc_fence_async();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = sy.tmem;
+    volatile uint32_t* abort = &sy.abort;
+
+    if (warp < NQ * 4) {
+        if constexpr (NQ == 2) tc_regs_up<208>();
+        // ---- softmax: row `row` of tile `t` ----
+        const int t = warp >> 2, wl = warp & 3, row = wl * 32 + lane;
+        const int q = q0 + t * p.qpt + row / p.G, h = n * p.G + row % p.G;
+        const bool valid = row < p.rows && q < a.Q;
+        const bool warp_on = __any_sync(0xffffffffu, valid);
+        const int seen = valid ? tc_seen(a, q) : 0;
+        const int seen_least = __reduce_min_sync(0xffffffffu, valid ? seen : a.S);
+        const uint32_t lanes = (uint32_t)wl << 21;  // this warp's lanes of tensor memory
+        const uint32_t s_at = tmem + t * 128 + lanes, o_at = tmem + NQ * 128 + t * (NC * 64) + lanes;
+        const uint32_t* bits = p.bits && valid ? p.bits + b * p.bits_sb + h * p.bits_sh + (long long)q * p.W : nullptr;
+        const int chunks = (a.D + 15) / 16;
+        float m = -attn_inf(), l = 0.f;
+        for (int i = 0; i < nt; ++i) {
+            const int j0 = (t0 + i) * kTcRows;
+            uint4 bw = make_uint4(~0u, ~0u, ~0u, ~0u);
+            if (bits) bw = *reinterpret_cast<const uint4*>(bits + (t0 + i) * 4);
+            if (!tc_bar_wait(tc_smem(&sy.s_full[t]), i & 1, abort, a.err)) break;
+            tc_fence_after();
+            if (warp_on) {
+                uint32_t s[4][32];
+#pragma unroll
+                for (int c = 0; c < 4; ++c) tmem_ld32(s[c], s_at + c * 32);
+                tmem_wait_ld();
+                if (km || p.bits || seen_least - j0 < kTcRows) {
+                    const int see = seen - j0;
+                    uint32_t w[4] = {bw.x & tc_low_bits(see), bw.y & tc_low_bits(see - 32), bw.z & tc_low_bits(see - 64),
+                                     bw.w & tc_low_bits(see - 96)};
+                    if (km) {
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) w[c] &= sy.words[i & 7][c];
+                    }
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)
+#pragma unroll
+                        for (int k = 0; k < 32; ++k)
+                            if (!((w[c] >> k) & 1u)) s[c][k] = 0xff800000u;
+                }
+                float mx[4];
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    mx[c] = __uint_as_float(s[c][0]);
+#pragma unroll
+                    for (int k = 1; k < 32; ++k) mx[c] = fmaxf(mx[c], __uint_as_float(s[c][k]));
+                }
+                const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * a.c2;
+                if (__any_sync(0xffffffffu, top > m + 8.f)) {
+                    const float next = fmaxf(m, top);
+                    const float f = next == m ? 1.f : tc_ex2(m - next);
+                    m = next;
+                    l *= f;
+                    if (i > 0) {
+                        for (int c = 0; c < chunks; ++c) {
+                            uint32_t o[16];
+                            tmem_ld16(o, o_at + c * 16);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
+                            tmem_st16(o_at + c * 16, o);
+                        }
+                    }
+                }
+                const float ref = m == -attn_inf() ? 0.f : m;
+                float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    uint32_t pk[16];
+#pragma unroll
+                    for (int k = 0; k < 16; ++k) {
+                        const float e0 = tc_ex2(fmaf(__uint_as_float(s[c][2 * k]), a.c2, -ref));
+                        const float e1 = tc_ex2(fmaf(__uint_as_float(s[c][2 * k + 1]), a.c2, -ref));
+                        sum[k & 3] += e0 + e1;
+                        pk[k] = tc_pack<BF16>(e0, e1);
+                    }
+                    tmem_st16(s_at + c * 16, pk);
+                }
+                l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                tmem_wait_st();
+                tc_fence_before();
+            }
+            __syncwarp();
+            if (lane == 0) tc_bar_arrive(tc_smem(&sy.p_full[t]));
+        }
+        // ---- output ----
+        bool ok = true;
+        if (nt > 0) {
+            ok = tc_bar_wait(tc_smem(&sy.o_full[t]), 0, abort, a.err);
+            tc_fence_after();
+        }
+        if (warp_on && ok) {
+            const float inv = l == 0.f ? 0.f : 1.f / l;
+            const float l2 = l == 0.f ? -attn_inf() : m + log2f(l);
+            const long long r = ((long long)b * a.M + h) * a.Q + q;
+            const long long part = (long long)split * a.B * a.M * a.Q + r;
+            for (int c = 0; c < chunks; ++c) {
+                uint32_t o[16];
+                if (nt > 0) {
+                    tmem_ld16(o, o_at + c * 16);
+                    tmem_wait_ld();
+                }
+                if (!valid) continue;
+#pragma unroll
+                for (int k = 0; k < 16; ++k) o[k] = l == 0.f ? 0u : __float_as_uint(__uint_as_float(o[k]) * inv);
+                if (a.splits > 1) {
+                    float* out = a.part_o + part * a.D + c * 16;
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        if (c * 16 + 4 * k < a.D) reinterpret_cast<uint4*>(out)[k] = make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+                } else {
+                    unsigned char* out = static_cast<unsigned char*>(a.out) +
+                                         ((((long long)b * a.Q + q) * a.M + h) * a.D + c * 16) * 2;
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        uint32_t v[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            v[e] = tc_pack<BF16>(__uint_as_float(o[8 * k + 2 * e]), __uint_as_float(o[8 * k + 2 * e + 1]));
+                        if (c * 16 + 8 * k < a.D) reinterpret_cast<uint4*>(out)[k] = make_uint4(v[0], v[1], v[2], v[3]);
+                    }
+                }
+            }
+            if (valid) {
+                if (a.splits > 1) a.part_lse[part] = l2;
+                else a.lse[r] = l2 * kLn2;
+            }
+        }
+        if (!ok) tc_drain();
+    } else {
+        if constexpr (NQ == 2) tc_regs_down<88>();
+        const int role = warp - NQ * 4;
+        bool ok = true;
+        if (role == 0 && lane == 0 && nt > 0) {
+            // ---- copies ----
+            const uint32_t qbar = tc_smem(&sy.q_full);
+            tc_bar_expect(qbar, NQ * NC * p.rows * 128);
+            for (int t = 0; t < NQ; ++t)
+                for (int c = 0; c < NC; ++c)
+                    tc_tma_5d(tc_smem(q_tiles) + (t * NC + c) * kTcTile, &map_q, qbar, c * 64, 0, q0 + t * p.qpt, n, b);
+            for (int i = 0; i < 2 * nt && ok; ++i) {  // K(0), V(0), K(1), ...
+                const int st = i % ST;
+                if (i >= ST) ok = tc_bar_wait(tc_smem(&sy.empty[st]), (i / ST - 1) & 1, abort, a.err);
+                if (!ok) break;
+                const uint32_t bar = tc_smem(&sy.full[st]);
+                tc_bar_expect(bar, Cfg::kTileBytes);
+                for (int c = 0; c < NC; ++c)
+                    tc_tma_5d(tc_smem(ring) + st * Cfg::kTileBytes + c * kTcTile, (i & 1) ? &map_v : &map_k, bar, c * 64, 0,
+                              (t0 + (i >> 1)) * kTcRows, n, b);
+            }
+        } else if (role == 1 && lane == 0 && nt > 0) {
+            // ---- products ----
+            const uint32_t id_qk = tc_idesc(BF16, false, false, 128, 128);
+            const int steps = (a.D + 15) / 16;
+            const uint32_t id_pv = tc_idesc(BF16, false, true, 128, steps * 16);
+            uint64_t* full = km ? sy.ready : sy.full;
+            const uint32_t q_at = tc_smem(q_tiles), ring_at = tc_smem(ring);
+            auto product_s = [&](int t, int st) {
+                for (int k = 0; k < steps; ++k) {
+                    const uint32_t off = (k >> 2) * kTcTile + (k & 3) * 32;
+                    tc_mma_ss(tmem + t * 128, tc_desc(q_at + t * Cfg::kTileBytes + off, 16, 1024),
+                              tc_desc(ring_at + st * Cfg::kTileBytes + off, 16, 1024), id_qk, k > 0);
+                }
+                tc_commit(tc_smem(&sy.s_full[t]));
+            };
+            ok = tc_bar_wait(tc_smem(&sy.q_full), 0, abort, a.err) && tc_bar_wait(tc_smem(&full[0]), 0, abort, a.err);
+            if (ok) {
+                tc_fence_after();
+                for (int t = 0; t < NQ; ++t) product_s(t, 0);
+                tc_commit(tc_smem(&sy.empty[0]));
+            }
+            for (int i = 0; i < nt && ok; ++i) {
+                const int iv = 2 * i + 1, ik = 2 * i + 2;
+                const int sv = iv % ST, sk = ik % ST;
+                const bool more = i + 1 < nt;
+                ok = tc_bar_wait(tc_smem(&full[sv]), (iv / ST) & 1, abort, a.err) &&
+                     (!more || tc_bar_wait(tc_smem(&full[sk]), (ik / ST) & 1, abort, a.err));
+                for (int t = 0; t < NQ && ok; ++t) {
+                    ok = tc_bar_wait(tc_smem(&sy.p_full[t]), i & 1, abort, a.err);
+                    if (!ok) break;
+                    tc_fence_after();
+                    for (int k = 0; k < 8; ++k)
+                        tc_mma_ts(tmem + NQ * 128 + t * (NC * 64), tmem + t * 128 + k * 8,
+                                  tc_desc(ring_at + sv * Cfg::kTileBytes + k * 2048, kTcTile, 1024), id_pv, i > 0 || k > 0);
+                    if (more) product_s(t, sk);
+                    else tc_commit(tc_smem(&sy.o_full[t]));
+                }
+                if (ok) {
+                    tc_commit(tc_smem(&sy.empty[sv]));
+                    if (more) tc_commit(tc_smem(&sy.empty[sk]));
+                }
+            }
+        } else if (role == 2 && km && nt > 0) {
+            // ---- keys that take no part ----
+            for (int i = 0; i < 2 * nt && ok; ++i) {
+                const int st = i % ST, j0 = (t0 + (i >> 1)) * kTcRows;
+                uint32_t w[4];
+                tc_key_words(km + j0, a.S - j0, lane, w);
+                if (!(i & 1) && lane == 0) {
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) sy.words[(i >> 1) & 7][c] = w[c];
+                }
+                ok = tc_bar_wait(tc_smem(&sy.full[st]), (i / ST) & 1, abort, a.err);
+                if (!ok) break;
+                if ((w[0] & w[1] & w[2] & w[3]) != 0xffffffffu) {
+                    tc_clear_rows<NC>(ring + st * Cfg::kTileBytes, w, lane);
+                    tc_fence_async();
+                }
+                __syncwarp();
+                if (lane == 0) tc_bar_arrive(tc_smem(&sy.ready[st]));
+            }
+        }
+        __syncwarp();
+        if (!ok) tc_drain();
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == NQ * 4 + 1) tmem_dealloc(tmem, Cfg::kCols);
+}
+
+// ---- host ----
+
+template <bool BF16, int NQ, int NC>
+static cudaError_t forward_go(const TcArgs& p, const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v,
+                              cudaStream_t st) {
+    using Cfg = TcForwardCfg<NQ, NC>;
+    cudaError_t e = cudaFuncSetAttribute(msda_attention_tc_forward_kernel<BF16, NQ, NC>,
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Cfg::kSmem);
+    if (e != cudaSuccess) return e;
+    const long long grid = (long long)p.a.B * p.a.N * p.qblocks * p.a.splits;
+    msda_attention_tc_forward_kernel<BF16, NQ, NC><<<(unsigned)grid, Cfg::kThreads, Cfg::kSmem, st>>>(p, q, k, v);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_attention_tc_forward(const TcArgs& p, bool bf16, int nq, const CUtensorMap& q, const CUtensorMap& k,
+                                        const CUtensorMap& v, cudaStream_t st) {
+    const int nc = p.a.D > 64 ? 2 : 1;
+#define MSDA_TC_GO(BF, NQ, NC) return forward_go<BF, NQ, NC>(p, q, k, v, st)
+    if (bf16) {
+        if (nq == 2) {
+            if (nc == 1) MSDA_TC_GO(true, 2, 1);
+            MSDA_TC_GO(true, 2, 2);
+        }
+        if (nc == 1) MSDA_TC_GO(true, 1, 1);
+        MSDA_TC_GO(true, 1, 2);
+    }
+    if (nq == 2) {
+        if (nc == 1) MSDA_TC_GO(false, 2, 1);
+        MSDA_TC_GO(false, 2, 2);
+    }
+    if (nc == 1) MSDA_TC_GO(false, 1, 1);
+    MSDA_TC_GO(false, 1, 2);
+#undef MSDA_TC_GO
+}
+
+}  // namespace msda

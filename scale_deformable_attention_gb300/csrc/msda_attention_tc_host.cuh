@@ -1,0 +1,13 @@
+// msda_attention_tc_host.cuh -- launches of the tensor-core attention kernels.
+#pragma once
+
+#include "msda_attention_tc.cuh"
+
+namespace msda {
+
+// Row tiles of the forward a block takes: two where that leaves a block for
+// each SM, else one.
+cudaError_t launch_attention_tc_forward(const TcArgs& p, bool bf16, int nq, const CUtensorMap& q, const CUtensorMap& k,
+                                        const CUtensorMap& v, cudaStream_t st);
+
+}  // namespace msda

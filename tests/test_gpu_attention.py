@@ -99,6 +99,21 @@ def test_masks(msda, size, kind, dtype):
         R.check(got[name], want[name], name)
 
 
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("kind", ["", "keys none", "pairs", "pairs each", "causal"])
+@pytest.mark.parametrize("size", [(20, 300, 260, 8, 8, 32), (10, 513, 140, 16, 16, 128), (30, 300, 300, 6, 6, 80),
+                                  (20, 70, 400, 24, 8, 64)], ids=lambda s: "x".join(map(str, s)))
+def test_many_rows(msda, size, kind, dtype):
+    """Enough rows for every SM to take two row tiles at a time."""
+    B, Q, S, M, N, D = size
+    q, k, v, do = make(19, dtype, *size)
+    kw, ok = masks(kind, 20, B, Q, S, M)
+    want = R.attention(q, k, v, do, ok)
+    got = both(msda, q, k, v, do, kw)
+    for name in want:
+        R.check(got[name], want[name], name)
+
+
 @pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
 @pytest.mark.parametrize("kind", ["keys", "pairs", "keys pairs"])
 @pytest.mark.parametrize("D", [32, 128, 20])
