@@ -8,16 +8,17 @@
 // all of them) and walks the tiles of 128 keys.  Warps:
 //   - one warpgroup a row tile: a thread owns a row, so its maximum and sum need
 //     no exchange; it reads S from tensor memory, writes P (16 bits) over it;
-//   - one warp issues the TMA copies (a ring of K and V tiles), one the
-//     products, one clears keys that key_mask leaves out.
+//   - one warp issues the TMA copies (a ring of K and V tiles), one a row tile
+//     its products, one clears keys that key_mask leaves out.
 // With two row tiles the products of one run while the other's exponentials
 // are worked out.  O stays in tensor memory; it is rescaled only when a row's
 // maximum has grown by more than 2^8 since the last time (P is then at most
 // 2^8, which f16 and the binary32 sums hold), in practice in the first tiles.
 //
-// The product S(j+1) is issued behind P(j) V(j) by the same thread, and the
-// barrier that hands S(j+1) over covers both: at that point O holds all tiles
-// up to j, so the rescaling needs no barrier of its own.
+// Up to 64 channels P has columns of its own: S(j+1) is made while P(j) is
+// still worked out, so a row's warps never wait for a product.  Beyond, P lies
+// over S, and S(j+1) is issued behind P(j) V(j) by the same thread: the other
+// row tile's exponentials fill that time.
 #include "msda_attention_tc.cuh"
 #include "msda_attention_tc_host.cuh"
 
@@ -28,13 +29,19 @@ struct TcForwardCfg {
     static constexpr int kStages = NC == 1 ? (NQ == 2 ? 8 : 4) : 4;  // ring of K and V tiles
     static constexpr int kThreads = NQ * 128 + 128;
     static constexpr uint32_t kTileBytes = NC * kTcTile;
-    static constexpr uint32_t kCols = NQ == 2 ? 512 : 256;  // tensor memory: NQ * (128 for S and P, up to 128 for O)
+    // tensor memory: S (128 columns a row tile), P (64), O (64 or 128).  With
+    // two tiles of up to 128 channels the 512 columns have no room for P: it
+    // then lies over S, and the next S waits until P is used up.
+    static constexpr bool kOwnP = NC == 1;
+    static constexpr uint32_t kP = kOwnP ? NQ * 128 : 0, kPStep = kOwnP ? 64 : 128;
+    static constexpr uint32_t kO = kOwnP ? NQ * 192 : NQ * 128;
+    static constexpr uint32_t kCols = NQ == 2 ? 512 : 256;
     static constexpr size_t kSmem = (size_t)(NQ + kStages) * kTileBytes + 1024 + 512;
 };
 
 struct TcForwardSync {
     uint64_t full[8], empty[8], ready[8];
-    uint64_t q_full, s_full[2], p_full[2], o_full[2];
+    uint64_t q_full, s_full[2], s_free[2], p_full[2], pv_done[2];
     uint32_t tmem, abort;
     uint32_t words[8][4];
 };
@@ -74,14 +81,15 @@ __global__ void __launch_bounds__(TcForwardCfg<NQ, NC>::kThreads, 1)
         if (lane == 0) {
             for (int i = 0; i < ST; ++i) {
                 tc_bar_init(tc_smem(&sy.full[i]), 1);
-                tc_bar_init(tc_smem(&sy.empty[i]), 1);
+                tc_bar_init(tc_smem(&sy.empty[i]), NQ);
                 tc_bar_init(tc_smem(&sy.ready[i]), 1);
             }
             tc_bar_init(tc_smem(&sy.q_full), 1);
             for (int i = 0; i < 2; ++i) {
                 tc_bar_init(tc_smem(&sy.s_full[i]), 1);
+                tc_bar_init(tc_smem(&sy.s_free[i]), 4);
                 tc_bar_init(tc_smem(&sy.p_full[i]), 4);
-                tc_bar_init(tc_smem(&sy.o_full[i]), 1);
+                tc_bar_init(tc_smem(&sy.pv_done[i]), 1);
             }
             sy.abort = 0;
             asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -116,7 +124,8 @@ __global__ void __launch_bounds__(TcForwardCfg<NQ, NC>::kThreads, 1)
         const int seen = valid ? tc_seen(a, q) : 0;
         const int seen_least = __reduce_min_sync(0xffffffffu, valid ? seen : a.S);
         const uint32_t lanes = (uint32_t)wl << 21;  // this warp's lanes of tensor memory
-        const uint32_t s_at = tmem + t * 128 + lanes, o_at = tmem + NQ * 128 + t * (NC * 64) + lanes;
+        const uint32_t s_at = tmem + t * 128 + lanes, o_at = tmem + Cfg::kO + t * (NC * 64) + lanes;
+        const uint32_t p_at = tmem + Cfg::kP + t * Cfg::kPStep + lanes;
         const uint32_t* bits = p.bits && valid ? p.bits + b * p.bits_sb + h * p.bits_sh + (long long)q * p.W : nullptr;
         const int chunks = (a.D + 15) / 16;
         float m = -attn_inf(), l = 0.f;
@@ -131,6 +140,11 @@ __global__ void __launch_bounds__(TcForwardCfg<NQ, NC>::kThreads, 1)
 #pragma unroll
                 for (int c = 0; c < 4; ++c) tmem_ld32(s[c], s_at + c * 32);
                 tmem_wait_ld();
+                if constexpr (Cfg::kOwnP) {  // S(i+1) may be written now
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) tc_bar_arrive(tc_smem(&sy.s_free[t]));
+                }
                 if (km || p.bits || seen_least - j0 < kTcRows) {
                     const int see = seen - j0;
                     uint32_t w[4] = {bw.x & tc_low_bits(see), bw.y & tc_low_bits(see - 32), bw.z & tc_low_bits(see - 64),
@@ -139,18 +153,21 @@ __global__ void __launch_bounds__(TcForwardCfg<NQ, NC>::kThreads, 1)
 #pragma unroll
                         for (int c = 0; c < 4; ++c) w[c] &= sy.words[i & 7][c];
                     }
+                    if (__any_sync(0xffffffffu, (w[0] & w[1] & w[2] & w[3]) != 0xffffffffu)) {
 #pragma unroll
-                    for (int c = 0; c < 4; ++c)
+                        for (int c = 0; c < 4; ++c)
 #pragma unroll
-                        for (int k = 0; k < 32; ++k)
-                            if (!((w[c] >> k) & 1u)) s[c][k] = 0xff800000u;
+                            for (int k = 0; k < 32; ++k)
+                                if (!((w[c] >> k) & 1u)) s[c][k] = 0xff800000u;
+                    }
                 }
                 float mx[4];
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
-                    mx[c] = __uint_as_float(s[c][0]);
+                    mx[c] = fmaxf(__uint_as_float(s[c][0]), __uint_as_float(s[c][1]));
 #pragma unroll
-                    for (int k = 1; k < 32; ++k) mx[c] = fmaxf(mx[c], __uint_as_float(s[c][k]));
+                    for (int k = 2; k < 32; k += 2)
+                        mx[c] = tc_max3(mx[c], __uint_as_float(s[c][k]), __uint_as_float(s[c][k + 1]));
                 }
                 const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * a.c2;
                 if (__any_sync(0xffffffffu, top > m + 8.f)) {
@@ -159,6 +176,9 @@ __global__ void __launch_bounds__(TcForwardCfg<NQ, NC>::kThreads, 1)
                     m = next;
                     l *= f;
                     if (i > 0) {
+                        // P(i-1) V(i-1) has ended: with P over S, S(i) was behind it
+                        if (Cfg::kOwnP && !tc_bar_wait(tc_smem(&sy.pv_done[t]), (i - 1) & 1, abort, a.err)) break;
+                        tc_fence_after();
                         for (int c = 0; c < chunks; ++c) {
                             uint32_t o[16];
                             tmem_ld16(o, o_at + c * 16);
@@ -169,23 +189,35 @@ __global__ void __launch_bounds__(TcForwardCfg<NQ, NC>::kThreads, 1)
                         }
                     }
                 }
+                if (Cfg::kOwnP && i > 0) {  // P(i-1) is used up
+                    if (!tc_bar_wait(tc_smem(&sy.pv_done[t]), (i - 1) & 1, abort, a.err)) break;
+                    tc_fence_after();
+                }
                 const float ref = m == -attn_inf() ? 0.f : m;
-                float sum[4] = {0.f, 0.f, 0.f, 0.f};
+                const uint64_t c2 = tc_two(a.c2, a.c2), nref = tc_two(-ref, -ref);
+                uint64_t sum[2] = {0, 0};
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
                     uint32_t pk[16];
 #pragma unroll
                     for (int k = 0; k < 16; ++k) {
-                        const float e0 = tc_ex2(fmaf(__uint_as_float(s[c][2 * k]), a.c2, -ref));
-                        const float e1 = tc_ex2(fmaf(__uint_as_float(s[c][2 * k + 1]), a.c2, -ref));
-                        sum[k & 3] += e0 + e1;
+                        float x0, x1;
+                        tc_split(tc_fma2(tc_two(__uint_as_float(s[c][2 * k]), __uint_as_float(s[c][2 * k + 1])), c2, nref), x0, x1);
+                        const float e0 = tc_ex2(x0), e1 = tc_ex2(x1);
+                        sum[k & 1] = tc_add2(sum[k & 1], tc_two(e0, e1));
                         pk[k] = tc_pack<BF16>(e0, e1);
                     }
-                    tmem_st16(s_at + c * 16, pk);
+                    tmem_st16(p_at + c * 16, pk);
                 }
-                l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                float s0, s1;
+                tc_split(tc_add2(sum[0], sum[1]), s0, s1);
+                l += s0 + s1;
                 tmem_wait_st();
                 tc_fence_before();
+            } else if constexpr (Cfg::kOwnP) {
+                if (lane == 0) tc_bar_arrive(tc_smem(&sy.s_free[t]));
+                // a warp without rows may not run a tile ahead of the others: its arrival would count for theirs
+                if (i > 0 && !tc_bar_wait(tc_smem(&sy.pv_done[t]), (i - 1) & 1, abort, a.err)) break;
             }
             __syncwarp();
             if (lane == 0) tc_bar_arrive(tc_smem(&sy.p_full[t]));
@@ -193,7 +225,7 @@ __global__ void __launch_bounds__(TcForwardCfg<NQ, NC>::kThreads, 1)
         // ---- output ----
         bool ok = true;
         if (nt > 0) {
-            ok = tc_bar_wait(tc_smem(&sy.o_full[t]), 0, abort, a.err);
+            ok = tc_bar_wait(tc_smem(&sy.pv_done[t]), (nt - 1) & 1, abort, a.err);
             tc_fence_after();
         }
         if (warp_on && ok) {
@@ -255,57 +287,80 @@ __global__ void __launch_bounds__(TcForwardCfg<NQ, NC>::kThreads, 1)
                     tc_tma_5d(tc_smem(ring) + st * Cfg::kTileBytes + c * kTcTile, (i & 1) ? &map_v : &map_k, bar, c * 64, 0,
                               (t0 + (i >> 1)) * kTcRows, n, b);
             }
-        } else if (role == 1 && lane == 0 && nt > 0) {
-            // ---- products ----
+        } else if ((role == 1 || (NQ == 2 && role == 3)) && nt > 0) {
+            // ---- products of row tile t ----
+            const int t = role >> 1;
+            const uint32_t on = tc_elect();
             const uint32_t id_qk = tc_idesc(BF16, false, false, 128, 128);
             const int steps = (a.D + 15) / 16;
             const uint32_t id_pv = tc_idesc(BF16, false, true, 128, steps * 16);
             uint64_t* full = km ? sy.ready : sy.full;
-            const uint32_t q_at = tc_smem(q_tiles), ring_at = tc_smem(ring);
-            auto product_s = [&](int t, int st) {
-                for (int k = 0; k < steps; ++k) {
-                    const uint32_t off = (k >> 2) * kTcTile + (k & 3) * 32;
-                    tc_mma_ss(tmem + t * 128, tc_desc(q_at + t * Cfg::kTileBytes + off, 16, 1024),
-                              tc_desc(ring_at + st * Cfg::kTileBytes + off, 16, 1024), id_qk, k > 0);
+            const uint32_t ring_at = tc_smem(ring);
+            const uint64_t q_desc = tc_desc(tc_smem(q_tiles) + t * Cfg::kTileBytes, 16, 1024);
+            const uint32_t s_at = tmem + t * 128, o_at = tmem + Cfg::kO + t * (NC * 64);
+            const uint32_t p_at = tmem + Cfg::kP + t * Cfg::kPStep;
+            auto product_s = [&](int st) {
+                const uint64_t k_desc = tc_desc(ring_at + st * Cfg::kTileBytes, 16, 1024);
+#pragma unroll
+                for (int k = 0; k < NC * 4; ++k) {  // 16 channels: 32 bytes further, 64: the next tile
+                    const uint64_t off = ((k >> 2) * kTcTile + (k & 3) * 32) >> 4;
+                    if (k < steps) tc_mma_ss(on, s_at, q_desc + off, k_desc + off, id_qk, k > 0);
                 }
-                tc_commit(tc_smem(&sy.s_full[t]));
+                tc_commit(on, tc_smem(&sy.s_full[t]));
             };
             ok = tc_bar_wait(tc_smem(&sy.q_full), 0, abort, a.err) && tc_bar_wait(tc_smem(&full[0]), 0, abort, a.err);
             if (ok) {
                 tc_fence_after();
-                for (int t = 0; t < NQ; ++t) product_s(t, 0);
-                tc_commit(tc_smem(&sy.empty[0]));
+                product_s(0);
+                tc_commit(on, tc_smem(&sy.empty[0]));
             }
             for (int i = 0; i < nt && ok; ++i) {
                 const int iv = 2 * i + 1, ik = 2 * i + 2;
                 const int sv = iv % ST, sk = ik % ST;
                 const bool more = i + 1 < nt;
-                ok = tc_bar_wait(tc_smem(&full[sv]), (iv / ST) & 1, abort, a.err) &&
-                     (!more || tc_bar_wait(tc_smem(&full[sk]), (ik / ST) & 1, abort, a.err));
-                for (int t = 0; t < NQ && ok; ++t) {
-                    ok = tc_bar_wait(tc_smem(&sy.p_full[t]), i & 1, abort, a.err);
+                if (Cfg::kOwnP && more) {
+                    ok = tc_bar_wait(tc_smem(&full[sk]), (ik / ST) & 1, abort, a.err) &&
+                         tc_bar_wait(tc_smem(&sy.s_free[t]), i & 1, abort, a.err);
                     if (!ok) break;
                     tc_fence_after();
-                    for (int k = 0; k < 8; ++k)
-                        tc_mma_ts(tmem + NQ * 128 + t * (NC * 64), tmem + t * 128 + k * 8,
-                                  tc_desc(ring_at + sv * Cfg::kTileBytes + k * 2048, kTcTile, 1024), id_pv, i > 0 || k > 0);
-                    if (more) product_s(t, sk);
-                    else tc_commit(tc_smem(&sy.o_full[t]));
+                    product_s(sk);
+                    tc_commit(on, tc_smem(&sy.empty[sk]));
                 }
-                if (ok) {
-                    tc_commit(tc_smem(&sy.empty[sv]));
-                    if (more) tc_commit(tc_smem(&sy.empty[sk]));
+                ok = tc_bar_wait(tc_smem(&full[sv]), (iv / ST) & 1, abort, a.err) &&
+                     tc_bar_wait(tc_smem(&sy.p_full[t]), i & 1, abort, a.err);
+                if (!ok) break;
+                tc_fence_after();
+                const uint64_t v_desc = tc_desc(ring_at + sv * Cfg::kTileBytes, kTcTile, 1024);
+#pragma unroll
+                for (int k = 0; k < 8; ++k)  // 16 keys: two atoms further
+                    tc_mma_ts(on, o_at, p_at + k * 8, v_desc + ((k * 2048) >> 4), id_pv, i > 0 || k > 0);
+                tc_commit(on, tc_smem(&sy.pv_done[t]));
+                tc_commit(on, tc_smem(&sy.empty[sv]));
+                if (!Cfg::kOwnP && more) {
+                    ok = tc_bar_wait(tc_smem(&full[sk]), (ik / ST) & 1, abort, a.err);
+                    if (!ok) break;
+                    tc_fence_after();
+                    product_s(sk);
+                    tc_commit(on, tc_smem(&sy.empty[sk]));
                 }
             }
         } else if (role == 2 && km && nt > 0) {
             // ---- keys that take no part ----
-            for (int i = 0; i < 2 * nt && ok; ++i) {
-                const int st = i % ST, j0 = (t0 + (i >> 1)) * kTcRows;
-                uint32_t w[4];
-                tc_key_words(km + j0, a.S - j0, lane, w);
-                if (!(i & 1) && lane == 0) {
+            uint32_t w[4];
+            uint8_t next[4];
+            auto read = [&](int j0) {
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) sy.words[(i >> 1) & 7][c] = w[c];
+                for (int c = 0; c < 4; ++c) next[c] = j0 + c * 32 + lane < a.S ? km[j0 + c * 32 + lane] : 0;
+            };
+            read(t0 * kTcRows);
+            for (int i = 0; i < 2 * nt && ok; ++i) {
+                const int st = i % ST;
+                if (!(i & 1)) {  // a new tile's keys: their bytes were read a tile ahead
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) w[c] = __ballot_sync(0xffffffffu, next[c] != 0);
+                    if (lane < 4) sy.words[(i >> 1) & 7][lane] = lane == 0 ? w[0] : lane == 1 ? w[1] : lane == 2 ? w[2] : w[3];
+                    __syncwarp();
+                    if (i + 2 < 2 * nt) read((t0 + (i >> 1) + 1) * kTcRows);
                 }
                 ok = tc_bar_wait(tc_smem(&sy.full[st]), (i / ST) & 1, abort, a.err);
                 if (!ok) break;
