@@ -11,9 +11,16 @@
 //   - one warp issues the TMA copies (a ring of K and V tiles), one a row tile
 //     its products, one clears keys that key_mask leaves out.
 // With two row tiles the products of one run while the other's exponentials
-// are worked out.  O stays in tensor memory; it is rescaled only when a row's
-// maximum has grown by more than 2^8 since the last time (P is then at most
-// 2^8, which f16 and the binary32 sums hold), in practice in the first tiles.
+// are worked out.  O stays in tensor memory.
+//
+// The reference m is a row's maximum when it was last looked for, not the
+// running one: any m that keeps P in range gives the same quotient.  A tile
+// takes its exponentials against the m at hand, and only where a row's sum
+// then exceeds 2^14 (f16 holds 65504, and every P is at most its sum) are the
+// maximum looked for, O and l rescaled and the exponentials taken again.  That
+// is the first tile, and then only rows whose scores keep rising; the others
+// save the maximum, which stood between reading S and the first exponential
+// (about 500 of 2600 cycles a pair of tiles).
 //
 // Up to 64 channels P has columns of its own: S(j+1) is made while P(j) is
 // still worked out, so a row's warps never wait for a product.  Beyond, P lies
@@ -23,6 +30,8 @@
 #include "msda_attention_tc_host.cuh"
 
 namespace msda {
+
+constexpr float kSumLimit = 16384.f;  // a row's sum over a tile that asks for a new reference
 
 template <int NQ, int NC>
 struct TcForwardCfg {
@@ -41,7 +50,7 @@ struct TcForwardCfg {
 
 struct TcForwardSync {
     uint64_t full[8], empty[8], ready[8];
-    uint64_t q_full, s_full[2], s_free[2], p_full[2], pv_done[2];
+    uint64_t q_full, s_full[2], s_free[2], p_full[2], pv_done[2], turn;
     uint32_t tmem, abort;
     uint32_t words[8][4];
 };
@@ -85,6 +94,7 @@ __global__ void __launch_bounds__(TcForwardCfg<NQ, NC>::kThreads, 1)
                 tc_bar_init(tc_smem(&sy.ready[i]), 1);
             }
             tc_bar_init(tc_smem(&sy.q_full), 1);
+            tc_bar_init(tc_smem(&sy.turn), 1);
             for (int i = 0; i < 2; ++i) {
                 tc_bar_init(tc_smem(&sy.s_full[i]), 1);
                 tc_bar_init(tc_smem(&sy.s_free[i]), 4);
@@ -128,7 +138,9 @@ __global__ void __launch_bounds__(TcForwardCfg<NQ, NC>::kThreads, 1)
         const uint32_t p_at = tmem + Cfg::kP + t * Cfg::kPStep + lanes;
         const uint32_t* bits = p.bits && valid ? p.bits + b * p.bits_sb + h * p.bits_sh + (long long)q * p.W : nullptr;
         const int chunks = (a.D + 15) / 16;
+        const uint32_t first = lane == 0;
         float m = -attn_inf(), l = 0.f;
+#pragma unroll 1
         for (int i = 0; i < nt; ++i) {
             const int j0 = (t0 + i) * kTcRows;
             uint4 bw = make_uint4(~0u, ~0u, ~0u, ~0u);
@@ -142,10 +154,9 @@ __global__ void __launch_bounds__(TcForwardCfg<NQ, NC>::kThreads, 1)
                 tmem_wait_ld();
                 if constexpr (Cfg::kOwnP) {  // S(i+1) may be written now
                     tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) tc_bar_arrive(tc_smem(&sy.s_free[t]));
+                    tc_bar_arrive_if(first, tc_smem(&sy.s_free[t]));
                 }
-                if (km || p.bits || seen_least - j0 < kTcRows) {
+                if (__builtin_expect(km || p.bits || seen_least - j0 < kTcRows, 0)) {
                     const int see = seen - j0;
                     uint32_t w[4] = {bw.x & tc_low_bits(see), bw.y & tc_low_bits(see - 32), bw.z & tc_low_bits(see - 64),
                                      bw.w & tc_low_bits(see - 96)};
@@ -153,7 +164,7 @@ __global__ void __launch_bounds__(TcForwardCfg<NQ, NC>::kThreads, 1)
 #pragma unroll
                         for (int c = 0; c < 4; ++c) w[c] &= sy.words[i & 7][c];
                     }
-                    if (__any_sync(0xffffffffu, (w[0] & w[1] & w[2] & w[3]) != 0xffffffffu)) {
+                    if (__builtin_expect(__any_sync(0xffffffffu, (w[0] & w[1] & w[2] & w[3]) != 0xffffffffu), 0)) {
 #pragma unroll
                         for (int c = 0; c < 4; ++c)
 #pragma unroll
@@ -161,24 +172,58 @@ __global__ void __launch_bounds__(TcForwardCfg<NQ, NC>::kThreads, 1)
                                 if (!((w[c] >> k) & 1u)) s[c][k] = 0xff800000u;
                     }
                 }
-                float mx[4];
+                const uint64_t c2 = tc_two(a.c2, a.c2);
+                bool gone = false;
+                // P = 2^(c S - m) into tensor memory; the row's sum.  `wait`: P(i-1) may still be read.
+                auto probabilities = [&](bool wait) {
+                    const float ref = m == -attn_inf() ? 0.f : m;
+                    const uint64_t nref = tc_two(-ref, -ref);
+                    uint64_t part[2] = {0, 0};
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    mx[c] = fmaxf(__uint_as_float(s[c][0]), __uint_as_float(s[c][1]));
+                    for (int c = 0; c < 4; ++c) {
+                        uint32_t pk[16];
 #pragma unroll
-                    for (int k = 2; k < 32; k += 2)
-                        mx[c] = tc_max3(mx[c], __uint_as_float(s[c][k]), __uint_as_float(s[c][k + 1]));
+                        for (int k = 0; k < 16; ++k) {
+                            float x0, x1;
+                            tc_split(tc_fma2(tc_two(__uint_as_float(s[c][2 * k]), __uint_as_float(s[c][2 * k + 1])), c2, nref), x0,
+                                     x1);
+                            const float e0 = tc_ex2(x0), e1 = tc_ex2(x1);
+                            part[k & 1] = tc_add2(part[k & 1], tc_two(e0, e1));
+                            pk[k] = tc_pack<BF16>(e0, e1);
+                        }
+                        if (c == 0 && wait) {
+                            gone = !tc_bar_wait(tc_smem(&sy.pv_done[t]), (i - 1) & 1, abort, a.err);
+                            tc_fence_after();
+                        }
+                        tmem_st16(p_at + c * 16, pk);
+                    }
+                    float s0, s1;
+                    tc_split(tc_add2(part[0], part[1]), s0, s1);
+                    return s0 + s1;
+                };
+                bool renew = __any_sync(0xffffffffu, valid && m == -attn_inf());
+                float sum = 0.f;
+                if (__builtin_expect(!renew, 1)) {
+                    sum = probabilities(Cfg::kOwnP && i > 0);
+                    renew = __any_sync(0xffffffffu, valid && !(sum <= kSumLimit));
+                } else if (Cfg::kOwnP && i > 0) {
+                    gone = !tc_bar_wait(tc_smem(&sy.pv_done[t]), (i - 1) & 1, abort, a.err);
+                    tc_fence_after();
                 }
-                const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * a.c2;
-                if (__any_sync(0xffffffffu, top > m + 8.f)) {
-                    const float next = fmaxf(m, top);
+                if (__builtin_expect(renew, 0)) {
+                    float mx[4];
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        mx[c] = fmaxf(__uint_as_float(s[c][0]), __uint_as_float(s[c][1]));
+#pragma unroll
+                        for (int k = 2; k < 32; k += 2)
+                            mx[c] = tc_max3(mx[c], __uint_as_float(s[c][k]), __uint_as_float(s[c][k + 1]));
+                    }
+                    const float next = fmaxf(m, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * a.c2);
                     const float f = next == m ? 1.f : tc_ex2(m - next);
                     m = next;
                     l *= f;
                     if (i > 0) {
-                        // P(i-1) V(i-1) has ended: with P over S, S(i) was behind it
-                        if (Cfg::kOwnP && !tc_bar_wait(tc_smem(&sy.pv_done[t]), (i - 1) & 1, abort, a.err)) break;
-                        tc_fence_after();
                         for (int c = 0; c < chunks; ++c) {
                             uint32_t o[16];
                             tmem_ld16(o, o_at + c * 16);
@@ -188,39 +233,20 @@ __global__ void __launch_bounds__(TcForwardCfg<NQ, NC>::kThreads, 1)
                             tmem_st16(o_at + c * 16, o);
                         }
                     }
+                    sum = probabilities(false);
                 }
-                if (Cfg::kOwnP && i > 0) {  // P(i-1) is used up
-                    if (!tc_bar_wait(tc_smem(&sy.pv_done[t]), (i - 1) & 1, abort, a.err)) break;
-                    tc_fence_after();
-                }
-                const float ref = m == -attn_inf() ? 0.f : m;
-                const uint64_t c2 = tc_two(a.c2, a.c2), nref = tc_two(-ref, -ref);
-                uint64_t sum[2] = {0, 0};
-#pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    uint32_t pk[16];
-#pragma unroll
-                    for (int k = 0; k < 16; ++k) {
-                        float x0, x1;
-                        tc_split(tc_fma2(tc_two(__uint_as_float(s[c][2 * k]), __uint_as_float(s[c][2 * k + 1])), c2, nref), x0, x1);
-                        const float e0 = tc_ex2(x0), e1 = tc_ex2(x1);
-                        sum[k & 1] = tc_add2(sum[k & 1], tc_two(e0, e1));
-                        pk[k] = tc_pack<BF16>(e0, e1);
-                    }
-                    tmem_st16(p_at + c * 16, pk);
-                }
-                float s0, s1;
-                tc_split(tc_add2(sum[0], sum[1]), s0, s1);
-                l += s0 + s1;
+                if (__builtin_expect(gone, 0)) break;
+                l += sum;
                 tmem_wait_st();
                 tc_fence_before();
             } else if constexpr (Cfg::kOwnP) {
-                if (lane == 0) tc_bar_arrive(tc_smem(&sy.s_free[t]));
+                tc_bar_arrive_if(first, tc_smem(&sy.s_free[t]));
                 // a warp without rows may not run a tile ahead of the others: its arrival would count for theirs
                 if (i > 0 && !tc_bar_wait(tc_smem(&sy.pv_done[t]), (i - 1) & 1, abort, a.err)) break;
             }
-            __syncwarp();
-            if (lane == 0) tc_bar_arrive(tc_smem(&sy.p_full[t]));
+            // the warp's loads and stores of tensor memory have ended for all its lanes (wait::ld and wait::st are
+            // instructions of the whole warp): one lane arrives for it
+            tc_bar_arrive_if(first, tc_smem(&sy.p_full[t]));
         }
         // ---- output ----
         bool ok = true;
@@ -309,6 +335,10 @@ __global__ void __launch_bounds__(TcForwardCfg<NQ, NC>::kThreads, 1)
                 tc_commit(on, tc_smem(&sy.s_full[t]));
             };
             ok = tc_bar_wait(tc_smem(&sy.q_full), 0, abort, a.err) && tc_bar_wait(tc_smem(&full[0]), 0, abort, a.err);
+            // P over S: the second row tile starts when the first has worked out its first P, so that from then on
+            // the products of one run beside the exponentials of the other (together they took 4200 cycles a pair
+            // of tiles of 128 channels)
+            if (!Cfg::kOwnP && t == 1) ok = ok && tc_bar_wait(tc_smem(&sy.turn), 0, abort, a.err);
             if (ok) {
                 tc_fence_after();
                 product_s(0);
@@ -330,6 +360,7 @@ __global__ void __launch_bounds__(TcForwardCfg<NQ, NC>::kThreads, 1)
                      tc_bar_wait(tc_smem(&sy.p_full[t]), i & 1, abort, a.err);
                 if (!ok) break;
                 tc_fence_after();
+                if (!Cfg::kOwnP && NQ == 2 && t == 0 && i == 0) tc_bar_arrive_if(on, tc_smem(&sy.turn));
                 const uint64_t v_desc = tc_desc(ring_at + sv * Cfg::kTileBytes, kTcTile, 1024);
 #pragma unroll
                 for (int k = 0; k < 8; ++k)  // 16 keys: two atoms further

@@ -26,6 +26,13 @@ __device__ __forceinline__ void tc_bar_init(uint32_t bar, uint32_t count) {
 __device__ __forceinline__ void tc_bar_arrive(uint32_t bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
+// the arrival of one lane (on = 1), without a branch
+__device__ __forceinline__ void tc_bar_arrive_if(uint32_t on, uint32_t bar) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %1, 0;\n\t@q mbarrier.arrive.shared::cta.b64 _, [%0];\n\t}" ::"r"(bar),
+        "r"(on)
+        : "memory");
+}
 __device__ __forceinline__ void tc_bar_expect(uint32_t bar, uint32_t bytes) {
     asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
 }
@@ -54,7 +61,7 @@ __device__ __forceinline__ bool tc_bar_wait_slow(uint32_t bar, uint32_t parity, 
     return false;
 }
 __device__ __forceinline__ bool tc_bar_wait(uint32_t bar, uint32_t parity, volatile uint32_t* abort, unsigned* err) {
-    if (tc_bar_try(bar, parity)) return true;
+    if (__builtin_expect(tc_bar_try(bar, parity), 1)) return true;
     return tc_bar_wait_slow(bar, parity, abort, err);
 }
 // After a wait gave up: time for copies and products in flight to end before
