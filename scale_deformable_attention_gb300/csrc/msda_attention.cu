@@ -286,18 +286,22 @@ msda_status launched(cudaError_t e, const char* what) {
     return e == cudaSuccess ? MSDA_OK : failf(MSDA_ERR_CUDA, "%s: %s (%s)", what, cudaGetErrorString(e), cudaGetErrorName(e));
 }
 
-// Workspace of the backward: the rows' statistics, then the keys' liveness.
+// Workspace of the backward: the rows' statistics, f16's norms, the mask.
+// Row tiles are 128 rows on the tensor cores, 64 on the FMA pipe; which runs
+// depends on the addresses, and 128 needs as much space or more.
 struct BackwardLayout {
     AttentionRows rows;
-    size_t l2 = 0, dl = 0, mask = 0, bytes = 0;
+    size_t l2 = 0, dl = 0, top = 0, mask = 0, bytes = 0;
 };
-BackwardLayout backward_layout(msda_dtype dt, unsigned flags, const msda_attention_problem* p) {
+BackwardLayout backward_layout(msda_dtype dt, unsigned flags, const msda_attention_problem* p, bool tc) {
     BackwardLayout w;
-    w.rows = {64, 64, (int)((p->Q + 63) / 64), (int)p->M, 1};
+    const int rt = tc ? msda::kTcRows : 64;
+    w.rows = {rt, rt, (int)((p->Q + rt - 1) / rt), (int)p->M, 1};
     const size_t n = up((size_t)p->B * w.rows.N * w.rows.tiles * w.rows.rt * 4);
     w.dl = n;
-    w.mask = 2 * n;
-    w.bytes = 2 * n + mask_space(dt, flags, p).bytes;
+    w.top = 2 * n;
+    w.mask = 2 * n + 256;
+    w.bytes = w.mask + mask_space(dt, flags, p).bytes;
     return w;
 }
 
@@ -319,7 +323,7 @@ size_t msda_attention_forward_workspace_size(msda_dtype dt, unsigned flags, cons
 
 size_t msda_attention_backward_workspace_size(msda_dtype dt, unsigned flags, const msda_attention_problem* p) {
     if (check(dt, flags, p) != MSDA_OK) return 0;
-    return backward_layout(dt, flags, p).bytes;
+    return backward_layout(dt, flags, p, tc_type(dt, p)).bytes;
 }
 
 msda_status msda_attention_forward(msda_dtype dt, unsigned flags, const msda_attention_problem* p, double scale,
@@ -413,9 +417,14 @@ msda_status msda_attention_backward(msda_dtype dt, unsigned flags, const msda_at
         if (keys && e == cudaSuccess) e = cudaMemsetAsync(grad_value, 0, (size_t)p->B * p->S * p->N * p->D * es, st);
         return launched(e, "cudaMemsetAsync");
     }
-    const BackwardLayout w = backward_layout(dt, flags, p);
-    if (!workspace || workspace_bytes < w.bytes || !msda::aligned_to(workspace, 256))
-        return failf(MSDA_ERR_WORKSPACE, "workspace of %zu bytes, 256-byte aligned, needed (got %zu)", w.bytes,
+    const bool tc = tc_type(dt, p) && tma_rows(query, p->query_stride, p->B, p->Q, p->M) &&
+                    tma_rows(key, p->key_stride, p->B, p->S, p->N) && tma_rows(value, p->value_stride, p->B, p->S, p->N) &&
+                    msda::aligned_to(grad_out, 16) && msda::aligned_to(grad_query, 16) && msda::aligned_to(grad_key, 16) &&
+                    msda::aligned_to(grad_value, 16);
+    const size_t need = msda_attention_backward_workspace_size(dt, flags, p);
+    const BackwardLayout w = backward_layout(dt, flags, p, tc);
+    if (!workspace || workspace_bytes < need || !msda::aligned_to(workspace, 256))
+        return failf(MSDA_ERR_WORKSPACE, "workspace of %zu bytes, 256-byte aligned, needed (got %zu)", need,
                      workspace_bytes);
     unsigned char* ws = static_cast<unsigned char*>(workspace);
     AttentionArgs a = args_of(flags, p, scale, query, key, value, key_mask, mask);
@@ -423,13 +432,50 @@ msda_status msda_attention_backward(msda_dtype dt, unsigned flags, const msda_at
     float* l2 = reinterpret_cast<float*>(ws + w.l2);
     float* dl = reinterpret_cast<float*>(ws + w.dl);
     a.row_l2 = l2, a.row_dl = dl;
-    if ((s = make_mask(a, mask_space(dt, flags, p), ws + w.mask, nullptr, st)) != MSDA_OK) return s;
+    msda::TcArgs t{};
+    if ((s = make_mask(a, mask_space(dt, flags, p), ws + w.mask, tc ? &t : nullptr, st)) != MSDA_OK) return s;
     {
         msda::TraceSpan ts(st);
         s = launched(MSDA_BY_DTYPE(dt, launch_attention_prepare, a, w.rows, out, lse, l2, dl, st),
                      "attention statistics kernel launch");
         ts.end(MSDA_KERNEL_ATTENTION_PREPARE, p->B * p->M * p->Q);
         if (s != MSDA_OK) return s;
+    }
+    if (tc) {
+        int sms;
+        if ((s = msda::device_facts(&a.err, &sms)) != MSDA_OK) return s;
+        if (dt == MSDA_F16) {
+            float* top = reinterpret_cast<float*>(ws + w.top);
+            msda::TraceSpan ts(st);
+            cudaError_t e = cudaMemsetAsync(top, 0, 8, st);
+            if (e == cudaSuccess) e = msda::launch_attention_amax(a, w.rows, top, st);
+            s = launched(e, "attention norms kernel launch");
+            ts.end(MSDA_KERNEL_ATTENTION_PREPARE, p->B * p->M * p->Q);
+            if (s != MSDA_OK) return s;
+            t.scale_in = top;
+        }
+        CUtensorMap mq, mk, mv, mg;
+        const int64_t row = p->M * p->D;
+        if (!rows_map(dt, query, p->D, 1, p->Q, p->M, p->B, a.q_sb, a.q_ss, a.q_sh, msda::kTcRows, &mq) ||
+            !rows_map(dt, key, p->D, 1, p->S, p->N, p->B, a.k_sb, a.k_ss, a.k_sh, msda::kTcRows, &mk) ||
+            !rows_map(dt, value, p->D, 1, p->S, p->N, p->B, a.v_sb, a.v_ss, a.v_sh, msda::kTcRows, &mv) ||
+            !rows_map(dt, grad_out, p->D, 1, p->Q, p->M, p->B, p->Q * row, row, p->D, msda::kTcRows, &mg))
+            return failf(MSDA_ERR_CUDA, "cuTensorMapEncodeTiled failed");
+        t.a = a;
+        t.G = 1, t.qpt = t.rows = msda::kTcRows, t.qblocks = w.rows.tiles;
+        t.fix_rows = a.causal && p->Q > p->S;
+        {
+            msda::TraceSpan ts(st);
+            s = launched(msda::launch_attention_tc_grad_key(t, dt == MSDA_BF16, mq, mk, mv, mg, st),
+                         "attention key gradient kernel launch");
+            ts.end(MSDA_KERNEL_ATTENTION_GRAD_KEY, p->B * p->N * p->S);
+            if (s != MSDA_OK) return s;
+        }
+        msda::TraceSpan ts(st);
+        s = launched(msda::launch_attention_tc_grad_query(t, dt == MSDA_BF16, mq, mk, mv, mg, st),
+                     "attention query gradient kernel launch");
+        ts.end(MSDA_KERNEL_ATTENTION_GRAD_QUERY, p->B * p->M * p->Q);
+        return s;
     }
     {
         msda::TraceSpan ts(st);

@@ -1,0 +1,694 @@
+// msda_attention_tc_backward.cu -- gradients of softmax attention on the tensor
+// cores (tcgen05, sm_103a), fp16 and bf16, D a multiple of 8 up to 128.
+//
+//   P = 2^(c S - l2),  dS = P (dP - delta),  dP = dO V^T
+//   dV = P^T dO,  dK = scale dS^T Q,  dQ = scale dS K
+//
+// Two kernels, each recomputing P: one a tile of 128 keys walking the queries
+// (S^T, dP^T, dV, dK: four products), one a tile of 128 queries walking the keys
+// (S, dP, dQ: three).  One kernel for all would need five products, not seven,
+// but its dQ is summed over blocks: 128 x D binary32 values a pair of tiles
+// through the L2's reductions, which take 4.2 TB/s here (14.5 bytes a cycle
+// and SM: 4500 cycles for 128 channels, against 1536 for the two products saved),
+// in an order that changes from run to run.  These two add in a fixed order.
+//
+// P^T and dS^T (16 bits) are operands in tensor memory, where a product with D
+// columns takes D/2 cycles (from shared memory it is bound by reading its
+// 128 x 16 operand: 32 + D/4).  Both are written over the scores they come from.
+// f16 would lose small values: P is scaled by 2^12 and dS by a power of two that the
+// largest norms of dO and V rows bound from above; the sums are scaled back.
+#include "msda_attention_tc.cuh"
+#include "msda_attention_tc_host.cuh"
+
+namespace msda {
+
+constexpr int kBwdThreads = 384;  // two warpgroups on the scores, one of copies, products and clearing
+
+// Exponents of the scalings: P 2^kp and dS 2^ks.
+struct TcScale {
+    float p, ds, inv_p, inv_ds;  // 2^kp as an offset of the exponent; 2^(ks - kp); 2^-kp; 2^-ks
+};
+template <bool BF16>
+__device__ __forceinline__ TcScale tc_scale(const TcArgs& p) {
+    TcScale r{0.f, 1.f, 1.f, 1.f};
+    if constexpr (!BF16) {
+        // |dS| <= 2 |dO row| |v row|: the power of two that brings this to 2^14 at most
+        const float top = 2.f * sqrtf(p.scale_in[0]) * sqrtf(p.scale_in[1]);
+        int ks = 0;
+        if (top > 0.f && top < 1e30f) ks = 14 - (int)ceilf(log2f(top));
+        ks = ks < -40 ? -40 : ks > 40 ? 40 : ks;
+        r.p = 12.f;
+        r.ds = exp2f((float)(ks - 12));
+        r.inv_p = 1.f / 4096.f;
+        r.inv_ds = exp2f((float)-ks);
+    }
+    return r;
+}
+
+struct TcBackwardSync {
+    uint64_t own, full[3], empty[3], ready[3];
+    uint64_t s_full, dp_full, p_ready, ds_ready, s_free, ds_done, acc;
+    uint32_t tmem, abort;
+    uint32_t words[4][4];
+};
+
+// ---- gradients of keys and values ----
+
+template <int NC>
+struct TcKeyCfg {
+    static constexpr int kStages = NC == 1 ? 3 : 2;
+    static constexpr uint32_t kTileBytes = NC * kTcTile;
+    static constexpr uint32_t kStatBytes = 1024;  // l2 and delta of 128 rows
+    static constexpr uint32_t kStageBytes = 2 * kTileBytes;
+    static constexpr size_t kSmem = 2 * kTileBytes + kStages * (kStageBytes + kStatBytes) + 1024;
+    static constexpr uint32_t kDV = 256, kDK = 256 + NC * 64;  // tensor memory: S 0, dP 128
+};
+
+template <bool BF16, int NC>
+__global__ void __launch_bounds__(kBwdThreads, 1)
+    msda_attention_tc_grad_key_kernel(const TcArgs p, const __grid_constant__ CUtensorMap map_q,
+                                      const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
+                                      const __grid_constant__ CUtensorMap map_do) {
+    using Cfg = TcKeyCfg<NC>;
+    constexpr int ST = Cfg::kStages;
+    const AttentionArgs& a = p.a;
+    extern __shared__ unsigned char tc_smem_raw[];
+    unsigned char* smem = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(tc_smem_raw) + 1023) & ~(uintptr_t)1023);
+    unsigned char* k_tile = smem;
+    unsigned char* v_tile = smem + Cfg::kTileBytes;
+    unsigned char* stages = smem + 2 * Cfg::kTileBytes;                            // Q, dO
+    float* stats = reinterpret_cast<float*>(stages + ST * Cfg::kStageBytes);       // l2[128], delta[128] a stage
+    __shared__ TcBackwardSync sy;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+    const int ktiles = (a.S + kTcRows - 1) / kTcRows;
+    long long id = blockIdx.x;
+    const int kt = (int)(id % ktiles);  // causal: the keys that most queries see come first
+    id /= ktiles;
+    const int n = (int)(id % a.N), b = (int)(id / a.N);
+    const int j0 = kt * kTcRows;
+    const uint8_t* km = a.key_mask ? a.key_mask + b * a.km_sb + n * a.km_sh : nullptr;
+    // row tiles that see a key of the tile: causal rows below j0 - (S - Q) see none
+    long long first_q = a.causal ? (long long)j0 - (a.S - a.Q) : 0;
+    const int r0 = first_q <= 0 ? 0 : (int)(first_q < a.Q ? first_q / kTcRows : p.qblocks);
+    const int per_head = p.qblocks - r0;
+    int nt = a.G * per_head;
+    if (km) {  // a tile of keys that take no part has no gradients
+        const bool any = tid < min(kTcRows, a.S - j0) && km[j0 + tid] != 0;
+        if (!__syncthreads_or(any)) nt = 0;
+    }
+
+    if (warp == 8) {
+        if (lane == 0) {
+            for (int i = 0; i < ST; ++i) {
+                tc_bar_init(tc_smem(&sy.full[i]), 1);
+                tc_bar_init(tc_smem(&sy.empty[i]), 1);
+                tc_bar_init(tc_smem(&sy.ready[i]), 1);
+            }
+            tc_bar_init(tc_smem(&sy.own), 1);
+            tc_bar_init(tc_smem(&sy.s_full), 1);
+            tc_bar_init(tc_smem(&sy.dp_full), 1);
+            tc_bar_init(tc_smem(&sy.p_ready), 8);
+            tc_bar_init(tc_smem(&sy.ds_ready), 8);
+            tc_bar_init(tc_smem(&sy.acc), 1);
+            tc_bar_init(tc_smem(&sy.s_free), 1);  // here: K and V are cleared
+            sy.abort = 0;
+            asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        }
+    } else if (warp == 9) {
+        tmem_alloc(tc_smem(&sy.tmem), 512);
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = sy.tmem;
+    volatile uint32_t* abort = &sy.abort;
+    const bool fix = km || p.fix_rows;  // operands that a warp clears before the products read them
+    bool ok = true;
+
+    if (warp < 8) {
+        // ---- probabilities and their gradients: thread = key row, 64 of a tile's 128 queries ----
+        const int w = warp >> 2, wl = warp & 3, row = wl * 32 + lane, j = j0 + row;
+        const uint32_t first = lane == 0;
+        const uint32_t lanes = (uint32_t)wl << 21;
+        const uint32_t s_at = tmem + w * 64 + lanes, dp_at = tmem + 128 + w * 64 + lanes;
+        const TcScale sc = tc_scale<BF16>(p);
+        const uint64_t c2 = tc_two(a.c2, a.c2), ds2 = tc_two(sc.ds, sc.ds);
+        const bool has_bits = p.bits_t != nullptr;
+        const int shift = a.S - a.Q;
+#pragma unroll 1
+        for (int i = 0; i < nt; ++i) {
+            const int g = i / per_head, rt = r0 + i - g * per_head, st = i % ST;
+            const int q0 = rt * kTcRows + w * 64;
+            uint2 bw = make_uint2(~0u, ~0u);
+            if (has_bits) {
+                if (j < a.S) bw = *reinterpret_cast<const uint2*>(p.bits_t + b * p.bits_t_sb + (n * a.G + g) * p.bits_t_sh +
+                                                                  (long long)j * p.Wq + rt * 4 + w * 2);
+            }
+            const float* l2 = stats + st * 256 + w * 64;
+            const float* dl = l2 + 128;
+            ok = tc_bar_wait(tc_smem(&sy.full[st]), (i / ST) & 1, abort, a.err) &&
+                 tc_bar_wait(tc_smem(&sy.s_full), i & 1, abort, a.err);
+            if (!ok) break;
+            tc_fence_after();
+            uint32_t s[2][32];
+            tmem_ld32(s[0], s_at);
+            tmem_ld32(s[1], s_at + 32);
+            tmem_wait_ld();
+            // causal: query q sees key j if q >= j - shift
+            const int lo = a.causal ? j - shift - q0 : 0;
+            if (__builtin_expect(has_bits || __any_sync(0xffffffffu, lo > 0), 0)) {
+                const uint32_t m0 = bw.x & ~tc_low_bits(lo), m1 = bw.y & ~tc_low_bits(lo - 32);
+                if (__any_sync(0xffffffffu, (m0 & m1) != 0xffffffffu)) {
+#pragma unroll
+                    for (int k = 0; k < 32; ++k) {
+                        if (!((m0 >> k) & 1u)) s[0][k] = 0xff800000u;
+                        if (!((m1 >> k) & 1u)) s[1][k] = 0xff800000u;
+                    }
+                }
+            }
+            // P^T over the thread's own columns of S^T
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                uint32_t pk[16];
+#pragma unroll
+                for (int k = 0; k < 32; k += 4) {
+                    const float4 l = *reinterpret_cast<const float4*>(l2 + c * 32 + k);
+                    float x0, x1, x2, x3;
+                    tc_split(tc_fma2(tc_two(__uint_as_float(s[c][k]), __uint_as_float(s[c][k + 1])), c2, tc_two(sc.p - l.x, sc.p - l.y)), x0, x1);
+                    tc_split(tc_fma2(tc_two(__uint_as_float(s[c][k + 2]), __uint_as_float(s[c][k + 3])), c2, tc_two(sc.p - l.z, sc.p - l.w)), x2, x3);
+                    const float e0 = tc_ex2(x0), e1 = tc_ex2(x1), e2 = tc_ex2(x2), e3 = tc_ex2(x3);
+                    s[c][k] = __float_as_uint(e0), s[c][k + 1] = __float_as_uint(e1);
+                    s[c][k + 2] = __float_as_uint(e2), s[c][k + 3] = __float_as_uint(e3);
+                    pk[k / 2] = tc_pack<BF16>(e0, e1);
+                    pk[k / 2 + 1] = tc_pack<BF16>(e2, e3);
+                }
+                tmem_st16(s_at + c * 16, pk);
+            }
+            tmem_wait_st();
+            tc_fence_before();
+            tc_bar_arrive_if(first, tc_smem(&sy.p_ready));
+            ok = tc_bar_wait(tc_smem(&sy.dp_full), i & 1, abort, a.err);
+            if (!ok) break;
+            tc_fence_after();
+            // dS^T over dP^T
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                uint32_t d[32], pk[16];
+                tmem_ld32(d, dp_at + c * 32);
+                tmem_wait_ld();
+#pragma unroll
+                for (int k = 0; k < 32; k += 4) {
+                    const float4 l = *reinterpret_cast<const float4*>(dl + c * 32 + k);
+                    float x0, x1, x2, x3;
+                    uint64_t y0 = tc_add2(tc_two(__uint_as_float(d[k]), __uint_as_float(d[k + 1])), tc_two(-l.x, -l.y));
+                    uint64_t y1 = tc_add2(tc_two(__uint_as_float(d[k + 2]), __uint_as_float(d[k + 3])), tc_two(-l.z, -l.w));
+                    y0 = tc_mul2(y0, tc_two(__uint_as_float(s[c][k]), __uint_as_float(s[c][k + 1])));
+                    y1 = tc_mul2(y1, tc_two(__uint_as_float(s[c][k + 2]), __uint_as_float(s[c][k + 3])));
+                    if constexpr (!BF16) y0 = tc_mul2(y0, ds2), y1 = tc_mul2(y1, ds2);
+                    tc_split(y0, x0, x1);
+                    tc_split(y1, x2, x3);
+                    pk[k / 2] = tc_pack<BF16>(x0, x1);
+                    pk[k / 2 + 1] = tc_pack<BF16>(x2, x3);
+                }
+                tmem_st16(dp_at + c * 16, pk);
+            }
+            tmem_wait_st();
+            tc_fence_before();
+            tc_bar_arrive_if(first, tc_smem(&sy.ds_ready));
+        }
+        // ---- dV (first warpgroup) and dK (second) ----
+        if (nt > 0 && ok) {
+            ok = tc_bar_wait(tc_smem(&sy.acc), 0, abort, a.err);
+            tc_fence_after();
+        }
+        if (ok) {
+            const bool live = nt > 0 && j < a.S && (!km || km[j]);
+            const float f = w == 0 ? sc.inv_p : sc.inv_ds * a.scale;
+            const uint32_t at = tmem + (w == 0 ? Cfg::kDV : Cfg::kDK) + lanes;
+            unsigned char* out = static_cast<unsigned char*>(w == 0 ? a.dv : a.dk) + (((long long)b * a.S + j) * a.N + n) * a.D * 2;
+            for (int c = 0; c < (a.D + 15) / 16; ++c) {
+                uint32_t o[16];
+                if (nt > 0) {
+                    tmem_ld16(o, at + c * 16);
+                    tmem_wait_ld();
+                }
+                if (j >= a.S) continue;
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    uint32_t v[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        v[e] = live ? tc_pack<BF16>(__uint_as_float(o[8 * k + 2 * e]) * f, __uint_as_float(o[8 * k + 2 * e + 1]) * f) : 0u;
+                    if (c * 16 + 8 * k < a.D) reinterpret_cast<uint4*>(out + c * 32)[k] = make_uint4(v[0], v[1], v[2], v[3]);
+                }
+            }
+        }
+    } else {
+        const int role = warp - 8;
+        uint64_t* full = fix ? sy.ready : sy.full;
+        if (role == 0 && lane == 0 && nt > 0) {
+            // ---- copies ----
+            const uint32_t own = tc_smem(&sy.own);
+            tc_bar_expect(own, 2 * Cfg::kTileBytes);
+            for (int c = 0; c < NC; ++c) {
+                tc_tma_5d(tc_smem(k_tile) + c * kTcTile, &map_k, own, c * 64, 0, j0, n, b);
+                tc_tma_5d(tc_smem(v_tile) + c * kTcTile, &map_v, own, c * 64, 0, j0, n, b);
+            }
+            for (int i = 0; i < nt; ++i) {
+                const int g = i / per_head, rt = r0 + i - g * per_head, st = i % ST, h = n * a.G + g;
+                if (i >= ST) ok = tc_bar_wait(tc_smem(&sy.empty[st]), (i / ST - 1) & 1, abort, a.err);
+                if (!ok) break;
+                const uint32_t bar = tc_smem(&sy.full[st]), at = tc_smem(stages) + st * Cfg::kStageBytes;
+                tc_bar_expect(bar, Cfg::kStageBytes + Cfg::kStatBytes);
+                for (int c = 0; c < NC; ++c) {
+                    tc_tma_5d(at + c * kTcTile, &map_q, bar, c * 64, 0, rt * kTcRows, h, b);
+                    tc_tma_5d(at + Cfg::kTileBytes + c * kTcTile, &map_do, bar, c * 64, 0, rt * kTcRows, h, b);
+                }
+                const long long r = (((long long)b * a.M + h) * p.qblocks + rt) * kTcRows;
+                tc_bulk(tc_smem(stats + st * 256), a.row_l2 + r, 512, bar);
+                tc_bulk(tc_smem(stats + st * 256 + 128), a.row_dl + r, 512, bar);
+            }
+        } else if (role == 1 && nt > 0) {
+            // ---- products ----
+            const uint32_t on = tc_elect();
+            const int steps = (a.D + 15) / 16;
+            const uint32_t id_s = tc_idesc(BF16, false, false, 128, 128), id_g = tc_idesc(BF16, false, true, 128, steps * 16);
+            const uint64_t k_desc = tc_desc(tc_smem(k_tile), 16, 1024), v_desc = tc_desc(tc_smem(v_tile), 16, 1024);
+            const uint32_t base = tc_smem(stages);
+            auto scores = [&](uint32_t d, uint64_t x_desc, uint32_t y) {  // 128 keys x 128 queries
+                const uint64_t y_desc = tc_desc(y, 16, 1024);
+#pragma unroll
+                for (int k = 0; k < NC * 4; ++k) {
+                    const uint64_t off = ((k >> 2) * kTcTile + (k & 3) * 32) >> 4;
+                    if (k < steps) tc_mma_ss(on, d, x_desc + off, y_desc + off, id_s, k > 0);
+                }
+            };
+            auto gradient = [&](uint32_t d, uint32_t x, uint32_t y, bool acc) {  // sums over 128 queries
+                const uint64_t y_desc = tc_desc(y, kTcTile, 1024);
+#pragma unroll
+                for (int k = 0; k < 8; ++k)  // 16 queries: the two warpgroups' halves lie 64 columns apart
+                    tc_mma_ts(on, d, x + (k >> 2) * 64 + (k & 3) * 8, y_desc + ((k * 2048) >> 4), id_g, acc || k > 0);
+            };
+            ok = tc_bar_wait(tc_smem(&sy.own), 0, abort, a.err);
+            if (ok && fix) ok = tc_bar_wait(tc_smem(&sy.s_free), 0, abort, a.err);  // K and V cleared
+            ok = ok && tc_bar_wait(tc_smem(&full[0]), 0, abort, a.err);
+            if (ok) {
+                tc_fence_after();
+                scores(tmem, k_desc, base);
+                tc_commit(on, tc_smem(&sy.s_full));
+                scores(tmem + 128, v_desc, base + Cfg::kTileBytes);
+                tc_commit(on, tc_smem(&sy.dp_full));
+            }
+            for (int i = 0; i < nt && ok; ++i) {
+                const int st = i % ST, sn = (i + 1) % ST;
+                const bool more = i + 1 < nt;
+                const uint32_t q_at = base + st * Cfg::kStageBytes, next = base + sn * Cfg::kStageBytes;
+                ok = tc_bar_wait(tc_smem(&sy.p_ready), i & 1, abort, a.err);
+                if (!ok) break;
+                tc_fence_after();
+                gradient(tmem + Cfg::kDV, tmem, q_at + Cfg::kTileBytes, i > 0);
+                if (more) {
+                    ok = tc_bar_wait(tc_smem(&full[sn]), ((i + 1) / ST) & 1, abort, a.err);
+                    if (!ok) break;
+                    tc_fence_after();
+                    scores(tmem, k_desc, next);
+                    tc_commit(on, tc_smem(&sy.s_full));
+                }
+                ok = tc_bar_wait(tc_smem(&sy.ds_ready), i & 1, abort, a.err);
+                if (!ok) break;
+                tc_fence_after();
+                gradient(tmem + Cfg::kDK, tmem + 128, q_at, i > 0);
+                tc_commit(on, tc_smem(&sy.empty[st]));
+                if (more) {
+                    scores(tmem + 128, v_desc, next + Cfg::kTileBytes);
+                    tc_commit(on, tc_smem(&sy.dp_full));
+                } else {
+                    tc_commit(on, tc_smem(&sy.acc));
+                }
+            }
+        } else if (role == 2 && fix && nt > 0) {
+            // ---- keys, and rows without keys, that take no part ----
+            ok = tc_bar_wait(tc_smem(&sy.own), 0, abort, a.err);
+            if (ok) {
+                if (km) {
+                    uint32_t w[4];
+                    tc_key_words(km + j0, a.S - j0, lane, w);
+                    tc_clear_rows<NC>(k_tile, w, lane);
+                    tc_clear_rows<NC>(v_tile, w, lane);
+                    tc_fence_async();
+                }
+                __syncwarp();
+                if (lane == 0) tc_bar_arrive(tc_smem(&sy.s_free));
+            }
+            for (int i = 0; i < nt && ok; ++i) {
+                const int st = i % ST;
+                ok = tc_bar_wait(tc_smem(&sy.full[st]), (i / ST) & 1, abort, a.err);
+                if (!ok) break;
+                uint32_t w[4];
+#pragma unroll
+                for (int c = 0; c < 4; ++c) w[c] = __ballot_sync(0xffffffffu, stats[st * 256 + c * 32 + lane] != attn_inf());
+                if ((w[0] & w[1] & w[2] & w[3]) != 0xffffffffu) {
+                    tc_clear_rows<NC>(stages + st * Cfg::kStageBytes, w, lane);
+                    tc_clear_rows<NC>(stages + st * Cfg::kStageBytes + Cfg::kTileBytes, w, lane);
+                    tc_fence_async();
+                }
+                __syncwarp();
+                if (lane == 0) tc_bar_arrive(tc_smem(&sy.ready[st]));
+            }
+        }
+        __syncwarp();
+    }
+    if (!ok) tc_drain();
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 9) tmem_dealloc(tmem, 512);
+}
+
+// ---- gradient of queries ----
+
+template <int NC>
+struct TcQueryCfg {
+    static constexpr int kStages = NC == 1 ? 3 : 2;
+    static constexpr uint32_t kTileBytes = NC * kTcTile;
+    static constexpr uint32_t kStageBytes = 2 * kTileBytes;  // K, V
+    static constexpr size_t kSmem = 2 * kTileBytes + kStages * kStageBytes + 1024;
+    static constexpr uint32_t kDS = 256, kDQ = 320;  // tensor memory: S 0, dP 128
+};
+
+template <bool BF16, int NC>
+__global__ void __launch_bounds__(kBwdThreads, 1)
+    msda_attention_tc_grad_query_kernel(const TcArgs p, const __grid_constant__ CUtensorMap map_q,
+                                        const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
+                                        const __grid_constant__ CUtensorMap map_do) {
+    using Cfg = TcQueryCfg<NC>;
+    constexpr int ST = Cfg::kStages;
+    const AttentionArgs& a = p.a;
+    extern __shared__ unsigned char tc_smem_raw[];
+    unsigned char* smem = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(tc_smem_raw) + 1023) & ~(uintptr_t)1023);
+    unsigned char* q_tile = smem;
+    unsigned char* do_tile = smem + Cfg::kTileBytes;
+    unsigned char* stages = smem + 2 * Cfg::kTileBytes;
+    __shared__ TcBackwardSync sy;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+    long long id = blockIdx.x;
+    int rt = (int)(id % p.qblocks);
+    id /= p.qblocks;
+    const int h = (int)(id % a.M), b = (int)(id / a.M), n = h / a.G;
+    if (a.causal) rt = p.qblocks - 1 - rt;
+    const int q0 = rt * kTcRows;
+    const uint8_t* km = a.key_mask ? a.key_mask + b * a.km_sb + n * a.km_sh : nullptr;
+    int t0 = 0, t1 = (tc_seen(a, min(q0 + kTcRows, a.Q) - 1) + kTcRows - 1) / kTcRows;
+    if (km) tc_trim(km, a.S, &t0, &t1);
+    const int nt = max(0, t1 - t0);
+
+    if (warp == 8) {
+        if (lane == 0) {
+            for (int i = 0; i < ST; ++i) {
+                tc_bar_init(tc_smem(&sy.full[i]), 1);
+                tc_bar_init(tc_smem(&sy.empty[i]), 1);
+                tc_bar_init(tc_smem(&sy.ready[i]), 1);
+            }
+            tc_bar_init(tc_smem(&sy.own), 1);
+            tc_bar_init(tc_smem(&sy.s_full), 1);
+            tc_bar_init(tc_smem(&sy.s_free), 8);
+            tc_bar_init(tc_smem(&sy.ds_ready), 8);
+            tc_bar_init(tc_smem(&sy.ds_done), 1);
+            sy.abort = 0;
+            asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        }
+    } else if (warp == 9) {
+        tmem_alloc(tc_smem(&sy.tmem), 512);
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = sy.tmem;
+    volatile uint32_t* abort = &sy.abort;
+    bool ok = true;
+
+    if (warp < 8) {
+        // thread = query row, 64 of a tile's 128 keys
+        const int w = warp >> 2, wl = warp & 3, row = wl * 32 + lane, q = q0 + row;
+        const uint32_t first = lane == 0;
+        const uint32_t lanes = (uint32_t)wl << 21;
+        const uint32_t s_at = tmem + w * 64 + lanes, dp_at = tmem + 128 + w * 64 + lanes, ds_at = tmem + Cfg::kDS + w * 32 + lanes;
+        const TcScale sc = tc_scale<BF16>(p);
+        const long long r = (((long long)b * a.M + h) * p.qblocks + rt) * kTcRows + row;
+        const float l2 = a.row_l2[r], dl = a.row_dl[r];
+        const bool live = l2 != attn_inf();  // q < Q and some key seen
+        const int seen = live ? tc_seen(a, q) : 0;
+        const int seen_least = __reduce_min_sync(0xffffffffu, live ? seen : a.S);
+        const uint32_t* bits = p.bits && q < a.Q ? p.bits + b * p.bits_sb + h * p.bits_sh + (long long)q * p.W : nullptr;
+        const uint64_t c2 = tc_two(a.c2, a.c2), nl = tc_two(sc.p - l2, sc.p - l2), nd = tc_two(-dl, -dl), ds2 = tc_two(sc.ds, sc.ds);
+#pragma unroll 1
+        for (int i = 0; i < nt; ++i) {
+            const int j0 = (t0 + i) * kTcRows + w * 64;
+            uint2 bw = make_uint2(~0u, ~0u);
+            if (bits) bw = *reinterpret_cast<const uint2*>(bits + (t0 + i) * 4 + w * 2);
+            ok = tc_bar_wait(tc_smem(&sy.s_full), i & 1, abort, a.err);
+            if (!ok) break;
+            tc_fence_after();
+            uint32_t s[2][32], d[2][32];
+            tmem_ld32(s[0], s_at);
+            tmem_ld32(s[1], s_at + 32);
+            tmem_ld32(d[0], dp_at);
+            tmem_ld32(d[1], dp_at + 32);
+            tmem_wait_ld();
+            tc_fence_before();
+            tc_bar_arrive_if(first, tc_smem(&sy.s_free));
+            if (__builtin_expect(km || p.bits || seen_least - j0 < 64, 0)) {
+                const int see = seen - j0;
+                uint32_t m0 = bw.x & tc_low_bits(see), m1 = bw.y & tc_low_bits(see - 32);
+                if (km) m0 &= sy.words[i & 3][w * 2], m1 &= sy.words[i & 3][w * 2 + 1];
+                if (__any_sync(0xffffffffu, (m0 & m1) != 0xffffffffu)) {
+#pragma unroll
+                    for (int k = 0; k < 32; ++k) {
+                        if (!((m0 >> k) & 1u)) s[0][k] = 0xff800000u;
+                        if (!((m1 >> k) & 1u)) s[1][k] = 0xff800000u;
+                    }
+                }
+            }
+            if (i > 0) {  // dS(i-1) is used up
+                ok = tc_bar_wait(tc_smem(&sy.ds_done), (i - 1) & 1, abort, a.err);
+                if (!ok) break;
+                tc_fence_after();
+            }
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                uint32_t pk[16];
+#pragma unroll
+                for (int k = 0; k < 32; k += 2) {
+                    float x0, x1;
+                    tc_split(tc_fma2(tc_two(__uint_as_float(s[c][k]), __uint_as_float(s[c][k + 1])), c2, nl), x0, x1);
+                    const uint64_t e = tc_two(tc_ex2(x0), tc_ex2(x1));
+                    uint64_t y = tc_mul2(tc_add2(tc_two(__uint_as_float(d[c][k]), __uint_as_float(d[c][k + 1])), nd), e);
+                    if constexpr (!BF16) y = tc_mul2(y, ds2);
+                    tc_split(y, x0, x1);
+                    pk[k / 2] = tc_pack<BF16>(x0, x1);
+                }
+                tmem_st16(ds_at + c * 16, pk);
+            }
+            tmem_wait_st();
+            tc_fence_before();
+            tc_bar_arrive_if(first, tc_smem(&sy.ds_ready));
+        }
+        if (nt > 0 && ok) {
+            ok = tc_bar_wait(tc_smem(&sy.ds_done), (nt - 1) & 1, abort, a.err);
+            tc_fence_after();
+        }
+        if (ok) {  // the two warpgroups take alternate chunks of 16 channels
+            const float f = sc.inv_ds * a.scale;
+            unsigned char* out = static_cast<unsigned char*>(a.dq) + (((long long)b * a.Q + q) * a.M + h) * a.D * 2;
+            for (int c = w; c < (a.D + 15) / 16; c += 2) {
+                uint32_t o[16];
+                if (nt > 0) {
+                    tmem_ld16(o, tmem + Cfg::kDQ + lanes + c * 16);
+                    tmem_wait_ld();
+                }
+                if (q >= a.Q) continue;
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    uint32_t v[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        v[e] = live && nt > 0 ? tc_pack<BF16>(__uint_as_float(o[8 * k + 2 * e]) * f, __uint_as_float(o[8 * k + 2 * e + 1]) * f) : 0u;
+                    if (c * 16 + 8 * k < a.D) reinterpret_cast<uint4*>(out + c * 32)[k] = make_uint4(v[0], v[1], v[2], v[3]);
+                }
+            }
+        }
+    } else {
+        const int role = warp - 8;
+        uint64_t* full = km ? sy.ready : sy.full;
+        if (role == 0 && lane == 0 && nt > 0) {
+            const uint32_t own = tc_smem(&sy.own);
+            tc_bar_expect(own, 2 * Cfg::kTileBytes);
+            for (int c = 0; c < NC; ++c) {
+                tc_tma_5d(tc_smem(q_tile) + c * kTcTile, &map_q, own, c * 64, 0, q0, h, b);
+                tc_tma_5d(tc_smem(do_tile) + c * kTcTile, &map_do, own, c * 64, 0, q0, h, b);
+            }
+            for (int i = 0; i < nt; ++i) {
+                const int st = i % ST;
+                if (i >= ST) ok = tc_bar_wait(tc_smem(&sy.empty[st]), (i / ST - 1) & 1, abort, a.err);
+                if (!ok) break;
+                const uint32_t bar = tc_smem(&sy.full[st]), at = tc_smem(stages) + st * Cfg::kStageBytes;
+                tc_bar_expect(bar, Cfg::kStageBytes);
+                for (int c = 0; c < NC; ++c) {
+                    tc_tma_5d(at + c * kTcTile, &map_k, bar, c * 64, 0, (t0 + i) * kTcRows, n, b);
+                    tc_tma_5d(at + Cfg::kTileBytes + c * kTcTile, &map_v, bar, c * 64, 0, (t0 + i) * kTcRows, n, b);
+                }
+            }
+        } else if (role == 1 && nt > 0) {
+            const uint32_t on = tc_elect();
+            const int steps = (a.D + 15) / 16;
+            const uint32_t id_s = tc_idesc(BF16, false, false, 128, 128), id_g = tc_idesc(BF16, false, true, 128, steps * 16);
+            const uint64_t q_desc = tc_desc(tc_smem(q_tile), 16, 1024), do_desc = tc_desc(tc_smem(do_tile), 16, 1024);
+            const uint32_t base = tc_smem(stages);
+            auto scores = [&](int st) {  // S = Q K^T, dP = dO V^T
+                const uint64_t k_desc = tc_desc(base + st * Cfg::kStageBytes, 16, 1024);
+                const uint64_t v_desc = tc_desc(base + st * Cfg::kStageBytes + Cfg::kTileBytes, 16, 1024);
+#pragma unroll
+                for (int k = 0; k < NC * 4; ++k) {
+                    const uint64_t off = ((k >> 2) * kTcTile + (k & 3) * 32) >> 4;
+                    if (k < steps) {
+                        tc_mma_ss(on, tmem, q_desc + off, k_desc + off, id_s, k > 0);
+                        tc_mma_ss(on, tmem + 128, do_desc + off, v_desc + off, id_s, k > 0);
+                    }
+                }
+                tc_commit(on, tc_smem(&sy.s_full));
+            };
+            ok = tc_bar_wait(tc_smem(&sy.own), 0, abort, a.err) && tc_bar_wait(tc_smem(&full[0]), 0, abort, a.err);
+            if (ok) {
+                tc_fence_after();
+                scores(0);
+            }
+            for (int i = 0; i < nt && ok; ++i) {
+                const int st = i % ST, sn = (i + 1) % ST;
+                if (i + 1 < nt) {
+                    ok = tc_bar_wait(tc_smem(&full[sn]), ((i + 1) / ST) & 1, abort, a.err) &&
+                         tc_bar_wait(tc_smem(&sy.s_free), i & 1, abort, a.err);
+                    if (!ok) break;
+                    tc_fence_after();
+                    scores(sn);
+                }
+                ok = tc_bar_wait(tc_smem(&sy.ds_ready), i & 1, abort, a.err);
+                if (!ok) break;
+                tc_fence_after();
+                const uint64_t k_desc = tc_desc(base + st * Cfg::kStageBytes, kTcTile, 1024);
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    tc_mma_ts(on, tmem + Cfg::kDQ, tmem + Cfg::kDS + k * 8, k_desc + ((k * 2048) >> 4), id_g, i > 0 || k > 0);
+                tc_commit(on, tc_smem(&sy.ds_done));
+                tc_commit(on, tc_smem(&sy.empty[st]));
+            }
+        } else if (role == 2 && km && nt > 0) {
+            for (int i = 0; i < nt && ok; ++i) {
+                const int st = i % ST, j0 = (t0 + i) * kTcRows;
+                uint32_t w[4];
+                tc_key_words(km + j0, a.S - j0, lane, w);
+                if (lane < 4) sy.words[i & 3][lane] = lane == 0 ? w[0] : lane == 1 ? w[1] : lane == 2 ? w[2] : w[3];
+                ok = tc_bar_wait(tc_smem(&sy.full[st]), (i / ST) & 1, abort, a.err);
+                if (!ok) break;
+                if ((w[0] & w[1] & w[2] & w[3]) != 0xffffffffu) {
+                    tc_clear_rows<NC>(stages + st * Cfg::kStageBytes, w, lane);
+                    tc_clear_rows<NC>(stages + st * Cfg::kStageBytes + Cfg::kTileBytes, w, lane);
+                    tc_fence_async();
+                }
+                __syncwarp();
+                if (lane == 0) tc_bar_arrive(tc_smem(&sy.ready[st]));
+            }
+        }
+        __syncwarp();
+    }
+    if (!ok) tc_drain();
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 9) tmem_dealloc(tmem, 512);
+}
+
+// f16: the largest squared norms of the gradient's rows that take part and of
+// the values that a query may see (as bits of non-negative binary32 numbers,
+// whose order is that of integers).  Eight lanes a row.
+__global__ void __launch_bounds__(256) msda_attention_amax_kernel(const AttentionArgs a, const AttentionRows rw, float* top) {
+    const long long rows = (long long)a.B * rw.N * rw.tiles * rw.rt, keys = (long long)a.B * a.S * a.N;
+    const int lane = threadIdx.x & 7;
+    const long long step = (long long)gridDim.x * 32;
+    float best[2] = {0.f, 0.f};
+    for (long long i = (long long)blockIdx.x * 32 + (threadIdx.x >> 3); i < (rows + keys + 3) / 4 * 4; i += step) {
+        const __half* x = nullptr;
+        if (i < rows) {
+            if (a.row_l2[i] != attn_inf()) {
+                const long long bt = i / rw.rt, bn = bt / rw.tiles, b = bn / rw.N;
+                const long long q = (bt - bn * rw.tiles) * rw.qpt + (i - bt * rw.rt), m = bn - b * rw.N;
+                x = static_cast<const __half*>(a.dout) + ((b * a.Q + q) * a.M + m) * a.D;
+            }
+        } else if (i < rows + keys) {
+            const long long e = i - rows, bs = e / a.N, b = bs / a.S;
+            const long long j = bs - b * a.S;
+            const int n = (int)(e - bs * a.N);
+            if (!a.key_mask || a.key_mask[b * a.km_sb + n * a.km_sh + j])
+                x = static_cast<const __half*>(a.v) + b * a.v_sb + j * a.v_ss + n * a.v_sh;
+        }
+        float s = 0.f;
+        if (x)
+            for (int c = lane * 8; c < a.D; c += 64) {  // 16-byte rows: D is a multiple of 8
+                const uint4 u = *reinterpret_cast<const uint4*>(x + c);
+                const uint32_t v[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&v[k]));
+                    s = fmaf(f.x, f.x, fmaf(f.y, f.y, s));
+                }
+            }
+        for (int o = 4; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+        // a NaN or infinity leaves the scaling at 1 (its bits are above every number's)
+        best[i < rows ? 0 : 1] = s != s ? s : best[i < rows ? 0 : 1] != best[i < rows ? 0 : 1] ? best[i < rows ? 0 : 1] : fmaxf(best[i < rows ? 0 : 1], s);
+    }
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        const unsigned u = __reduce_max_sync(0xffffffffu, __float_as_uint(best[k]) & 0x7fffffffu);
+        if ((threadIdx.x & 31) == 0 && u) atomicMax(reinterpret_cast<unsigned*>(top) + k, u);
+    }
+}
+
+// ---- host ----
+
+template <bool BF16, int NC>
+static cudaError_t grad_key_go(const TcArgs& p, const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v,
+                               const CUtensorMap& g, cudaStream_t st) {
+    constexpr size_t smem = TcKeyCfg<NC>::kSmem;
+    cudaError_t e = cudaFuncSetAttribute(msda_attention_tc_grad_key_kernel<BF16, NC>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    const long long grid = (long long)p.a.B * p.a.N * ((p.a.S + kTcRows - 1) / kTcRows);
+    msda_attention_tc_grad_key_kernel<BF16, NC><<<(unsigned)grid, kBwdThreads, smem, st>>>(p, q, k, v, g);
+    return cudaGetLastError();
+}
+template <bool BF16, int NC>
+static cudaError_t grad_query_go(const TcArgs& p, const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v,
+                                 const CUtensorMap& g, cudaStream_t st) {
+    constexpr size_t smem = TcQueryCfg<NC>::kSmem;
+    cudaError_t e = cudaFuncSetAttribute(msda_attention_tc_grad_query_kernel<BF16, NC>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    const long long grid = (long long)p.a.B * p.a.M * p.qblocks;
+    msda_attention_tc_grad_query_kernel<BF16, NC><<<(unsigned)grid, kBwdThreads, smem, st>>>(p, q, k, v, g);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_attention_tc_grad_key(const TcArgs& p, bool bf16, const CUtensorMap& q, const CUtensorMap& k,
+                                         const CUtensorMap& v, const CUtensorMap& g, cudaStream_t st) {
+    if (p.a.D > 64) return bf16 ? grad_key_go<true, 2>(p, q, k, v, g, st) : grad_key_go<false, 2>(p, q, k, v, g, st);
+    return bf16 ? grad_key_go<true, 1>(p, q, k, v, g, st) : grad_key_go<false, 1>(p, q, k, v, g, st);
+}
+cudaError_t launch_attention_tc_grad_query(const TcArgs& p, bool bf16, const CUtensorMap& q, const CUtensorMap& k,
+                                           const CUtensorMap& v, const CUtensorMap& g, cudaStream_t st) {
+    if (p.a.D > 64) return bf16 ? grad_query_go<true, 2>(p, q, k, v, g, st) : grad_query_go<false, 2>(p, q, k, v, g, st);
+    return bf16 ? grad_query_go<true, 1>(p, q, k, v, g, st) : grad_query_go<false, 1>(p, q, k, v, g, st);
+}
+cudaError_t launch_attention_amax(const AttentionArgs& a, const AttentionRows& rw, float* top, cudaStream_t st) {
+    const long long rows = ((long long)a.B * rw.N * rw.tiles * rw.rt + (long long)a.B * a.S * a.N + 31) / 32;
+    msda_attention_amax_kernel<<<(unsigned)(rows < 152 * 8 ? rows : 152 * 8), 256, 0, st>>>(a, rw, top);
+    return cudaGetLastError();
+}
+
+}  // namespace msda
