@@ -436,24 +436,20 @@ msda_status msda_attention_backward(msda_dtype dt, unsigned flags, const msda_at
     if ((s = make_mask(a, mask_space(dt, flags, p), ws + w.mask, tc ? &t : nullptr, st)) != MSDA_OK) return s;
     {
         msda::TraceSpan ts(st);
-        s = launched(MSDA_BY_DTYPE(dt, launch_attention_prepare, a, w.rows, out, lse, l2, dl, st),
-                     "attention statistics kernel launch");
+        const bool half = tc && dt == MSDA_F16;
+        float* top = half ? reinterpret_cast<float*>(ws + w.top) : nullptr;
+        t.scale_in = top;
+        cudaError_t e = half ? cudaMemsetAsync(top, 0, 8, st) : cudaSuccess;
+        if (e == cudaSuccess)
+            e = MSDA_BY_DTYPE(dt, launch_attention_prepare, a, w.rows, out, lse, half ? msda::kHalfScale : 0.f, l2, dl, top,
+                              tc && msda::aligned_to(out, 16), st);
+        s = launched(e, "attention statistics kernel launch");
         ts.end(MSDA_KERNEL_ATTENTION_PREPARE, p->B * p->M * p->Q);
         if (s != MSDA_OK) return s;
     }
     if (tc) {
         int sms;
         if ((s = msda::device_facts(&a.err, &sms)) != MSDA_OK) return s;
-        if (dt == MSDA_F16) {
-            float* top = reinterpret_cast<float*>(ws + w.top);
-            msda::TraceSpan ts(st);
-            cudaError_t e = cudaMemsetAsync(top, 0, 8, st);
-            if (e == cudaSuccess) e = msda::launch_attention_amax(a, w.rows, top, st);
-            s = launched(e, "attention norms kernel launch");
-            ts.end(MSDA_KERNEL_ATTENTION_PREPARE, p->B * p->M * p->Q);
-            if (s != MSDA_OK) return s;
-            t.scale_in = top;
-        }
         CUtensorMap mq, mk, mv, mg;
         const int64_t row = p->M * p->D;
         if (!rows_map(dt, query, p->D, 1, p->Q, p->M, p->B, a.q_sb, a.q_ss, a.q_sh, msda::kTcRows, &mq) ||

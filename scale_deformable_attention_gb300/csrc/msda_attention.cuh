@@ -32,9 +32,8 @@ struct AttentionArgs {
     int splits, tiles_per_split;
     // backward
     const void* dout;     // [B, Q, M, D]
-    const float* row_l2;  // lse * log2(e) of the kernels' rows, +inf where a row takes no part
-    const float* row_dl;  // delta = sum_d dout * out of the kernels' rows
-    const float* amax;    // fp16: largest squared norms of dout rows and of value rows (else null)
+    const float* row_l2;  // -lse * log2(e) of the kernels' rows (f16 on the tensor cores: + kHalfScale), -inf where a row takes no part
+    const float* row_dl;  // -delta, delta = sum_d dout * out of the kernels' rows
     void *dq, *dk, *dv;   // [B, Q, M, D], [B, S, N, D], [B, S, N, D]
     unsigned* err;
 };
@@ -45,6 +44,10 @@ struct AttentionRows {
     int rt, qpt, tiles;  // rows a tile, queries a tile, tiles
     int N, G;            // heads with rows of their own, heads sharing them
 };
+
+// f16 on the tensor cores: probabilities are held times 2^12 (at most 4096; what
+// lies under 2^-26 of a row's sum would otherwise fall below f16's steps)
+constexpr float kHalfScale = 12.f;
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;

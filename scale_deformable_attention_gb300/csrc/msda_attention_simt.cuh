@@ -250,15 +250,15 @@ __global__ void __launch_bounds__(kSimtThreads) msda_attention_simt_kernel(const
 }
 
 // p and ds of a tile: s in, on return s = p and dp = p (dp - delta), each 0
-// where the pair takes no part.  Rows' statistics: l2 (+inf: no part), dl.
+// where the pair takes no part.  Rows' statistics: l2 = -lse (-inf: no part), dl = -delta.
 __device__ __forceinline__ void simt_prob_grad(float (&s)[8][4], float (&dp)[8][4], const float* l2, const float* dl) {
 #pragma unroll
     for (int i = 0; i < 8; ++i)
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
-            const float p = s[i][c] == -attn_inf() ? 0.f : exp2f(s[i][c] - l2[i]);
+            const float p = s[i][c] == -attn_inf() ? 0.f : exp2f(s[i][c] + l2[i]);
             s[i][c] = p;
-            dp[i][c] = p == 0.f ? 0.f : p * (dp[i][c] - dl[i]);
+            dp[i][c] = p == 0.f ? 0.f : p * (dp[i][c] + dl[i]);
         }
 }
 
@@ -296,7 +296,7 @@ __global__ void __launch_bounds__(kSimtThreads) msda_attention_simt_grad_key_ker
             const float* l2p = a.row_l2 + ((long long)(b * rw.N + m) * rw.tiles + q0 / 64) * 64;
             const float* dlp = a.row_dl + ((long long)(b * rw.N + m) * rw.tiles + q0 / 64) * 64;
             __syncthreads();
-            if (threadIdx.x < 64) live[threadIdx.x] = l2p[threadIdx.x] != attn_inf();
+            if (threadIdx.x < 64) live[threadIdx.x] = l2p[threadIdx.x] != -attn_inf();
             __syncthreads();
             simt_load<T, DP>(Qs, static_cast<const T*>(a.q) + b * a.q_sb + m * a.q_sh + q0 * a.q_ss, a.q_ss, a.Q - q0,
                              a.D, vec, live);
@@ -439,35 +439,85 @@ __global__ void __launch_bounds__(128) msda_attention_join_kernel(const Attentio
     if (lane == 0) a.lse[row] = sum == 0.f ? -attn_inf() : (ref + log2f(sum)) * kLn2;
 }
 
-// Statistics of the backward's rows: lse in log2 units (+inf where the row
-// takes no part or is padding) and delta = <dout, out>.  Eight lanes a row.
+// Statistics of the backward's rows: `off` - lse in log2 units (-inf where the
+// row takes no part or is padding) and -<dout, out>.  Eight lanes a row.
+// With `top` (f16 on the tensor cores) also the largest squared norms of the
+// rows of dout that take part, top[0], and of the values that a query may see,
+// top[1]; cleared before, taken as bits: non-negative numbers are in the order
+// of their bits, so the order of the atomics changes nothing.
 template <typename T>
 __global__ void __launch_bounds__(256) msda_attention_prepare_kernel(const AttentionArgs a, const AttentionRows rw,
-                                                                     const void* out_, const float* lse, float* l2,
-                                                                     float* dl) {
-    const long long total = (long long)a.B * rw.N * rw.tiles * rw.rt;
+                                                                     const void* out_, const float* lse, float off,
+                                                                     float* l2, float* dl, float* top, bool vec) {
+    const long long rows = (long long)a.B * rw.N * rw.tiles * rw.rt;
+    const long long total = rows + (top ? (long long)a.B * a.S * a.N : 0);
     const int lane = threadIdx.x & 7;
+    float best_g = 0.f, best_v = 0.f;
     for (long long i = (long long)blockIdx.x * 32 + (threadIdx.x >> 3); i < (total + 3) / 4 * 4; i += (long long)gridDim.x * 32) {
-        const long long bt = i / rw.rt;
-        const int r = (int)(i - bt * rw.rt);
-        const long long bn = bt / rw.tiles;
-        const int q = (int)(bt - bn * rw.tiles) * rw.qpt + r / rw.G;
-        const int b = (int)(bn / rw.N), m = (int)(bn - (long long)b * rw.N) * rw.G + r % rw.G;
-        bool on = i < total && r < rw.qpt * rw.G && q < a.Q;
-        float x = on ? lse[((long long)b * a.M + m) * a.Q + q] : -attn_inf();
-        on = on && x != -attn_inf();
-        float d = 0.f;
-        if (on) {
-            const long long at = (((long long)b * a.Q + q) * a.M + m) * a.D;
-            const T* g = static_cast<const T*>(a.dout) + at;
-            const T* o = static_cast<const T*>(out_) + at;
-            for (int c = lane; c < a.D; c += 8) d = fmaf(attn_f32(g[c]), attn_f32(o[c]), d);
+        const T* g = nullptr;
+        const T* o = nullptr;
+        float x = 0.f;
+        if (i < rows) {
+            const long long bt = i / rw.rt;
+            const int r = (int)(i - bt * rw.rt);
+            const long long bn = bt / rw.tiles;
+            const int q = (int)(bt - bn * rw.tiles) * rw.qpt + r / rw.G;
+            const int b = (int)(bn / rw.N), m = (int)(bn - (long long)b * rw.N) * rw.G + r % rw.G;
+            if (r < rw.qpt * rw.G && q < a.Q) {
+                x = lse[((long long)b * a.M + m) * a.Q + q];
+                if (x != -attn_inf()) {
+                    const long long at = (((long long)b * a.Q + q) * a.M + m) * a.D;
+                    g = static_cast<const T*>(a.dout) + at;
+                    o = static_cast<const T*>(out_) + at;
+                }
+            }
+        } else if (i < total) {
+            const long long e = i - rows, bs = e / a.N, b = bs / a.S, j = bs - b * a.S;
+            const int n = (int)(e - bs * a.N);
+            if (!a.key_mask || a.key_mask[b * a.km_sb + n * a.km_sh + j])
+                g = static_cast<const T*>(a.v) + b * a.v_sb + j * a.v_ss + n * a.v_sh;
         }
-        for (int s = 4; s > 0; s >>= 1) d += __shfl_xor_sync(0xffffffffu, d, s);
-        if (lane == 0 && i < total) {
-            l2[i] = on ? x * kLog2e : attn_inf();
-            dl[i] = on ? d : 0.f;
+        float d = 0.f, gg = 0.f;
+        if (g) {
+            if (sizeof(T) == 2 && vec) {  // rows of whole 16-byte vectors
+                for (int c = lane * 8; c < a.D; c += 64) {
+                    alignas(16) T gv[8], ov[8];
+                    *reinterpret_cast<uint4*>(gv) = *reinterpret_cast<const uint4*>(g + c);
+                    if (o) *reinterpret_cast<uint4*>(ov) = *reinterpret_cast<const uint4*>(o + c);
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        const float y = attn_f32(gv[k]);
+                        gg = fmaf(y, y, gg);
+                        if (o) d = fmaf(y, attn_f32(ov[k]), d);
+                    }
+                }
+            } else {
+                for (int c = lane; c < a.D; c += 8) {
+                    const float y = attn_f32(g[c]);
+                    gg = fmaf(y, y, gg);
+                    if (o) d = fmaf(y, attn_f32(o[c]), d);
+                }
+            }
         }
+        for (int s = 4; s > 0; s >>= 1) {
+            d += __shfl_xor_sync(0xffffffffu, d, s);
+            gg += __shfl_xor_sync(0xffffffffu, gg, s);
+        }
+        if (i < rows) {
+            if (lane == 0) {
+                l2[i] = g ? off - x * kLog2e : -attn_inf();
+                dl[i] = g ? -d : 0.f;
+            }
+            best_g = gg > best_g || gg != gg ? gg : best_g;
+        } else {
+            best_v = gg > best_v || gg != gg ? gg : best_v;
+        }
+    }
+    if (top) {
+        const unsigned ug = __reduce_max_sync(0xffffffffu, __float_as_uint(best_g) & 0x7fffffffu);
+        const unsigned uv = __reduce_max_sync(0xffffffffu, __float_as_uint(best_v) & 0x7fffffffu);
+        if ((threadIdx.x & 31) == 0 && ug) atomicMax(reinterpret_cast<unsigned*>(top), ug);
+        if ((threadIdx.x & 31) == 0 && uv) atomicMax(reinterpret_cast<unsigned*>(top) + 1, uv);
     }
 }
 
@@ -482,7 +532,7 @@ template <typename T>
 cudaError_t launch_attention_join(const AttentionArgs& a, cudaStream_t st);
 template <typename T>
 cudaError_t launch_attention_prepare(const AttentionArgs& a, const AttentionRows& rw, const void* out, const float* lse,
-                                     float* l2, float* dl, cudaStream_t st);
+                                     float off, float* l2, float* dl, float* top, bool vec, cudaStream_t st);
 
 #ifdef MSDA_ATTENTION_SIMT_INSTANTIATE
 // head channels padded to a multiple of the 16 lanes that share a row
@@ -548,10 +598,10 @@ cudaError_t launch_attention_join(const AttentionArgs& a, cudaStream_t st) {
 }
 template <typename T>
 cudaError_t launch_attention_prepare(const AttentionArgs& a, const AttentionRows& rw, const void* out, const float* lse,
-                                     float* l2, float* dl, cudaStream_t st) {
-    const long long blocks = ((long long)a.B * rw.N * rw.tiles * rw.rt + 31) / 32;
+                                     float off, float* l2, float* dl, float* top, bool vec, cudaStream_t st) {
+    const long long blocks = ((long long)a.B * rw.N * rw.tiles * rw.rt + (top ? (long long)a.B * a.S * a.N : 0) + 31) / 32;
     const unsigned grid = (unsigned)(blocks < 152 * 32 ? blocks : 152 * 32);
-    msda_attention_prepare_kernel<T><<<grid, 256, 0, st>>>(a, rw, out, lse, l2, dl);
+    msda_attention_prepare_kernel<T><<<grid, 256, 0, st>>>(a, rw, out, lse, off, l2, dl, top, vec);
     return cudaGetLastError();
 }
 #define MSDA_SIMT_INSTANCES(T)                                                                                          \
@@ -560,7 +610,7 @@ cudaError_t launch_attention_prepare(const AttentionArgs& a, const AttentionRows
     template cudaError_t launch_attention_simt_grad_query<T>(const AttentionArgs&, const AttentionRows&, bool, cudaStream_t); \
     template cudaError_t launch_attention_join<T>(const AttentionArgs&, cudaStream_t);                                  \
     template cudaError_t launch_attention_prepare<T>(const AttentionArgs&, const AttentionRows&, const void*,           \
-                                                     const float*, float*, float*, cudaStream_t);
+                                                     const float*, float, float*, float*, float*, bool, cudaStream_t);
 #endif
 
 }  // namespace msda

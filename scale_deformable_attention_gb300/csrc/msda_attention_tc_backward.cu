@@ -15,7 +15,7 @@
 // P^T and dS^T (16 bits) are operands in tensor memory, where a product with D
 // columns takes D/2 cycles (from shared memory it is bound by reading its
 // 128 x 16 operand: 32 + D/4).  Both are written over the scores they come from.
-// f16 would lose small values: P is scaled by 2^12 and dS by a power of two that the
+// f16 would lose small values: P is scaled by 2^12 (kHalfScale) and dS by a power of two that the
 // largest norms of dO and V rows bound from above; the sums are scaled back.
 #include "msda_attention_tc.cuh"
 #include "msda_attention_tc_host.cuh"
@@ -26,41 +26,40 @@ constexpr int kBwdThreads = 384;  // two warpgroups on the scores, one of copies
 
 // Exponents of the scalings: P 2^kp and dS 2^ks.
 struct TcScale {
-    float p, ds, inv_p, inv_ds;  // 2^kp as an offset of the exponent; 2^(ks - kp); 2^-kp; 2^-ks
+    float ds, inv_p, inv_ds;  // 2^(ks - kp); 2^-kp; 2^-ks (kp is within the rows' l2)
 };
 template <bool BF16>
 __device__ __forceinline__ TcScale tc_scale(const TcArgs& p) {
-    TcScale r{0.f, 1.f, 1.f, 1.f};
+    TcScale r{1.f, 1.f, 1.f};
     if constexpr (!BF16) {
         // |dS| <= 2 |dO row| |v row|: the power of two that brings this to 2^14 at most
         const float top = 2.f * sqrtf(p.scale_in[0]) * sqrtf(p.scale_in[1]);
         int ks = 0;
         if (top > 0.f && top < 1e30f) ks = 14 - (int)ceilf(log2f(top));
         ks = ks < -40 ? -40 : ks > 40 ? 40 : ks;
-        r.p = 12.f;
-        r.ds = exp2f((float)(ks - 12));
-        r.inv_p = 1.f / 4096.f;
+        r.ds = exp2f(ks - kHalfScale);
+        r.inv_p = exp2f(-kHalfScale);
         r.inv_ds = exp2f((float)-ks);
     }
     return r;
 }
 
 struct TcBackwardSync {
-    uint64_t own, full[3], empty[3], ready[3];
+    uint64_t own, full[8], empty[8], ready[8];
     uint64_t s_full, dp_full, p_ready, ds_ready, s_free, ds_done, acc;
     uint32_t tmem, abort;
-    uint32_t words[4][4];
+    uint32_t words[8][4];
 };
 
 // ---- gradients of keys and values ----
 
 template <int NC>
 struct TcKeyCfg {
-    static constexpr int kStages = NC == 1 ? 3 : 2;
+    // a ring of tiles: Q(0), dO(0), Q(1), ..., each let go on its own
+    static constexpr int kRing = NC == 1 ? 8 : 4;
     static constexpr uint32_t kTileBytes = NC * kTcTile;
-    static constexpr uint32_t kStatBytes = 1024;  // l2 and delta of 128 rows
-    static constexpr uint32_t kStageBytes = 2 * kTileBytes;
-    static constexpr size_t kSmem = 2 * kTileBytes + kStages * (kStageBytes + kStatBytes) + 1024;
+    static constexpr uint32_t kStatBytes = 1024;  // l2 and delta of 128 rows, beside a tile of Q
+    static constexpr size_t kSmem = 2 * kTileBytes + kRing * (kTileBytes + kStatBytes) + 1024;
     static constexpr uint32_t kDV = 256, kDK = 256 + NC * 64;  // tensor memory: S 0, dP 128
 };
 
@@ -70,14 +69,14 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                                       const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
                                       const __grid_constant__ CUtensorMap map_do) {
     using Cfg = TcKeyCfg<NC>;
-    constexpr int ST = Cfg::kStages;
+    constexpr int R = Cfg::kRing;
     const AttentionArgs& a = p.a;
     extern __shared__ unsigned char tc_smem_raw[];
-    unsigned char* smem = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(tc_smem_raw) + 1023) & ~(uintptr_t)1023);
+    unsigned char* smem = tc_smem_raw + ((1024u - (tc_smem(tc_smem_raw) & 1023u)) & 1023u);  // stays a shared-memory address to the compiler
     unsigned char* k_tile = smem;
     unsigned char* v_tile = smem + Cfg::kTileBytes;
-    unsigned char* stages = smem + 2 * Cfg::kTileBytes;                            // Q, dO
-    float* stats = reinterpret_cast<float*>(stages + ST * Cfg::kStageBytes);       // l2[128], delta[128] a stage
+    unsigned char* ring = smem + 2 * Cfg::kTileBytes;
+    float* stats = reinterpret_cast<float*>(ring + R * Cfg::kTileBytes);  // -l2[128], -delta[128] a slot
     __shared__ TcBackwardSync sy;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
@@ -100,7 +99,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
 
     if (warp == 8) {
         if (lane == 0) {
-            for (int i = 0; i < ST; ++i) {
+            for (int i = 0; i < R; ++i) {
                 tc_bar_init(tc_smem(&sy.full[i]), 1);
                 tc_bar_init(tc_smem(&sy.empty[i]), 1);
                 tc_bar_init(tc_smem(&sy.ready[i]), 1);
@@ -138,7 +137,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         const int shift = a.S - a.Q;
 #pragma unroll 1
         for (int i = 0; i < nt; ++i) {
-            const int g = i / per_head, rt = r0 + i - g * per_head, st = i % ST;
+            const int g = i / per_head, rt = r0 + i - g * per_head, st = 2 * i % R;
             const int q0 = rt * kTcRows + w * 64;
             uint2 bw = make_uint2(~0u, ~0u);
             if (has_bits) {
@@ -147,7 +146,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             }
             const float* l2 = stats + st * 256 + w * 64;
             const float* dl = l2 + 128;
-            ok = tc_bar_wait(tc_smem(&sy.full[st]), (i / ST) & 1, abort, a.err) &&
+            ok = tc_bar_wait(tc_smem(&sy.full[st]), (2 * i / R) & 1, abort, a.err) &&
                  tc_bar_wait(tc_smem(&sy.s_full), i & 1, abort, a.err);
             if (!ok) break;
             tc_fence_after();
@@ -175,8 +174,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                 for (int k = 0; k < 32; k += 4) {
                     const float4 l = *reinterpret_cast<const float4*>(l2 + c * 32 + k);
                     float x0, x1, x2, x3;
-                    tc_split(tc_fma2(tc_two(__uint_as_float(s[c][k]), __uint_as_float(s[c][k + 1])), c2, tc_two(sc.p - l.x, sc.p - l.y)), x0, x1);
-                    tc_split(tc_fma2(tc_two(__uint_as_float(s[c][k + 2]), __uint_as_float(s[c][k + 3])), c2, tc_two(sc.p - l.z, sc.p - l.w)), x2, x3);
+                    tc_split(tc_fma2(tc_two(__uint_as_float(s[c][k]), __uint_as_float(s[c][k + 1])), c2, tc_two(l.x, l.y)), x0, x1);
+                    tc_split(tc_fma2(tc_two(__uint_as_float(s[c][k + 2]), __uint_as_float(s[c][k + 3])), c2, tc_two(l.z, l.w)), x2, x3);
                     const float e0 = tc_ex2(x0), e1 = tc_ex2(x1), e2 = tc_ex2(x2), e3 = tc_ex2(x3);
                     s[c][k] = __float_as_uint(e0), s[c][k + 1] = __float_as_uint(e1);
                     s[c][k + 2] = __float_as_uint(e2), s[c][k + 3] = __float_as_uint(e3);
@@ -201,8 +200,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                 for (int k = 0; k < 32; k += 4) {
                     const float4 l = *reinterpret_cast<const float4*>(dl + c * 32 + k);
                     float x0, x1, x2, x3;
-                    uint64_t y0 = tc_add2(tc_two(__uint_as_float(d[k]), __uint_as_float(d[k + 1])), tc_two(-l.x, -l.y));
-                    uint64_t y1 = tc_add2(tc_two(__uint_as_float(d[k + 2]), __uint_as_float(d[k + 3])), tc_two(-l.z, -l.w));
+                    uint64_t y0 = tc_add2(tc_two(__uint_as_float(d[k]), __uint_as_float(d[k + 1])), tc_two(l.x, l.y));
+                    uint64_t y1 = tc_add2(tc_two(__uint_as_float(d[k + 2]), __uint_as_float(d[k + 3])), tc_two(l.z, l.w));
                     y0 = tc_mul2(y0, tc_two(__uint_as_float(s[c][k]), __uint_as_float(s[c][k + 1])));
                     y1 = tc_mul2(y1, tc_two(__uint_as_float(s[c][k + 2]), __uint_as_float(s[c][k + 3])));
                     if constexpr (!BF16) y0 = tc_mul2(y0, ds2), y1 = tc_mul2(y1, ds2);
@@ -255,19 +254,19 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                 tc_tma_5d(tc_smem(k_tile) + c * kTcTile, &map_k, own, c * 64, 0, j0, n, b);
                 tc_tma_5d(tc_smem(v_tile) + c * kTcTile, &map_v, own, c * 64, 0, j0, n, b);
             }
-            for (int i = 0; i < nt; ++i) {
-                const int g = i / per_head, rt = r0 + i - g * per_head, st = i % ST, h = n * a.G + g;
-                if (i >= ST) ok = tc_bar_wait(tc_smem(&sy.empty[st]), (i / ST - 1) & 1, abort, a.err);
+            for (int x = 0; x < 2 * nt; ++x) {
+                const int i = x >> 1, g = i / per_head, rt = r0 + i - g * per_head, st = x % R, h = n * a.G + g;
+                if (x >= R) ok = tc_bar_wait(tc_smem(&sy.empty[st]), (x / R - 1) & 1, abort, a.err);
                 if (!ok) break;
-                const uint32_t bar = tc_smem(&sy.full[st]), at = tc_smem(stages) + st * Cfg::kStageBytes;
-                tc_bar_expect(bar, Cfg::kStageBytes + Cfg::kStatBytes);
-                for (int c = 0; c < NC; ++c) {
-                    tc_tma_5d(at + c * kTcTile, &map_q, bar, c * 64, 0, rt * kTcRows, h, b);
-                    tc_tma_5d(at + Cfg::kTileBytes + c * kTcTile, &map_do, bar, c * 64, 0, rt * kTcRows, h, b);
+                const uint32_t bar = tc_smem(&sy.full[st]), at = tc_smem(ring) + st * Cfg::kTileBytes;
+                tc_bar_expect(bar, Cfg::kTileBytes + ((x & 1) ? 0 : Cfg::kStatBytes));
+                for (int c = 0; c < NC; ++c)
+                    tc_tma_5d(at + c * kTcTile, (x & 1) ? &map_do : &map_q, bar, c * 64, 0, rt * kTcRows, h, b);
+                if (!(x & 1)) {
+                    const long long r = (((long long)b * a.M + h) * p.qblocks + rt) * kTcRows;
+                    tc_bulk(tc_smem(stats + st * 256), a.row_l2 + r, 512, bar);
+                    tc_bulk(tc_smem(stats + st * 256 + 128), a.row_dl + r, 512, bar);
                 }
-                const long long r = (((long long)b * a.M + h) * p.qblocks + rt) * kTcRows;
-                tc_bulk(tc_smem(stats + st * 256), a.row_l2 + r, 512, bar);
-                tc_bulk(tc_smem(stats + st * 256 + 128), a.row_dl + r, 512, bar);
             }
         } else if (role == 1 && nt > 0) {
             // ---- products ----
@@ -275,7 +274,9 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             const int steps = (a.D + 15) / 16;
             const uint32_t id_s = tc_idesc(BF16, false, false, 128, 128), id_g = tc_idesc(BF16, false, true, 128, steps * 16);
             const uint64_t k_desc = tc_desc(tc_smem(k_tile), 16, 1024), v_desc = tc_desc(tc_smem(v_tile), 16, 1024);
-            const uint32_t base = tc_smem(stages);
+            const uint32_t base = tc_smem(ring);
+            auto at = [&](int x) { return base + (x % R) * Cfg::kTileBytes; };  // Q(i) is tile 2i, dO(i) 2i + 1
+            auto filled = [&](int x) { return tc_bar_wait(tc_smem(&full[x % R]), (x / R) & 1, abort, a.err); };
             auto scores = [&](uint32_t d, uint64_t x_desc, uint32_t y) {  // 128 keys x 128 queries
                 const uint64_t y_desc = tc_desc(y, 16, 1024);
 #pragma unroll
@@ -292,36 +293,38 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             };
             ok = tc_bar_wait(tc_smem(&sy.own), 0, abort, a.err);
             if (ok && fix) ok = tc_bar_wait(tc_smem(&sy.s_free), 0, abort, a.err);  // K and V cleared
-            ok = ok && tc_bar_wait(tc_smem(&full[0]), 0, abort, a.err);
+            ok = ok && filled(0) && filled(1);
             if (ok) {
                 tc_fence_after();
-                scores(tmem, k_desc, base);
+                scores(tmem, k_desc, at(0));
                 tc_commit(on, tc_smem(&sy.s_full));
-                scores(tmem + 128, v_desc, base + Cfg::kTileBytes);
+                scores(tmem + 128, v_desc, at(1));
                 tc_commit(on, tc_smem(&sy.dp_full));
             }
             for (int i = 0; i < nt && ok; ++i) {
-                const int st = i % ST, sn = (i + 1) % ST;
                 const bool more = i + 1 < nt;
-                const uint32_t q_at = base + st * Cfg::kStageBytes, next = base + sn * Cfg::kStageBytes;
                 ok = tc_bar_wait(tc_smem(&sy.p_ready), i & 1, abort, a.err);
                 if (!ok) break;
                 tc_fence_after();
-                gradient(tmem + Cfg::kDV, tmem, q_at + Cfg::kTileBytes, i > 0);
+                gradient(tmem + Cfg::kDV, tmem, at(2 * i + 1), i > 0);
+                tc_commit(on, tc_smem(&sy.empty[(2 * i + 1) % R]));
                 if (more) {
-                    ok = tc_bar_wait(tc_smem(&full[sn]), ((i + 1) / ST) & 1, abort, a.err);
+                    ok = filled(2 * i + 2);
                     if (!ok) break;
                     tc_fence_after();
-                    scores(tmem, k_desc, next);
+                    scores(tmem, k_desc, at(2 * i + 2));
                     tc_commit(on, tc_smem(&sy.s_full));
                 }
                 ok = tc_bar_wait(tc_smem(&sy.ds_ready), i & 1, abort, a.err);
                 if (!ok) break;
                 tc_fence_after();
-                gradient(tmem + Cfg::kDK, tmem + 128, q_at, i > 0);
-                tc_commit(on, tc_smem(&sy.empty[st]));
+                gradient(tmem + Cfg::kDK, tmem + 128, at(2 * i), i > 0);
+                tc_commit(on, tc_smem(&sy.empty[2 * i % R]));
                 if (more) {
-                    scores(tmem + 128, v_desc, next + Cfg::kTileBytes);
+                    ok = filled(2 * i + 3);
+                    if (!ok) break;
+                    tc_fence_after();
+                    scores(tmem + 128, v_desc, at(2 * i + 3));
                     tc_commit(on, tc_smem(&sy.dp_full));
                 } else {
                     tc_commit(on, tc_smem(&sy.acc));
@@ -341,16 +344,18 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                 __syncwarp();
                 if (lane == 0) tc_bar_arrive(tc_smem(&sy.s_free));
             }
-            for (int i = 0; i < nt && ok; ++i) {
-                const int st = i % ST;
-                ok = tc_bar_wait(tc_smem(&sy.full[st]), (i / ST) & 1, abort, a.err);
+            uint32_t w[4];
+            for (int x = 0; x < 2 * nt && ok; ++x) {
+                const int st = x % R;
+                ok = tc_bar_wait(tc_smem(&sy.full[st]), (x / R) & 1, abort, a.err);
                 if (!ok) break;
-                uint32_t w[4];
+                if (!(x & 1)) {
 #pragma unroll
-                for (int c = 0; c < 4; ++c) w[c] = __ballot_sync(0xffffffffu, stats[st * 256 + c * 32 + lane] != attn_inf());
+                    for (int c = 0; c < 4; ++c)
+                        w[c] = __ballot_sync(0xffffffffu, stats[st * 256 + c * 32 + lane] != -attn_inf());
+                }
                 if ((w[0] & w[1] & w[2] & w[3]) != 0xffffffffu) {
-                    tc_clear_rows<NC>(stages + st * Cfg::kStageBytes, w, lane);
-                    tc_clear_rows<NC>(stages + st * Cfg::kStageBytes + Cfg::kTileBytes, w, lane);
+                    tc_clear_rows<NC>(ring + st * Cfg::kTileBytes, w, lane);
                     tc_fence_async();
                 }
                 __syncwarp();
@@ -369,10 +374,12 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
 
 template <int NC>
 struct TcQueryCfg {
-    static constexpr int kStages = NC == 1 ? 3 : 2;
+    // a ring of tiles: V(0), K(0), V(1), ...; V is let go behind its scores, K behind dQ.
+    // (Pairs of K and V in two stages left the products waiting 1600 of 3200
+    // cycles a tile for them at 128 channels.)
+    static constexpr int kRing = NC == 1 ? 8 : 5;
     static constexpr uint32_t kTileBytes = NC * kTcTile;
-    static constexpr uint32_t kStageBytes = 2 * kTileBytes;  // K, V
-    static constexpr size_t kSmem = 2 * kTileBytes + kStages * kStageBytes + 1024;
+    static constexpr size_t kSmem = (2 + kRing) * kTileBytes + 1024;
     static constexpr uint32_t kDS = 256, kDQ = 320;  // tensor memory: S 0, dP 128
 };
 
@@ -382,13 +389,13 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                                         const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
                                         const __grid_constant__ CUtensorMap map_do) {
     using Cfg = TcQueryCfg<NC>;
-    constexpr int ST = Cfg::kStages;
+    constexpr int R = Cfg::kRing;
     const AttentionArgs& a = p.a;
     extern __shared__ unsigned char tc_smem_raw[];
-    unsigned char* smem = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(tc_smem_raw) + 1023) & ~(uintptr_t)1023);
+    unsigned char* smem = tc_smem_raw + ((1024u - (tc_smem(tc_smem_raw) & 1023u)) & 1023u);  // stays a shared-memory address to the compiler
     unsigned char* q_tile = smem;
     unsigned char* do_tile = smem + Cfg::kTileBytes;
-    unsigned char* stages = smem + 2 * Cfg::kTileBytes;
+    unsigned char* ring = smem + 2 * Cfg::kTileBytes;
     __shared__ TcBackwardSync sy;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
@@ -405,7 +412,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
 
     if (warp == 8) {
         if (lane == 0) {
-            for (int i = 0; i < ST; ++i) {
+            for (int i = 0; i < R; ++i) {
                 tc_bar_init(tc_smem(&sy.full[i]), 1);
                 tc_bar_init(tc_smem(&sy.empty[i]), 1);
                 tc_bar_init(tc_smem(&sy.ready[i]), 1);
@@ -437,11 +444,11 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         const TcScale sc = tc_scale<BF16>(p);
         const long long r = (((long long)b * a.M + h) * p.qblocks + rt) * kTcRows + row;
         const float l2 = a.row_l2[r], dl = a.row_dl[r];
-        const bool live = l2 != attn_inf();  // q < Q and some key seen
+        const bool live = l2 != -attn_inf();  // q < Q and some key seen
         const int seen = live ? tc_seen(a, q) : 0;
         const int seen_least = __reduce_min_sync(0xffffffffu, live ? seen : a.S);
         const uint32_t* bits = p.bits && q < a.Q ? p.bits + b * p.bits_sb + h * p.bits_sh + (long long)q * p.W : nullptr;
-        const uint64_t c2 = tc_two(a.c2, a.c2), nl = tc_two(sc.p - l2, sc.p - l2), nd = tc_two(-dl, -dl), ds2 = tc_two(sc.ds, sc.ds);
+        const uint64_t c2 = tc_two(a.c2, a.c2), nl = tc_two(l2, l2), nd = tc_two(dl * sc.ds, dl * sc.ds), ds2 = tc_two(sc.ds, sc.ds);
 #pragma unroll 1
         for (int i = 0; i < nt; ++i) {
             const int j0 = (t0 + i) * kTcRows + w * 64;
@@ -461,7 +468,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             if (__builtin_expect(km || p.bits || seen_least - j0 < 64, 0)) {
                 const int see = seen - j0;
                 uint32_t m0 = bw.x & tc_low_bits(see), m1 = bw.y & tc_low_bits(see - 32);
-                if (km) m0 &= sy.words[i & 3][w * 2], m1 &= sy.words[i & 3][w * 2 + 1];
+                if (km) m0 &= sy.words[i & 7][w * 2], m1 &= sy.words[i & 7][w * 2 + 1];
                 if (__any_sync(0xffffffffu, (m0 & m1) != 0xffffffffu)) {
 #pragma unroll
                     for (int k = 0; k < 32; ++k) {
@@ -483,8 +490,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                     float x0, x1;
                     tc_split(tc_fma2(tc_two(__uint_as_float(s[c][k]), __uint_as_float(s[c][k + 1])), c2, nl), x0, x1);
                     const uint64_t e = tc_two(tc_ex2(x0), tc_ex2(x1));
-                    uint64_t y = tc_mul2(tc_add2(tc_two(__uint_as_float(d[c][k]), __uint_as_float(d[c][k + 1])), nd), e);
-                    if constexpr (!BF16) y = tc_mul2(y, ds2);
+                    const uint64_t dp = tc_two(__uint_as_float(d[c][k]), __uint_as_float(d[c][k + 1]));
+                    const uint64_t y = tc_mul2(BF16 ? tc_add2(dp, nd) : tc_fma2(dp, ds2, nd), e);
                     tc_split(y, x0, x1);
                     pk[k / 2] = tc_pack<BF16>(x0, x1);
                 }
@@ -528,71 +535,73 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                 tc_tma_5d(tc_smem(q_tile) + c * kTcTile, &map_q, own, c * 64, 0, q0, h, b);
                 tc_tma_5d(tc_smem(do_tile) + c * kTcTile, &map_do, own, c * 64, 0, q0, h, b);
             }
-            for (int i = 0; i < nt; ++i) {
-                const int st = i % ST;
-                if (i >= ST) ok = tc_bar_wait(tc_smem(&sy.empty[st]), (i / ST - 1) & 1, abort, a.err);
+            for (int x = 0; x < 2 * nt; ++x) {
+                const int st = x % R;
+                if (x >= R) ok = tc_bar_wait(tc_smem(&sy.empty[st]), (x / R - 1) & 1, abort, a.err);
                 if (!ok) break;
-                const uint32_t bar = tc_smem(&sy.full[st]), at = tc_smem(stages) + st * Cfg::kStageBytes;
-                tc_bar_expect(bar, Cfg::kStageBytes);
-                for (int c = 0; c < NC; ++c) {
-                    tc_tma_5d(at + c * kTcTile, &map_k, bar, c * 64, 0, (t0 + i) * kTcRows, n, b);
-                    tc_tma_5d(at + Cfg::kTileBytes + c * kTcTile, &map_v, bar, c * 64, 0, (t0 + i) * kTcRows, n, b);
-                }
+                const uint32_t bar = tc_smem(&sy.full[st]);
+                tc_bar_expect(bar, Cfg::kTileBytes);
+                for (int c = 0; c < NC; ++c)
+                    tc_tma_5d(tc_smem(ring) + st * Cfg::kTileBytes + c * kTcTile, (x & 1) ? &map_k : &map_v, bar, c * 64, 0,
+                              (t0 + (x >> 1)) * kTcRows, n, b);
             }
         } else if (role == 1 && nt > 0) {
             const uint32_t on = tc_elect();
             const int steps = (a.D + 15) / 16;
             const uint32_t id_s = tc_idesc(BF16, false, false, 128, 128), id_g = tc_idesc(BF16, false, true, 128, steps * 16);
             const uint64_t q_desc = tc_desc(tc_smem(q_tile), 16, 1024), do_desc = tc_desc(tc_smem(do_tile), 16, 1024);
-            const uint32_t base = tc_smem(stages);
-            auto scores = [&](int st) {  // S = Q K^T, dP = dO V^T
-                const uint64_t k_desc = tc_desc(base + st * Cfg::kStageBytes, 16, 1024);
-                const uint64_t v_desc = tc_desc(base + st * Cfg::kStageBytes + Cfg::kTileBytes, 16, 1024);
+            const uint32_t base = tc_smem(ring);
+            auto at = [&](int x) { return base + (x % R) * Cfg::kTileBytes; };  // V(i) is tile 2i, K(i) 2i + 1
+            auto filled = [&](int x) { return tc_bar_wait(tc_smem(&full[x % R]), (x / R) & 1, abort, a.err); };
+            auto scores = [&](int i) {  // dP = dO V^T, S = Q K^T
+                const uint64_t v_desc = tc_desc(at(2 * i), 16, 1024), k_desc = tc_desc(at(2 * i + 1), 16, 1024);
 #pragma unroll
                 for (int k = 0; k < NC * 4; ++k) {
                     const uint64_t off = ((k >> 2) * kTcTile + (k & 3) * 32) >> 4;
-                    if (k < steps) {
-                        tc_mma_ss(on, tmem, q_desc + off, k_desc + off, id_s, k > 0);
-                        tc_mma_ss(on, tmem + 128, do_desc + off, v_desc + off, id_s, k > 0);
-                    }
+                    if (k < steps) tc_mma_ss(on, tmem + 128, do_desc + off, v_desc + off, id_s, k > 0);
+                }
+                tc_commit(on, tc_smem(&sy.empty[2 * i % R]));
+#pragma unroll
+                for (int k = 0; k < NC * 4; ++k) {
+                    const uint64_t off = ((k >> 2) * kTcTile + (k & 3) * 32) >> 4;
+                    if (k < steps) tc_mma_ss(on, tmem, q_desc + off, k_desc + off, id_s, k > 0);
                 }
                 tc_commit(on, tc_smem(&sy.s_full));
             };
-            ok = tc_bar_wait(tc_smem(&sy.own), 0, abort, a.err) && tc_bar_wait(tc_smem(&full[0]), 0, abort, a.err);
+            ok = tc_bar_wait(tc_smem(&sy.own), 0, abort, a.err) && filled(0) && filled(1);
             if (ok) {
                 tc_fence_after();
                 scores(0);
             }
             for (int i = 0; i < nt && ok; ++i) {
-                const int st = i % ST, sn = (i + 1) % ST;
                 if (i + 1 < nt) {
-                    ok = tc_bar_wait(tc_smem(&full[sn]), ((i + 1) / ST) & 1, abort, a.err) &&
-                         tc_bar_wait(tc_smem(&sy.s_free), i & 1, abort, a.err);
+                    ok = filled(2 * i + 2) && filled(2 * i + 3) && tc_bar_wait(tc_smem(&sy.s_free), i & 1, abort, a.err);
                     if (!ok) break;
                     tc_fence_after();
-                    scores(sn);
+                    scores(i + 1);
                 }
                 ok = tc_bar_wait(tc_smem(&sy.ds_ready), i & 1, abort, a.err);
                 if (!ok) break;
                 tc_fence_after();
-                const uint64_t k_desc = tc_desc(base + st * Cfg::kStageBytes, kTcTile, 1024);
+                const uint64_t k_desc = tc_desc(at(2 * i + 1), kTcTile, 1024);
 #pragma unroll
                 for (int k = 0; k < 8; ++k)
                     tc_mma_ts(on, tmem + Cfg::kDQ, tmem + Cfg::kDS + k * 8, k_desc + ((k * 2048) >> 4), id_g, i > 0 || k > 0);
                 tc_commit(on, tc_smem(&sy.ds_done));
-                tc_commit(on, tc_smem(&sy.empty[st]));
+                tc_commit(on, tc_smem(&sy.empty[(2 * i + 1) % R]));
             }
         } else if (role == 2 && km && nt > 0) {
-            for (int i = 0; i < nt && ok; ++i) {
-                const int st = i % ST, j0 = (t0 + i) * kTcRows;
-                uint32_t w[4];
-                tc_key_words(km + j0, a.S - j0, lane, w);
-                if (lane < 4) sy.words[i & 3][lane] = lane == 0 ? w[0] : lane == 1 ? w[1] : lane == 2 ? w[2] : w[3];
-                ok = tc_bar_wait(tc_smem(&sy.full[st]), (i / ST) & 1, abort, a.err);
+            uint32_t w[4];
+            for (int x = 0; x < 2 * nt && ok; ++x) {
+                const int st = x % R, i = x >> 1;
+                if (!(x & 1)) {
+                    tc_key_words(km + (t0 + i) * kTcRows, a.S - (t0 + i) * kTcRows, lane, w);
+                    if (lane < 4) sy.words[i & 7][lane] = lane == 0 ? w[0] : lane == 1 ? w[1] : lane == 2 ? w[2] : w[3];
+                }
+                ok = tc_bar_wait(tc_smem(&sy.full[st]), (x / R) & 1, abort, a.err);
                 if (!ok) break;
                 if ((w[0] & w[1] & w[2] & w[3]) != 0xffffffffu) {
-                    tc_clear_rows<NC>(stages + st * Cfg::kStageBytes, w, lane);
-                    tc_clear_rows<NC>(stages + st * Cfg::kStageBytes + Cfg::kTileBytes, w, lane);
+                    tc_clear_rows<NC>(ring + st * Cfg::kTileBytes, w, lane);
                     tc_fence_async();
                 }
                 __syncwarp();
@@ -605,51 +614,6 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     tc_fence_before();
     __syncthreads();
     if (warp == 9) tmem_dealloc(tmem, 512);
-}
-
-// f16: the largest squared norms of the gradient's rows that take part and of
-// the values that a query may see (as bits of non-negative binary32 numbers,
-// whose order is that of integers).  Eight lanes a row.
-__global__ void __launch_bounds__(256) msda_attention_amax_kernel(const AttentionArgs a, const AttentionRows rw, float* top) {
-    const long long rows = (long long)a.B * rw.N * rw.tiles * rw.rt, keys = (long long)a.B * a.S * a.N;
-    const int lane = threadIdx.x & 7;
-    const long long step = (long long)gridDim.x * 32;
-    float best[2] = {0.f, 0.f};
-    for (long long i = (long long)blockIdx.x * 32 + (threadIdx.x >> 3); i < (rows + keys + 3) / 4 * 4; i += step) {
-        const __half* x = nullptr;
-        if (i < rows) {
-            if (a.row_l2[i] != attn_inf()) {
-                const long long bt = i / rw.rt, bn = bt / rw.tiles, b = bn / rw.N;
-                const long long q = (bt - bn * rw.tiles) * rw.qpt + (i - bt * rw.rt), m = bn - b * rw.N;
-                x = static_cast<const __half*>(a.dout) + ((b * a.Q + q) * a.M + m) * a.D;
-            }
-        } else if (i < rows + keys) {
-            const long long e = i - rows, bs = e / a.N, b = bs / a.S;
-            const long long j = bs - b * a.S;
-            const int n = (int)(e - bs * a.N);
-            if (!a.key_mask || a.key_mask[b * a.km_sb + n * a.km_sh + j])
-                x = static_cast<const __half*>(a.v) + b * a.v_sb + j * a.v_ss + n * a.v_sh;
-        }
-        float s = 0.f;
-        if (x)
-            for (int c = lane * 8; c < a.D; c += 64) {  // 16-byte rows: D is a multiple of 8
-                const uint4 u = *reinterpret_cast<const uint4*>(x + c);
-                const uint32_t v[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&v[k]));
-                    s = fmaf(f.x, f.x, fmaf(f.y, f.y, s));
-                }
-            }
-        for (int o = 4; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-        // a NaN or infinity leaves the scaling at 1 (its bits are above every number's)
-        best[i < rows ? 0 : 1] = s != s ? s : best[i < rows ? 0 : 1] != best[i < rows ? 0 : 1] ? best[i < rows ? 0 : 1] : fmaxf(best[i < rows ? 0 : 1], s);
-    }
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-        const unsigned u = __reduce_max_sync(0xffffffffu, __float_as_uint(best[k]) & 0x7fffffffu);
-        if ((threadIdx.x & 31) == 0 && u) atomicMax(reinterpret_cast<unsigned*>(top) + k, u);
-    }
 }
 
 // ---- host ----
@@ -684,11 +648,6 @@ cudaError_t launch_attention_tc_grad_query(const TcArgs& p, bool bf16, const CUt
                                            const CUtensorMap& v, const CUtensorMap& g, cudaStream_t st) {
     if (p.a.D > 64) return bf16 ? grad_query_go<true, 2>(p, q, k, v, g, st) : grad_query_go<false, 2>(p, q, k, v, g, st);
     return bf16 ? grad_query_go<true, 1>(p, q, k, v, g, st) : grad_query_go<false, 1>(p, q, k, v, g, st);
-}
-cudaError_t launch_attention_amax(const AttentionArgs& a, const AttentionRows& rw, float* top, cudaStream_t st) {
-    const long long rows = ((long long)a.B * rw.N * rw.tiles * rw.rt + (long long)a.B * a.S * a.N + 31) / 32;
-    msda_attention_amax_kernel<<<(unsigned)(rows < 152 * 8 ? rows : 152 * 8), 256, 0, st>>>(a, rw, top);
-    return cudaGetLastError();
 }
 
 }  // namespace msda

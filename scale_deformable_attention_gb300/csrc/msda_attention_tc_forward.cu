@@ -64,7 +64,7 @@ __global__ void __launch_bounds__(TcForwardCfg<NQ, NC>::kThreads, 1)
     constexpr int ST = Cfg::kStages;
     const AttentionArgs& a = p.a;
     extern __shared__ unsigned char tc_smem_raw[];
-    unsigned char* smem = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(tc_smem_raw) + 1023) & ~(uintptr_t)1023);
+    unsigned char* smem = tc_smem_raw + ((1024u - (tc_smem(tc_smem_raw) & 1023u)) & 1023u);  // stays a shared-memory address to the compiler
     unsigned char* q_tiles = smem;
     unsigned char* ring = smem + NQ * Cfg::kTileBytes;
     __shared__ TcForwardSync sy;

@@ -15,7 +15,5 @@ cudaError_t launch_attention_tc_grad_key(const TcArgs& p, bool bf16, const CUten
                                          const CUtensorMap& v, const CUtensorMap& g, cudaStream_t st);
 cudaError_t launch_attention_tc_grad_query(const TcArgs& p, bool bf16, const CUtensorMap& q, const CUtensorMap& k,
                                            const CUtensorMap& v, const CUtensorMap& g, cudaStream_t st);
-// f16: largest squared norms of the rows of dout (a.row_l2 set) and of v, into top[2] (cleared before)
-cudaError_t launch_attention_amax(const AttentionArgs& a, const AttentionRows& rw, float* top, cudaStream_t st);
 
 }  // namespace msda
