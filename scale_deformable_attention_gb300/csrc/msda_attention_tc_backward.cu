@@ -46,7 +46,7 @@ __device__ __forceinline__ TcScale tc_scale(const TcArgs& p) {
 
 struct TcBackwardSync {
     uint64_t own, full[8], empty[8], ready[8];
-    uint64_t s_full, dp_full, p_ready, ds_ready, s_free, ds_done, acc;
+    uint64_t s_full, dp_full, p_ready, ds_ready, s_free, ds_done[2], acc;
     uint32_t tmem, abort;
     uint32_t words[8][4];
 };
@@ -380,7 +380,7 @@ struct TcQueryCfg {
     static constexpr int kRing = NC == 1 ? 8 : 5;
     static constexpr uint32_t kTileBytes = NC * kTcTile;
     static constexpr size_t kSmem = (2 + kRing) * kTileBytes + 1024;
-    static constexpr uint32_t kDS = 256, kDQ = 320;  // tensor memory: S 0, dP 128
+    static constexpr uint32_t kDS = 256, kDQ = 384;  // tensor memory: S 0, dP 128, dS twice 64 (dQ of a tile runs beside the next tile's dS)
 };
 
 template <bool BF16, int NC>
@@ -421,7 +421,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             tc_bar_init(tc_smem(&sy.s_full), 1);
             tc_bar_init(tc_smem(&sy.s_free), 8);
             tc_bar_init(tc_smem(&sy.ds_ready), 8);
-            tc_bar_init(tc_smem(&sy.ds_done), 1);
+            for (int i = 0; i < 2; ++i) tc_bar_init(tc_smem(&sy.ds_done[i]), 1);
             sy.abort = 0;
             asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         }
@@ -477,8 +477,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                     }
                 }
             }
-            if (i > 0) {  // dS(i-1) is used up
-                ok = tc_bar_wait(tc_smem(&sy.ds_done), (i - 1) & 1, abort, a.err);
+            if (i > 1) {  // dS(i-2) is used up
+                ok = tc_bar_wait(tc_smem(&sy.ds_done[i & 1]), (i / 2 - 1) & 1, abort, a.err);
                 if (!ok) break;
                 tc_fence_after();
             }
@@ -495,14 +495,14 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                     tc_split(y, x0, x1);
                     pk[k / 2] = tc_pack<BF16>(x0, x1);
                 }
-                tmem_st16(ds_at + c * 16, pk);
+                tmem_st16(ds_at + (i & 1) * 64 + c * 16, pk);
             }
             tmem_wait_st();
             tc_fence_before();
             tc_bar_arrive_if(first, tc_smem(&sy.ds_ready));
         }
         if (nt > 0 && ok) {
-            ok = tc_bar_wait(tc_smem(&sy.ds_done), (nt - 1) & 1, abort, a.err);
+            ok = tc_bar_wait(tc_smem(&sy.ds_done[(nt - 1) & 1]), ((nt - 1) / 2) & 1, abort, a.err);
             tc_fence_after();
         }
         if (ok) {  // the two warpgroups take alternate chunks of 16 channels
@@ -586,8 +586,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                 const uint64_t k_desc = tc_desc(at(2 * i + 1), kTcTile, 1024);
 #pragma unroll
                 for (int k = 0; k < 8; ++k)
-                    tc_mma_ts(on, tmem + Cfg::kDQ, tmem + Cfg::kDS + k * 8, k_desc + ((k * 2048) >> 4), id_g, i > 0 || k > 0);
-                tc_commit(on, tc_smem(&sy.ds_done));
+                    tc_mma_ts(on, tmem + Cfg::kDQ, tmem + Cfg::kDS + (i & 1) * 64 + k * 8, k_desc + ((k * 2048) >> 4), id_g, i > 0 || k > 0);
+                tc_commit(on, tc_smem(&sy.ds_done[i & 1]));
                 tc_commit(on, tc_smem(&sy.empty[(2 * i + 1) % R]));
             }
         } else if (role == 2 && km && nt > 0) {
