@@ -18,7 +18,7 @@ namespace msda {
 //   live [LB, LN, S] bytes (cleared before): 1 where some query of the heads that
 //     share the key sees it; a key outside it may hold anything, NaN too (every
 //     writer of a byte writes the same 1);
-//   bits [Bm, Mm, Q, W] and bits_t [Bm, Mm, S, Wq] (tensor-core kernels; may be
+//   bits [Bm, Mm, Q, W] and bits_t [Bm, Mm, S, Wq] (tensor-core kernels; or
 //     null): the mask and its transpose, 32 pairs a word, zeros behind S and Q.
 // A warp takes 32 queries and 32 keys: lane j reads byte j of each row, the
 // row's word is a ballot, and the lane's own column of the transpose builds up.
@@ -108,7 +108,7 @@ msda_status check(msda_dtype dt, unsigned flags, const msda_attention_problem* p
 }
 
 // What the mask becomes in the workspace: the liveness of keys [LB][LN][S]
-// bytes and, for the tensor-core kernels, the pairs as bits by query and by key.
+// bytes, the pairs as bits by query and, for the tensor-core kernels, by key.
 struct MaskSpace {
     int Bm = 1, Mm = 1, LB = 1, LN = 1, W = 0, Wq = 0;
     size_t bits = 0, bits_t = 0, bytes = 0;  // offsets of the bits behind the liveness
@@ -123,8 +123,7 @@ MaskSpace mask_space(msda_dtype dt, unsigned flags, const msda_attention_problem
     l.W = (int)((p->S + 127) / 128 * 4);
     l.Wq = (int)((p->Q + 127) / 128 * 4);
     l.bits = up((size_t)l.LB * l.LN * (size_t)p->S);
-    l.bits_t = l.bits;
-    if (tc_type(dt, p)) l.bits_t += up((size_t)l.Bm * l.Mm * p->Q * l.W * 4);
+    l.bits_t = l.bits + up((size_t)l.Bm * l.Mm * p->Q * l.W * 4);
     l.bytes = l.bits_t;
     if (tc_type(dt, p)) l.bytes += up((size_t)l.Bm * l.Mm * p->S * l.Wq * 4);
     return l;
@@ -186,7 +185,7 @@ AttentionArgs args_of(unsigned flags, const msda_attention_problem* p, double sc
 msda_status make_mask(AttentionArgs& a, const MaskSpace& l, void* ws, msda::TcArgs* t, cudaStream_t st) {
     if (!a.mask) return MSDA_OK;
     uint8_t* live = static_cast<uint8_t*>(ws);
-    uint32_t* bits = t ? reinterpret_cast<uint32_t*>(live + l.bits) : nullptr;
+    uint32_t* bits = reinterpret_cast<uint32_t*>(live + l.bits);
     uint32_t* bits_t = t ? reinterpret_cast<uint32_t*>(live + l.bits_t) : nullptr;
     if (a.S > 0) {
         msda::TraceSpan ts(st);
@@ -206,10 +205,11 @@ msda_status make_mask(AttentionArgs& a, const MaskSpace& l, void* ws, msda::TcAr
     a.key_mask = live;
     a.km_sb = l.LB > 1 ? (long long)l.LN * a.S : 0;
     a.km_sh = l.LN > 1 ? a.S : 0;
+    a.bits = bits, a.W = l.W;
+    a.bits_sh = l.Mm > 1 ? (long long)a.Q * l.W : 0;
+    a.bits_sb = l.Bm > 1 ? (long long)l.Mm * a.Q * l.W : 0;
     if (t) {
-        t->bits = bits, t->bits_t = bits_t, t->W = l.W, t->Wq = l.Wq;
-        t->bits_sh = l.Mm > 1 ? (long long)a.Q * l.W : 0;
-        t->bits_sb = l.Bm > 1 ? (long long)l.Mm * a.Q * l.W : 0;
+        t->bits_t = bits_t, t->Wq = l.Wq;
         t->bits_t_sh = l.Mm > 1 ? (long long)a.S * l.Wq : 0;
         t->bits_t_sb = l.Bm > 1 ? (long long)l.Mm * a.S * l.Wq : 0;
     }

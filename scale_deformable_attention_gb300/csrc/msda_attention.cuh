@@ -19,6 +19,9 @@ struct AttentionArgs {
     long long km_sb, km_sh;
     const uint8_t* mask;  // [B|1, M|1, Q, S] or null: 0 = the pair takes no part
     long long mk_sb, mk_sh, mk_sq;
+    const uint32_t* bits;  // the mask as bits [Bm, Mm, Q, W] (W words a row, a multiple of 4), or null
+    long long bits_sb, bits_sh;
+    int W;
     int B, Q, S, M, N, D;
     int G;        // M / N query heads share a key head
     int causal;   // query i sees keys up to i + S - Q

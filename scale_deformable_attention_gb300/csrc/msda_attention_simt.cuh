@@ -19,6 +19,8 @@ namespace msda {
 
 constexpr int kSimtThreads = 128;
 constexpr int kSimtRows = 64;
+// blocks an SM that registers leave room for (accumulators grow with DP)
+constexpr int simt_blocks(int dp) { return dp <= 64 ? 3 : 2; }
 
 template <typename T>
 __device__ __forceinline__ float attn_f32(T v) { return (float)v; }
@@ -33,6 +35,9 @@ __device__ __forceinline__ __nv_bfloat16 attn_round<__nv_bfloat16>(float v) { re
 
 // 64 rows of D channels (rows at or above `rows`, and those `alive` says no
 // for, as zeros) into dst[64][DP + 4]; channels from D to DP are zeros.
+// binary32 rows of whole 16-byte vectors go by asynchronous copies, which a
+// caller issues as soon as a buffer is free and waits for (simt_landed) only
+// before its use: with plain loads the FMA pipe was busy 28 % of the time.
 template <typename T, int DP>
 __device__ __forceinline__ void simt_load(float* dst, const T* src, long long stride, int rows, int D, bool vec,
                                           const uint8_t* alive) {
@@ -41,10 +46,14 @@ __device__ __forceinline__ void simt_load(float* dst, const T* src, long long st
         if (vec) {
             for (int i = threadIdx.x; i < kSimtRows * (DP / 4); i += kSimtThreads) {
                 const int r = i / (DP / 4), c = (i - r * (DP / 4)) * 4;
-                float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-                if (r < rows && c < D && (!alive || alive[r])) v = *reinterpret_cast<const float4*>(src + r * stride + c);
-                *reinterpret_cast<float4*>(dst + r * LD + c) = v;
+                const bool in = r < rows && c < D && (!alive || alive[r]);
+                const uint32_t to = (uint32_t)__cvta_generic_to_shared(dst + r * LD + c);
+                // a source size of 0 writes zeros and reads nothing
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to),
+                             "l"(in ? (const void*)(src + r * stride + c) : (const void*)src), "r"(in ? 16 : 0)
+                             : "memory");
             }
+            asm volatile("cp.async.commit_group;" ::: "memory");
             return;
         }
     }
@@ -52,13 +61,20 @@ __device__ __forceinline__ void simt_load(float* dst, const T* src, long long st
         const int r = i / DP, c = i - r * DP;
         dst[r * LD + c] = r < rows && c < D && (!alive || alive[r]) ? attn_f32(src[r * stride + c]) : 0.f;
     }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+}
+// all but the last `N` loads have landed, for every thread of the block
+template <int N>
+__device__ __forceinline__ void simt_landed() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+    __syncthreads();
 }
 
 // acc[i][c] += sum_d A[ty*8+i][d] B[tx+16c][d]
 template <int DP>
 __device__ __forceinline__ void simt_nt(float (&acc)[8][4], const float* A, const float* B, int tx, int ty) {
     constexpr int LD = DP + 4;
-#pragma unroll 2
+#pragma unroll 1
     for (int d = 0; d < DP; d += 4) {
         float4 a[8], b[4];
 #pragma unroll
@@ -83,7 +99,7 @@ constexpr int kSimtLdP = 64 + 4;
 template <int DP>
 __device__ __forceinline__ void simt_nn(float (&acc)[8][DP / 16], const float* P, const float* X, int tx, int ty) {
     constexpr int LD = DP + 4;
-#pragma unroll 2
+#pragma unroll 1
     for (int k = 0; k < 64; k += 4) {
         float4 p[8];
 #pragma unroll
@@ -121,21 +137,39 @@ __device__ __forceinline__ void simt_tn(float (&acc)[8][DP / 16], const float* P
     }
 }
 
+// Words of a row's 64 keys from j0 on (a multiple of 64) in the mask's bits.
+__device__ __forceinline__ uint2 simt_bits(const AttentionArgs& a, int b, int m, int q, int j0) {
+    return *reinterpret_cast<const uint2*>(a.bits + b * a.bits_sb + m * a.bits_sh + (long long)q * a.W + (j0 >> 5));
+}
+// Whether the mask leaves any pair of the tile (the whole block asks; also a barrier).
+__device__ __forceinline__ bool simt_tile_seen(const AttentionArgs& a, int b, int m, int q0, int j0) {
+    bool any = false;
+    if (threadIdx.x < 64 && q0 + (int)threadIdx.x < a.Q) {
+        const uint2 w = simt_bits(a, b, m, q0 + threadIdx.x, j0);
+        any = (w.x | w.y) != 0;
+    }
+    return __syncthreads_or(any);
+}
+
 // Scores in log2 units of the block's rows q0 + ty*8 + i and keys j0 + tx + 16c; -inf where the pair takes no part.
 __device__ __forceinline__ void simt_mask(float (&s)[8][4], const AttentionArgs& a, int b, int m, int q0, int j0, int tx,
                                           int ty) {
     const uint8_t* km = a.key_mask ? a.key_mask + b * a.km_sb + (m / a.G) * a.km_sh : nullptr;
-    const uint8_t* mk = a.mask ? a.mask + b * a.mk_sb + m * a.mk_sh : nullptr;
+    bool in[4];
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
         const int j = j0 + tx + 16 * c;
-        const bool in = j < a.S && (!km || km[j]);
+        in[c] = j < a.S && (!km || km[j]);
+    }
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const int q = q0 + ty * 8 + i;
-            bool ok = in && q < a.Q;
-            if (a.causal) ok = ok && j <= q + (a.S - a.Q);
-            if (mk && ok) ok = mk[q * a.mk_sq + j] != 0;
+    for (int i = 0; i < 8; ++i) {
+        const int q = q0 + ty * 8 + i;
+        uint2 w = make_uint2(~0u, ~0u);
+        if (a.bits && q < a.Q) w = simt_bits(a, b, m, q, j0);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            bool ok = in[c] && q < a.Q && (((c < 2 ? w.x : w.y) >> (tx + 16 * (c & 1))) & 1u);
+            if (a.causal) ok = ok && j0 + tx + 16 * c <= q + (a.S - a.Q);
             s[i][c] = ok ? s[i][c] * a.c2 : -attn_inf();
         }
     }
@@ -164,12 +198,13 @@ __device__ __forceinline__ int simt_key_tiles(const AttentionArgs& a, int q0) {
 
 // Forward: running maximum m and sum l of each row, O rescaled when m grows.
 template <typename T, int DP>
-__global__ void __launch_bounds__(kSimtThreads) msda_attention_simt_kernel(const AttentionArgs a, bool vec) {
+__global__ void __launch_bounds__(kSimtThreads, simt_blocks(DP)) msda_attention_simt_kernel(const AttentionArgs a, bool vec) {
     extern __shared__ __align__(16) float simt_smem[];
     constexpr int LD = DP + 4;
     float* Qs = simt_smem;
-    float* Xs = Qs + kSimtRows * LD;  // keys, then values
-    float* Ps = Xs + kSimtRows * LD;
+    float* Ks = Qs + kSimtRows * LD;
+    float* Vs = Ks + kSimtRows * LD;
+    float* Ps = Vs + kSimtRows * LD;
     const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
     const int qtiles = (a.Q + kSimtRows - 1) / kSimtRows;
     long long id = blockIdx.x;
@@ -192,13 +227,24 @@ __global__ void __launch_bounds__(kSimtThreads) msda_attention_simt_kernel(const
     }
     const int t0 = split * a.tiles_per_split;
     const int t1 = min(simt_key_tiles(a, q0), t0 + a.tiles_per_split);
-    for (int t = t0; t < t1; ++t) {
-        const int j0 = t * 64;
-        __syncthreads();
-        simt_load<T, DP>(Xs, k + j0 * a.k_ss, a.k_ss, a.S - j0, a.D, vec, km ? km + j0 : nullptr);
-        __syncthreads();
+    auto fetch = [&](float* to, const T* from, long long stride, int t) {
+        simt_load<T, DP>(to, from + t * 64 * stride, stride, a.S - t * 64, a.D, vec, km ? km + t * 64 : nullptr);
+    };
+    auto seen_from = [&](int t) {  // the next tile that the mask leaves a pair of
+        if (a.bits)
+            while (t < t1 && !simt_tile_seen(a, b, m, q0, t * 64)) ++t;
+        return t;
+    };
+    int t = seen_from(t0);
+    if (t < t1) {
+        fetch(Ks, k, a.k_ss, t);
+        fetch(Vs, v, a.v_ss, t);
+    }
+    while (t < t1) {
+        const int j0 = t * 64, next = seen_from(t + 1);
+        simt_landed<1>();
         float s[8][4] = {};
-        simt_nt<DP>(s, Qs, Xs, tx, ty);
+        simt_nt<DP>(s, Qs, Ks, tx, ty);
         simt_mask(s, a, b, m, q0, j0, tx, ty);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
@@ -217,11 +263,19 @@ __global__ void __launch_bounds__(kSimtThreads) msda_attention_simt_kernel(const
 #pragma unroll
             for (int c = 0; c < DP / 16; ++c) o[i][c] *= f;
         }
+        __syncthreads();  // keys read, P written
+        if (next < t1) {
+            fetch(Ks, k, a.k_ss, next);
+            simt_landed<1>();
+        } else {
+            simt_landed<0>();
+        }
+        simt_nn<DP>(o, Ps, Vs, tx, ty);
         __syncthreads();
-        simt_load<T, DP>(Xs, v + j0 * a.v_ss, a.v_ss, a.S - j0, a.D, vec, km ? km + j0 : nullptr);
-        __syncthreads();
-        simt_nn<DP>(o, Ps, Xs, tx, ty);
+        if (next < t1) fetch(Vs, v, a.v_ss, next);
+        t = next;
     }
+    simt_landed<0>();
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         const int qi = q0 + ty * 8 + i;
@@ -265,7 +319,7 @@ __device__ __forceinline__ void simt_prob_grad(float (&s)[8][4], float (&dp)[8][
 // Gradients of 64 keys and values of one key head: over all queries of the
 // heads that share it, so the sums over shared heads stay in registers.
 template <typename T, int DP>
-__global__ void __launch_bounds__(kSimtThreads) msda_attention_simt_grad_key_kernel(const AttentionArgs a,
+__global__ void __launch_bounds__(kSimtThreads, simt_blocks(DP)) msda_attention_simt_grad_key_kernel(const AttentionArgs a,
                                                                                     const AttentionRows rw, bool vec) {
     extern __shared__ __align__(16) float simt_smem[];
     constexpr int LD = DP + 4;
@@ -290,41 +344,67 @@ __global__ void __launch_bounds__(kSimtThreads) msda_attention_simt_grad_key_ker
     // causal: queries below j0 - (S - Q) see none of these keys
     long long first = a.causal ? (long long)j0 - (a.S - a.Q) : 0;
     if (first < 0) first = 0;
-    for (int g = 0; g < a.G; ++g) {
-        const int m = n * a.G + g;
-        for (int q0 = (int)(first / 64) * 64; q0 < a.Q; q0 += 64) {
-            const float* l2p = a.row_l2 + ((long long)(b * rw.N + m) * rw.tiles + q0 / 64) * 64;
-            const float* dlp = a.row_dl + ((long long)(b * rw.N + m) * rw.tiles + q0 / 64) * 64;
-            __syncthreads();
-            if (threadIdx.x < 64) live[threadIdx.x] = l2p[threadIdx.x] != -attn_inf();
-            __syncthreads();
-            simt_load<T, DP>(Qs, static_cast<const T*>(a.q) + b * a.q_sb + m * a.q_sh + q0 * a.q_ss, a.q_ss, a.Q - q0,
-                             a.D, vec, live);
-            simt_load<T, DP>(Gs, static_cast<const T*>(a.dout) + (((long long)b * a.Q + q0) * a.M + m) * a.D,
-                             (long long)a.M * a.D, a.Q - q0, a.D, vec, live);
-            __syncthreads();
-            float s[8][4] = {}, dp[8][4] = {}, l2[8], dl[8];
-            simt_nt<DP>(s, Qs, Ks, tx, ty);
-            simt_nt<DP>(dp, Gs, Vs, tx, ty);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) l2[i] = l2p[ty * 8 + i], dl[i] = dlp[ty * 8 + i];
-            simt_mask(s, a, b, m, q0, j0, tx, ty);
-            simt_prob_grad(s, dp, l2, dl);
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-#pragma unroll
-                for (int c = 0; c < 4; ++c) Ps[(ty * 8 + i) * kSimtLdP + tx + 16 * c] = s[i][c];
-            __syncthreads();
-            simt_tn<DP>(dv, Ps, Gs, tx, ty);
-            __syncthreads();
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-#pragma unroll
-                for (int c = 0; c < 4; ++c) Ps[(ty * 8 + i) * kSimtLdP + tx + 16 * c] = dp[i][c];
-            __syncthreads();
-            simt_tn<DP>(dk, Ps, Qs, tx, ty);
-        }
+    const int qt0 = (int)(first / 64), qts = (a.Q + 63) / 64, per = qts > qt0 ? qts - qt0 : 0, total = a.G * per;
+    // step x: query tile qt0 + x % per of head x / per; the next one that the mask leaves a pair of
+    auto seen_from = [&](int x) {
+        if (a.bits)
+            while (x < total && !simt_tile_seen(a, b, n * a.G + x / per, (qt0 + x % per) * 64, j0)) ++x;
+        return x;
+    };
+    auto stat_at = [&](int x) { return ((long long)(b * rw.N + n * a.G + x / per) * rw.tiles + qt0 + x % per) * 64; };
+    // rows that take no part are cleared: their flags are written a tile ahead of the copies that ask for them
+    auto flags = [&](int x) {
+        if (threadIdx.x < 64) live[threadIdx.x] = a.row_l2[stat_at(x) + threadIdx.x] != -attn_inf();
+    };
+    auto fetch_q = [&](int x) {
+        const int m = n * a.G + x / per, q0 = (qt0 + x % per) * 64;
+        simt_load<T, DP>(Qs, static_cast<const T*>(a.q) + b * a.q_sb + m * a.q_sh + q0 * a.q_ss, a.q_ss, a.Q - q0, a.D, vec, live);
+    };
+    auto fetch_g = [&](int x) {
+        const int m = n * a.G + x / per, q0 = (qt0 + x % per) * 64;
+        simt_load<T, DP>(Gs, static_cast<const T*>(a.dout) + (((long long)b * a.Q + q0) * a.M + m) * a.D,
+                         (long long)a.M * a.D, a.Q - q0, a.D, vec, live);
+    };
+    int x = seen_from(0);
+    if (x < total) {
+        flags(x);
+        __syncthreads();
+        fetch_g(x);
+        fetch_q(x);
     }
+    while (x < total) {
+        const int m = n * a.G + x / per, q0 = (qt0 + x % per) * 64;
+        const int next = seen_from(x + 1);
+        simt_landed<1>();  // the gradient's rows (and K, V)
+        float s[8][4] = {}, dp[8][4] = {}, l2[8], dl[8];
+        simt_nt<DP>(dp, Gs, Vs, tx, ty);
+        const long long at = stat_at(x);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) l2[i] = a.row_l2[at + ty * 8 + i], dl[i] = a.row_dl[at + ty * 8 + i];
+        simt_landed<0>();
+        if (next < total) flags(next);  // both tiles have landed: the old flags are done with
+        simt_nt<DP>(s, Qs, Ks, tx, ty);
+        simt_mask(s, a, b, m, q0, j0, tx, ty);
+        simt_prob_grad(s, dp, l2, dl);
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) Ps[(ty * 8 + i) * kSimtLdP + tx + 16 * c] = s[i][c];
+        __syncthreads();
+        simt_tn<DP>(dv, Ps, Gs, tx, ty);
+        __syncthreads();
+        if (next < total) fetch_g(next);
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) Ps[(ty * 8 + i) * kSimtLdP + tx + 16 * c] = dp[i][c];
+        __syncthreads();
+        simt_tn<DP>(dk, Ps, Qs, tx, ty);
+        __syncthreads();
+        if (next < total) fetch_q(next);
+        x = next;
+    }
+    simt_landed<0>();
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         const int j = j0 + ty * 8 + i;
@@ -343,7 +423,7 @@ __global__ void __launch_bounds__(kSimtThreads) msda_attention_simt_grad_key_ker
 
 // Gradient of 64 queries of one head: over the keys that they see.
 template <typename T, int DP>
-__global__ void __launch_bounds__(kSimtThreads) msda_attention_simt_grad_query_kernel(const AttentionArgs a,
+__global__ void __launch_bounds__(kSimtThreads, simt_blocks(DP)) msda_attention_simt_grad_query_kernel(const AttentionArgs a,
                                                                                       const AttentionRows rw, bool vec) {
     extern __shared__ __align__(16) float simt_smem[];
     constexpr int LD = DP + 4;
@@ -370,15 +450,27 @@ __global__ void __launch_bounds__(kSimtThreads) msda_attention_simt_grad_query_k
 #pragma unroll
     for (int i = 0; i < 8; ++i) l2[i] = a.row_l2[at0 + ty * 8 + i], dl[i] = a.row_dl[at0 + ty * 8 + i];
     const int tiles = simt_key_tiles(a, q0);
-    for (int t = 0; t < tiles; ++t) {
-        const int j0 = t * 64;
-        __syncthreads();
-        simt_load<T, DP>(Ks, k + j0 * a.k_ss, a.k_ss, a.S - j0, a.D, vec, km ? km + j0 : nullptr);
-        simt_load<T, DP>(Vs, v + j0 * a.v_ss, a.v_ss, a.S - j0, a.D, vec, km ? km + j0 : nullptr);
-        __syncthreads();
+    auto fetch = [&](float* to, const T* from, long long stride, int t) {
+        simt_load<T, DP>(to, from + t * 64 * stride, stride, a.S - t * 64, a.D, vec, km ? km + t * 64 : nullptr);
+    };
+    auto seen_from = [&](int t) {
+        if (a.bits)
+            while (t < tiles && !simt_tile_seen(a, b, m, q0, t * 64)) ++t;
+        return t;
+    };
+    int t = seen_from(0);
+    if (t < tiles) {
+        fetch(Vs, v, a.v_ss, t);
+        fetch(Ks, k, a.k_ss, t);
+    }
+    while (t < tiles) {
+        const int j0 = t * 64, next = seen_from(t + 1);
+        simt_landed<1>();
         float s[8][4] = {}, dp[8][4] = {};
-        simt_nt<DP>(s, Qs, Ks, tx, ty);
         simt_nt<DP>(dp, Gs, Vs, tx, ty);
+        simt_landed<0>();
+        if (next < tiles) fetch(Vs, v, a.v_ss, next);
+        simt_nt<DP>(s, Qs, Ks, tx, ty);
         simt_mask(s, a, b, m, q0, j0, tx, ty);
         simt_prob_grad(s, dp, l2, dl);
 #pragma unroll
@@ -387,7 +479,11 @@ __global__ void __launch_bounds__(kSimtThreads) msda_attention_simt_grad_query_k
             for (int c = 0; c < 4; ++c) Ps[(ty * 8 + i) * kSimtLdP + tx + 16 * c] = dp[i][c];
         __syncthreads();
         simt_nn<DP>(dq, Ps, Ks, tx, ty);
+        __syncthreads();
+        if (next < tiles) fetch(Ks, k, a.k_ss, next);
+        t = next;
     }
+    simt_landed<0>();
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         const int qi = q0 + ty * 8 + i;
@@ -547,7 +643,7 @@ cudaError_t launch_attention_prepare(const AttentionArgs& a, const AttentionRows
 
 template <typename T, int DP>
 static cudaError_t simt_go(const AttentionArgs& a, bool vec, cudaStream_t st) {
-    const size_t smem = (size_t)(2 * kSimtRows * (DP + 4) + kSimtRows * kSimtLdP) * 4;
+    const size_t smem = (size_t)(3 * kSimtRows * (DP + 4) + kSimtRows * kSimtLdP) * 4;
     cudaError_t e = cudaFuncSetAttribute(msda_attention_simt_kernel<T, DP>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
     const long long grid = (long long)a.B * a.M * ((a.Q + 63) / 64) * a.splits;

@@ -15,10 +15,9 @@ struct TcArgs {
     AttentionArgs a;
     int G, qpt, rows;     // heads side by side in a row tile, queries a tile, rows used (G * qpt)
     int qblocks;          // row blocks of a key head (forward), row tiles of a head (backward)
-    const uint32_t* bits;   // pairs of the mask as bits [Bm, Mm, Q, W] (W = words a row, a multiple of 4) or null
-    const uint32_t* bits_t; // the same with keys as rows: [Bm, Mm, S, Wq]
-    long long bits_sb, bits_sh, bits_t_sb, bits_t_sh;
-    int W, Wq;
+    const uint32_t* bits_t;  // the mask's bits with keys as rows: [Bm, Mm, S, Wq], or null
+    long long bits_t_sb, bits_t_sh;
+    int Wq;
     int fix_rows;         // backward: rows without keys may occur, and are cleared
     const float* scale_in; // f16: the largest squared norms (see attention_amax), else null
 };

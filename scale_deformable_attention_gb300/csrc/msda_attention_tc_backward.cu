@@ -46,7 +46,7 @@ __device__ __forceinline__ TcScale tc_scale(const TcArgs& p) {
 
 struct TcBackwardSync {
     uint64_t own, full[8], empty[8], ready[8];
-    uint64_t s_full, dp_full, p_ready, ds_ready, s_free, ds_done[2], acc;
+    uint64_t s_full, dp_full, p_ready, ds_ready[2], s_free, ds_done[2], acc;
     uint32_t tmem, abort;
     uint32_t words[8][4];
 };
@@ -108,7 +108,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             tc_bar_init(tc_smem(&sy.s_full), 1);
             tc_bar_init(tc_smem(&sy.dp_full), 1);
             tc_bar_init(tc_smem(&sy.p_ready), 8);
-            tc_bar_init(tc_smem(&sy.ds_ready), 8);
+            tc_bar_init(tc_smem(&sy.ds_ready[0]), 8);
             tc_bar_init(tc_smem(&sy.acc), 1);
             tc_bar_init(tc_smem(&sy.s_free), 1);  // here: K and V are cleared
             sy.abort = 0;
@@ -214,7 +214,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             }
             tmem_wait_st();
             tc_fence_before();
-            tc_bar_arrive_if(first, tc_smem(&sy.ds_ready));
+            tc_bar_arrive_if(first, tc_smem(&sy.ds_ready[0]));
         }
         // ---- dV (first warpgroup) and dK (second) ----
         if (nt > 0 && ok) {
@@ -315,7 +315,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                     scores(tmem, k_desc, at(2 * i + 2));
                     tc_commit(on, tc_smem(&sy.s_full));
                 }
-                ok = tc_bar_wait(tc_smem(&sy.ds_ready), i & 1, abort, a.err);
+                ok = tc_bar_wait(tc_smem(&sy.ds_ready[0]), i & 1, abort, a.err);
                 if (!ok) break;
                 tc_fence_after();
                 gradient(tmem + Cfg::kDK, tmem + 128, at(2 * i), i > 0);
@@ -420,8 +420,10 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             tc_bar_init(tc_smem(&sy.own), 1);
             tc_bar_init(tc_smem(&sy.s_full), 1);
             tc_bar_init(tc_smem(&sy.s_free), 8);
-            tc_bar_init(tc_smem(&sy.ds_ready), 8);
-            for (int i = 0; i < 2; ++i) tc_bar_init(tc_smem(&sy.ds_done[i]), 1);
+            for (int i = 0; i < 2; ++i) {
+                tc_bar_init(tc_smem(&sy.ds_ready[i]), 8);
+                tc_bar_init(tc_smem(&sy.ds_done[i]), 1);
+            }
             sy.abort = 0;
             asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         }
@@ -447,7 +449,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         const bool live = l2 != -attn_inf();  // q < Q and some key seen
         const int seen = live ? tc_seen(a, q) : 0;
         const int seen_least = __reduce_min_sync(0xffffffffu, live ? seen : a.S);
-        const uint32_t* bits = p.bits && q < a.Q ? p.bits + b * p.bits_sb + h * p.bits_sh + (long long)q * p.W : nullptr;
+        const uint32_t* bits = a.bits && q < a.Q ? a.bits + b * a.bits_sb + h * a.bits_sh + (long long)q * a.W : nullptr;
         const uint64_t c2 = tc_two(a.c2, a.c2), nl = tc_two(l2, l2), nd = tc_two(dl * sc.ds, dl * sc.ds), ds2 = tc_two(sc.ds, sc.ds);
 #pragma unroll 1
         for (int i = 0; i < nt; ++i) {
@@ -465,7 +467,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             tmem_wait_ld();
             tc_fence_before();
             tc_bar_arrive_if(first, tc_smem(&sy.s_free));
-            if (__builtin_expect(km || p.bits || seen_least - j0 < 64, 0)) {
+            if (__builtin_expect(km || a.bits || seen_least - j0 < 64, 0)) {
                 const int see = seen - j0;
                 uint32_t m0 = bw.x & tc_low_bits(see), m1 = bw.y & tc_low_bits(see - 32);
                 if (km) m0 &= sy.words[i & 7][w * 2], m1 &= sy.words[i & 7][w * 2 + 1];
@@ -499,7 +501,9 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             }
             tmem_wait_st();
             tc_fence_before();
-            tc_bar_arrive_if(first, tc_smem(&sy.ds_ready));
+            // one barrier a buffer: a warp may be a tile ahead of another (it waits for dS(i-2) only), and its
+            // arrival must not count for that other's
+            tc_bar_arrive_if(first, tc_smem(&sy.ds_ready[i & 1]));
         }
         if (nt > 0 && ok) {
             ok = tc_bar_wait(tc_smem(&sy.ds_done[(nt - 1) & 1]), ((nt - 1) / 2) & 1, abort, a.err);
@@ -580,7 +584,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                     tc_fence_after();
                     scores(i + 1);
                 }
-                ok = tc_bar_wait(tc_smem(&sy.ds_ready), i & 1, abort, a.err);
+                ok = tc_bar_wait(tc_smem(&sy.ds_ready[i & 1]), (i / 2) & 1, abort, a.err);
                 if (!ok) break;
                 tc_fence_after();
                 const uint64_t k_desc = tc_desc(at(2 * i + 1), kTcTile, 1024);

@@ -136,7 +136,7 @@ __global__ void __launch_bounds__(TcForwardCfg<NQ, NC>::kThreads, 1)
         const uint32_t lanes = (uint32_t)wl << 21;  // this warp's lanes of tensor memory
         const uint32_t s_at = tmem + t * 128 + lanes, o_at = tmem + Cfg::kO + t * (NC * 64) + lanes;
         const uint32_t p_at = tmem + Cfg::kP + t * Cfg::kPStep + lanes;
-        const uint32_t* bits = p.bits && valid ? p.bits + b * p.bits_sb + h * p.bits_sh + (long long)q * p.W : nullptr;
+        const uint32_t* bits = a.bits && valid ? a.bits + b * a.bits_sb + h * a.bits_sh + (long long)q * a.W : nullptr;
         const int chunks = (a.D + 15) / 16;
         const uint32_t first = lane == 0;
         float m = -attn_inf(), l = 0.f;
@@ -156,7 +156,7 @@ __global__ void __launch_bounds__(TcForwardCfg<NQ, NC>::kThreads, 1)
                     tc_fence_before();
                     tc_bar_arrive_if(first, tc_smem(&sy.s_free[t]));
                 }
-                if (__builtin_expect(km || p.bits || seen_least - j0 < kTcRows, 0)) {
+                if (__builtin_expect(km || a.bits || seen_least - j0 < kTcRows, 0)) {
                     const int see = seen - j0;
                     uint32_t w[4] = {bw.x & tc_low_bits(see), bw.y & tc_low_bits(see - 32), bw.z & tc_low_bits(see - 64),
                                      bw.w & tc_low_bits(see - 96)};
