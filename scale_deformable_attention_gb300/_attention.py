@@ -13,6 +13,8 @@ from ._binding import DTYPE_CODE, on_device, ptr, stream
 def _rows(name: str, x: torch.Tensor) -> torch.Tensor:
     """``x`` [B, rows, heads, D] as the kernels read it: channels contiguous,
     every other stride at least a row (a broadcast dimension is copied)."""
+    if x.is_contiguous() and x.dim() == 4:
+        return x
     if x.dim() != 4:
         raise ValueError(f"{name} must be [B, rows, heads, D], got shape {tuple(x.shape)}")
     st, sh = x.stride(), x.shape
@@ -40,7 +42,7 @@ def _problem(query, key, value, mask, key_mask, causal, scale):
     if dev.type != "cuda":
         raise ValueError("the operator runs on CUDA tensors only (there is no CPU implementation)")
     for name, t in (("key", key), ("value", value)):
-        if tuple(t.shape) != (B, S, N, D):
+        if t.shape != (B, S, N, D):
             raise ValueError(f"{name} must be [B={B}, S={S}, heads={N}, D={D}], got {tuple(t.shape)}")
         if t.dtype != query.dtype:
             raise TypeError(f"{name} is {t.dtype}, query {query.dtype}; all float tensors share one dtype")

@@ -15,7 +15,8 @@ def ptr(t: Optional[torch.Tensor]) -> Optional[int]:
 
 
 def stream(device: torch.device) -> int:
-    return torch.cuda.current_stream(device).cuda_stream
+    """The current stream of ``device`` as a pointer (without the Stream object around it, which costs 2 us a call)."""
+    return torch._C._cuda_getCurrentRawStream(device.index)
 
 
 def on_device(device: torch.device):

@@ -661,6 +661,17 @@ msda_status device_facts(unsigned** err, int* sms) {
     return MSDA_OK;
 }
 
+cudaError_t allow_smem(const void* kernel, size_t bytes, SmemSeen& seen) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const unsigned long long ctx = current_context_id();
+    if (ctx != 0 && dev >= 0 && dev < kMaxDevices && seen.ctx[dev].load(std::memory_order_relaxed) == ctx) return cudaSuccess;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+    if (e == cudaSuccess && dev >= 0 && dev < kMaxDevices) seen.ctx[dev].store(ctx, std::memory_order_relaxed);
+    return e;
+}
+
 void* tensor_map_encoder() { return reinterpret_cast<void*>(encode_tiled()); }
 
 size_t fp32_workspace_bytes(msda_dtype dt, int64_t B, int64_t S, int64_t M, int64_t D, int64_t L, int64_t K,

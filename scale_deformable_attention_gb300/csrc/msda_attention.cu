@@ -129,15 +129,26 @@ MaskSpace mask_space(msda_dtype dt, unsigned flags, const msda_attention_problem
     return l;
 }
 
+struct ForwardPlan {
+    int G, qpt, nq, qblocks, splits, per;  // heads and queries a row tile, row tiles a block, blocks, split of the key axis
+};
+
 // Split of the key axis of the FMA-pipe forward: enough blocks for four a SM,
 // so that a single query over a long key axis uses the whole GPU.
-void simt_splits(const msda_attention_problem* p, int* splits, int* per) {
+// 16-bit tensors that come here for their addresses alone split no further than
+// the tensor-core form would, so that the workspace is that form's.
+ForwardPlan forward_plan(const msda_attention_problem* p);
+void simt_splits(msda_dtype dt, const msda_attention_problem* p, int* splits, int* per) {
     const int64_t blocks = p->B * p->M * ((p->Q + 63) / 64), tiles = (p->S + 63) / 64;
     int64_t n = 1;
     if (blocks > 0 && blocks < 2 * kSms && tiles > 1) {
         n = (4 * kSms + blocks - 1) / blocks;
         if (n > tiles) n = tiles;
         if (n > 64) n = 64;
+        if (tc_type(dt, p)) {
+            const int64_t most = forward_plan(p).splits;
+            if (n > most) n = most;
+        }
     }
     const int64_t each = tiles > 0 ? (tiles + n - 1) / n : 1;
     *per = (int)each;
@@ -249,9 +260,6 @@ bool tma_rows(const void* p, const int64_t* stride, int64_t B, int64_t rows, int
 // would leave SMs without a block.  A key axis of many tiles is split until
 // every SM has a block, but not into pieces of less than four tiles: a piece
 // costs a launch's start and the joining of its rows.
-struct ForwardPlan {
-    int G, qpt, nq, qblocks, splits, per;
-};
 ForwardPlan forward_plan(const msda_attention_problem* p) {
     ForwardPlan f;
     f.G = (int)(p->M / p->N);
@@ -312,13 +320,9 @@ extern "C" {
 size_t msda_attention_forward_workspace_size(msda_dtype dt, unsigned flags, const msda_attention_problem* p) {
     if (check(dt, flags, p) != MSDA_OK) return 0;
     int splits, per;
-    simt_splits(p, &splits, &per);
-    size_t part = part_bytes(p, splits);
-    if (tc_type(dt, p)) {  // which of the two runs depends on the addresses
-        const size_t tc = part_bytes(p, forward_plan(p).splits);
-        if (tc > part) part = tc;
-    }
-    return part + mask_space(dt, flags, p).bytes;
+    simt_splits(dt, p, &splits, &per);
+    if (tc_type(dt, p)) splits = forward_plan(p).splits;  // which of the two runs depends on the addresses
+    return part_bytes(p, splits) + mask_space(dt, flags, p).bytes;
 }
 
 size_t msda_attention_backward_workspace_size(msda_dtype dt, unsigned flags, const msda_attention_problem* p) {
@@ -358,7 +362,7 @@ msda_status msda_attention_forward(msda_dtype dt, unsigned flags, const msda_att
         f = forward_plan(p);
         a.splits = f.splits, a.tiles_per_split = f.per;
     } else {
-        simt_splits(p, &a.splits, &a.tiles_per_split);
+        simt_splits(dt, p, &a.splits, &a.tiles_per_split);
     }
     if (a.splits > 1) {
         unsigned char* part = static_cast<unsigned char*>(workspace) + ms.bytes;

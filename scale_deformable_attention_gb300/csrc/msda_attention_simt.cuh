@@ -14,6 +14,7 @@
 #pragma once
 
 #include "msda_attention.cuh"
+#include "msda_host.cuh"
 
 namespace msda {
 
@@ -644,7 +645,8 @@ cudaError_t launch_attention_prepare(const AttentionArgs& a, const AttentionRows
 template <typename T, int DP>
 static cudaError_t simt_go(const AttentionArgs& a, bool vec, cudaStream_t st) {
     const size_t smem = (size_t)(3 * kSimtRows * (DP + 4) + kSimtRows * kSimtLdP) * 4;
-    cudaError_t e = cudaFuncSetAttribute(msda_attention_simt_kernel<T, DP>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    static SmemSeen seen;
+    cudaError_t e = allow_smem(reinterpret_cast<const void*>(&msda_attention_simt_kernel<T, DP>), smem, seen);
     if (e != cudaSuccess) return e;
     const long long grid = (long long)a.B * a.M * ((a.Q + 63) / 64) * a.splits;
     msda_attention_simt_kernel<T, DP><<<(unsigned)grid, kSimtThreads, smem, st>>>(a, vec);
@@ -653,7 +655,8 @@ static cudaError_t simt_go(const AttentionArgs& a, bool vec, cudaStream_t st) {
 template <typename T, int DP>
 static cudaError_t simt_grad_key_go(const AttentionArgs& a, const AttentionRows& rw, bool vec, cudaStream_t st) {
     const size_t smem = (size_t)(4 * kSimtRows * (DP + 4) + kSimtRows * kSimtLdP + 16) * 4;
-    cudaError_t e = cudaFuncSetAttribute(msda_attention_simt_grad_key_kernel<T, DP>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    static SmemSeen seen;
+    cudaError_t e = allow_smem(reinterpret_cast<const void*>(&msda_attention_simt_grad_key_kernel<T, DP>), smem, seen);
     if (e != cudaSuccess) return e;
     const long long grid = (long long)a.B * a.N * ((a.S + 63) / 64);
     msda_attention_simt_grad_key_kernel<T, DP><<<(unsigned)grid, kSimtThreads, smem, st>>>(a, rw, vec);
@@ -662,7 +665,8 @@ static cudaError_t simt_grad_key_go(const AttentionArgs& a, const AttentionRows&
 template <typename T, int DP>
 static cudaError_t simt_grad_query_go(const AttentionArgs& a, const AttentionRows& rw, bool vec, cudaStream_t st) {
     const size_t smem = (size_t)(4 * kSimtRows * (DP + 4) + kSimtRows * kSimtLdP) * 4;
-    cudaError_t e = cudaFuncSetAttribute(msda_attention_simt_grad_query_kernel<T, DP>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    static SmemSeen seen;
+    cudaError_t e = allow_smem(reinterpret_cast<const void*>(&msda_attention_simt_grad_query_kernel<T, DP>), smem, seen);
     if (e != cudaSuccess) return e;
     const long long grid = (long long)a.B * a.M * ((a.Q + 63) / 64);
     msda_attention_simt_grad_query_kernel<T, DP><<<(unsigned)grid, kSimtThreads, smem, st>>>(a, rw, vec);

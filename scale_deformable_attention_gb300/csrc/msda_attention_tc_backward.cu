@@ -19,6 +19,7 @@
 // largest norms of dO and V rows bound from above; the sums are scaled back.
 #include "msda_attention_tc.cuh"
 #include "msda_attention_tc_host.cuh"
+#include "msda_host.cuh"
 
 namespace msda {
 
@@ -626,7 +627,8 @@ template <bool BF16, int NC>
 static cudaError_t grad_key_go(const TcArgs& p, const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v,
                                const CUtensorMap& g, cudaStream_t st) {
     constexpr size_t smem = TcKeyCfg<NC>::kSmem;
-    cudaError_t e = cudaFuncSetAttribute(msda_attention_tc_grad_key_kernel<BF16, NC>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    static SmemSeen seen;
+    cudaError_t e = allow_smem(reinterpret_cast<const void*>(&msda_attention_tc_grad_key_kernel<BF16, NC>), smem, seen);
     if (e != cudaSuccess) return e;
     const long long grid = (long long)p.a.B * p.a.N * ((p.a.S + kTcRows - 1) / kTcRows);
     msda_attention_tc_grad_key_kernel<BF16, NC><<<(unsigned)grid, kBwdThreads, smem, st>>>(p, q, k, v, g);
@@ -636,7 +638,8 @@ template <bool BF16, int NC>
 static cudaError_t grad_query_go(const TcArgs& p, const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v,
                                  const CUtensorMap& g, cudaStream_t st) {
     constexpr size_t smem = TcQueryCfg<NC>::kSmem;
-    cudaError_t e = cudaFuncSetAttribute(msda_attention_tc_grad_query_kernel<BF16, NC>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    static SmemSeen seen;
+    cudaError_t e = allow_smem(reinterpret_cast<const void*>(&msda_attention_tc_grad_query_kernel<BF16, NC>), smem, seen);
     if (e != cudaSuccess) return e;
     const long long grid = (long long)p.a.B * p.a.M * p.qblocks;
     msda_attention_tc_grad_query_kernel<BF16, NC><<<(unsigned)grid, kBwdThreads, smem, st>>>(p, q, k, v, g);

@@ -28,6 +28,7 @@
 // row tile's exponentials fill that time.
 #include "msda_attention_tc.cuh"
 #include "msda_attention_tc_host.cuh"
+#include "msda_host.cuh"
 
 namespace msda {
 
@@ -417,8 +418,8 @@ template <bool BF16, int NQ, int NC>
 static cudaError_t forward_go(const TcArgs& p, const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v,
                               cudaStream_t st) {
     using Cfg = TcForwardCfg<NQ, NC>;
-    cudaError_t e = cudaFuncSetAttribute(msda_attention_tc_forward_kernel<BF16, NQ, NC>,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Cfg::kSmem);
+    static SmemSeen seen;
+    cudaError_t e = allow_smem(reinterpret_cast<const void*>(&msda_attention_tc_forward_kernel<BF16, NQ, NC>), Cfg::kSmem, seen);
     if (e != cudaSuccess) return e;
     const long long grid = (long long)p.a.B * p.a.N * p.qblocks * p.a.splits;
     msda_attention_tc_forward_kernel<BF16, NQ, NC><<<(unsigned)grid, Cfg::kThreads, Cfg::kSmem, st>>>(p, q, k, v);

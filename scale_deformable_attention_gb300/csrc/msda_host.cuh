@@ -6,6 +6,7 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cstdarg>
 #include <cstdint>
 #include <cstdio>
@@ -30,6 +31,13 @@ struct TraceSpan {
 // Device address of the error word on the current device (its bits are those
 // of msda_device_errors()) and the number of its SMs.
 msda_status device_facts(unsigned** err, int* sms);
+
+// Sets a kernel's limit of dynamic shared memory, once a device context
+// (`seen`: one a kernel; a device reset gives a new context and sets it again).
+struct SmemSeen {
+    std::atomic<unsigned long long> ctx[64] = {};
+};
+cudaError_t allow_smem(const void* kernel, size_t bytes, SmemSeen& seen);
 
 // cuTensorMapEncodeTiled, or null where the driver does not give it.
 void* tensor_map_encoder();
