@@ -22,7 +22,7 @@ def _rows(name: str, x: torch.Tensor) -> torch.Tensor:
 
 
 def _like(name: str, t: torch.Tensor, shape, x: torch.Tensor) -> torch.Tensor:
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name} must be {tuple(shape)}, got {tuple(t.shape)}")
     if t.dtype != x.dtype:
         raise TypeError(f"{name} is {t.dtype}, query {x.dtype}; all float tensors share one dtype")
@@ -47,7 +47,7 @@ def _problem(query, key, positions, frequencies, sections):
         if key.dtype != query.dtype or key.device != dev:
             raise TypeError(f"key must be a {query.dtype} tensor on {dev}")
         ks = key.stride()
-    sections = tuple(int(n) for n in sections)
+    sections = tuple(sections)
     A, P = len(sections), sum(sections)
     if not 1 <= A <= 4:
         raise ValueError(f"sections must name 1 to 4 axes, got {sections}")
@@ -70,7 +70,7 @@ def _problem(query, key, positions, frequencies, sections):
 
 
 def _dense(x: torch.Tensor) -> torch.Tensor:
-    return torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    return torch.empty_like(x) if x.is_contiguous() else torch.empty(x.shape, dtype=x.dtype, device=x.device)
 
 
 def _forward(query, key, wq, wk, positions, frequencies, sections, eps, flags):

@@ -12,15 +12,14 @@ namespace {
 
 using msda::RotaryArgs;
 
-// Blocks of 256 threads, persistent over the chunks: six a SM of 152 are
-// resident at the kernels' register counts; the partial sums of the weights'
+// Blocks of 256 threads, persistent; the partial sums of the weights'
 // gradients have one row a block.
 constexpr int kRotaryMaxGrid = 152 * 6;
 constexpr int kChunkTokens[] = {32, 16, 8, 4};
 
-// Tokens a chunk: as many as leave two chunks an SM, 32 at most (the angles of
-// a chunk are worked out before its rows are read, so a small call wants many
-// small chunks and a large one few).
+// Element form, tokens a chunk: as many as leave two chunks an SM, 32 at most
+// (the angles of a chunk are worked out before its rows are read, so a small
+// call wants many small chunks and a large one few).
 int chunk_tokens(int64_t B, int64_t S) {
     for (int t : kChunkTokens)
         if (B * ((S + t - 1) / t) >= 2 * 152) return t;
@@ -133,19 +132,31 @@ msda_status run(msda_dtype dt, unsigned flags, const msda_rotary_problem* p, dou
     const bool inter = (flags & MSDA_ROTARY_INTERLEAVED) != 0;
     const int V = (int)(16 / es);
     // 16-byte vectors where every row is made of them (and, in halves, both
-    // halves of the pairs); items of a row go to up to 32 lanes
-    const bool fit = p->D % V == 0 && (inter || pairs % V == 0) &&
+    // halves of the pairs) and a row takes no more lanes than a warp has
+    const bool fit = p->D % V == 0 && p->D / V <= 32 && (inter || pairs % V == 0) &&
                      (p->M == 0 || vectors_fit(es, q, p->query_stride, oq, gq, wq)) &&
                      (p->N == 0 || vectors_fit(es, k, p->key_stride, ok, gk, wk));
-    const int items = fit ? (int)(p->D / V - (inter ? 0 : pairs / V)) : 0;
     int mode = msda::ROT_SCALAR, lg = 0;
-    if (fit && items <= 32) {
-        mode = inter ? msda::ROT_INTERLEAVED : msda::ROT_HALVES;
-        while ((1 << lg) < items) ++lg;
-    }
     size_t smem = (size_t)a.T * a.P * sizeof(float2);
+    int64_t blocks = a.chunks;
+    if (fit) {
+        mode = inter ? msda::ROT_INTERLEAVED : msda::ROT_HALVES;
+        while ((1 << lg) < p->D / V) ++lg;
+        // a warp takes all heads of its tokens, so that an angle is worked out
+        // once, unless that leaves fewer than 16 warps an SM
+        a.tokens = rows;
+        const int64_t groups = (rows + (32 >> lg) - 1) / (32 >> lg), heads = p->M + p->N;
+        int64_t parts = (152 * 16 + groups - 1) / groups;
+        if (parts > heads) parts = heads;
+        a.per = (int)((heads + parts - 1) / parts);
+        a.parts = (int)((heads + a.per - 1) / a.per);
+        smem = 0;
+        const int warps = msda::kRotaryThreads / 32;
+        blocks = (groups * a.parts + warps - 1) / warps;
+    }
     if (bwd && smem < (size_t)(msda::kRotaryThreads / 32) * a.D * 4) smem = (size_t)(msda::kRotaryThreads / 32) * a.D * 4;
-    const unsigned grid = (unsigned)(a.chunks < kRotaryMaxGrid ? a.chunks : kRotaryMaxGrid);
+    const int64_t most = bwd ? kRotaryMaxGrid : (int64_t)1 << 30;
+    const unsigned grid = (unsigned)(blocks < most ? blocks : most);
     cudaError_t e;
     {
         msda::TraceSpan ts(st);
@@ -174,10 +185,7 @@ extern "C" {
 
 size_t msda_norm_rotary_backward_workspace_size(const msda_rotary_problem* p) {
     if (!p || p->B <= 0 || p->S <= 0 || p->D <= 0 || p->D > msda::kRotaryMaxChannels) return 0;
-    const int T = chunk_tokens(p->B, p->S);
-    int64_t chunks;
-    if (__builtin_mul_overflow(p->B, (p->S + T - 1) / T, &chunks) || chunks > kRotaryMaxGrid) chunks = kRotaryMaxGrid;
-    return (size_t)chunks * 2 * (size_t)p->D * 4;
+    return (size_t)kRotaryMaxGrid * 2 * (size_t)p->D * 4;
 }
 
 msda_status msda_norm_rotary_forward(msda_dtype dt, unsigned flags, const msda_rotary_problem* problem, double eps,

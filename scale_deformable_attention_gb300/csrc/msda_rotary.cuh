@@ -9,14 +9,17 @@
 //   dx = r (w dz - n mean(n w dz)),   dw = sum over rows of n dz.
 //
 // What bounds it: memory.  Every element is read once (twice in the backward:
-// x and dy) and written once; all heads of a token share its angles, so a
-// block first works out cos and sin of a chunk of tokens into shared memory
-// (one sincos a token and pair, against (M + N) * 2 elements that use it) and
-// then streams the rows.  A row is taken by a group of lanes, 16 bytes a load;
-// a lane owns both halves of its pairs, so the rotation needs no exchange and
-// the row's sums take log2(lanes) shuffles.  The weights' gradients stay in
-// registers over all rows of a lane, then go through one partial row a block
-// and a second kernel that adds the partials in a fixed order: no atomics.
+// x and dy) and written once.  All heads of a token share its angles, so in the
+// vector form a lane owns 16 bytes of channels of one token, works out their cos
+// and sin once in registers and walks the heads: several 16-byte loads in
+// flight a lane, no shared memory, no barrier.  In halves a pair's two channels
+// belong to two lanes: each works out half of the pair's angles, and the raw 16
+// bytes are exchanged by four shuffles a row.  A row's sums take log2(lanes)
+// shuffles.  (With the angles of a chunk of tokens in shared memory and a lane
+// holding both halves of its pairs, a call of 20 heads of 128 ran at 26 % of the
+// copy rate.)  The weights' gradients stay in registers over all rows of a lane,
+// then go through one partial row a block and a second kernel that adds the
+// partials in a fixed order: no atomics.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -49,9 +52,11 @@ struct RotaryArgs {
     int pos_type;       // 0 float32, 1 int32, 2 int64
     int S, D, P, A;
     int axis_end[kRotaryMaxAxes];  // pairs below axis_end[a] (and not below axis_end[a-1]) turn by axis a
-    int T;              // tokens a chunk
+    int T;              // element form: tokens a chunk, chunks
     int chunks_per_b;
     long long chunks;
+    long long tokens;   // vector form: B * S, and the heads in `parts` parts of `per` (a warp takes one)
+    int parts, per;
     float eps, inv_d, sign;
 };
 
@@ -151,202 +156,225 @@ __device__ __forceinline__ void angle_cos_sin(double p64, float p, bool exact32,
     sincosf(r, s, c);
 }
 
-// cos / sin table of the chunk's tokens: [tokens][P] (cos, sin)
-__device__ __forceinline__ void rotary_table(const RotaryArgs& a, long long b, int s0, int nt, float2* table) {
-    for (int i = threadIdx.x; i < nt * a.P; i += kRotaryThreads) {
-        const int t = i / a.P, j = i - t * a.P;
-        int ax = 0;
-        while (ax < a.A - 1 && j >= a.axis_end[ax]) ++ax;
-        const long long at = b * a.pos_sb + (long long)(s0 + t) * a.A + ax;
-        double p64;
-        float p;
-        bool exact32 = true;
-        if (a.pos_type == 0) {
-            p = static_cast<const float*>(a.pos)[at];
-            p64 = p;
-        } else {
-            const long long v = a.pos_type == 1 ? (long long)static_cast<const int*>(a.pos)[at]
-                                                : static_cast<const long long*>(a.pos)[at];
-            p = (float)v;
-            p64 = (double)v;
-            exact32 = v > -16777217ll && v < 16777217ll;
-        }
-        float c, s;
-        angle_cos_sin(p64, p, exact32, a.freq[j], &c, &s);
-        table[i] = make_float2(c, s * a.sign);
-    }
-}
-
 enum { ROT_SCALAR = 0, ROT_HALVES = 1, ROT_INTERLEAVED = 2 };
 
-// What a lane holds of a row: up to two vectors of V channels at channel c0
-// and c1 (c1 < 0: absent); HALVES: c1 = c0 + P when the item is rotated.
+// cos and sin of pair j of the token whose positions start at element `at`
+__device__ __forceinline__ void rotary_angle(const RotaryArgs& a, long long at, int j, float* c, float* s) {
+    int ax = 0;
+    while (ax < a.A - 1 && j >= a.axis_end[ax]) ++ax;
+    double p64;
+    float p;
+    bool exact32 = true;
+    if (a.pos_type == 0) {
+        p = static_cast<const float*>(a.pos)[at + ax];
+        p64 = p;
+    } else {
+        const long long v = a.pos_type == 1 ? (long long)static_cast<const int*>(a.pos)[at + ax]
+                                            : static_cast<const long long*>(a.pos)[at + ax];
+        p = (float)v;
+        p64 = (double)v;
+        exact32 = v > -16777217ll && v < 16777217ll;
+    }
+    angle_cos_sin(p64, p, exact32, a.freq[j], c, s);
+    *s *= a.sign;
+}
+
+// A lane's channels [c, c + V) of a token and what turns them: channel i becomes
+//   own_i * cs[i] + other_i * sn[i]
+// with `other` the channel it is paired with (interleaved: its neighbour).
 template <int V>
-struct RotaryItem {
-    int c0, c1;
-    bool on, turned;
+struct RotaryLane {
+    int c, src;   // first channel; the lane that holds the other halves (halves)
+    bool on;      // channels inside D
+    float cs[V], sn[V];
 };
 
 template <int MODE, int V>
-__device__ __forceinline__ RotaryItem<V> rotary_item(int l, int D, int P) {
-    RotaryItem<V> it;
-    if constexpr (MODE == ROT_HALVES) {
-        const int np = P / V;
-        it.turned = l < np;
-        it.c0 = it.turned ? l * V : (l + np) * V;
-        it.c1 = it.turned ? l * V + P : -1;
-        it.on = it.c0 < D;
-    } else {
-        it.turned = true;
-        it.c0 = l * V;
-        it.c1 = -1;
-        it.on = it.c0 < D;
-    }
-    return it;
-}
-
-// z (the lane's channels: V of the first vector, V of the second) turned by
-// the token's angles; `inv` turns back (dz = R^T dy).
-template <int MODE, int V>
-__device__ __forceinline__ void rotary_turn(float* z, const RotaryItem<V>& it, const float2* tab, int P, bool inv) {
-    if constexpr (MODE == ROT_HALVES) {
-        if (it.turned) {
+__device__ __forceinline__ void rotary_lane(const RotaryArgs& a, int lg, long long token, RotaryLane<V>& r) {
+    const int lane = threadIdx.x & 31, l = lane & ((1 << lg) - 1);
+    r.c = l * V;
+    r.on = r.c < a.D && token < a.tokens;
+    r.src = lane;
 #pragma unroll
-            for (int i = 0; i < V; ++i) {
-                const float2 cs = tab[it.c0 + i];
-                const float s = inv ? -cs.y : cs.y;
-                const float u = z[i], v = z[V + i];
-                z[i] = u * cs.x - v * s;
-                z[V + i] = v * cs.x + u * s;
-            }
-        }
-    } else {
+    for (int i = 0; i < V; ++i) r.cs[i] = 1.f, r.sn[i] = 0.f;
+    long long at = 0;
+    if (token < a.tokens) {
+        const long long b = token / a.S;
+        at = b * a.pos_sb + (token - b * a.S) * a.A;
+    }
+    if constexpr (MODE == ROT_INTERLEAVED) {
 #pragma unroll
         for (int i = 0; i < V; i += 2) {
-            const int j = (it.c0 + i) >> 1;
-            if (j < P) {
-                const float2 cs = tab[j];
-                const float s = inv ? -cs.y : cs.y;
-                const float u = z[i], v = z[i + 1];
-                z[i] = u * cs.x - v * s;
-                z[i + 1] = v * cs.x + u * s;
+            const int j = (r.c + i) >> 1;
+            if (r.on && j < a.P) {
+                float c, s;
+                rotary_angle(a, at, j, &c, &s);
+                r.cs[i] = r.cs[i + 1] = c;
+                r.sn[i] = -s, r.sn[i + 1] = s;
+            }
+        }
+    } else {
+        const bool first = r.c < a.P, second = !first && r.c < 2 * a.P;
+        if (first) r.src = lane + a.P / V;
+        if (second) r.src = lane - a.P / V;
+        const int j0 = first ? r.c : r.c - a.P;
+        float c[V / 2], s[V / 2];  // the first half's lane takes pairs j0 .. j0 + V/2, the second's the rest
+#pragma unroll
+        for (int i = 0; i < V / 2; ++i) {
+            c[i] = 1.f, s[i] = 0.f;
+            if (r.on && (first || second)) rotary_angle(a, at, j0 + (first ? 0 : V / 2) + i, &c[i], &s[i]);
+        }
+#pragma unroll
+        for (int i = 0; i < V / 2; ++i) {
+            const float oc = __shfl_sync(0xffffffffu, c[i], r.src), os = __shfl_sync(0xffffffffu, s[i], r.src);
+            if (first || second) {
+                r.cs[i] = first ? c[i] : oc;
+                r.cs[V / 2 + i] = first ? oc : c[i];
+                const float lo = first ? s[i] : os, hi = first ? os : s[i];
+                r.sn[i] = first ? -lo : lo;
+                r.sn[V / 2 + i] = first ? -hi : hi;
             }
         }
     }
 }
 
-// The chunk's rows of one tensor, vector form.  LG = log2 of the lanes a row.
+// the paired channels' values (halves: from the other lane, as raw 16 bytes)
+template <typename T, int MODE>
+__device__ __forceinline__ uint4 rotary_other(uint4 v, int src) {
+    if constexpr (MODE == ROT_INTERLEAVED) return v;
+    return make_uint4(__shfl_sync(0xffffffffu, v.x, src), __shfl_sync(0xffffffffu, v.y, src),
+                      __shfl_sync(0xffffffffu, v.z, src), __shfl_sync(0xffffffffu, v.w, src));
+}
+
+template <typename T>
+__device__ __forceinline__ void rotary_unpack(uint4 u, float* v) {
+    alignas(16) T t[Vec16<T>::N];
+    *reinterpret_cast<uint4*>(t) = u;
+    Vec16<T>::load(t, v);
+}
+
+// Heads [h0, h1) of one tensor for the warp's tokens.
 template <typename T, int MODE, bool NORM, bool BWD>
-__device__ __forceinline__ void rotary_rows_vec(const RotaryArgs& a, const RotaryTensor& t, int lg, long long b, int s0,
-                                                int nt, const float2* table, float* dw) {
+__device__ __forceinline__ void rotary_heads(const RotaryArgs& a, const RotaryTensor& t, int lg, long long token,
+                                             const RotaryLane<Vec16<T>::N>& r, int h0, int h1, float* dw) {
     constexpr int V = Vec16<T>::N;
-    constexpr int W = MODE == ROT_HALVES ? 2 * V : V;
-    constexpr int U = BWD ? 1 : 2;  // rows in flight a lane (measured: two hide the loads' latency; the backward has two tensors in flight already)
-    const int lane_row = threadIdx.x & ((1 << lg) - 1);
-    const int group = threadIdx.x >> lg;
-    const int groups = kRotaryThreads >> lg;
-    const RotaryItem<V> it = rotary_item<MODE, V>(lane_row, a.D, a.P);
-    const T* x = static_cast<const T*>(t.x) + b * t.sb + (long long)s0 * t.ss;
-    const long long dense0 = (b * a.S + s0) * (long long)t.heads * a.D;
-    T* y = static_cast<T*>(t.y) + dense0;
-    const T* dy = BWD ? static_cast<const T*>(t.dy) + dense0 : nullptr;
-    float w[NORM ? W : 1];
+    // rows worked on at once; as many more are loaded meanwhile (backward of 20
+    // heads of 128: 438 us, 504 without the loads ahead, 467 with one row at once)
+    constexpr int U = 2;
+    if (h0 >= h1) return;           // the same for the whole warp (no keys: their pointers are null)
+    const long long b = token / a.S, s = token - b * a.S;
+    const T* x = static_cast<const T*>(t.x) + b * t.sb + s * t.ss + r.c;
+    T* y = static_cast<T*>(t.y) + token * t.heads * a.D + r.c;
+    const T* dy = BWD ? static_cast<const T*>(t.dy) + token * t.heads * a.D + r.c : nullptr;
+    // forward: what multiplies the own channels and the paired ones, weights included; backward: the weights
+    float w[V], wo[BWD ? 1 : V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) w[i] = 1.f;
     if constexpr (NORM) {
-        const T* wp = static_cast<const T*>(t.w);
+        uint4 raw = make_uint4(0, 0, 0, 0);
+        if (r.c < a.D) raw = *reinterpret_cast<const uint4*>(static_cast<const T*>(t.w) + r.c);
+        rotary_unpack<T>(raw, w);
+        if constexpr (!BWD) {
+            float o[V];
+            rotary_unpack<T>(rotary_other<T, MODE>(raw, r.src), o);
 #pragma unroll
-        for (int i = 0; i < W; ++i) w[i] = 0.f;
-        if (it.on) {
-            Vec16<T>::load(wp + it.c0, w);
-            if (MODE == ROT_HALVES && it.c1 >= 0) Vec16<T>::load(wp + it.c1, w + (MODE == ROT_HALVES ? V : 0));
+            for (int i = 0; i < V; ++i) wo[i] = o[MODE == ROT_INTERLEAVED ? i ^ 1 : i] * r.sn[i];
         }
+    } else if constexpr (!BWD) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) wo[i] = r.sn[i];
     }
-    const int rows = nt * t.heads;
-    int tok[U], head[U];
-    // rows group, group + groups, ... : token and head advance without a division
-    const int dt = groups / t.heads, dh = groups - dt * t.heads;
-    {
-        int tk = group / t.heads, hd = group - tk * t.heads;
+    if constexpr (!BWD) {
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            tok[u] = tk, head[u] = hd;
-            tk += dt, hd += dh;
-            if (hd >= t.heads) hd -= t.heads, ++tk;
-        }
+        for (int i = 0; i < V; ++i) w[i] *= r.cs[i];
     }
-    // every lane of a warp takes the same number of turns: the shuffles below need all of them
-    const int first_in_warp = (threadIdx.x & ~31) >> lg;
-    for (int r0 = 0; first_in_warp + r0 < rows; r0 += groups * U) {
-        float xv[U][W], gv[BWD ? W : 1];
+    uint4 xn[U], gn[BWD ? U : 1];
+    auto fetch = [&](int h) {
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-#pragma unroll
-            for (int i = 0; i < W; ++i) xv[u][i] = 0.f;
-            if (it.on && tok[u] < nt) {
-                const T* p = x + (long long)tok[u] * t.ss + (long long)head[u] * t.sh;
-                Vec16<T>::load(p + it.c0, xv[u]);
-                if (MODE == ROT_HALVES && it.c1 >= 0) Vec16<T>::load(p + it.c1, xv[u] + (MODE == ROT_HALVES ? V : 0));
+            const bool in = r.on && h + u < h1;
+            xn[u] = make_uint4(0, 0, 0, 0);
+            if (in) xn[u] = *reinterpret_cast<const uint4*>(x + (h + u) * t.sh);
+            if constexpr (BWD) {
+                gn[u] = make_uint4(0, 0, 0, 0);
+                if (in) gn[u] = *reinterpret_cast<const uint4*>(dy + (long long)(h + u) * a.D);
             }
         }
-        if constexpr (BWD) {
-#pragma unroll
-            for (int i = 0; i < W; ++i) gv[i] = 0.f;
-            if (it.on && tok[0] < nt) {
-                const T* p = dy + ((long long)tok[0] * t.heads + head[0]) * a.D;
-                Vec16<T>::load(p + it.c0, gv);
-                if (MODE == ROT_HALVES && it.c1 >= 0) Vec16<T>::load(p + it.c1, gv + (MODE == ROT_HALVES ? V : 0));
-            }
-        }
+    };
+    fetch(h0);
+#pragma unroll 1
+    for (int h = h0; h < h1; h += U) {
+        uint4 xr[U], gr[BWD ? U : 1];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            float r = 1.f;
-            if constexpr (NORM) {
-                float ss = 0.f;
-#pragma unroll
-                for (int i = 0; i < W; ++i) ss = fmaf(xv[u][i], xv[u][i], ss);
-                for (int o = (1 << lg) >> 1; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-                r = rsqrtf(ss * a.inv_d + a.eps);
-            }
-            const bool live = it.on && tok[u] < nt;
-            const float2* tab = table + (live ? tok[u] : 0) * a.P;
-            if constexpr (!BWD) {
-                if constexpr (NORM) {
-#pragma unroll
-                    for (int i = 0; i < W; ++i) xv[u][i] = xv[u][i] * r * w[i];
-                }
-                if (live) {
-                    rotary_turn<MODE, V>(xv[u], it, tab, a.P, false);
-                    T* p = y + ((long long)tok[u] * t.heads + head[u]) * a.D;
-                    Vec16<T>::store(p + it.c0, xv[u]);
-                    if (MODE == ROT_HALVES && it.c1 >= 0) Vec16<T>::store(p + it.c1, xv[u] + (MODE == ROT_HALVES ? V : 0));
-                }
-            } else {
-                if (live) rotary_turn<MODE, V>(gv, it, tab, a.P, true);
-                float dot = 0.f;
-#pragma unroll
-                for (int i = 0; i < W; ++i) {
-                    xv[u][i] *= r;  // n
-                    dw[i] = fmaf(gv[i], xv[u][i], dw[i]);
-                    gv[i] *= w[i];
-                    dot = fmaf(gv[i], xv[u][i], dot);
-                }
-                for (int o = (1 << lg) >> 1; o > 0; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
-                dot *= a.inv_d;
-                if (live) {
-#pragma unroll
-                    for (int i = 0; i < W; ++i) gv[i] = r * fmaf(-xv[u][i], dot, gv[i]);
-                    T* p = y + ((long long)tok[u] * t.heads + head[u]) * a.D;
-                    Vec16<T>::store(p + it.c0, gv);
-                    if (MODE == ROT_HALVES && it.c1 >= 0) Vec16<T>::store(p + it.c1, gv + (MODE == ROT_HALVES ? V : 0));
-                }
-            }
+            xr[u] = xn[u];
+            if constexpr (BWD) gr[u] = gn[u];
         }
-        // U * groups rows on
+        if (h + U < h1) fetch(h + U);
+        float rn[U];
+        if constexpr (NORM) {
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
+            for (int u = 0; u < U; ++u) {
+                float v[V], ss = 0.f;
+                rotary_unpack<T>(xr[u], v);
 #pragma unroll
-            for (int k = 0; k < U; ++k) {
-                tok[u] += dt, head[u] += dh;
-                if (head[u] >= t.heads) head[u] -= t.heads, ++tok[u];
+                for (int i = 0; i < V; ++i) ss = fmaf(v[i], v[i], ss);
+                rn[u] = ss;
+            }
+            for (int o = (1 << lg) >> 1; o > 0; o >>= 1) {
+#pragma unroll
+                for (int u = 0; u < U; ++u) rn[u] += __shfl_xor_sync(0xffffffffu, rn[u], o);
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u) rn[u] = rsqrtf(rn[u] * a.inv_d + a.eps);
+        }
+        if constexpr (!BWD) {
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                float v[V], o[V], z[V];
+                const uint4 other = rotary_other<T, MODE>(xr[u], r.src);
+                rotary_unpack<T>(xr[u], v);
+                rotary_unpack<T>(other, o);
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                    z[i] = fmaf(v[i], w[i], o[MODE == ROT_INTERLEAVED ? i ^ 1 : i] * wo[i]);
+                    if constexpr (NORM) z[i] *= rn[u];
+                }
+                if (r.on && h + u < h1) Vec16<T>::store(y + (long long)(h + u) * a.D, z);
+            }
+        } else {
+            float dot[U], g[U][V], n[U][V];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                float o[V];
+                const uint4 other = rotary_other<T, MODE>(gr[u], r.src);
+                rotary_unpack<T>(gr[u], g[u]);
+                rotary_unpack<T>(other, o);
+                rotary_unpack<T>(xr[u], n[u]);
+                dot[u] = 0.f;
+                float z[V];
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                    z[i] = fmaf(g[u][i], r.cs[i], -o[MODE == ROT_INTERLEAVED ? i ^ 1 : i] * r.sn[i]);  // turned back
+                    n[u][i] *= rn[u];
+                    dw[i] = fmaf(z[i], n[u][i], dw[i]);
+                }
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                    g[u][i] = z[i] * w[i];
+                    dot[u] = fmaf(g[u][i], n[u][i], dot[u]);
+                }
+            }
+            for (int o = (1 << lg) >> 1; o > 0; o >>= 1) {
+#pragma unroll
+                for (int u = 0; u < U; ++u) dot[u] += __shfl_xor_sync(0xffffffffu, dot[u], o);
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                dot[u] *= a.inv_d;
+#pragma unroll
+                for (int i = 0; i < V; ++i) g[u][i] = rn[u] * fmaf(-n[u][i], dot[u], g[u][i]);
+                if (r.on && h + u < h1) Vec16<T>::store(y + (long long)(h + u) * a.D, g[u]);
             }
         }
     }
@@ -442,33 +470,50 @@ __device__ __forceinline__ void rotary_rows_scalar(const RotaryArgs& a, const Ro
     }
 }
 
-// Persistent over chunks of T tokens of one batch item.  Shared memory:
-// float2[T][P], reused as float[8][D] for the weights' gradients at the end.
+// Vector form: a warp takes 32 >> lg tokens and one part of the heads (queries'
+// heads, then keys'); persistent.  Element form: a block takes chunks of T
+// tokens of one batch item, with their cos and sin in shared memory (float2[T][P]).
+// Shared memory is reused as float[8][D] for the weights' gradients at the end.
 template <typename T, int MODE, bool NORM, bool BWD>
-__global__ void __launch_bounds__(kRotaryThreads) msda_rotary_kernel(const RotaryArgs a, int lg, bool inter) {
+__global__ void __launch_bounds__(kRotaryThreads, MODE == ROT_SCALAR || BWD ? 2 : 3) msda_rotary_kernel(const RotaryArgs a, int lg, bool inter) {
     extern __shared__ __align__(16) unsigned char rotary_smem[];
-    float2* table = reinterpret_cast<float2*>(rotary_smem);
     constexpr int V = Vec16<T>::N;
-    constexpr int W = MODE == ROT_SCALAR ? 16 : MODE == ROT_HALVES ? 2 * V : V;
+    constexpr int W = MODE == ROT_SCALAR ? 16 : V;
     float dw[2][BWD ? W : 1];
     if constexpr (BWD) {
 #pragma unroll
         for (int i = 0; i < W; ++i) dw[0][i] = dw[1][i] = 0.f;
     }
-    for (long long ch = blockIdx.x; ch < a.chunks; ch += gridDim.x) {
-        const long long b = ch / a.chunks_per_b;
-        const int s0 = (int)(ch - b * a.chunks_per_b) * a.T;
-        const int nt = min(a.T, a.S - s0);
-        __syncthreads();  // the table of the chunk before is no longer read
-        rotary_table(a, b, s0, nt, table);
-        __syncthreads();
+    if constexpr (MODE == ROT_SCALAR) {
+        float2* table = reinterpret_cast<float2*>(rotary_smem);
+        for (long long ch = blockIdx.x; ch < a.chunks; ch += gridDim.x) {
+            const long long b = ch / a.chunks_per_b;
+            const int s0 = (int)(ch - b * a.chunks_per_b) * a.T;
+            const int nt = min(a.T, a.S - s0);
+            __syncthreads();  // the table of the chunk before is no longer read
+            for (int i = threadIdx.x; i < nt * a.P; i += kRotaryThreads) {
+                const int t = i / a.P, j = i - t * a.P;
+                rotary_angle(a, b * a.pos_sb + (long long)(s0 + t) * a.A, j, &table[i].x, &table[i].y);
+            }
+            __syncthreads();
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            if (a.t[k].heads == 0) continue;
-            if constexpr (MODE == ROT_SCALAR)
-                rotary_rows_scalar<T, NORM, BWD>(a, a.t[k], inter, b, s0, nt, table, dw[k]);
-            else
-                rotary_rows_vec<T, MODE, NORM, BWD>(a, a.t[k], lg, b, s0, nt, table, dw[k]);
+            for (int k = 0; k < 2; ++k)
+                if (a.t[k].heads > 0) rotary_rows_scalar<T, NORM, BWD>(a, a.t[k], inter, b, s0, nt, table, dw[k]);
+        }
+    } else {
+        const int tw = 32 >> lg;
+        const long long groups = (a.tokens + tw - 1) / tw, items = groups * a.parts;
+        const long long stride = (long long)gridDim.x * (kRotaryThreads / 32);
+        for (long long it = (long long)blockIdx.x * (kRotaryThreads / 32) + (threadIdx.x >> 5); it < items; it += stride) {
+            const long long group = it / a.parts;
+            const int h0 = (int)(it - group * a.parts) * a.per, h1 = h0 + a.per;
+            const long long token = group * tw + ((threadIdx.x & 31) >> lg);
+            RotaryLane<V> r;
+            rotary_lane<MODE, V>(a, lg, token, r);
+            const long long safe = token < a.tokens ? token : a.tokens - 1;  // a lane past the end reads and writes nothing
+            const int M = a.t[0].heads, all = M + a.t[1].heads;
+            rotary_heads<T, MODE, NORM, BWD>(a, a.t[0], lg, safe, r, min(h0, M), min(h1, M), dw[0]);
+            rotary_heads<T, MODE, NORM, BWD>(a, a.t[1], lg, safe, r, max(h0, M) - M, max(min(h1, all), M) - M, dw[1]);
         }
     }
     if constexpr (BWD) {
@@ -479,8 +524,6 @@ __global__ void __launch_bounds__(kRotaryThreads) msda_rotary_kernel(const Rotar
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
             __syncthreads();
-            for (int c = lane; c < a.D; c += 32) red[warp * a.D + c] = 0.f;
-            __syncwarp();
             if constexpr (MODE == ROT_SCALAR) {
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
@@ -496,13 +539,12 @@ __global__ void __launch_bounds__(kRotaryThreads) msda_rotary_kernel(const Rotar
                     if (c < a.D) red[warp * a.D + c] = dw[k][8 + i];
                 }
             } else {
-                const RotaryItem<V> it = rotary_item<MODE, V>(lane & ((1 << lg) - 1), a.D, a.P);
+                const int c = (lane & ((1 << lg) - 1)) * V;
 #pragma unroll
                 for (int i = 0; i < W; ++i) {
                     float v = dw[k][i];
                     for (int o = 1 << lg; o < 32; o <<= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-                    const int c = i < V ? it.c0 + i : it.c1 + i - V;
-                    if (lane < (1 << lg) && it.on && (i < V || it.c1 >= 0)) red[warp * a.D + c] = v;
+                    if (lane < (1 << lg) && c < a.D) red[warp * a.D + c + i] = v;
                 }
             }
             __syncthreads();
@@ -517,18 +559,19 @@ __global__ void __launch_bounds__(kRotaryThreads) msda_rotary_kernel(const Rotar
 
 // Weights' gradients: partial[n][2][D] added over n in a fixed order, rounded once.
 template <typename T>
-__global__ void __launch_bounds__(256) msda_rotary_weight_kernel(const float* partial, int n, int D, T* dwq, T* dwk) {
-    __shared__ float red[8][33];
+__global__ void __launch_bounds__(1024) msda_rotary_weight_kernel(const float* partial, int n, int D, T* dwq, T* dwk) {
+    __shared__ float red[32][33];
     const int col = blockIdx.x * 32 + (threadIdx.x & 31), part = threadIdx.x >> 5;
     float v = 0.f;
     if (col < 2 * D)
-        for (int i = part; i < n; i += 8) v += partial[(long long)i * 2 * D + col];
+#pragma unroll 4
+        for (int i = part; i < n; i += 32) v += partial[(long long)i * 2 * D + col];
     red[part][threadIdx.x & 31] = v;
     __syncthreads();
     if (part == 0 && col < 2 * D) {
         float s = 0.f;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) s += red[i][threadIdx.x & 31];
+        for (int i = 0; i < 32; ++i) s += red[i][threadIdx.x & 31];
         if (col < D) {
             if (dwq) dwq[col] = from_f32<T>(s);
         } else if (dwk) {
@@ -564,7 +607,7 @@ cudaError_t launch_rotary(const RotaryArgs& a, int mode, bool norm, bool bwd, in
 }
 template <typename T>
 cudaError_t launch_rotary_weight(const float* partial, int n, int D, void* dwq, void* dwk, cudaStream_t st) {
-    msda_rotary_weight_kernel<T><<<(2 * D + 31) / 32, 256, 0, st>>>(partial, n, D, static_cast<T*>(dwq),
+    msda_rotary_weight_kernel<T><<<(2 * D + 31) / 32, 1024, 0, st>>>(partial, n, D, static_cast<T*>(dwq),
                                                                    static_cast<T*>(dwk));
     return cudaGetLastError();
 }
