@@ -23,7 +23,10 @@
 
 namespace msda {
 
-constexpr int kBwdThreads = 384;  // two warpgroups on the scores, one of copies, products and clearing
+// Four warpgroups on the scores (32 columns of a tile each), one of copies,
+// products and clearing.  With two (64 columns each) a tile of 64 channels took
+// 2170 cycles, half of them waits that two warps a scheduler do not cover.
+constexpr int kBwdThreads = 640;
 
 // Exponents of the scalings: P 2^kp and dS 2^ks.
 struct TcScale {
@@ -47,7 +50,7 @@ __device__ __forceinline__ TcScale tc_scale(const TcArgs& p) {
 
 struct TcBackwardSync {
     uint64_t own, full[8], empty[8], ready[8];
-    uint64_t s_full, dp_full, p_ready, ds_ready[2], s_free, ds_done[2], acc;
+    uint64_t s_full[2], dp_full[2], p_ready[2], ds_ready[2], s_free, ds_done[2], acc;
     uint32_t tmem, abort;
     uint32_t words[8][4];
 };
@@ -61,7 +64,13 @@ struct TcKeyCfg {
     static constexpr uint32_t kTileBytes = NC * kTcTile;
     static constexpr uint32_t kStatBytes = 1024;  // l2 and delta of 128 rows, beside a tile of Q
     static constexpr size_t kSmem = 2 * kTileBytes + kRing * (kTileBytes + kStatBytes) + 1024;
-    static constexpr uint32_t kDV = 256, kDK = 256 + NC * 64;  // tensor memory: S 0, dP 128
+    // Up to 64 channels the halves of a tile (64 queries, two warpgroups each) are
+    // streams with products, barriers and sums of their own: neither waits for
+    // the other.  Beyond, tensor memory has no room for sums of each (and scores of
+    // 64 columns cost 48 cycles a step for 32 of work): both halves are one product.
+    static constexpr bool kStreams = NC == 1;
+    static constexpr int kParts = kStreams ? 2 : 1;
+    static constexpr uint32_t kDV = 256, kDK = 384;  // tensor memory: S 0, dP 128; streams' sums 64 apart
 };
 
 template <bool BF16, int NC>
@@ -98,24 +107,26 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         if (!__syncthreads_or(any)) nt = 0;
     }
 
-    if (warp == 8) {
+    if (warp == 16) {
         if (lane == 0) {
             for (int i = 0; i < R; ++i) {
                 tc_bar_init(tc_smem(&sy.full[i]), 1);
-                tc_bar_init(tc_smem(&sy.empty[i]), 1);
+                tc_bar_init(tc_smem(&sy.empty[i]), Cfg::kParts);
                 tc_bar_init(tc_smem(&sy.ready[i]), 1);
             }
             tc_bar_init(tc_smem(&sy.own), 1);
-            tc_bar_init(tc_smem(&sy.s_full), 1);
-            tc_bar_init(tc_smem(&sy.dp_full), 1);
-            tc_bar_init(tc_smem(&sy.p_ready), 8);
-            tc_bar_init(tc_smem(&sy.ds_ready[0]), 8);
-            tc_bar_init(tc_smem(&sy.acc), 1);
+            for (int i = 0; i < 2; ++i) {
+                tc_bar_init(tc_smem(&sy.s_full[i]), 1);
+                tc_bar_init(tc_smem(&sy.dp_full[i]), 1);
+                tc_bar_init(tc_smem(&sy.p_ready[i]), Cfg::kStreams ? 8 : 16);
+                tc_bar_init(tc_smem(&sy.ds_ready[i]), Cfg::kStreams ? 8 : 16);
+            }
+            tc_bar_init(tc_smem(&sy.acc), Cfg::kParts);
             tc_bar_init(tc_smem(&sy.s_free), 1);  // here: K and V are cleared
             sy.abort = 0;
             asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         }
-    } else if (warp == 9) {
+    } else if (warp == 17) {
         tmem_alloc(tc_smem(&sy.tmem), 512);
     }
     tc_fence_before();
@@ -126,112 +137,111 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     const bool fix = km || p.fix_rows;  // operands that a warp clears before the products read them
     bool ok = true;
 
-    if (warp < 8) {
-        // ---- probabilities and their gradients: thread = key row, 64 of a tile's 128 queries ----
+    if (warp < 16) {
+        tc_regs_up<104>();
+        // ---- probabilities and their gradients: thread = key row, 32 of a tile's 128 queries ----
         const int w = warp >> 2, wl = warp & 3, row = wl * 32 + lane, j = j0 + row;
         const uint32_t first = lane == 0;
+        const int h = Cfg::kStreams ? w >> 1 : 0;
         const uint32_t lanes = (uint32_t)wl << 21;
-        const uint32_t s_at = tmem + w * 64 + lanes, dp_at = tmem + 128 + w * 64 + lanes;
-        const TcScale sc = tc_scale<BF16>(p);
-        const uint64_t c2 = tc_two(a.c2, a.c2), ds2 = tc_two(sc.ds, sc.ds);
+        const uint32_t s_at = tmem + w * 32 + lanes, dp_at = tmem + 128 + w * 32 + lanes;
+        const uint64_t c2 = tc_two(a.c2, a.c2);
+        const float dscale = tc_scale<BF16>(p).ds;
         const bool has_bits = p.bits_t != nullptr;
         const int shift = a.S - a.Q;
 #pragma unroll 1
         for (int i = 0; i < nt; ++i) {
             const int g = i / per_head, rt = r0 + i - g * per_head, st = 2 * i % R;
-            const int q0 = rt * kTcRows + w * 64;
-            uint2 bw = make_uint2(~0u, ~0u);
-            if (has_bits) {
-                if (j < a.S) bw = *reinterpret_cast<const uint2*>(p.bits_t + b * p.bits_t_sb + (n * a.G + g) * p.bits_t_sh +
-                                                                  (long long)j * p.Wq + rt * 4 + w * 2);
-            }
-            const float* l2 = stats + st * 256 + w * 64;
+            const int q0 = rt * kTcRows + w * 32;
+            uint32_t bw = ~0u;
+            if (has_bits && j < a.S)
+                bw = p.bits_t[b * p.bits_t_sb + (n * a.G + g) * p.bits_t_sh + (long long)j * p.Wq + rt * 4 + w];
+            const float* l2 = stats + st * 256 + w * 32;
             const float* dl = l2 + 128;
             ok = tc_bar_wait(tc_smem(&sy.full[st]), (2 * i / R) & 1, abort, a.err) &&
-                 tc_bar_wait(tc_smem(&sy.s_full), i & 1, abort, a.err);
+                 tc_bar_wait(tc_smem(&sy.s_full[h]), i & 1, abort, a.err);
             if (!ok) break;
             tc_fence_after();
-            uint32_t s[2][32];
-            tmem_ld32(s[0], s_at);
-            tmem_ld32(s[1], s_at + 32);
+            uint32_t s[32];
+            tmem_ld32(s, s_at);
             tmem_wait_ld();
             // causal: query q sees key j if q >= j - shift
-            const int lo = a.causal ? j - shift - q0 : 0;
-            if (__builtin_expect(has_bits || __any_sync(0xffffffffu, lo > 0), 0)) {
-                const uint32_t m0 = bw.x & ~tc_low_bits(lo), m1 = bw.y & ~tc_low_bits(lo - 32);
-                if (__any_sync(0xffffffffu, (m0 & m1) != 0xffffffffu)) {
+            if (a.causal) bw &= ~tc_low_bits(j - shift - q0);
+            if (__builtin_expect(__any_sync(0xffffffffu, bw != 0xffffffffu), 0)) {
 #pragma unroll
-                    for (int k = 0; k < 32; ++k) {
-                        if (!((m0 >> k) & 1u)) s[0][k] = 0xff800000u;
-                        if (!((m1 >> k) & 1u)) s[1][k] = 0xff800000u;
-                    }
-                }
+                for (int k = 0; k < 32; ++k)
+                    if (!((bw >> k) & 1u)) s[k] = 0xff800000u;
             }
             // P^T over the thread's own columns of S^T
-#pragma unroll
-            for (int c = 0; c < 2; ++c) {
+            {
                 uint32_t pk[16];
 #pragma unroll
                 for (int k = 0; k < 32; k += 4) {
-                    const float4 l = *reinterpret_cast<const float4*>(l2 + c * 32 + k);
+                    const float4 l = *reinterpret_cast<const float4*>(l2 + k);
                     float x0, x1, x2, x3;
-                    tc_split(tc_fma2(tc_two(__uint_as_float(s[c][k]), __uint_as_float(s[c][k + 1])), c2, tc_two(l.x, l.y)), x0, x1);
-                    tc_split(tc_fma2(tc_two(__uint_as_float(s[c][k + 2]), __uint_as_float(s[c][k + 3])), c2, tc_two(l.z, l.w)), x2, x3);
+                    tc_split(tc_fma2(tc_two(__uint_as_float(s[k]), __uint_as_float(s[k + 1])), c2, tc_two(l.x, l.y)), x0, x1);
+                    tc_split(tc_fma2(tc_two(__uint_as_float(s[k + 2]), __uint_as_float(s[k + 3])), c2, tc_two(l.z, l.w)), x2, x3);
                     const float e0 = tc_ex2(x0), e1 = tc_ex2(x1), e2 = tc_ex2(x2), e3 = tc_ex2(x3);
-                    s[c][k] = __float_as_uint(e0), s[c][k + 1] = __float_as_uint(e1);
-                    s[c][k + 2] = __float_as_uint(e2), s[c][k + 3] = __float_as_uint(e3);
+                    s[k] = __float_as_uint(e0), s[k + 1] = __float_as_uint(e1);
+                    s[k + 2] = __float_as_uint(e2), s[k + 3] = __float_as_uint(e3);
                     pk[k / 2] = tc_pack<BF16>(e0, e1);
                     pk[k / 2 + 1] = tc_pack<BF16>(e2, e3);
                 }
-                tmem_st16(s_at + c * 16, pk);
+                tmem_st16(s_at, pk);
             }
             tmem_wait_st();
             tc_fence_before();
-            tc_bar_arrive_if(first, tc_smem(&sy.p_ready));
-            ok = tc_bar_wait(tc_smem(&sy.dp_full), i & 1, abort, a.err);
+            tc_bar_arrive_if(first, tc_smem(&sy.p_ready[h]));
+            ok = tc_bar_wait(tc_smem(&sy.dp_full[h]), i & 1, abort, a.err);
             if (!ok) break;
             tc_fence_after();
             // dS^T over dP^T
-#pragma unroll
-            for (int c = 0; c < 2; ++c) {
+            {
                 uint32_t d[32], pk[16];
-                tmem_ld32(d, dp_at + c * 32);
+                tmem_ld32(d, dp_at);
                 tmem_wait_ld();
 #pragma unroll
                 for (int k = 0; k < 32; k += 4) {
-                    const float4 l = *reinterpret_cast<const float4*>(dl + c * 32 + k);
+                    const float4 l = *reinterpret_cast<const float4*>(dl + k);
                     float x0, x1, x2, x3;
                     uint64_t y0 = tc_add2(tc_two(__uint_as_float(d[k]), __uint_as_float(d[k + 1])), tc_two(l.x, l.y));
                     uint64_t y1 = tc_add2(tc_two(__uint_as_float(d[k + 2]), __uint_as_float(d[k + 3])), tc_two(l.z, l.w));
-                    y0 = tc_mul2(y0, tc_two(__uint_as_float(s[c][k]), __uint_as_float(s[c][k + 1])));
-                    y1 = tc_mul2(y1, tc_two(__uint_as_float(s[c][k + 2]), __uint_as_float(s[c][k + 3])));
-                    if constexpr (!BF16) y0 = tc_mul2(y0, ds2), y1 = tc_mul2(y1, ds2);
+                    y0 = tc_mul2(y0, tc_two(__uint_as_float(s[k]), __uint_as_float(s[k + 1])));
+                    y1 = tc_mul2(y1, tc_two(__uint_as_float(s[k + 2]), __uint_as_float(s[k + 3])));
+                    if constexpr (!BF16) y0 = tc_mul2(y0, tc_two(dscale, dscale)), y1 = tc_mul2(y1, tc_two(dscale, dscale));
                     tc_split(y0, x0, x1);
                     tc_split(y1, x2, x3);
                     pk[k / 2] = tc_pack<BF16>(x0, x1);
                     pk[k / 2 + 1] = tc_pack<BF16>(x2, x3);
                 }
-                tmem_st16(dp_at + c * 16, pk);
+                tmem_st16(dp_at, pk);
             }
             tmem_wait_st();
             tc_fence_before();
-            tc_bar_arrive_if(first, tc_smem(&sy.ds_ready[0]));
+            tc_bar_arrive_if(first, tc_smem(&sy.ds_ready[h]));
         }
-        // ---- dV (first warpgroup) and dK (second) ----
+        // ---- dV (the first two warpgroups) and dK, alternate chunks of 16 channels ----
         if (nt > 0 && ok) {
             ok = tc_bar_wait(tc_smem(&sy.acc), 0, abort, a.err);
             tc_fence_after();
         }
         if (ok) {
             const bool live = nt > 0 && j < a.S && (!km || km[j]);
-            const float f = w == 0 ? sc.inv_p : sc.inv_ds * a.scale;
-            const uint32_t at = tmem + (w == 0 ? Cfg::kDV : Cfg::kDK) + lanes;
-            unsigned char* out = static_cast<unsigned char*>(w == 0 ? a.dv : a.dk) + (((long long)b * a.S + j) * a.N + n) * a.D * 2;
-            for (int c = 0; c < (a.D + 15) / 16; ++c) {
+            const TcScale sc = tc_scale<BF16>(p);
+            const float f = w < 2 ? sc.inv_p : sc.inv_ds * a.scale;
+            const uint32_t at = tmem + (w < 2 ? Cfg::kDV : Cfg::kDK) + lanes;
+            unsigned char* out = static_cast<unsigned char*>(w < 2 ? a.dv : a.dk) + (((long long)b * a.S + j) * a.N + n) * a.D * 2;
+            for (int c = w & 1; c < (a.D + 15) / 16; c += 2) {
                 uint32_t o[16];
                 if (nt > 0) {
+                    uint32_t o2[16];
                     tmem_ld16(o, at + c * 16);
+                    if (Cfg::kStreams) tmem_ld16(o2, at + 64 + c * 16);
                     tmem_wait_ld();
+                    if (Cfg::kStreams) {
+#pragma unroll
+                        for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) + __uint_as_float(o2[k]));
+                    }
                 }
                 if (j >= a.S) continue;
 #pragma unroll
@@ -245,7 +255,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             }
         }
     } else {
-        const int role = warp - 8;
+        tc_regs_down<64>();
+        const int role = warp - 16;
         uint64_t* full = fix ? sy.ready : sy.full;
         if (role == 0 && lane == 0 && nt > 0) {
             // ---- copies ----
@@ -269,64 +280,66 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                     tc_bulk(tc_smem(stats + st * 256 + 128), a.row_dl + r, 512, bar);
                 }
             }
-        } else if (role == 1 && nt > 0) {
-            // ---- products ----
+        } else if ((role == 1 || (Cfg::kStreams && role == 3)) && nt > 0) {
+            // ---- products (of stream h) ----
+            const int h = role >> 1;
             const uint32_t on = tc_elect();
             const int steps = (a.D + 15) / 16;
-            const uint32_t id_s = tc_idesc(BF16, false, false, 128, 128), id_g = tc_idesc(BF16, false, true, 128, steps * 16);
+            constexpr int NQ = 128 / Cfg::kParts;  // queries a product
+            const uint32_t dv_at = tmem + Cfg::kDV + h * 64, dk_at = tmem + Cfg::kDK + h * 64;
+            const uint32_t id_s = tc_idesc(BF16, false, false, 128, NQ), id_g = tc_idesc(BF16, false, true, 128, steps * 16);
             const uint64_t k_desc = tc_desc(tc_smem(k_tile), 16, 1024), v_desc = tc_desc(tc_smem(v_tile), 16, 1024);
             const uint32_t base = tc_smem(ring);
             auto at = [&](int x) { return base + (x % R) * Cfg::kTileBytes; };  // Q(i) is tile 2i, dO(i) 2i + 1
             auto filled = [&](int x) { return tc_bar_wait(tc_smem(&full[x % R]), (x / R) & 1, abort, a.err); };
-            auto scores = [&](uint32_t d, uint64_t x_desc, uint32_t y) {  // 128 keys x 128 queries
-                const uint64_t y_desc = tc_desc(y, 16, 1024);
+            // 128 keys x the stream's queries: into d, with y the tile of queries (or of their gradients)
+            auto scores = [&](uint32_t d, uint64_t x_desc, uint32_t y, uint32_t bar) {
+                const uint64_t y_desc = tc_desc(y + h * NQ * 128, 16, 1024);
 #pragma unroll
                 for (int k = 0; k < NC * 4; ++k) {
                     const uint64_t off = ((k >> 2) * kTcTile + (k & 3) * 32) >> 4;
-                    if (k < steps) tc_mma_ss(on, d, x_desc + off, y_desc + off, id_s, k > 0);
+                    if (k < steps) tc_mma_ss(on, d + h * NQ, x_desc + off, y_desc + off, id_s, k > 0);
                 }
+                tc_commit(on, bar);
             };
-            auto gradient = [&](uint32_t d, uint32_t x, uint32_t y, bool acc) {  // sums over 128 queries
-                const uint64_t y_desc = tc_desc(y, kTcTile, 1024);
+            // sums over the stream's queries
+            auto gradient = [&](uint32_t d, uint32_t x, uint32_t y, bool acc) {
+                const uint64_t y_desc = tc_desc(y + h * (NQ / 16) * 2048, kTcTile, 1024);
 #pragma unroll
-                for (int k = 0; k < 8; ++k)  // 16 queries: the two warpgroups' halves lie 64 columns apart
-                    tc_mma_ts(on, d, x + (k >> 2) * 64 + (k & 3) * 8, y_desc + ((k * 2048) >> 4), id_g, acc || k > 0);
+                for (int k = 0; k < NQ / 16; ++k)  // 16 queries; the warpgroups' parts of 32 lie 32 columns apart
+                    tc_mma_ts(on, d, x + h * 64 + (k >> 1) * 32 + (k & 1) * 8, y_desc + ((k * 2048) >> 4), id_g, acc || k > 0);
             };
             ok = tc_bar_wait(tc_smem(&sy.own), 0, abort, a.err);
             if (ok && fix) ok = tc_bar_wait(tc_smem(&sy.s_free), 0, abort, a.err);  // K and V cleared
             ok = ok && filled(0) && filled(1);
             if (ok) {
                 tc_fence_after();
-                scores(tmem, k_desc, at(0));
-                tc_commit(on, tc_smem(&sy.s_full));
-                scores(tmem + 128, v_desc, at(1));
-                tc_commit(on, tc_smem(&sy.dp_full));
+                scores(tmem, k_desc, at(0), tc_smem(&sy.s_full[h]));
+                scores(tmem + 128, v_desc, at(1), tc_smem(&sy.dp_full[h]));
             }
             for (int i = 0; i < nt && ok; ++i) {
                 const bool more = i + 1 < nt;
-                ok = tc_bar_wait(tc_smem(&sy.p_ready), i & 1, abort, a.err);
+                ok = tc_bar_wait(tc_smem(&sy.p_ready[h]), i & 1, abort, a.err);
                 if (!ok) break;
                 tc_fence_after();
-                gradient(tmem + Cfg::kDV, tmem, at(2 * i + 1), i > 0);
+                gradient(dv_at, tmem, at(2 * i + 1), i > 0);
                 tc_commit(on, tc_smem(&sy.empty[(2 * i + 1) % R]));
                 if (more) {
                     ok = filled(2 * i + 2);
                     if (!ok) break;
                     tc_fence_after();
-                    scores(tmem, k_desc, at(2 * i + 2));
-                    tc_commit(on, tc_smem(&sy.s_full));
+                    scores(tmem, k_desc, at(2 * i + 2), tc_smem(&sy.s_full[h]));
                 }
-                ok = tc_bar_wait(tc_smem(&sy.ds_ready[0]), i & 1, abort, a.err);
+                ok = tc_bar_wait(tc_smem(&sy.ds_ready[h]), i & 1, abort, a.err);
                 if (!ok) break;
                 tc_fence_after();
-                gradient(tmem + Cfg::kDK, tmem + 128, at(2 * i), i > 0);
+                gradient(dk_at, tmem + 128, at(2 * i), i > 0);
                 tc_commit(on, tc_smem(&sy.empty[2 * i % R]));
                 if (more) {
                     ok = filled(2 * i + 3);
                     if (!ok) break;
                     tc_fence_after();
-                    scores(tmem + 128, v_desc, at(2 * i + 3));
-                    tc_commit(on, tc_smem(&sy.dp_full));
+                    scores(tmem + 128, v_desc, at(2 * i + 3), tc_smem(&sy.dp_full[h]));
                 } else {
                     tc_commit(on, tc_smem(&sy.acc));
                 }
@@ -368,7 +381,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     if (!ok) tc_drain();
     tc_fence_before();
     __syncthreads();
-    if (warp == 9) tmem_dealloc(tmem, 512);
+    if (warp == 17) tmem_dealloc(tmem, 512);
 }
 
 // ---- gradient of queries ----
@@ -411,7 +424,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     if (km) tc_trim(km, a.S, &t0, &t1);
     const int nt = max(0, t1 - t0);
 
-    if (warp == 8) {
+    if (warp == 16) {
         if (lane == 0) {
             for (int i = 0; i < R; ++i) {
                 tc_bar_init(tc_smem(&sy.full[i]), 1);
@@ -419,16 +432,16 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                 tc_bar_init(tc_smem(&sy.ready[i]), 1);
             }
             tc_bar_init(tc_smem(&sy.own), 1);
-            tc_bar_init(tc_smem(&sy.s_full), 1);
-            tc_bar_init(tc_smem(&sy.s_free), 8);
+            tc_bar_init(tc_smem(&sy.s_full[0]), 1);
+            tc_bar_init(tc_smem(&sy.s_free), 16);
             for (int i = 0; i < 2; ++i) {
-                tc_bar_init(tc_smem(&sy.ds_ready[i]), 8);
+                tc_bar_init(tc_smem(&sy.ds_ready[i]), 16);
                 tc_bar_init(tc_smem(&sy.ds_done[i]), 1);
             }
             sy.abort = 0;
             asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         }
-    } else if (warp == 9) {
+    } else if (warp == 17) {
         tmem_alloc(tc_smem(&sy.tmem), 512);
     }
     tc_fence_before();
@@ -438,12 +451,13 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     volatile uint32_t* abort = &sy.abort;
     bool ok = true;
 
-    if (warp < 8) {
-        // thread = query row, 64 of a tile's 128 keys
+    if (warp < 16) {
+        tc_regs_up<104>();
+        // thread = query row, 32 of a tile's 128 keys
         const int w = warp >> 2, wl = warp & 3, row = wl * 32 + lane, q = q0 + row;
         const uint32_t first = lane == 0;
         const uint32_t lanes = (uint32_t)wl << 21;
-        const uint32_t s_at = tmem + w * 64 + lanes, dp_at = tmem + 128 + w * 64 + lanes, ds_at = tmem + Cfg::kDS + w * 32 + lanes;
+        const uint32_t s_at = tmem + w * 32 + lanes, dp_at = tmem + 128 + w * 32 + lanes, ds_at = tmem + Cfg::kDS + w * 16 + lanes;
         const TcScale sc = tc_scale<BF16>(p);
         const long long r = (((long long)b * a.M + h) * p.qblocks + rt) * kTcRows + row;
         const float l2 = a.row_l2[r], dl = a.row_dl[r];
@@ -454,30 +468,25 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         const uint64_t c2 = tc_two(a.c2, a.c2), nl = tc_two(l2, l2), nd = tc_two(dl * sc.ds, dl * sc.ds), ds2 = tc_two(sc.ds, sc.ds);
 #pragma unroll 1
         for (int i = 0; i < nt; ++i) {
-            const int j0 = (t0 + i) * kTcRows + w * 64;
-            uint2 bw = make_uint2(~0u, ~0u);
-            if (bits) bw = *reinterpret_cast<const uint2*>(bits + (t0 + i) * 4 + w * 2);
-            ok = tc_bar_wait(tc_smem(&sy.s_full), i & 1, abort, a.err);
+            const int j0 = (t0 + i) * kTcRows + w * 32;
+            uint32_t bw = ~0u;
+            if (bits) bw = bits[(t0 + i) * 4 + w];
+            ok = tc_bar_wait(tc_smem(&sy.s_full[0]), i & 1, abort, a.err);
             if (!ok) break;
             tc_fence_after();
-            uint32_t s[2][32], d[2][32];
-            tmem_ld32(s[0], s_at);
-            tmem_ld32(s[1], s_at + 32);
-            tmem_ld32(d[0], dp_at);
-            tmem_ld32(d[1], dp_at + 32);
+            uint32_t s[32], d[32];
+            tmem_ld32(s, s_at);
+            tmem_ld32(d, dp_at);
             tmem_wait_ld();
             tc_fence_before();
             tc_bar_arrive_if(first, tc_smem(&sy.s_free));
-            if (__builtin_expect(km || a.bits || seen_least - j0 < 64, 0)) {
-                const int see = seen - j0;
-                uint32_t m0 = bw.x & tc_low_bits(see), m1 = bw.y & tc_low_bits(see - 32);
-                if (km) m0 &= sy.words[i & 7][w * 2], m1 &= sy.words[i & 7][w * 2 + 1];
-                if (__any_sync(0xffffffffu, (m0 & m1) != 0xffffffffu)) {
+            if (__builtin_expect(km || a.bits || seen_least - j0 < 32, 0)) {
+                bw &= tc_low_bits(seen - j0);
+                if (km) bw &= sy.words[i & 7][w];
+                if (__any_sync(0xffffffffu, bw != 0xffffffffu)) {
 #pragma unroll
-                    for (int k = 0; k < 32; ++k) {
-                        if (!((m0 >> k) & 1u)) s[0][k] = 0xff800000u;
-                        if (!((m1 >> k) & 1u)) s[1][k] = 0xff800000u;
-                    }
+                    for (int k = 0; k < 32; ++k)
+                        if (!((bw >> k) & 1u)) s[k] = 0xff800000u;
                 }
             }
             if (i > 1) {  // dS(i-2) is used up
@@ -485,20 +494,19 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                 if (!ok) break;
                 tc_fence_after();
             }
-#pragma unroll
-            for (int c = 0; c < 2; ++c) {
+            {
                 uint32_t pk[16];
 #pragma unroll
                 for (int k = 0; k < 32; k += 2) {
                     float x0, x1;
-                    tc_split(tc_fma2(tc_two(__uint_as_float(s[c][k]), __uint_as_float(s[c][k + 1])), c2, nl), x0, x1);
+                    tc_split(tc_fma2(tc_two(__uint_as_float(s[k]), __uint_as_float(s[k + 1])), c2, nl), x0, x1);
                     const uint64_t e = tc_two(tc_ex2(x0), tc_ex2(x1));
-                    const uint64_t dp = tc_two(__uint_as_float(d[c][k]), __uint_as_float(d[c][k + 1]));
+                    const uint64_t dp = tc_two(__uint_as_float(d[k]), __uint_as_float(d[k + 1]));
                     const uint64_t y = tc_mul2(BF16 ? tc_add2(dp, nd) : tc_fma2(dp, ds2, nd), e);
                     tc_split(y, x0, x1);
                     pk[k / 2] = tc_pack<BF16>(x0, x1);
                 }
-                tmem_st16(ds_at + (i & 1) * 64 + c * 16, pk);
+                tmem_st16(ds_at + (i & 1) * 64, pk);
             }
             tmem_wait_st();
             tc_fence_before();
@@ -510,10 +518,10 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             ok = tc_bar_wait(tc_smem(&sy.ds_done[(nt - 1) & 1]), ((nt - 1) / 2) & 1, abort, a.err);
             tc_fence_after();
         }
-        if (ok) {  // the two warpgroups take alternate chunks of 16 channels
+        if (ok) {  // the warpgroups take every fourth chunk of 16 channels
             const float f = sc.inv_ds * a.scale;
             unsigned char* out = static_cast<unsigned char*>(a.dq) + (((long long)b * a.Q + q) * a.M + h) * a.D * 2;
-            for (int c = w; c < (a.D + 15) / 16; c += 2) {
+            for (int c = w; c < (a.D + 15) / 16; c += 4) {
                 uint32_t o[16];
                 if (nt > 0) {
                     tmem_ld16(o, tmem + Cfg::kDQ + lanes + c * 16);
@@ -531,7 +539,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             }
         }
     } else {
-        const int role = warp - 8;
+        tc_regs_down<64>();
+        const int role = warp - 16;
         uint64_t* full = km ? sy.ready : sy.full;
         if (role == 0 && lane == 0 && nt > 0) {
             const uint32_t own = tc_smem(&sy.own);
@@ -571,7 +580,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                     const uint64_t off = ((k >> 2) * kTcTile + (k & 3) * 32) >> 4;
                     if (k < steps) tc_mma_ss(on, tmem, q_desc + off, k_desc + off, id_s, k > 0);
                 }
-                tc_commit(on, tc_smem(&sy.s_full));
+                tc_commit(on, tc_smem(&sy.s_full[0]));
             };
             ok = tc_bar_wait(tc_smem(&sy.own), 0, abort, a.err) && filled(0) && filled(1);
             if (ok) {
@@ -618,7 +627,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     if (!ok) tc_drain();
     tc_fence_before();
     __syncthreads();
-    if (warp == 9) tmem_dealloc(tmem, 512);
+    if (warp == 17) tmem_dealloc(tmem, 512);
 }
 
 // ---- host ----

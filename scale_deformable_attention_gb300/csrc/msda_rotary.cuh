@@ -260,7 +260,7 @@ __device__ __forceinline__ void rotary_heads(const RotaryArgs& a, const RotaryTe
     constexpr int V = Vec16<T>::N;
     // rows worked on at once; as many more are loaded meanwhile (backward of 20
     // heads of 128: 438 us, 504 without the loads ahead, 467 with one row at once)
-    constexpr int U = 2;
+    constexpr int U = NORM ? 2 : 4;
     if (h0 >= h1) return;           // the same for the whole warp (no keys: their pointers are null)
     const long long b = token / a.S, s = token - b * a.S;
     const T* x = static_cast<const T*>(t.x) + b * t.sb + s * t.ss + r.c;
