@@ -47,13 +47,25 @@ __device__ __forceinline__ bool tc_bar_try(uint32_t bar, uint32_t parity) {
     return done != 0;
 }
 
-// Waits for the phase of `parity`; gives up after about 2^22 tries (a tile takes
-// microseconds, a try up to some), or when another role of the block has: then
-// the block's abort flag and the device's error bit 2 are set, and every role
-// leaves its loop.
+// The same, asleep for up to 20 us: a warp that polls takes issue slots from
+// those that work.
+__device__ __forceinline__ bool tc_bar_sleep(uint32_t bar, uint32_t parity) {
+    uint32_t done;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(done)
+        : "r"(bar), "r"(parity), "r"(20000u)
+        : "memory");
+    return done != 0;
+}
+
+// Waits for the phase of `parity`; gives up after 2^17 sleeps (a tile takes
+// microseconds), or when another role of the block has: then the block's abort
+// flag and the device's error bit 2 are set, and every role leaves its loop.
 __device__ __forceinline__ bool tc_bar_wait_slow(uint32_t bar, uint32_t parity, volatile uint32_t* abort, unsigned* err) {
-    for (int i = 0; i < (1 << 22); ++i) {
-        if (tc_bar_try(bar, parity)) return true;
+    for (int i = 0; i < (1 << 17); ++i) {
+        if (tc_bar_sleep(bar, parity)) return true;
         if (*abort) return false;
     }
     *abort = 1;
