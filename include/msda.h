@@ -425,7 +425,9 @@ const char* msda_last_error(void);
 const char* msda_status_string(msda_status s);
 
 /* Device-side error bits raised by kernels on the current device since the
- * last clear (bit 0: a level failed its shape check).  Synchronises the
+ * last clear (bit 0: a level failed its shape check; bit 1: a parameter copy
+ * timed out; bit 2: a wait inside a tensor-core attention kernel gave up and its
+ * output is not valid).  Synchronises the
  * device.  clear != 0 resets the bits. */
 msda_status msda_device_errors(uint32_t* bits, int clear);
 

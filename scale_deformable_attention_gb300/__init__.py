@@ -442,7 +442,8 @@ def reduction_ceiling(dtype=torch.bfloat16, *, row_bytes: int = 64, blocks_per_s
 
 def device_errors(clear: bool = True) -> int:
     """Error bits raised by kernels on the current device (bit 0: a level failed
-    its shape check; bit 1: a parameter copy timed out).  Synchronises."""
+    its shape check; bit 1: a parameter copy timed out; bit 2: a wait inside an
+    attention kernel gave up, its output is not valid).  Synchronises."""
     v = ctypes.c_uint32(0)
     _lib.check(_lib.lib().msda_device_errors(ctypes.byref(v), 1 if clear else 0))
     return int(v.value)

@@ -148,8 +148,8 @@ class _AttentionFunction(torch.autograd.Function):
     def backward(ctx, grad_out):
         query, key, value, out, lse, mask, key_mask = ctx.saved_tensors
         causal, scale = ctx.how
-        got = attention_backward(query, key, value, out, lse, grad_out, mask=mask, key_mask=key_mask, causal=causal,
-                                 scale=scale)
+        got = attention_backward(query, key, value, out, lse, grad_out.to(query.dtype), mask=mask, key_mask=key_mask,
+                                 causal=causal, scale=scale)
         return (*got, None, None, None, None)
 
 

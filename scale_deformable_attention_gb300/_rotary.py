@@ -22,6 +22,8 @@ def _rows(name: str, x: torch.Tensor) -> torch.Tensor:
 
 
 def _like(name: str, t: torch.Tensor, shape, x: torch.Tensor) -> torch.Tensor:
+    if t is None:
+        raise TypeError(f"{name} is missing")
     if t.shape != shape:
         raise ValueError(f"{name} must be {tuple(shape)}, got {tuple(t.shape)}")
     if t.dtype != x.dtype:
@@ -47,7 +49,7 @@ def _problem(query, key, positions, frequencies, sections):
         if key.dtype != query.dtype or key.device != dev:
             raise TypeError(f"key must be a {query.dtype} tensor on {dev}")
         ks = key.stride()
-    sections = tuple(sections)
+    sections = tuple(map(int, sections))
     A, P = len(sections), sum(sections)
     if not 1 <= A <= 4:
         raise ValueError(f"sections must name 1 to 4 axes, got {sections}")
@@ -76,7 +78,7 @@ def _dense(x: torch.Tensor) -> torch.Tensor:
 def _forward(query, key, wq, wk, positions, frequencies, sections, eps, flags):
     query, key, positions, frequencies, p = _problem(query, key, positions, frequencies, sections)
     D = query.shape[3]
-    if wq is not None:
+    if key is not None:
         wq = _like("query_weight", wq, (D,), query)
         wk = _like("key_weight", wk, (D,), query)
     q_out = _dense(query)
@@ -116,6 +118,8 @@ def norm_rotary_forward(query: torch.Tensor, key: torch.Tensor, query_weight: to
     """Queries [B, S, M, D] and keys [B, S, N, D], each row normed over its D
     channels (x w / sqrt(mean(x^2) + eps)) and rotated as by ``rotary_forward``,
     in one pass (C ABI ``msda_norm_rotary_forward``).  Weights [D]."""
+    if key is None:
+        raise TypeError("key is missing")
     return _forward(query, key, query_weight, key_weight, positions, frequencies, sections, float(eps),
                     _lib.ROTARY_INTERLEAVED if interleaved else 0)
 
@@ -126,6 +130,8 @@ def norm_rotary_backward(query: torch.Tensor, key: torch.Tensor, query_weight: t
                          interleaved: bool = False, workspace: Optional[torch.Tensor] = None
                          ) -> Tuple[torch.Tensor, torch.Tensor, torch.Tensor, torch.Tensor]:
     """(grad_query, grad_key, grad_query_weight, grad_key_weight) (C ABI ``msda_norm_rotary_backward``)."""
+    if key is None:
+        raise TypeError("key is missing")
     query, key, positions, frequencies, p = _problem(query, key, positions, frequencies, sections)
     D = query.shape[3]
     wq = _like("query_weight", query_weight, (D,), query)
@@ -151,6 +157,7 @@ class _RotaryFunction(torch.autograd.Function):
     def forward(ctx, x, positions, frequencies, sections, interleaved):
         ctx.save_for_backward(positions, frequencies)
         ctx.how = (sections, interleaved)
+        ctx.dtype = x.dtype
         return rotary_forward(x, positions, frequencies, sections, interleaved=interleaved)
 
     @staticmethod
@@ -158,7 +165,7 @@ class _RotaryFunction(torch.autograd.Function):
     def backward(ctx, grad):
         positions, frequencies = ctx.saved_tensors
         sections, interleaved = ctx.how
-        return rotary_backward(grad, positions, frequencies, sections, interleaved=interleaved), None, None, None, None
+        return rotary_backward(grad.to(ctx.dtype), positions, frequencies, sections, interleaved=interleaved), None, None, None, None
 
 
 class _NormRotaryFunction(torch.autograd.Function):
@@ -174,8 +181,8 @@ class _NormRotaryFunction(torch.autograd.Function):
     def backward(ctx, gq, gk):
         query, key, wq, wk, positions, frequencies = ctx.saved_tensors
         sections, eps, interleaved = ctx.how
-        got = norm_rotary_backward(query, key, wq, wk, positions, frequencies, sections, gq, gk, eps=eps,
-                                   interleaved=interleaved)
+        got = norm_rotary_backward(query, key, wq, wk, positions, frequencies, sections, gq.to(query.dtype),
+                                   gk.to(query.dtype), eps=eps, interleaved=interleaved)
         return (*got, None, None, None, None, None)
 
 

@@ -158,6 +158,89 @@ def test_strides(msda, how, dtype):
         R.check(got[name], want[name], name)
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("shape", [(1, 300), (2, 1, 1, 300), (4, 1, 300), (1, 4, 70, 300), (2, 1, 70, 300), (70, 300)])
+def test_broadcast_masks(msda, shape, dtype):
+    B, Q, S, M, N, D = 2, 70, 300, 4, 2, 64
+    q, k, v, do = make(21, dtype, B, Q, S, M, N, D)
+    mask = torch.rand(shape, device=DEV, generator=torch.Generator(device=DEV).manual_seed(22)) < 0.5
+    want = R.attention(q, k, v, do, mask.view((1,) * (4 - mask.dim()) + tuple(shape)))
+    for m in (mask, torch.stack((mask, ~mask), -1)[..., 0]):      # the second: keys are not next to one another
+        got = both(msda, q, k, v, do, {"mask": m})
+        for name in want:
+            R.check(got[name], want[name], name)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("size", [(1, 37, 200, 16, 1, 32), (2, 3, 1500, 32, 2, 64), (1, 150, 140, 9, 1, 128),
+                                  (1, 2, 300, 130, 1, 16), (300, 5, 6, 2, 1, 24)], ids=lambda s: "x".join(map(str, s)))
+def test_shared_heads(msda, size, dtype):
+    """Few and many query heads on one key head, more than a row tile holds, and many batch items."""
+    B, Q, S, M, N, D = size
+    q, k, v, do = make(23, dtype, *size)
+    kw, ok = masks("keys causal", 24, B, Q, S, M)
+    want = R.attention(q, k, v, do, ok)
+    got = both(msda, q, k, v, do, kw)
+    for name in want:
+        R.check(got[name], want[name], name)
+
+
+@pytest.mark.parametrize("dtype,D", [("f32", 48), ("bf16", 64), ("bf16", 72), ("f16", 20)])
+def test_nothing_is_written_outside(msda, dtype, D):
+    """Outputs inside larger buffers: what lies before and behind them stays (sizes that end inside every tile)."""
+    from scale_deformable_attention_gb300 import _lib
+    from scale_deformable_attention_gb300._attention import _problem
+
+    B, Q, S, M, N = 2, 131, 197, 4, 2
+    q, k, v, do = make(25, dtype, B, Q, S, M, N, D)
+    _, _, _, _, _, flags, p, scale, _ = _problem(q, k, v, None, None, True, None)
+    lib, dt = _lib.lib(), {"f32": 0, "f16": 1, "bf16": 2}[dtype]
+    pad = 1024
+
+    def guarded(n, t):
+        buf = torch.full((n + 2 * pad,), -7.0, dtype=t, device=DEV)
+        return buf, buf[pad:pad + n]
+
+    st = torch.cuda.current_stream().cuda_stream
+    need = max(lib.msda_attention_forward_workspace_size(dt, flags, p), lib.msda_attention_backward_workspace_size(dt, flags, p))
+    wb = torch.full((need + 4096,), 77, dtype=torch.uint8, device=DEV)
+    bufs = {n: guarded(e, t) for n, e, t in (("out", q.numel(), q.dtype), ("lse", B * M * Q, torch.float32),
+                                             ("gq", q.numel(), q.dtype), ("gk", k.numel(), q.dtype), ("gv", v.numel(), q.dtype))}
+    ptr = {n: b[1].data_ptr() for n, b in bufs.items()}
+    _lib.check(lib.msda_attention_forward(dt, flags, p, scale, q.data_ptr(), k.data_ptr(), v.data_ptr(), None, None,
+                                          ptr["out"], ptr["lse"], wb.data_ptr(), need, st))
+    _lib.check(lib.msda_attention_backward(dt, flags, p, scale, q.data_ptr(), k.data_ptr(), v.data_ptr(), None, None,
+                                           ptr["out"], ptr["lse"], do.data_ptr(), ptr["gq"], ptr["gk"], ptr["gv"],
+                                           wb.data_ptr(), need, st))
+    torch.cuda.synchronize()
+    for name, (buf, inner) in bufs.items():
+        assert (buf[:pad] == -7).all() and (buf[-pad:] == -7).all(), name
+        assert torch.isfinite(inner.float()).all() or name == "lse", name
+    assert (wb[need:] == 77).all()
+    want = both(msda, q, k, v, do, {"causal": True})
+    for a, b in (("out", "out"), ("lse", "lse"), ("gq", "grad_query"), ("gk", "grad_key"), ("gv", "grad_value")):
+        assert torch.equal(bufs[a][1], want[b].reshape(-1)), a
+
+
+def test_two_calls_at_once(msda):
+    """Two streams at the same time, forward and gradients, many times: each gives the lone call's bits."""
+    size = (2, 500, 900, 8, 4, 64)
+    ins = [make(s, "bf16", *size) for s in (26, 27)]
+    kw, _ = masks("pairs", 28, 2, 500, 900, 8)
+    alone = [both(msda, *t, kw) for t in ins]
+    streams = [torch.cuda.Stream() for _ in ins]
+    torch.cuda.synchronize()
+    for _ in range(10):
+        got = []
+        for st, t in zip(streams, ins):
+            with torch.cuda.stream(st):
+                got.append(both(msda, *t, kw))
+        torch.cuda.synchronize()
+        for a, g in zip(alone, got):
+            for name in a:
+                assert torch.equal(a[name], g[name]), name
+
+
 @pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
 def test_large_scores_and_gradients(msda, dtype):
     """Scores far apart (one key takes everything) and gradients of a scaled loss."""
