@@ -50,7 +50,7 @@ __device__ __forceinline__ TcScale tc_scale(const TcArgs& p) {
 
 struct TcBackwardSync {
     uint64_t own, full[8], empty[8], ready[8];
-    uint64_t s_full[2], dp_full[2], p_ready[2], ds_ready[2][2], s_free[2], ds_done[2][2], acc;
+    uint64_t s_full[2], dp_full[2], p_ready[2], ds_ready[2][2], s_free[2], ds_done[2][2], acc, delta;
     uint32_t tmem, abort;
     uint32_t words[8][4];
 };
@@ -439,6 +439,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             }
             tc_bar_init(tc_smem(&sy.own), 1);
             tc_bar_init(tc_smem(&sy.acc), Cfg::kParts);
+            tc_bar_init(tc_smem(&sy.delta), 16);
             for (int h = 0; h < 2; ++h) {
                 tc_bar_init(tc_smem(&sy.s_full[h]), 1);
                 tc_bar_init(tc_smem(&sy.s_free[h]), 16 / Cfg::kParts);
@@ -476,7 +477,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         const int seen = live ? tc_seen(a, q) : 0;
         const int seen_least = __reduce_min_sync(0xffffffffu, live ? seen : a.S);
         const uint32_t* bits = a.bits && q < a.Q ? a.bits + b * a.bits_sb + h * a.bits_sh + (long long)q * a.W : nullptr;
-        const uint64_t c2 = tc_two(a.c2, a.c2), nl = tc_two(l2, l2), nd = tc_two(dl * sc.ds, dl * sc.ds), ds2 = tc_two(sc.ds, sc.ds);
+        const uint64_t c2 = tc_two(a.c2, a.c2), nl = tc_two(l2, l2), ds2 = tc_two(sc.ds, sc.ds);
+        uint64_t nd = tc_two(dl * sc.ds, dl * sc.ds);
 #pragma unroll 1
         for (int i = 0; i < nt; ++i) {
             const int j0 = (t0 + i) * kTcRows + w * 32;
@@ -499,6 +501,30 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                     for (int k = 0; k < 32; ++k)
                         if (!((bw >> k) & 1u)) s[k] = 0xff800000u;
                 }
+            }
+            if (p.delta_out) {
+                // One tile of keys: delta = sum_j p dP from the values at hand, not <dout, out>.  With few keys out is
+                // as large as a value and its rounding to 16 bits, carried into dP - delta, was the largest error
+                // (twice the others together for two keys).
+                float2* part_sum = reinterpret_cast<float2*>(ring + 2 * Cfg::kTileBytes);  // one tile: the ring's third is free
+                float sum = 0.f, ps = 0.f;
+#pragma unroll
+                for (int k = 0; k < 32; ++k) {  // a pair that takes no part adds nothing, whatever its dP
+                    const float e = tc_ex2(fmaf(__uint_as_float(s[k]), a.c2, l2));
+                    if (s[k] != 0xff800000u) sum = fmaf(e, __uint_as_float(d[k]), sum), ps += e;
+                }
+                part_sum[w * 128 + row] = make_float2(sum, ps);
+                __syncwarp();
+                if (lane == 0) tc_bar_arrive(tc_smem(&sy.delta));
+                ok = tc_bar_wait(tc_smem(&sy.delta), 0, abort, a.err);
+                if (!ok) break;
+                sum = ps = 0.f;
+#pragma unroll
+                for (int g = 0; g < 4; ++g) sum += part_sum[g * 128 + row].x, ps += part_sum[g * 128 + row].y;
+                // over the probabilities' own sum, which their rounding keeps off 1: the row's dS then add up to 0
+                const float delta = live && ps > 0.f ? -sum / ps : 0.f;
+                nd = tc_two(delta * sc.ds, delta * sc.ds);
+                if (w == 0) p.delta_out[r] = delta;
             }
             if (i > 1) {  // dS(i-2) is used up
                 ok = tc_bar_wait(tc_smem(&sy.ds_done[part][i & 1]), (i / 2 - 1) & 1, abort, a.err);

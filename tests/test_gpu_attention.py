@@ -281,6 +281,20 @@ def test_small_values_in_half_precision(msda):
         assert rel <= 2 * 2.0 ** -11, (name, rel)
 
 
+@pytest.mark.parametrize("S", [2, 3, 7, 40, 128])
+def test_few_keys_keep_their_gradients(msda, S):
+    """With few keys the output is as large as a value: delta = <dout, out> from its 16 bits would carry an error of
+    |dout| |out| 2^-8 into differences dP - delta that are smaller.  Left are the roundings of dS, of P and of the result, each
+    uniform within 2^-8 (2^-8 / sqrt(3) of a value in the root mean square): at most 2^-8 together."""
+    for D in (8, 96):
+        q, k, v, do = make(29, "bf16", 7, 3, S, 16, 16, D)
+        want = R.attention(q, k, v, do)
+        got = both(msda, q, k, v, do, {})
+        for name in ("grad_query", "grad_key", "grad_value"):
+            value = want[name][0]
+            assert float((got[name].double() - value).norm() / value.norm()) <= 2.0 ** -8, (name, D)
+
+
 def test_empty_tensors(msda):
     dev = torch.device(DEV)
     for B, Q, S in ((0, 5, 5), (2, 0, 5), (2, 5, 0), (0, 0, 0)):
