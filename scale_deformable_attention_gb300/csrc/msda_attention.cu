@@ -257,7 +257,7 @@ bool tma_rows(const void* p, const int64_t* stride, int64_t B, int64_t rows, int
 
 // Row blocks and split of the tensor-core forward.  Two row tiles a block
 // overlap one's products with the other's exponentials; one tile where two
-// would leave SMs without a block.  A key axis of many tiles is split until
+// would leave SMs without a block, or where the last round of blocks eats the gain.  A key axis of many tiles is split until
 // every SM has a block, but not into pieces of less than four tiles: a piece
 // costs a launch's start and the joining of its rows.
 ForwardPlan forward_plan(const msda_attention_problem* p) {
@@ -265,7 +265,9 @@ ForwardPlan forward_plan(const msda_attention_problem* p) {
     f.G = (int)(p->M / p->N);
     f.qpt = msda::kTcRows / f.G;
     const int64_t one = (p->Q + f.qpt - 1) / f.qpt, two = (p->Q + 2 * f.qpt - 1) / (2 * f.qpt);
-    f.nq = p->B * p->N * two >= kSms ? 2 : 1;
+    // rounds of blocks, one an SM; a step of two tiles takes about three halves of a step of one
+    const int64_t heads = p->B * p->N, rounds1 = (heads * one + kSms - 1) / kSms, rounds2 = (heads * two + kSms - 1) / kSms;
+    f.nq = heads * two >= kSms && 3 * rounds2 <= 2 * rounds1 ? 2 : 1;
     f.qblocks = (int)(f.nq == 2 ? two : one);
     const int64_t blocks = p->B * p->N * f.qblocks, tiles = (p->S + msda::kTcRows - 1) / msda::kTcRows;
     int64_t n = blocks > 0 ? kSms / blocks : 1;

@@ -50,7 +50,7 @@ __device__ __forceinline__ TcScale tc_scale(const TcArgs& p) {
 
 struct TcBackwardSync {
     uint64_t own, full[8], empty[8], ready[8];
-    uint64_t s_full[2], dp_full[2], p_ready[2], ds_ready[2][2], s_free[2], ds_done[2][2], acc, delta;
+    uint64_t s_full, dp_full, p_ready, ds_ready[2], s_free, ds_done[2], acc, delta;
     uint32_t tmem, abort;
     uint32_t words[8][4];
 };
@@ -64,13 +64,7 @@ struct TcKeyCfg {
     static constexpr uint32_t kTileBytes = NC * kTcTile;
     static constexpr uint32_t kStatBytes = 1024;  // l2 and delta of 128 rows, beside a tile of Q
     static constexpr size_t kSmem = 2 * kTileBytes + kRing * (kTileBytes + kStatBytes) + 1024;
-    // Up to 64 channels the halves of a tile (64 queries, two warpgroups each) are
-    // streams with products, barriers and sums of their own: neither waits for
-    // the other.  Beyond, tensor memory has no room for sums of each (and scores of
-    // 64 columns cost 48 cycles a step for 32 of work): both halves are one product.
-    static constexpr bool kStreams = NC == 1;
-    static constexpr int kParts = kStreams ? 2 : 1;
-    static constexpr uint32_t kDV = 256, kDK = 384;  // tensor memory: S 0, dP 128; streams' sums 64 apart
+    static constexpr uint32_t kDV = 256, kDK = 384;  // tensor memory: S 0, dP 128
 };
 
 template <bool BF16, int NC>
@@ -111,18 +105,16 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         if (lane == 0) {
             for (int i = 0; i < R; ++i) {
                 tc_bar_init(tc_smem(&sy.full[i]), 1);
-                tc_bar_init(tc_smem(&sy.empty[i]), Cfg::kParts);
+                tc_bar_init(tc_smem(&sy.empty[i]), 1);
                 tc_bar_init(tc_smem(&sy.ready[i]), 1);
             }
             tc_bar_init(tc_smem(&sy.own), 1);
-            for (int i = 0; i < 2; ++i) {
-                tc_bar_init(tc_smem(&sy.s_full[i]), 1);
-                tc_bar_init(tc_smem(&sy.dp_full[i]), 1);
-                tc_bar_init(tc_smem(&sy.p_ready[i]), Cfg::kStreams ? 8 : 16);
-                tc_bar_init(tc_smem(&sy.ds_ready[i][0]), Cfg::kStreams ? 8 : 16);
-            }
-            tc_bar_init(tc_smem(&sy.acc), Cfg::kParts);
-            tc_bar_init(tc_smem(&sy.s_free[0]), 1);  // here: K and V are cleared
+            tc_bar_init(tc_smem(&sy.s_full), 1);
+            tc_bar_init(tc_smem(&sy.dp_full), 1);
+            tc_bar_init(tc_smem(&sy.p_ready), 16);
+            tc_bar_init(tc_smem(&sy.ds_ready[0]), 16);
+            tc_bar_init(tc_smem(&sy.acc), 1);
+            tc_bar_init(tc_smem(&sy.s_free), 1);  // here: K and V are cleared
             sy.abort = 0;
             asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         }
@@ -142,7 +134,6 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         // ---- probabilities and their gradients: thread = key row, 32 of a tile's 128 queries ----
         const int w = warp >> 2, wl = warp & 3, row = wl * 32 + lane, j = j0 + row;
         const uint32_t first = lane == 0;
-        const int h = Cfg::kStreams ? w >> 1 : 0;
         const uint32_t lanes = (uint32_t)wl << 21;
         const uint32_t s_at = tmem + w * 32 + lanes, dp_at = tmem + 128 + w * 32 + lanes;
         const uint64_t c2 = tc_two(a.c2, a.c2);
@@ -159,7 +150,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             const float* l2 = stats + st * 256 + w * 32;
             const float* dl = l2 + 128;
             ok = tc_bar_wait(tc_smem(&sy.full[st]), (2 * i / R) & 1, abort, a.err) &&
-                 tc_bar_wait(tc_smem(&sy.s_full[h]), i & 1, abort, a.err);
+                 tc_bar_wait(tc_smem(&sy.s_full), i & 1, abort, a.err);
             if (!ok) break;
             tc_fence_after();
             uint32_t s[32];
@@ -191,8 +182,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             }
             tmem_wait_st();
             tc_fence_before();
-            tc_bar_arrive_if(first, tc_smem(&sy.p_ready[h]));
-            ok = tc_bar_wait(tc_smem(&sy.dp_full[h]), i & 1, abort, a.err);
+            tc_bar_arrive_if(first, tc_smem(&sy.p_ready));
+            ok = tc_bar_wait(tc_smem(&sy.dp_full), i & 1, abort, a.err);
             if (!ok) break;
             tc_fence_after();
             // dS^T over dP^T
@@ -218,7 +209,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             }
             tmem_wait_st();
             tc_fence_before();
-            tc_bar_arrive_if(first, tc_smem(&sy.ds_ready[h][0]));
+            tc_bar_arrive_if(first, tc_smem(&sy.ds_ready[0]));
         }
         // ---- dV (the first two warpgroups) and dK, alternate chunks of 16 channels ----
         if (nt > 0 && ok) {
@@ -234,14 +225,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             for (int c = w & 1; c < (a.D + 15) / 16; c += 2) {
                 uint32_t o[16];
                 if (nt > 0) {
-                    uint32_t o2[16];
                     tmem_ld16(o, at + c * 16);
-                    if (Cfg::kStreams) tmem_ld16(o2, at + 64 + c * 16);
                     tmem_wait_ld();
-                    if (Cfg::kStreams) {
-#pragma unroll
-                        for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) + __uint_as_float(o2[k]));
-                    }
                 }
                 if (j >= a.S) continue;
 #pragma unroll
@@ -280,46 +265,44 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                     tc_bulk(tc_smem(stats + st * 256 + 128), a.row_dl + r, 512, bar);
                 }
             }
-        } else if ((role == 1 || (Cfg::kStreams && role == 3)) && nt > 0) {
-            // ---- products (of stream h) ----
-            const int h = role >> 1;
+        } else if (role == 1 && nt > 0) {
+            // ---- products ----
             const uint32_t on = tc_elect();
             const int steps = (a.D + 15) / 16;
-            constexpr int NQ = 128 / Cfg::kParts;  // queries a product
-            const uint32_t dv_at = tmem + Cfg::kDV + h * 64, dk_at = tmem + Cfg::kDK + h * 64;
-            const uint32_t id_s = tc_idesc(BF16, false, false, 128, NQ), id_g = tc_idesc(BF16, false, true, 128, steps * 16);
+            const uint32_t dv_at = tmem + Cfg::kDV, dk_at = tmem + Cfg::kDK;
+            const uint32_t id_s = tc_idesc(BF16, false, false, 128, 128), id_g = tc_idesc(BF16, false, true, 128, steps * 16);
             const uint64_t k_desc = tc_desc(tc_smem(k_tile), 16, 1024), v_desc = tc_desc(tc_smem(v_tile), 16, 1024);
             const uint32_t base = tc_smem(ring);
             auto at = [&](int x) { return base + (x % R) * Cfg::kTileBytes; };  // Q(i) is tile 2i, dO(i) 2i + 1
             auto filled = [&](int x) { return tc_bar_wait(tc_smem(&full[x % R]), (x / R) & 1, abort, a.err); };
-            // 128 keys x the stream's queries: into d, with y the tile of queries (or of their gradients)
+            // 128 keys x 128 queries: into d, with y the tile of queries (or of their gradients)
             auto scores = [&](uint32_t d, uint64_t x_desc, uint32_t y, uint32_t bar) {
-                const uint64_t y_desc = tc_desc(y + h * NQ * 128, 16, 1024);
+                const uint64_t y_desc = tc_desc(y, 16, 1024);
 #pragma unroll
                 for (int k = 0; k < NC * 4; ++k) {
                     const uint64_t off = ((k >> 2) * kTcTile + (k & 3) * 32) >> 4;
-                    if (k < steps) tc_mma_ss(on, d + h * NQ, x_desc + off, y_desc + off, id_s, k > 0);
+                    if (k < steps) tc_mma_ss(on, d, x_desc + off, y_desc + off, id_s, k > 0);
                 }
                 tc_commit(on, bar);
             };
-            // sums over the stream's queries
+            // sums over the tile's queries
             auto gradient = [&](uint32_t d, uint32_t x, uint32_t y, bool acc) {
-                const uint64_t y_desc = tc_desc(y + h * (NQ / 16) * 2048, kTcTile, 1024);
+                const uint64_t y_desc = tc_desc(y, kTcTile, 1024);
 #pragma unroll
-                for (int k = 0; k < NQ / 16; ++k)  // 16 queries; the warpgroups' parts of 32 lie 32 columns apart
-                    tc_mma_ts(on, d, x + h * 64 + (k >> 1) * 32 + (k & 1) * 8, y_desc + ((k * 2048) >> 4), id_g, acc || k > 0);
+                for (int k = 0; k < 8; ++k)  // 16 queries; the warpgroups' parts of 32 lie 32 columns apart
+                    tc_mma_ts(on, d, x + (k >> 1) * 32 + (k & 1) * 8, y_desc + ((k * 2048) >> 4), id_g, acc || k > 0);
             };
             ok = tc_bar_wait(tc_smem(&sy.own), 0, abort, a.err);
-            if (ok && fix) ok = tc_bar_wait(tc_smem(&sy.s_free[0]), 0, abort, a.err);  // K and V cleared
+            if (ok && fix) ok = tc_bar_wait(tc_smem(&sy.s_free), 0, abort, a.err);  // K and V cleared
             ok = ok && filled(0) && filled(1);
             if (ok) {
                 tc_fence_after();
-                scores(tmem, k_desc, at(0), tc_smem(&sy.s_full[h]));
-                scores(tmem + 128, v_desc, at(1), tc_smem(&sy.dp_full[h]));
+                scores(tmem, k_desc, at(0), tc_smem(&sy.s_full));
+                scores(tmem + 128, v_desc, at(1), tc_smem(&sy.dp_full));
             }
             for (int i = 0; i < nt && ok; ++i) {
                 const bool more = i + 1 < nt;
-                ok = tc_bar_wait(tc_smem(&sy.p_ready[h]), i & 1, abort, a.err);
+                ok = tc_bar_wait(tc_smem(&sy.p_ready), i & 1, abort, a.err);
                 if (!ok) break;
                 tc_fence_after();
                 gradient(dv_at, tmem, at(2 * i + 1), i > 0);
@@ -328,9 +311,9 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                     ok = filled(2 * i + 2);
                     if (!ok) break;
                     tc_fence_after();
-                    scores(tmem, k_desc, at(2 * i + 2), tc_smem(&sy.s_full[h]));
+                    scores(tmem, k_desc, at(2 * i + 2), tc_smem(&sy.s_full));
                 }
-                ok = tc_bar_wait(tc_smem(&sy.ds_ready[h][0]), i & 1, abort, a.err);
+                ok = tc_bar_wait(tc_smem(&sy.ds_ready[0]), i & 1, abort, a.err);
                 if (!ok) break;
                 tc_fence_after();
                 gradient(dk_at, tmem + 128, at(2 * i), i > 0);
@@ -339,7 +322,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                     ok = filled(2 * i + 3);
                     if (!ok) break;
                     tc_fence_after();
-                    scores(tmem + 128, v_desc, at(2 * i + 3), tc_smem(&sy.dp_full[h]));
+                    scores(tmem + 128, v_desc, at(2 * i + 3), tc_smem(&sy.dp_full));
                 } else {
                     tc_commit(on, tc_smem(&sy.acc));
                 }
@@ -356,7 +339,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                     tc_fence_async();
                 }
                 __syncwarp();
-                if (lane == 0) tc_bar_arrive(tc_smem(&sy.s_free[0]));
+                if (lane == 0) tc_bar_arrive(tc_smem(&sy.s_free));
             }
             uint32_t w[4];
             for (int x = 0; x < 2 * nt && ok; ++x) {
@@ -394,12 +377,7 @@ struct TcQueryCfg {
     static constexpr int kRing = NC == 1 ? 8 : 5;
     static constexpr uint32_t kTileBytes = NC * kTcTile;
     static constexpr size_t kSmem = (2 + kRing) * kTileBytes + 1024;
-    // Up to 64 channels the halves of a tile (64 keys) are streams with scores,
-    // barriers and sums of their own, so that the scores of one are made while
-    // the other's are read; beyond, both are one product (as for the keys).
-    static constexpr bool kStreams = NC == 1;
-    static constexpr int kParts = kStreams ? 2 : 1, kKeys = 128 / kParts;
-    // tensor memory: a part's S and dP (kKeys columns each), dS twice (dQ of a tile runs beside the next tile's dS), dQ
+    // tensor memory: S 0, dP 128, dS twice 64 (dQ of a tile runs beside the next tile's dS), dQ
     static constexpr uint32_t kDS = 256, kDQ = 384;
 };
 
@@ -434,19 +412,17 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         if (lane == 0) {
             for (int i = 0; i < R; ++i) {
                 tc_bar_init(tc_smem(&sy.full[i]), 1);
-                tc_bar_init(tc_smem(&sy.empty[i]), Cfg::kParts);
+                tc_bar_init(tc_smem(&sy.empty[i]), 1);
                 tc_bar_init(tc_smem(&sy.ready[i]), 1);
             }
             tc_bar_init(tc_smem(&sy.own), 1);
-            tc_bar_init(tc_smem(&sy.acc), Cfg::kParts);
+            tc_bar_init(tc_smem(&sy.acc), 1);
             tc_bar_init(tc_smem(&sy.delta), 16);
-            for (int h = 0; h < 2; ++h) {
-                tc_bar_init(tc_smem(&sy.s_full[h]), 1);
-                tc_bar_init(tc_smem(&sy.s_free[h]), 16 / Cfg::kParts);
-                for (int i = 0; i < 2; ++i) {
-                    tc_bar_init(tc_smem(&sy.ds_ready[h][i]), 16 / Cfg::kParts);
-                    tc_bar_init(tc_smem(&sy.ds_done[h][i]), 1);
-                }
+            tc_bar_init(tc_smem(&sy.s_full), 1);
+            tc_bar_init(tc_smem(&sy.s_free), 16);
+            for (int i = 0; i < 2; ++i) {
+                tc_bar_init(tc_smem(&sy.ds_ready[i]), 16);
+                tc_bar_init(tc_smem(&sy.ds_done[i]), 1);
             }
             sy.abort = 0;
             asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -467,9 +443,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         const int w = warp >> 2, wl = warp & 3, row = wl * 32 + lane, q = q0 + row;
         const uint32_t first = lane == 0;
         const uint32_t lanes = (uint32_t)wl << 21;
-        const int part = Cfg::kStreams ? w >> 1 : 0, slot = Cfg::kStreams ? w & 1 : w;  // part, and which 32 of its keys
-        const uint32_t s_at = tmem + part * 128 + slot * 32 + lanes, dp_at = s_at + Cfg::kKeys;
-        const uint32_t ds_at = tmem + Cfg::kDS + part * 64 + slot * 16 + lanes;
+        const uint32_t s_at = tmem + w * 32 + lanes, dp_at = s_at + 128, ds_at = tmem + Cfg::kDS + w * 16 + lanes;
         const TcScale sc = tc_scale<BF16>(p);
         const long long r = (((long long)b * a.M + h) * p.qblocks + rt) * kTcRows + row;
         const float l2 = a.row_l2[r], dl = a.row_dl[r];
@@ -484,7 +458,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             const int j0 = (t0 + i) * kTcRows + w * 32;
             uint32_t bw = ~0u;
             if (bits) bw = bits[(t0 + i) * 4 + w];
-            ok = tc_bar_wait(tc_smem(&sy.s_full[part]), i & 1, abort, a.err);
+            ok = tc_bar_wait(tc_smem(&sy.s_full), i & 1, abort, a.err);
             if (!ok) break;
             tc_fence_after();
             uint32_t s[32], d[32];
@@ -492,7 +466,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             tmem_ld32(d, dp_at);
             tmem_wait_ld();
             tc_fence_before();
-            tc_bar_arrive_if(first, tc_smem(&sy.s_free[part]));
+            tc_bar_arrive_if(first, tc_smem(&sy.s_free));
             if (__builtin_expect(km || a.bits || seen_least - j0 < 32, 0)) {
                 bw &= tc_low_bits(seen - j0);
                 if (km) bw &= sy.words[i & 7][w];
@@ -527,7 +501,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                 if (w == 0) p.delta_out[r] = delta;
             }
             if (i > 1) {  // dS(i-2) is used up
-                ok = tc_bar_wait(tc_smem(&sy.ds_done[part][i & 1]), (i / 2 - 1) & 1, abort, a.err);
+                ok = tc_bar_wait(tc_smem(&sy.ds_done[i & 1]), (i / 2 - 1) & 1, abort, a.err);
                 if (!ok) break;
                 tc_fence_after();
             }
@@ -543,13 +517,13 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                     tc_split(y, x0, x1);
                     pk[k / 2] = tc_pack<BF16>(x0, x1);
                 }
-                tmem_st16(ds_at + (i & 1) * (Cfg::kKeys / 2), pk);
+                tmem_st16(ds_at + (i & 1) * 64, pk);
             }
             tmem_wait_st();
             tc_fence_before();
             // one barrier a buffer: a warp may be a tile ahead of another (it waits for dS(i-2) only), and its
             // arrival must not count for that other's
-            tc_bar_arrive_if(first, tc_smem(&sy.ds_ready[part][i & 1]));
+            tc_bar_arrive_if(first, tc_smem(&sy.ds_ready[i & 1]));
         }
         if (nt > 0 && ok) {
             ok = tc_bar_wait(tc_smem(&sy.acc), 0, abort, a.err);
@@ -561,14 +535,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             for (int c = w; c < (a.D + 15) / 16; c += 4) {
                 uint32_t o[16];
                 if (nt > 0) {
-                    uint32_t o2[16];
                     tmem_ld16(o, tmem + Cfg::kDQ + lanes + c * 16);
-                    if (Cfg::kStreams) tmem_ld16(o2, tmem + Cfg::kDQ + 64 + lanes + c * 16);
                     tmem_wait_ld();
-                    if (Cfg::kStreams) {
-#pragma unroll
-                        for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) + __uint_as_float(o2[k]));
-                    }
                 }
                 if (q >= a.Q) continue;
 #pragma unroll
@@ -602,32 +570,29 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                     tc_tma_5d(tc_smem(ring) + st * Cfg::kTileBytes + c * kTcTile, (x & 1) ? &map_k : &map_v, bar, c * 64, 0,
                               (t0 + (x >> 1)) * kTcRows, n, b);
             }
-        } else if ((role == 1 || (Cfg::kStreams && role == 3)) && nt > 0) {
-            // ---- products (of part `part`) ----
-            const int part = role >> 1;
-            constexpr int NK = Cfg::kKeys;
+        } else if (role == 1 && nt > 0) {
+            // ---- products ----
             const uint32_t on = tc_elect();
             const int steps = (a.D + 15) / 16;
-            const uint32_t id_s = tc_idesc(BF16, false, false, 128, NK), id_g = tc_idesc(BF16, false, true, 128, steps * 16);
+            const uint32_t id_s = tc_idesc(BF16, false, false, 128, 128), id_g = tc_idesc(BF16, false, true, 128, steps * 16);
             const uint64_t q_desc = tc_desc(tc_smem(q_tile), 16, 1024), do_desc = tc_desc(tc_smem(do_tile), 16, 1024);
-            const uint32_t base = tc_smem(ring), s_at = tmem + part * 128, ds_at = tmem + Cfg::kDS + part * 64;
+            const uint32_t base = tc_smem(ring);
             auto at = [&](int x) { return base + (x % R) * Cfg::kTileBytes; };  // V(i) is tile 2i, K(i) 2i + 1
             auto filled = [&](int x) { return tc_bar_wait(tc_smem(&full[x % R]), (x / R) & 1, abort, a.err); };
             auto scores = [&](int i) {  // dP = dO V^T, S = Q K^T
-                const uint64_t v_desc = tc_desc(at(2 * i) + part * NK * 128, 16, 1024);
-                const uint64_t k_desc = tc_desc(at(2 * i + 1) + part * NK * 128, 16, 1024);
+                const uint64_t v_desc = tc_desc(at(2 * i), 16, 1024), k_desc = tc_desc(at(2 * i + 1), 16, 1024);
 #pragma unroll
                 for (int k = 0; k < NC * 4; ++k) {
                     const uint64_t off = ((k >> 2) * kTcTile + (k & 3) * 32) >> 4;
-                    if (k < steps) tc_mma_ss(on, s_at + NK, do_desc + off, v_desc + off, id_s, k > 0);
+                    if (k < steps) tc_mma_ss(on, tmem + 128, do_desc + off, v_desc + off, id_s, k > 0);
                 }
                 tc_commit(on, tc_smem(&sy.empty[2 * i % R]));
 #pragma unroll
                 for (int k = 0; k < NC * 4; ++k) {
                     const uint64_t off = ((k >> 2) * kTcTile + (k & 3) * 32) >> 4;
-                    if (k < steps) tc_mma_ss(on, s_at, q_desc + off, k_desc + off, id_s, k > 0);
+                    if (k < steps) tc_mma_ss(on, tmem, q_desc + off, k_desc + off, id_s, k > 0);
                 }
-                tc_commit(on, tc_smem(&sy.s_full[part]));
+                tc_commit(on, tc_smem(&sy.s_full));
             };
             ok = tc_bar_wait(tc_smem(&sy.own), 0, abort, a.err) && filled(0) && filled(1);
             if (ok) {
@@ -636,20 +601,20 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             }
             for (int i = 0; i < nt && ok; ++i) {
                 if (i + 1 < nt) {
-                    ok = filled(2 * i + 2) && filled(2 * i + 3) && tc_bar_wait(tc_smem(&sy.s_free[part]), i & 1, abort, a.err);
+                    ok = filled(2 * i + 2) && filled(2 * i + 3) && tc_bar_wait(tc_smem(&sy.s_free), i & 1, abort, a.err);
                     if (!ok) break;
                     tc_fence_after();
                     scores(i + 1);
                 }
-                ok = tc_bar_wait(tc_smem(&sy.ds_ready[part][i & 1]), (i / 2) & 1, abort, a.err);
+                ok = tc_bar_wait(tc_smem(&sy.ds_ready[i & 1]), (i / 2) & 1, abort, a.err);
                 if (!ok) break;
                 tc_fence_after();
-                const uint64_t k_desc = tc_desc(at(2 * i + 1) + part * (NK / 16) * 2048, kTcTile, 1024);
+                const uint64_t k_desc = tc_desc(at(2 * i + 1), kTcTile, 1024);
 #pragma unroll
-                for (int k = 0; k < NK / 16; ++k)
-                    tc_mma_ts(on, tmem + Cfg::kDQ + part * 64, ds_at + (i & 1) * (NK / 2) + k * 8, k_desc + ((k * 2048) >> 4), id_g,
+                for (int k = 0; k < 8; ++k)
+                    tc_mma_ts(on, tmem + Cfg::kDQ, tmem + Cfg::kDS + (i & 1) * 64 + k * 8, k_desc + ((k * 2048) >> 4), id_g,
                               i > 0 || k > 0);
-                tc_commit(on, tc_smem(&sy.ds_done[part][i & 1]));
+                tc_commit(on, tc_smem(&sy.ds_done[i & 1]));
                 tc_commit(on, tc_smem(&sy.empty[(2 * i + 1) % R]));
             }
             if (ok) tc_commit(on, tc_smem(&sy.acc));
