@@ -50,7 +50,7 @@ __device__ __forceinline__ TcScale tc_scale(const TcArgs& p) {
 
 struct TcBackwardSync {
     uint64_t own, full[8], empty[8], ready[8];
-    uint64_t s_full, dp_full, p_ready, ds_ready[2], s_free, ds_done[2], acc, delta;
+    uint64_t s_full[2], dp_full, dp_free, p_ready[2], ds_ready[2], cleared, acc, delta;
     uint32_t tmem, abort;
     uint32_t words[8][4];
 };
@@ -64,7 +64,13 @@ struct TcKeyCfg {
     static constexpr uint32_t kTileBytes = NC * kTcTile;
     static constexpr uint32_t kStatBytes = 1024;  // l2 and delta of 128 rows, beside a tile of Q
     static constexpr size_t kSmem = 2 * kTileBytes + kRing * (kTileBytes + kStatBytes) + 1024;
-    static constexpr uint32_t kDV = 256, kDK = 384;  // tensor memory: S 0, dP 128
+    // Tensor memory.  Up to 64 channels there is room for S twice: dS then lies beside P over
+    // its S, so dP's columns are free once read, and S is made two tiles ahead and dP one: the
+    // score warps wait for no product.  (With one S the kernel stood 2300 cycles a tile
+    // whatever was taken out of it: a round through barrier, product and
+    // barrier costs about 1000 of them.)  Beyond, P lies over S and dS over dP.
+    static constexpr bool kAhead = NC == 1;
+    static constexpr uint32_t kDP = kAhead ? 256 : 128, kDV = kAhead ? 384 : 256, kDK = kAhead ? 448 : 384;
 };
 
 template <bool BF16, int NC>
@@ -109,12 +115,15 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                 tc_bar_init(tc_smem(&sy.ready[i]), 1);
             }
             tc_bar_init(tc_smem(&sy.own), 1);
-            tc_bar_init(tc_smem(&sy.s_full), 1);
             tc_bar_init(tc_smem(&sy.dp_full), 1);
-            tc_bar_init(tc_smem(&sy.p_ready), 16);
-            tc_bar_init(tc_smem(&sy.ds_ready[0]), 16);
+            tc_bar_init(tc_smem(&sy.dp_free), 16);
+            for (int i = 0; i < 2; ++i) {
+                tc_bar_init(tc_smem(&sy.s_full[i]), 1);
+                tc_bar_init(tc_smem(&sy.p_ready[i]), 16);
+                tc_bar_init(tc_smem(&sy.ds_ready[i]), 16);
+            }
             tc_bar_init(tc_smem(&sy.acc), 1);
-            tc_bar_init(tc_smem(&sy.s_free), 1);  // here: K and V are cleared
+            tc_bar_init(tc_smem(&sy.cleared), 1);
             sy.abort = 0;
             asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         }
@@ -135,7 +144,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         const int w = warp >> 2, wl = warp & 3, row = wl * 32 + lane, j = j0 + row;
         const uint32_t first = lane == 0;
         const uint32_t lanes = (uint32_t)wl << 21;
-        const uint32_t s_at = tmem + w * 32 + lanes, dp_at = tmem + 128 + w * 32 + lanes;
+        const uint32_t dp_at = tmem + Cfg::kDP + w * 32 + lanes;
         const uint64_t c2 = tc_two(a.c2, a.c2);
         const float dscale = tc_scale<BF16>(p).ds;
         const bool has_bits = p.bits_t != nullptr;
@@ -144,13 +153,15 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         for (int i = 0; i < nt; ++i) {
             const int g = i / per_head, rt = r0 + i - g * per_head, st = 2 * i % R;
             const int q0 = rt * kTcRows + w * 32;
+            const int buf = Cfg::kAhead ? i & 1 : 0, phase = (Cfg::kAhead ? i >> 1 : i) & 1;
+            const uint32_t s_at = tmem + buf * 128 + w * 32 + lanes;
             uint32_t bw = ~0u;
             if (has_bits && j < a.S)
                 bw = p.bits_t[b * p.bits_t_sb + (n * a.G + g) * p.bits_t_sh + (long long)j * p.Wq + rt * 4 + w];
             const float* l2 = stats + st * 256 + w * 32;
             const float* dl = l2 + 128;
             ok = tc_bar_wait(tc_smem(&sy.full[st]), (2 * i / R) & 1, abort, a.err) &&
-                 tc_bar_wait(tc_smem(&sy.s_full), i & 1, abort, a.err);
+                 tc_bar_wait(tc_smem(&sy.s_full[buf]), phase, abort, a.err);
             if (!ok) break;
             tc_fence_after();
             uint32_t s[32];
@@ -182,15 +193,19 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             }
             tmem_wait_st();
             tc_fence_before();
-            tc_bar_arrive_if(first, tc_smem(&sy.p_ready));
+            tc_bar_arrive_if(first, tc_smem(&sy.p_ready[buf]));
             ok = tc_bar_wait(tc_smem(&sy.dp_full), i & 1, abort, a.err);
             if (!ok) break;
             tc_fence_after();
-            // dS^T over dP^T
+            // dS^T beside P^T, or over dP^T
             {
                 uint32_t d[32], pk[16];
                 tmem_ld32(d, dp_at);
                 tmem_wait_ld();
+                if constexpr (Cfg::kAhead) {
+                    tc_fence_before();
+                    tc_bar_arrive_if(first, tc_smem(&sy.dp_free));
+                }
 #pragma unroll
                 for (int k = 0; k < 32; k += 4) {
                     const float4 l = *reinterpret_cast<const float4*>(dl + k);
@@ -205,11 +220,12 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                     pk[k / 2] = tc_pack<BF16>(x0, x1);
                     pk[k / 2 + 1] = tc_pack<BF16>(x2, x3);
                 }
-                tmem_st16(dp_at, pk);
+                tmem_st16(Cfg::kAhead ? s_at + 16 : dp_at, pk);
             }
             tmem_wait_st();
             tc_fence_before();
-            tc_bar_arrive_if(first, tc_smem(&sy.ds_ready[0]));
+            // (two tiles ahead: a barrier a buffer, as a warp may be a tile ahead of another)
+            tc_bar_arrive_if(first, tc_smem(&sy.ds_ready[buf]));
         }
         // ---- dV (the first two warpgroups) and dK, alternate chunks of 16 channels ----
         if (nt > 0 && ok) {
@@ -292,41 +308,58 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                 for (int k = 0; k < 8; ++k)  // 16 queries; the warpgroups' parts of 32 lie 32 columns apart
                     tc_mma_ts(on, d, x + (k >> 1) * 32 + (k & 1) * 8, y_desc + ((k * 2048) >> 4), id_g, acc || k > 0);
             };
+            const uint32_t dp = tmem + Cfg::kDP;
             ok = tc_bar_wait(tc_smem(&sy.own), 0, abort, a.err);
-            if (ok && fix) ok = tc_bar_wait(tc_smem(&sy.s_free), 0, abort, a.err);  // K and V cleared
-            ok = ok && filled(0) && filled(1);
+            if (ok && fix) ok = tc_bar_wait(tc_smem(&sy.cleared), 0, abort, a.err);
+            ok = ok && filled(0) && filled(1) && (!Cfg::kAhead || nt < 2 || filled(2));
             if (ok) {
                 tc_fence_after();
-                scores(tmem, k_desc, at(0), tc_smem(&sy.s_full));
-                scores(tmem + 128, v_desc, at(1), tc_smem(&sy.dp_full));
+                scores(tmem, k_desc, at(0), tc_smem(&sy.s_full[0]));
+                scores(dp, v_desc, at(1), tc_smem(&sy.dp_full));
+                if (Cfg::kAhead && nt > 1) scores(tmem + 128, k_desc, at(2), tc_smem(&sy.s_full[1]));
             }
             for (int i = 0; i < nt && ok; ++i) {
                 const bool more = i + 1 < nt;
-                ok = tc_bar_wait(tc_smem(&sy.p_ready), i & 1, abort, a.err);
+                const int buf = Cfg::kAhead ? i & 1 : 0, phase = (Cfg::kAhead ? i >> 1 : i) & 1;
+                const uint32_t s_at = tmem + buf * 128;
+                ok = tc_bar_wait(tc_smem(&sy.p_ready[buf]), phase, abort, a.err);
                 if (!ok) break;
                 tc_fence_after();
-                gradient(dv_at, tmem, at(2 * i + 1), i > 0);
+                gradient(dv_at, s_at, at(2 * i + 1), i > 0);
                 tc_commit(on, tc_smem(&sy.empty[(2 * i + 1) % R]));
-                if (more) {
+                if constexpr (Cfg::kAhead) {
+                    if (more) {
+                        ok = filled(2 * i + 3) && tc_bar_wait(tc_smem(&sy.dp_free), i & 1, abort, a.err);
+                        if (!ok) break;
+                        tc_fence_after();
+                        scores(dp, v_desc, at(2 * i + 3), tc_smem(&sy.dp_full));
+                    }
+                } else if (more) {
                     ok = filled(2 * i + 2);
                     if (!ok) break;
                     tc_fence_after();
-                    scores(tmem, k_desc, at(2 * i + 2), tc_smem(&sy.s_full));
+                    scores(tmem, k_desc, at(2 * i + 2), tc_smem(&sy.s_full[0]));
                 }
-                ok = tc_bar_wait(tc_smem(&sy.ds_ready[0]), i & 1, abort, a.err);
+                ok = tc_bar_wait(tc_smem(&sy.ds_ready[buf]), phase, abort, a.err);
                 if (!ok) break;
                 tc_fence_after();
-                gradient(dk_at, tmem + 128, at(2 * i), i > 0);
+                gradient(dk_at, Cfg::kAhead ? s_at + 16 : dp, at(2 * i), i > 0);
                 tc_commit(on, tc_smem(&sy.empty[2 * i % R]));
-                if (more) {
+                if constexpr (Cfg::kAhead) {
+                    if (i + 2 < nt) {
+                        ok = filled(2 * i + 4);
+                        if (!ok) break;
+                        tc_fence_after();
+                        scores(s_at, k_desc, at(2 * i + 4), tc_smem(&sy.s_full[buf]));
+                    }
+                } else if (more) {
                     ok = filled(2 * i + 3);
                     if (!ok) break;
                     tc_fence_after();
-                    scores(tmem + 128, v_desc, at(2 * i + 3), tc_smem(&sy.dp_full));
-                } else {
-                    tc_commit(on, tc_smem(&sy.acc));
+                    scores(dp, v_desc, at(2 * i + 3), tc_smem(&sy.dp_full));
                 }
             }
+            if (ok) tc_commit(on, tc_smem(&sy.acc));
         } else if (role == 2 && fix && nt > 0) {
             // ---- keys, and rows without keys, that take no part ----
             ok = tc_bar_wait(tc_smem(&sy.own), 0, abort, a.err);
@@ -339,7 +372,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                     tc_fence_async();
                 }
                 __syncwarp();
-                if (lane == 0) tc_bar_arrive(tc_smem(&sy.s_free));
+                if (lane == 0) tc_bar_arrive(tc_smem(&sy.cleared));
             }
             uint32_t w[4];
             for (int x = 0; x < 2 * nt && ok; ++x) {
@@ -371,14 +404,14 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
 
 template <int NC>
 struct TcQueryCfg {
-    // a ring of tiles: V(0), K(0), V(1), ...; V is let go behind its scores, K behind dQ.
+    // a ring of tiles: K(0), V(0), K(1), ...; V is let go behind its scores, K behind dQ.
     // (Pairs of K and V in two stages left the products waiting 1600 of 3200
     // cycles a tile for them at 128 channels.)
     static constexpr int kRing = NC == 1 ? 8 : 5;
     static constexpr uint32_t kTileBytes = NC * kTcTile;
     static constexpr size_t kSmem = (2 + kRing) * kTileBytes + 1024;
-    // tensor memory: S 0, dP 128, dS twice 64 (dQ of a tile runs beside the next tile's dS), dQ
-    static constexpr uint32_t kDS = 256, kDQ = 384;
+    // tensor memory: S twice, dP, dQ; dS lies over its S (as in the key kernel: S two tiles ahead, dP one)
+    static constexpr uint32_t kDP = 256, kDQ = 384;
 };
 
 template <bool BF16, int NC>
@@ -418,11 +451,11 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             tc_bar_init(tc_smem(&sy.own), 1);
             tc_bar_init(tc_smem(&sy.acc), 1);
             tc_bar_init(tc_smem(&sy.delta), 16);
-            tc_bar_init(tc_smem(&sy.s_full), 1);
-            tc_bar_init(tc_smem(&sy.s_free), 16);
+            tc_bar_init(tc_smem(&sy.dp_full), 1);
+            tc_bar_init(tc_smem(&sy.dp_free), 16);
             for (int i = 0; i < 2; ++i) {
+                tc_bar_init(tc_smem(&sy.s_full[i]), 1);
                 tc_bar_init(tc_smem(&sy.ds_ready[i]), 16);
-                tc_bar_init(tc_smem(&sy.ds_done[i]), 1);
             }
             sy.abort = 0;
             asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -443,7 +476,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         const int w = warp >> 2, wl = warp & 3, row = wl * 32 + lane, q = q0 + row;
         const uint32_t first = lane == 0;
         const uint32_t lanes = (uint32_t)wl << 21;
-        const uint32_t s_at = tmem + w * 32 + lanes, dp_at = s_at + 128, ds_at = tmem + Cfg::kDS + w * 16 + lanes;
+        const uint32_t dp_at = tmem + Cfg::kDP + w * 32 + lanes;
         const TcScale sc = tc_scale<BF16>(p);
         const long long r = (((long long)b * a.M + h) * p.qblocks + rt) * kTcRows + row;
         const float l2 = a.row_l2[r], dl = a.row_dl[r];
@@ -458,15 +491,14 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             const int j0 = (t0 + i) * kTcRows + w * 32;
             uint32_t bw = ~0u;
             if (bits) bw = bits[(t0 + i) * 4 + w];
-            ok = tc_bar_wait(tc_smem(&sy.s_full), i & 1, abort, a.err);
+            const int buf = i & 1;
+            const uint32_t s_at = tmem + buf * 128 + w * 32 + lanes;
+            ok = tc_bar_wait(tc_smem(&sy.s_full[buf]), (i >> 1) & 1, abort, a.err);
             if (!ok) break;
             tc_fence_after();
             uint32_t s[32], d[32];
             tmem_ld32(s, s_at);
-            tmem_ld32(d, dp_at);
             tmem_wait_ld();
-            tc_fence_before();
-            tc_bar_arrive_if(first, tc_smem(&sy.s_free));
             if (__builtin_expect(km || a.bits || seen_least - j0 < 32, 0)) {
                 bw &= tc_low_bits(seen - j0);
                 if (km) bw &= sy.words[i & 7][w];
@@ -476,6 +508,21 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                         if (!((bw >> k) & 1u)) s[k] = 0xff800000u;
                 }
             }
+            // probabilities
+#pragma unroll
+            for (int k = 0; k < 32; k += 2) {
+                float x0, x1;
+                tc_split(tc_fma2(tc_two(__uint_as_float(s[k]), __uint_as_float(s[k + 1])), c2, nl), x0, x1);
+                s[k] = __float_as_uint(tc_ex2(x0));
+                s[k + 1] = __float_as_uint(tc_ex2(x1));
+            }
+            ok = tc_bar_wait(tc_smem(&sy.dp_full), i & 1, abort, a.err);
+            if (!ok) break;
+            tc_fence_after();
+            tmem_ld32(d, dp_at);
+            tmem_wait_ld();
+            tc_fence_before();
+            tc_bar_arrive_if(first, tc_smem(&sy.dp_free));
             if (p.delta_out) {
                 // One tile of keys: delta = sum_j p dP from the values at hand, not <dout, out>.  With few keys out is
                 // as large as a value and its rounding to 16 bits, carried into dP - delta, was the largest error
@@ -484,8 +531,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                 float sum = 0.f, ps = 0.f;
 #pragma unroll
                 for (int k = 0; k < 32; ++k) {  // a pair that takes no part adds nothing, whatever its dP
-                    const float e = tc_ex2(fmaf(__uint_as_float(s[k]), a.c2, l2));
-                    if (s[k] != 0xff800000u) sum = fmaf(e, __uint_as_float(d[k]), sum), ps += e;
+                    const float e = __uint_as_float(s[k]);
+                    if (e != 0.f) sum = fmaf(e, __uint_as_float(d[k]), sum), ps += e;
                 }
                 part_sum[w * 128 + row] = make_float2(sum, ps);
                 __syncwarp();
@@ -500,30 +547,22 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                 nd = tc_two(delta * sc.ds, delta * sc.ds);
                 if (w == 0) p.delta_out[r] = delta;
             }
-            if (i > 1) {  // dS(i-2) is used up
-                ok = tc_bar_wait(tc_smem(&sy.ds_done[i & 1]), (i / 2 - 1) & 1, abort, a.err);
-                if (!ok) break;
-                tc_fence_after();
-            }
             {
                 uint32_t pk[16];
 #pragma unroll
                 for (int k = 0; k < 32; k += 2) {
                     float x0, x1;
-                    tc_split(tc_fma2(tc_two(__uint_as_float(s[k]), __uint_as_float(s[k + 1])), c2, nl), x0, x1);
-                    const uint64_t e = tc_two(tc_ex2(x0), tc_ex2(x1));
+                    const uint64_t e = tc_two(__uint_as_float(s[k]), __uint_as_float(s[k + 1]));
                     const uint64_t dp = tc_two(__uint_as_float(d[k]), __uint_as_float(d[k + 1]));
-                    const uint64_t y = tc_mul2(BF16 ? tc_add2(dp, nd) : tc_fma2(dp, ds2, nd), e);
-                    tc_split(y, x0, x1);
+                    tc_split(tc_mul2(BF16 ? tc_add2(dp, nd) : tc_fma2(dp, ds2, nd), e), x0, x1);
                     pk[k / 2] = tc_pack<BF16>(x0, x1);
                 }
-                tmem_st16(ds_at + (i & 1) * 64, pk);
+                tmem_st16(s_at, pk);
             }
             tmem_wait_st();
             tc_fence_before();
-            // one barrier a buffer: a warp may be a tile ahead of another (it waits for dS(i-2) only), and its
-            // arrival must not count for that other's
-            tc_bar_arrive_if(first, tc_smem(&sy.ds_ready[i & 1]));
+            // one barrier a buffer: a warp may be a tile ahead of another, and its arrival must not count for that other's
+            tc_bar_arrive_if(first, tc_smem(&sy.ds_ready[buf]));
         }
         if (nt > 0 && ok) {
             ok = tc_bar_wait(tc_smem(&sy.acc), 0, abort, a.err);
@@ -567,7 +606,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                 const uint32_t bar = tc_smem(&sy.full[st]);
                 tc_bar_expect(bar, Cfg::kTileBytes);
                 for (int c = 0; c < NC; ++c)
-                    tc_tma_5d(tc_smem(ring) + st * Cfg::kTileBytes + c * kTcTile, (x & 1) ? &map_k : &map_v, bar, c * 64, 0,
+                    tc_tma_5d(tc_smem(ring) + st * Cfg::kTileBytes + c * kTcTile, (x & 1) ? &map_v : &map_k, bar, c * 64, 0,
                               (t0 + (x >> 1)) * kTcRows, n, b);
             }
         } else if (role == 1 && nt > 0) {
@@ -577,45 +616,51 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             const uint32_t id_s = tc_idesc(BF16, false, false, 128, 128), id_g = tc_idesc(BF16, false, true, 128, steps * 16);
             const uint64_t q_desc = tc_desc(tc_smem(q_tile), 16, 1024), do_desc = tc_desc(tc_smem(do_tile), 16, 1024);
             const uint32_t base = tc_smem(ring);
-            auto at = [&](int x) { return base + (x % R) * Cfg::kTileBytes; };  // V(i) is tile 2i, K(i) 2i + 1
+            auto at = [&](int x) { return base + (x % R) * Cfg::kTileBytes; };  // K(i) is tile 2i, V(i) 2i + 1
             auto filled = [&](int x) { return tc_bar_wait(tc_smem(&full[x % R]), (x / R) & 1, abort, a.err); };
-            auto scores = [&](int i) {  // dP = dO V^T, S = Q K^T
-                const uint64_t v_desc = tc_desc(at(2 * i), 16, 1024), k_desc = tc_desc(at(2 * i + 1), 16, 1024);
+            auto scores = [&](uint32_t d, uint64_t x_desc, uint32_t y, uint32_t bar) {
+                const uint64_t y_desc = tc_desc(y, 16, 1024);
 #pragma unroll
                 for (int k = 0; k < NC * 4; ++k) {
                     const uint64_t off = ((k >> 2) * kTcTile + (k & 3) * 32) >> 4;
-                    if (k < steps) tc_mma_ss(on, tmem + 128, do_desc + off, v_desc + off, id_s, k > 0);
+                    if (k < steps) tc_mma_ss(on, d, x_desc + off, y_desc + off, id_s, k > 0);
                 }
-                tc_commit(on, tc_smem(&sy.empty[2 * i % R]));
-#pragma unroll
-                for (int k = 0; k < NC * 4; ++k) {
-                    const uint64_t off = ((k >> 2) * kTcTile + (k & 3) * 32) >> 4;
-                    if (k < steps) tc_mma_ss(on, tmem, q_desc + off, k_desc + off, id_s, k > 0);
-                }
-                tc_commit(on, tc_smem(&sy.s_full));
+                tc_commit(on, bar);
             };
-            ok = tc_bar_wait(tc_smem(&sy.own), 0, abort, a.err) && filled(0) && filled(1);
+            auto product_dp = [&](int i) {
+                scores(tmem + Cfg::kDP, do_desc, at(2 * i + 1), tc_smem(&sy.dp_full));
+                tc_commit(on, tc_smem(&sy.empty[(2 * i + 1) % R]));
+            };
+            ok = tc_bar_wait(tc_smem(&sy.own), 0, abort, a.err) && filled(0) && filled(1) && (nt < 2 || filled(2));
             if (ok) {
                 tc_fence_after();
-                scores(0);
+                scores(tmem, q_desc, at(0), tc_smem(&sy.s_full[0]));
+                product_dp(0);
+                if (nt > 1) scores(tmem + 128, q_desc, at(2), tc_smem(&sy.s_full[1]));
             }
             for (int i = 0; i < nt && ok; ++i) {
+                const int buf = i & 1;
                 if (i + 1 < nt) {
-                    ok = filled(2 * i + 2) && filled(2 * i + 3) && tc_bar_wait(tc_smem(&sy.s_free), i & 1, abort, a.err);
+                    ok = filled(2 * i + 3) && tc_bar_wait(tc_smem(&sy.dp_free), i & 1, abort, a.err);
                     if (!ok) break;
                     tc_fence_after();
-                    scores(i + 1);
+                    product_dp(i + 1);
                 }
-                ok = tc_bar_wait(tc_smem(&sy.ds_ready[i & 1]), (i / 2) & 1, abort, a.err);
+                ok = tc_bar_wait(tc_smem(&sy.ds_ready[buf]), (i >> 1) & 1, abort, a.err);
                 if (!ok) break;
                 tc_fence_after();
-                const uint64_t k_desc = tc_desc(at(2 * i + 1), kTcTile, 1024);
+                const uint64_t k_desc = tc_desc(at(2 * i), kTcTile, 1024);
 #pragma unroll
-                for (int k = 0; k < 8; ++k)
-                    tc_mma_ts(on, tmem + Cfg::kDQ, tmem + Cfg::kDS + (i & 1) * 64 + k * 8, k_desc + ((k * 2048) >> 4), id_g,
-                              i > 0 || k > 0);
-                tc_commit(on, tc_smem(&sy.ds_done[i & 1]));
-                tc_commit(on, tc_smem(&sy.empty[(2 * i + 1) % R]));
+                for (int k = 0; k < 8; ++k)  // 16 keys; the warpgroups' parts of 32 lie 32 columns apart
+                    tc_mma_ts(on, tmem + Cfg::kDQ, tmem + buf * 128 + (k >> 1) * 32 + (k & 1) * 8, k_desc + ((k * 2048) >> 4),
+                              id_g, i > 0 || k > 0);
+                tc_commit(on, tc_smem(&sy.empty[2 * i % R]));
+                if (i + 2 < nt) {
+                    ok = filled(2 * i + 4);
+                    if (!ok) break;
+                    tc_fence_after();
+                    scores(tmem + buf * 128, q_desc, at(2 * i + 4), tc_smem(&sy.s_full[buf]));
+                }
             }
             if (ok) tc_commit(on, tc_smem(&sy.acc));
         } else if (role == 2 && km && nt > 0) {
