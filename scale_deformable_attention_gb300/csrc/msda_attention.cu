@@ -301,16 +301,15 @@ msda_status launched(cudaError_t e, const char* what) {
 // depends on the addresses, and 128 needs as much space or more.
 struct BackwardLayout {
     AttentionRows rows;
-    size_t l2 = 0, dl = 0, top = 0, mask = 0, bytes = 0;
+    size_t l2 = 0, top = 0, mask = 0, bytes = 0;
 };
 BackwardLayout backward_layout(msda_dtype dt, unsigned flags, const msda_attention_problem* p, bool tc) {
     BackwardLayout w;
     const int rt = tc ? msda::kTcRows : 64;
     w.rows = {rt, rt, (int)((p->Q + rt - 1) / rt), (int)p->M, 1};
-    const size_t n = up((size_t)p->B * w.rows.N * w.rows.tiles * w.rows.rt * 4);
-    w.dl = n;
-    w.top = 2 * n;
-    w.mask = 2 * n + 256;
+    const size_t n = up((size_t)p->B * w.rows.N * w.rows.tiles * w.rows.rt * 8);
+    w.top = n;
+    w.mask = n + 256;
     w.bytes = w.mask + mask_space(dt, flags, p).bytes;
     return w;
 }
@@ -436,7 +435,7 @@ msda_status msda_attention_backward(msda_dtype dt, unsigned flags, const msda_at
     AttentionArgs a = args_of(flags, p, scale, query, key, value, key_mask, mask);
     a.dout = grad_out, a.dq = grad_query, a.dk = grad_key, a.dv = grad_value;
     float* l2 = reinterpret_cast<float*>(ws + w.l2);
-    float* dl = reinterpret_cast<float*>(ws + w.dl);
+    float* dl = l2 + w.rows.rt;
     a.row_l2 = l2, a.row_dl = dl;
     msda::TcArgs t{};
     if ((s = make_mask(a, mask_space(dt, flags, p), ws + w.mask, tc ? &t : nullptr, st)) != MSDA_OK) return s;
@@ -447,7 +446,7 @@ msda_status msda_attention_backward(msda_dtype dt, unsigned flags, const msda_at
         t.scale_in = top;
         cudaError_t e = half ? cudaMemsetAsync(top, 0, 8, st) : cudaSuccess;
         if (e == cudaSuccess)
-            e = MSDA_BY_DTYPE(dt, launch_attention_prepare, a, w.rows, out, lse, half ? msda::kHalfScale : 0.f, l2, dl, top,
+            e = MSDA_BY_DTYPE(dt, launch_attention_prepare, a, w.rows, out, lse, half ? msda::kHalfScale : 0.f, l2, top,
                               tc && msda::aligned_to(out, 16), st);
         s = launched(e, "attention statistics kernel launch");
         ts.end(MSDA_KERNEL_ATTENTION_PREPARE, p->B * p->M * p->Q);

@@ -43,6 +43,7 @@ struct AttentionArgs {
 
 // Rows of the backward's per-row statistics: tiles of `rt` rows, the G query
 // heads of a key head beside one another (row = (q - tile's first) * G + g).
+// A tile's l2 and delta lie side by side: [tile][rt], [rt].
 struct AttentionRows {
     int rt, qpt, tiles;  // rows a tile, queries a tile, tiles
     int N, G;            // heads with rows of their own, heads sharing them

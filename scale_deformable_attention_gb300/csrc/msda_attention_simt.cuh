@@ -352,7 +352,7 @@ __global__ void __launch_bounds__(kSimtThreads, simt_blocks(DP)) msda_attention_
             while (x < total && !simt_tile_seen(a, b, n * a.G + x / per, (qt0 + x % per) * 64, j0)) ++x;
         return x;
     };
-    auto stat_at = [&](int x) { return ((long long)(b * rw.N + n * a.G + x / per) * rw.tiles + qt0 + x % per) * 64; };
+    auto stat_at = [&](int x) { return ((long long)(b * rw.N + n * a.G + x / per) * rw.tiles + qt0 + x % per) * 128; };
     // rows that take no part are cleared: their flags are written a tile ahead of the copies that ask for them
     auto flags = [&](int x) {
         if (threadIdx.x < 64) live[threadIdx.x] = a.row_l2[stat_at(x) + threadIdx.x] != -attn_inf();
@@ -447,7 +447,7 @@ __global__ void __launch_bounds__(kSimtThreads, simt_blocks(DP)) msda_attention_
     simt_load<T, DP>(Gs, static_cast<const T*>(a.dout) + (((long long)b * a.Q + q0) * a.M + m) * a.D,
                      (long long)a.M * a.D, a.Q - q0, a.D, vec, nullptr);
     float l2[8], dl[8], dq[8][DP / 16] = {};
-    const long long at0 = ((long long)(b * rw.N + m) * rw.tiles + q0 / 64) * 64;
+    const long long at0 = ((long long)(b * rw.N + m) * rw.tiles + q0 / 64) * 128;
 #pragma unroll
     for (int i = 0; i < 8; ++i) l2[i] = a.row_l2[at0 + ty * 8 + i], dl[i] = a.row_dl[at0 + ty * 8 + i];
     const int tiles = simt_key_tiles(a, q0);
@@ -545,7 +545,7 @@ __global__ void __launch_bounds__(128) msda_attention_join_kernel(const Attentio
 template <typename T>
 __global__ void __launch_bounds__(256) msda_attention_prepare_kernel(const AttentionArgs a, const AttentionRows rw,
                                                                      const void* out_, const float* lse, float off,
-                                                                     float* l2, float* dl, float* top, bool vec) {
+                                                                     float* l2, float* top, bool vec) {
     const long long rows = (long long)a.B * rw.N * rw.tiles * rw.rt;
     const long long total = rows + (top ? (long long)a.B * a.S * a.N : 0);
     const int lane = threadIdx.x & 7;
@@ -602,8 +602,9 @@ __global__ void __launch_bounds__(256) msda_attention_prepare_kernel(const Atten
         }
         if (i < rows) {
             if (lane == 0) {
-                l2[i] = g ? off - x * kLog2e : -attn_inf();
-                dl[i] = g ? -d : 0.f;
+                const long long bt = i / rw.rt, at = bt * rw.rt + i;
+                l2[at] = g ? off - x * kLog2e : -attn_inf();
+                l2[at + rw.rt] = g ? -d : 0.f;
             }
             best_g = gg > best_g || gg != gg ? gg : best_g;
         } else {
@@ -629,7 +630,7 @@ template <typename T>
 cudaError_t launch_attention_join(const AttentionArgs& a, cudaStream_t st);
 template <typename T>
 cudaError_t launch_attention_prepare(const AttentionArgs& a, const AttentionRows& rw, const void* out, const float* lse,
-                                     float off, float* l2, float* dl, float* top, bool vec, cudaStream_t st);
+                                     float off, float* l2, float* top, bool vec, cudaStream_t st);
 
 #ifdef MSDA_ATTENTION_SIMT_INSTANTIATE
 // head channels padded to a multiple of the 16 lanes that share a row
@@ -698,10 +699,10 @@ cudaError_t launch_attention_join(const AttentionArgs& a, cudaStream_t st) {
 }
 template <typename T>
 cudaError_t launch_attention_prepare(const AttentionArgs& a, const AttentionRows& rw, const void* out, const float* lse,
-                                     float off, float* l2, float* dl, float* top, bool vec, cudaStream_t st) {
+                                     float off, float* l2, float* top, bool vec, cudaStream_t st) {
     const long long blocks = ((long long)a.B * rw.N * rw.tiles * rw.rt + (top ? (long long)a.B * a.S * a.N : 0) + 31) / 32;
     const unsigned grid = (unsigned)(blocks < 152 * 32 ? blocks : 152 * 32);
-    msda_attention_prepare_kernel<T><<<grid, 256, 0, st>>>(a, rw, out, lse, off, l2, dl, top, vec);
+    msda_attention_prepare_kernel<T><<<grid, 256, 0, st>>>(a, rw, out, lse, off, l2, top, vec);
     return cudaGetLastError();
 }
 #define MSDA_SIMT_INSTANCES(T)                                                                                          \
@@ -710,7 +711,7 @@ cudaError_t launch_attention_prepare(const AttentionArgs& a, const AttentionRows
     template cudaError_t launch_attention_simt_grad_query<T>(const AttentionArgs&, const AttentionRows&, bool, cudaStream_t); \
     template cudaError_t launch_attention_join<T>(const AttentionArgs&, cudaStream_t);                                  \
     template cudaError_t launch_attention_prepare<T>(const AttentionArgs&, const AttentionRows&, const void*,           \
-                                                     const float*, float, float*, float*, float*, bool, cudaStream_t);
+                                                     const float*, float, float*, float*, bool, cudaStream_t);
 #endif
 
 }  // namespace msda

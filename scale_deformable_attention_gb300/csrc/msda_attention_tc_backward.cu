@@ -23,10 +23,13 @@
 
 namespace msda {
 
-// Four warpgroups on the scores (32 columns of a tile each), one of copies,
-// products and clearing.  With two (64 columns each) a tile of 64 channels took
-// 2170 cycles, half of them waits that two warps a scheduler do not cover.
-constexpr int kBwdThreads = 640;
+// Warpgroups on the scores, beside one of copies, products and clearing.  Up to
+// 64 channels four, 32 columns of a tile each: two left half of the cycles to
+// waits.  Beyond, where the products bound the kernel, two of 64 columns: four
+// took issue slots from the warps that feed the tensor cores (query kernel, 128
+// channels: 566 -> 600 us).
+constexpr int bwd_groups(int nc) { return nc == 1 ? 4 : 2; }
+constexpr int bwd_threads(int nc) { return bwd_groups(nc) * 128 + 128; }
 
 // Exponents of the scalings: P 2^kp and dS 2^ks.
 struct TcScale {
@@ -50,7 +53,7 @@ __device__ __forceinline__ TcScale tc_scale(const TcArgs& p) {
 
 struct TcBackwardSync {
     uint64_t own, full[8], empty[8], ready[8];
-    uint64_t s_full[2], dp_full, dp_free, p_ready[2], ds_ready[2], cleared, acc, delta;
+    uint64_t s_full[2], dp_full, dp_free, p_ready[2], ds_ready[2], ds_done[2], cleared, acc, delta;
     uint32_t tmem, abort;
     uint32_t words[8][4];
 };
@@ -59,35 +62,37 @@ struct TcBackwardSync {
 
 template <int NC>
 struct TcKeyCfg {
-    // a ring of tiles: Q(0), dO(0), Q(1), ..., each let go on its own
-    static constexpr int kRing = NC == 1 ? 8 : 4;
+    static constexpr int kStages = NC == 1 ? 4 : 2;  // Q, dO and the rows' statistics
     static constexpr uint32_t kTileBytes = NC * kTcTile;
-    static constexpr uint32_t kStatBytes = 1024;  // l2 and delta of 128 rows, beside a tile of Q
-    static constexpr size_t kSmem = 2 * kTileBytes + kRing * (kTileBytes + kStatBytes) + 1024;
+    static constexpr uint32_t kStatBytes = 1024;
+    static constexpr size_t kSmem = 2 * kTileBytes + kStages * (2 * kTileBytes + kStatBytes) + 1024;
     // Tensor memory.  Up to 64 channels there is room for S twice: dS then lies beside P over
-    // its S, so dP's columns are free once read, and S is made two tiles ahead and dP one: the
-    // score warps wait for no product.  (With one S the kernel stood 2300 cycles a tile
-    // whatever was taken out of it: a round through barrier, product and
-    // barrier costs about 1000 of them.)  Beyond, P lies over S and dS over dP.
+    // its S, so dP's columns are free once read, S is made two tiles ahead and dP one, and the
+    // products go to two warps (scores; gradients).  One warp had five waits, four commits and
+    // 24 products a tile to issue, 2380 cycles one behind the other, while nothing else was
+    // busy for half of them.  Beyond, P lies over S, dS over dP, and one warp issues all: its
+    // order then stands for barriers.
     static constexpr bool kAhead = NC == 1;
     static constexpr uint32_t kDP = kAhead ? 256 : 128, kDV = kAhead ? 384 : 256, kDK = kAhead ? 448 : 384;
 };
 
 template <bool BF16, int NC>
-__global__ void __launch_bounds__(kBwdThreads, 1)
+__global__ void __launch_bounds__(bwd_threads(NC), 1)
     msda_attention_tc_grad_key_kernel(const TcArgs p, const __grid_constant__ CUtensorMap map_q,
                                       const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
                                       const __grid_constant__ CUtensorMap map_do) {
     using Cfg = TcKeyCfg<NC>;
-    constexpr int R = Cfg::kRing;
+    constexpr int ST = Cfg::kStages;
+    constexpr uint32_t kStage = 2 * Cfg::kTileBytes;
     const AttentionArgs& a = p.a;
     extern __shared__ unsigned char tc_smem_raw[];
     unsigned char* smem = tc_smem_raw + ((1024u - (tc_smem(tc_smem_raw) & 1023u)) & 1023u);  // stays a shared-memory address to the compiler
     unsigned char* k_tile = smem;
     unsigned char* v_tile = smem + Cfg::kTileBytes;
-    unsigned char* ring = smem + 2 * Cfg::kTileBytes;
-    float* stats = reinterpret_cast<float*>(ring + R * Cfg::kTileBytes);  // -l2[128], -delta[128] a slot
+    unsigned char* ring = smem + 2 * Cfg::kTileBytes;                      // Q, dO a stage
+    float* stats = reinterpret_cast<float*>(ring + ST * kStage);  // l2[128], delta[128] a stage (signs turned: ready to add)
     __shared__ TcBackwardSync sy;
+    constexpr int NG = bwd_groups(NC), CH = 4 / NG;  // warpgroups, parts of 32 columns each
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
     const int ktiles = (a.S + kTcRows - 1) / kTcRows;
@@ -107,27 +112,27 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         if (!__syncthreads_or(any)) nt = 0;
     }
 
-    if (warp == 16) {
+    if (warp == NG * 4) {
         if (lane == 0) {
-            for (int i = 0; i < R; ++i) {
+            for (int i = 0; i < ST; ++i) {
                 tc_bar_init(tc_smem(&sy.full[i]), 1);
                 tc_bar_init(tc_smem(&sy.empty[i]), 1);
                 tc_bar_init(tc_smem(&sy.ready[i]), 1);
             }
             tc_bar_init(tc_smem(&sy.own), 1);
             tc_bar_init(tc_smem(&sy.dp_full), 1);
-            tc_bar_init(tc_smem(&sy.dp_free), 16);
+            tc_bar_init(tc_smem(&sy.dp_free), NG * 4);
             for (int i = 0; i < 2; ++i) {
                 tc_bar_init(tc_smem(&sy.s_full[i]), 1);
-                tc_bar_init(tc_smem(&sy.p_ready[i]), 16);
-                tc_bar_init(tc_smem(&sy.ds_ready[i]), 16);
+                tc_bar_init(tc_smem(&sy.p_ready[i]), NG * 4);
+                tc_bar_init(tc_smem(&sy.ds_ready[i]), NG * 4);
             }
             tc_bar_init(tc_smem(&sy.acc), 1);
             tc_bar_init(tc_smem(&sy.cleared), 1);
             sy.abort = 0;
             asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         }
-    } else if (warp == 17) {
+    } else if (warp == NG * 4 + 1) {
         tmem_alloc(tc_smem(&sy.tmem), 512);
     }
     tc_fence_before();
@@ -138,58 +143,63 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     const bool fix = km || p.fix_rows;  // operands that a warp clears before the products read them
     bool ok = true;
 
-    if (warp < 16) {
-        tc_regs_up<104>();
-        // ---- probabilities and their gradients: thread = key row, 32 of a tile's 128 queries ----
+    if (warp < NG * 4) {
+        // ---- probabilities and their gradients: thread = key row, CH parts of 32 of a tile's 128 queries ----
         const int w = warp >> 2, wl = warp & 3, row = wl * 32 + lane, j = j0 + row;
         const uint32_t first = lane == 0;
         const uint32_t lanes = (uint32_t)wl << 21;
-        const uint32_t dp_at = tmem + Cfg::kDP + w * 32 + lanes;
+        const uint32_t dp_at = tmem + Cfg::kDP + w * CH * 32 + lanes;
         const uint64_t c2 = tc_two(a.c2, a.c2);
         const float dscale = tc_scale<BF16>(p).ds;
         const bool has_bits = p.bits_t != nullptr;
         const int shift = a.S - a.Q;
+        int g = 0, rt = r0;  // head of the group and row tile of step i
 #pragma unroll 1
-        for (int i = 0; i < nt; ++i) {
-            const int g = i / per_head, rt = r0 + i - g * per_head, st = 2 * i % R;
-            const int q0 = rt * kTcRows + w * 32;
+        for (int i = 0; i < nt; ++i, rt + 1 < p.qblocks ? ++rt : (++g, rt = r0)) {
+            const int st = i % ST, q0 = rt * kTcRows + w * CH * 32;
             const int buf = Cfg::kAhead ? i & 1 : 0, phase = (Cfg::kAhead ? i >> 1 : i) & 1;
-            const uint32_t s_at = tmem + buf * 128 + w * 32 + lanes;
-            uint32_t bw = ~0u;
-            if (has_bits && j < a.S)
-                bw = p.bits_t[b * p.bits_t_sb + (n * a.G + g) * p.bits_t_sh + (long long)j * p.Wq + rt * 4 + w];
-            const float* l2 = stats + st * 256 + w * 32;
+            const uint32_t s_at = tmem + buf * 128 + w * CH * 32 + lanes;
+            uint32_t bw[CH];
+#pragma unroll
+            for (int c = 0; c < CH; ++c) {
+                bw[c] = ~0u;
+                if (has_bits && j < a.S)
+                    bw[c] = p.bits_t[b * p.bits_t_sb + (n * a.G + g) * p.bits_t_sh + (long long)j * p.Wq + rt * 4 + w * CH + c];
+            }
+            const float* l2 = stats + st * 256 + w * CH * 32;
             const float* dl = l2 + 128;
-            ok = tc_bar_wait(tc_smem(&sy.full[st]), (2 * i / R) & 1, abort, a.err) &&
+            ok = tc_bar_wait(tc_smem(&sy.full[st]), (i / ST) & 1, abort, a.err) &&
                  tc_bar_wait(tc_smem(&sy.s_full[buf]), phase, abort, a.err);
             if (!ok) break;
             tc_fence_after();
-            uint32_t s[32];
-            tmem_ld32(s, s_at);
-            tmem_wait_ld();
-            // causal: query q sees key j if q >= j - shift
-            if (a.causal) bw &= ~tc_low_bits(j - shift - q0);
-            if (__builtin_expect(__any_sync(0xffffffffu, bw != 0xffffffffu), 0)) {
+            uint32_t s[CH][32];
 #pragma unroll
-                for (int k = 0; k < 32; ++k)
-                    if (!((bw >> k) & 1u)) s[k] = 0xff800000u;
-            }
+            for (int c = 0; c < CH; ++c) tmem_ld32(s[c], s_at + c * 32);
+            tmem_wait_ld();
             // P^T over the thread's own columns of S^T
-            {
+#pragma unroll
+            for (int c = 0; c < CH; ++c) {
+                // causal: query q sees key j if q >= j - shift
+                if (a.causal) bw[c] &= ~tc_low_bits(j - shift - q0 - c * 32);
+                if (__builtin_expect(__any_sync(0xffffffffu, bw[c] != 0xffffffffu), 0)) {
+#pragma unroll
+                    for (int k = 0; k < 32; ++k)
+                        if (!((bw[c] >> k) & 1u)) s[c][k] = 0xff800000u;
+                }
                 uint32_t pk[16];
 #pragma unroll
                 for (int k = 0; k < 32; k += 4) {
-                    const float4 l = *reinterpret_cast<const float4*>(l2 + k);
+                    const float4 l = *reinterpret_cast<const float4*>(l2 + c * 32 + k);
                     float x0, x1, x2, x3;
-                    tc_split(tc_fma2(tc_two(__uint_as_float(s[k]), __uint_as_float(s[k + 1])), c2, tc_two(l.x, l.y)), x0, x1);
-                    tc_split(tc_fma2(tc_two(__uint_as_float(s[k + 2]), __uint_as_float(s[k + 3])), c2, tc_two(l.z, l.w)), x2, x3);
+                    tc_split(tc_fma2(tc_two(__uint_as_float(s[c][k]), __uint_as_float(s[c][k + 1])), c2, tc_two(l.x, l.y)), x0, x1);
+                    tc_split(tc_fma2(tc_two(__uint_as_float(s[c][k + 2]), __uint_as_float(s[c][k + 3])), c2, tc_two(l.z, l.w)), x2, x3);
                     const float e0 = tc_ex2(x0), e1 = tc_ex2(x1), e2 = tc_ex2(x2), e3 = tc_ex2(x3);
-                    s[k] = __float_as_uint(e0), s[k + 1] = __float_as_uint(e1);
-                    s[k + 2] = __float_as_uint(e2), s[k + 3] = __float_as_uint(e3);
+                    s[c][k] = __float_as_uint(e0), s[c][k + 1] = __float_as_uint(e1);
+                    s[c][k + 2] = __float_as_uint(e2), s[c][k + 3] = __float_as_uint(e3);
                     pk[k / 2] = tc_pack<BF16>(e0, e1);
                     pk[k / 2 + 1] = tc_pack<BF16>(e2, e3);
                 }
-                tmem_st16(s_at, pk);
+                tmem_st16(s_at + c * 32, pk);
             }
             tmem_wait_st();
             tc_fence_before();
@@ -198,36 +208,37 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             if (!ok) break;
             tc_fence_after();
             // dS^T beside P^T, or over dP^T
-            {
+#pragma unroll
+            for (int c = 0; c < CH; ++c) {
                 uint32_t d[32], pk[16];
-                tmem_ld32(d, dp_at);
+                tmem_ld32(d, dp_at + c * 32);
                 tmem_wait_ld();
-                if constexpr (Cfg::kAhead) {
+                if (Cfg::kAhead && c == CH - 1) {
                     tc_fence_before();
                     tc_bar_arrive_if(first, tc_smem(&sy.dp_free));
                 }
 #pragma unroll
                 for (int k = 0; k < 32; k += 4) {
-                    const float4 l = *reinterpret_cast<const float4*>(dl + k);
+                    const float4 l = *reinterpret_cast<const float4*>(dl + c * 32 + k);
                     float x0, x1, x2, x3;
                     uint64_t y0 = tc_add2(tc_two(__uint_as_float(d[k]), __uint_as_float(d[k + 1])), tc_two(l.x, l.y));
                     uint64_t y1 = tc_add2(tc_two(__uint_as_float(d[k + 2]), __uint_as_float(d[k + 3])), tc_two(l.z, l.w));
-                    y0 = tc_mul2(y0, tc_two(__uint_as_float(s[k]), __uint_as_float(s[k + 1])));
-                    y1 = tc_mul2(y1, tc_two(__uint_as_float(s[k + 2]), __uint_as_float(s[k + 3])));
+                    y0 = tc_mul2(y0, tc_two(__uint_as_float(s[c][k]), __uint_as_float(s[c][k + 1])));
+                    y1 = tc_mul2(y1, tc_two(__uint_as_float(s[c][k + 2]), __uint_as_float(s[c][k + 3])));
                     if constexpr (!BF16) y0 = tc_mul2(y0, tc_two(dscale, dscale)), y1 = tc_mul2(y1, tc_two(dscale, dscale));
                     tc_split(y0, x0, x1);
                     tc_split(y1, x2, x3);
                     pk[k / 2] = tc_pack<BF16>(x0, x1);
                     pk[k / 2 + 1] = tc_pack<BF16>(x2, x3);
                 }
-                tmem_st16(Cfg::kAhead ? s_at + 16 : dp_at, pk);
+                tmem_st16(Cfg::kAhead ? s_at + c * 32 + 16 : dp_at + c * 32, pk);
             }
             tmem_wait_st();
             tc_fence_before();
             // (two tiles ahead: a barrier a buffer, as a warp may be a tile ahead of another)
             tc_bar_arrive_if(first, tc_smem(&sy.ds_ready[buf]));
         }
-        // ---- dV (the first two warpgroups) and dK, alternate chunks of 16 channels ----
+        // ---- dV (the first half of the warpgroups) and dK, in chunks of 16 channels ----
         if (nt > 0 && ok) {
             ok = tc_bar_wait(tc_smem(&sy.acc), 0, abort, a.err);
             tc_fence_after();
@@ -235,10 +246,11 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         if (ok) {
             const bool live = nt > 0 && j < a.S && (!km || km[j]);
             const TcScale sc = tc_scale<BF16>(p);
-            const float f = w < 2 ? sc.inv_p : sc.inv_ds * a.scale;
-            const uint32_t at = tmem + (w < 2 ? Cfg::kDV : Cfg::kDK) + lanes;
-            unsigned char* out = static_cast<unsigned char*>(w < 2 ? a.dv : a.dk) + (((long long)b * a.S + j) * a.N + n) * a.D * 2;
-            for (int c = w & 1; c < (a.D + 15) / 16; c += 2) {
+            const bool is_v = w < NG / 2;
+            const float f = is_v ? sc.inv_p : sc.inv_ds * a.scale;
+            const uint32_t at = tmem + (is_v ? Cfg::kDV : Cfg::kDK) + lanes;
+            unsigned char* out = static_cast<unsigned char*>(is_v ? a.dv : a.dk) + (((long long)b * a.S + j) * a.N + n) * a.D * 2;
+            for (int c = w % (NG / 2); c < (a.D + 15) / 16; c += NG / 2) {
                 uint32_t o[16];
                 if (nt > 0) {
                     tmem_ld16(o, at + c * 16);
@@ -256,110 +268,127 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             }
         }
     } else {
-        tc_regs_down<64>();
-        const int role = warp - 16;
+        const int role = warp - NG * 4;
         uint64_t* full = fix ? sy.ready : sy.full;
-        if (role == 0 && lane == 0 && nt > 0) {
+        if (role == 0 && nt > 0) {
             // ---- copies ----
-            const uint32_t own = tc_smem(&sy.own);
-            tc_bar_expect(own, 2 * Cfg::kTileBytes);
+            const uint32_t on = tc_elect(), own = tc_smem(&sy.own);
+            tc_bar_expect_if(on, own, 2 * Cfg::kTileBytes);
             for (int c = 0; c < NC; ++c) {
-                tc_tma_5d(tc_smem(k_tile) + c * kTcTile, &map_k, own, c * 64, 0, j0, n, b);
-                tc_tma_5d(tc_smem(v_tile) + c * kTcTile, &map_v, own, c * 64, 0, j0, n, b);
+                tc_tma_5d_if(on, tc_smem(k_tile) + c * kTcTile, &map_k, own, c * 64, j0, n, b);
+                tc_tma_5d_if(on, tc_smem(v_tile) + c * kTcTile, &map_v, own, c * 64, j0, n, b);
             }
-            for (int x = 0; x < 2 * nt; ++x) {
-                const int i = x >> 1, g = i / per_head, rt = r0 + i - g * per_head, st = x % R, h = n * a.G + g;
-                if (x >= R) ok = tc_bar_wait(tc_smem(&sy.empty[st]), (x / R - 1) & 1, abort, a.err);
+            int g = 0, rt = r0;
+            const float* stat = a.row_l2 + ((long long)b * a.M + n * a.G) * p.qblocks * 256;
+            for (int i = 0; i < nt; ++i, rt + 1 < p.qblocks ? ++rt : (++g, rt = r0)) {
+                const int st = i % ST, h = n * a.G + g;
+                if (i >= ST) ok = tc_bar_wait(tc_smem(&sy.empty[st]), (i / ST - 1) & 1, abort, a.err);
                 if (!ok) break;
-                const uint32_t bar = tc_smem(&sy.full[st]), at = tc_smem(ring) + st * Cfg::kTileBytes;
-                tc_bar_expect(bar, Cfg::kTileBytes + ((x & 1) ? 0 : Cfg::kStatBytes));
-                for (int c = 0; c < NC; ++c)
-                    tc_tma_5d(at + c * kTcTile, (x & 1) ? &map_do : &map_q, bar, c * 64, 0, rt * kTcRows, h, b);
-                if (!(x & 1)) {
-                    const long long r = (((long long)b * a.M + h) * p.qblocks + rt) * kTcRows;
-                    tc_bulk(tc_smem(stats + st * 256), a.row_l2 + r, 512, bar);
-                    tc_bulk(tc_smem(stats + st * 256 + 128), a.row_dl + r, 512, bar);
+                const uint32_t bar = tc_smem(&sy.full[st]), at = tc_smem(ring) + st * kStage;
+                tc_bar_expect_if(on, bar, kStage + Cfg::kStatBytes);
+#pragma unroll
+                for (int c = 0; c < NC; ++c) {
+                    tc_tma_5d_if(on, at + c * kTcTile, &map_q, bar, c * 64, rt * kTcRows, h, b);
+                    tc_tma_5d_if(on, at + Cfg::kTileBytes + c * kTcTile, &map_do, bar, c * 64, rt * kTcRows, h, b);
                 }
+                tc_bulk_if(on, tc_smem(stats) + st * 1024, stat + ((long long)g * p.qblocks + rt) * 256, 1024, bar);
             }
-        } else if (role == 1 && nt > 0) {
+        } else if ((role == 1 || (Cfg::kAhead && role == 3)) && nt > 0) {
             // ---- products ----
             const uint32_t on = tc_elect();
             const int steps = (a.D + 15) / 16;
-            const uint32_t dv_at = tmem + Cfg::kDV, dk_at = tmem + Cfg::kDK;
             const uint32_t id_s = tc_idesc(BF16, false, false, 128, 128), id_g = tc_idesc(BF16, false, true, 128, steps * 16);
             const uint64_t k_desc = tc_desc(tc_smem(k_tile), 16, 1024), v_desc = tc_desc(tc_smem(v_tile), 16, 1024);
             const uint32_t base = tc_smem(ring);
-            auto at = [&](int x) { return base + (x % R) * Cfg::kTileBytes; };  // Q(i) is tile 2i, dO(i) 2i + 1
-            auto filled = [&](int x) { return tc_bar_wait(tc_smem(&full[x % R]), (x / R) & 1, abort, a.err); };
+            uint32_t step_on[NC * 4];
+#pragma unroll
+            for (int k = 0; k < NC * 4; ++k) step_on[k] = k < steps ? on : 0u;
+            // stage of step i: Q, and dO a tile further
+            const uint64_t row_desc = tc_desc(base, 16, 1024), col_desc = tc_desc(base, kTcTile, 1024);
+            auto off = [&](int i) { return (uint64_t)((i % ST) * (kStage >> 4)); };
+            constexpr uint64_t kToDo = Cfg::kTileBytes >> 4;
+            auto filled = [&](int i) { return tc_bar_wait(tc_smem(&full[i % ST]), (i / ST) & 1, abort, a.err); };
             // 128 keys x 128 queries: into d, with y the tile of queries (or of their gradients)
-            auto scores = [&](uint32_t d, uint64_t x_desc, uint32_t y, uint32_t bar) {
-                const uint64_t y_desc = tc_desc(y, 16, 1024);
+            auto scores = [&](uint32_t d, uint64_t x_desc, uint64_t y_desc, uint32_t bar) {
 #pragma unroll
                 for (int k = 0; k < NC * 4; ++k) {
-                    const uint64_t off = ((k >> 2) * kTcTile + (k & 3) * 32) >> 4;
-                    if (k < steps) tc_mma_ss(on, d, x_desc + off, y_desc + off, id_s, k > 0);
+                    const uint64_t o = ((k >> 2) * kTcTile + (k & 3) * 32) >> 4;
+                    tc_mma_ss(step_on[k], d, x_desc + o, y_desc + o, id_s, k > 0);
                 }
                 tc_commit(on, bar);
             };
             // sums over the tile's queries
-            auto gradient = [&](uint32_t d, uint32_t x, uint32_t y, bool acc) {
-                const uint64_t y_desc = tc_desc(y, kTcTile, 1024);
+            auto gradient = [&](uint32_t d, uint32_t x, uint64_t y_desc, bool acc) {
 #pragma unroll
                 for (int k = 0; k < 8; ++k)  // 16 queries; the warpgroups' parts of 32 lie 32 columns apart
                     tc_mma_ts(on, d, x + (k >> 1) * 32 + (k & 1) * 8, y_desc + ((k * 2048) >> 4), id_g, acc || k > 0);
             };
-            const uint32_t dp = tmem + Cfg::kDP;
-            ok = tc_bar_wait(tc_smem(&sy.own), 0, abort, a.err);
-            if (ok && fix) ok = tc_bar_wait(tc_smem(&sy.cleared), 0, abort, a.err);
-            ok = ok && filled(0) && filled(1) && (!Cfg::kAhead || nt < 2 || filled(2));
-            if (ok) {
-                tc_fence_after();
-                scores(tmem, k_desc, at(0), tc_smem(&sy.s_full[0]));
-                scores(dp, v_desc, at(1), tc_smem(&sy.dp_full));
-                if (Cfg::kAhead && nt > 1) scores(tmem + 128, k_desc, at(2), tc_smem(&sy.s_full[1]));
-            }
-            for (int i = 0; i < nt && ok; ++i) {
-                const bool more = i + 1 < nt;
-                const int buf = Cfg::kAhead ? i & 1 : 0, phase = (Cfg::kAhead ? i >> 1 : i) & 1;
-                const uint32_t s_at = tmem + buf * 128;
-                ok = tc_bar_wait(tc_smem(&sy.p_ready[buf]), phase, abort, a.err);
-                if (!ok) break;
-                tc_fence_after();
-                gradient(dv_at, s_at, at(2 * i + 1), i > 0);
-                tc_commit(on, tc_smem(&sy.empty[(2 * i + 1) % R]));
-                if constexpr (Cfg::kAhead) {
-                    if (more) {
-                        ok = filled(2 * i + 3) && tc_bar_wait(tc_smem(&sy.dp_free), i & 1, abort, a.err);
-                        if (!ok) break;
-                        tc_fence_after();
-                        scores(dp, v_desc, at(2 * i + 3), tc_smem(&sy.dp_full));
-                    }
-                } else if (more) {
-                    ok = filled(2 * i + 2);
-                    if (!ok) break;
+            const uint32_t dp = tmem + Cfg::kDP, dv_at = tmem + Cfg::kDV, dk_at = tmem + Cfg::kDK;
+            if (role == 1) {
+                ok = tc_bar_wait(tc_smem(&sy.own), 0, abort, a.err);
+                if (ok && fix) ok = tc_bar_wait(tc_smem(&sy.cleared), 0, abort, a.err);
+                ok = ok && filled(0);
+                if (ok) {
                     tc_fence_after();
-                    scores(tmem, k_desc, at(2 * i + 2), tc_smem(&sy.s_full[0]));
-                }
-                ok = tc_bar_wait(tc_smem(&sy.ds_ready[buf]), phase, abort, a.err);
-                if (!ok) break;
-                tc_fence_after();
-                gradient(dk_at, Cfg::kAhead ? s_at + 16 : dp, at(2 * i), i > 0);
-                tc_commit(on, tc_smem(&sy.empty[2 * i % R]));
-                if constexpr (Cfg::kAhead) {
-                    if (i + 2 < nt) {
-                        ok = filled(2 * i + 4);
-                        if (!ok) break;
-                        tc_fence_after();
-                        scores(s_at, k_desc, at(2 * i + 4), tc_smem(&sy.s_full[buf]));
-                    }
-                } else if (more) {
-                    ok = filled(2 * i + 3);
-                    if (!ok) break;
-                    tc_fence_after();
-                    scores(dp, v_desc, at(2 * i + 3), tc_smem(&sy.dp_full));
+                    scores(tmem, k_desc, row_desc + off(0), tc_smem(&sy.s_full[0]));
+                    scores(dp, v_desc, row_desc + off(0) + kToDo, tc_smem(&sy.dp_full));
                 }
             }
-            if (ok) tc_commit(on, tc_smem(&sy.acc));
+            if constexpr (Cfg::kAhead) {
+                if (role == 1) {
+                    if (ok && nt > 1) {
+                        ok = filled(1);
+                        tc_fence_after();
+                        if (ok) scores(tmem + 128, k_desc, row_desc + off(1), tc_smem(&sy.s_full[1]));
+                    }
+                    for (int i = 0; i + 1 < nt && ok; ++i) {
+                        ok = tc_bar_wait(tc_smem(&sy.dp_free), i & 1, abort, a.err);
+                        if (!ok) break;
+                        tc_fence_after();
+                        scores(dp, v_desc, row_desc + off(i + 1) + kToDo, tc_smem(&sy.dp_full));
+                        if (i + 2 < nt) {  // over S(i), when P(i) and dS(i) are used up
+                            ok = filled(i + 2) && tc_bar_wait(tc_smem(&sy.empty[i % ST]), (i / ST) & 1, abort, a.err);
+                            if (!ok) break;
+                            tc_fence_after();
+                            scores(tmem + (i & 1) * 128, k_desc, row_desc + off(i + 2), tc_smem(&sy.s_full[i & 1]));
+                        }
+                    }
+                } else {
+                    for (int i = 0; i < nt; ++i) {
+                        const int buf = i & 1, phase = (i >> 1) & 1;
+                        ok = tc_bar_wait(tc_smem(&sy.p_ready[buf]), phase, abort, a.err);
+                        if (!ok) break;
+                        tc_fence_after();
+                        gradient(dv_at, tmem + buf * 128, col_desc + off(i) + kToDo, i > 0);
+                        ok = tc_bar_wait(tc_smem(&sy.ds_ready[buf]), phase, abort, a.err);
+                        if (!ok) break;
+                        tc_fence_after();
+                        gradient(dk_at, tmem + buf * 128 + 16, col_desc + off(i), i > 0);
+                        tc_commit(on, tc_smem(&sy.empty[i % ST]));
+                    }
+                    if (ok) tc_commit(on, tc_smem(&sy.acc));
+                }
+            } else {
+                for (int i = 0; i < nt && ok; ++i) {
+                    ok = tc_bar_wait(tc_smem(&sy.p_ready[0]), i & 1, abort, a.err);
+                    if (!ok) break;
+                    tc_fence_after();
+                    gradient(dv_at, tmem, col_desc + off(i) + kToDo, i > 0);
+                    if (i + 1 < nt) {
+                        ok = filled(i + 1);
+                        if (!ok) break;
+                        tc_fence_after();
+                        scores(tmem, k_desc, row_desc + off(i + 1), tc_smem(&sy.s_full[0]));
+                    }
+                    ok = tc_bar_wait(tc_smem(&sy.ds_ready[0]), i & 1, abort, a.err);
+                    if (!ok) break;
+                    tc_fence_after();
+                    gradient(dk_at, dp, col_desc + off(i), i > 0);
+                    tc_commit(on, tc_smem(&sy.empty[i % ST]));
+                    if (i + 1 < nt) scores(dp, v_desc, row_desc + off(i + 1) + kToDo, tc_smem(&sy.dp_full));
+                }
+                if (ok) tc_commit(on, tc_smem(&sy.acc));
+            }
         } else if (role == 2 && fix && nt > 0) {
             // ---- keys, and rows without keys, that take no part ----
             ok = tc_bar_wait(tc_smem(&sy.own), 0, abort, a.err);
@@ -374,18 +403,17 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                 __syncwarp();
                 if (lane == 0) tc_bar_arrive(tc_smem(&sy.cleared));
             }
-            uint32_t w[4];
-            for (int x = 0; x < 2 * nt && ok; ++x) {
-                const int st = x % R;
-                ok = tc_bar_wait(tc_smem(&sy.full[st]), (x / R) & 1, abort, a.err);
+            for (int i = 0; i < nt && ok; ++i) {
+                const int st = i % ST;
+                ok = tc_bar_wait(tc_smem(&sy.full[st]), (i / ST) & 1, abort, a.err);
                 if (!ok) break;
-                if (!(x & 1)) {
+                uint32_t w[4];
 #pragma unroll
-                    for (int c = 0; c < 4; ++c)
-                        w[c] = __ballot_sync(0xffffffffu, stats[st * 256 + c * 32 + lane] != -attn_inf());
-                }
+                for (int c = 0; c < 4; ++c)
+                    w[c] = __ballot_sync(0xffffffffu, stats[st * 256 + c * 32 + lane] != -attn_inf());
                 if ((w[0] & w[1] & w[2] & w[3]) != 0xffffffffu) {
-                    tc_clear_rows<NC>(ring + st * Cfg::kTileBytes, w, lane);
+                    tc_clear_rows<NC>(ring + st * kStage, w, lane);
+                    tc_clear_rows<NC>(ring + st * kStage + Cfg::kTileBytes, w, lane);
                     tc_fence_async();
                 }
                 __syncwarp();
@@ -397,25 +425,28 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     if (!ok) tc_drain();
     tc_fence_before();
     __syncthreads();
-    if (warp == 17) tmem_dealloc(tmem, 512);
+    if (warp == NG * 4 + 1) tmem_dealloc(tmem, 512);
 }
 
 // ---- gradient of queries ----
 
 template <int NC>
 struct TcQueryCfg {
-    // a ring of tiles: K(0), V(0), K(1), ...; V is let go behind its scores, K behind dQ.
+    // Up to 64 channels: stages of K and V, S two tiles ahead, dP one, dS over its S, the
+    // products on two warps (as in the key kernel).  Beyond: a ring of tiles
+    // V(0), K(0), V(1), ...; V is let go behind its scores, K behind dQ.
     // (Pairs of K and V in two stages left the products waiting 1600 of 3200
     // cycles a tile for them at 128 channels.)
-    static constexpr int kRing = NC == 1 ? 8 : 5;
+    static constexpr bool kAhead = NC == 1;
+    static constexpr int kRing = NC == 1 ? 8 : 5;  // tiles
     static constexpr uint32_t kTileBytes = NC * kTcTile;
     static constexpr size_t kSmem = (2 + kRing) * kTileBytes + 1024;
-    // tensor memory: S twice, dP, dQ; dS lies over its S (as in the key kernel: S two tiles ahead, dP one)
-    static constexpr uint32_t kDP = 256, kDQ = 384;
+    // tensor memory, kAhead: S twice (dS over it), dP, dQ; else S, dP, dS twice (dQ of a tile runs beside the next tile's dS), dQ
+    static constexpr uint32_t kDP = kAhead ? 256 : 128, kDS = 256, kDQ = 384;
 };
 
 template <bool BF16, int NC>
-__global__ void __launch_bounds__(kBwdThreads, 1)
+__global__ void __launch_bounds__(bwd_threads(NC), 1)
     msda_attention_tc_grad_query_kernel(const TcArgs p, const __grid_constant__ CUtensorMap map_q,
                                         const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
                                         const __grid_constant__ CUtensorMap map_do) {
@@ -428,6 +459,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     unsigned char* do_tile = smem + Cfg::kTileBytes;
     unsigned char* ring = smem + 2 * Cfg::kTileBytes;
     __shared__ TcBackwardSync sy;
+    constexpr int NG = bwd_groups(NC), CH = 4 / NG;  // warpgroups, parts of 32 columns each
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
     long long id = blockIdx.x;
@@ -441,7 +473,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     if (km) tc_trim(km, a.S, &t0, &t1);
     const int nt = max(0, t1 - t0);
 
-    if (warp == 16) {
+    if (warp == NG * 4) {
         if (lane == 0) {
             for (int i = 0; i < R; ++i) {
                 tc_bar_init(tc_smem(&sy.full[i]), 1);
@@ -450,17 +482,18 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             }
             tc_bar_init(tc_smem(&sy.own), 1);
             tc_bar_init(tc_smem(&sy.acc), 1);
-            tc_bar_init(tc_smem(&sy.delta), 16);
+            tc_bar_init(tc_smem(&sy.delta), NG * 4);
             tc_bar_init(tc_smem(&sy.dp_full), 1);
-            tc_bar_init(tc_smem(&sy.dp_free), 16);
+            tc_bar_init(tc_smem(&sy.dp_free), NG * 4);
             for (int i = 0; i < 2; ++i) {
                 tc_bar_init(tc_smem(&sy.s_full[i]), 1);
-                tc_bar_init(tc_smem(&sy.ds_ready[i]), 16);
+                tc_bar_init(tc_smem(&sy.ds_ready[i]), NG * 4);
+                tc_bar_init(tc_smem(&sy.ds_done[i]), 1);
             }
             sy.abort = 0;
             asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         }
-    } else if (warp == 17) {
+    } else if (warp == NG * 4 + 1) {
         tmem_alloc(tc_smem(&sy.tmem), 512);
     }
     tc_fence_before();
@@ -470,15 +503,14 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     volatile uint32_t* abort = &sy.abort;
     bool ok = true;
 
-    if (warp < 16) {
-        tc_regs_up<104>();
-        // thread = query row, 32 of a tile's 128 keys
+    if (warp < NG * 4) {
+        // thread = query row, CH parts of 32 of a tile's 128 keys
         const int w = warp >> 2, wl = warp & 3, row = wl * 32 + lane, q = q0 + row;
         const uint32_t first = lane == 0;
         const uint32_t lanes = (uint32_t)wl << 21;
-        const uint32_t dp_at = tmem + Cfg::kDP + w * 32 + lanes;
+        const uint32_t dp_at = tmem + Cfg::kDP + w * CH * 32 + lanes;
         const TcScale sc = tc_scale<BF16>(p);
-        const long long r = (((long long)b * a.M + h) * p.qblocks + rt) * kTcRows + row;
+        const long long r = (((long long)b * a.M + h) * p.qblocks + rt) * 256 + row;
         const float l2 = a.row_l2[r], dl = a.row_dl[r];
         const bool live = l2 != -attn_inf();  // q < Q and some key seen
         const int seen = live ? tc_seen(a, q) : 0;
@@ -488,41 +520,66 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         uint64_t nd = tc_two(dl * sc.ds, dl * sc.ds);
 #pragma unroll 1
         for (int i = 0; i < nt; ++i) {
-            const int j0 = (t0 + i) * kTcRows + w * 32;
-            uint32_t bw = ~0u;
-            if (bits) bw = bits[(t0 + i) * 4 + w];
+            const int j0 = (t0 + i) * kTcRows + w * CH * 32;
+            uint32_t bw[CH];
+#pragma unroll
+            for (int c = 0; c < CH; ++c) bw[c] = bits ? bits[(t0 + i) * 4 + w * CH + c] : ~0u;
             const int buf = i & 1;
-            const uint32_t s_at = tmem + buf * 128 + w * 32 + lanes;
-            ok = tc_bar_wait(tc_smem(&sy.s_full[buf]), (i >> 1) & 1, abort, a.err);
+            const uint32_t s_at = tmem + (Cfg::kAhead ? buf * 128 : 0) + w * CH * 32 + lanes;
+            ok = tc_bar_wait(tc_smem(&sy.s_full[Cfg::kAhead ? buf : 0]), (Cfg::kAhead ? i >> 1 : i) & 1, abort, a.err);
             if (!ok) break;
             tc_fence_after();
-            uint32_t s[32], d[32];
-            tmem_ld32(s, s_at);
-            tmem_wait_ld();
-            if (__builtin_expect(km || a.bits || seen_least - j0 < 32, 0)) {
-                bw &= tc_low_bits(seen - j0);
-                if (km) bw &= sy.words[i & 7][w];
-                if (__any_sync(0xffffffffu, bw != 0xffffffffu)) {
+            uint32_t s[CH][32], d[CH][32];
 #pragma unroll
-                    for (int k = 0; k < 32; ++k)
-                        if (!((bw >> k) & 1u)) s[k] = 0xff800000u;
+            for (int c = 0; c < CH; ++c) tmem_ld32(s[c], s_at + c * 32);
+            if constexpr (!Cfg::kAhead) {
+#pragma unroll
+                for (int c = 0; c < CH; ++c) tmem_ld32(d[c], dp_at + c * 32);
+            }
+            tmem_wait_ld();
+            if constexpr (!Cfg::kAhead) {  // both are read: the next may be made
+                tc_fence_before();
+                tc_bar_arrive_if(first, tc_smem(&sy.dp_free));
+            }
+            if (__builtin_expect(km || a.bits || seen_least - j0 < CH * 32, 0)) {
+#pragma unroll
+                for (int c = 0; c < CH; ++c) {
+                    bw[c] &= tc_low_bits(seen - j0 - c * 32);
+                    if (km) bw[c] &= sy.words[i & 7][w * CH + c];
+                    if (__any_sync(0xffffffffu, bw[c] != 0xffffffffu)) {
+#pragma unroll
+                        for (int k = 0; k < 32; ++k)
+                            if (!((bw[c] >> k) & 1u)) s[c][k] = 0xff800000u;
+                    }
                 }
             }
-            // probabilities
-#pragma unroll
-            for (int k = 0; k < 32; k += 2) {
+            auto probability = [&](int c, int k) {
                 float x0, x1;
-                tc_split(tc_fma2(tc_two(__uint_as_float(s[k]), __uint_as_float(s[k + 1])), c2, nl), x0, x1);
-                s[k] = __float_as_uint(tc_ex2(x0));
-                s[k + 1] = __float_as_uint(tc_ex2(x1));
+                tc_split(tc_fma2(tc_two(__uint_as_float(s[c][k]), __uint_as_float(s[c][k + 1])), c2, nl), x0, x1);
+                return tc_two(tc_ex2(x0), tc_ex2(x1));
+            };
+            if constexpr (Cfg::kAhead) {  // while dP is on its way
+#pragma unroll
+                for (int c = 0; c < CH; ++c)
+#pragma unroll
+                    for (int k = 0; k < 32; k += 2) {
+                        float e0, e1;
+                        tc_split(probability(c, k), e0, e1);
+                        s[c][k] = __float_as_uint(e0), s[c][k + 1] = __float_as_uint(e1);
+                    }
+                ok = tc_bar_wait(tc_smem(&sy.dp_full), i & 1, abort, a.err);
+                if (!ok) break;
+                tc_fence_after();
+#pragma unroll
+                for (int c = 0; c < CH; ++c) tmem_ld32(d[c], dp_at + c * 32);
+                tmem_wait_ld();
+                tc_fence_before();
+                tc_bar_arrive_if(first, tc_smem(&sy.dp_free));
+            } else if (i > 1) {  // dS(i-2) is used up
+                ok = tc_bar_wait(tc_smem(&sy.ds_done[buf]), (i / 2 - 1) & 1, abort, a.err);
+                if (!ok) break;
+                tc_fence_after();
             }
-            ok = tc_bar_wait(tc_smem(&sy.dp_full), i & 1, abort, a.err);
-            if (!ok) break;
-            tc_fence_after();
-            tmem_ld32(d, dp_at);
-            tmem_wait_ld();
-            tc_fence_before();
-            tc_bar_arrive_if(first, tc_smem(&sy.dp_free));
             if (p.delta_out) {
                 // One tile of keys: delta = sum_j p dP from the values at hand, not <dout, out>.  With few keys out is
                 // as large as a value and its rounding to 16 bits, carried into dP - delta, was the largest error
@@ -530,10 +587,13 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                 float2* part_sum = reinterpret_cast<float2*>(ring + 2 * Cfg::kTileBytes);  // one tile: the ring's third is free
                 float sum = 0.f, ps = 0.f;
 #pragma unroll
-                for (int k = 0; k < 32; ++k) {  // a pair that takes no part adds nothing, whatever its dP
-                    const float e = __uint_as_float(s[k]);
-                    if (e != 0.f) sum = fmaf(e, __uint_as_float(d[k]), sum), ps += e;
-                }
+                for (int c = 0; c < CH; ++c)
+#pragma unroll
+                    for (int k = 0; k < 32; ++k) {  // a pair that takes no part adds nothing, whatever its dP
+                        float e = __uint_as_float(s[c][k]);
+                        if (!Cfg::kAhead) e = tc_ex2(fmaf(e, a.c2, l2));
+                        if (e != 0.f) sum = fmaf(e, __uint_as_float(d[c][k]), sum), ps += e;
+                    }
                 part_sum[w * 128 + row] = make_float2(sum, ps);
                 __syncwarp();
                 if (lane == 0) tc_bar_arrive(tc_smem(&sy.delta));
@@ -541,23 +601,24 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                 if (!ok) break;
                 sum = ps = 0.f;
 #pragma unroll
-                for (int g = 0; g < 4; ++g) sum += part_sum[g * 128 + row].x, ps += part_sum[g * 128 + row].y;
+                for (int g = 0; g < NG; ++g) sum += part_sum[g * 128 + row].x, ps += part_sum[g * 128 + row].y;
                 // over the probabilities' own sum, which their rounding keeps off 1: the row's dS then add up to 0
                 const float delta = live && ps > 0.f ? -sum / ps : 0.f;
                 nd = tc_two(delta * sc.ds, delta * sc.ds);
                 if (w == 0) p.delta_out[r] = delta;
             }
-            {
+#pragma unroll
+            for (int c = 0; c < CH; ++c) {
                 uint32_t pk[16];
 #pragma unroll
                 for (int k = 0; k < 32; k += 2) {
                     float x0, x1;
-                    const uint64_t e = tc_two(__uint_as_float(s[k]), __uint_as_float(s[k + 1]));
-                    const uint64_t dp = tc_two(__uint_as_float(d[k]), __uint_as_float(d[k + 1]));
+                    const uint64_t e = Cfg::kAhead ? tc_two(__uint_as_float(s[c][k]), __uint_as_float(s[c][k + 1])) : probability(c, k);
+                    const uint64_t dp = tc_two(__uint_as_float(d[c][k]), __uint_as_float(d[c][k + 1]));
                     tc_split(tc_mul2(BF16 ? tc_add2(dp, nd) : tc_fma2(dp, ds2, nd), e), x0, x1);
                     pk[k / 2] = tc_pack<BF16>(x0, x1);
                 }
-                tmem_st16(s_at, pk);
+                tmem_st16(Cfg::kAhead ? s_at + c * 32 : tmem + Cfg::kDS + buf * 64 + (w * CH + c) * 16 + lanes, pk);
             }
             tmem_wait_st();
             tc_fence_before();
@@ -568,10 +629,10 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             ok = tc_bar_wait(tc_smem(&sy.acc), 0, abort, a.err);
             tc_fence_after();
         }
-        if (ok) {  // the warpgroups take every fourth chunk of 16 channels
+        if (ok) {  // the warpgroups take chunks of 16 channels in turn
             const float f = sc.inv_ds * a.scale;
             unsigned char* out = static_cast<unsigned char*>(a.dq) + (((long long)b * a.Q + q) * a.M + h) * a.D * 2;
-            for (int c = w; c < (a.D + 15) / 16; c += 4) {
+            for (int c = w; c < (a.D + 15) / 16; c += NG) {
                 uint32_t o[16];
                 if (nt > 0) {
                     tmem_ld16(o, tmem + Cfg::kDQ + lanes + c * 16);
@@ -589,96 +650,158 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             }
         }
     } else {
-        tc_regs_down<64>();
-        const int role = warp - 16;
+        const int role = warp - NG * 4;
         uint64_t* full = km ? sy.ready : sy.full;
-        if (role == 0 && lane == 0 && nt > 0) {
-            const uint32_t own = tc_smem(&sy.own);
-            tc_bar_expect(own, 2 * Cfg::kTileBytes);
+        // kAhead: stage i holds K and V in tiles 2i and 2i + 1 of the ring, under one barrier (that of the even tile);
+        // else V(i) is tile 2i, K(i) tile 2i + 1, each with its own
+        constexpr int ST = R / 2;
+        if (role == 0 && nt > 0) {
+            // ---- copies ----
+            const uint32_t on = tc_elect(), own = tc_smem(&sy.own);
+            tc_bar_expect_if(on, own, 2 * Cfg::kTileBytes);
             for (int c = 0; c < NC; ++c) {
-                tc_tma_5d(tc_smem(q_tile) + c * kTcTile, &map_q, own, c * 64, 0, q0, h, b);
-                tc_tma_5d(tc_smem(do_tile) + c * kTcTile, &map_do, own, c * 64, 0, q0, h, b);
+                tc_tma_5d_if(on, tc_smem(q_tile) + c * kTcTile, &map_q, own, c * 64, q0, h, b);
+                tc_tma_5d_if(on, tc_smem(do_tile) + c * kTcTile, &map_do, own, c * 64, q0, h, b);
             }
-            for (int x = 0; x < 2 * nt; ++x) {
-                const int st = x % R;
-                if (x >= R) ok = tc_bar_wait(tc_smem(&sy.empty[st]), (x / R - 1) & 1, abort, a.err);
-                if (!ok) break;
-                const uint32_t bar = tc_smem(&sy.full[st]);
-                tc_bar_expect(bar, Cfg::kTileBytes);
-                for (int c = 0; c < NC; ++c)
-                    tc_tma_5d(tc_smem(ring) + st * Cfg::kTileBytes + c * kTcTile, (x & 1) ? &map_v : &map_k, bar, c * 64, 0,
-                              (t0 + (x >> 1)) * kTcRows, n, b);
+            if constexpr (Cfg::kAhead) {
+                for (int i = 0; i < nt; ++i) {
+                    const int st = 2 * (i % ST);
+                    if (i >= ST) ok = tc_bar_wait(tc_smem(&sy.empty[st]), (i / ST - 1) & 1, abort, a.err);
+                    if (!ok) break;
+                    const uint32_t bar = tc_smem(&sy.full[st]), at = tc_smem(ring) + st * Cfg::kTileBytes;
+                    tc_bar_expect_if(on, bar, 2 * Cfg::kTileBytes);
+                    tc_tma_5d_if(on, at, &map_k, bar, 0, (t0 + i) * kTcRows, n, b);
+                    tc_tma_5d_if(on, at + Cfg::kTileBytes, &map_v, bar, 0, (t0 + i) * kTcRows, n, b);
+                }
+            } else {
+                for (int x = 0, st = 0, wrap = 0; x < 2 * nt; ++x) {
+                    if (x >= R) ok = tc_bar_wait(tc_smem(&sy.empty[st]), (wrap - 1) & 1, abort, a.err);
+                    if (!ok) break;
+                    const uint32_t bar = tc_smem(&sy.full[st]), at = tc_smem(ring) + st * Cfg::kTileBytes;
+                    tc_bar_expect_if(on, bar, Cfg::kTileBytes);
+#pragma unroll
+                    for (int c = 0; c < NC; ++c)
+                        tc_tma_5d_if(on, at + c * kTcTile, (x & 1) ? &map_k : &map_v, bar, c * 64, (t0 + (x >> 1)) * kTcRows, n, b);
+                    if (++st == R) st = 0, ++wrap;
+                }
             }
-        } else if (role == 1 && nt > 0) {
+        } else if ((role == 1 || (Cfg::kAhead && role == 3)) && nt > 0) {
             // ---- products ----
             const uint32_t on = tc_elect();
             const int steps = (a.D + 15) / 16;
             const uint32_t id_s = tc_idesc(BF16, false, false, 128, 128), id_g = tc_idesc(BF16, false, true, 128, steps * 16);
             const uint64_t q_desc = tc_desc(tc_smem(q_tile), 16, 1024), do_desc = tc_desc(tc_smem(do_tile), 16, 1024);
-            const uint32_t base = tc_smem(ring);
-            auto at = [&](int x) { return base + (x % R) * Cfg::kTileBytes; };  // K(i) is tile 2i, V(i) 2i + 1
-            auto filled = [&](int x) { return tc_bar_wait(tc_smem(&full[x % R]), (x / R) & 1, abort, a.err); };
-            auto scores = [&](uint32_t d, uint64_t x_desc, uint32_t y, uint32_t bar) {
-                const uint64_t y_desc = tc_desc(y, 16, 1024);
+            const uint32_t base = tc_smem(ring), dp = tmem + Cfg::kDP;
+            const uint64_t row_desc = tc_desc(base, 16, 1024), col_desc = tc_desc(base, kTcTile, 1024);
+            constexpr uint64_t kTile = Cfg::kTileBytes >> 4;
+            uint32_t step_on[NC * 4];
+#pragma unroll
+            for (int k = 0; k < NC * 4; ++k) step_on[k] = k < steps ? on : 0u;
+            auto scores = [&](uint32_t d, uint64_t x_desc, uint64_t y_desc) {  // 128 queries x 128 keys
 #pragma unroll
                 for (int k = 0; k < NC * 4; ++k) {
-                    const uint64_t off = ((k >> 2) * kTcTile + (k & 3) * 32) >> 4;
-                    if (k < steps) tc_mma_ss(on, d, x_desc + off, y_desc + off, id_s, k > 0);
+                    const uint64_t o = ((k >> 2) * kTcTile + (k & 3) * 32) >> 4;
+                    tc_mma_ss(step_on[k], d, x_desc + o, y_desc + o, id_s, k > 0);
                 }
-                tc_commit(on, bar);
             };
-            auto product_dp = [&](int i) {
-                scores(tmem + Cfg::kDP, do_desc, at(2 * i + 1), tc_smem(&sy.dp_full));
-                tc_commit(on, tc_smem(&sy.empty[(2 * i + 1) % R]));
-            };
-            ok = tc_bar_wait(tc_smem(&sy.own), 0, abort, a.err) && filled(0) && filled(1) && (nt < 2 || filled(2));
-            if (ok) {
-                tc_fence_after();
-                scores(tmem, q_desc, at(0), tc_smem(&sy.s_full[0]));
-                product_dp(0);
-                if (nt > 1) scores(tmem + 128, q_desc, at(2), tc_smem(&sy.s_full[1]));
-            }
-            for (int i = 0; i < nt && ok; ++i) {
-                const int buf = i & 1;
-                if (i + 1 < nt) {
-                    ok = filled(2 * i + 3) && tc_bar_wait(tc_smem(&sy.dp_free), i & 1, abort, a.err);
-                    if (!ok) break;
-                    tc_fence_after();
-                    product_dp(i + 1);
-                }
-                ok = tc_bar_wait(tc_smem(&sy.ds_ready[buf]), (i >> 1) & 1, abort, a.err);
-                if (!ok) break;
-                tc_fence_after();
-                const uint64_t k_desc = tc_desc(at(2 * i), kTcTile, 1024);
+            // dQ += dS K over the tile's keys: 16 a step, a warpgroup's part of 32 `part` columns behind the one before
+            auto gradient = [&](uint32_t x, uint32_t part, uint64_t y_desc, bool acc) {
 #pragma unroll
-                for (int k = 0; k < 8; ++k)  // 16 keys; the warpgroups' parts of 32 lie 32 columns apart
-                    tc_mma_ts(on, tmem + Cfg::kDQ, tmem + buf * 128 + (k >> 1) * 32 + (k & 1) * 8, k_desc + ((k * 2048) >> 4),
-                              id_g, i > 0 || k > 0);
-                tc_commit(on, tc_smem(&sy.empty[2 * i % R]));
-                if (i + 2 < nt) {
-                    ok = filled(2 * i + 4);
+                for (int k = 0; k < 8; ++k)
+                    tc_mma_ts(on, tmem + Cfg::kDQ, x + (k >> 1) * part + (k & 1) * 8, y_desc + ((k * 2048) >> 4), id_g, acc || k > 0);
+            };
+            if constexpr (Cfg::kAhead) {
+                auto off = [&](int i) { return 2 * (i % ST) * kTile; };
+                auto filled = [&](int i) { return tc_bar_wait(tc_smem(&full[2 * (i % ST)]), (i / ST) & 1, abort, a.err); };
+                if (role == 1) {
+                    ok = tc_bar_wait(tc_smem(&sy.own), 0, abort, a.err) && filled(0);
+                    if (ok) {
+                        tc_fence_after();
+                        scores(tmem, q_desc, row_desc);
+                        tc_commit(on, tc_smem(&sy.s_full[0]));
+                        scores(dp, do_desc, row_desc + kTile);
+                        tc_commit(on, tc_smem(&sy.dp_full));
+                    }
+                    if (ok && nt > 1) {
+                        ok = filled(1);
+                        tc_fence_after();
+                        if (ok) {
+                            scores(tmem + 128, q_desc, row_desc + off(1));
+                            tc_commit(on, tc_smem(&sy.s_full[1]));
+                        }
+                    }
+                    for (int i = 0; i + 1 < nt && ok; ++i) {
+                        ok = tc_bar_wait(tc_smem(&sy.dp_free), i & 1, abort, a.err);
+                        if (!ok) break;
+                        tc_fence_after();
+                        scores(dp, do_desc, row_desc + off(i + 1) + kTile);
+                        tc_commit(on, tc_smem(&sy.dp_full));
+                        if (i + 2 < nt) {  // over S(i), when dS(i) is used up
+                            ok = filled(i + 2) && tc_bar_wait(tc_smem(&sy.empty[2 * (i % ST)]), (i / ST) & 1, abort, a.err);
+                            if (!ok) break;
+                            tc_fence_after();
+                            scores(tmem + (i & 1) * 128, q_desc, row_desc + off(i + 2));
+                            tc_commit(on, tc_smem(&sy.s_full[i & 1]));
+                        }
+                    }
+                } else {
+                    for (int i = 0; i < nt; ++i) {
+                        ok = tc_bar_wait(tc_smem(&sy.ds_ready[i & 1]), (i >> 1) & 1, abort, a.err);
+                        if (!ok) break;
+                        tc_fence_after();
+                        gradient(tmem + (i & 1) * 128, 32, col_desc + off(i), i > 0);
+                        tc_commit(on, tc_smem(&sy.empty[2 * (i % ST)]));
+                    }
+                    if (ok) tc_commit(on, tc_smem(&sy.acc));
+                }
+            } else {
+                int sv = 0, pv = 0;  // slot of V(i + 1) and its phase
+                auto pair = [&](int i) {  // dP = dO V^T, S = Q K^T of step i, tiles sv and the next
+                    const int sk = sv + 1 == R ? 0 : sv + 1, pk = sk == 0 ? pv ^ 1 : pv;
+                    ok = tc_bar_wait(tc_smem(&full[sv]), pv, abort, a.err) && tc_bar_wait(tc_smem(&full[sk]), pk, abort, a.err) &&
+                         (i == 0 || tc_bar_wait(tc_smem(&sy.dp_free), (i - 1) & 1, abort, a.err));
+                    if (!ok) return;
+                    tc_fence_after();
+                    scores(dp, do_desc, row_desc + sv * kTile);
+                    tc_commit(on, tc_smem(&sy.empty[sv]));
+                    scores(tmem, q_desc, row_desc + sk * kTile);
+                    tc_commit(on, tc_smem(&sy.s_full[0]));
+                    sv = sk + 1 == R ? 0 : sk + 1;
+                    pv = sv == 0 ? pk ^ 1 : pk;
+                };
+                ok = tc_bar_wait(tc_smem(&sy.own), 0, abort, a.err);
+                if (ok) pair(0);
+                int sk = 1;  // slot of K(i)
+                for (int i = 0; i < nt && ok; ++i) {
+                    if (i + 1 < nt) pair(i + 1);
+                    ok = ok && tc_bar_wait(tc_smem(&sy.ds_ready[i & 1]), (i >> 1) & 1, abort, a.err);
                     if (!ok) break;
                     tc_fence_after();
-                    scores(tmem + buf * 128, q_desc, at(2 * i + 4), tc_smem(&sy.s_full[buf]));
+                    gradient(tmem + Cfg::kDS + (i & 1) * 64, 16, col_desc + sk * kTile, i > 0);
+                    tc_commit(on, tc_smem(&sy.ds_done[i & 1]));
+                    tc_commit(on, tc_smem(&sy.empty[sk]));
+                    sk = sk + 2 >= R ? sk + 2 - R : sk + 2;
                 }
+                if (ok) tc_commit(on, tc_smem(&sy.acc));
             }
-            if (ok) tc_commit(on, tc_smem(&sy.acc));
         } else if (role == 2 && km && nt > 0) {
+            // ---- keys that take no part ----
             uint32_t w[4];
-            for (int x = 0; x < 2 * nt && ok; ++x) {
-                const int st = x % R, i = x >> 1;
+            for (int x = 0, st = 0, wrap = 0; x < 2 * nt && ok; ++x) {
+                const int i = x >> 1;
                 if (!(x & 1)) {
                     tc_key_words(km + (t0 + i) * kTcRows, a.S - (t0 + i) * kTcRows, lane, w);
                     if (lane < 4) sy.words[i & 7][lane] = lane == 0 ? w[0] : lane == 1 ? w[1] : lane == 2 ? w[2] : w[3];
                 }
-                ok = tc_bar_wait(tc_smem(&sy.full[st]), (x / R) & 1, abort, a.err);
+                if (!Cfg::kAhead || !(x & 1)) ok = tc_bar_wait(tc_smem(&sy.full[st]), wrap & 1, abort, a.err);
                 if (!ok) break;
                 if ((w[0] & w[1] & w[2] & w[3]) != 0xffffffffu) {
                     tc_clear_rows<NC>(ring + st * Cfg::kTileBytes, w, lane);
                     tc_fence_async();
                 }
                 __syncwarp();
-                if (lane == 0) tc_bar_arrive(tc_smem(&sy.ready[st]));
+                if (lane == 0 && (!Cfg::kAhead || (x & 1))) tc_bar_arrive(tc_smem(&sy.ready[Cfg::kAhead ? st - 1 : st]));
+                if (++st == R) st = 0, ++wrap;
             }
         }
         __syncwarp();
@@ -686,7 +809,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     if (!ok) tc_drain();
     tc_fence_before();
     __syncthreads();
-    if (warp == 17) tmem_dealloc(tmem, 512);
+    if (warp == NG * 4 + 1) tmem_dealloc(tmem, 512);
 }
 
 // ---- host ----
@@ -699,7 +822,7 @@ static cudaError_t grad_key_go(const TcArgs& p, const CUtensorMap& q, const CUte
     cudaError_t e = allow_smem(reinterpret_cast<const void*>(&msda_attention_tc_grad_key_kernel<BF16, NC>), smem, seen);
     if (e != cudaSuccess) return e;
     const long long grid = (long long)p.a.B * p.a.N * ((p.a.S + kTcRows - 1) / kTcRows);
-    msda_attention_tc_grad_key_kernel<BF16, NC><<<(unsigned)grid, kBwdThreads, smem, st>>>(p, q, k, v, g);
+    msda_attention_tc_grad_key_kernel<BF16, NC><<<(unsigned)grid, bwd_threads(NC), smem, st>>>(p, q, k, v, g);
     return cudaGetLastError();
 }
 template <bool BF16, int NC>
@@ -710,7 +833,7 @@ static cudaError_t grad_query_go(const TcArgs& p, const CUtensorMap& q, const CU
     cudaError_t e = allow_smem(reinterpret_cast<const void*>(&msda_attention_tc_grad_query_kernel<BF16, NC>), smem, seen);
     if (e != cudaSuccess) return e;
     const long long grid = (long long)p.a.B * p.a.M * p.qblocks;
-    msda_attention_tc_grad_query_kernel<BF16, NC><<<(unsigned)grid, kBwdThreads, smem, st>>>(p, q, k, v, g);
+    msda_attention_tc_grad_query_kernel<BF16, NC><<<(unsigned)grid, bwd_threads(NC), smem, st>>>(p, q, k, v, g);
     return cudaGetLastError();
 }
 

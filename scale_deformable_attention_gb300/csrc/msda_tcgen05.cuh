@@ -97,6 +97,29 @@ __device__ __forceinline__ void tc_bulk(uint32_t dst, const void* src, uint32_t 
                  "r"(bytes), "r"(bar)
                  : "memory");
 }
+// the same from one lane (on = 1) of a converged warp
+__device__ __forceinline__ void tc_tma_5d_if(uint32_t on, uint32_t dst, const CUtensorMap* map, uint32_t bar, int c0, int c2, int c3,
+                                             int c4) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %7, 0;\n\t"
+        "@q cp.async.bulk.tensor.5d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, 0, %4, %5, %6}], "
+        "[%2];\n\t}" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c2), "r"(c3), "r"(c4), "r"(on)
+        : "memory");
+}
+__device__ __forceinline__ void tc_bulk_if(uint32_t on, uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %4, 0;\n\t"
+        "@q cp.async.bulk.shared::cta.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];\n\t}" ::"r"(dst),
+        "l"(src), "r"(bytes), "r"(bar), "r"(on)
+        : "memory");
+}
+__device__ __forceinline__ void tc_bar_expect_if(uint32_t on, uint32_t bar, uint32_t bytes) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %2, 0;\n\t@q mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n\t}" ::"r"(bar),
+        "r"(bytes), "r"(on)
+        : "memory");
+}
 __device__ __forceinline__ void tc_prefetch_map(const CUtensorMap* map) {
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
 }
