@@ -306,8 +306,8 @@ struct BackwardLayout {
 BackwardLayout backward_layout(msda_dtype dt, unsigned flags, const msda_attention_problem* p, bool tc) {
     BackwardLayout w;
     const int rt = tc ? msda::kTcRows : 64;
-    w.rows = {rt, rt, (int)((p->Q + rt - 1) / rt), (int)p->M, 1};
-    const size_t n = up((size_t)p->B * w.rows.N * w.rows.tiles * w.rows.rt * 8);
+    w.rows = {rt, (int)((p->Q + rt - 1) / rt), (int)p->M};
+    const size_t n = up((size_t)p->B * w.rows.heads * w.rows.tiles * w.rows.rt * 8);
     w.top = n;
     w.mask = n + 256;
     w.bytes = w.mask + mask_space(dt, flags, p).bytes;

@@ -41,12 +41,10 @@ struct AttentionArgs {
     unsigned* err;
 };
 
-// Rows of the backward's per-row statistics: tiles of `rt` rows, the G query
-// heads of a key head beside one another (row = (q - tile's first) * G + g).
-// A tile's l2 and delta lie side by side: [tile][rt], [rt].
+// The backward's per-row statistics: tiles of `rt` rows of a head; a tile's l2
+// and delta lie side by side: [B, heads, tiles][2][rt].
 struct AttentionRows {
-    int rt, qpt, tiles;  // rows a tile, queries a tile, tiles
-    int N, G;            // heads with rows of their own, heads sharing them
+    int rt, tiles, heads;
 };
 
 // f16 on the tensor cores: probabilities are held times 2^12 (at most 4096; what

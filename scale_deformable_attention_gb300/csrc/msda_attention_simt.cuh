@@ -352,7 +352,7 @@ __global__ void __launch_bounds__(kSimtThreads, simt_blocks(DP)) msda_attention_
             while (x < total && !simt_tile_seen(a, b, n * a.G + x / per, (qt0 + x % per) * 64, j0)) ++x;
         return x;
     };
-    auto stat_at = [&](int x) { return ((long long)(b * rw.N + n * a.G + x / per) * rw.tiles + qt0 + x % per) * 128; };
+    auto stat_at = [&](int x) { return ((long long)(b * rw.heads + n * a.G + x / per) * rw.tiles + qt0 + x % per) * 128; };
     // rows that take no part are cleared: their flags are written a tile ahead of the copies that ask for them
     auto flags = [&](int x) {
         if (threadIdx.x < 64) live[threadIdx.x] = a.row_l2[stat_at(x) + threadIdx.x] != -attn_inf();
@@ -447,7 +447,7 @@ __global__ void __launch_bounds__(kSimtThreads, simt_blocks(DP)) msda_attention_
     simt_load<T, DP>(Gs, static_cast<const T*>(a.dout) + (((long long)b * a.Q + q0) * a.M + m) * a.D,
                      (long long)a.M * a.D, a.Q - q0, a.D, vec, nullptr);
     float l2[8], dl[8], dq[8][DP / 16] = {};
-    const long long at0 = ((long long)(b * rw.N + m) * rw.tiles + q0 / 64) * 128;
+    const long long at0 = ((long long)(b * rw.heads + m) * rw.tiles + q0 / 64) * 128;
 #pragma unroll
     for (int i = 0; i < 8; ++i) l2[i] = a.row_l2[at0 + ty * 8 + i], dl[i] = a.row_dl[at0 + ty * 8 + i];
     const int tiles = simt_key_tiles(a, q0);
@@ -537,78 +537,80 @@ __global__ void __launch_bounds__(128) msda_attention_join_kernel(const Attentio
 }
 
 // Statistics of the backward's rows: `off` - lse in log2 units (-inf where the
-// row takes no part or is padding) and -<dout, out>.  Eight lanes a row.
+// row takes no part or is padding) and -<dout, out>.  A block takes a tile of
+// rows of a head, eight lanes a row.
 // With `top` (f16 on the tensor cores) also the largest squared norms of the
-// rows of dout that take part, top[0], and of the values that a query may see,
-// top[1]; cleared before, taken as bits: non-negative numbers are in the order
-// of their bits, so the order of the atomics changes nothing.
+// rows of dout that take part, top[0], and, over tiles of 128 keys behind the
+// rows' tiles, of the values that a query may see, top[1]; cleared before, taken
+// as bits: non-negative numbers are in the order of their bits, so the order of
+// the atomics changes nothing.
 template <typename T>
 __global__ void __launch_bounds__(256) msda_attention_prepare_kernel(const AttentionArgs a, const AttentionRows rw,
                                                                      const void* out_, const float* lse, float off,
                                                                      float* l2, float* top, bool vec) {
-    const long long rows = (long long)a.B * rw.N * rw.tiles * rw.rt;
-    const long long total = rows + (top ? (long long)a.B * a.S * a.N : 0);
-    const int lane = threadIdx.x & 7;
+    const int vtiles = (a.S + 127) / 128;
+    const long long tiles = (long long)a.B * rw.heads * rw.tiles;
+    const long long units = tiles + (top ? (long long)a.B * a.N * vtiles : 0);
+    const int lane = threadIdx.x & 7, group = threadIdx.x >> 3;
     float best_g = 0.f, best_v = 0.f;
-    for (long long i = (long long)blockIdx.x * 32 + (threadIdx.x >> 3); i < (total + 3) / 4 * 4; i += (long long)gridDim.x * 32) {
-        const T* g = nullptr;
-        const T* o = nullptr;
-        float x = 0.f;
-        if (i < rows) {
-            const long long bt = i / rw.rt;
-            const int r = (int)(i - bt * rw.rt);
-            const long long bn = bt / rw.tiles;
-            const int q = (int)(bt - bn * rw.tiles) * rw.qpt + r / rw.G;
-            const int b = (int)(bn / rw.N), m = (int)(bn - (long long)b * rw.N) * rw.G + r % rw.G;
-            if (r < rw.qpt * rw.G && q < a.Q) {
-                x = lse[((long long)b * a.M + m) * a.Q + q];
-                if (x != -attn_inf()) {
-                    const long long at = (((long long)b * a.Q + q) * a.M + m) * a.D;
-                    g = static_cast<const T*>(a.dout) + at;
-                    o = static_cast<const T*>(out_) + at;
-                }
-            }
-        } else if (i < total) {
-            const long long e = i - rows, bs = e / a.N, b = bs / a.S, j = bs - b * a.S;
-            const int n = (int)(e - bs * a.N);
-            if (!a.key_mask || a.key_mask[b * a.km_sb + n * a.km_sh + j])
-                g = static_cast<const T*>(a.v) + b * a.v_sb + j * a.v_ss + n * a.v_sh;
-        }
-        float d = 0.f, gg = 0.f;
-        if (g) {
-            if (sizeof(T) == 2 && vec) {  // rows of whole 16-byte vectors
-                for (int c = lane * 8; c < a.D; c += 64) {
-                    alignas(16) T gv[8], ov[8];
-                    *reinterpret_cast<uint4*>(gv) = *reinterpret_cast<const uint4*>(g + c);
-                    if (o) *reinterpret_cast<uint4*>(ov) = *reinterpret_cast<const uint4*>(o + c);
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) {
-                        const float y = attn_f32(gv[k]);
-                        gg = fmaf(y, y, gg);
-                        if (o) d = fmaf(y, attn_f32(ov[k]), d);
+    for (long long u = blockIdx.x; u < units; u += gridDim.x) {
+        const bool rows = u < tiles;
+        const long long e = rows ? u : u - tiles;
+        const int per = rows ? rw.tiles : vtiles, heads = rows ? rw.heads : a.N;
+        const long long bh = e / per, b = bh / heads;
+        const int t = (int)(e - bh * per), h = (int)(bh - b * heads), n = rows ? rw.rt : 128;
+        for (int r = group; r < n; r += 32) {  // n is a multiple of 32: whole warps stay together
+            const long long i = (long long)t * n + r;
+            const T* g = nullptr;
+            const T* o = nullptr;
+            float x = 0.f;
+            if (rows) {
+                if (i < a.Q) {
+                    x = lse[bh * a.Q + i];
+                    if (x != -attn_inf()) {
+                        const long long at = ((b * a.Q + i) * a.M + h) * a.D;
+                        g = static_cast<const T*>(a.dout) + at;
+                        o = static_cast<const T*>(out_) + at;
                     }
                 }
-            } else {
-                for (int c = lane; c < a.D; c += 8) {
-                    const float y = attn_f32(g[c]);
-                    gg = fmaf(y, y, gg);
-                    if (o) d = fmaf(y, attn_f32(o[c]), d);
+            } else if (i < a.S && (!a.key_mask || a.key_mask[b * a.km_sb + h * a.km_sh + i])) {
+                g = static_cast<const T*>(a.v) + b * a.v_sb + i * a.v_ss + h * a.v_sh;
+            }
+            float d = 0.f, gg = 0.f;
+            if (g) {
+                if (sizeof(T) == 2 && vec) {  // rows of whole 16-byte vectors
+                    for (int c = lane * 8; c < a.D; c += 64) {
+                        alignas(16) T gv[8], ov[8];
+                        *reinterpret_cast<uint4*>(gv) = *reinterpret_cast<const uint4*>(g + c);
+                        if (o) *reinterpret_cast<uint4*>(ov) = *reinterpret_cast<const uint4*>(o + c);
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) {
+                            const float y = attn_f32(gv[k]);
+                            gg = fmaf(y, y, gg);
+                            if (o) d = fmaf(y, attn_f32(ov[k]), d);
+                        }
+                    }
+                } else {
+                    for (int c = lane; c < a.D; c += 8) {
+                        const float y = attn_f32(g[c]);
+                        gg = fmaf(y, y, gg);
+                        if (o) d = fmaf(y, attn_f32(o[c]), d);
+                    }
                 }
             }
-        }
-        for (int s = 4; s > 0; s >>= 1) {
-            d += __shfl_xor_sync(0xffffffffu, d, s);
-            gg += __shfl_xor_sync(0xffffffffu, gg, s);
-        }
-        if (i < rows) {
-            if (lane == 0) {
-                const long long bt = i / rw.rt, at = bt * rw.rt + i;
-                l2[at] = g ? off - x * kLog2e : -attn_inf();
-                l2[at + rw.rt] = g ? -d : 0.f;
+            for (int s = 4; s > 0; s >>= 1) {
+                d += __shfl_xor_sync(0xffffffffu, d, s);
+                gg += __shfl_xor_sync(0xffffffffu, gg, s);
             }
-            best_g = gg > best_g || gg != gg ? gg : best_g;
-        } else {
-            best_v = gg > best_v || gg != gg ? gg : best_v;
+            if (rows) {
+                if (lane == 0) {
+                    l2[u * 2 * n + r] = g ? off - x * kLog2e : -attn_inf();
+                    l2[u * 2 * n + n + r] = g ? -d : 0.f;
+                }
+                best_g = gg > best_g || gg != gg ? gg : best_g;
+            } else {
+                best_v = gg > best_v || gg != gg ? gg : best_v;
+            }
         }
     }
     if (top) {
@@ -700,8 +702,8 @@ cudaError_t launch_attention_join(const AttentionArgs& a, cudaStream_t st) {
 template <typename T>
 cudaError_t launch_attention_prepare(const AttentionArgs& a, const AttentionRows& rw, const void* out, const float* lse,
                                      float off, float* l2, float* top, bool vec, cudaStream_t st) {
-    const long long blocks = ((long long)a.B * rw.N * rw.tiles * rw.rt + (top ? (long long)a.B * a.S * a.N : 0) + 31) / 32;
-    const unsigned grid = (unsigned)(blocks < 152 * 32 ? blocks : 152 * 32);
+    const long long units = (long long)a.B * rw.heads * rw.tiles + (top ? (long long)a.B * a.N * ((a.S + 127) / 128) : 0);
+    const unsigned grid = (unsigned)(units < 152 * 16 ? units : 152 * 16);
     msda_attention_prepare_kernel<T><<<grid, 256, 0, st>>>(a, rw, out, lse, off, l2, top, vec);
     return cudaGetLastError();
 }

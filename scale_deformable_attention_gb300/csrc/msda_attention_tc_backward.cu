@@ -685,8 +685,8 @@ __global__ void __launch_bounds__(bwd_threads(NC), 1)
                     if (++st == R) st = 0, ++wrap;
                 }
             }
-        } else if ((role == 1 || (Cfg::kAhead && role == 3)) && nt > 0) {
-            // ---- products ----
+        } else if ((role == 1 || role == 3) && nt > 0) {
+            // ---- products: scores, and dQ ----
             const uint32_t on = tc_elect();
             const int steps = (a.D + 15) / 16;
             const uint32_t id_s = tc_idesc(BF16, false, false, 128, 128), id_g = tc_idesc(BF16, false, true, 128, steps * 16);
@@ -755,34 +755,33 @@ __global__ void __launch_bounds__(bwd_threads(NC), 1)
                     if (ok) tc_commit(on, tc_smem(&sy.acc));
                 }
             } else {
-                int sv = 0, pv = 0;  // slot of V(i + 1) and its phase
-                auto pair = [&](int i) {  // dP = dO V^T, S = Q K^T of step i, tiles sv and the next
-                    const int sk = sv + 1 == R ? 0 : sv + 1, pk = sk == 0 ? pv ^ 1 : pv;
-                    ok = tc_bar_wait(tc_smem(&full[sv]), pv, abort, a.err) && tc_bar_wait(tc_smem(&full[sk]), pk, abort, a.err) &&
-                         (i == 0 || tc_bar_wait(tc_smem(&sy.dp_free), (i - 1) & 1, abort, a.err));
-                    if (!ok) return;
-                    tc_fence_after();
-                    scores(dp, do_desc, row_desc + sv * kTile);
-                    tc_commit(on, tc_smem(&sy.empty[sv]));
-                    scores(tmem, q_desc, row_desc + sk * kTile);
-                    tc_commit(on, tc_smem(&sy.s_full[0]));
-                    sv = sk + 1 == R ? 0 : sk + 1;
-                    pv = sv == 0 ? pk ^ 1 : pk;
-                };
-                ok = tc_bar_wait(tc_smem(&sy.own), 0, abort, a.err);
-                if (ok) pair(0);
-                int sk = 1;  // slot of K(i)
-                for (int i = 0; i < nt && ok; ++i) {
-                    if (i + 1 < nt) pair(i + 1);
-                    ok = ok && tc_bar_wait(tc_smem(&sy.ds_ready[i & 1]), (i >> 1) & 1, abort, a.err);
-                    if (!ok) break;
-                    tc_fence_after();
-                    gradient(tmem + Cfg::kDS + (i & 1) * 64, 16, col_desc + sk * kTile, i > 0);
-                    tc_commit(on, tc_smem(&sy.ds_done[i & 1]));
-                    tc_commit(on, tc_smem(&sy.empty[sk]));
-                    sk = sk + 2 >= R ? sk + 2 - R : sk + 2;
+                if (role == 1) {
+                    ok = tc_bar_wait(tc_smem(&sy.own), 0, abort, a.err);
+                    for (int i = 0, sv = 0, pv = 0; i < nt && ok; ++i) {  // slot and phase of V(i), then of K(i)
+                        const int sk = sv + 1 == R ? 0 : sv + 1, pk = sk == 0 ? pv ^ 1 : pv;
+                        ok = tc_bar_wait(tc_smem(&full[sv]), pv, abort, a.err) && tc_bar_wait(tc_smem(&full[sk]), pk, abort, a.err) &&
+                             (i == 0 || tc_bar_wait(tc_smem(&sy.dp_free), (i - 1) & 1, abort, a.err));
+                        if (!ok) break;
+                        tc_fence_after();
+                        scores(dp, do_desc, row_desc + sv * kTile);
+                        tc_commit(on, tc_smem(&sy.empty[sv]));
+                        scores(tmem, q_desc, row_desc + sk * kTile);
+                        tc_commit(on, tc_smem(&sy.s_full[0]));
+                        sv = sk + 1 == R ? 0 : sk + 1;
+                        pv = sv == 0 ? pk ^ 1 : pk;
+                    }
+                } else {
+                    for (int i = 0, sk = 1; i < nt; ++i) {  // slot of K(i)
+                        ok = tc_bar_wait(tc_smem(&sy.ds_ready[i & 1]), (i >> 1) & 1, abort, a.err);
+                        if (!ok) break;
+                        tc_fence_after();
+                        gradient(tmem + Cfg::kDS + (i & 1) * 64, 16, col_desc + sk * kTile, i > 0);
+                        tc_commit(on, tc_smem(&sy.ds_done[i & 1]));
+                        tc_commit(on, tc_smem(&sy.empty[sk]));
+                        sk = sk + 2 >= R ? sk + 2 - R : sk + 2;
+                    }
+                    if (ok) tc_commit(on, tc_smem(&sy.acc));
                 }
-                if (ok) tc_commit(on, tc_smem(&sy.acc));
             }
         } else if (role == 2 && km && nt > 0) {
             // ---- keys that take no part ----

@@ -36,7 +36,7 @@ constexpr float kSumLimit = 16384.f;  // a row's sum over a tile that asks for a
 
 template <int NQ, int NC>
 struct TcForwardCfg {
-    static constexpr int kStages = NC == 1 ? (NQ == 2 ? 8 : 4) : 4;  // ring of K and V tiles
+    static constexpr int kStages = NC == 1 ? 8 : 4;  // ring of K and V tiles
     static constexpr int kThreads = NQ * 128 + 128;
     static constexpr uint32_t kTileBytes = NC * kTcTile;
     // tensor memory: S (128 columns a row tile), P (64), O (64 or 128).  With
