@@ -258,7 +258,7 @@ template <typename T, int MODE, bool NORM, bool BWD>
 __device__ __forceinline__ void rotary_heads(const RotaryArgs& a, const RotaryTensor& t, int lg, long long token,
                                              const RotaryLane<Vec16<T>::N>& r, int h0, int h1, float* dw) {
     constexpr int V = Vec16<T>::N;
-    // rows worked on at once; as many more are loaded meanwhile (backward of 20
+    // rows worked on at once; with the norm as many more are loaded meanwhile (backward of 20
     // heads of 128: 438 us, 504 without the loads ahead, 467 with one row at once)
     constexpr int U = NORM ? 2 : 4;
     if (h0 >= h1) return;           // the same for the whole warp (no keys: their pointers are null)
@@ -301,16 +301,17 @@ __device__ __forceinline__ void rotary_heads(const RotaryArgs& a, const RotaryTe
             }
         }
     };
-    fetch(h0);
+    if constexpr (NORM) fetch(h0);  // the rotation alone: four rows at once (59 us a direction of the clip), 67 with loads ahead
 #pragma unroll 1
     for (int h = h0; h < h1; h += U) {
+        if constexpr (!NORM) fetch(h);
         uint4 xr[U], gr[BWD ? U : 1];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             xr[u] = xn[u];
             if constexpr (BWD) gr[u] = gn[u];
         }
-        if (h + U < h1) fetch(h + U);
+        if (NORM && h + U < h1) fetch(h + U);
         float rn[U];
         if constexpr (NORM) {
 #pragma unroll
