@@ -26,7 +26,7 @@ int chunk_tokens(int64_t B, int64_t S) {
     return 4;
 }
 
-msda_status check(msda_dtype dt, unsigned flags, const msda_rotary_problem* p, bool bwd) {
+msda_status check(msda_dtype dt, unsigned flags, const msda_rotary_problem* p) {
     using msda::failf;
     if (dt != MSDA_F32 && dt != MSDA_F16 && dt != MSDA_BF16) return failf(MSDA_ERR_INVALID_ARG, "unknown dtype %d", (int)dt);
     if (flags & ~(MSDA_ROTARY_INTERLEAVED | MSDA_ROTARY_INVERSE)) return failf(MSDA_ERR_INVALID_ARG, "unknown flags 0x%x", flags);
@@ -60,7 +60,6 @@ msda_status check(msda_dtype dt, unsigned flags, const msda_rotary_problem* p, b
         if (p->query_stride[i] < 0 || p->key_stride[i] < 0)
             return failf(MSDA_ERR_INVALID_ARG, "negative stride");
     if (p->position_stride < 0) return failf(MSDA_ERR_INVALID_ARG, "negative stride");
-    (void)bwd;
     return MSDA_OK;
 }
 
@@ -193,7 +192,7 @@ msda_status msda_norm_rotary_forward(msda_dtype dt, unsigned flags, const msda_r
                                      const void* key, const void* query_weight, const void* key_weight,
                                      void* query_out, void* key_out, msda_stream_t stream) {
     msda::clear_error();
-    msda_status s = check(dt, flags, problem, false);
+    msda_status s = check(dt, flags, problem);
     if (s != MSDA_OK) return s;
     const bool norm = query_weight || key_weight;
     if (norm && !(eps >= 0.0 && eps < 1e30)) return msda::failf(MSDA_ERR_INVALID_ARG, "eps=%g is not a non-negative number", eps);
@@ -208,7 +207,7 @@ msda_status msda_norm_rotary_backward(msda_dtype dt, unsigned flags, const msda_
                                       void* grad_key, void* grad_query_weight, void* grad_key_weight, void* workspace,
                                       size_t workspace_bytes, msda_stream_t stream) {
     msda::clear_error();
-    msda_status s = check(dt, flags, problem, true);
+    msda_status s = check(dt, flags, problem);
     if (s != MSDA_OK) return s;
     if (!(eps >= 0.0 && eps < 1e30)) return msda::failf(MSDA_ERR_INVALID_ARG, "eps=%g is not a non-negative number", eps);
     if (flags & MSDA_ROTARY_INVERSE)
