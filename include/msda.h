@@ -480,7 +480,8 @@ enum { MSDA_KERNEL_FORWARD = 0, MSDA_KERNEL_BACKWARD = 1, MSDA_KERNEL_ZERO = 2, 
        MSDA_KERNEL_TILE_ACCUM = 7, MSDA_KERNEL_TOUCH = 8,
        MSDA_KERNEL_ROTARY = 9, MSDA_KERNEL_ROTARY_BACKWARD = 10, MSDA_KERNEL_ATTENTION = 11,
        MSDA_KERNEL_ATTENTION_JOIN = 12, MSDA_KERNEL_ATTENTION_MASK = 13, MSDA_KERNEL_ATTENTION_PREPARE = 14,
-       MSDA_KERNEL_ATTENTION_GRAD_KEY = 15, MSDA_KERNEL_ATTENTION_GRAD_QUERY = 16, MSDA_KERNEL_COUNT = 17 };
+       MSDA_KERNEL_ATTENTION_GRAD_KEY = 15, MSDA_KERNEL_ATTENTION_GRAD_QUERY = 16,
+       MSDA_KERNEL_ATTENTION_SPLIT = 17, MSDA_KERNEL_COUNT = 18 };
 
 msda_status msda_trace_enable(int capacity);
 /* Pause (paused != 0) or resume recording without destroying the events:

@@ -23,7 +23,7 @@ BWD_WORKSPACE_ZEROED = 2
 KERNEL_NAMES = {0: "forward", 1: "backward", 2: "zero", 3: "convert", 4: "tile_count", 5: "tile_scan",
                 6: "tile_place", 7: "tile_accum", 8: "touch_count", 9: "rotary", 10: "rotary_backward", 11: "attention",
                 12: "attention_join", 13: "attention_mask", 14: "attention_prepare", 15: "attention_grad_key",
-                16: "attention_grad_query"}
+                16: "attention_grad_query", 17: "attention_split"}
 ROTARY_INTERLEAVED = 1
 ROTARY_INVERSE = 2
 ATTENTION_CAUSAL = 1

@@ -832,6 +832,7 @@ const char* msda_kernel_name(int k) {
     case MSDA_KERNEL_ATTENTION_PREPARE: return "attention_prepare";
     case MSDA_KERNEL_ATTENTION_GRAD_KEY: return "attention_grad_key";
     case MSDA_KERNEL_ATTENTION_GRAD_QUERY: return "attention_grad_query";
+    case MSDA_KERNEL_ATTENTION_SPLIT: return "attention_split";
     }
     return "unknown";
 }

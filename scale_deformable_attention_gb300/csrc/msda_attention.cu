@@ -75,6 +75,33 @@ bool tc_type(msda_dtype dt, const msda_attention_problem* p) {
     return dt != MSDA_F32 && p->D % 8 == 0 && p->M / p->N <= 128 && p->S > 0;
 }
 
+// binary32 that the tensor cores take in three bf16 pieces, whatever its
+// addresses and strides: up to 64 channels (an operand's pieces of a tile take
+// 48 KB), and enough pairs to pay for the cutting.  Against the FMA pipe, all
+// launches in one graph, 8 heads: forward 22 : 15 us at 300 x 300 and 27 : 17 at 900 x 900 of one
+// head, 25 : 34 at four times 300 x 300, 35 : 49 at 64 x 4000 and 45 : 128 at 1 x 20000 (FMA-pipe blocks take 64 rows, which
+// the count rounds up to; 64 keys fill half a tile: 45 : 21 at 64 times 64 x 64).  Backward: 59 : 81 us at 64 times 64 x 64
+// against 31 : 38 at 100 x 100, 49 : 81 at 300 x 300, 202 : 901 at 4000 x 64.
+bool tc_pieces(msda_dtype dt, const msda_attention_problem* p, bool backward) {
+    if (dt != MSDA_F32 || p->D > 64 || p->M / p->N > 128 || p->S == 0) return false;
+    if (backward) return p->Q > 64 || p->S > 64;
+    return p->S > 64 && p->B * p->M * ((p->Q + 63) / 64) * ((p->S + 63) / 64) >= 3 << 7;  // tiles of 64 x 64
+}
+
+// The pieces in the workspace: the flag, then query, key, value and (backward) the output's gradient.
+struct PieceSpace {
+    int Dp;
+    size_t q, k, v, g, bytes;
+};
+PieceSpace piece_space(const msda_attention_problem* p, bool backward) {
+    PieceSpace s;
+    s.Dp = (int)((p->D + 7) / 8 * 8);
+    const size_t rows = up((size_t)p->B * p->Q * p->M * s.Dp * 6), keys = up((size_t)p->B * p->S * p->N * s.Dp * 6);
+    s.q = 256, s.k = s.q + rows, s.v = s.k + keys, s.g = s.v + keys;
+    s.bytes = s.g + (backward ? rows : 0);
+    return s;
+}
+
 msda_status check(msda_dtype dt, unsigned flags, const msda_attention_problem* p) {
     if (dt != MSDA_F32 && dt != MSDA_F16 && dt != MSDA_BF16) return failf(MSDA_ERR_INVALID_ARG, "unknown dtype %d", (int)dt);
     if (flags & ~kFlags) return failf(MSDA_ERR_INVALID_ARG, "unknown flags 0x%x", flags);
@@ -113,7 +140,7 @@ struct MaskSpace {
     int Bm = 1, Mm = 1, LB = 1, LN = 1, W = 0, Wq = 0;
     size_t bits = 0, bits_t = 0, bytes = 0;  // offsets of the bits behind the liveness
 };
-MaskSpace mask_space(msda_dtype dt, unsigned flags, const msda_attention_problem* p) {
+MaskSpace mask_space(unsigned flags, const msda_attention_problem* p, bool by_key) {
     MaskSpace l;
     if (!(flags & MSDA_ATTENTION_MASK)) return l;
     l.Bm = p->B > 1 && p->mask_stride[0] != 0 ? (int)p->B : 1;
@@ -125,7 +152,7 @@ MaskSpace mask_space(msda_dtype dt, unsigned flags, const msda_attention_problem
     l.bits = up((size_t)l.LB * l.LN * (size_t)p->S);
     l.bits_t = l.bits + up((size_t)l.Bm * l.Mm * p->Q * l.W * 4);
     l.bytes = l.bits_t;
-    if (tc_type(dt, p)) l.bytes += up((size_t)l.Bm * l.Mm * p->S * l.Wq * 4);
+    if (by_key) l.bytes += up((size_t)l.Bm * l.Mm * p->S * l.Wq * 4);
     return l;
 }
 
@@ -137,7 +164,7 @@ struct ForwardPlan {
 // so that a single query over a long key axis uses the whole GPU.
 // 16-bit tensors that come here for their addresses alone split no further than
 // the tensor-core form would, so that the workspace is that form's.
-ForwardPlan forward_plan(const msda_attention_problem* p);
+ForwardPlan forward_plan(const msda_attention_problem* p, int most_tiles = 2);
 void simt_splits(msda_dtype dt, const msda_attention_problem* p, int* splits, int* per) {
     const int64_t blocks = p->B * p->M * ((p->Q + 63) / 64), tiles = (p->S + 63) / 64;
     int64_t n = 1;
@@ -260,14 +287,14 @@ bool tma_rows(const void* p, const int64_t* stride, int64_t B, int64_t rows, int
 // would leave SMs without a block, or where the last round of blocks eats the gain.  A key axis of many tiles is split until
 // every SM has a block, but not into pieces of less than four tiles: a piece
 // costs a launch's start and the joining of its rows.
-ForwardPlan forward_plan(const msda_attention_problem* p) {
+ForwardPlan forward_plan(const msda_attention_problem* p, int most_tiles) {
     ForwardPlan f;
     f.G = (int)(p->M / p->N);
     f.qpt = msda::kTcRows / f.G;
     const int64_t one = (p->Q + f.qpt - 1) / f.qpt, two = (p->Q + 2 * f.qpt - 1) / (2 * f.qpt);
     // rounds of blocks, one an SM; a step of two tiles takes about three halves of a step of one
     const int64_t heads = p->B * p->N, rounds1 = (heads * one + kSms - 1) / kSms, rounds2 = (heads * two + kSms - 1) / kSms;
-    f.nq = heads * two >= kSms && 3 * rounds2 <= 2 * rounds1 ? 2 : 1;
+    f.nq = most_tiles == 2 && heads * two >= kSms && 3 * rounds2 <= 2 * rounds1 ? 2 : 1;
     f.qblocks = (int)(f.nq == 2 ? two : one);
     const int64_t blocks = p->B * p->N * f.qblocks, tiles = (p->S + msda::kTcRows - 1) / msda::kTcRows;
     int64_t n = blocks > 0 ? kSms / blocks : 1;
@@ -287,6 +314,13 @@ bool simt_vec(const AttentionArgs& a) {  // binary32 rows read as 16-byte vector
            msda::aligned_to(a.dout, 16);
 }
 
+// A tensor's three pieces: boxes of `box_rows` rows of `group` heads.
+bool piece_map(const msda_attention_problem* p, const void* base, int group, int64_t rows, int64_t heads, int box_rows,
+               CUtensorMap* map) {
+    const int64_t Dp = (p->D + 7) / 8 * 8, row = heads * group * Dp;
+    return rows_map(MSDA_BF16, base, Dp, group, rows, heads, 3 * p->B, rows * row, row, Dp, box_rows, map);
+}
+
 #define MSDA_BY_DTYPE(dt, f, ...)                       \
     ((dt) == MSDA_F32   ? msda::f<float>(__VA_ARGS__)   \
      : (dt) == MSDA_F16 ? msda::f<__half>(__VA_ARGS__)  \
@@ -296,12 +330,32 @@ msda_status launched(cudaError_t e, const char* what) {
     return e == cudaSuccess ? MSDA_OK : failf(MSDA_ERR_CUDA, "%s: %s (%s)", what, cudaGetErrorString(e), cudaGetErrorName(e));
 }
 
+// Clears the flag and cuts the tensors; a.key_mask (and, backward, lse) say which rows take part.
+msda_status make_pieces(AttentionArgs& a, const msda_attention_problem* p, const float* lse, unsigned char* ws, cudaStream_t st) {
+    const PieceSpace w = piece_space(p, a.dout != nullptr);
+    unsigned* odd = reinterpret_cast<unsigned*>(ws);
+    msda::SplitArgs s{};
+    const bool vec = simt_vec(a);
+    auto f = [](const void* x) { return static_cast<const float*>(x); };
+    s.t[0] = {f(a.q), a.q_sb, a.q_ss, a.q_sh, a.Q, a.M, vec, nullptr, 0, 0, lse, ws + w.q};
+    s.t[1] = {f(a.k), a.k_sb, a.k_ss, a.k_sh, a.S, a.N, vec, a.key_mask, a.km_sb, a.km_sh, nullptr, ws + w.k};
+    s.t[2] = {f(a.v), a.v_sb, a.v_ss, a.v_sh, a.S, a.N, vec, a.key_mask, a.km_sb, a.km_sh, nullptr, ws + w.v};
+    s.t[3] = {f(a.dout), (long long)a.Q * a.M * a.D, (long long)a.M * a.D, a.D, a.Q, a.M, vec, nullptr, 0, 0, lse, ws + w.g};
+    s.B = a.B, s.D = a.D, s.Dp = w.Dp, s.odd = odd;
+    a.odd = odd;
+    msda::TraceSpan ts(st);
+    cudaError_t e = cudaMemsetAsync(odd, 0, 4, st);
+    if (e == cudaSuccess) e = msda::launch_attention_split(s, a.dout ? 4 : 3, st);
+    ts.end(MSDA_KERNEL_ATTENTION_SPLIT, p->B * p->M * p->Q);
+    return launched(e, "attention split kernel launch");
+}
+
 // Workspace of the backward: the rows' statistics, f16's norms, the mask.
 // Row tiles are 128 rows on the tensor cores, 64 on the FMA pipe; which runs
 // depends on the addresses, and 128 needs as much space or more.
 struct BackwardLayout {
     AttentionRows rows;
-    size_t l2 = 0, top = 0, mask = 0, bytes = 0;
+    size_t l2 = 0, top = 0, mask = 0, pieces = 0, bytes = 0;
 };
 BackwardLayout backward_layout(msda_dtype dt, unsigned flags, const msda_attention_problem* p, bool tc) {
     BackwardLayout w;
@@ -310,7 +364,8 @@ BackwardLayout backward_layout(msda_dtype dt, unsigned flags, const msda_attenti
     const size_t n = up((size_t)p->B * w.rows.heads * w.rows.tiles * w.rows.rt * 8);
     w.top = n;
     w.mask = n + 256;
-    w.bytes = w.mask + mask_space(dt, flags, p).bytes;
+    w.pieces = w.mask + mask_space(flags, p, tc_type(dt, p) || tc_pieces(dt, p, true)).bytes;
+    w.bytes = w.pieces + (tc_pieces(dt, p, true) ? piece_space(p, true).bytes : 0);
     return w;
 }
 
@@ -323,12 +378,14 @@ size_t msda_attention_forward_workspace_size(msda_dtype dt, unsigned flags, cons
     int splits, per;
     simt_splits(dt, p, &splits, &per);
     if (tc_type(dt, p)) splits = forward_plan(p).splits;  // which of the two runs depends on the addresses
-    return part_bytes(p, splits) + mask_space(dt, flags, p).bytes;
+    size_t pieces = 0;
+    if (tc_pieces(dt, p, false)) splits = forward_plan(p, 1).splits, pieces = piece_space(p, false).bytes;
+    return part_bytes(p, splits) + mask_space(flags, p, false).bytes + pieces;
 }
 
 size_t msda_attention_backward_workspace_size(msda_dtype dt, unsigned flags, const msda_attention_problem* p) {
     if (check(dt, flags, p) != MSDA_OK) return 0;
-    return backward_layout(dt, flags, p, tc_type(dt, p)).bytes;
+    return backward_layout(dt, flags, p, tc_type(dt, p) || tc_pieces(dt, p, true)).bytes;
 }
 
 msda_status msda_attention_forward(msda_dtype dt, unsigned flags, const msda_attention_problem* p, double scale,
@@ -355,12 +412,13 @@ msda_status msda_attention_forward(msda_dtype dt, unsigned flags, const msda_att
     const bool tc = tc_type(dt, p) && tma_rows(query, p->query_stride, p->B, p->Q, p->M) &&
                     tma_rows(key, p->key_stride, p->B, p->S, p->N) && tma_rows(value, p->value_stride, p->B, p->S, p->N) &&
                     msda::aligned_to(out, 16);
-    const MaskSpace ms = mask_space(dt, flags, p);
+    const MaskSpace ms = mask_space(flags, p, false);
     msda::TcArgs t{};
-    if ((s = make_mask(a, ms, workspace, tc ? &t : nullptr, st)) != MSDA_OK) return s;
+    const bool pieces = tc_pieces(dt, p, false);
+    if ((s = make_mask(a, ms, workspace, nullptr, st)) != MSDA_OK) return s;
     ForwardPlan f{};
-    if (tc) {
-        f = forward_plan(p);
+    if (tc || pieces) {
+        f = forward_plan(p, pieces ? 1 : 2);
         a.splits = f.splits, a.tiles_per_split = f.per;
     } else {
         simt_splits(dt, p, &a.splits, &a.tiles_per_split);
@@ -370,7 +428,25 @@ msda_status msda_attention_forward(msda_dtype dt, unsigned flags, const msda_att
         a.part_o = reinterpret_cast<float*>(part);
         a.part_lse = reinterpret_cast<float*>(part + up((size_t)a.splits * p->B * p->M * p->Q * p->D * 4));
     }
-    if (tc) {
+    if (pieces) {
+        int sms;
+        if ((s = msda::device_facts(&a.err, &sms)) != MSDA_OK) return s;
+        unsigned char* ws = static_cast<unsigned char*>(workspace) + ms.bytes + part_bytes(p, a.splits);
+        if ((s = make_pieces(a, p, nullptr, ws, st)) != MSDA_OK) return s;
+        const PieceSpace w = piece_space(p, false);
+        CUtensorMap mq, mk, mv;
+        if (!piece_map(p, ws + w.q, f.G, p->Q, p->N, f.qpt, &mq) || !piece_map(p, ws + w.k, 1, p->S, p->N, msda::kTcRows, &mk) ||
+            !piece_map(p, ws + w.v, 1, p->S, p->N, msda::kTcRows, &mv))
+            return failf(MSDA_ERR_CUDA, "cuTensorMapEncodeTiled failed");
+        t.a = a;
+        t.G = f.G, t.qpt = f.qpt, t.rows = f.G * f.qpt, t.qblocks = f.qblocks;
+        msda::TraceSpan ts(st);
+        cudaError_t e = msda::launch_attention_tc_f32(t, mq, mk, mv, st);
+        a.tiles_per_split *= 2;  // of 64 keys
+        if (e == cudaSuccess) e = msda::launch_attention_simt<float>(a, simt_vec(a), st);
+        s = launched(e, "attention kernel launch");
+        ts.end(MSDA_KERNEL_ATTENTION, p->B * p->M * p->Q);
+    } else if (tc) {
         int sms;
         if ((s = msda::device_facts(&a.err, &sms)) != MSDA_OK) return s;
         CUtensorMap mq, mk, mv;
@@ -427,7 +503,8 @@ msda_status msda_attention_backward(msda_dtype dt, unsigned flags, const msda_at
                     msda::aligned_to(grad_out, 16) && msda::aligned_to(grad_query, 16) && msda::aligned_to(grad_key, 16) &&
                     msda::aligned_to(grad_value, 16);
     const size_t need = msda_attention_backward_workspace_size(dt, flags, p);
-    const BackwardLayout w = backward_layout(dt, flags, p, tc);
+    const bool pieces = tc_pieces(dt, p, true);
+    const BackwardLayout w = backward_layout(dt, flags, p, tc || pieces);
     if (!workspace || workspace_bytes < need || !msda::aligned_to(workspace, 256))
         return failf(MSDA_ERR_WORKSPACE, "workspace of %zu bytes, 256-byte aligned, needed (got %zu)", need,
                      workspace_bytes);
@@ -438,7 +515,7 @@ msda_status msda_attention_backward(msda_dtype dt, unsigned flags, const msda_at
     float* dl = l2 + w.rows.rt;
     a.row_l2 = l2, a.row_dl = dl;
     msda::TcArgs t{};
-    if ((s = make_mask(a, mask_space(dt, flags, p), ws + w.mask, tc ? &t : nullptr, st)) != MSDA_OK) return s;
+    if ((s = make_mask(a, mask_space(flags, p, tc || pieces), ws + w.mask, tc || pieces ? &t : nullptr, st)) != MSDA_OK) return s;
     {
         msda::TraceSpan ts(st);
         const bool half = tc && dt == MSDA_F16;
@@ -478,6 +555,32 @@ msda_status msda_attention_backward(msda_dtype dt, unsigned flags, const msda_at
                      "attention key gradient kernel launch");
         ts.end(MSDA_KERNEL_ATTENTION_GRAD_KEY, p->B * p->N * p->S);
         return s;
+    }
+    if (pieces) {
+        int sms;
+        if ((s = msda::device_facts(&a.err, &sms)) != MSDA_OK) return s;
+        unsigned char* at = ws + w.pieces;
+        if ((s = make_pieces(a, p, lse, at, st)) != MSDA_OK) return s;
+        const PieceSpace x = piece_space(p, true);
+        CUtensorMap mq, mk, mv, mg;
+        if (!piece_map(p, at + x.q, 1, p->Q, p->M, msda::kTcRows, &mq) || !piece_map(p, at + x.k, 1, p->S, p->N, msda::kTcRows, &mk) ||
+            !piece_map(p, at + x.v, 1, p->S, p->N, msda::kTcRows, &mv) || !piece_map(p, at + x.g, 1, p->Q, p->M, msda::kTcRows, &mg))
+            return failf(MSDA_ERR_CUDA, "cuTensorMapEncodeTiled failed");
+        t.a = a;
+        t.G = 1, t.qpt = t.rows = msda::kTcRows, t.qblocks = w.rows.tiles;
+        {
+            msda::TraceSpan ts(st);
+            cudaError_t e = msda::launch_attention_tc_f32_grad_key(t, mq, mk, mv, mg, st);
+            if (e == cudaSuccess) e = msda::launch_attention_simt_grad_key<float>(a, w.rows, simt_vec(a), st);
+            s = launched(e, "attention key gradient kernel launch");
+            ts.end(MSDA_KERNEL_ATTENTION_GRAD_KEY, p->B * p->N * p->S);
+            if (s != MSDA_OK) return s;
+        }
+        msda::TraceSpan ts(st);
+        cudaError_t e = msda::launch_attention_tc_f32_grad_query(t, mq, mk, mv, mg, st);
+        if (e == cudaSuccess) e = msda::launch_attention_simt_grad_query<float>(a, w.rows, simt_vec(a), st);
+        ts.end(MSDA_KERNEL_ATTENTION_GRAD_QUERY, p->B * p->M * p->Q);
+        return launched(e, "attention query gradient kernel launch");
     }
     {
         msda::TraceSpan ts(st);

@@ -39,6 +39,7 @@ struct AttentionArgs {
     const float* row_dl;  // -delta, delta = sum_d dout * out of the kernels' rows
     void *dq, *dk, *dv;   // [B, Q, M, D], [B, S, N, D], [B, S, N, D]
     unsigned* err;
+    const unsigned* odd;  // binary32 on the tensor cores: where set those kernels return, else the FMA pipe's behind them; null: no such pair
 };
 
 // The backward's per-row statistics: tiles of `rt` rows of a head; a tile's l2

@@ -1,9 +1,9 @@
 // msda_attention_simt.cuh -- softmax attention and its gradients on the FMA
 // pipe: every dtype, every D up to 128, every alignment.
 //
-// binary32 tensors run here whatever their size (the tensor pipe has no
-// binary32 product: its tf32 form keeps 11 bits), and 16-bit tensors whose
-// rows or strides are not made of 16-byte vectors.
+// binary32 tensors run here where the tensor cores do not take them in pieces
+// (more than 64 channels, small calls, values beyond the pieces' range), and
+// 16-bit tensors whose rows or strides are not made of 16-byte vectors.
 //
 // A block takes 64 rows against tiles of 64 others; 128 threads, each 8 x 4
 // scores and 8 x D/16 outputs in registers.  Per 4 channels a thread reads
@@ -197,10 +197,19 @@ __device__ __forceinline__ int simt_key_tiles(const AttentionArgs& a, int q0) {
     return (int)((last + 63) / 64);
 }
 
+// Statistics of a head's rows from q0 on (a multiple of 64) in tiles of rw.rt rows.
+__device__ __forceinline__ long long simt_stat(const AttentionRows& rw, long long head, int q0) {
+    return (head * rw.tiles + q0 / rw.rt) * 2 * rw.rt + q0 % rw.rt;
+}
+
+// binary32 behind the tensor cores' kernels, which did the work unless a value was not fit for them
+__device__ __forceinline__ bool simt_done(const AttentionArgs& a) { return a.odd && !*a.odd; }
+
 // Forward: running maximum m and sum l of each row, O rescaled when m grows.
 template <typename T, int DP>
 __global__ void __launch_bounds__(kSimtThreads, simt_blocks(DP)) msda_attention_simt_kernel(const AttentionArgs a, bool vec) {
     extern __shared__ __align__(16) float simt_smem[];
+    if (simt_done(a)) return;
     constexpr int LD = DP + 4;
     float* Qs = simt_smem;
     float* Ks = Qs + kSimtRows * LD;
@@ -323,6 +332,7 @@ template <typename T, int DP>
 __global__ void __launch_bounds__(kSimtThreads, simt_blocks(DP)) msda_attention_simt_grad_key_kernel(const AttentionArgs a,
                                                                                     const AttentionRows rw, bool vec) {
     extern __shared__ __align__(16) float simt_smem[];
+    if (simt_done(a)) return;
     constexpr int LD = DP + 4;
     float* Ks = simt_smem;
     float* Vs = Ks + kSimtRows * LD;
@@ -352,7 +362,7 @@ __global__ void __launch_bounds__(kSimtThreads, simt_blocks(DP)) msda_attention_
             while (x < total && !simt_tile_seen(a, b, n * a.G + x / per, (qt0 + x % per) * 64, j0)) ++x;
         return x;
     };
-    auto stat_at = [&](int x) { return ((long long)(b * rw.heads + n * a.G + x / per) * rw.tiles + qt0 + x % per) * 128; };
+    auto stat_at = [&](int x) { return simt_stat(rw, (long long)b * rw.heads + n * a.G + x / per, (qt0 + x % per) * 64); };
     // rows that take no part are cleared: their flags are written a tile ahead of the copies that ask for them
     auto flags = [&](int x) {
         if (threadIdx.x < 64) live[threadIdx.x] = a.row_l2[stat_at(x) + threadIdx.x] != -attn_inf();
@@ -427,6 +437,7 @@ template <typename T, int DP>
 __global__ void __launch_bounds__(kSimtThreads, simt_blocks(DP)) msda_attention_simt_grad_query_kernel(const AttentionArgs a,
                                                                                       const AttentionRows rw, bool vec) {
     extern __shared__ __align__(16) float simt_smem[];
+    if (simt_done(a)) return;
     constexpr int LD = DP + 4;
     float* Qs = simt_smem;
     float* Gs = Qs + kSimtRows * LD;
@@ -447,7 +458,7 @@ __global__ void __launch_bounds__(kSimtThreads, simt_blocks(DP)) msda_attention_
     simt_load<T, DP>(Gs, static_cast<const T*>(a.dout) + (((long long)b * a.Q + q0) * a.M + m) * a.D,
                      (long long)a.M * a.D, a.Q - q0, a.D, vec, nullptr);
     float l2[8], dl[8], dq[8][DP / 16] = {};
-    const long long at0 = ((long long)(b * rw.heads + m) * rw.tiles + q0 / 64) * 128;
+    const long long at0 = simt_stat(rw, (long long)b * rw.heads + m, q0);
 #pragma unroll
     for (int i = 0; i < 8; ++i) l2[i] = a.row_l2[at0 + ty * 8 + i], dl[i] = a.row_dl[at0 + ty * 8 + i];
     const int tiles = simt_key_tiles(a, q0);
