@@ -34,12 +34,12 @@ __device__ constexpr int kPairA[kPairs] = {1, 0, 2, 0, 1, 0}, kPairB[kPairs] = {
 
 // The pieces of two finite values, side by side.
 __device__ __forceinline__ void pieces(float x, float y, uint32_t& p0, uint32_t& p1, uint32_t& p2) {
+    const uint64_t minus = tc_two(-1.f, -1.f);
     p0 = __byte_perm(__float_as_uint(x), __float_as_uint(y), 0x7632);
-    x -= __uint_as_float(__float_as_uint(x) & 0xffff0000u);
-    y -= __uint_as_float(__float_as_uint(y) & 0xffff0000u);
+    const uint64_t r = tc_fma2(tc_two(__uint_as_float(p0 << 16), __uint_as_float(p0 & 0xffff0000u)), minus, tc_two(x, y));
+    tc_split(r, x, y);
     p1 = tc_pack<true>(x, y);
-    x -= __uint_as_float(p1 << 16);
-    y -= __uint_as_float(p1 & 0xffff0000u);
+    tc_split(tc_fma2(tc_two(__uint_as_float(p1 << 16), __uint_as_float(p1 & 0xffff0000u)), minus, r), x, y);
     p2 = tc_pack<true>(x, y);
 }
 // 16 values' pieces into tensor memory, 8 columns each at a, b and c
@@ -151,7 +151,7 @@ struct TcF32Forward {
     static constexpr uint32_t kP = 256, kO = 448;  // tensor memory: S twice, P in three pieces of 64, O
 };
 struct TcF32ForwardSync {
-    uint64_t q_full, full[3], empty[3], s_full[2], p_full, pv_done;
+    uint64_t q_full, full[3], empty[3], s_full[2], s_free[2], p_full, pv_done;
     uint32_t tmem, abort;
 };
 
@@ -188,7 +188,10 @@ __global__ void __launch_bounds__(256, 1)
                 tc_bar_init(tc_smem(&sy.empty[i]), 1);
             }
             tc_bar_init(tc_smem(&sy.q_full), 1);
-            for (int i = 0; i < 2; ++i) tc_bar_init(tc_smem(&sy.s_full[i]), 1);
+            for (int i = 0; i < 2; ++i) {
+                tc_bar_init(tc_smem(&sy.s_full[i]), 1);
+                tc_bar_init(tc_smem(&sy.s_free[i]), 4);
+            }
             tc_bar_init(tc_smem(&sy.p_full), 4);
             tc_bar_init(tc_smem(&sy.pv_done), 1);
             sy.abort = 0;
@@ -287,6 +290,8 @@ __global__ void __launch_bounds__(256, 1)
                 sum = probabilities();
             }
             l += sum;
+            tc_fence_before();
+            tc_bar_arrive_if(first, tc_smem(&sy.s_free[i & 1]));
             if (i > 0) {  // P(i-1) is used up, and O holds its product
                 ok = tc_bar_wait(tc_smem(&sy.pv_done), (i - 1) & 1, abort, a.err);
                 if (!ok) break;
@@ -301,7 +306,7 @@ __global__ void __launch_bounds__(256, 1)
             for (int c = 0; c < 8; ++c) store_pieces(&e[c >> 1][(c & 1) * 16], p_at + c * 8, p_at + 64 + c * 8, p_at + 128 + c * 8);
             tmem_wait_st();
             tc_fence_before();
-            tc_bar_arrive_if(first, tc_smem(&sy.p_full));  // S(i) is done with too
+            tc_bar_arrive_if(first, tc_smem(&sy.p_full));
         }
         if (nt > 0 && ok) {
             ok = tc_bar_wait(tc_smem(&sy.pv_done), (nt - 1) & 1, abort, a.err);
@@ -332,7 +337,7 @@ __global__ void __launch_bounds__(256, 1)
                 tc_bar_expect_if(on, bar, kPieces);
                 load_pieces(on, tc_smem(ring) + st * kPieces, (x & 1) ? &map_v : &map_k, bar, (t0 + (x >> 1)) * kTcRows, n, b, a.B);
             }
-        } else if (role == 1 && nt > 0) {
+        } else if ((role == 1 || role == 2) && nt > 0) {  // scores; outputs
             const uint32_t on = tc_elect();
             const int steps = (a.D + 15) / 16;
             const uint32_t id_s = tc_idesc(true, false, false, 128, 128), id_o = tc_idesc(true, false, true, 128, steps * 16);
@@ -341,32 +346,32 @@ __global__ void __launch_bounds__(256, 1)
             for (int k = 0; k < 4; ++k) step_on[k] = k < steps ? on : 0u;
             const uint64_t q_desc = tc_desc(tc_smem(q_tile), 16, 1024);
             auto filled = [&](int x) { return tc_bar_wait(tc_smem(&sy.full[x % R]), (x / R) & 1, abort, a.err); };
-            auto product_s = [&](int i) {
-                ok = filled(2 * i);
-                if (!ok) return;
-                tc_fence_after();
-                products_nt(step_on, tmem + (i & 1) * 128, q_desc, tc_desc(tc_smem(ring) + (2 * i % R) * kPieces, 16, 1024), id_s);
-                tc_commit(on, tc_smem(&sy.s_full[i & 1]));
-                tc_commit(on, tc_smem(&sy.empty[2 * i % R]));
-            };
-            ok = tc_bar_wait(tc_smem(&sy.q_full), 0, abort, a.err);
-            if (ok) product_s(0);
-            if (ok && nt > 1) product_s(1);
-            for (int i = 0; i < nt && ok; ++i) {
-                const int x = 2 * i + 1;
-                ok = filled(x) && tc_bar_wait(tc_smem(&sy.p_full), i & 1, abort, a.err);
-                if (!ok) break;
-                tc_fence_after();
-                const uint64_t v_desc = tc_desc(tc_smem(ring) + (x % R) * kPieces, kTcTile, 1024);
+            if (role == 1) {
+                ok = tc_bar_wait(tc_smem(&sy.q_full), 0, abort, a.err);
+                for (int i = 0; i < nt && ok; ++i) {
+                    ok = filled(2 * i) && (i < 2 || tc_bar_wait(tc_smem(&sy.s_free[i & 1]), ((i >> 1) - 1) & 1, abort, a.err));
+                    if (!ok) break;
+                    tc_fence_after();
+                    products_nt(step_on, tmem + (i & 1) * 128, q_desc, tc_desc(tc_smem(ring) + (2 * i % R) * kPieces, 16, 1024), id_s);
+                    tc_commit(on, tc_smem(&sy.s_full[i & 1]));
+                    tc_commit(on, tc_smem(&sy.empty[2 * i % R]));
+                }
+            } else {
+                for (int i = 0; i < nt; ++i) {
+                    const int x = 2 * i + 1;
+                    ok = filled(x) && tc_bar_wait(tc_smem(&sy.p_full), i & 1, abort, a.err);
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint64_t v_desc = tc_desc(tc_smem(ring) + (x % R) * kPieces, kTcTile, 1024);
 #pragma unroll
-                for (int e = 0; e < kPairs; ++e)
+                    for (int e = 0; e < kPairs; ++e)
 #pragma unroll
-                    for (int k = 0; k < 8; ++k)
-                        tc_mma_ts(on, tmem + Cfg::kO, tmem + Cfg::kP + kPairA[e] * 64 + k * 8,
-                                  v_desc + ((kPairB[e] * kTcTile + k * 2048) >> 4), id_o, e > 0 || k > 0);
-                tc_commit(on, tc_smem(&sy.pv_done));
-                tc_commit(on, tc_smem(&sy.empty[x % R]));
-                if (i + 2 < nt) product_s(i + 2);  // over S(i)
+                        for (int k = 0; k < 8; ++k)
+                            tc_mma_ts(on, tmem + Cfg::kO, tmem + Cfg::kP + kPairA[e] * 64 + k * 8,
+                                      v_desc + ((kPairB[e] * kTcTile + k * 2048) >> 4), id_o, e > 0 || k > 0);
+                    tc_commit(on, tc_smem(&sy.pv_done));
+                    tc_commit(on, tc_smem(&sy.empty[x % R]));
+                }
             }
         }
         __syncwarp();
@@ -479,6 +484,7 @@ __global__ void __launch_bounds__(kF32Threads, 1)
         const uint32_t sum_at = tmem + (w < 2 ? Cfg::kDV : Cfg::kDK) + (w & 1) * 32 + lanes;
         const int sum_steps = (a.D + 15) / 16 - (w & 1) * 2;
         auto gather = [&]() { add_columns<2>(sum, sum_at, sum_steps); };
+        const uint64_t c2 = tc_two(a.c2, a.c2);
         int g = 0, rt = r0;
 #pragma unroll 1
         for (int i = 0; i < nt; ++i, rt + 1 < p.qblocks ? ++rt : (++g, rt = r0)) {
@@ -494,10 +500,17 @@ __global__ void __launch_bounds__(kF32Threads, 1)
             float s[32];
             tmem_ld32(reinterpret_cast<uint32_t(&)[32]>(s), tmem + w * 32 + lanes);
             tmem_wait_ld();
+            if (__any_sync(0xffffffffu, bw != ~0u)) {
 #pragma unroll
-            for (int k = 0; k < 32; ++k) {
-                const float x = fmaf(s[k], a.c2, l2[k]);
-                s[k] = (bw >> k) & 1u ? tc_ex2(x) : 0.f;
+                for (int k = 0; k < 32; ++k)
+                    if (!((bw >> k) & 1u)) s[k] = -attn_inf();
+            }
+#pragma unroll
+            for (int k = 0; k < 32; k += 4) {
+                const float4 l = *reinterpret_cast<const float4*>(l2 + k);
+                tc_split(tc_fma2(tc_two(s[k], s[k + 1]), c2, tc_two(l.x, l.y)), s[k], s[k + 1]);
+                tc_split(tc_fma2(tc_two(s[k + 2], s[k + 3]), c2, tc_two(l.z, l.w)), s[k + 2], s[k + 3]);
+                s[k] = tc_ex2(s[k]), s[k + 1] = tc_ex2(s[k + 1]), s[k + 2] = tc_ex2(s[k + 2]), s[k + 3] = tc_ex2(s[k + 3]);
             }
             store_pieces_over(tmem, lanes, w, s);
             if (i > 0) {  // the products of the tile before
@@ -518,7 +531,14 @@ __global__ void __launch_bounds__(kF32Threads, 1)
                 tmem_ld16(d, tmem + Cfg::kDP + w * 32 + c * 16 + lanes);
                 tmem_wait_ld();
 #pragma unroll
-                for (int k = 0; k < 16; ++k) s[c * 16 + k] *= __uint_as_float(d[k]) + l2[128 + c * 16 + k];
+                for (int k = 0; k < 16; k += 4) {
+                    const float4 l = *reinterpret_cast<const float4*>(l2 + 128 + c * 16 + k);
+                    float* x = s + c * 16 + k;
+                    tc_split(tc_mul2(tc_add2(tc_two(__uint_as_float(d[k]), __uint_as_float(d[k + 1])), tc_two(l.x, l.y)),
+                                     tc_two(x[0], x[1])), x[0], x[1]);
+                    tc_split(tc_mul2(tc_add2(tc_two(__uint_as_float(d[k + 2]), __uint_as_float(d[k + 3])), tc_two(l.z, l.w)),
+                                     tc_two(x[2], x[3])), x[2], x[3]);
+                }
             }
             store_pieces_over(tmem + Cfg::kDP, lanes, w, s);
             tmem_wait_st();
@@ -657,6 +677,7 @@ __global__ void __launch_bounds__(kF32Threads, 1)
         const bool live = l2 != -attn_inf();
         const int seen = live ? tc_seen(a, q) : 0;
         const uint32_t* bits = a.bits && q < a.Q ? a.bits + b * a.bits_sb + h * a.bits_sh + (long long)q * a.W : nullptr;
+        const uint64_t c2 = tc_two(a.c2, a.c2), nl = tc_two(l2, l2), nd = tc_two(dl, dl);
         // a warpgroup sums 16 channels
         float sum[16];
 #pragma unroll
@@ -672,18 +693,36 @@ __global__ void __launch_bounds__(kF32Threads, 1)
             ok = tc_bar_wait(tc_smem(&sy.s_full), i & 1, abort, a.err);  // dP(i) and dQ(i-1) too
             if (!ok) break;
             tc_fence_after();
-            float s[32], d[32];
+            float s[32];
             tmem_ld32(reinterpret_cast<uint32_t(&)[32]>(s), tmem + w * 32 + lanes);
-            tmem_ld32(reinterpret_cast<uint32_t(&)[32]>(d), tmem + Cfg::kDP + w * 32 + lanes);
             tmem_wait_ld();
+            if (__any_sync(0xffffffffu, bw != ~0u)) {
+#pragma unroll
+                for (int k = 0; k < 32; ++k)
+                    if (!((bw >> k) & 1u)) s[k] = -attn_inf();
+            }
+#pragma unroll
+            for (int k = 0; k < 32; k += 2) {
+                tc_split(tc_fma2(tc_two(s[k], s[k + 1]), c2, nl), s[k], s[k + 1]);
+                s[k] = tc_ex2(s[k]), s[k + 1] = tc_ex2(s[k + 1]);
+            }
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                uint32_t d[16];
+                tmem_ld16(d, tmem + Cfg::kDP + w * 32 + c * 16 + lanes);
+                tmem_wait_ld();
+#pragma unroll
+                for (int k = 0; k < 16; k += 2) {
+                    float* x = s + c * 16 + k;
+                    tc_split(tc_mul2(tc_add2(tc_two(__uint_as_float(d[k]), __uint_as_float(d[k + 1])), nd), tc_two(x[0], x[1])), x[0], x[1]);
+                }
+            }
             tc_fence_before();
             tc_bar_arrive_if(first, tc_smem(&sy.s_free));
             if (i > 0) add_columns<1>(sum, sum_at, sum_steps);
-#pragma unroll
-            for (int k = 0; k < 32; ++k) d[k] = (bw >> k) & 1u ? tc_ex2(fmaf(s[k], a.c2, l2)) * (d[k] + dl) : 0.f;
             const uint32_t at = tmem + Cfg::kDS + w * 16 + lanes;
 #pragma unroll
-            for (int k = 0; k < 2; ++k) store_pieces(d + k * 16, at + k * 8, at + 64 + k * 8, at + 128 + k * 8);
+            for (int k = 0; k < 2; ++k) store_pieces(s + k * 16, at + k * 8, at + 64 + k * 8, at + 128 + k * 8);
             tmem_wait_st();
             tc_fence_before();
             tc_bar_arrive_if(first, tc_smem(&sy.ds_ready));
