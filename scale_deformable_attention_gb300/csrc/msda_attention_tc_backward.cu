@@ -300,9 +300,6 @@ __global__ void __launch_bounds__(bwd_threads(NC), 1)
             const uint32_t id_s = tc_idesc(BF16, false, false, 128, 128), id_g = tc_idesc(BF16, false, true, 128, steps * 16);
             const uint64_t k_desc = tc_desc(tc_smem(k_tile), 16, 1024), v_desc = tc_desc(tc_smem(v_tile), 16, 1024);
             const uint32_t base = tc_smem(ring);
-            uint32_t step_on[NC * 4];
-#pragma unroll
-            for (int k = 0; k < NC * 4; ++k) step_on[k] = k < steps ? on : 0u;
             // stage of step i: Q, and dO a tile further
             const uint64_t row_desc = tc_desc(base, 16, 1024), col_desc = tc_desc(base, kTcTile, 1024);
             auto off = [&](int i) { return (uint64_t)((i % ST) * (kStage >> 4)); };
@@ -313,7 +310,7 @@ __global__ void __launch_bounds__(bwd_threads(NC), 1)
 #pragma unroll
                 for (int k = 0; k < NC * 4; ++k) {
                     const uint64_t o = ((k >> 2) * kTcTile + (k & 3) * 32) >> 4;
-                    tc_mma_ss(step_on[k], d, x_desc + o, y_desc + o, id_s, k > 0);
+                    if (k < steps) tc_mma_ss(on, d, x_desc + o, y_desc + o, id_s, k > 0);
                 }
                 tc_commit(on, bar);
             };
@@ -694,14 +691,11 @@ __global__ void __launch_bounds__(bwd_threads(NC), 1)
             const uint32_t base = tc_smem(ring), dp = tmem + Cfg::kDP;
             const uint64_t row_desc = tc_desc(base, 16, 1024), col_desc = tc_desc(base, kTcTile, 1024);
             constexpr uint64_t kTile = Cfg::kTileBytes >> 4;
-            uint32_t step_on[NC * 4];
-#pragma unroll
-            for (int k = 0; k < NC * 4; ++k) step_on[k] = k < steps ? on : 0u;
             auto scores = [&](uint32_t d, uint64_t x_desc, uint64_t y_desc) {  // 128 queries x 128 keys
 #pragma unroll
                 for (int k = 0; k < NC * 4; ++k) {
                     const uint64_t o = ((k >> 2) * kTcTile + (k & 3) * 32) >> 4;
-                    tc_mma_ss(step_on[k], d, x_desc + o, y_desc + o, id_s, k > 0);
+                    if (k < steps) tc_mma_ss(on, d, x_desc + o, y_desc + o, id_s, k > 0);
                 }
             };
             // dQ += dS K over the tile's keys: 16 a step, a warpgroup's part of 32 `part` columns behind the one before
