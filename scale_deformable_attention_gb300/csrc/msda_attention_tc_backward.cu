@@ -26,8 +26,7 @@ namespace msda {
 // Warpgroups on the scores, beside one of copies, products and clearing.  Up to
 // 64 channels four, 32 columns of a tile each: two left half of the cycles to
 // waits.  Beyond, where the products bound the kernel, two of 64 columns: four
-// took issue slots from the warps that feed the tensor cores (query kernel, 128
-// channels: 566 -> 600 us).
+// measured the same.
 constexpr int bwd_groups(int nc) { return nc == 1 ? 4 : 2; }
 constexpr int bwd_threads(int nc) { return bwd_groups(nc) * 128 + 128; }
 
