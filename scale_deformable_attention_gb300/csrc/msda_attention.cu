@@ -542,8 +542,8 @@ msda_status msda_attention_backward(msda_dtype dt, unsigned flags, const msda_at
         t.a = a;
         t.G = 1, t.qpt = t.rows = msda::kTcRows, t.qblocks = w.rows.tiles;
         t.fix_rows = a.causal && p->Q > p->S;
-        t.delta_out = p->S <= msda::kTcRows ? dl : nullptr;
-        {   // the query kernel first: with one tile of keys it leaves delta for the other
+        t.delta_out = dl;
+        {   // the query kernel first: it leaves delta of rows with one tile of keys for the other
             msda::TraceSpan ts(st);
             s = launched(msda::launch_attention_tc_grad_query(t, dt == MSDA_BF16, mq, mk, mv, mg, st),
                          "attention query gradient kernel launch");

@@ -19,7 +19,7 @@ struct TcArgs {
     long long bits_t_sb, bits_t_sh;
     int Wq;
     int fix_rows;         // backward: rows without keys may occur, and are cleared
-    float* delta_out;      // backward, keys that fit one tile: the query kernel works delta out and leaves it here for the key kernel
+    float* delta_out;      // backward: -delta, which the query kernel works out itself where one tile holds all keys of its rows
     const float* scale_in; // f16: the largest squared norms (see attention_amax), else null
 };
 

@@ -576,10 +576,10 @@ __global__ void __launch_bounds__(bwd_threads(NC), 1)
                 if (!ok) break;
                 tc_fence_after();
             }
-            if (p.delta_out) {
-                // One tile of keys: delta = sum_j p dP from the values at hand, not <dout, out>.  With few keys out is
-                // as large as a value and its rounding to 16 bits, carried into dP - delta, was the largest error
-                // (twice the others together for two keys).
+            if (nt == 1) {
+                // All keys that the tile's rows see are in this one: delta = sum_j p dP from the values at hand, not <dout, out>.
+                // With few keys out is as large as a value and its rounding to 16 bits, carried into dP - delta, was the
+                // largest error (twice the others together for two keys).
                 float2* part_sum = reinterpret_cast<float2*>(ring + 2 * Cfg::kTileBytes);  // one tile: the ring's third is free
                 float sum = 0.f, ps = 0.f;
 #pragma unroll
