@@ -19,36 +19,81 @@ namespace msda {
 //     share the key sees it; a key outside it may hold anything, NaN too (every
 //     writer of a byte writes the same 1);
 //   bits [Bm, Mm, Q, W] and bits_t [Bm, Mm, S, Wq] (tensor-core kernels; or
-//     null): the mask and its transpose, 32 pairs a word, zeros behind S and Q.
-// A warp takes 32 queries and 32 keys: lane j reads byte j of each row, the
-// row's word is a ballot, and the lane's own column of the transpose builds up.
+//     null): the mask and its transpose, 32 pairs a word, zeros behind S and Q;
+//   ext_q, ext_k (cleared before): where a tile of queries, and one of keys, begins and ends (see TcArgs; maxima of
+//     integers, the same in any order).
+// A warp takes 32 queries and 128 keys, a lane four keys: one 32-bit load a row
+// where the row's address allows it, else four of a byte.  A row's words are
+// put together by eight lanes each, the keys' columns build up in each lane.
+// (One key a lane took 330 us for 16000 x 16000 pairs, four times the loads.)
 __global__ void __launch_bounds__(128) msda_attention_mask_kernel(const uint8_t* mask, long long mk_sb, long long mk_sh,
                                                                   long long mk_sq, const uint8_t* key_mask,
                                                                   long long km_sb, int Q, int S, int G, int Bm, int Mm,
                                                                   int LB, int LN, int B, uint8_t* live, uint32_t* bits,
-                                                                  uint32_t* bits_t, int W, int Wq) {
-    const int lane = threadIdx.x & 31, word = blockIdx.x * 4 + (threadIdx.x >> 5), j = word * 32 + lane;
+                                                                  uint32_t* bits_t, int W, int Wq, int2* ext_q, int2* ext_k) {
+    const int lane = threadIdx.x & 31, j = blockIdx.x * 128 + lane * 4, n = S - j < 4 ? S - j : 4;  // the lane's keys: n > 0 of them
     for (int z = blockIdx.z; z < Bm * Mm; z += gridDim.z) {
         const int bm = z / Mm, mm = z - bm * Mm;
         const uint8_t* src = mask + bm * mk_sb + mm * mk_sh + j;
-        for (int qw = blockIdx.y; qw < Wq; qw += gridDim.y) {
-            const int q0 = qw * 32;
-            uint32_t row = 0, col = 0;
-#pragma unroll 8
-            for (int r = 0; r < 32; ++r) {
-                const bool on = j < S && q0 + r < Q && src[(q0 + r) * mk_sq] != 0;
-                const uint32_t w = __ballot_sync(0xffffffffu, on);
-                if (lane == r) row = w;
-                col |= (on ? 1u : 0u) << r;
+        for (int qt = blockIdx.y; qt < Wq / 4; qt += gridDim.y) {
+            const int qw = qt * 4 + (threadIdx.x >> 5), q0 = qw * 32;
+            uint32_t row[4] = {}, col[4] = {};
+#pragma unroll
+            for (int r0 = 0; r0 < 32; r0 += 16) {
+                uint32_t v[16];
+#pragma unroll
+                for (int r = 0; r < 16; ++r) {
+                    const uint8_t* at = src + (q0 + r0 + r) * mk_sq;
+                    v[r] = 0;
+                    if (q0 + r0 + r < Q) {
+                        if (n == 4 && (reinterpret_cast<uintptr_t>(at) & 3) == 0) {
+                            v[r] = *reinterpret_cast<const uint32_t*>(at);
+                        } else {
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                if (e < n) v[r] |= (uint32_t)at[e] << (8 * e);
+                        }
+                    }
+                }
+#pragma unroll
+                for (int r = 0; r < 16; ++r) {
+                    const uint32_t four = ((__vcmpne4(v[r], 0u) & 0x08040201u) * 0x01010101u) >> 24;  // a bit a key
+                    uint32_t w = four << (4 * (lane & 7));
+                    w |= __shfl_xor_sync(0xffffffffu, w, 1);
+                    w |= __shfl_xor_sync(0xffffffffu, w, 2);
+                    w |= __shfl_xor_sync(0xffffffffu, w, 4);
+                    if ((lane & 7) == (r & 7)) row[(r0 + r) >> 3] = w;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) col[e] |= ((four >> e) & 1u) << (r0 + r);
+                }
             }
-            if (bits && q0 + lane < Q) bits[((long long)z * Q + q0 + lane) * W + word] = row;
-            if (bits_t && j < S) bits_t[((long long)z * S + j) * Wq + qw] = col;
-            if (col) {
+            if (bits) {
+#pragma unroll
+                for (int t = 0; t < 4; ++t) {
+                    const int q = q0 + t * 8 + (lane & 7);
+                    if (q < Q) bits[((long long)z * Q + q) * W + blockIdx.x * 4 + (lane >> 3)] = row[t];
+                }
+            }
+            if (bits_t) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (e < n) bits_t[((long long)z * S + j + e) * Wq + qw] = col[e];
+            }
+            const uint32_t any = col[0] | col[1] | col[2] | col[3];
+            if (__any_sync(0xffffffffu, any != 0) && lane < 4) {
+                int2* e = lane < 2 ? ext_q + (long long)z * (Wq / 4) + qt : ext_k + (long long)z * (W / 4) + blockIdx.x;
+                const int t = lane < 2 ? (int)blockIdx.x : qt, v = lane & 1 ? t + 1 : kTcFar - t;
+                atomicMax(lane & 1 ? &e->y : &e->x, v);
+            }
+            if (any) {
                 const int ln = LN > 1 ? mm / G : 0;
                 // a mask that all batch items share meets the key_mask of each
                 const int b0 = Bm > 1 ? bm : 0, b1 = Bm > 1 ? bm + 1 : LB;
                 for (int b = b0; b < b1; ++b)
-                    if (!key_mask || key_mask[b * km_sb + j]) live[((long long)(LB > 1 ? b : 0) * LN + ln) * S + j] = 1;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (col[e] && (!key_mask || key_mask[b * km_sb + j + e]))
+                            live[((long long)(LB > 1 ? b : 0) * LN + ln) * S + j + e] = 1;
             }
         }
     }
@@ -138,7 +183,7 @@ msda_status check(msda_dtype dt, unsigned flags, const msda_attention_problem* p
 // bytes, the pairs as bits by query and, for the tensor-core kernels, by key.
 struct MaskSpace {
     int Bm = 1, Mm = 1, LB = 1, LN = 1, W = 0, Wq = 0;
-    size_t bits = 0, bits_t = 0, bytes = 0;  // offsets of the bits behind the liveness
+    size_t ext_q = 0, ext_k = 0, bits = 0, bits_t = 0, bytes = 0;  // offsets behind the liveness; what lies before `bits` is cleared
 };
 MaskSpace mask_space(unsigned flags, const msda_attention_problem* p, bool by_key) {
     MaskSpace l;
@@ -149,7 +194,9 @@ MaskSpace mask_space(unsigned flags, const msda_attention_problem* p, bool by_ke
     l.LN = l.Mm > 1 ? (int)p->N : 1;
     l.W = (int)((p->S + 127) / 128 * 4);
     l.Wq = (int)((p->Q + 127) / 128 * 4);
-    l.bits = up((size_t)l.LB * l.LN * (size_t)p->S);
+    l.ext_q = up((size_t)l.LB * l.LN * (size_t)p->S);
+    l.ext_k = l.ext_q + (size_t)l.Bm * l.Mm * (l.Wq / 4) * 8;
+    l.bits = up(l.ext_k + (size_t)l.Bm * l.Mm * (l.W / 4) * 8);
     l.bits_t = l.bits + up((size_t)l.Bm * l.Mm * p->Q * l.W * 4);
     l.bytes = l.bits_t;
     if (by_key) l.bytes += up((size_t)l.Bm * l.Mm * p->S * l.Wq * 4);
@@ -219,22 +266,23 @@ AttentionArgs args_of(unsigned flags, const msda_attention_problem* p, double sc
 }
 
 // Replaces key_mask by the keys that some pair of the mask leaves, and brings
-// the mask's bits up where `t` is given.
-msda_status make_mask(AttentionArgs& a, const MaskSpace& l, void* ws, msda::TcArgs* t, cudaStream_t st) {
+// the mask's bits up (by key where asked for).
+msda_status make_mask(AttentionArgs& a, const MaskSpace& l, void* ws, msda::TcArgs& t, bool by_key, cudaStream_t st) {
     if (!a.mask) return MSDA_OK;
     uint8_t* live = static_cast<uint8_t*>(ws);
     uint32_t* bits = reinterpret_cast<uint32_t*>(live + l.bits);
-    uint32_t* bits_t = t ? reinterpret_cast<uint32_t*>(live + l.bits_t) : nullptr;
+    int2 *ext_q = reinterpret_cast<int2*>(live + l.ext_q), *ext_k = reinterpret_cast<int2*>(live + l.ext_k);
+    uint32_t* bits_t = by_key ? reinterpret_cast<uint32_t*>(live + l.bits_t) : nullptr;
     if (a.S > 0) {
         msda::TraceSpan ts(st);
-        cudaError_t e = cudaMemsetAsync(live, 0, (size_t)l.LB * l.LN * a.S, st);
+        cudaError_t e = cudaMemsetAsync(live, 0, l.bits, st);
         if (e == cudaSuccess) {
             const int64_t z = (int64_t)l.Bm * l.Mm;
-            const dim3 grid((unsigned)((a.S + 127) / 128), (unsigned)(l.Wq < 65535 ? l.Wq : 65535),
+            const dim3 grid((unsigned)((a.S + 127) / 128), (unsigned)(l.Wq / 4 < 65535 ? l.Wq / 4 : 65535),
                             (unsigned)(z < 65535 ? z : 65535));
             msda::msda_attention_mask_kernel<<<grid, 128, 0, st>>>(a.mask, a.mk_sb, a.mk_sh, a.mk_sq, a.key_mask, a.km_sb, a.Q,
                                                                    a.S, a.G, l.Bm, l.Mm, l.LB, l.LN, a.B, live, bits, bits_t,
-                                                                   l.W, l.Wq);
+                                                                   l.W, l.Wq, ext_q, ext_k);
             e = cudaGetLastError();
         }
         ts.end(MSDA_KERNEL_ATTENTION_MASK, (int64_t)a.Q * a.S);
@@ -246,11 +294,11 @@ msda_status make_mask(AttentionArgs& a, const MaskSpace& l, void* ws, msda::TcAr
     a.bits = bits, a.W = l.W;
     a.bits_sh = l.Mm > 1 ? (long long)a.Q * l.W : 0;
     a.bits_sb = l.Bm > 1 ? (long long)l.Mm * a.Q * l.W : 0;
-    if (t) {
-        t->bits_t = bits_t, t->Wq = l.Wq;
-        t->bits_t_sh = l.Mm > 1 ? (long long)a.S * l.Wq : 0;
-        t->bits_t_sb = l.Bm > 1 ? (long long)l.Mm * a.S * l.Wq : 0;
-    }
+    t.ext_q = ext_q, t.ext_k = ext_k;
+    t.ext_sh = l.Mm > 1 ? 1 : 0, t.ext_sb = l.Bm > 1 ? l.Mm : 0;
+    t.bits_t = bits_t, t.Wq = l.Wq;
+    t.bits_t_sh = l.Mm > 1 ? (long long)a.S * l.Wq : 0;
+    t.bits_t_sb = l.Bm > 1 ? (long long)l.Mm * a.S * l.Wq : 0;
     return MSDA_OK;
 }
 
@@ -415,7 +463,7 @@ msda_status msda_attention_forward(msda_dtype dt, unsigned flags, const msda_att
     const MaskSpace ms = mask_space(flags, p, false);
     msda::TcArgs t{};
     const bool pieces = tc_pieces(dt, p, false);
-    if ((s = make_mask(a, ms, workspace, nullptr, st)) != MSDA_OK) return s;
+    if ((s = make_mask(a, ms, workspace, t, false, st)) != MSDA_OK) return s;
     ForwardPlan f{};
     if (tc || pieces) {
         f = forward_plan(p, pieces ? 1 : 2);
@@ -515,7 +563,7 @@ msda_status msda_attention_backward(msda_dtype dt, unsigned flags, const msda_at
     float* dl = l2 + w.rows.rt;
     a.row_l2 = l2, a.row_dl = dl;
     msda::TcArgs t{};
-    if ((s = make_mask(a, mask_space(flags, p, tc || pieces), ws + w.mask, tc || pieces ? &t : nullptr, st)) != MSDA_OK) return s;
+    if ((s = make_mask(a, mask_space(flags, p, tc || pieces), ws + w.mask, t, tc || pieces, st)) != MSDA_OK) return s;
     {
         msda::TraceSpan ts(st);
         const bool half = tc && dt == MSDA_F16;

@@ -18,6 +18,10 @@ struct TcArgs {
     const uint32_t* bits_t;  // the mask's bits with keys as rows: [Bm, Mm, S, Wq], or null
     long long bits_t_sb, bits_t_sh;
     int Wq;
+    // Where the mask leaves anything, in tiles of 128 (null without a mask): for a tile of queries the first and last
+    // tile of keys, for one of keys those of queries, as kTcFar - first and last + 1 (0: none): [Bm, Mm, tiles][2].
+    const int2 *ext_q, *ext_k;
+    long long ext_sb, ext_sh;  // batch and head, in rows of tiles
     int fix_rows;         // backward: rows without keys may occur, and are cleared
     float* delta_out;      // backward: -delta, which the query kernel works out itself where one tile holds all keys of its rows
     const float* scale_in; // f16: the largest squared norms (see attention_amax), else null
@@ -28,6 +32,24 @@ __device__ __forceinline__ int tc_seen(const AttentionArgs& a, int q) {
     if (!a.causal) return a.S;
     const long long n = (long long)q + 1 + (a.S - a.Q);
     return n < 0 ? 0 : n < a.S ? (int)n : a.S;
+}
+
+constexpr int kTcFar = 1 << 30;
+
+// Narrows the tiles [*t0, *t1) to those between the first and the last that the mask leaves anything of, for the tiles
+// x0..x1 (of `tiles`) of the other axis and `heads` heads from h on.
+__device__ __forceinline__ void tc_narrow(const TcArgs& p, const int2* ext, int tiles, int b, int h, int heads, int x0, int x1,
+                                          int* t0, int* t1) {
+    if (!ext) return;
+    int first = 0, last = 0;
+    if (p.ext_sh == 0) heads = 1;
+    for (int i = 0; i < heads; ++i)
+        for (int x = x0; x <= x1; ++x) {
+            const int2 e = ext[(b * p.ext_sb + (h + i) * p.ext_sh) * tiles + x];
+            first = max(first, e.x), last = max(last, e.y);
+        }
+    *t0 = max(*t0, kTcFar - first);
+    *t1 = min(*t1, last);
 }
 
 // the lowest n bits, n clamped to 0..32

@@ -103,9 +103,9 @@ __global__ void __launch_bounds__(bwd_threads(NC), 1)
     const uint8_t* km = a.key_mask ? a.key_mask + b * a.km_sb + n * a.km_sh : nullptr;
     // row tiles that see a key of the tile: causal rows below j0 - (S - Q) see none
     long long first_q = a.causal ? (long long)j0 - (a.S - a.Q) : 0;
-    const int r0 = first_q <= 0 ? 0 : (int)(first_q < a.Q ? first_q / kTcRows : p.qblocks);
-    const int per_head = p.qblocks - r0;
-    int nt = a.G * per_head;
+    int r0 = first_q <= 0 ? 0 : (int)(first_q < a.Q ? first_q / kTcRows : p.qblocks), r1 = p.qblocks;
+    tc_narrow(p, p.ext_k, ktiles, b, n * a.G, a.G, kt, kt, &r0, &r1);
+    int nt = a.G * max(0, r1 - r0);
     if (km) {  // a tile of keys that take no part has no gradients
         const bool any = tid < min(kTcRows, a.S - j0) && km[j0 + tid] != 0;
         if (!__syncthreads_or(any)) nt = 0;
@@ -154,7 +154,7 @@ __global__ void __launch_bounds__(bwd_threads(NC), 1)
         const int shift = a.S - a.Q;
         int g = 0, rt = r0;  // head of the group and row tile of step i
 #pragma unroll 1
-        for (int i = 0; i < nt; ++i, rt + 1 < p.qblocks ? ++rt : (++g, rt = r0)) {
+        for (int i = 0; i < nt; ++i, rt + 1 < r1 ? ++rt : (++g, rt = r0)) {
             const int st = i % ST, q0 = rt * kTcRows + w * CH * 32;
             const int buf = Cfg::kAhead ? i & 1 : 0, phase = (Cfg::kAhead ? i >> 1 : i) & 1;
             const uint32_t s_at = tmem + buf * 128 + w * CH * 32 + lanes;
@@ -279,7 +279,7 @@ __global__ void __launch_bounds__(bwd_threads(NC), 1)
             }
             int g = 0, rt = r0;
             const float* stat = a.row_l2 + ((long long)b * a.M + n * a.G) * p.qblocks * 256;
-            for (int i = 0; i < nt; ++i, rt + 1 < p.qblocks ? ++rt : (++g, rt = r0)) {
+            for (int i = 0; i < nt; ++i, rt + 1 < r1 ? ++rt : (++g, rt = r0)) {
                 const int st = i % ST, h = n * a.G + g;
                 if (i >= ST) ok = tc_bar_wait(tc_smem(&sy.empty[st]), (i / ST - 1) & 1, abort, a.err);
                 if (!ok) break;
@@ -466,6 +466,7 @@ __global__ void __launch_bounds__(bwd_threads(NC), 1)
     const int q0 = rt * kTcRows;
     const uint8_t* km = a.key_mask ? a.key_mask + b * a.km_sb + n * a.km_sh : nullptr;
     int t0 = 0, t1 = (tc_seen(a, min(q0 + kTcRows, a.Q) - 1) + kTcRows - 1) / kTcRows;
+    tc_narrow(p, p.ext_q, p.qblocks, b, h, 1, rt, rt, &t0, &t1);
     if (km) tc_trim(km, a.S, &t0, &t1);
     const int nt = max(0, t1 - t0);
 

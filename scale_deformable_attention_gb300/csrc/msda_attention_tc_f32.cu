@@ -179,6 +179,7 @@ __global__ void __launch_bounds__(256, 1)
     const uint8_t* km = a.key_mask ? a.key_mask + b * a.km_sb + n * a.km_sh : nullptr;
     int t0 = split * a.tiles_per_split;
     int t1 = min(t0 + a.tiles_per_split, (tc_seen(a, min(q0 + p.qpt, a.Q) - 1) + kTcRows - 1) / kTcRows);
+    tc_narrow(p, p.ext_q, (a.Q + kTcRows - 1) / kTcRows, b, n * p.G, p.G, q0 / kTcRows, (min(q0 + p.qpt, a.Q) - 1) / kTcRows, &t0, &t1);
     if (km) tc_trim(km, a.S, &t0, &t1);
     const int nt = max(0, t1 - t0);
     if (warp == 4) {
@@ -444,8 +445,9 @@ __global__ void __launch_bounds__(kF32Threads, 1)
     const int j0 = kt * kTcRows;
     const uint8_t* km = a.key_mask ? a.key_mask + b * a.km_sb + n * a.km_sh : nullptr;
     long long first_q = a.causal ? (long long)j0 - (a.S - a.Q) : 0;
-    const int r0 = first_q <= 0 ? 0 : (int)(first_q < a.Q ? first_q / kTcRows : p.qblocks);
-    int nt = a.G * (p.qblocks - r0);
+    int r0 = first_q <= 0 ? 0 : (int)(first_q < a.Q ? first_q / kTcRows : p.qblocks), r1 = p.qblocks;
+    tc_narrow(p, p.ext_k, ktiles, b, n * a.G, a.G, kt, kt, &r0, &r1);
+    int nt = a.G * max(0, r1 - r0);
     if (km) {
         const bool any = tid < min(kTcRows, a.S - j0) && km[j0 + tid] != 0;
         if (!__syncthreads_or(any)) nt = 0;
@@ -487,7 +489,7 @@ __global__ void __launch_bounds__(kF32Threads, 1)
         const uint64_t c2 = tc_two(a.c2, a.c2);
         int g = 0, rt = r0;
 #pragma unroll 1
-        for (int i = 0; i < nt; ++i, rt + 1 < p.qblocks ? ++rt : (++g, rt = r0)) {
+        for (int i = 0; i < nt; ++i, rt + 1 < r1 ? ++rt : (++g, rt = r0)) {
             const int q0 = rt * kTcRows + w * 32;
             uint32_t bw = ~0u;
             if (p.bits_t && j < a.S)
@@ -564,7 +566,7 @@ __global__ void __launch_bounds__(kF32Threads, 1)
             load_pieces(on, v_tile, &map_v, own, j0, n, b, a.B);
             int g = 0, rt = r0;
             const float* stat = a.row_l2 + ((long long)b * a.M + n * a.G) * p.qblocks * 256;
-            for (int i = 0; i < nt; ++i, rt + 1 < p.qblocks ? ++rt : (++g, rt = r0)) {
+            for (int i = 0; i < nt; ++i, rt + 1 < r1 ? ++rt : (++g, rt = r0)) {
                 const int h = n * a.G + g;
                 // dO is let go before Q, and wanted before it
                 if (i > 0) ok = tc_bar_wait(tc_smem(&sy.empty[1]), (i - 1) & 1, abort, a.err);
@@ -644,6 +646,7 @@ __global__ void __launch_bounds__(kF32Threads, 1)
     const int q0 = rt * kTcRows;
     const uint8_t* km = a.key_mask ? a.key_mask + b * a.km_sb + n * a.km_sh : nullptr;
     int t0 = 0, t1 = (tc_seen(a, min(q0 + kTcRows, a.Q) - 1) + kTcRows - 1) / kTcRows;
+    tc_narrow(p, p.ext_q, p.qblocks, b, h, 1, rt, rt, &t0, &t1);
     if (km) tc_trim(km, a.S, &t0, &t1);
     const int nt = max(0, t1 - t0);
     if (warp == 16) {

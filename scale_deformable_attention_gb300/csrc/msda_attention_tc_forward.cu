@@ -84,6 +84,8 @@ __global__ void __launch_bounds__(TcForwardCfg<NQ, NC>::kThreads, 1)
     const uint8_t* km = a.key_mask ? a.key_mask + b * a.km_sb + n * a.km_sh : nullptr;
     int t0 = split * a.tiles_per_split;
     int t1 = min(t0 + a.tiles_per_split, (tc_seen(a, min(q0 + NQ * p.qpt, a.Q) - 1) + kTcRows - 1) / kTcRows);
+    tc_narrow(p, p.ext_q, (a.Q + kTcRows - 1) / kTcRows, b, n * p.G, p.G, q0 / kTcRows, (min(q0 + NQ * p.qpt, a.Q) - 1) / kTcRows,
+              &t0, &t1);
     if (km) tc_trim(km, a.S, &t0, &t1);
     const int nt = max(0, t1 - t0);
 
