@@ -377,7 +377,12 @@ msda_status msda_norm_rotary_backward(msda_dtype dt, unsigned flags, const msda_
  * dtype before their matrix product, as tensor-core products need.  No atomics
  * take part in any sum: results are the same bits every run.
  * 16-bit tensors with D a multiple of 8 and 16-byte aligned addresses and
- * strides run on the tensor cores, others (and fp32) on the FMA pipe.
+ * strides run on the tensor cores, others on the FMA pipe.  fp32 with D <= 64
+ * and enough pairs runs on the tensor cores too, each value cut into three bf16
+ * pieces in the workspace (6 bytes an element of query, key, value and, in the
+ * backward, grad_out): as exact as fp32 products, whatever the addresses.  A call
+ * with a value beyond 2^60, an infinity or a NaN in a place that takes part (or in
+ * a query without keys) runs on the FMA pipe instead, at its speed.
  *
  * Requirements: D <= 128; N divides M; scale > 0.  Q == 0 or B == 0 enqueue
  * nothing; S == 0 writes zeros and -inf.

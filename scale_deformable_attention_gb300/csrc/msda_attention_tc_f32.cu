@@ -4,21 +4,31 @@
 // A binary32 value is the sum of three bf16 values, x = x0 + x1 + x2: x0 its
 // upper 16 bits, x1 and x2 what is left, rounded twice (24 bits and more).  A
 // product is taken as x1 y1 + x0 y2 + x2 y0 + x0 y1 + x1 y0 + x0 y0; the three
-// pieces left out are below 2^-22 |x y|, 2^-24 on average.  The tensor cores cut a sum off where it
-// is added to the accumulator (64 times 0.97 of a unit in the last place added
-// to 1 leaves 1), so the small products go first: at the size of the result
-// only x0 y0 is cut, one step per 16 values contracted.  For the same
-// reason no sum over tiles stays in tensor memory: each tile's products start
-// anew, and the threads add them up in registers, rounded.
+// pieces left out are below 2^-22 |x y|, 2^-24 on average.  The tensor cores cut
+// a sum off where it is added to the accumulator (64 times 0.97 of a unit in the
+// last place added to 1 leaves 1), so the small products go first: at the size
+// of the result only x0 y0 is cut, one step per 16 values contracted.  For the
+// same reason no sum over tiles stays in tensor memory: each tile's products
+// start anew, and the threads add them up in registers, rounded.
 //
 // Six bf16 products of 128 x 128 x 16 take 384 cycles, on the FMA pipe that
-// step takes 2048.
+// step takes 2048.  64 heads of 48, 900 queries and keys, a mask of pairs:
+// forward 350 us on the FMA pipe, 129 here and 16 to cut the tensors; key
+// gradient 585 and 160, query gradient 485 and 140 (and 21 to cut).  4096 x 4096
+// of 8 heads of 64: 239, 338 and 282 us.  What bounds them: exponentials and
+// cutting (11 operations a pair of values) in turn with the products of one tile, as
+// 48 KB a tile of an operand leave room for one block and three to four tiles an
+// SM, and copies of 96 KB a step.  Pieces let go one by one, and two warpgroups
+// on alternate key tiles in the forward, measured the same or worse: a wait and
+// a commit more per piece, and 2600 cycles of 3000 for a tile's products then
+// stood behind the threads that share their issue slots.
 //
 // A first kernel cuts the tensors into pieces [3][B, rows, heads, Dp] in the
 // workspace, whatever their strides and D, with rows that take no part as
-// zeros.  A value beyond 2^60 (an infinity and NaN too) cannot be cut so that its products
-// come out as they should (inf * 0): it sets a flag by which these kernels return and
-// those of the FMA pipe, launched behind them, run; without it those return.
+// zeros.  A value beyond 2^60 (an infinity and NaN too) cannot be cut so that
+// its products come out as they should (inf * 0): it sets a flag by which these
+// kernels return and those of the FMA pipe, launched behind them, run; without
+// it those return.
 #include "msda_attention_tc.cuh"
 #include "msda_attention_tc_host.cuh"
 #include "msda_host.cuh"
