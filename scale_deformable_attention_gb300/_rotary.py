@@ -44,7 +44,7 @@ def _problem(query, key, positions, frequencies, sections):
     if key is not None:
         key = _rows("key", key)
         N = key.shape[2]
-        if tuple(key.shape) != (B, S, N, D):
+        if key.shape != (B, S, N, D):
             raise ValueError(f"key must be [B={B}, S={S}, heads, D={D}], got {tuple(key.shape)}")
         if key.dtype != query.dtype or key.device != dev:
             raise TypeError(f"key must be a {query.dtype} tensor on {dev}")
@@ -55,14 +55,15 @@ def _problem(query, key, positions, frequencies, sections):
         raise ValueError(f"sections must name 1 to 4 axes, got {sections}")
     if positions.dtype not in POSITION_CODE:
         raise TypeError(f"positions must be float32, int32 or int64, got {positions.dtype}")
-    if positions.dim() != 3 or positions.shape[0] not in (1, B) or tuple(positions.shape[1:]) != (S, A):
+    if positions.shape not in ((B, S, A), (1, S, A)):
         raise ValueError(f"positions must be [{B} or 1, S={S}, {A}], got {tuple(positions.shape)}")
-    if tuple(frequencies.shape) != (P,) or frequencies.dtype != torch.float32:
+    if frequencies.shape != (P,) or frequencies.dtype != torch.float32:
         raise ValueError(f"frequencies must be a float32 tensor of the sections' sum {P}, "
                          f"got {frequencies.dtype} {tuple(frequencies.shape)}")
-    for name, t in (("positions", positions), ("frequencies", frequencies)):
-        if t.device != dev:
-            raise ValueError(f"{name} is on {t.device}, query on {dev}")
+    if positions.device != dev:
+        raise ValueError(f"positions is on {positions.device}, query on {dev}")
+    if frequencies.device != dev:
+        raise ValueError(f"frequencies is on {frequencies.device}, query on {dev}")
     positions = positions.contiguous()
     frequencies = frequencies.contiguous()
     qs = query.stride()
