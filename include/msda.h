@@ -383,6 +383,8 @@ msda_status msda_norm_rotary_backward(msda_dtype dt, unsigned flags, const msda_
  * backward, grad_out): as exact as fp32 products, whatever the addresses.  A call
  * with a value beyond 2^60, an infinity or a NaN in a place that takes part (or in
  * a query without keys) runs on the FMA pipe instead, at its speed.
+ * A single row of queries and heads a key head (fp32: up to eight) over 256 keys
+ * or more runs on the FMA pipe in one pass over the keys.
  *
  * Requirements: D <= 128; N divides M; scale > 0.  Q == 0 or B == 0 enqueue
  * nothing; S == 0 writes zeros and -inf.

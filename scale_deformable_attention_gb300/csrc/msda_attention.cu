@@ -8,6 +8,7 @@
 #include <cstdint>
 
 #include "msda_attention.cuh"
+#include "msda_attention_decode.cuh"
 #include "msda_attention_simt.cuh"
 #include "msda_attention_tc_host.cuh"
 #include "msda_host.cuh"
@@ -131,6 +132,25 @@ bool tc_pieces(msda_dtype dt, const msda_attention_problem* p, bool backward) {
     if (dt != MSDA_F32 || p->D > 64 || p->M / p->N > 128 || p->S == 0) return false;
     if (backward) return p->Q > 64 || p->S > 64;
     return p->S > 64 && p->B * p->M * ((p->Q + 63) / 64) * ((p->S + 63) / 64) >= 3 << 7;  // tiles of 64 x 64
+}
+
+// A few rows over many keys, where addresses and strides are made of 16 bytes: one row in 16 bits, up to eight in
+// binary32.  In 16 bits (8 x 22223 keys of 8 heads of 64: 65 us against 78 on the tensor cores; 64 x 300 of 8 of 128: 13
+// against 30) more rows cost this form in proportion and a tile of the tensor cores nothing (four rows, 8 x 22223 of 2
+// of 64: 45 against 26).  binary32: one row 120 against 567, four 58 against 162, eight (1 x 22223 of 8 of 64) 58 against 94.
+bool decode_shape(msda_dtype dt, const msda_attention_problem* p) {
+    const int64_t rows = p->Q * (p->M / p->N);
+    return p->S >= 256 && (dt == MSDA_F32 ? rows <= msda::kDecodeRows && p->D % 4 == 0 : rows == 1 && p->D % 8 == 0);
+}
+// Keys a block of four warps takes, 128 at least: one wave of the four blocks that an SM holds (at 4.2 an SM 94 us, not 66).
+void decode_splits(const msda_attention_problem* p, int* splits, int* per) {
+    const int64_t heads = p->B * p->N, most = (p->S + 127) / 128;
+    int64_t n = heads > 0 ? 4 * kSms / heads : 1;
+    if (n < 1) n = 1;
+    if (n > most) n = most;
+    const int64_t each = (p->S + n - 1) / n;
+    *per = (int)each;
+    *splits = (int)((p->S + each - 1) / each);
 }
 
 // The pieces in the workspace: the flag, then query, key, value and (backward) the output's gradient.
@@ -330,6 +350,14 @@ bool tma_rows(const void* p, const int64_t* stride, int64_t B, int64_t rows, int
     return msda::aligned_to(p, 16);
 }
 
+// Whether rows are made of 16-byte vectors of `v` elements.
+bool vector_rows(const void* x, const int64_t* stride, int64_t v, int64_t B, int64_t rows, int64_t heads) {
+    const int64_t n[3] = {B, rows, heads};
+    for (int i = 0; i < 3; ++i)
+        if (n[i] > 1 && stride[i] % v) return false;
+    return msda::aligned_to(x, 16);
+}
+
 // Row blocks and split of the tensor-core forward.  Two row tiles a block
 // overlap one's products with the other's exponentials; one tile where two
 // would leave SMs without a block, or where the last round of blocks eats the gain.  A key axis of many tiles is split until
@@ -376,6 +404,13 @@ bool piece_map(const msda_attention_problem* p, const void* base, int group, int
 
 msda_status launched(cudaError_t e, const char* what) {
     return e == cudaSuccess ? MSDA_OK : failf(MSDA_ERR_CUDA, "%s: %s (%s)", what, cudaGetErrorString(e), cudaGetErrorName(e));
+}
+
+msda_status join_parts(msda_dtype dt, const AttentionArgs& a, const msda_attention_problem* p, cudaStream_t st) {
+    msda::TraceSpan ts(st);
+    const msda_status s = launched(MSDA_BY_DTYPE(dt, launch_attention_join, a, st), "attention join kernel launch");
+    ts.end(MSDA_KERNEL_ATTENTION_JOIN, p->B * p->M * p->Q);
+    return s;
 }
 
 // Clears the flag and cuts the tensors; a.key_mask (and, backward, lse) say which rows take part.
@@ -428,7 +463,13 @@ size_t msda_attention_forward_workspace_size(msda_dtype dt, unsigned flags, cons
     if (tc_type(dt, p)) splits = forward_plan(p).splits;  // which of the two runs depends on the addresses
     size_t pieces = 0;
     if (tc_pieces(dt, p, false)) splits = forward_plan(p, 1).splits, pieces = piece_space(p, false).bytes;
-    return part_bytes(p, splits) + mask_space(flags, p, false).bytes + pieces;
+    size_t need = part_bytes(p, splits) + mask_space(flags, p, false).bytes + pieces;
+    if (decode_shape(dt, p)) {
+        decode_splits(p, &splits, &per);
+        const size_t n = part_bytes(p, splits);
+        if (n > need) need = n;
+    }
+    return need;
 }
 
 size_t msda_attention_backward_workspace_size(msda_dtype dt, unsigned flags, const msda_attention_problem* p) {
@@ -460,6 +501,21 @@ msda_status msda_attention_forward(msda_dtype dt, unsigned flags, const msda_att
     const bool tc = tc_type(dt, p) && tma_rows(query, p->query_stride, p->B, p->Q, p->M) &&
                     tma_rows(key, p->key_stride, p->B, p->S, p->N) && tma_rows(value, p->value_stride, p->B, p->S, p->N) &&
                     msda::aligned_to(out, 16);
+    const int64_t v = 16 / (int64_t)es;
+    if (decode_shape(dt, p) && vector_rows(query, p->query_stride, v, p->B, p->Q, p->M) &&
+        vector_rows(key, p->key_stride, v, p->B, p->S, p->N) && vector_rows(value, p->value_stride, v, p->B, p->S, p->N)) {
+        decode_splits(p, &a.splits, &a.tiles_per_split);
+        if (a.splits > 1) {
+            a.part_o = static_cast<float*>(workspace);
+            a.part_lse = reinterpret_cast<float*>(static_cast<unsigned char*>(workspace) + up((size_t)a.splits * p->B * p->M * p->Q * p->D * 4));
+        }
+        {
+            msda::TraceSpan ts(st);
+            s = launched(MSDA_BY_DTYPE(dt, launch_attention_decode, a, st), "attention kernel launch");
+            ts.end(MSDA_KERNEL_ATTENTION, p->B * p->M * p->Q);
+        }
+        return s == MSDA_OK && a.splits > 1 ? join_parts(dt, a, p, st) : s;
+    }
     const MaskSpace ms = mask_space(flags, p, false);
     msda::TcArgs t{};
     const bool pieces = tc_pieces(dt, p, false);
@@ -512,12 +568,7 @@ msda_status msda_attention_forward(msda_dtype dt, unsigned flags, const msda_att
         s = launched(MSDA_BY_DTYPE(dt, launch_attention_simt, a, simt_vec(a), st), "attention kernel launch");
         ts.end(MSDA_KERNEL_ATTENTION, p->B * p->M * p->Q);
     }
-    if (s == MSDA_OK && a.splits > 1) {
-        msda::TraceSpan ts(st);
-        s = launched(MSDA_BY_DTYPE(dt, launch_attention_join, a, st), "attention join kernel launch");
-        ts.end(MSDA_KERNEL_ATTENTION_JOIN, p->B * p->M * p->Q);
-    }
-    return s;
+    return s == MSDA_OK && a.splits > 1 ? join_parts(dt, a, p, st) : s;
 }
 
 msda_status msda_attention_backward(msda_dtype dt, unsigned flags, const msda_attention_problem* p, double scale,

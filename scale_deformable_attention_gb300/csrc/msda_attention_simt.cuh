@@ -509,13 +509,14 @@ __global__ void __launch_bounds__(kSimtThreads, simt_blocks(DP)) msda_attention_
     }
 }
 
-// Joins the rows of a split key axis: out = sum_i 2^(lse_i - lse) o_i.  A warp a row.
+// Joins the rows of a split key axis: out = sum_i 2^(lse_i - lse) o_i.  A block
+// a row, each warp every fourth part (one warp for 57 parts took 16 us), then
+// the warps' sums in a fixed order.
 template <typename T>
 __global__ void __launch_bounds__(128) msda_attention_join_kernel(const AttentionArgs a) {
-    const long long rows = (long long)a.B * a.M * a.Q;
-    const long long row = (long long)blockIdx.x * 4 + (threadIdx.x >> 5);
-    if (row >= rows) return;
-    const int lane = threadIdx.x & 31;
+    __shared__ float part[4][kAttnMaxChannels + 1];
+    const long long rows = (long long)a.B * a.M * a.Q, row = blockIdx.x;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     float top = -attn_inf();
     for (int i = lane; i < a.splits; i += 32) {
         const float x = a.part_lse[i * rows + row];
@@ -527,13 +528,28 @@ __global__ void __launch_bounds__(128) msda_attention_join_kernel(const Attentio
     }
     const float ref = top == -attn_inf() ? 0.f : top;
     float sum = 0.f, o[kAttnMaxChannels / 32] = {};
-    for (int i = 0; i < a.splits; ++i) {
+#pragma unroll 4
+    for (int i = warp; i < a.splits; i += 4) {
         const float w = exp2f(a.part_lse[i * rows + row] - ref);
         sum += w;
         const float* p = a.part_o + (i * rows + row) * a.D;
 #pragma unroll
         for (int c = 0; c < kAttnMaxChannels / 32; ++c)
             if (lane + 32 * c < a.D) o[c] = fmaf(w, p[lane + 32 * c], o[c]);
+    }
+#pragma unroll
+    for (int c = 0; c < kAttnMaxChannels / 32; ++c) part[warp][lane + 32 * c] = o[c];
+    if (lane == 0) part[warp][kAttnMaxChannels] = sum;
+    __syncthreads();
+    if (warp != 0) return;
+    sum = 0.f;
+#pragma unroll
+    for (int w = 0; w < 4; ++w) sum += part[w][kAttnMaxChannels];
+#pragma unroll
+    for (int c = 0; c < kAttnMaxChannels / 32; ++c) {
+        o[c] = 0.f;
+#pragma unroll
+        for (int w = 0; w < 4; ++w) o[c] += part[w][lane + 32 * c];
     }
     const float inv = sum == 0.f ? 0.f : 1.f / sum;
     const long long bm = row / a.Q;
@@ -707,7 +723,7 @@ cudaError_t launch_attention_simt_grad_query(const AttentionArgs& a, const Atten
 template <typename T>
 cudaError_t launch_attention_join(const AttentionArgs& a, cudaStream_t st) {
     const long long rows = (long long)a.B * a.M * a.Q;
-    msda_attention_join_kernel<T><<<(unsigned)((rows + 3) / 4), 128, 0, st>>>(a);
+    msda_attention_join_kernel<T><<<(unsigned)rows, 128, 0, st>>>(a);
     return cudaGetLastError();
 }
 template <typename T>
