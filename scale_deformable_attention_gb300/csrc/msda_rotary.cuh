@@ -326,8 +326,10 @@ __device__ __forceinline__ void rotary_heads(const RotaryArgs& a, const RotaryTe
 #pragma unroll
                 for (int u = 0; u < U; ++u) rn[u] += __shfl_xor_sync(0xffffffffu, rn[u], o);
             }
+            // a row that does not exist (heads end inside a step, tokens inside a warp) holds zeros, and without eps its
+            // 1 / sqrt(0) would make the weights' sums 0 * inf
 #pragma unroll
-            for (int u = 0; u < U; ++u) rn[u] = rsqrtf(rn[u] * a.inv_d + a.eps);
+            for (int u = 0; u < U; ++u) rn[u] = r.on && h + u < h1 ? rsqrtf(rn[u] * a.inv_d + a.eps) : 0.f;
         }
         if constexpr (!BWD) {
 #pragma unroll
