@@ -289,11 +289,15 @@ __device__ __forceinline__ void rotary_heads(const RotaryArgs& a, const RotaryTe
         for (int i = 0; i < V; ++i) w[i] *= r.cs[i];
     }
     uint4 xn[U], gn[BWD ? U : 1];
+    // A row that does not exist (heads end inside a step, tokens inside a warp) holds values near 1 in each type: zeros would,
+    // without eps, make its 1 / sqrt(0) times 0 a NaN in the weights' sums.  (Its factor set to 0 instead: 745 us for
+    // 737, 8 x 16641 tokens of 20 heads of 128, both directions.)
+    const uint32_t none = BWD && r.c < a.D ? 0x3f803f80u : 0u;
     auto fetch = [&](int h) {
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const bool in = r.on && h + u < h1;
-            xn[u] = make_uint4(0, 0, 0, 0);
+            xn[u] = make_uint4(none, none, none, none);
             if (in) xn[u] = *reinterpret_cast<const uint4*>(x + (h + u) * t.sh);
             if constexpr (BWD) {
                 gn[u] = make_uint4(0, 0, 0, 0);
@@ -326,10 +330,8 @@ __device__ __forceinline__ void rotary_heads(const RotaryArgs& a, const RotaryTe
 #pragma unroll
                 for (int u = 0; u < U; ++u) rn[u] += __shfl_xor_sync(0xffffffffu, rn[u], o);
             }
-            // a row that does not exist (heads end inside a step, tokens inside a warp) holds zeros, and without eps its
-            // 1 / sqrt(0) would make the weights' sums 0 * inf
 #pragma unroll
-            for (int u = 0; u < U; ++u) rn[u] = r.on && h + u < h1 ? rsqrtf(rn[u] * a.inv_d + a.eps) : 0.f;
+            for (int u = 0; u < U; ++u) rn[u] = rsqrtf(rn[u] * a.inv_d + a.eps);
         }
         if constexpr (!BWD) {
 #pragma unroll
