@@ -16,11 +16,19 @@
 // The reference m is a row's maximum when it was last looked for, not the
 // running one: any m that keeps P in range gives the same quotient.  A tile
 // takes its exponentials against the m at hand, and only where a row's sum
-// then exceeds 2^14 (f16 holds 65504, and every P is at most its sum) are the
-// maximum looked for, O and l rescaled and the exponentials taken again.  That
-// is the first tile, and then only rows whose scores keep rising; the others
-// save the maximum, which stood between reading S and the first exponential
-// (about 500 of 2600 cycles a pair of tiles).
+// then leaves a range (TcForwardRange) are the maximum looked for, O and l
+// rescaled and the exponentials taken again.  That is the first tile, and then
+// only rows whose scores keep rising; the others save the maximum, which stood
+// between reading S and the first exponential (about 500 of 2600 cycles a pair
+// of tiles).
+//
+// bf16 has the range of binary32 and needs the upper limit alone.  f16 has no
+// more than 2^-14 with all its bits and 2^-25 at all: m there lies 8 binary
+// places below the maximum, and a row that one key outweighs while the rest of
+// it makes the output gets a lower m too, O and l going up: a row's sum keeps
+// what its product would lose otherwise (22222 keys 17.6 below one whose value
+// is 0 gave 0 instead of 5.0e-4 of theirs).  What is left is the spread inside
+// a tile: 2^-34 of its largest probability.
 //
 // Up to 64 channels P has columns of its own: S(j+1) is made while P(j) is
 // still worked out, so a row's warps never wait for a product.  Beyond, P lies
@@ -32,7 +40,27 @@
 
 namespace msda {
 
-constexpr float kSumLimit = 16384.f;  // a row's sum over a tile that asks for a new reference
+// A row's sum over a tile that asks for no new reference m, and m's distance from the maximum.  Every P is at most its
+// tile's sum, 128 equal ones at the maximum are 2^15.
+template <bool BF16>
+struct TcForwardRange {
+    static constexpr float kBelow = BF16 ? 0.f : 8.f;
+    static constexpr float kTop = BF16 ? 16384.f : 49152.f;  // f16 holds 65504
+    // f16: sums of a tile between 2^-40 and 2^-5 ask for a lower m (128 values that add up to 2^-5 lose 2^-13 of it at
+    // most), below it is lost in l even 2^16 times over; l < 2^40 before and a step of 2^60 at most keep O below 2^127.
+    static constexpr float kLow = 0x1p-5f, kNothing = 0x1p-40f, kMostL = 0x1p40f, kStep = 60.f;
+    static __device__ __forceinline__ bool fits(float sum, float l) {
+        if constexpr (BF16) return sum <= kTop;
+        return sum <= kTop && (sum >= kLow || sum <= kNothing || l >= kMostL);
+    }
+    // the reference after a tile whose maximum asks for `want`
+    static __device__ __forceinline__ float next(float m, float want, float l) {
+        if constexpr (!BF16) {
+            if (want < m - 12.f && want > m - kStep && l < kMostL) return want;
+        }
+        return fmaxf(m, want);
+    }
+};
 
 template <int NQ, int NC>
 struct TcForwardCfg {
@@ -62,6 +90,7 @@ __global__ void __launch_bounds__(TcForwardCfg<NQ, NC>::kThreads, 1)
                                      const __grid_constant__ CUtensorMap map_k,
                                      const __grid_constant__ CUtensorMap map_v) {
     using Cfg = TcForwardCfg<NQ, NC>;
+    using Range = TcForwardRange<BF16>;
     constexpr int ST = Cfg::kStages;
     const AttentionArgs& a = p.a;
     extern __shared__ unsigned char tc_smem_raw[];
@@ -208,7 +237,7 @@ __global__ void __launch_bounds__(TcForwardCfg<NQ, NC>::kThreads, 1)
                 float sum = 0.f;
                 if (__builtin_expect(!renew, 1)) {
                     sum = probabilities(Cfg::kOwnP && i > 0);
-                    renew = __any_sync(0xffffffffu, valid && !(sum <= kSumLimit));
+                    renew = __any_sync(0xffffffffu, valid && !Range::fits(sum, l));
                 } else if (Cfg::kOwnP && i > 0) {
                     gone = !tc_bar_wait(tc_smem(&sy.pv_done[t]), (i - 1) & 1, abort, a.err);
                     tc_fence_after();
@@ -222,7 +251,7 @@ __global__ void __launch_bounds__(TcForwardCfg<NQ, NC>::kThreads, 1)
                         for (int k = 2; k < 32; k += 2)
                             mx[c] = tc_max3(mx[c], __uint_as_float(s[c][k]), __uint_as_float(s[c][k + 1]));
                     }
-                    const float next = fmaxf(m, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * a.c2);
+                    const float next = Range::next(m, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * a.c2 - Range::kBelow, l);
                     const float f = next == m ? 1.f : tc_ex2(m - next);
                     m = next;
                     l *= f;
