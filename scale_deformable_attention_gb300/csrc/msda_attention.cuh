@@ -48,9 +48,11 @@ struct AttentionRows {
     int rt, tiles, heads;
 };
 
-// f16 on the tensor cores: probabilities are held times 2^12 (at most 4096; what
-// lies under 2^-26 of a row's sum would otherwise fall below f16's steps)
-constexpr float kHalfScale = 12.f;
+// f16 on the tensor cores, backward: probabilities are held times 2^14, so that a
+// share of 2^-28 of a row still has all its bits and one of 2^-39 some; f16 holds
+// 65504, which leaves a factor of 4 for an lse that binary32 holds to 1 (above
+// 2^24).  (The forward's scale is its own: a reference that follows the tiles.)
+constexpr float kHalfScale = 14.f;
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;

@@ -15,7 +15,7 @@
 // P^T and dS^T (16 bits) are operands in tensor memory, where a product with D
 // columns takes D/2 cycles (from shared memory it is bound by reading its
 // 128 x 16 operand: 32 + D/4).  Both are written over the scores they come from.
-// f16 would lose small values: P is scaled by 2^12 (kHalfScale) and dS by a power of two that the
+// f16 would lose small values: P is scaled by 2^14 (kHalfScale) and dS by a power of two that the
 // largest norms of dO and V rows bound from above; the sums are scaled back.
 #include "msda_attention_tc.cuh"
 #include "msda_attention_tc_host.cuh"
