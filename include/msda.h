@@ -294,9 +294,10 @@ msda_status msda_backward_static_workspace(msda_dtype dt, unsigned flags, int64_
  *   (u, v) -> (u cos t - v sin t, v cos t + u sin t)
  *
  * with (u, v) = channels (j, j + P), or (2j, 2j + 1) with
- * MSDA_ROTARY_INTERLEAVED; channels from 2P on pass through.  Angles are good
- * to about 2^-24 at any position (the product and its reduction are carried
- * in two binary32 numbers, or in binary64 where these do not hold it).
+ * MSDA_ROTARY_INTERLEAVED; channels from 2P on pass through.  Angles below 2^51
+ * are good to 2^-22, their rounding to binary32 behind the reduction by 2 pi, at any
+ * position (the product and its reduction are carried in two binary32 numbers, or
+ * two of binary64 where these do not hold it); beyond 2^51 they have no meaning.
  * With weights, a row x is first normed: z = x w / sqrt(mean(x^2) + eps).
  * Sums and the rotation are in fp32, rounded once.
  *

@@ -129,31 +129,30 @@ __device__ __forceinline__ __half from_f32<__half>(float v) { return __float2hal
 template <>
 __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
 
-// cos and sin of p * f.  The product of two binary32 numbers is held exactly
-// as hi + lo; hi is brought near [-pi, pi] by subtracting n times 2 pi, taken
-// as three binary32 parts (Cody and Waite's reduction): the first subtraction
-// is exact for |hi| < 2^23 (both sides are multiples of the smaller one's last
-// place and the difference is below 4), so the angle is off by about 2^-24 in
-// all whatever the position.  Larger products, and integer positions that
-// binary32 does not hold, take the same reduction in binary64.
-__device__ __forceinline__ void angle_cos_sin(double p64, float p, bool exact32, float f, float* c, float* s) {
-    float r;
-    const float hi = p * f;
-    if (exact32 && fabsf(hi) < 8388608.f) {
-        const float lo = fmaf(p, f, -hi);
-        const float n = rintf(hi * 0.15915494309189535f);
-        r = fmaf(-n, 6.2831854820251465f, hi);      // binary32 nearest to 2 pi
-        r = fmaf(-n, -1.7484555314695172e-07f, r);  // the rest of 2 pi
-        r += lo;
-    } else {
-        // up to 2^53 the product keeps its fraction; 2 pi in two binary64 parts
-        const double t = p64 * (double)f;
-        const double n = rint(t * 0.15915494309189535);
-        double d = fma(-n, 6.283185307179586, t);
-        d = fma(-n, 2.4492935982947064e-16, d);
-        r = (float)d;
-    }
-    sincosf(r, s, c);
+// (p + rest) * f near [-pi, pi]: the product as two binary64 numbers, 2 pi as
+// two; good for products below 2^51 (n and the difference are held exactly).
+// Not inlined: few positions need it, and beside the other path's it cost the
+// rotation alone 3 %.
+static __device__ __noinline__ float far_angle(double p, double rest, float f) {
+    const double t = p * (double)f, lo = fma(p, (double)f, -t) + rest * (double)f;
+    const double n = rint(t * 0.15915494309189535);
+    double d = fma(-n, 6.283185307179586, t);
+    d = fma(-n, 2.4492935982947064e-16, d);
+    return (float)(d + lo);
+}
+
+// p * f for |p * f| < 2^23, near [-pi, pi].  The product of two binary32 numbers
+// is held exactly as hi + lo; n times 2 pi is subtracted, taken as two binary32
+// parts (Cody and Waite's reduction): the first subtraction is exact (both sides
+// are multiples of the smaller one's last place and the difference is below 4),
+// what 2 pi has behind its second part is below 2^-27 after n, so the angle is
+// off by its own rounding to binary32 alone.
+__device__ __forceinline__ float near_angle(float hi, float p, float f) {
+    const float lo = fmaf(p, f, -hi);
+    const float n = rintf(hi * 0.15915494309189535f);
+    float r = fmaf(-n, 6.2831854820251465f, hi);  // binary32 nearest to 2 pi
+    r = fmaf(-n, -1.7484555314695172e-07f, r);    // the rest of 2 pi
+    return r + lo;
 }
 
 enum { ROT_SCALAR = 0, ROT_HALVES = 1, ROT_INTERLEAVED = 2 };
@@ -162,20 +161,23 @@ enum { ROT_SCALAR = 0, ROT_HALVES = 1, ROT_INTERLEAVED = 2 };
 __device__ __forceinline__ void rotary_angle(const RotaryArgs& a, long long at, int j, float* c, float* s) {
     int ax = 0;
     while (ax < a.A - 1 && j >= a.axis_end[ax]) ++ax;
-    double p64;
-    float p;
-    bool exact32 = true;
+    const float f = a.freq[j];
+    float r;
     if (a.pos_type == 0) {
-        p = static_cast<const float*>(a.pos)[at + ax];
-        p64 = p;
+        const float p = static_cast<const float*>(a.pos)[at + ax], hi = p * f;
+        r = fabsf(hi) < 8388608.f ? near_angle(hi, p, f) : far_angle(p, 0.0, f);
     } else {
         const long long v = a.pos_type == 1 ? (long long)static_cast<const int*>(a.pos)[at + ax]
                                             : static_cast<const long long*>(a.pos)[at + ax];
-        p = (float)v;
-        p64 = (double)v;
-        exact32 = v > -16777217ll && v < 16777217ll;
+        const float p = (float)v, hi = p * f;
+        if (v > -16777217ll && v < 16777217ll && fabsf(hi) < 8388608.f) {
+            r = near_angle(hi, p, f);
+        } else {  // what binary64 leaves of the position: its upper half is a multiple of 2^32, near p64
+            const double p64 = (double)v;
+            r = far_angle(p64, fma((double)(v >> 32), 4294967296.0, -p64) + (double)(v & 0xffffffffll), f);
+        }
     }
-    angle_cos_sin(p64, p, exact32, a.freq[j], c, s);
+    sincosf(r, s, c);
     *s *= a.sign;
 }
 
