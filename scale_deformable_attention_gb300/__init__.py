@@ -38,6 +38,7 @@ import torch
 
 from . import _lib
 from ._attention import attention, attention_backward, attention_forward
+from ._binding import workspace_of
 from ._lib import ACCUM, BWD_ACCUMULATE, BWD_WORKSPACE_ZEROED, MsdaError
 from ._rotary import norm_rotary, norm_rotary_backward, norm_rotary_forward, rotary, rotary_backward, rotary_forward
 
@@ -240,7 +241,7 @@ def backward(value: torch.Tensor, spatial_shapes: torch.Tensor, level_start_inde
     need = workspace_size(value.dtype, accum, dims, _aligned16(value, grad_out, grad_value))
     if need and workspace is None:
         workspace = torch.empty((need + 3) // 4, dtype=torch.float32, device=value.device)
-    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    workspace, ws_bytes = workspace_of(0, workspace, value.device)
     if workspace_zeroed and workspace is None:
         raise ValueError("workspace_zeroed=True needs the workspace it describes")
     flags = (BWD_ACCUMULATE if accumulate else 0) | (BWD_WORKSPACE_ZEROED if workspace_zeroed else 0)
@@ -382,7 +383,7 @@ def backward_fused(value, spatial_shapes, level_start_index, reference_points, s
     need = workspace_size(value.dtype, accum, dims)
     if need and workspace is None:
         workspace = torch.empty((need + 3) // 4, dtype=torch.float32, device=value.device)
-    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    workspace, ws_bytes = workspace_of(0, workspace, value.device)
     with torch.cuda.device(value.device):
         _lib.check(_lib.lib().msda_backward_fused(
             DTYPE_CODE[value.dtype], ACCUM[accum], BWD_ACCUMULATE if accumulate else 0, *dims, _ptr(value), _ptr(ss),

@@ -7,7 +7,7 @@ from typing import Optional, Tuple
 import torch
 
 from . import _lib
-from ._binding import DTYPE_CODE, on_device, ptr, stream
+from ._binding import DTYPE_CODE, on_device, ptr, stream, workspace_of
 
 
 def _rows(name: str, x: torch.Tensor) -> torch.Tensor:
@@ -76,12 +76,6 @@ def _problem(query, key, value, mask, key_mask, causal, scale):
     return query, key, value, mask, key_mask, flags, p, float(scale), (B, Q, S, M, N, D)
 
 
-def _workspace(need: int, workspace: Optional[torch.Tensor], dev: torch.device):
-    if workspace is None and need:
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-    return workspace, 0 if workspace is None else workspace.numel() * workspace.element_size()
-
-
 def attention_forward(query: torch.Tensor, key: torch.Tensor, value: torch.Tensor, *,
                       mask: Optional[torch.Tensor] = None, key_mask: Optional[torch.Tensor] = None,
                       causal: bool = False, scale: Optional[float] = None, workspace: Optional[torch.Tensor] = None
@@ -99,7 +93,7 @@ def attention_forward(query: torch.Tensor, key: torch.Tensor, value: torch.Tenso
     out = torch.empty((B, Q, M * D), dtype=query.dtype, device=dev)
     lse = torch.empty((B, M, Q), dtype=torch.float32, device=dev)
     lib, dt = _lib.lib(), DTYPE_CODE[query.dtype]
-    workspace, n = _workspace(lib.msda_attention_forward_workspace_size(dt, flags, p), workspace, dev)
+    workspace, n = workspace_of(lib.msda_attention_forward_workspace_size(dt, flags, p), workspace, dev)
     with on_device(dev):
         _lib.check(lib.msda_attention_forward(dt, flags, p, scale, ptr(query), ptr(key), ptr(value), ptr(key_mask),
                                               ptr(mask), ptr(out), ptr(lse), ptr(workspace), n, stream(dev)))
@@ -125,7 +119,7 @@ def attention_backward(query: torch.Tensor, key: torch.Tensor, value: torch.Tens
     gk = torch.empty((B, S, N, D), dtype=query.dtype, device=dev)
     gv = torch.empty((B, S, N, D), dtype=query.dtype, device=dev)
     lib, dt = _lib.lib(), DTYPE_CODE[query.dtype]
-    workspace, n = _workspace(lib.msda_attention_backward_workspace_size(dt, flags, p), workspace, dev)
+    workspace, n = workspace_of(lib.msda_attention_backward_workspace_size(dt, flags, p), workspace, dev)
     with on_device(dev):
         _lib.check(lib.msda_attention_backward(dt, flags, p, scale, ptr(query), ptr(key), ptr(value), ptr(key_mask),
                                                ptr(mask), ptr(out), ptr(lse), ptr(grad_out), ptr(gq), ptr(gk), ptr(gv),

@@ -7,7 +7,7 @@ from typing import Optional, Sequence, Tuple
 import torch
 
 from . import _lib
-from ._binding import DTYPE_CODE, on_device, ptr, stream
+from ._binding import DTYPE_CODE, on_device, ptr, stream, workspace_of
 
 POSITION_CODE = {torch.float32: 0, torch.int32: 1, torch.int64: 2}
 
@@ -141,10 +141,7 @@ def norm_rotary_backward(query: torch.Tensor, key: torch.Tensor, query_weight: t
     gk = _like("grad_key_out", grad_key_out, key.shape, query)
     dq, dk, dwq, dwk = _dense(query), _dense(key), torch.empty_like(wq), torch.empty_like(wk)
     lib = _lib.lib()
-    need = lib.msda_norm_rotary_backward_workspace_size(p)
-    if workspace is None and need:
-        workspace = torch.empty(need, dtype=torch.uint8, device=query.device)
-    n = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    workspace, n = workspace_of(lib.msda_norm_rotary_backward_workspace_size(p), workspace, query.device)
     with on_device(query.device):
         _lib.check(lib.msda_norm_rotary_backward(
             DTYPE_CODE[query.dtype], _lib.ROTARY_INTERLEAVED if interleaved else 0, p, float(eps), ptr(positions),
