@@ -6,6 +6,7 @@
 
 #include <cmath>
 #include <cstdint>
+#include <limits>
 
 #include "msda_attention.cuh"
 #include "msda_attention_decode.cuh"
@@ -279,7 +280,8 @@ AttentionArgs args_of(unsigned flags, const msda_attention_problem* p, double sc
     a.G = (int)(p->M / p->N);
     a.causal = (flags & MSDA_ATTENTION_CAUSAL) != 0;
     a.scale = (float)scale;
-    a.c2 = (float)(scale * 1.4426950408889634);
+    // never 0, by which the -inf of a masked pair would become NaN (a score is then off by 2^-149 |q k|, below 2^-20)
+    a.c2 = std::fmax((float)(scale * 1.4426950408889634), std::numeric_limits<float>::denorm_min());
     a.splits = 1;
     a.tiles_per_split = 1 << 30;
     return a;
