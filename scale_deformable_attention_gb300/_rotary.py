@@ -185,6 +185,8 @@ class _NormRotaryFunction(torch.autograd.Function):
 
 
 def _no_gradient(positions, frequencies):
+    if not torch.is_grad_enabled():
+        return
     for name, t in (("positions", positions), ("frequencies", frequencies)):
         if t.requires_grad:
             raise ValueError(f"{name} gets no gradient from this operator: detach it")

@@ -20,3 +20,16 @@ def test_workspace_lies_on_the_tensors_device_in_one_piece():
         workspace_of(16, buf[::2], cpu)
     with pytest.raises(ValueError, match="contiguous"):
         workspace_of(16, torch.empty((8, 8), dtype=torch.uint8).t()[:, :4], cpu)
+
+
+def test_positions_that_would_want_a_gradient():
+    """Refused where a gradient would be recorded, taken under no_grad."""
+    from scale_deformable_attention_gb300._rotary import _no_gradient
+
+    plain, leaf = torch.ones(2), torch.ones(2, requires_grad=True)
+    _no_gradient(plain, plain)
+    for args in ((leaf, plain), (plain, leaf)):
+        with pytest.raises(ValueError, match="detach"):
+            _no_gradient(*args)
+        with torch.no_grad():
+            _no_gradient(*args)
