@@ -652,12 +652,11 @@ void trace_end(int slot, cudaStream_t st, int kernel, int64_t work) {
     g_trace.work[slot] = work;
 }
 
-msda_status device_facts(unsigned** err, int* sms) {
+msda_status error_word(unsigned** err) {
     DeviceInfo* di = nullptr;
     msda_status s = device_info(&di);
     if (s != MSDA_OK) return s;
     *err = di->err;
-    *sms = di->sms;
     return MSDA_OK;
 }
 

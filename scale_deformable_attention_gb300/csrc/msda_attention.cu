@@ -108,8 +108,7 @@ namespace {
 using msda::AttentionArgs;
 using msda::AttentionRows;
 using msda::failf;
-
-constexpr int kSms = 152;  // SMs that a grid is sized for
+using msda::kPlanSms;
 
 constexpr unsigned kFlags = MSDA_ATTENTION_CAUSAL | MSDA_ATTENTION_KEY_MASK | MSDA_ATTENTION_MASK;
 
@@ -146,7 +145,7 @@ bool decode_shape(msda_dtype dt, const msda_attention_problem* p) {
 // Keys a block of four warps takes, 128 at least: one wave of the four blocks that an SM holds (at 4.2 an SM 94 us, not 66).
 void decode_splits(const msda_attention_problem* p, int* splits, int* per) {
     const int64_t heads = p->B * p->N, most = (p->S + 127) / 128;
-    int64_t n = heads > 0 ? 4 * kSms / heads : 1;
+    int64_t n = heads > 0 ? 4 * kPlanSms / heads : 1;
     if (n < 1) n = 1;
     if (n > most) n = most;
     const int64_t each = (p->S + n - 1) / n;
@@ -236,8 +235,8 @@ ForwardPlan forward_plan(const msda_attention_problem* p, int most_tiles = 2);
 void simt_splits(msda_dtype dt, const msda_attention_problem* p, int* splits, int* per) {
     const int64_t blocks = p->B * p->M * ((p->Q + 63) / 64), tiles = (p->S + 63) / 64;
     int64_t n = 1;
-    if (blocks > 0 && blocks < 2 * kSms && tiles > 1) {
-        n = (4 * kSms + blocks - 1) / blocks;
+    if (blocks > 0 && blocks < 2 * kPlanSms && tiles > 1) {
+        n = (4 * kPlanSms + blocks - 1) / blocks;
         if (n > tiles) n = tiles;
         if (n > 64) n = 64;
         if (tc_type(dt, p)) {
@@ -371,11 +370,11 @@ ForwardPlan forward_plan(const msda_attention_problem* p, int most_tiles) {
     f.qpt = msda::kTcRows / f.G;
     const int64_t one = (p->Q + f.qpt - 1) / f.qpt, two = (p->Q + 2 * f.qpt - 1) / (2 * f.qpt);
     // rounds of blocks, one an SM; a step of two tiles takes about three halves of a step of one
-    const int64_t heads = p->B * p->N, rounds1 = (heads * one + kSms - 1) / kSms, rounds2 = (heads * two + kSms - 1) / kSms;
-    f.nq = most_tiles == 2 && heads * two >= kSms && 3 * rounds2 <= 2 * rounds1 ? 2 : 1;
+    const int64_t heads = p->B * p->N, rounds1 = (heads * one + kPlanSms - 1) / kPlanSms, rounds2 = (heads * two + kPlanSms - 1) / kPlanSms;
+    f.nq = most_tiles == 2 && heads * two >= kPlanSms && 3 * rounds2 <= 2 * rounds1 ? 2 : 1;
     f.qblocks = (int)(f.nq == 2 ? two : one);
     const int64_t blocks = p->B * p->N * f.qblocks, tiles = (p->S + msda::kTcRows - 1) / msda::kTcRows;
-    int64_t n = blocks > 0 ? kSms / blocks : 1;
+    int64_t n = blocks > 0 ? kPlanSms / blocks : 1;
     if (n > tiles / 4) n = tiles / 4;
     if (n < 1) n = 1;
     const int64_t each = tiles > 0 ? (tiles + n - 1) / n : 1;
@@ -535,8 +534,7 @@ msda_status msda_attention_forward(msda_dtype dt, unsigned flags, const msda_att
         a.part_lse = reinterpret_cast<float*>(part + up((size_t)a.splits * p->B * p->M * p->Q * p->D * 4));
     }
     if (pieces) {
-        int sms;
-        if ((s = msda::device_facts(&a.err, &sms)) != MSDA_OK) return s;
+        if ((s = msda::error_word(&a.err)) != MSDA_OK) return s;
         unsigned char* ws = static_cast<unsigned char*>(workspace) + ms.bytes + part_bytes(p, a.splits);
         if ((s = make_pieces(a, p, nullptr, ws, st)) != MSDA_OK) return s;
         const PieceSpace w = piece_space(p, false);
@@ -553,8 +551,7 @@ msda_status msda_attention_forward(msda_dtype dt, unsigned flags, const msda_att
         s = launched(e, "attention kernel launch");
         ts.end(MSDA_KERNEL_ATTENTION, p->B * p->M * p->Q);
     } else if (tc) {
-        int sms;
-        if ((s = msda::device_facts(&a.err, &sms)) != MSDA_OK) return s;
+        if ((s = msda::error_word(&a.err)) != MSDA_OK) return s;
         CUtensorMap mq, mk, mv;
         if (!rows_map(dt, query, p->D, f.G, p->Q, p->N, p->B, a.q_sb, a.q_ss, a.q_sh, f.qpt, &mq) ||
             !rows_map(dt, key, p->D, 1, p->S, p->N, p->B, a.k_sb, a.k_ss, a.k_sh, msda::kTcRows, &mk) ||
@@ -631,8 +628,7 @@ msda_status msda_attention_backward(msda_dtype dt, unsigned flags, const msda_at
         if (s != MSDA_OK) return s;
     }
     if (tc) {
-        int sms;
-        if ((s = msda::device_facts(&a.err, &sms)) != MSDA_OK) return s;
+        if ((s = msda::error_word(&a.err)) != MSDA_OK) return s;
         CUtensorMap mq, mk, mv, mg;
         const int64_t row = p->M * p->D;
         if (!rows_map(dt, query, p->D, 1, p->Q, p->M, p->B, a.q_sb, a.q_ss, a.q_sh, msda::kTcRows, &mq) ||
@@ -658,8 +654,7 @@ msda_status msda_attention_backward(msda_dtype dt, unsigned flags, const msda_at
         return s;
     }
     if (pieces) {
-        int sms;
-        if ((s = msda::device_facts(&a.err, &sms)) != MSDA_OK) return s;
+        if ((s = msda::error_word(&a.err)) != MSDA_OK) return s;
         unsigned char* at = ws + w.pieces;
         if ((s = make_pieces(a, p, lse, at, st)) != MSDA_OK) return s;
         const PieceSpace x = piece_space(p, true);

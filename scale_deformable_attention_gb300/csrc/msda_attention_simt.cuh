@@ -730,7 +730,7 @@ template <typename T>
 cudaError_t launch_attention_prepare(const AttentionArgs& a, const AttentionRows& rw, const void* out, const float* lse,
                                      float off, float* l2, float* top, bool vec, cudaStream_t st) {
     const long long units = (long long)a.B * rw.heads * rw.tiles + (top ? (long long)a.B * a.N * ((a.S + 127) / 128) : 0);
-    const unsigned grid = (unsigned)(units < 152 * 16 ? units : 152 * 16);
+    const unsigned grid = (unsigned)(units < kPlanSms * 16 ? units : kPlanSms * 16);
     msda_attention_prepare_kernel<T><<<grid, 256, 0, st>>>(a, rw, out, lse, off, l2, top, vec);
     return cudaGetLastError();
 }

@@ -826,7 +826,7 @@ cudaError_t launch_attention_split(const SplitArgs& a, int tensors, cudaStream_t
         const long long n = ((long long)a.B * a.t[i].rows * a.t[i].heads * (a.Dp / 8) + 255) / 256;
         if (n > most) most = n;
     }
-    const dim3 grid((unsigned)(most < 152 * 16 ? most : 152 * 16), (unsigned)tensors);
+    const dim3 grid((unsigned)(most < kPlanSms * 16 ? most : kPlanSms * 16), (unsigned)tensors);
     msda_attention_split_kernel<<<grid, 256, 0, st>>>(a);
     return cudaGetLastError();
 }

@@ -29,8 +29,13 @@ struct TraceSpan {
 };
 
 // Device address of the error word on the current device (its bits are those
-// of msda_device_errors()) and the number of its SMs.
-msda_status device_facts(unsigned** err, int* sms);
+// of msda_device_errors()).
+msda_status error_word(unsigned** err);
+
+// SMs that the dense operators' grids and splits are planned for, those of a
+// GB300 whatever the device has: a workspace's size and the order of a sum
+// then depend on the call alone.
+constexpr int kPlanSms = 152;
 
 // Sets a kernel's limit of dynamic shared memory, once a device context
 // (`seen`: one a kernel; a device reset gives a new context and sets it again).

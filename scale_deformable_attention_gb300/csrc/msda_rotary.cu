@@ -14,7 +14,7 @@ using msda::RotaryArgs;
 
 // Blocks of 256 threads, persistent; the partial sums of the weights'
 // gradients have one row a block.
-constexpr int kRotaryMaxGrid = 152 * 6;
+constexpr int kRotaryMaxGrid = msda::kPlanSms * 6;
 constexpr int kChunkTokens[] = {32, 16, 8, 4};
 
 // Element form, tokens a chunk: as many as leave two chunks an SM, 32 at most
@@ -22,7 +22,7 @@ constexpr int kChunkTokens[] = {32, 16, 8, 4};
 // call wants many small chunks and a large one few).
 int chunk_tokens(int64_t B, int64_t S) {
     for (int t : kChunkTokens)
-        if (B * ((S + t - 1) / t) >= 2 * 152) return t;
+        if (B * ((S + t - 1) / t) >= 2 * msda::kPlanSms) return t;
     return 4;
 }
 
@@ -145,7 +145,7 @@ msda_status run(msda_dtype dt, unsigned flags, const msda_rotary_problem* p, dou
         // once, unless that leaves fewer than 16 warps an SM
         a.tokens = rows;
         const int64_t groups = (rows + (32 >> lg) - 1) / (32 >> lg), heads = p->M + p->N;
-        int64_t parts = (152 * 16 + groups - 1) / groups;
+        int64_t parts = (msda::kPlanSms * 16 + groups - 1) / groups;
         if (parts > heads) parts = heads;
         a.per = (int)((heads + parts - 1) / parts);
         a.parts = (int)((heads + a.per - 1) / a.per);
