@@ -24,11 +24,14 @@
 //
 // bf16 has the range of binary32 and needs the upper limit alone.  f16 has no
 // more than 2^-14 with all its bits and 2^-25 at all: m there lies 8 binary
-// places below the maximum, and a row that one key outweighs while the rest of
-// it makes the output gets a lower m too, O and l going up: a row's sum keeps
-// what its product would lose otherwise (22222 keys 17.6 below one whose value
-// is 0 gave 0 instead of 5.0e-4 of theirs).  What is left is the spread inside
-// a tile: 2^-34 of its largest probability.
+// places below the maximum, so that a P is rounded to half a step or to 2^-33 of
+// the row's largest.  That would still lose a row's output where one key
+// outweighs the others while its value is small (22222 keys 17.6 below one
+// whose value is 0: without the 8 places 0 instead of 5.0e-4 of theirs, with
+// them 4e-3 of that off).  Such rows, one key with all but 1/128 of the sum so
+// far, have a lower limit too: a tile that falls below it gets an m of its own,
+// O and l going up.  Rows whose scores are spread by a standard deviation of 5
+// run 17 % longer for both (12: 43 %), others 1 to 2 %, 6 % at 128 channels.
 //
 // Up to 64 channels P has columns of its own: S(j+1) is made while P(j) is
 // still worked out, so a row's warps never wait for a product.  Beyond, P lies
@@ -40,26 +43,16 @@
 
 namespace msda {
 
-// A row's sum over a tile that asks for no new reference m, and m's distance from the maximum.  Every P is at most its
-// tile's sum, 128 equal ones at the maximum are 2^15.
+// When a row's sum over a tile asks for a new reference m, and where that lies.
+// Every P is at most its tile's sum; 128 equal ones at the maximum are 2^15.
 template <bool BF16>
 struct TcForwardRange {
-    static constexpr float kBelow = BF16 ? 0.f : 8.f;
-    static constexpr float kTop = BF16 ? 16384.f : 49152.f;  // f16 holds 65504
-    // f16: sums of a tile between 2^-40 and 2^-5 ask for a lower m (128 values that add up to 2^-5 lose 2^-13 of it at
-    // most), below it is lost in l even 2^16 times over; l < 2^40 before and a step of 2^60 at most keep O below 2^127.
-    static constexpr float kLow = 0x1p-5f, kNothing = 0x1p-40f, kMostL = 0x1p40f, kStep = 60.f;
-    static __device__ __forceinline__ bool fits(float sum, float l) {
-        if constexpr (BF16) return sum <= kTop;
-        return sum <= kTop && (sum >= kLow || sum <= kNothing || l >= kMostL);
-    }
-    // the reference after a tile whose maximum asks for `want`
-    static __device__ __forceinline__ float next(float m, float want, float l) {
-        if constexpr (!BF16) {
-            if (want < m - 12.f && want > m - kStep && l < kMostL) return want;
-        }
-        return fmaxf(m, want);
-    }
+    static constexpr float kTop = BF16 ? 16384.f : 49152.f;  // the largest sum; f16 holds 65504
+    static constexpr float kBelow = BF16 ? 0.f : 8.f;        // m below the maximum
+    // f16, rows that one key outweighs: the smallest sum (128 values that add up to it are off by 2^-11 of it at most), m
+    // below the maximum when it goes down (room for 2^12 above and 2^10 below), and what keeps O under 2^127: l before, m's way.
+    static constexpr float kLow = 0x1p-7f, kBelowLow = 3.f, kMostL = 0x1p40f, kWay = 56.f;
+    static constexpr float kAlone = 0x1p-7f;  // of the largest key's P: what the others add up to at most
 };
 
 template <int NQ, int NC>
@@ -75,6 +68,13 @@ struct TcForwardCfg {
     static constexpr uint32_t kO = kOwnP ? NQ * 192 : NQ * 128;
     static constexpr uint32_t kCols = NQ == 2 ? 512 : 256;
     static constexpr size_t kSmem = (size_t)(NQ + kStages) * kTileBytes + 1024 + 512;
+};
+// Registers of the two warpgroups on the scores and of the third, 504 together of 3 x 168.  Splits measured within 8 % of one
+// another, the best another for each type and width (22223 x 22223, us at 200/104, 208/88, 232/40: f16 at 32 channels
+// 1037, 996, 931, at 128 channels 1459, 1504, 1583; bf16 951, 925, 988 and 1452, 1363, 1523).
+template <bool BF16, int NC>
+struct TcForwardRegs {
+    static constexpr int kUp = BF16 ? 208 : NC == 1 ? 232 : 200, kDown = 504 - 2 * kUp;
 };
 
 struct TcForwardSync {
@@ -157,7 +157,7 @@ __global__ void __launch_bounds__(TcForwardCfg<NQ, NC>::kThreads, 1)
     volatile uint32_t* abort = &sy.abort;
 
     if (warp < NQ * 4) {
-        if constexpr (NQ == 2) tc_regs_up<208>();
+        if constexpr (NQ == 2) tc_regs_up<TcForwardRegs<BF16, NC>::kUp>();
         // ---- softmax: row `row` of tile `t` ----
         const int t = warp >> 2, wl = warp & 3, row = wl * 32 + lane;
         const int q = q0 + t * p.qpt + row / p.G, h = n * p.G + row % p.G;
@@ -171,7 +171,8 @@ __global__ void __launch_bounds__(TcForwardCfg<NQ, NC>::kThreads, 1)
         const uint32_t* bits = a.bits && valid ? a.bits + b * a.bits_sb + h * a.bits_sh + (long long)q * a.W : nullptr;
         const int chunks = (a.D + 15) / 16;
         const uint32_t first = lane == 0;
-        float m = -attn_inf(), l = 0.f;
+        // reference, sum; f16: the sum of a tile that asks for a lower reference (0: none), the largest key's part of l
+        float m = -attn_inf(), l = 0.f, low = 0.f, alone = 0.f;
 #pragma unroll 1
         for (int i = 0; i < nt; ++i) {
             const int j0 = (t0 + i) * kTcRows;
@@ -237,7 +238,7 @@ __global__ void __launch_bounds__(TcForwardCfg<NQ, NC>::kThreads, 1)
                 float sum = 0.f;
                 if (__builtin_expect(!renew, 1)) {
                     sum = probabilities(Cfg::kOwnP && i > 0);
-                    renew = __any_sync(0xffffffffu, valid && !Range::fits(sum, l));
+                    renew = __any_sync(0xffffffffu, valid && !(sum <= Range::kTop && (BF16 || sum >= low)));
                 } else if (Cfg::kOwnP && i > 0) {
                     gone = !tc_bar_wait(tc_smem(&sy.pv_done[t]), (i - 1) & 1, abort, a.err);
                     tc_fence_after();
@@ -251,8 +252,14 @@ __global__ void __launch_bounds__(TcForwardCfg<NQ, NC>::kThreads, 1)
                         for (int k = 2; k < 32; k += 2)
                             mx[c] = tc_max3(mx[c], __uint_as_float(s[c][k]), __uint_as_float(s[c][k + 1]));
                     }
-                    const float next = Range::next(m, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * a.c2 - Range::kBelow, l);
+                    const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * a.c2;
+                    float next = fmaxf(m, top - Range::kBelow);
+                    if constexpr (!BF16) {
+                        if (next > m) alone = exp2f(Range::kBelow);
+                        if (low > 0.f && top < m - 6.f && top > m - Range::kWay) next = top - Range::kBelowLow;
+                    }
                     const float f = next == m ? 1.f : tc_ex2(m - next);
+                    if (!BF16 && next < m) alone *= f;
                     m = next;
                     l *= f;
                     if (i > 0) {
@@ -266,6 +273,7 @@ __global__ void __launch_bounds__(TcForwardCfg<NQ, NC>::kThreads, 1)
                         }
                     }
                     sum = probabilities(false);
+                    if constexpr (!BF16) low = l + sum - alone < alone * Range::kAlone && l < Range::kMostL ? Range::kLow : 0.f;
                 }
                 if (__builtin_expect(gone, 0)) break;
                 l += sum;
@@ -325,7 +333,7 @@ __global__ void __launch_bounds__(TcForwardCfg<NQ, NC>::kThreads, 1)
         }
         if (!ok) tc_drain();
     } else {
-        if constexpr (NQ == 2) tc_regs_down<88>();
+        if constexpr (NQ == 2) tc_regs_down<TcForwardRegs<BF16, NC>::kDown>();
         const int role = warp - NQ * 4;
         bool ok = true;
         if (role == 0 && lane == 0 && nt > 0) {
