@@ -368,8 +368,8 @@ msda_status msda_norm_rotary_backward(msda_dtype dt, unsigned flags, const msda_
  *   out [B, Q, M * D], lse [B, M, Q] float32 (natural logarithm), dense
  *
  * A row that sees no key gives out = 0 and lse = -inf and takes no part in the
- * gradients.  A key that no query sees through key_mask or mask, and in the
- * backward a row without keys, may hold anything, NaN included.  A NaN or
+ * gradients.  A key that no query sees, and in the backward a row without keys,
+ * may hold anything, NaN included.  A NaN or
  * infinity in a value that some query sees reaches every query whose tile of
  * 128 keys holds it, masked or not (0 * NaN), as it does in the matrix form.
  *

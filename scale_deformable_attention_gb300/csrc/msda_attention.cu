@@ -16,7 +16,8 @@
 
 namespace msda {
 
-// One pass over a mask of bytes [Bm, Mm, Q, S].  Writes
+// One pass over a mask of bytes [Bm, Mm, Q, S]; with `causal` a pair that it hides
+// counts as masked.  Writes
 //   live [LB, LN, S] bytes (cleared before): 1 where some query of the heads that
 //     share the key sees it; a key outside it may hold anything, NaN too (every
 //     writer of a byte writes the same 1);
@@ -31,7 +32,7 @@ namespace msda {
 __global__ void __launch_bounds__(128) msda_attention_mask_kernel(const uint8_t* mask, long long mk_sb, long long mk_sh,
                                                                   long long mk_sq, const uint8_t* key_mask,
                                                                   long long km_sb, int Q, int S, int G, int Bm, int Mm,
-                                                                  int LB, int LN, int B, uint8_t* live, uint32_t* bits,
+                                                                  int LB, int LN, int B, int causal, uint8_t* live, uint32_t* bits,
                                                                   uint32_t* bits_t, int W, int Wq, int2* ext_q, int2* ext_k) {
     const int lane = threadIdx.x & 31, j = blockIdx.x * 128 + lane * 4, n = S - j < 4 ? S - j : 4;  // the lane's keys: n > 0 of them
     for (int z = blockIdx.z; z < Bm * Mm; z += gridDim.z) {
@@ -59,7 +60,8 @@ __global__ void __launch_bounds__(128) msda_attention_mask_kernel(const uint8_t*
                 }
 #pragma unroll
                 for (int r = 0; r < 16; ++r) {
-                    const uint32_t four = ((__vcmpne4(v[r], 0u) & 0x08040201u) * 0x01010101u) >> 24;  // a bit a key
+                    uint32_t four = ((__vcmpne4(v[r], 0u) & 0x08040201u) * 0x01010101u) >> 24;  // a bit a key
+                    if (causal) four &= tc_low_bits(q0 + r0 + r + (S - Q) - j + 1);
                     uint32_t w = four << (4 * (lane & 7));
                     w |= __shfl_xor_sync(0xffffffffu, w, 1);
                     w |= __shfl_xor_sync(0xffffffffu, w, 2);
@@ -302,7 +304,7 @@ msda_status make_mask(AttentionArgs& a, const MaskSpace& l, void* ws, msda::TcAr
             const dim3 grid((unsigned)((a.S + 127) / 128), (unsigned)(l.Wq / 4 < 65535 ? l.Wq / 4 : 65535),
                             (unsigned)(z < 65535 ? z : 65535));
             msda::msda_attention_mask_kernel<<<grid, 128, 0, st>>>(a.mask, a.mk_sb, a.mk_sh, a.mk_sq, a.key_mask, a.km_sb, a.Q,
-                                                                   a.S, a.G, l.Bm, l.Mm, l.LB, l.LN, a.B, live, bits, bits_t,
+                                                                   a.S, a.G, l.Bm, l.Mm, l.LB, l.LN, a.B, a.causal, live, bits, bits_t,
                                                                    l.W, l.Wq, ext_q, ext_k);
             e = cudaGetLastError();
         }
