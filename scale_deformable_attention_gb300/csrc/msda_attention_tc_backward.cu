@@ -38,10 +38,10 @@ template <bool BF16>
 __device__ __forceinline__ TcScale tc_scale(const TcArgs& p) {
     TcScale r{1.f, 1.f, 1.f};
     if constexpr (!BF16) {
-        // |dS| <= 2 |dO row| |v row|: the power of two that brings this to 2^14 at most
+        // |dS| <= 2 |dO row| |v row|: the power of two that brings this to 2^15 at most (f16 holds 65504)
         const float top = 2.f * sqrtf(p.scale_in[0]) * sqrtf(p.scale_in[1]);
         int ks = 0;
-        if (top > 0.f && top < 1e30f) ks = 14 - (int)ceilf(log2f(top));
+        if (top > 0.f && top < 1e30f) ks = 15 - (int)ceilf(log2f(top));
         ks = ks < -40 ? -40 : ks > 40 ? 40 : ks;
         r.ds = exp2f(ks - kHalfScale);
         r.inv_p = exp2f(-kHalfScale);

@@ -3,6 +3,7 @@ import math
 
 import pytest
 
+import dense_reference as R
 from test_gpu_attention import DEV, both, msda  # noqa: F401
 
 torch = pytest.importorskip("torch")
@@ -24,3 +25,19 @@ def test_value_gradients_of_small_shares(msda, gap, D):  # noqa: F811
     share = math.exp(-gap) / (1 + (S - 1) * math.exp(-gap))
     want = Q * 256 * share
     assert float((got["grad_value"][:, 1:].double() / want - 1).abs().max()) <= 2 * 2.0 ** -11 + 2.0 ** -12
+
+
+@pytest.mark.parametrize("size", [(3, 1, 5351, 2, 2, 72), (2, 1, 3000, 4, 4, 128)], ids=lambda s: "x".join(map(str, s)))
+@pytest.mark.parametrize("spread", [3, 6])
+def test_key_gradients_of_one_query(msda, size, spread):  # noqa: F811
+    """One query over a long axis, scores spread, gradients of a scaled loss: each key's gradient is one product of a small dS."""
+    B, Q, S, M, N, D = size
+    for seed in range(6):
+        g = torch.Generator(device=DEV).manual_seed(seed)
+        rnd = lambda *s: torch.randn(s, generator=g, device=DEV)   # noqa: E731
+        q, k, v = (rnd(B, Q, M, D) * spread).half(), rnd(B, S, N, D).half(), rnd(B, S, N, D).half()
+        do = (rnd(B, Q, M * D) * 300).half()
+        want = R.attention(q, k, v, do)
+        got = both(msda, q, k, v, do, {})
+        for name in want:
+            R.check(got[name], want[name], name)
