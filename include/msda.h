@@ -369,20 +369,28 @@ msda_status msda_norm_rotary_backward(msda_dtype dt, unsigned flags, const msda_
  *
  * A row that sees no key gives out = 0 and lse = -inf and takes no part in the
  * gradients.  A key that no query sees, and in the backward a row without keys,
- * may hold anything, NaN included.  A NaN or
- * infinity in a value that some query sees reaches every query whose tile of
- * 128 keys holds it, masked or not (0 * NaN), as it does in the matrix form.
+ * may hold anything, NaN included.  A NaN or infinity in a value that some query
+ * sees reaches every query whose tile of 128 keys holds it, masked or not
+ * (0 * NaN), as it does in the matrix form.
  *
- * Statistics, sums and products accumulate in fp32.  For fp16 / bf16 the
- * probabilities, and in the backward the scores' gradients, are rounded to the
- * dtype before their matrix product, as tensor-core products need.  No atomics
- * take part in any sum: results are the same bits every run.
+ * Statistics, sums and products accumulate in fp32.  On the tensor cores the
+ * probabilities of fp16 / bf16, and in the backward the scores' gradients, are
+ * rounded to the dtype before their matrix product, as those products need: an
+ * output is off by about 1.4 times what rounding it once costs.  fp16 has few
+ * small values: a probability is rounded to half a step, or to 2^-33 of the
+ * row's largest (a row whose largest has all but 1/128 of the sum: of the
+ * largest in the tile of 128 keys), in the backward to 2^-39; a score's gradient
+ * to 2^-39 of twice the product of the largest norms of grad_out's and value's
+ * rows.  The backward's probabilities come from lse, whose rounding to fp32 is a
+ * relative error of up to 2^-24 |lse| of each.  No atomics take part in any sum:
+ * results are the same bits every run.
  * 16-bit tensors with D a multiple of 8 and 16-byte aligned addresses and
  * strides run on the tensor cores, others on the FMA pipe.  fp32 with D <= 64
  * and enough pairs runs on the tensor cores too, each value cut into three bf16
  * pieces in the workspace (6 bytes an element of query, key, value and, in the
- * backward, grad_out): as exact as fp32 products, whatever the addresses.  A call
- * with a value beyond 2^60, an infinity or a NaN in a place that takes part (or in
+ * backward, grad_out), whatever the addresses.  What a product of two values
+ * leaves out is below 2^-22 of it, 2^-24 on average, between 2^-100 and 2^60 in
+ * size; sums are rounded as fp32 sums are.  A call with a value beyond 2^60, an infinity or a NaN in a place that takes part (or in
  * a query without keys) runs on the FMA pipe instead, at its speed.
  * A single row of queries and heads a key head (fp32: up to eight) over 256 keys
  * or more runs on the FMA pipe in one pass over the keys.

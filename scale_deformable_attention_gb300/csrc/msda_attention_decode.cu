@@ -11,8 +11,10 @@
 // shuffles.  Each group of L lanes walks its own keys (32 / L a warp at once, U
 // times that loaded a step ahead) with its own running maximum and sum; groups,
 // warps and, through the workspace, blocks are joined in a fixed order.  8 x
-// 22223 keys of 8 heads of 64, one row: bf16 5.6 TB/s, binary32 6.1 TB/s; four
-// rows are bound by the FMA pipe and shuffles (binary32, 2 heads: 3.1 TB/s).
+// 22223 keys of 8 heads of 64, one row: bf16 5.6 TB/s, binary32 6.1 TB/s.  Four
+// rows (binary32, 2 heads) reach 3.1 TB/s: a dot product takes log2(L) shuffles a
+// row, and four blocks an SM leave 128 registers, of which four rows spill up to
+// 80 bytes and eight up to 268.
 #include "msda_attention.cuh"
 #include "msda_attention_decode.cuh"
 

@@ -8,8 +8,10 @@
 // Gradients, with dz = R^T dy (the rotation by -t) and n = x r:
 //   dx = r (w dz - n mean(n w dz)),   dw = sum over rows of n dz.
 //
-// What bounds it: memory.  Every element is read once (twice in the backward:
-// x and dy) and written once.  All heads of a token share its angles, so in the
+// What bounds it: memory, then issue.  Every element is read once (twice in the
+// backward: x and dy) and written once, at 55 % of the DRAM's rate under a
+// profiler with 63 to 71 % of the issue slots taken (conversions and selects on
+// the ALU 39 to 45 %, FMA pipe 26 to 31 %) by 16 to 28 warps an SM.  All heads of a token share its angles, so in the
 // vector form a lane owns 16 bytes of channels of one token, works out their cos
 // and sin once in registers and walks the heads: several 16-byte loads in
 // flight a lane, no shared memory, no barrier.  In halves a pair's two channels
