@@ -434,6 +434,109 @@ msda_status msda_attention_backward(msda_dtype dt, unsigned flags, const msda_at
                                     void* grad_query, void* grad_key, void* grad_value, void* workspace,
                                     size_t workspace_bytes, msda_stream_t stream);
 
+/*
+ * A paged cache of keys and values: pages of `page` tokens (a power of two, 16
+ * or more) that sequences take one by one, in 16 or 32 bits or quantised to 8 as
+ * they are written.  Token i of sequence b lies in page table[b, i / page], place
+ * i % page.
+ *
+ *   cache key, cache value [pages, page, N, D]: rows of D contiguous elements at
+ *       the given strides (elements; page, token, head); each row begins at a
+ *       multiple of 16 bytes, D is a multiple of 16 up to 128
+ *   format MSDA_CACHE_SAME: elements of the call's dtype
+ *   format MSDA_CACHE_E4M3, MSDA_CACHE_INT8: codes of 8 bits, and for each row
+ *       (token and head) a byte of key scale and value scale [pages, page, N] at
+ *       the given strides: the row is code * 2^(byte - 127); byte 255: the row
+ *       held an infinity or a NaN, and is NaN; byte 0: zeros
+ *   table [B, width] int32 (rows contiguous, table_stride between sequences): page
+ *       numbers; only those of tokens that are written or read are looked at
+ *
+ * Lengths, starts, counts, page numbers and selected tokens are on the device
+ * and are checked there: a sequence's length or count outside its range is
+ * brought into it, a token whose page number, place or selection lies outside is
+ * neither written nor read (read: zeros; attention: not seen), and each raises
+ * bit 3 of msda_device_errors().
+ */
+typedef struct {
+    int64_t B, T, M, N, D;      /* sequences, tokens of each in this call, query heads, key heads, channels */
+    int64_t source;             /* tokens of key and value */
+    int64_t pages, page, width; /* of the cache and the table */
+    int64_t longest;            /* tokens that a sequence has in the cache at most: width * page or less */
+    int64_t cache_key_stride[3], cache_value_stride[3];  /* page, token, head; elements */
+    int64_t key_scale_stride[3], value_scale_stride[3];  /* page, token, head; bytes */
+    int64_t table_stride;
+    int64_t query_stride[3], key_stride[3], value_stride[3]; /* sequence, token, head; elements */
+    int64_t mask_stride[2];     /* sequence (0: shared), query; keys contiguous */
+    int64_t select_stride;
+} msda_cache_problem;
+
+enum { MSDA_CACHE_SAME = 0, MSDA_CACHE_E4M3 = 1, MSDA_CACHE_INT8 = 2 };
+
+/*
+ * Writes rows r < counts[b] (all T if counts is NULL) of each sequence: token
+ * start[b] + r of the cache becomes token select[b, r] (r if select is NULL) of
+ * key and value [B, source, N, D].  What else the pages hold stays.
+ *
+ * Quantised rows: with m the row's largest magnitude, the scale is the least
+ * power of two s >= 2^-100 with m <= 448 s (e4m3) or m <= 127 s (int8), a code
+ * the nearest to x / s, ties to even: x is off by at most half a step of its
+ * code, 2^-4 of it (e4m3, down to 2^-6 s) or s / 2 (int8).  A power of two
+ * costs e4m3 nothing (its steps follow the value) and makes every code times its
+ * scale a value that 16 bits hold.
+ * Two sequences that write the same place in one call leave either's row.
+ */
+msda_status msda_cache_write(msda_dtype dt, int format, const msda_cache_problem* problem, const void* key,
+                             const void* value, const int32_t* table, const int32_t* start, const int32_t* counts,
+                             const int32_t* select, void* cache_key, void* cache_value, uint8_t* key_scale,
+                             uint8_t* value_scale, msda_stream_t stream);
+
+/* key, value [B, T, N, D], dense, 16-byte aligned: the first T tokens of each sequence, zeros from lengths[b] on;
+ * quantised rows are code * scale rounded once to the dtype, the dtype's largest value where that is beyond its range
+ * (a row written from finite values is read back finite). */
+msda_status msda_cache_read(msda_dtype dt, int format, const msda_cache_problem* problem, const void* cache_key,
+                            const void* cache_value, const uint8_t* key_scale, const uint8_t* value_scale,
+                            const int32_t* table, const int32_t* lengths, void* key, void* value, msda_stream_t stream);
+
+/*
+ * Softmax attention of new tokens over the cache: one token, a tree of drafted
+ * ones, or a piece of a prompt.  Query t of sequence b sees the tokens
+ * i < lengths[b] of the cache and, if source is T (key and value [B, T, N, D],
+ * the new tokens' own, unquantised, not yet in the cache), the new tokens j <
+ * counts[b] with mask[b, t, j] != 0, or j <= t where mask is NULL; source 0: the
+ * cache alone.
+ *
+ *   s = scale <query, key>,  lse = log sum exp s,  out = sum exp(s - lse) value
+ *
+ *   query [B, T, M, D], out [B, T, M * D] and lse [B, M, T] as in
+ *       msda_attention_forward; M / N query heads share a key head
+ *   mask [B or 1, T, T] bytes; counts [B] or NULL: rows t >= counts[b] are
+ *       padding and give zeros and lse = -inf, as does a row that sees nothing.
+ *       Padding may hold anything, NaN included, and so may what the cache holds
+ *       behind lengths[b].  A NaN or infinity in a value that some query of a
+ *       sequence sees reaches those that do not (0 * NaN), as in the matrix form.
+ *
+ * Sums, statistics and products accumulate in fp32.  Probabilities are rounded
+ * to 16 bits for their product: those of fp16 and of quantised caches to fp16
+ * (half a step, or 2^-30 of a row's largest), bf16 over a bf16 cache to bf16; fp32
+ * runs in two fp16 pieces (quantised) or three bf16 pieces a value, products
+ * below 2^-22 of a value left out.  fp16 pieces: a quantised value below 2^-24
+ * of the largest value that its warp meets loses bits.  No atomics take part in a sum: equal
+ * calls give equal bits; the order depends on the sizes and lengths.
+ *
+ * `longest` plans the launch; a smaller bound on the lengths than the table's
+ * saves blocks and, for short sequences, the joining launch.
+ * Requirements: N divides M; scale > 0.  B == 0 or T == 0 enqueue nothing.
+ * workspace: msda_cache_attention_workspace_size() bytes (0 for many sizes: then
+ * it may be NULL), 256-byte aligned; not shared by calls that can overlap.
+ */
+size_t msda_cache_attention_workspace_size(msda_dtype dt, int format, const msda_cache_problem* problem);
+msda_status msda_cache_attention(msda_dtype dt, int format, const msda_cache_problem* problem, double scale,
+                                 const void* query, const void* cache_key, const void* cache_value,
+                                 const uint8_t* key_scale, const uint8_t* value_scale, const int32_t* table,
+                                 const int32_t* lengths, const void* key, const void* value, const uint8_t* mask,
+                                 const int32_t* counts, void* out, float* lse, void* workspace, size_t workspace_bytes,
+                                 msda_stream_t stream);
+
 /* Message for the last non-OK status returned on the calling thread ("" if none). */
 const char* msda_last_error(void);
 
@@ -443,7 +546,8 @@ const char* msda_status_string(msda_status s);
 /* Device-side error bits raised by kernels on the current device since the
  * last clear (bit 0: a level failed its shape check; bit 1: a parameter copy
  * timed out; bit 2: a wait inside a tensor-core attention kernel gave up and its
- * output is not valid).  Synchronises the
+ * output is not valid; bit 3: a length, count, page number or selected token of
+ * the paged cache was outside its range).  Synchronises the
  * device.  clear != 0 resets the bits. */
 msda_status msda_device_errors(uint32_t* bits, int clear);
 
@@ -497,7 +601,8 @@ enum { MSDA_KERNEL_FORWARD = 0, MSDA_KERNEL_BACKWARD = 1, MSDA_KERNEL_ZERO = 2, 
        MSDA_KERNEL_ROTARY = 9, MSDA_KERNEL_ROTARY_BACKWARD = 10, MSDA_KERNEL_ATTENTION = 11,
        MSDA_KERNEL_ATTENTION_JOIN = 12, MSDA_KERNEL_ATTENTION_MASK = 13, MSDA_KERNEL_ATTENTION_PREPARE = 14,
        MSDA_KERNEL_ATTENTION_GRAD_KEY = 15, MSDA_KERNEL_ATTENTION_GRAD_QUERY = 16,
-       MSDA_KERNEL_ATTENTION_SPLIT = 17, MSDA_KERNEL_COUNT = 18 };
+       MSDA_KERNEL_ATTENTION_SPLIT = 17, MSDA_KERNEL_CACHE_WRITE = 18, MSDA_KERNEL_CACHE_READ = 19,
+       MSDA_KERNEL_CACHE_ATTENTION = 20, MSDA_KERNEL_CACHE_JOIN = 21, MSDA_KERNEL_COUNT = 22 };
 
 msda_status msda_trace_enable(int capacity);
 /* Pause (paused != 0) or resume recording without destroying the events:

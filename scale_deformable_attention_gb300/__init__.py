@@ -23,6 +23,10 @@ Entry points:
 * ``rotary(...)``, ``norm_rotary(...)`` and their ``_forward`` / ``_backward``
   -- rotary positions with several axes, alone and behind the norm of queries
   and keys per head;
+* ``PagedCache``, ``cache_create(...)``, ``cache_write(...)``, ``cache_read(...)``
+  and ``cache_attention(...)`` -- a paged cache of keys and values, in the
+  tensors' type or quantised to 8 bits as it is written, and the attention of
+  new tokens (one, a drafted tree, a piece of a prompt) over it;
 * ``device_errors()``, ``trace_enable()`` / ``trace_read()`` -- diagnostics;
 * ``reduction_ceiling()`` -- the L2's rate for the backward's reduction
   traffic, for roofline reporting.
@@ -39,6 +43,7 @@ import torch
 from . import _lib
 from ._attention import attention, attention_backward, attention_forward
 from ._binding import workspace_of
+from ._cache import PagedCache, cache_attention, cache_create, cache_read, cache_write
 from ._lib import ACCUM, BWD_ACCUMULATE, BWD_WORKSPACE_ZEROED, MsdaError
 from ._rotary import norm_rotary, norm_rotary_backward, norm_rotary_forward, rotary, rotary_backward, rotary_forward
 
@@ -46,6 +51,7 @@ __all__ = ["multi_scale_deformable_attention", "multi_scale_deformable_attention
            "forward_fused", "backward_fused", "workspace_size", "resolve_accum",
            "attention", "attention_forward", "attention_backward", "rotary", "rotary_forward", "rotary_backward",
            "norm_rotary", "norm_rotary_forward", "norm_rotary_backward",
+           "PagedCache", "cache_create", "cache_write", "cache_read", "cache_attention",
            "device_errors", "trace_enable", "trace_pause", "trace_read", "MsdaError", "DTYPE_CODE"]
 
 DTYPE_CODE = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}

@@ -23,15 +23,18 @@ BWD_WORKSPACE_ZEROED = 2
 KERNEL_NAMES = {0: "forward", 1: "backward", 2: "zero", 3: "convert", 4: "tile_count", 5: "tile_scan",
                 6: "tile_place", 7: "tile_accum", 8: "touch_count", 9: "rotary", 10: "rotary_backward", 11: "attention",
                 12: "attention_join", 13: "attention_mask", 14: "attention_prepare", 15: "attention_grad_key",
-                16: "attention_grad_query", 17: "attention_split"}
+                16: "attention_grad_query", 17: "attention_split", 18: "cache_write", 19: "cache_read",
+                20: "cache_attention", 21: "cache_join"}
 ROTARY_INTERLEAVED = 1
 ROTARY_INVERSE = 2
 ATTENTION_CAUSAL = 1
 ATTENTION_KEY_MASK = 2
 ATTENTION_MASK = 4
+CACHE_SAME, CACHE_E4M3, CACHE_INT8 = 0, 1, 2
 # the problem structs of include/msda.h: nothing but int64 members, so a flat array lays them out
 RotaryProblem = ctypes.c_int64 * 18
 AttentionProblem = ctypes.c_int64 * 19
+CacheProblem = ctypes.c_int64 * 35
 
 
 class MsdaError(RuntimeError):
@@ -81,6 +84,14 @@ def _declare(lib):
     for f in (lib.msda_attention_forward_workspace_size, lib.msda_attention_backward_workspace_size):
         f.argtypes = [c_int, c_uint, vp]
         f.restype = sz
+    lib.msda_cache_write.argtypes = [c_int, c_int, vp] + [vp] * 11
+    lib.msda_cache_write.restype = c_int
+    lib.msda_cache_read.argtypes = [c_int, c_int, vp] + [vp] * 9
+    lib.msda_cache_read.restype = c_int
+    lib.msda_cache_attention.argtypes = [c_int, c_int, vp, f64] + [vp] * 14 + [sz, vp]
+    lib.msda_cache_attention.restype = c_int
+    lib.msda_cache_attention_workspace_size.argtypes = [c_int, c_int, vp]
+    lib.msda_cache_attention_workspace_size.restype = sz
     lib.msda_last_error.restype = ctypes.c_char_p
     lib.msda_status_string.argtypes = [c_int]
     lib.msda_status_string.restype = ctypes.c_char_p

@@ -832,6 +832,10 @@ const char* msda_kernel_name(int k) {
     case MSDA_KERNEL_ATTENTION_GRAD_KEY: return "attention_grad_key";
     case MSDA_KERNEL_ATTENTION_GRAD_QUERY: return "attention_grad_query";
     case MSDA_KERNEL_ATTENTION_SPLIT: return "attention_split";
+    case MSDA_KERNEL_CACHE_WRITE: return "cache_write";
+    case MSDA_KERNEL_CACHE_READ: return "cache_read";
+    case MSDA_KERNEL_CACHE_ATTENTION: return "cache_attention";
+    case MSDA_KERNEL_CACHE_JOIN: return "cache_join";
     }
     return "unknown";
 }

@@ -1,0 +1,758 @@
+// msda_cache_rows.cuh -- attention over the paged cache of few rows a key head
+// (queries times the heads that share the key head: tiles of 16 or 32).
+//
+//   s = c Q K^T,  P = 2^(s - m),  l += row sums,  O += P V
+//
+// What bounds it: reading K and V once.  A block of four warps takes a share of
+// the keys of one key head (see the plan); a warp walks its own steps of KS keys
+// with its own reference m and sum l, fed by its own ring in shared memory
+// (cp.async, no barrier of the block inside the loop), and the warps are joined
+// at the end in a fixed order.  The products are mma.sync m16n8k16: with 16 rows
+// tcgen05 would fill an eighth of its tile of 128, and its chain of product,
+// tensor memory, exponentials and product takes 1 us a tile.
+//
+// Which channel a place of a product's contraction holds is free as long as both
+// operands agree.  So a lane reads 16 bytes of a key in one load and uses them
+// for 4, 2 or 1 steps of K, and of V it reads the same 16 bytes of channels of
+// the four keys that it has in a step of 16, which one byte permutation a
+// register brings next to each other: no transposing load.  16-byte chunks of a
+// row are swizzled by the row so that both reads are free of bank conflicts.
+//
+// Types.  16 bits: as they are.  8 bits: codes are whole f16 values, so the
+// product is of f16 whatever the queries are; these are scaled by a power of two
+// a row (bf16 has fewer bits than f16, binary32 takes two pieces), the scales of
+// keys multiply the scores, those of values the probabilities, relative to the
+// largest that the warp has met.  binary32: three bf16 pieces a value, six
+// products, the small ones first, summed anew each step (a tensor core cuts its
+// sums off).  P is rounded to 16 bits for its product (binary32: 2 pieces of f16
+// or 3 of bf16).  f16 P: m lies 2^6 below the row's maximum when it was looked
+// for, and is looked for again when a score passes 2^14 of it: a P is off by half a
+// step or 2^-31 of the row's largest.
+#pragma once
+
+#include "msda_cache.cuh"
+#include "msda_host.cuh"
+
+namespace msda {
+
+constexpr int kCacheWarps = 4;
+
+template <typename T>
+struct CacheType;
+template <>
+struct CacheType<float> {
+    static constexpr int code = 0;
+    static __device__ __forceinline__ float get(float x) { return x; }
+    static __device__ __forceinline__ float put(float x) { return x; }
+};
+template <>
+struct CacheType<__half> {
+    static constexpr int code = 1;
+    static __device__ __forceinline__ float get(__half x) { return __half2float(x); }
+    static __device__ __forceinline__ __half put(float x) { return __float2half_rn(x); }
+};
+template <>
+struct CacheType<__nv_bfloat16> {
+    static constexpr int code = 2;
+    static __device__ __forceinline__ float get(__nv_bfloat16 x) { return __bfloat162float(x); }
+    static __device__ __forceinline__ __nv_bfloat16 put(float x) { return __float2bfloat16_rn(x); }
+};
+
+// How a product runs for queries T over rows of format F: in bf16 or f16, and in how many pieces.
+template <typename T, int F>
+struct CacheProduct {
+    static constexpr bool f32 = sizeof(T) == 4;
+    static constexpr bool bf16 = F == kCacheSame && CacheType<T>::code != 1;
+    static constexpr int es = F == kCacheSame ? (int)sizeof(T) : 1;
+    static constexpr int qp = !f32 ? 1 : F == kCacheSame ? 3 : 2, kp = f32 && F == kCacheSame ? 3 : 1, pp = qp;
+    static constexpr float below = bf16 ? 0.f : 6.f;  // m below the maximum, in binary places
+};
+constexpr float kCacheAbove = 14.f;  // how far a score may pass m
+
+template <typename T, int F, int DP, int MT>
+struct CacheRowsCfg {
+    using P = CacheProduct<T, F>;
+    static constexpr int E = 16 / P::es;                  // channels a 16-byte chunk
+    static constexpr int RB = DP * P::es, CH = RB / 16;   // bytes and chunks a row
+    static constexpr int EV = DP / 8 < E ? DP / 8 : E;    // channels of V a lane has at a time
+    static constexpr int KS = RB >= 256 ? 16 : 32;        // keys a step
+    static constexpr int kStage = 2 * KS * RB;
+    static constexpr int kStages = 3;
+    static constexpr int kTailStage = 2 * 16 * DP * (int)sizeof(T);
+    static constexpr int kRing = kStages * kStage > kTailStage ? kStages * kStage : kTailStage;
+    static constexpr int kTailStages = F == kCacheSame ? kStages : kRing / kTailStage >= 2 ? 2 : 1;
+    static constexpr int kTailKeys = F == kCacheSame ? KS : 16;
+    static constexpr int kFragments = MT * (DP / 16) * 32 * 16;  // bytes of a piece of the queries
+    static constexpr int kQ = kFragments * (P::qp + (F == kCacheSame ? 0 : CacheProduct<T, kCacheSame>::qp));
+    static constexpr int kOut = kCacheWarps * MT * 16 * (DP + 4) * 4;  // the warps' parts, over the ring
+    static constexpr int kSmem = kQ + (kCacheWarps * kRing > kOut ? kCacheWarps * kRing : kOut);
+    static constexpr int kResident = kSmem > 111 * 1024 ? 1 : kSmem > 73 * 1024 ? 2 : 3;
+};
+
+__device__ __forceinline__ uint32_t cache_smem(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
+__device__ __forceinline__ void cache_copy16(uint32_t dst, const void* src, uint32_t bytes) {  // bytes: 16, or 0 for zeros
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cache_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cache_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+template <bool BF16>
+__device__ __forceinline__ void cache_mma(float (&d)[4], const uint4& a, uint32_t b0, uint32_t b1) {
+    if constexpr (BF16)
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+            : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1));
+    else
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+            : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1));
+}
+template <bool BF16>
+__device__ __forceinline__ uint32_t cache_pack(float lo, float hi) {
+    uint32_t r;
+    if constexpr (BF16)
+        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    else
+        asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+template <bool BF16>
+__device__ __forceinline__ float2 cache_unpack(uint32_t v) {
+    if constexpr (BF16) return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u));
+    return __half22float2(*reinterpret_cast<const __half2*>(&v));
+}
+// two values in N pieces of 16 bits, each what the ones before leave, rounded
+template <bool BF16, int N>
+__device__ __forceinline__ void cache_pieces(float lo, float hi, uint32_t (&p)[N]) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        p[i] = cache_pack<BF16>(lo, hi);
+        if (i + 1 < N) {
+            const float2 f = cache_unpack<BF16>(p[i]);
+            lo -= f.x, hi -= f.y;
+        }
+    }
+}
+__device__ __forceinline__ float cache_ex2(float x) {  // 2 units in the last place; 0 for -inf
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// Where a row's 16-byte chunk lies in a stage (rows of RB bytes).  Both reads take eight lanes at a time: K two rows (2k, 2k + 1) of
+// chunks 0..3 or 4..7, V four rows (all even or all odd) of two chunks that follow one another.
+template <int RB>
+__device__ __forceinline__ int cache_chunk(int row, int chunk) {
+    if constexpr (RB == 64) {
+        return (row >> 1) * 128 + (((((row & 1) << 2) | chunk) ^ (((row >> 1) & 3) << 1)) << 4);
+    } else {
+        const int f = (((row >> 1) & 3) << 1) ^ ((row & 1) << 2);
+        return row * RB + ((chunk ^ f) << 4);  // f < 8: stays within the row's line of 128 bytes
+    }
+}
+
+// The state of a warp's rows: MT tiles of 16, of each the rows lane / 4 and lane / 4 + 8.
+template <int DP, int MT>
+struct CacheState {
+    float o[MT][DP / 8][4];
+    float m[MT][2], l[MT][2];
+    uint32_t top;  // 8 bits: O is in units of the scale of this byte (the largest met)
+};
+
+// One walk over steps of KS keys: over the cache in format F, or (TAIL) over the new tokens in the queries' type.  E, EV: which
+// channels a lane has, those of the cache's format in both.
+template <typename T, int F, int DP, int MT, int E, int EV, int KS, int STAGES, bool TAIL>
+struct CacheWalk {
+    using P = CacheProduct<T, F>;
+    static constexpr int RB = DP * P::es, CH = RB / 16, EC = 16 / P::es, NT = KS / 8, GR = KS / 16, SETS = DP / (8 * EV);
+    static constexpr int kStage = 2 * KS * RB;
+
+    const CacheArgs& a;
+    const CacheUnit& u;
+    unsigned char* ring;
+    const uint4* qf;      // fragments [piece][MT][DP / 16][32]
+    const float* factor;  // [MT * 16]: what scores of a row are multiplied by
+    int lane, warp, first, steps, step_keys;  // this warp's steps begin at keys first, first + step_keys, ...
+    // pages of this warp's groups of 16 keys, 32 of them at a time in the lanes, and the next 32
+    int here, next, have;
+
+    __device__ __forceinline__ int group_page(int gi) const {
+        const int token = first + (gi / GR) * step_keys + (gi % GR) * 16;
+        return gi < steps * GR && token < u.length ? cache_page(a.c, u.b, token) : -1;
+    }
+    __device__ __forceinline__ void begin() {
+        if constexpr (!TAIL) {
+            have = 0;
+            here = group_page(lane);
+            next = group_page(32 + lane);
+        }
+    }
+    // page of group gi: asked for in ascending order
+    __device__ __forceinline__ int page_of(int gi) {
+        if (gi >= have + 32) {
+            have += 32;
+            here = next;
+            next = group_page(have + 32 + lane);
+        }
+        return __shfl_sync(0xffffffffu, here, gi & 31);
+    }
+
+    // Starts the copies of step i, and reads the bytes of its scales (lane: key); which groups of 16 keys are there.
+    __device__ __forceinline__ void issue(int i, uint32_t& bytes, uint32_t& there) {
+        bytes = 0, there = 0;
+        const uint32_t dst = cache_smem(ring) + (uint32_t)(i % STAGES) * kStage;
+        const int key0 = first + i * step_keys;
+        if constexpr (TAIL) {
+            const T* k = static_cast<const T*>(a.nk) + u.b * a.nk_sb + u.n * a.nk_sh;
+            const T* v = static_cast<const T*>(a.nv) + u.b * a.nv_sb + u.n * a.nv_sh;
+#pragma unroll
+            for (int x = lane; x < KS * CH; x += 32) {
+                const int row = x / CH, chunk = x % CH, j = key0 + row;
+                const bool in = j < u.count && chunk * EC < a.D;
+                const uint32_t at = dst + cache_chunk<RB>(row, chunk);
+                cache_copy16(at, in ? k + j * a.nk_st + chunk * EC : k, in ? 16 : 0);
+                cache_copy16(at + KS * RB, in ? v + j * a.nv_st + chunk * EC : v, in ? 16 : 0);
+            }
+            there = ~0u;
+        } else {
+            const char* kb = static_cast<const char*>(a.c.k) + (u.n * a.c.k_sh) * P::es;
+            const char* vb = static_cast<const char*>(a.c.v) + (u.n * a.c.v_sh) * P::es;
+#pragma unroll
+            for (int g = 0; g < GR; ++g) {
+                const int page = page_of(i * GR + g), token = key0 + g * 16, left = u.length - token;
+                if (page >= 0) there |= 1u << g;
+                const long long p = page < 0 ? 0 : page;
+                const int in_page = page < 0 ? 0 : token & (a.c.page - 1);
+                const char* k = kb + (p * a.c.k_sp + in_page * a.c.k_st) * P::es;
+                const char* v = vb + (p * a.c.v_sp + in_page * a.c.v_st) * P::es;
+#pragma unroll
+                for (int x = lane; x < 16 * CH; x += 32) {
+                    const int row = x / CH, chunk = x % CH;
+                    const bool in = page >= 0 && row < left && chunk * EC < a.D;
+                    const uint32_t at = dst + cache_chunk<RB>(g * 16 + row, chunk);
+                    cache_copy16(at, in ? k + row * a.c.k_st * P::es + chunk * 16 : k, in ? 16 : 0);
+                    cache_copy16(at + KS * RB, in ? v + row * a.c.v_st * P::es + chunk * 16 : v, in ? 16 : 0);
+                }
+                if constexpr (F != kCacheSame) {
+                    const int row = lane - g * 16;
+                    if (page >= 0 && row >= 0 && row < 16 && row < left) {
+                        bytes = a.c.ks[p * a.c.ks_sp + (in_page + row) * a.c.ks_st + u.n * a.c.ks_sh];
+                        bytes |= (uint32_t)a.c.vs[p * a.c.vs_sp + (in_page + row) * a.c.vs_st + u.n * a.c.vs_sh] << 8;
+                    }
+                }
+            }
+        }
+    }
+
+    // the four channels of key `row` that this lane has at K step s, as N-piece operands
+    __device__ __forceinline__ void k_operand(const unsigned char* k, int row, int s, uint32_t (&b)[P::kp][2]) const {
+        const int c = lane & 3, ch = E * (c + 4 * (s / (E / 4))) + 4 * (s % (E / 4));
+        const unsigned char* at = k + cache_chunk<RB>(row, ch / EC) + (ch % EC) * P::es;
+        if constexpr (P::es == 4) {
+            const float4 x = *reinterpret_cast<const float4*>(at);
+            uint32_t lo[3], hi[3];
+            cache_pieces<true, 3>(x.x, x.y, lo);
+            cache_pieces<true, 3>(x.z, x.w, hi);
+#pragma unroll
+            for (int i = 0; i < 3; ++i) b[i][0] = lo[i], b[i][1] = hi[i];
+        } else if constexpr (P::es == 2) {
+            const uint2 x = *reinterpret_cast<const uint2*>(at);
+            b[0][0] = x.x, b[0][1] = x.y;
+        } else {
+            cache_four_f16<F>(*reinterpret_cast<const uint32_t*>(at), b[0][0], b[0][1]);
+        }
+    }
+
+    __device__ __forceinline__ void scores(const unsigned char* k, float (&s)[MT][NT][4]) const {
+        const int g = lane >> 2;
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+#pragma unroll
+            for (int j = 0; j < NT; ++j)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) s[i][j][e] = 0.f;
+        constexpr int STEPS = DP / 16;
+        if constexpr (E == EC && P::es < 4) {  // a 16-byte chunk at a time: E / 4 steps
+#pragma unroll
+            for (int i = 0; i < STEPS / (E / 4); ++i) {
+                uint4 x[NT];
+#pragma unroll
+                for (int j = 0; j < NT; ++j)
+                    x[j] = *reinterpret_cast<const uint4*>(k + cache_chunk<RB>(j * 8 + g, (lane & 3) + 4 * i));
+#pragma unroll
+                for (int h = 0; h < E / 4; ++h) {
+                    const int st = i * (E / 4) + h;
+                    uint4 q[P::qp][MT];
+#pragma unroll
+                    for (int p = 0; p < P::qp; ++p)
+#pragma unroll
+                        for (int t = 0; t < MT; ++t) q[p][t] = qf[((p * MT + t) * STEPS + st) * 32 + lane];
+#pragma unroll
+                    for (int j = 0; j < NT; ++j) {
+                        const uint32_t w[4] = {x[j].x, x[j].y, x[j].z, x[j].w};
+                        uint32_t b0, b1;
+                        if constexpr (P::es == 2) b0 = w[2 * h], b1 = w[2 * h + 1];
+                        else cache_four_f16<F>(w[h], b0, b1);
+#pragma unroll
+                        for (int p = P::qp - 1; p >= 0; --p)
+#pragma unroll
+                            for (int t = 0; t < MT; ++t) cache_mma<P::bf16>(s[t][j], q[p][t], b0, b1);
+                    }
+                }
+            }
+        } else {
+#pragma unroll
+            for (int st = 0; st < STEPS; ++st) {
+                uint4 q[P::qp][MT];
+#pragma unroll
+                for (int p = 0; p < P::qp; ++p)
+#pragma unroll
+                    for (int t = 0; t < MT; ++t) q[p][t] = qf[((p * MT + t) * STEPS + st) * 32 + lane];
+#pragma unroll
+                for (int j = 0; j < NT; ++j) {
+                    uint32_t b[P::kp][2];
+                    k_operand(k, j * 8 + g, st, b);
+#pragma unroll
+                    for (int sum = P::kp == 1 ? P::qp - 1 : 2; sum >= 0; --sum)  // pieces x and y with x + y = sum: small products first
+#pragma unroll
+                        for (int x = sum; x >= 0; --x)
+                            if (x < P::qp && sum - x < P::kp)
+#pragma unroll
+                                for (int t = 0; t < MT; ++t) cache_mma<P::bf16>(s[t][j], q[x][t], b[sum - x][0], b[sum - x][1]);
+                }
+            }
+        }
+    }
+
+    // O += P V for the keys 16 kk .. 16 kk + 15
+    __device__ __forceinline__ void outputs(const unsigned char* v, int kk, const uint4 (&p)[P::pp][MT], CacheState<DP, MT>& z) const {
+        const int g = lane >> 2, c = lane & 3;
+        constexpr int WORDS = EV * P::es / 4;
+#pragma unroll
+        for (int set = 0; set < SETS; ++set) {
+            uint32_t w[4][WORDS];
+            const int ch = E == EV ? E * (g + 8 * set) : EV * g;
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const int row = kk * 16 + 2 * c + (r & 1) + (r >> 1) * 8;
+                if constexpr (WORDS == 2) {
+                    const uint2 x = *reinterpret_cast<const uint2*>(v + cache_chunk<RB>(row, ch / EC) + (ch % EC) * P::es);
+                    w[r][0] = x.x, w[r][1] = x.y;
+                } else {
+#pragma unroll
+                    for (int i = 0; i < WORDS / 4; ++i) {
+                        const uint4 x = *reinterpret_cast<const uint4*>(v + cache_chunk<RB>(row, ch / EC + i));
+                        w[r][4 * i] = x.x, w[r][4 * i + 1] = x.y, w[r][4 * i + 2] = x.z, w[r][4 * i + 3] = x.w;
+                    }
+                }
+            }
+            if constexpr (P::es == 2) {
+#pragma unroll
+                for (int j = 0; j < EV; ++j) {
+                    const int sel = (j & 1) ? 0x7632 : 0x5410;
+                    const uint32_t b0 = __byte_perm(w[0][j / 2], w[1][j / 2], sel), b1 = __byte_perm(w[2][j / 2], w[3][j / 2], sel);
+#pragma unroll
+                    for (int t = 0; t < MT; ++t) cache_mma<P::bf16>(z.o[t][set * EV + j], p[0][t], b0, b1);
+                }
+            } else if constexpr (P::es == 1) {
+#pragma unroll
+                for (int j = 0; j < EV; j += 4) {
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {  // channels j + 2h and j + 2h + 1: key, next key, key, next key
+                        const int sel = h ? 0x7362 : 0x5140;
+                        uint32_t x0, x1, y0, y1;
+                        cache_four_f16<F>(__byte_perm(w[0][j / 4], w[1][j / 4], sel), x0, x1);
+                        cache_four_f16<F>(__byte_perm(w[2][j / 4], w[3][j / 4], sel), y0, y1);
+#pragma unroll
+                        for (int i = P::pp - 1; i >= 0; --i)
+#pragma unroll
+                            for (int t = 0; t < MT; ++t) {
+                                cache_mma<P::bf16>(z.o[t][set * EV + j + 2 * h], p[i][t], x0, y0);
+                                cache_mma<P::bf16>(z.o[t][set * EV + j + 2 * h + 1], p[i][t], x1, y1);
+                            }
+                    }
+                }
+            } else {
+#pragma unroll
+                for (int j = 0; j < EV; ++j) {
+                    uint32_t b0[3], b1[3];
+                    cache_pieces<true, 3>(__uint_as_float(w[0][j]), __uint_as_float(w[1][j]), b0);
+                    cache_pieces<true, 3>(__uint_as_float(w[2][j]), __uint_as_float(w[3][j]), b1);
+#pragma unroll
+                    for (int t = 0; t < MT; ++t) {
+                        float d[4] = {0.f, 0.f, 0.f, 0.f};  // a step's products start anew and are added in binary32
+#pragma unroll
+                        for (int sum = 2; sum >= 0; --sum)
+#pragma unroll
+                            for (int x = sum; x >= 0; --x) cache_mma<true>(d, p[x][t], b0[sum - x], b1[sum - x]);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) z.o[t][set * EV + j][e] += d[e];
+                    }
+                }
+            }
+        }
+    }
+
+    __device__ __forceinline__ void compute(int i, uint32_t bytes, uint32_t there, CacheState<DP, MT>& z) {
+        const unsigned char* k = ring + (i % STAGES) * kStage;
+        const unsigned char* v = k + KS * RB;
+        const int g = lane >> 2, c = lane & 3, key0 = first + i * step_keys;
+        float s[MT][NT][4];
+        scores(k, s);
+        float ks[NT][2], vs[NT][2];  // scales of the keys 8 j + 2 c and the next
+        if constexpr (F != kCacheSame) {
+            const uint32_t mine = (bytes >> 8) == 255u ? 0u : bytes >> 8;
+            const uint32_t top = __reduce_max_sync(0xffffffffu, mine);
+            if (top > z.top) {
+                const float f = z.top + 126 < top ? 0.f : cache_scale(127 + z.top - top);
+                z.top = top;
+#pragma unroll
+                for (int t = 0; t < MT; ++t)
+#pragma unroll
+                    for (int d = 0; d < DP / 8; ++d)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) z.o[t][d][e] *= f;
+            }
+#pragma unroll
+            for (int j = 0; j < NT; ++j)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const uint32_t y = __shfl_sync(0xffffffffu, bytes, j * 8 + 2 * c + e), w = y >> 8;
+                    ks[j][e] = cache_scale(y & 255u);
+                    vs[j][e] = w == 255u ? cache_scale(255u) : w + 126 < z.top ? 0.f : cache_scale(127 + w - z.top);
+                }
+        }
+        float factors[MT][2];
+#pragma unroll
+        for (int t = 0; t < MT; ++t) factors[t][0] = factor[t * 16 + g], factors[t][1] = factor[t * 16 + g + 8];
+#pragma unroll
+        for (int t = 0; t < MT; ++t)
+#pragma unroll
+            for (int j = 0; j < NT; ++j)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    s[t][j][e] *= factors[t][e >> 1];
+                    if constexpr (F != kCacheSame) s[t][j][e] *= ks[j][e & 1];
+                }
+        if constexpr (TAIL) {
+#pragma unroll
+            for (int t = 0; t < MT; ++t)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int q = (u.rt * a.tile_rows + t * 16 + g + 8 * h) / a.G;  // the row's token
+                    const uint8_t* mask = a.mask ? a.mask + u.b * a.mk_sb + q * a.mk_sq : nullptr;
+#pragma unroll
+                    for (int j = 0; j < NT; ++j)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const int key = key0 + j * 8 + 2 * c + e;
+                            const bool on = key < u.count && q < u.count && (mask ? mask[key] != 0 : key <= q);
+                            if (!on) s[t][j][2 * h + e] = -attn_inf();
+                        }
+                }
+        } else if (key0 + KS > u.length || there != (1u << GR) - 1) {
+#pragma unroll
+            for (int j = 0; j < NT; ++j)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const bool on = key0 + j * 8 + 2 * c + e < u.length && ((there >> (j / 2)) & 1u);
+#pragma unroll
+                    for (int t = 0; t < MT; ++t)
+                        if (!on) s[t][j][e] = s[t][j][2 + e] = -attn_inf();
+                }
+        }
+        // the reference of a row follows when a score passes it by kCacheAbove
+        bool renew = false;
+#pragma unroll
+        for (int t = 0; t < MT; ++t)
+#pragma unroll
+            for (int j = 0; j < NT; ++j)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) renew |= s[t][j][e] - z.m[t][e >> 1] > kCacheAbove;
+        if (__any_sync(0xffffffffu, renew)) {
+#pragma unroll
+            for (int t = 0; t < MT; ++t)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    float top = -attn_inf();
+#pragma unroll
+                    for (int j = 0; j < NT; ++j) top = fmaxf(top, fmaxf(s[t][j][2 * h], s[t][j][2 * h + 1]));
+                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+                    const float next = fmaxf(z.m[t][h], top - P::below);
+                    const float f = next == z.m[t][h] ? 1.f : cache_ex2(z.m[t][h] - next);
+                    z.m[t][h] = next;
+                    z.l[t][h] *= f;
+#pragma unroll
+                    for (int d = 0; d < DP / 8; ++d) z.o[t][d][2 * h] *= f, z.o[t][d][2 * h + 1] *= f;
+                }
+        }
+#pragma unroll
+        for (int t = 0; t < MT; ++t)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const float ref = z.m[t][h] == -attn_inf() ? 0.f : z.m[t][h];
+#pragma unroll
+                for (int j = 0; j < NT; ++j)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const float x = cache_ex2(s[t][j][2 * h + e] - ref);
+                        z.l[t][h] += x;
+                        s[t][j][2 * h + e] = F != kCacheSame ? x * vs[j][e] : x;
+                    }
+            }
+#pragma unroll
+        for (int kk = 0; kk < GR; ++kk) {
+            uint4 p[P::pp][MT];
+#pragma unroll
+            for (int t = 0; t < MT; ++t) {
+                uint32_t x[4][P::pp];
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    cache_pieces<P::bf16, P::pp>(s[t][2 * kk + (e >> 1)][2 * (e & 1)], s[t][2 * kk + (e >> 1)][2 * (e & 1) + 1], x[e]);
+#pragma unroll
+                for (int i2 = 0; i2 < P::pp; ++i2) p[i2][t] = make_uint4(x[0][i2], x[1][i2], x[2][i2], x[3][i2]);
+            }
+            outputs(v, kk, p, z);
+        }
+    }
+
+    __device__ __forceinline__ void run(CacheState<DP, MT>& z) {
+        begin();
+        uint32_t bytes[STAGES], there[STAGES];  // of the steps in flight, the nearest first
+#pragma unroll
+        for (int i = 0; i < STAGES - 1; ++i) {
+            bytes[i] = there[i] = 0;
+            if (i < steps) issue(i, bytes[i], there[i]);
+            cache_commit();
+        }
+#pragma unroll 1
+        for (int i = 0; i < steps; ++i) {
+            if constexpr (STAGES == 1) {
+                __syncwarp();
+                issue(i, bytes[0], there[0]);
+                cache_commit();
+                cache_wait<0>();
+                __syncwarp();
+            } else {
+                cache_wait<STAGES - 2>();
+                __syncwarp();  // the step's copies of all lanes are there, and the stage of step i - 1 is read
+                bytes[STAGES - 1] = there[STAGES - 1] = 0;
+                if (i + STAGES - 1 < steps) issue(i + STAGES - 1, bytes[STAGES - 1], there[STAGES - 1]);
+                cache_commit();
+            }
+            compute(i, bytes[0], there[0], z);
+#pragma unroll
+            for (int j = 0; j + 1 < STAGES; ++j) bytes[j] = bytes[j + 1], there[j] = there[j + 1];
+        }
+        cache_wait<0>();
+        __syncwarp();
+    }
+};
+
+template <typename T, int F, int DP, int MT>
+__global__ void __launch_bounds__(kCacheWarps * 32, CacheRowsCfg<T, F, DP, MT>::kResident) msda_cache_rows_kernel(const CacheArgs a) {
+    using Cfg = CacheRowsCfg<T, F, DP, MT>;
+    using P = CacheProduct<T, F>;
+    using PT = CacheProduct<T, kCacheSame>;
+    using Ty = CacheType<T>;
+    constexpr int R = MT * 16, STEPS = DP / 16, OB = DP + 4;
+    extern __shared__ __align__(128) unsigned char cache_smem_raw[];
+    __shared__ float factor[3][R], part_m[kCacheWarps][R], part_l[kCacheWarps][R];
+    uint4* qf = reinterpret_cast<uint4*>(cache_smem_raw);
+    uint4* qt = F == kCacheSame ? qf : qf + P::qp * Cfg::kFragments / 16;
+    unsigned char* ring = cache_smem_raw + Cfg::kQ;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, c = lane & 3;
+
+    cache_walk(a, [&](const CacheUnit& u, int tile, int tiles, int slot) {
+        const T* query = static_cast<const T*>(a.q) + u.b * a.q_sb + (long long)u.n * a.G * a.q_sh;
+        auto row_of = [&](int r) -> const T* {  // null where there is none
+            const int x = u.rt * R + r, t = x / a.G;
+            return x < a.rows && t < u.count ? query + t * a.q_st + (x - t * a.G) * a.q_sh : nullptr;
+        };
+        __syncthreads();  // the unit before is out
+        // ---- scales of the rows: with 8 bits a power of two that brings a row's largest to 2^14 or more ----
+        for (int r = warp; r < R; r += kCacheWarps) {
+            float up = 1.f;
+            if constexpr (F != kCacheSame) {
+                const T* q = row_of(r);
+                float top = 0.f;
+                if (q)
+                    for (int d = lane; d < a.D; d += 32) top = fmaxf(top, fabsf(Ty::get(q[d])));
+#pragma unroll
+                for (int w = 16; w > 0; w >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, w));
+                const int e = (int)(__float_as_uint(top) >> 23);  // 2^(e - 127) <= top
+                up = top > 0.f && e < 255 ? __uint_as_float((uint32_t)min(max(268 - e, 27), 227) << 23) : 1.f;
+            }
+            if (lane == 0) {
+                factor[0][r] = a.c2 * (1.f / up);  // a power of two: exact
+                factor[1][r] = up;
+                factor[2][r] = a.c2;
+            }
+        }
+        __syncthreads();
+        // ---- the queries' fragments: entry (tile t of 16, step s, lane) are the channels of lane % 4 at step s of rows lane / 4 and + 8 ----
+        for (int x = threadIdx.x; x < MT * STEPS * 32; x += kCacheWarps * 32) {
+            const int ln = x & 31, s = (x >> 5) % STEPS, t = (x >> 5) / STEPS;
+            const int ch = Cfg::E * ((ln & 3) + 4 * (s / (Cfg::E / 4))) + 4 * (s % (Cfg::E / 4));
+            float y[2][4];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int r = t * 16 + (ln >> 2) + 8 * h;
+                const T* q = row_of(r);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) y[h][e] = q && ch + e < a.D ? Ty::get(q[ch + e]) : 0.f;
+            }
+            auto put = [&](uint4* to, auto product, float up0, float up1) {
+                using Q = decltype(product);
+                uint32_t f[4][Q::qp];
+                cache_pieces<Q::bf16, Q::qp>(y[0][0] * up0, y[0][1] * up0, f[0]);
+                cache_pieces<Q::bf16, Q::qp>(y[1][0] * up1, y[1][1] * up1, f[1]);
+                cache_pieces<Q::bf16, Q::qp>(y[0][2] * up0, y[0][3] * up0, f[2]);
+                cache_pieces<Q::bf16, Q::qp>(y[1][2] * up1, y[1][3] * up1, f[3]);
+#pragma unroll
+                for (int p = 0; p < Q::qp; ++p) to[((p * MT + t) * STEPS + s) * 32 + ln] = make_uint4(f[0][p], f[1][p], f[2][p], f[3][p]);
+            };
+            put(qf, P{}, factor[1][t * 16 + (ln >> 2)], factor[1][t * 16 + (ln >> 2) + 8]);
+            if constexpr (F != kCacheSame) put(qt, PT{}, 1.f, 1.f);
+        }
+        __syncthreads();
+
+        CacheState<DP, MT> z;
+        z.top = 0;
+#pragma unroll
+        for (int t = 0; t < MT; ++t) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) z.m[t][h] = -attn_inf(), z.l[t][h] = 0.f;
+#pragma unroll
+            for (int d = 0; d < DP / 8; ++d)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) z.o[t][d][e] = 0.f;
+        }
+        const int from_cache = max(0, min(tile + tiles, u.cache_tiles) - tile);
+        unsigned char* my_ring = ring + warp * Cfg::kRing;
+        if (from_cache > 0) {
+            const int first = tile * (kCacheWarps * Cfg::KS) + warp * Cfg::KS;
+            const int mine = first < u.length ? (u.length - first + kCacheWarps * Cfg::KS - 1) / (kCacheWarps * Cfg::KS) : 0;
+            CacheWalk<T, F, DP, MT, Cfg::E, Cfg::EV, Cfg::KS, Cfg::kStages, false> walk{
+                a, u, my_ring, qf, factor[0], lane, warp, first, min(from_cache, mine), kCacheWarps * Cfg::KS, 0, 0, 0};
+            walk.run(z);
+        }
+        if (F != kCacheSame && z.top != 0) {  // back to units of 1
+            const float f = cache_scale(z.top);
+#pragma unroll
+            for (int t = 0; t < MT; ++t)
+#pragma unroll
+                for (int d = 0; d < DP / 8; ++d)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) z.o[t][d][e] *= f;
+        }
+        if (tile + tiles > u.cache_tiles && a.nk) {
+            const int keys = cache_tail_keys(a, u.rt, u.count), at = max(0, tile - u.cache_tiles);
+            constexpr int KT = Cfg::kTailKeys;
+            const int first = at * (kCacheWarps * KT) + warp * KT, end = min(keys, (tile + tiles - u.cache_tiles) * (kCacheWarps * KT));
+            const int steps = first < end ? (end - first + kCacheWarps * KT - 1) / (kCacheWarps * KT) : 0;
+            CacheWalk<T, kCacheSame, DP, MT, Cfg::E, Cfg::EV, KT, Cfg::kTailStages, true> walk{
+                a, u, my_ring, qt, factor[2], lane, warp, first, steps, kCacheWarps * KT, 0, 0, 0};
+            walk.run(z);
+        }
+        __syncthreads();  // rings and factors are done with
+        // ---- the warps' parts, joined in their order ----
+        float* po = reinterpret_cast<float*>(ring);
+#pragma unroll
+        for (int t = 0; t < MT; ++t)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int r = t * 16 + g + 8 * h;
+                float l = z.l[t][h];
+                l += __shfl_xor_sync(0xffffffffu, l, 1);
+                l += __shfl_xor_sync(0xffffffffu, l, 2);
+                if (c == 0) part_m[warp][r] = z.m[t][h], part_l[warp][r] = l;
+#pragma unroll
+                for (int d = 0; d < DP / 8; ++d)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const int set = d / Cfg::EV, j = d % Cfg::EV, lane8 = 2 * c + e;
+                        const int ch = (Cfg::E == Cfg::EV ? Cfg::E * (lane8 + 8 * set) : Cfg::EV * lane8) + j;
+                        po[(warp * R + r) * OB + ch] = z.o[t][d][2 * h + e];
+                    }
+            }
+        __syncthreads();
+        for (int x = threadIdx.x; x < R * (DP / 4); x += kCacheWarps * 32) {
+            const int r = x / (DP / 4), d = x % (DP / 4) * 4, row = u.rt * R + r;
+            if (row >= a.rows || d >= a.D) continue;
+            float top = -attn_inf();
+#pragma unroll
+            for (int w = 0; w < kCacheWarps; ++w) top = fmaxf(top, part_m[w][r]);
+            float sum = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int w = 0; w < kCacheWarps; ++w) {
+                const float f = top == -attn_inf() ? 1.f : exp2f(part_m[w][r] - top);  // none seen: zeros, or NaN scores alone
+                sum += part_l[w][r] * f;
+                const float4 y = *reinterpret_cast<const float4*>(&po[(w * R + r) * OB + d]);
+                o[0] += y.x * f, o[1] += y.y * f, o[2] += y.z * f, o[3] += y.w * f;
+            }
+            const int t = row / a.G, h = u.n * a.G + row - t * a.G;
+            const bool none = sum == 0.f || t >= u.count;
+            const float ref = top == -attn_inf() ? 0.f : top, l2 = none ? -attn_inf() : ref + log2f(sum), inv = none ? 0.f : 1.f / sum;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[e] = none ? 0.f : o[e] * inv;
+            if (slot >= 0) {
+                const long long at = (long long)slot * R + r;
+                *reinterpret_cast<float4*>(a.part_o + at * a.D + d) = make_float4(o[0], o[1], o[2], o[3]);
+                if (d == 0) a.part_l2[at] = l2;
+            } else {
+                T* out = static_cast<T*>(a.out) + (((long long)u.b * a.T + t) * a.M + h) * a.D + d;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) out[e] = Ty::put(o[e]);
+                if (d == 0) a.lse[((long long)u.b * a.M + h) * a.T + t] = l2 * kLn2;
+            }
+        }
+    });
+}
+
+template <typename T, int F, int DP, int MT>
+static CacheRowsShape cache_rows_shape_of() {
+    using Cfg = CacheRowsCfg<T, F, DP, MT>;
+    return {MT * 16, kCacheWarps * Cfg::KS, kCacheWarps * Cfg::kTailKeys, Cfg::kResident};
+}
+template <typename T, int F, int DP, int MT>
+static cudaError_t cache_rows_go(const CacheArgs& a, int grid, cudaStream_t st) {
+    using Cfg = CacheRowsCfg<T, F, DP, MT>;
+    static SmemSeen seen;
+    cudaError_t e = allow_smem(reinterpret_cast<const void*>(&msda_cache_rows_kernel<T, F, DP, MT>), Cfg::kSmem, seen);
+    if (e != cudaSuccess) return e;
+    msda_cache_rows_kernel<T, F, DP, MT><<<grid, kCacheWarps * 32, Cfg::kSmem, st>>>(a);
+    return cudaGetLastError();
+}
+
+#define MSDA_CACHE_ROWS_BY(format, D, two, f, ...)                                                               \
+    do {                                                                                                         \
+        const int key = ((format) << 2) | ((D) > 64 ? 2 : 0) | ((two) ? 1 : 0);                                  \
+        switch (key) {                                                                                           \
+            case 0: return f<T, kCacheSame, 64, 1>(__VA_ARGS__);                                                 \
+            case 1: return f<T, kCacheSame, 64, 2>(__VA_ARGS__);                                                 \
+            case 2: return f<T, kCacheSame, 128, 1>(__VA_ARGS__);                                                \
+            case 3: return f<T, kCacheSame, 128, sizeof(T) == 4 ? 1 : 2>(__VA_ARGS__);                           \
+            case 4: return f<T, kCacheE4m3, 64, 1>(__VA_ARGS__);                                                 \
+            case 5: return f<T, kCacheE4m3, 64, 2>(__VA_ARGS__);                                                 \
+            case 6: return f<T, kCacheE4m3, 128, 1>(__VA_ARGS__);                                                \
+            case 7: return f<T, kCacheE4m3, 128, sizeof(T) == 4 ? 1 : 2>(__VA_ARGS__);                           \
+            case 8: return f<T, kCacheInt8, 64, 1>(__VA_ARGS__);                                                 \
+            case 9: return f<T, kCacheInt8, 64, 2>(__VA_ARGS__);                                                 \
+            case 10: return f<T, kCacheInt8, 128, 1>(__VA_ARGS__);                                               \
+            default: return f<T, kCacheInt8, 128, sizeof(T) == 4 ? 1 : 2>(__VA_ARGS__);                          \
+        }                                                                                                        \
+    } while (0)
+
+template <typename T>
+CacheRowsShape cache_rows_shape(int format, int D, int rows) {
+    MSDA_CACHE_ROWS_BY(format, D, rows > 16, cache_rows_shape_of);
+}
+template <typename T>
+cudaError_t launch_cache_rows(const CacheArgs& a, int format, int grid, cudaStream_t st) {
+    MSDA_CACHE_ROWS_BY(format, a.D, a.rows > 16, cache_rows_go, a, grid, st);
+}
+
+}  // namespace msda
