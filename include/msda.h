@@ -525,7 +525,8 @@ msda_status msda_cache_read(msda_dtype dt, int format, const msda_cache_problem*
  *
  * `longest` plans the launch; a smaller bound on the lengths than the table's
  * saves blocks and, for short sequences, the joining launch.
- * Requirements: N divides M; scale > 0.  B == 0 or T == 0 enqueue nothing.
+ * Requirements: N divides M; scale > 0; B N times tiles of 16 rows times tiles of
+ * 64 keys below 2^30.  B == 0 or T == 0 enqueue nothing.
  * workspace: msda_cache_attention_workspace_size() bytes (0 for many sizes: then
  * it may be NULL), 256-byte aligned; not shared by calls that can overlap.
  */

@@ -3,6 +3,7 @@ attention of new tokens over it (C ABI ``msda_cache_write`` / ``_read`` / ``_att
 from __future__ import annotations
 
 import math
+import struct
 from typing import NamedTuple, Optional, Tuple
 
 import torch
@@ -10,6 +11,8 @@ import torch
 from . import _lib
 from ._binding import DTYPE_CODE, on_device, ptr, stream, workspace_of
 
+# the problem struct of include/msda.h: 35 int64 members
+_problem = struct.Struct("35q").pack
 CODE_FORMAT = {torch.float8_e4m3fn: _lib.CACHE_E4M3, torch.int8: _lib.CACHE_INT8}
 _NONE3 = (0, 0, 0)
 
@@ -67,12 +70,12 @@ def _pages(cache: PagedCache):
     return _lib.CACHE_SAME, dev, sh, (*st[:3], *sv[:3], *_NONE3, *_NONE3)
 
 
-def _index(name: str, t: torch.Tensor, shape, dev: torch.device) -> torch.Tensor:
-    """An int32 tensor of `shape` (None: any size) on `dev` with contiguous rows."""
+def _index(name: str, t: torch.Tensor, B: int, dim: int, dev: torch.device) -> torch.Tensor:
+    """An int32 tensor [B] or [B, any] (``dim``) on ``dev`` with contiguous rows."""
     sh = t.shape
-    if len(sh) != len(shape) or any(n is not None and n != m for n, m in zip(shape, sh)):
-        raise ValueError(f"{name} must be {[n if n is not None else 'any' for n in shape]}, got {tuple(sh)}")
-    if t.dtype != torch.int32:
+    if len(sh) != dim or sh[0] != B:
+        raise ValueError(f"{name} must be [{B}{', any' if dim == 2 else ''}], got {tuple(sh)}")
+    if t.dtype is not torch.int32:
         raise TypeError(f"{name} must be int32, got {t.dtype}")
     if t.device != dev:
         raise ValueError(f"{name} is on {t.device}, the cache on {dev}")
@@ -87,10 +90,12 @@ def _rows(name: str, x: torch.Tensor, shape, dtype: torch.dtype, dev: torch.devi
         raise TypeError(f"{name} is {x.dtype}, expected {dtype}")
     if x.device != dev:
         raise ValueError(f"{name} is on {x.device}, the cache on {dev}")
-    n = 16 // x.element_size()
-    st = x.stride()
-    if x.data_ptr() % 16 == 0 and st[3] == 1 and all(st[i] % n == 0 or shape[i] <= 1 for i in range(3)):
-        return x
+    if x.data_ptr() % 16 == 0:
+        if x.is_contiguous():
+            return x
+        n, st = 16 // x.element_size(), x.stride()
+        if st[3] == 1 and all(st[i] % n == 0 or shape[i] <= 1 for i in range(3)):
+            return x
     x = x.contiguous()
     return x if x.data_ptr() % 16 == 0 else x.clone()
 
@@ -126,15 +131,15 @@ def cache_write(cache: PagedCache, key: torch.Tensor, value: torch.Tensor, table
         raise ValueError(f"key has {N} heads of {D} channels, the cache {sh[2]} of {sh[3]}")
     dt = _float_dtype(key.dtype, fmt, cache)
     key, value = _rows("key", key, key.shape, key.dtype, dev), _rows("value", value, key.shape, key.dtype, dev)
-    table, start = _index("table", table, (B, None), dev), _index("start", start, (B,), dev)
+    table, start = _index("table", table, B, 2, dev), _index("start", start, B, 1, dev)
     R = T
     if select is not None:
-        select = _index("select", select, (B, None), dev)
+        select = _index("select", select, B, 2, dev)
         R = select.shape[1]
     if counts is not None:
-        counts = _index("counts", counts, (B,), dev)
+        counts = _index("counts", counts, B, 1, dev)
     width = table.shape[1]
-    p = _lib.CacheProblem(B, R, N, N, D, T, sh[0], sh[1], width, width * sh[1], *strides, table.stride(0), *_NONE3,
+    p = _problem(B, R, N, N, D, T, sh[0], sh[1], width, width * sh[1], *strides, table.stride(0), *_NONE3,
                           *key.stride()[:3], *value.stride()[:3], 0, 0, 0 if select is None else select.stride(0))
     with on_device(dev):
         _lib.check(_lib.lib().msda_cache_write(
@@ -154,10 +159,10 @@ def cache_read(cache: PagedCache, table: torch.Tensor, lengths: torch.Tensor, ro
     if table.dim() != 2:
         raise ValueError(f"table must be [B, width], got {tuple(table.shape)}")
     B, width = table.shape
-    table, lengths = _index("table", table, (B, None), dev), _index("lengths", lengths, (B,), dev)
+    table, lengths = _index("table", table, B, 2, dev), _index("lengths", lengths, B, 1, dev)
     key = torch.empty((B, rows, *sh[2:]), dtype=dtype, device=dev)
     value = torch.empty_like(key)
-    p = _lib.CacheProblem(B, rows, sh[2], sh[2], sh[3], rows, sh[0], sh[1], width, width * sh[1], *strides,
+    p = _problem(B, rows, sh[2], sh[2], sh[3], rows, sh[0], sh[1], width, width * sh[1], *strides,
                           table.stride(0), *_NONE3, *_NONE3, *_NONE3, 0, 0, 0)
     with on_device(dev):
         _lib.check(_lib.lib().msda_cache_read(
@@ -190,7 +195,7 @@ def cache_attention(query: torch.Tensor, cache: PagedCache, table: torch.Tensor,
         raise ValueError(f"query has {M} heads of {D} channels, the cache {N} (which must divide them) of {sh[3]}")
     dt = _float_dtype(query.dtype, fmt, cache)
     query = _rows("query", query, query.shape, query.dtype, dev)
-    table, lengths = _index("table", table, (B, None), dev), _index("lengths", lengths, (B,), dev)
+    table, lengths = _index("table", table, B, 2, dev), _index("lengths", lengths, B, 1, dev)
     width = table.shape[1]
     if longest is None:
         longest = width * sh[1]
@@ -216,8 +221,8 @@ def cache_attention(query: torch.Tensor, cache: PagedCache, table: torch.Tensor,
             mask = mask.contiguous()
         ms0, ms1 = 0 if mask.shape[0] == 1 else mask.stride(0), mask.stride(1)
     if counts is not None:
-        counts = _index("counts", counts, (B,), dev)
-    p = _lib.CacheProblem(B, T, M, N, D, 0 if key is None else T, sh[0], sh[1], width, longest, *strides, table.stride(0),
+        counts = _index("counts", counts, B, 1, dev)
+    p = _problem(B, T, M, N, D, 0 if key is None else T, sh[0], sh[1], width, longest, *strides, table.stride(0),
                           *query.stride()[:3], *ks, *vs, ms0, ms1, 0)
     out = torch.empty((B, T, M * D), dtype=query.dtype, device=dev)
     lse = torch.empty((B, M, T), dtype=torch.float32, device=dev)

@@ -4,15 +4,19 @@
 //
 // Writing and reading are bound by memory: a row of D channels lies in the lanes
 // that 16 bytes of the unquantised type each make, so its largest magnitude takes
-// log2(lanes) exchanges and every access is a whole vector.  A block takes 16
-// tokens of all heads, tokens of a head next to each other in its lanes: the
-// cache's side (head by head) is then read or written in runs of 16 rows, the
-// other side in whole tokens.
+// log2(lanes) exchanges and every access is a whole vector.  A warp takes 16
+// tokens of a head, so that pages, places and scales are looked up once for them
+// by one lane each and handed on by shuffles; a block's warps take the heads of the
+// same tokens.  The cache's side (head by head) is then read or written in runs of
+// 16 rows, the other side in whole tokens.
 #include <cuda_runtime.h>
 
 #include <cstdint>
+#include <type_traits>
 
+#include "msda_attention_tc.cuh"
 #include "msda_cache.cuh"
+#include "msda_cache_tc.cuh"
 #include "msda_host.cuh"
 
 namespace msda {
@@ -109,226 +113,256 @@ struct CacheMoveArgs {
     const int *first, *counts, *select;  // write: start, counts or null, select [B, T] or null; read: lengths
     long long select_sb;
     int B, T, N, D, source;
-    int lanes, block_log2;  // lanes a row (a power of two); tokens a block of rows (a power of two up to 16)
+    int lanes_log2;           // lanes a row: a power of two
 };
 
-// Row x of a sequence's rows in blocks of 2^k tokens: token fastest, then head, then block.
-__device__ __forceinline__ bool cache_row(const CacheMoveArgs& a, unsigned x, int* t, int* n) {
-    const unsigned in = x & ((1u << a.block_log2) - 1u), y = x >> a.block_log2, z = y / (unsigned)a.N;
-    *n = (int)(y - z * (unsigned)a.N);
-    const long long tok = ((long long)z << a.block_log2) + in;
-    *t = (int)tok;
-    return tok < a.T;
+constexpr int kMoveTokens = 16;
+
+// A warp takes 16 tokens of one head, 32 / lanes rows at a time; a block's warps take the heads of the same tokens.  False where
+// there are no such tokens.
+__device__ __forceinline__ bool cache_piece(const CacheMoveArgs& a, int* t0, int* n) {
+    const unsigned w = blockIdx.x * (kMoveThreads / 32) + (threadIdx.x >> 5), block = w / (unsigned)a.N;
+    *n = (int)(w - block * (unsigned)a.N);
+    *t0 = (int)block * kMoveTokens;
+    return *t0 < a.T;
 }
 
+// largest magnitude of a vector's elements as bits in the order of their size (NaN above infinity): of 16-bit types two maxima side by side
+template <typename T>
+__device__ __forceinline__ uint32_t cache_top(uint32_t a, uint32_t b) {
+    if constexpr (sizeof(T) == 4) return max(a, b);
+    else return __vmaxu2(a, b);
+}
+template <typename T>
+__device__ __forceinline__ uint32_t cache_top(const uint4& x) {
+    constexpr uint32_t m = sizeof(T) == 4 ? 0x7fffffffu : 0x7fff7fffu;
+    return cache_top<T>(cache_top<T>(x.x & m, x.y & m), cache_top<T>(x.z & m, x.w & m));
+}
+template <typename T>
+__device__ __forceinline__ float cache_top_value(uint32_t top) {
+    if constexpr (sizeof(T) == 4) return __uint_as_float(top);
+    else {
+        const uint32_t h = max(top & 0xffffu, top >> 16);
+        if constexpr (std::is_same<T, __half>::value) return __half2float(__ushort_as_half((unsigned short)h));
+        else return __uint_as_float(h << 16);
+    }
+}
+
+// U rows of K and of V at a time a lane.
 template <typename T, int F>
 __global__ void __launch_bounds__(kMoveThreads) msda_cache_write_kernel(const CacheMoveArgs a) {
-    constexpr int E = CacheVec<T>::n, U = 2;
-    const int at = threadIdx.x & (a.lanes - 1), rows = kMoveThreads / a.lanes;
+    constexpr int E = CacheVec<T>::n, U = 2, ES = F == kCacheSame ? (int)sizeof(T) : 1;
+    const int lane = threadIdx.x & 31, at = lane & ((1 << a.lanes_log2) - 1), row0 = lane >> a.lanes_log2, rows = 32 >> a.lanes_log2;
     const bool in = at * E < a.D;
+    int t0, n;
+    if (!cache_piece(a, &t0, &n)) return;
     for (int b = blockIdx.y; b < a.B; b += gridDim.y) {
-        const int start = a.first[b], count = cache_count(a.c, a.counts, b, a.T);
-        uint4 x[U][2];
-        long long to[U][2];
-        long long scale[U][2];
-        bool on[U];
-#pragma unroll
-        for (int i = 0; i < U; ++i) {
-            int t, n;
-            on[i] = cache_row(a, (blockIdx.x * U + i) * rows + threadIdx.x / a.lanes, &t, &n) && t < count;
-            x[i][0] = x[i][1] = make_uint4(0, 0, 0, 0);
-            if (!on[i]) continue;
-            const long long token = (long long)start + t;
-            int page = -1, src = t;
-            if (token >= 0 && token < a.c.longest) page = cache_page(a.c, b, (int)token);
-            else atomicOr(a.c.err, kCacheBad);
+        const int count = cache_count(a.c, a.counts, b, a.T);
+        if (t0 >= count) continue;
+        // lane i < 16: where row t0 + i comes from and goes to (page -1: nowhere)
+        int page = -1, place = 0, src = t0 + lane;
+        if (lane < kMoveTokens && t0 + lane < count) {
+            const long long token = (long long)a.first[b] + t0 + lane;
+            if (token >= 0 && token < a.c.longest) {
+                page = cache_page(a.c, b, (int)token);
+                place = (int)token & (a.c.page - 1);
+            } else {
+                atomicOr(a.c.err, kCacheBad);
+            }
             if (a.select) {
-                src = a.select[b * a.select_sb + t];
+                src = a.select[b * a.select_sb + t0 + lane];
                 if ((unsigned)src >= (unsigned)a.source) {
                     atomicOr(a.c.err, kCacheBad);
                     page = -1;
                 }
             }
-            on[i] = page >= 0;
-            if (!on[i]) continue;
-            const int place = (int)token & (a.c.page - 1);
-            if (in) {
-                x[i][0] = *reinterpret_cast<const uint4*>(static_cast<const T*>(a.key) + b * a.k_sb + src * a.k_st + n * a.k_sh + at * E);
-                x[i][1] = *reinterpret_cast<const uint4*>(static_cast<const T*>(a.value) + b * a.v_sb + src * a.v_st + n * a.v_sh + at * E);
-            }
-            to[i][0] = page * a.c.k_sp + place * a.c.k_st + n * a.c.k_sh + at * E;
-            to[i][1] = page * a.c.v_sp + place * a.c.v_st + n * a.c.v_sh + at * E;
-            scale[i][0] = page * a.c.ks_sp + place * a.c.ks_st + n * a.c.ks_sh;
-            scale[i][1] = page * a.c.vs_sp + place * a.c.vs_st + n * a.c.vs_sh;
         }
+        const T* key = static_cast<const T*>(a.key) + b * a.k_sb + n * a.k_sh + at * E;
+        const T* value = static_cast<const T*>(a.value) + b * a.v_sb + n * a.v_sh + at * E;
+        char* to_k = static_cast<char*>(a.c.k) + (n * a.c.k_sh + at * E) * ES;
+        char* to_v = static_cast<char*>(a.c.v) + (n * a.c.v_sh + at * E) * ES;
+        for (int r0 = 0; r0 < kMoveTokens && t0 + r0 < count; r0 += rows * U) {
+            uint4 x[U][2];
+            int pg[U], pl[U];
 #pragma unroll
-        for (int i = 0; i < U; ++i)
-#pragma unroll
-            for (int w = 0; w < 2; ++w) {
-                void* base = w ? a.c.v : a.c.k;
-                if constexpr (F == kCacheSame) {
-                    if (on[i] && in) *reinterpret_cast<uint4*>(static_cast<T*>(base) + to[i][w]) = x[i][w];
-                } else {
-                    float v[E];
-                    CacheVec<T>::get(x[i][w], v);
-                    uint32_t top = 0;  // of non-negative floats the bits are in order, and NaN is above infinity
-#pragma unroll
-                    for (int e = 0; e < E; ++e) top = max(top, __float_as_uint(v[e]) & 0x7fffffffu);
-                    for (int s = a.lanes >> 1; s > 0; s >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, s));
-                    const uint32_t byte = cache_scale_byte<F>(__uint_as_float(top));
-                    const float up = byte == 255u ? 0.f : __uint_as_float((254u - byte) << 23);
-                    uint32_t codes[E / 4];
-#pragma unroll
-                    for (int e = 0; e < E / 4; ++e) {
-                        codes[e] = byte == 255u ? 0u : cache_codes<F>(v[4 * e] * up, v[4 * e + 1] * up, v[4 * e + 2] * up, v[4 * e + 3] * up);
-                    }
-                    if (on[i]) {
-                        uint8_t* p = static_cast<uint8_t*>(base) + to[i][w];
-                        if (in) {
-                            if constexpr (E == 8) *reinterpret_cast<uint2*>(p) = make_uint2(codes[0], codes[1]);
-                            else *reinterpret_cast<uint32_t*>(p) = codes[0];
-                        }
-                        if (at == 0) (w ? a.c.vs : a.c.ks)[scale[i][w]] = (uint8_t)byte;
-                    }
+            for (int i = 0; i < U; ++i) {
+                const int r = r0 + i * rows + row0;
+                pg[i] = __shfl_sync(0xffffffffu, page, r & 31);
+                pl[i] = __shfl_sync(0xffffffffu, place, r & 31);
+                const int from = __shfl_sync(0xffffffffu, src, r & 31);
+                if (r >= kMoveTokens) pg[i] = -1;
+                x[i][0] = x[i][1] = make_uint4(0, 0, 0, 0);
+                if (pg[i] >= 0 && in) {
+                    x[i][0] = *reinterpret_cast<const uint4*>(key + from * a.k_st);
+                    x[i][1] = *reinterpret_cast<const uint4*>(value + from * a.v_st);
                 }
             }
+#pragma unroll
+            for (int i = 0; i < U; ++i)
+#pragma unroll
+                for (int w = 0; w < 2; ++w) {
+                    char* to = w ? to_v + (pg[i] * a.c.v_sp + pl[i] * a.c.v_st) * ES : to_k + (pg[i] * a.c.k_sp + pl[i] * a.c.k_st) * ES;
+                    if constexpr (F == kCacheSame) {
+                        if (pg[i] >= 0 && in) *reinterpret_cast<uint4*>(to) = x[i][w];
+                    } else {
+                        uint32_t top = cache_top<T>(x[i][w]);
+                        for (int l = a.lanes_log2 - 1; l >= 0; --l) top = cache_top<T>(top, __shfl_xor_sync(0xffffffffu, top, 1 << l));
+                        const uint32_t byte = cache_scale_byte<F>(cache_top_value<T>(top));
+                        const float up = __uint_as_float((254u - byte) << 23);
+                        float v[E];
+                        CacheVec<T>::get(x[i][w], v);
+                        uint32_t codes[E / 4];
+#pragma unroll
+                        for (int e = 0; e < E / 4; ++e)
+                            codes[e] = byte == 255u ? 0u : cache_codes<F>(v[4 * e] * up, v[4 * e + 1] * up, v[4 * e + 2] * up, v[4 * e + 3] * up);
+                        if (pg[i] >= 0) {
+                            if (in) {
+                                if constexpr (E == 8) *reinterpret_cast<uint2*>(to) = make_uint2(codes[0], codes[1]);
+                                else *reinterpret_cast<uint32_t*>(to) = codes[0];
+                            }
+                            if (at == 0) {
+                                if (w) a.c.vs[pg[i] * a.c.vs_sp + pl[i] * a.c.vs_st + n * a.c.vs_sh] = (uint8_t)byte;
+                                else a.c.ks[pg[i] * a.c.ks_sp + pl[i] * a.c.ks_st + n * a.c.ks_sh] = (uint8_t)byte;
+                            }
+                        }
+                    }
+                }
+        }
     }
 }
 
 template <typename T, int F>
 __global__ void __launch_bounds__(kMoveThreads) msda_cache_read_kernel(const CacheMoveArgs a) {
-    constexpr int E = CacheVec<T>::n, U = 4;
-    const int at = threadIdx.x & (a.lanes - 1), rows = kMoveThreads / a.lanes;
+    constexpr int E = CacheVec<T>::n, U = 4, ES = F == kCacheSame ? (int)sizeof(T) : 1;
+    const int lane = threadIdx.x & 31, at = lane & ((1 << a.lanes_log2) - 1), row0 = lane >> a.lanes_log2, rows = 32 >> a.lanes_log2;
     const bool in = at * E < a.D;
+    int t0, n;
+    if (!cache_piece(a, &t0, &n)) return;
     for (int b = blockIdx.y; b < a.B; b += gridDim.y) {
-        const int length = cache_length(a.c, a.first, b);
-        uint4 x[U][2];
-        uint32_t scale[U][2];
-        long long to[U];
+        const int here = min(kMoveTokens, a.T - t0);
+        int left = min(here, cache_length(a.c, a.first, b) - t0);  // rows that the sequence has; the 16 tokens share a page
+        const int page = left > 0 ? cache_page(a.c, b, t0) : -1, place = t0 & (a.c.page - 1);
+        if (page < 0) left = 0;
+        uint32_t bytes = 0;  // lane i < 16: row i's of K, lane 16 + i: of V
+        if constexpr (F != kCacheSame) {
+            const int r = lane & 15;
+            if (r < left)
+                bytes = lane < 16 ? a.c.ks[page * a.c.ks_sp + (place + r) * a.c.ks_st + n * a.c.ks_sh]
+                                  : a.c.vs[page * a.c.vs_sp + (place + r) * a.c.vs_st + n * a.c.vs_sh];
+        }
+        const char* from_k = static_cast<const char*>(a.c.k) + (page * a.c.k_sp + place * a.c.k_st + n * a.c.k_sh + at * E) * ES;
+        const char* from_v = static_cast<const char*>(a.c.v) + (page * a.c.v_sp + place * a.c.v_st + n * a.c.v_sh + at * E) * ES;
+        const long long out = (((long long)b * a.T + t0) * a.N + n) * a.D + at * E;
+        for (int r0 = 0; r0 < here; r0 += rows * U) {
+            uint4 x[U][2];
 #pragma unroll
-        for (int i = 0; i < U; ++i) {
-            int t, n;
-            const bool row = cache_row(a, (blockIdx.x * U + i) * rows + threadIdx.x / a.lanes, &t, &n);
-            x[i][0] = x[i][1] = make_uint4(0, 0, 0, 0);
-            scale[i][0] = scale[i][1] = 0;
-            to[i] = row && in ? (((long long)b * a.T + t) * a.N + n) * a.D + at * E : -1;
-            if (!row || t >= length) continue;
-            const int page = cache_page(a.c, b, t);
-            if (page < 0) continue;
-            const int place = t & (a.c.page - 1);
-            const long long k = page * a.c.k_sp + place * a.c.k_st + n * a.c.k_sh + at * E;
-            const long long v = page * a.c.v_sp + place * a.c.v_st + n * a.c.v_sh + at * E;
-            if constexpr (F == kCacheSame) {
-                if (in) {
-                    x[i][0] = *reinterpret_cast<const uint4*>(static_cast<const T*>(a.c.k) + k);
-                    x[i][1] = *reinterpret_cast<const uint4*>(static_cast<const T*>(a.c.v) + v);
-                }
-            } else {
-                if (in) {
-                    const uint8_t *kp = static_cast<const uint8_t*>(a.c.k) + k, *vp = static_cast<const uint8_t*>(a.c.v) + v;
-                    if constexpr (E == 8) {
-                        const uint2 p = *reinterpret_cast<const uint2*>(kp), q = *reinterpret_cast<const uint2*>(vp);
+            for (int i = 0; i < U; ++i) {
+                const int r = r0 + i * rows + row0;
+                x[i][0] = x[i][1] = make_uint4(0, 0, 0, 0);
+                if (r < left && in) {
+                    const char *k = from_k + r * a.c.k_st * ES, *v = from_v + r * a.c.v_st * ES;
+                    if constexpr (F == kCacheSame) {
+                        x[i][0] = *reinterpret_cast<const uint4*>(k), x[i][1] = *reinterpret_cast<const uint4*>(v);
+                    } else if constexpr (E == 8) {
+                        const uint2 p = *reinterpret_cast<const uint2*>(k), q = *reinterpret_cast<const uint2*>(v);
                         x[i][0].x = p.x, x[i][0].y = p.y, x[i][1].x = q.x, x[i][1].y = q.y;
                     } else {
-                        x[i][0].x = *reinterpret_cast<const uint32_t*>(kp), x[i][1].x = *reinterpret_cast<const uint32_t*>(vp);
+                        x[i][0].x = *reinterpret_cast<const uint32_t*>(k), x[i][1].x = *reinterpret_cast<const uint32_t*>(v);
                     }
                 }
-                scale[i][0] = a.c.ks[page * a.c.ks_sp + place * a.c.ks_st + n * a.c.ks_sh];
-                scale[i][1] = a.c.vs[page * a.c.vs_sp + place * a.c.vs_st + n * a.c.vs_sh];
             }
-        }
 #pragma unroll
-        for (int i = 0; i < U; ++i) {
-            if (to[i] < 0) continue;
+            for (int i = 0; i < U; ++i) {
+                const int r = r0 + i * rows + row0;
 #pragma unroll
-            for (int w = 0; w < 2; ++w) {
-                T* out = static_cast<T*>(const_cast<void*>(w ? a.value : a.key)) + to[i];
-                if constexpr (F == kCacheSame) {
-                    *reinterpret_cast<uint4*>(out) = x[i][w];
-                } else {
-                    const uint32_t c[2] = {x[i][w].x, x[i][w].y};
-                    const bool none = scale[i][w] == 255u;
-                    const float s = cache_scale(scale[i][w]);
-                    float v[E];
+                for (int w = 0; w < 2; ++w) {
+                    uint4 y = x[i][w];
+                    if constexpr (F != kCacheSame) {
+                        const uint32_t byte = __shfl_sync(0xffffffffu, bytes, (r & 15) + 16 * w), c[2] = {y.x, y.y};
+                        const float s = byte == 255u ? __uint_as_float(0x7fffffffu) : cache_scale(byte);
+                        float v[E];
 #pragma unroll
-                    for (int e = 0; e < E / 4; ++e) {
-                        uint32_t lo, hi;
-                        cache_four_f16<F>(c[e], lo, hi);
-                        const float2 p = __half22float2(*reinterpret_cast<const __half2*>(&lo)), q = __half22float2(*reinterpret_cast<const __half2*>(&hi));
-                        v[4 * e] = p.x * s, v[4 * e + 1] = p.y * s, v[4 * e + 2] = q.x * s, v[4 * e + 3] = q.y * s;
+                        for (int e = 0; e < E / 4; ++e) {
+                            uint32_t lo, hi;
+                            cache_four_f16<F>(c[e], lo, hi);
+                            const float2 p = __half22float2(*reinterpret_cast<const __half2*>(&lo)), q = __half22float2(*reinterpret_cast<const __half2*>(&hi));
+                            v[4 * e] = p.x * s, v[4 * e + 1] = p.y * s, v[4 * e + 2] = q.x * s, v[4 * e + 3] = q.y * s;
+                        }
+                        if (s * 512.f > CacheVec<T>::most()) {  // a code may be rounded up past the type's range: finite rows stay finite
+#pragma unroll
+                            for (int e = 0; e < E; ++e) v[e] = fminf(fmaxf(v[e], -CacheVec<T>::most()), CacheVec<T>::most());
+                        }
+                        y = CacheVec<T>::put(v);
                     }
-                    // a code may be rounded up past the type's range: finite rows stay finite
-#pragma unroll
-                    for (int e = 0; e < E; ++e)
-                        v[e] = none ? __uint_as_float(0x7fffffffu) : fminf(fmaxf(v[e], -CacheVec<T>::most()), CacheVec<T>::most());
-                    *reinterpret_cast<uint4*>(out) = CacheVec<T>::put(v);
+                    if (r < here && in) *reinterpret_cast<uint4*>(static_cast<T*>(const_cast<void*>(w ? a.value : a.key)) + out + (long long)r * a.N * a.D) = y;
                 }
             }
         }
     }
 }
 
-// A block a unit (and 32 rows of it): the parts of the blocks that shared it, in their order.  A row's parts lie a slot apart; a
-// warp takes a row, a lane its channels.
+// A block a row (of a unit): the parts of the blocks that shared the unit.  Four groups of 32 lanes take every fourth part, a lane
+// four channels; the groups are joined in their order.
 template <typename T>
 __global__ void __launch_bounds__(128) msda_cache_join_kernel(const CacheArgs a) {
+    __shared__ float4 part[4][32];
+    __shared__ float tops[4], sums[4];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    long long id = blockIdx.x;
-    const int rt = (int)(id % a.row_tiles);
+    int id = blockIdx.x;
+    const int rt = id % a.row_tiles, r = blockIdx.y, row = rt * a.tile_rows + r;
     id /= a.row_tiles;
-    const int n = (int)(id % a.N), b = (int)(id / a.N);
-    long long x;
-    const long long share = cache_share(a, cache_all_tiles(a, b, &x));
-    CacheUnit u;
-    cache_unit_at(a, b, n, 0, u);
-    if (n > 0) x += cache_head_tiles(a, b) * n;
-    for (; u.rt < rt; ++u.rt, cache_unit_tiles(a, u)) x += u.tiles;
-    const long long c0 = x / share, c1 = (x + u.tiles - 1) / share;
+    const int n = id % a.N, b = id / a.N;
     asm volatile("griddepcontrol.wait;" ::: "memory");  // launched as a programmatic dependent of the kernel that makes the parts
-    if (c0 == c1) return;
-    for (int r = blockIdx.y * 32 + warp; r < min(a.tile_rows, (int)(blockIdx.y + 1) * 32); r += 4) {
-        const int row = rt * a.tile_rows + r, t = row / a.G;
-        if (row >= a.rows) return;
-        auto slot = [&](long long c) { return (2 * c + (c == c0 && x != c0 * share ? 1 : 0)) * a.tile_rows + r; };
-        float top = -attn_inf();
-        bool nan = false;
-        for (long long c = c0 + lane; c <= c1; c += 32) {
-            const float l2 = a.part_l2[slot(c)];
-            top = fmaxf(top, l2), nan |= l2 != l2;
-        }
-#pragma unroll
-        for (int w = 16; w > 0; w >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, w));
-        if (__any_sync(0xffffffffu, nan)) top = __uint_as_float(0x7fffffffu);
-        float sum = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
-        for (long long c = c0; c <= c1; ++c) {
-            const long long at = slot(c);
-            const float w = top == -attn_inf() ? 0.f : exp2f(a.part_l2[at] - top);
-            sum += w;
-            if (lane * 4 < a.D) {
-                const float4 y = *reinterpret_cast<const float4*>(a.part_o + at * a.D + lane * 4);
-                o[0] += w * y.x, o[1] += w * y.y, o[2] += w * y.z, o[3] += w * y.w;
-            }
-        }
-        const int h = n * a.G + row - t * a.G;
-        const float inv = sum == 0.f ? 0.f : 1.f / sum;
-        if (lane * 4 < a.D) {
-            T* out = static_cast<T*>(a.out) + (((long long)b * a.T + t) * a.M + h) * a.D + lane * 4;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const float y = sum == 0.f ? 0.f : o[e] * inv;
-                if constexpr (sizeof(T) == 4) out[e] = y;
-                else if constexpr (std::is_same<T, __half>::value) out[e] = __float2half_rn(y);
-                else out[e] = __float2bfloat16_rn(y);
-            }
-        }
-        if (lane == 0) a.lse[((long long)b * a.M + h) * a.T + t] = sum == 0.f ? -attn_inf() : (top + log2f(sum)) * kLn2;
+    if (row >= a.rows) return;
+    const int2 parts = a.units[blockIdx.x];
+    if (parts.x < 0) return;
+    float top = -attn_inf(), sum = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+    for (int i = warp; i < parts.y; i += 4) {
+        // the first block's slot, then the first slots of the blocks behind it
+        const long long at = (long long)(i == 0 ? parts.x : 2 * ((parts.x >> 1) + i)) * a.tile_rows + r;
+        const float l2 = a.part_l2[at];
+        float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (lane * 4 < a.D) y = *reinterpret_cast<const float4*>(a.part_o + at * a.D + lane * 4);
+        // NaN: a part whose statistics are NaN makes the row NaN
+        const float next = fmaxf(top, l2), ref = next == -attn_inf() ? 0.f : next;
+        const float f = exp2f(top - ref), w = exp2f(l2 - ref);
+        top = next, sum = sum * f + w;
+        o[0] = o[0] * f + w * y.x, o[1] = o[1] * f + w * y.y, o[2] = o[2] * f + w * y.z, o[3] = o[3] * f + w * y.w;
     }
+    part[warp][lane] = make_float4(o[0], o[1], o[2], o[3]);
+    if (lane == 0) tops[warp] = top, sums[warp] = sum;
+    __syncthreads();
+    if (warp != 0) return;
+    top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
+    const float ref = top == -attn_inf() ? 0.f : top;
+    sum = o[0] = o[1] = o[2] = o[3] = 0.f;
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+        const float f = exp2f(tops[w] - ref);
+        const float4 y = part[w][lane];
+        sum += sums[w] * f;
+        o[0] += y.x * f, o[1] += y.y * f, o[2] += y.z * f, o[3] += y.w * f;
+    }
+    const int t = row / a.G, h = n * a.G + row - t * a.G;
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    if (lane * 4 < a.D) {
+        T* out = static_cast<T*>(a.out) + (((long long)b * a.T + t) * a.M + h) * a.D + lane * 4;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const float y = sum == 0.f ? 0.f : o[e] * inv;
+            if constexpr (sizeof(T) == 4) out[e] = y;
+            else if constexpr (std::is_same<T, __half>::value) out[e] = __float2half_rn(y);
+            else out[e] = __float2bfloat16_rn(y);
+        }
+    }
+    if (lane == 0) a.lse[((long long)b * a.M + h) * a.T + t] = sum == 0.f ? -attn_inf() : (ref + log2f(sum)) * kLn2;
 }
 
 template <typename T>
 static cudaError_t join_go(const CacheArgs& a, bool early, cudaStream_t st) {
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)((long long)a.B * a.N * a.row_tiles), (unsigned)((a.tile_rows + 31) / 32));
+    cfg.gridDim = dim3((unsigned)((long long)a.B * a.N * a.row_tiles), (unsigned)(a.rows < a.tile_rows ? a.rows : a.tile_rows));
     cfg.blockDim = dim3(128);
     cfg.stream = st;
     cudaLaunchAttribute at[1];
@@ -431,13 +465,10 @@ cudaError_t move_go(const CacheMoveArgs& a, bool write, dim3 grid, cudaStream_t 
 template <typename T>
 cudaError_t move_by_format(int format, CacheMoveArgs& a, bool write, cudaStream_t st) {
     const int vec = 16 / (int)sizeof(T);
-    a.lanes = 2;
-    while (a.lanes * vec < a.D) a.lanes *= 2;
-    a.block_log2 = 0;
-    while (a.block_log2 < 4 && (1 << a.block_log2) < a.T) ++a.block_log2;
-    const long long blocks = ((long long)a.T + (1 << a.block_log2) - 1) >> a.block_log2, rows = (blocks * a.N) << a.block_log2;
-    const long long each = (long long)(msda::kMoveThreads / a.lanes) * (write ? 2 : 4);
-    const dim3 grid((unsigned)((rows + each - 1) / each), (unsigned)(a.B < 65535 ? a.B : 65535));
+    a.lanes_log2 = 1;
+    while ((vec << a.lanes_log2) < a.D) ++a.lanes_log2;
+    const long long pieces = ((long long)a.T + msda::kMoveTokens - 1) / msda::kMoveTokens * a.N, each = msda::kMoveThreads / 32;
+    const dim3 grid((unsigned)((pieces + each - 1) / each), (unsigned)(a.B < 65535 ? a.B : 65535));
     if (format == MSDA_CACHE_SAME) return move_go<T, msda::kCacheSame>(a, write, grid, st);
     if (format == MSDA_CACHE_E4M3) return move_go<T, msda::kCacheE4m3>(a, write, grid, st);
     return move_go<T, msda::kCacheInt8>(a, write, grid, st);
@@ -466,8 +497,12 @@ msda_status check_attention(msda_dtype dt, int format, const msda_cache_problem*
     if (p->M < 1 || p->M % p->N) return failf(MSDA_ERR_INVALID_ARG, "N=%lld key heads do not divide M=%lld query heads", (long long)p->N, (long long)p->M);
     if (p->M > 65535) return failf(MSDA_ERR_UNSUPPORTED, "M=%lld too large", (long long)p->M);
     const int64_t G = p->M / p->N;
-    if (p->T * G > kMost || p->B * p->N * ((p->T * G + 15) / 16) > 0x7fffffffll / 2)
-        return failf(MSDA_ERR_UNSUPPORTED, "B=%lld sequences of T=%lld tokens and M=%lld heads are too many", (long long)p->B, (long long)p->T, (long long)p->M);
+    // the line of all tiles (16 rows, 64 keys at least) is counted in 32 bits
+    const int64_t tiles = (p->longest + 63) / 64 + (p->source + 63) / 64 + 1, rows = (p->T * G + 15) / 16;
+    int64_t all;
+    if (p->T * G > kMost || !msda::mul_fits(p->B * p->N, rows, &all) || !msda::mul_fits(all, tiles, &all) || all > 0x7fffffffll / 2)
+        return failf(MSDA_ERR_UNSUPPORTED, "B=%lld sequences of T=%lld tokens and M=%lld heads over %lld tokens are too many for one call", (long long)p->B,
+                     (long long)p->T, (long long)p->M, (long long)p->longest);
     return MSDA_OK;
 }
 
@@ -475,25 +510,64 @@ msda_status check_attention(msda_dtype dt, int format, const msda_cache_problem*
 struct CachePlan {
     msda::CacheRowsShape shape;
     int64_t rows, row_tiles, units, most_tiles;  // most_tiles: of a unit
+    int nq;                                      // row tiles of 128 a block on the tensor cores (tcgen05); 0: the kernel of few rows
     int blocks, least, whole;
-    size_t bytes;
+    size_t part_l2, units_at, bytes;             // workspace: rows, their statistics, where each unit's parts are
 };
+
+// Whether TMA can read a tensor's three dimensions at these strides (elements of `es` bytes): whole vectors, checked already, and
+// neither broadcast nor 2^40 bytes apart.
+bool tma_strides(const int64_t* st, int64_t a, int64_t b, int64_t c, int64_t es) {
+    const int64_t n[3] = {a, b, c};
+    for (int i = 0; i < 3; ++i)
+        if (n[i] > 1 && (st[i] == 0 || st[i] * es >= 1ll << 40)) return false;
+    return true;
+}
+
+// The tensor-core kernel's row tiles: 16-bit queries with more rows a key head than the mma.sync kernel has in a tile.
+int tc_tiles(msda_dtype dt, int format, const msda_cache_problem* p, int64_t rows) {
+    const int64_t G = p->M / p->N, es = format == MSDA_CACHE_SAME ? 2 : 1;
+    if (dt == MSDA_F32 || rows <= 32 || G > msda::kTcRows) return 0;
+    if (!tma_strides(p->query_stride, p->B, p->T, p->M, 2 * G) || !tma_strides(p->cache_key_stride, p->pages, p->page, p->N, es) ||
+        !tma_strides(p->cache_value_stride, p->pages, p->page, p->N, es))
+        return 0;
+    if (format == MSDA_CACHE_SAME && p->source > 0 &&
+        (!tma_strides(p->key_stride, p->B, p->source, p->N, 2) || !tma_strides(p->value_stride, p->B, p->source, p->N, 2)))
+        return 0;
+    return rows > msda::kTcRows / G * G ? 2 : 1;
+}
+
 CachePlan plan_of(msda_dtype dt, int format, const msda_cache_problem* p) {
     CachePlan c{};
-    c.rows = p->T * (p->M / p->N);
-    c.shape = dt == MSDA_F32   ? msda::cache_rows_shape<float>(format, (int)p->D, (int)c.rows)
+    const int64_t G = p->M / p->N;
+    c.rows = p->T * G;
+    c.nq = tc_tiles(dt, format, p, c.rows);
+    if (c.nq) c.shape = {(int)(c.nq * (msda::kTcRows / G * G)), msda::kTcRows, msda::kTcRows, 1};
+    else c.shape = dt == MSDA_F32   ? msda::cache_rows_shape<float>(format, (int)p->D, (int)c.rows)
               : dt == MSDA_F16 ? msda::cache_rows_shape<__half>(format, (int)p->D, (int)c.rows)
                                : msda::cache_rows_shape<__nv_bfloat16>(format, (int)p->D, (int)c.rows);
     c.row_tiles = (c.rows + c.shape.tile_rows - 1) / c.shape.tile_rows;
     c.units = p->B * p->N * c.row_tiles;
     c.most_tiles = (p->longest + c.shape.tile_keys - 1) / c.shape.tile_keys + (p->source + c.shape.tail_keys - 1) / c.shape.tail_keys;
     if (c.most_tiles < 1) c.most_tiles = 1;
-    c.least = 4;
+    c.least = c.nq ? 2 : 4;
     c.whole = c.most_tiles <= 2 * c.least;
     const int64_t most = msda::kPlanSms * c.shape.resident, want = (c.units * c.most_tiles + c.least - 1) / c.least;
     c.blocks = (int)(c.whole ? c.units : want < most ? want : most);
-    c.bytes = c.whole ? 0 : (size_t)c.blocks * 2 * c.shape.tile_rows * (p->D + 1) * 4;
+    c.part_l2 = (size_t)c.blocks * 2 * c.shape.tile_rows * p->D * 4;
+    c.units_at = c.part_l2 + (size_t)c.blocks * 2 * c.shape.tile_rows * 4;
+    c.bytes = c.whole ? 0 : c.units_at + (size_t)c.units * 8;
     return c;
+}
+
+template <int F>
+cudaError_t launch_tc_format(const CacheArgs& a, msda_dtype dt, int nq, int grid, cudaStream_t st) {
+    return dt == MSDA_BF16 ? msda::launch_cache_tc<true, F>(a, nq, grid, st) : msda::launch_cache_tc<false, F>(a, nq, grid, st);
+}
+cudaError_t launch_tc(const CacheArgs& a, msda_dtype dt, int format, int nq, int grid, cudaStream_t st) {
+    if (format == MSDA_CACHE_SAME) return launch_tc_format<msda::kCacheSame>(a, dt, nq, grid, st);
+    if (format == MSDA_CACHE_E4M3) return launch_tc_format<msda::kCacheE4m3>(a, dt, nq, grid, st);
+    return launch_tc_format<msda::kCacheInt8>(a, dt, nq, grid, st);
 }
 
 }  // namespace
@@ -590,15 +664,17 @@ msda_status msda_cache_attention(msda_dtype dt, int format, const msda_cache_pro
     a.tile_keys = plan.shape.tile_keys, a.tail_keys = plan.shape.tail_keys;
     a.c2 = (float)(scale * (double)msda::kLog2e);
     a.out = out, a.lse = lse;
-    a.part_o = static_cast<float*>(workspace);
-    a.part_l2 = a.part_o + (size_t)plan.blocks * 2 * plan.shape.tile_rows * p->D;
+    a.part_o = static_cast<float*>(workspace);  // null where no unit is shared
+    a.part_l2 = reinterpret_cast<float*>(static_cast<unsigned char*>(workspace) + plan.part_l2);
+    a.units = reinterpret_cast<int2*>(static_cast<unsigned char*>(workspace) + plan.units_at);
     a.blocks = plan.blocks, a.least = plan.least, a.whole = plan.whole;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     bool traced;
     {
         msda::TraceSpan ts(st);
         traced = ts.slot >= 0;
-        const cudaError_t e = dt == MSDA_F32   ? msda::launch_cache_rows<float>(a, format, plan.blocks, st)
+        const cudaError_t e = plan.nq          ? launch_tc(a, dt, format, plan.nq, plan.blocks, st)
+                              : dt == MSDA_F32 ? msda::launch_cache_rows<float>(a, format, plan.blocks, st)
                               : dt == MSDA_F16 ? msda::launch_cache_rows<__half>(a, format, plan.blocks, st)
                                                : msda::launch_cache_rows<__nv_bfloat16>(a, format, plan.blocks, st);
         ts.end(MSDA_KERNEL_CACHE_ATTENTION, p->B * p->M * p->T);

@@ -43,6 +43,7 @@ struct CacheArgs {
     void* out;                                        // [B, T, M, D]
     float* lse;                                       // [B, M, T]
     float *part_o, *part_l2;                          // [2 a block][tile_rows][D], [2 a block][tile_rows]
+    int2* units;                                      // of each unit: slot of its first part (-1: it has none), parts
     int blocks, least;                                // blocks of the grid; tiles a block takes at least
     int whole;                                        // a block a unit, nothing to join
 };
@@ -94,11 +95,11 @@ __device__ __forceinline__ void cache_unit_tiles(const CacheArgs& a, CacheUnit& 
     u.tiles = max(1, u.cache_tiles + (cache_tail_keys(a, u.rt, u.count) + a.tail_keys - 1) / a.tail_keys);
 }
 // tiles of all row tiles of one key head of sequence b
-__device__ __forceinline__ long long cache_head_tiles(const CacheArgs& a, int b) {
+__device__ __forceinline__ int cache_head_tiles(const CacheArgs& a, int b) {
     CacheUnit u;
     u.b = b, u.n = 0;
     u.length = cache_length(a.c, a.lengths, b), u.count = cache_count(a.c, a.counts, b, a.T);
-    long long sum = 0;
+    int sum = 0;
     for (u.rt = 0; u.rt < a.row_tiles; ++u.rt) {
         cache_unit_tiles(a, u);
         sum += u.tiles;
@@ -122,39 +123,25 @@ __device__ __forceinline__ void cache_next_unit(const CacheArgs& a, CacheUnit& u
     cache_unit_tiles(a, u);
 }
 
-// Whole warp.  Tiles of all sequences (returned) and of those in front of `b`.
-__device__ __forceinline__ long long cache_all_tiles(const CacheArgs& a, int b, long long* before) {
+// Whole warp.  Tiles of all sequences.
+__device__ __forceinline__ int cache_all_tiles(const CacheArgs& a) {
     const int lane = threadIdx.x & 31;
-    long long sum = 0, front = 0;
-    for (int i = lane; i < a.B; i += 32) {
-        const long long n = cache_head_tiles(a, i) * a.N;
-        sum += n;
-        if (i < b) front += n;
-    }
-#pragma unroll
-    for (int w = 16; w > 0; w >>= 1) {
-        sum += __shfl_xor_sync(0xffffffffu, sum, w);
-        front += __shfl_xor_sync(0xffffffffu, front, w);
-    }
-    *before = front;
-    return sum;
+    int sum = 0;
+    for (int i = lane; i < a.B; i += 32) sum += cache_head_tiles(a, i) * a.N;
+    return __reduce_add_sync(0xffffffffu, sum);
 }
-__device__ __forceinline__ long long cache_share(const CacheArgs& a, long long all) {
-    const long long each = (all + a.blocks - 1) / a.blocks;
-    return each > a.least ? each : a.least;
-}
+__device__ __forceinline__ int cache_share(const CacheArgs& a, int all) { return max((all + a.blocks - 1) / a.blocks, a.least); }
 
 // Whole warp.  The unit and the tile within it at place x of the line.
-__device__ __forceinline__ void cache_find(const CacheArgs& a, long long x, CacheUnit& u, int* tile) {
+__device__ __forceinline__ void cache_find(const CacheArgs& a, int x, CacheUnit& u, int* tile) {
     const int lane = threadIdx.x & 31;
-    int b = 0;
-    long long head = 1;
+    int b = 0, head = 1;
     for (int b0 = 0; b0 < a.B; b0 += 32) {
-        const long long mine = b0 + lane < a.B ? cache_head_tiles(a, b0 + lane) : 0;
-        long long upto = mine * a.N;
+        const int mine = b0 + lane < a.B ? cache_head_tiles(a, b0 + lane) : 0;
+        int upto = mine * a.N;
 #pragma unroll
         for (int w = 1; w < 32; w <<= 1) {
-            const long long o = __shfl_up_sync(0xffffffffu, upto, w);
+            const int o = __shfl_up_sync(0xffffffffu, upto, w);
             if (lane >= w) upto += o;
         }
         const unsigned behind = __ballot_sync(0xffffffffu, upto > x);
@@ -167,7 +154,7 @@ __device__ __forceinline__ void cache_find(const CacheArgs& a, long long x, Cach
         }
         x -= __shfl_sync(0xffffffffu, upto, 31);
     }
-    const int n = (int)(x / head);
+    const int n = x / head;
     x -= n * head;
     cache_unit_at(a, b, n, 0, u);
     while (x >= u.tiles) {
@@ -175,7 +162,7 @@ __device__ __forceinline__ void cache_find(const CacheArgs& a, long long x, Cach
         ++u.rt;
         cache_unit_tiles(a, u);
     }
-    *tile = (int)x;
+    *tile = x;
 }
 
 // The share of a block: calls f(unit, first tile, tiles, slot) for each unit that it has tiles of; `slot`: where the part
@@ -191,16 +178,19 @@ __device__ __forceinline__ void cache_walk(const CacheArgs& a, F f) {
         f(u, 0, u.tiles, -1);
         return;
     }
-    long long none;
-    const long long all = cache_all_tiles(a, 0, &none), share = cache_share(a, all);
-    const long long x0 = blockIdx.x * share;
-    long long left = min(share, all - x0);
-    if (left <= 0) return;
+    const int all = cache_all_tiles(a), share = cache_share(a, all);
+    const long long at = (long long)blockIdx.x * share;
+    if (at >= all) return;
+    const int x0 = (int)at;
+    int left = min(share, all - x0);
     int tile;
     cache_find(a, x0, u, &tile);
     bool first = true;
     while (left > 0) {
-        const int n = (int)min((long long)(u.tiles - tile), left);
+        const int n = min(u.tiles - tile, left);
+        if (tile == 0 && threadIdx.x == 0)  // its first block says where its parts are
+            a.units[(u.b * a.N + u.n) * a.row_tiles + u.rt] =
+                make_int2(n == u.tiles ? -1 : 2 * (int)blockIdx.x + (first ? 0 : 1), 1 + (u.tiles - n + share - 1) / share);
         f(u, tile, n, n == u.tiles ? -1 : 2 * (int)blockIdx.x + (first ? 0 : 1));
         left -= n, tile = 0, first = false;
         if (left > 0) cache_next_unit(a, u);
@@ -232,6 +222,7 @@ __device__ __forceinline__ void cache_four_f16(uint32_t w, uint32_t& lo, uint32_
     }
 }
 
+// Joins the parts of units that several blocks shared; `early`: as a programmatic dependent of the kernel that makes them.
 cudaError_t launch_cache_join(const CacheArgs& a, int dtype, bool early, cudaStream_t st);
 
 // Attention of few rows a key head (tiles of 16 or 32): 128 threads, `bytes` of shared memory a block, `resident` blocks an SM.

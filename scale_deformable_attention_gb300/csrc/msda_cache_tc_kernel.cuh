@@ -1,0 +1,786 @@
+// msda_cache_tc_kernel.cuh -- attention over the paged cache of many rows a key head
+// (drafted trees of shared heads, pieces of prompts) on the tensor cores
+// (tcgen05, sm_103a), fp16 and bf16 queries, D a multiple of 16 up to 128.
+//
+//   S = Q K^T,  P = 2^(c S - m),  l += row sums,  O = 2^(m_old - m) O + P V
+//
+// A block an SM takes an equal share of the line of all tiles (see the plan in
+// msda_cache.cuh), unit after unit: NQ tiles of up to 128 rows of one key head
+// (tokens times the G heads that share it side by side) over tiles of 128 keys.
+// Warps:
+//   - one warpgroup a row tile on the scores, a thread a row: it reads S from
+//     tensor memory and writes P (16 bits) back; O stays in tensor memory;
+//   - one issues the TMA copies, a box of each page's rows that a tile holds, one
+//     a row tile its products;
+//   - unquantised: one clears the value rows that lie behind a sequence's last;
+//   - 8 bits: a warpgroup turns the codes of a tile, a row a thread, into f16 rows
+//     of the operands (whole values, exact), brought to the scale of the tile's
+//     largest row: the scores of the tile are multiplied by that scale of K, its
+//     P by that of V over the largest met.  New tokens' rows go the same way.
+// bf16 queries of a quantised cache become f16 with a power of two a row.
+//
+// The reference m follows when a row's sum over a tile passes a limit, as in the
+// dense forward: P is in f16 at most 49152 and m 2^6 below the maximum when it is
+// looked for, in bf16 2^14.
+#pragma once
+
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
+#include "msda_attention_tc.cuh"
+#include "msda_cache.cuh"
+#include "msda_cache_tc.cuh"
+#include "msda_host.cuh"
+
+namespace msda {
+
+namespace {
+
+template <bool OB>
+struct CacheTcRange {
+    static constexpr float kTop = OB ? 16384.f : 49152.f;  // the largest sum of a row over a tile; f16 holds 65504
+    static constexpr float kBelow = OB ? 0.f : 6.f;        // m below the maximum
+};
+
+template <int F, int NQ, int NC>
+struct CacheTcCfg {
+    static constexpr bool kCodes = F != kCacheSame;
+    static constexpr int kStages = NC == 1 ? (kCodes ? 6 : 8) : (kCodes && NQ == 2) ? 3 : 4;  // ring of K and V operand tiles
+    static constexpr int kRaw = !kCodes ? 0 : NC == 1 ? 6 : 4;                                  // ring of tiles of codes
+    static constexpr int kThreads = NQ * 128 + 128 + (kCodes ? 128 : 0);
+    static constexpr uint32_t kTileBytes = NC * kTcTile, kRawBytes = NC * 64 * 128;
+    // registers of a thread of the warpgroups on the scores, of the one that issues and of the one that converts: the launch
+    // has 168 a thread with three warpgroups, 128 with four, 255 with two (no split there)
+    static constexpr int kUp = NQ == 1 ? (kCodes ? 232 : 0) : kCodes ? 192 : 208;
+    static constexpr int kDown = NQ == 1 ? 136 : kCodes ? 56 : 88, kConvert = NQ == 1 ? 136 : 72;
+    static_assert(kUp == 0 || NQ * kUp + kDown + (kCodes ? kConvert : 0) <= (kThreads == 512 ? 512 : 504), "more registers than the launch has");
+    // tensor memory: S (128 columns a row tile), P (64), O (64 or 128); two row tiles of up to 128 channels leave no room
+    // for P: it lies over S, and the next S waits until P is used up
+    static constexpr bool kOwnP = NC == 1 || NQ == 1;
+    static constexpr uint32_t kP = kOwnP ? NQ * 128 : 0, kPStep = kOwnP ? 64 : 128;
+    static constexpr uint32_t kO = kOwnP ? NQ * 192 : NQ * 128;
+    static constexpr uint32_t kCols = NQ == 2 || NC == 2 ? 512 : 256;
+    static constexpr size_t kSmem = (size_t)(NQ + kStages) * kTileBytes + (size_t)kRaw * kRawBytes + 1024;
+};
+
+struct CacheTcSync {
+    uint64_t full[8], empty[8], raw_full[6], raw_empty[6];
+    uint64_t cleared[8], q_full, q_empty, tops_full, s_full[2], s_free[2], p_full[2], pv_done[2], turn;
+    uint32_t tmem, abort;
+    uint32_t words[8][4];    // a tile's keys that are there
+    float k_scale[8];        // 8 bits: scale of a tile's K, and the byte of that of its V
+    uint32_t v_top[8];
+    uint32_t tops[2][4];
+};
+
+__device__ __forceinline__ void tc_tma_4d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int c0, int c1, int c2, int c3) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
+        : "memory");
+}
+
+// A unit's tiles of a block: cache tiles first, then those of the new tokens.
+struct CacheSegment {
+    CacheUnit u;
+    int first, n, slot;  // tiles [first, first + n) of the unit
+    int tail_keys;
+};
+
+// Calls f(segment) for each unit of the block; false ends it.  n is 0 for rows that see nothing.
+template <typename F>
+__device__ __forceinline__ void cache_segments(const CacheArgs& a, F f) {
+    bool ok = true;
+    cache_walk(a, [&](const CacheUnit& u, int tile, int tiles, int slot) {
+        if (!ok) return;
+        CacheSegment s;
+        s.u = u, s.first = tile, s.slot = slot;
+        s.tail_keys = cache_tail_keys(a, u.rt, u.count);
+        s.n = max(0, min(tiles, u.cache_tiles + (s.tail_keys + kTcRows - 1) / kTcRows - tile));
+        ok = f(s);
+    });
+}
+
+}  // namespace
+
+template <bool BF16, int F, int NQ, int NC>
+__global__ void __launch_bounds__(CacheTcCfg<F, NQ, NC>::kThreads, 1)
+    msda_cache_tc_kernel(const CacheArgs a, const int box_rows, const __grid_constant__ CUtensorMap map_q,
+                         const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
+                         const __grid_constant__ CUtensorMap map_nk, const __grid_constant__ CUtensorMap map_nv) {
+    using Cfg = CacheTcCfg<F, NQ, NC>;
+    constexpr bool CODES = Cfg::kCodes, OB = BF16 && !CODES, OWN_Q = BF16 && CODES;  // operands in bf16; queries turned into f16 by their rows' threads
+    using Range = CacheTcRange<OB>;
+    using T = typename std::conditional<BF16, __nv_bfloat16, __half>::type;
+    constexpr int ST = Cfg::kStages;
+    extern __shared__ unsigned char cache_tc_smem[];
+    unsigned char* smem = cache_tc_smem + ((1024u - (tc_smem(cache_tc_smem) & 1023u)) & 1023u);
+    unsigned char* q_tiles = smem;
+    unsigned char* ring = smem + NQ * Cfg::kTileBytes;
+    unsigned char* raw = ring + ST * Cfg::kTileBytes;
+    __shared__ CacheTcSync sy;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int qpt = a.tile_rows / (NQ * a.G), rows = qpt * a.G;  // tokens and rows of a row tile
+
+    if (warp == NQ * 4) {
+        if (lane == 0) {
+            for (int i = 0; i < 8; ++i) {
+                tc_bar_init(tc_smem(&sy.full[i]), CODES ? 4 : 1);
+                tc_bar_init(tc_smem(&sy.empty[i]), NQ);
+                tc_bar_init(tc_smem(&sy.cleared[i]), 1);
+            }
+            for (int i = 0; i < 6; ++i) {
+                tc_bar_init(tc_smem(&sy.raw_full[i]), 1);
+                tc_bar_init(tc_smem(&sy.raw_empty[i]), 4);
+            }
+            tc_bar_init(tc_smem(&sy.q_full), OWN_Q ? NQ * 4 : 1);
+            tc_bar_init(tc_smem(&sy.q_empty), NQ);
+            tc_bar_init(tc_smem(&sy.tops_full), 4);
+            tc_bar_init(tc_smem(&sy.turn), 1);
+            for (int i = 0; i < 2; ++i) {
+                tc_bar_init(tc_smem(&sy.s_full[i]), 1);
+                tc_bar_init(tc_smem(&sy.s_free[i]), 4);
+                tc_bar_init(tc_smem(&sy.p_full[i]), 4);
+                tc_bar_init(tc_smem(&sy.pv_done[i]), 1);
+            }
+            sy.abort = 0;
+            asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        }
+    } else if (warp == NQ * 4 + 1) {
+        tmem_alloc(tc_smem(&sy.tmem), Cfg::kCols);
+    }
+    if (rows < kTcRows) {  // rows that no query fills hold zeros, not what was there
+        const uint32_t words = (kTcRows - rows) * 8;
+        for (uint32_t i = tid; i < NQ * NC * words; i += Cfg::kThreads) {
+            const uint32_t c = i / words, w = i - c * words;
+            *reinterpret_cast<uint4*>(q_tiles + c * kTcTile + rows * 128 + w * 16) = make_uint4(0, 0, 0, 0);
+        }
+        tc_fence_async();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = sy.tmem;
+    volatile uint32_t* abort = &sy.abort;
+    unsigned* err = a.c.err;
+    bool ok = true;
+
+    if (warp < NQ * 4) {
+        if constexpr (Cfg::kUp > 0) tc_regs_up<Cfg::kUp>();
+        // ---- scores: row `row` of tile `t` ----
+        const int t = warp >> 2, wl = warp & 3, row = wl * 32 + lane;
+        const uint32_t lanes = (uint32_t)wl << 21;
+        const uint32_t s_at = tmem + t * 128 + lanes, o_at = tmem + Cfg::kO + t * (NC * 64) + lanes;
+        const uint32_t p_at = tmem + Cfg::kP + t * Cfg::kPStep + lanes;
+        const int chunks = a.D / 16;
+        const uint32_t first = lane == 0;
+        int g0 = 0;  // tiles before this segment
+        cache_segments(a, [&](const CacheSegment& sg) {
+            const CacheUnit& u = sg.u;
+            const int tok = u.rt * NQ * qpt + t * qpt + row / a.G, h = u.n * a.G + row % a.G;
+            const bool there = row < rows && tok < a.T, valid = there && tok < u.count;
+            const bool warp_on = __any_sync(0xffffffffu, valid);
+            float c2 = a.c2;
+            if constexpr (OWN_Q) {
+                if (sg.n > 0) {
+                    // the row in f16, its largest brought to 2^14 or more
+                    const T* q = static_cast<const T*>(a.q) + u.b * a.q_sb + tok * a.q_st + h * a.q_sh;
+                    uint32_t top = 0;
+                    if (valid)
+                        for (int d = 0; d < a.D; d += 8) {
+                            const uint4 x = *reinterpret_cast<const uint4*>(q + d);
+                            const uint32_t m = 0x7fff7fffu;
+                            top = __vmaxu2(top, __vmaxu2(__vmaxu2(x.x & m, x.y & m), __vmaxu2(x.z & m, x.w & m)));
+                        }
+                    const int e = (int)(max(top & 0xffffu, top >> 16) >> 7);
+                    const float up = e > 0 && e < 255 ? __uint_as_float((uint32_t)min(max(268 - e, 27), 227) << 23) : 1.f;
+                    c2 = a.c2 * (1.f / up);
+                    if (row < rows)
+                        for (int d = 0; d < NC * 64; d += 8) {
+                            uint4 y = make_uint4(0, 0, 0, 0);
+                            if (valid && d < a.D) {
+                                const uint4 x = *reinterpret_cast<const uint4*>(q + d);
+                                const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+                                uint32_t p[4];
+#pragma unroll
+                                for (int k = 0; k < 4; ++k)
+                                    p[k] = tc_pack<false>(__uint_as_float(w[k] << 16) * up, __uint_as_float(w[k] & 0xffff0000u) * up);
+                                y = make_uint4(p[0], p[1], p[2], p[3]);
+                            }
+                            *reinterpret_cast<uint4*>(q_tiles + (t * NC + d / 64) * kTcTile + row * 128 + ((((d / 8) & 7) ^ (row & 7)) << 4)) = y;
+                        }
+                    tc_fence_async();
+                    __syncwarp();
+                    tc_bar_arrive_if(first, tc_smem(&sy.q_full));
+                }
+            }
+            float m = -attn_inf(), l = 0.f;
+            uint32_t v_ref = 0;
+#pragma unroll 1
+            for (int i = 0; i < sg.n; ++i) {
+                const int gi = g0 + i, tile = sg.first + i;
+                uint32_t w[4] = {~0u, ~0u, ~0u, ~0u};
+                const bool tail = tile >= u.cache_tiles;
+                if (tail) {
+                    const int j0 = (tile - u.cache_tiles) * kTcRows, left = (valid ? u.count : 0) - j0;
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) w[c] = tc_low_bits((a.mask ? left : min(left, tok + 1 - j0)) - 32 * c);
+                    if (a.mask && valid) {
+                        const uint8_t* mask = a.mask + u.b * a.mk_sb + tok * a.mk_sq + j0;
+                        const int n = min(left, kTcRows);
+                        const bool fours = (reinterpret_cast<uintptr_t>(mask) & 3) == 0;
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) {
+                            uint32_t bits = 0;
+                            if (fours) {
+                                for (int k = 0; k < 32; k += 4) {
+                                    const int j = c * 32 + k;
+                                    uint32_t x = 0;
+                                    if (j + 4 <= n) x = *reinterpret_cast<const uint32_t*>(mask + j);
+                                    else
+                                        for (int e = 0; e < 4; ++e)
+                                            if (j + e < n) x |= (uint32_t)mask[j + e] << (8 * e);
+#pragma unroll
+                                    for (int e = 0; e < 4; ++e) bits |= ((x >> (8 * e)) & 255u ? 1u : 0u) << (k + e);
+                                }
+                            } else {
+                                for (int k = 0; k < 32; ++k)
+                                    if (c * 32 + k < n && mask[c * 32 + k]) bits |= 1u << k;
+                            }
+                            w[c] &= bits;
+                        }
+                    }
+                }
+                __syncwarp();
+                if (!tc_bar_wait(tc_smem(&sy.s_full[t]), gi & 1, abort, err)) return false;
+                tc_fence_after();
+                if (warp_on) {
+                    uint32_t s[4][32];
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) tmem_ld32(s[c], s_at + c * 32);
+                    tmem_wait_ld();
+                    if constexpr (Cfg::kOwnP) {  // the next S may be written now
+                        tc_fence_before();
+                        tc_bar_arrive_if(first, tc_smem(&sy.s_free[t]));
+                    }
+                    if (!tail) {
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) w[c] = sy.words[gi & 7][c];
+                    }
+                    if (__builtin_expect(__any_sync(0xffffffffu, (w[0] & w[1] & w[2] & w[3]) != 0xffffffffu), 0)) {
+#pragma unroll
+                        for (int c = 0; c < 4; ++c)
+#pragma unroll
+                            for (int k = 0; k < 32; ++k)
+                                if (!((w[c] >> k) & 1u)) s[c][k] = 0xff800000u;
+                    }
+                    float ct = c2, dv = 0.f;  // this tile's factor of the scores; binary places of its values' scale below v_ref
+                    uint32_t v_old = v_ref;
+                    if constexpr (CODES) {
+                        ct = fmaxf(c2 * sy.k_scale[gi & 7], 1e-37f);  // never 0, which would make NaN of what is masked
+                        const uint32_t vt = sy.v_top[gi & 7];
+                        if (vt > v_ref) v_ref = vt;
+                        dv = fmaxf((float)((int)vt - (int)v_ref), -60.f);  // beyond 2^-60 of the largest value nothing counts
+                    }
+                    const uint64_t cc = tc_two(ct, ct);
+                    bool gone = false;
+                    // P = 2^(c S - m) into tensor memory; the row's sum.  `wait`: the last P may still be read.
+                    auto probabilities = [&](bool wait) {
+                        const float ref = (m == -attn_inf() ? 0.f : m) - dv;
+                        const uint64_t nref = tc_two(-ref, -ref);
+                        uint64_t part[2] = {0, 0};
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) {
+                            uint32_t pk[16];
+#pragma unroll
+                            for (int k = 0; k < 16; ++k) {
+                                float x0, x1;
+                                tc_split(tc_fma2(tc_two(__uint_as_float(s[c][2 * k]), __uint_as_float(s[c][2 * k + 1])), cc, nref), x0, x1);
+                                const float e0 = tc_ex2(x0), e1 = tc_ex2(x1);
+                                part[k & 1] = tc_add2(part[k & 1], tc_two(e0, e1));
+                                pk[k] = tc_pack<OB>(e0, e1);
+                            }
+                            if (c == 0 && wait) {
+                                gone = !tc_bar_wait(tc_smem(&sy.pv_done[t]), (gi - 1) & 1, abort, err);
+                                tc_fence_after();
+                            }
+                            tmem_st16(p_at + c * 16, pk);
+                        }
+                        float s0, s1;
+                        tc_split(tc_add2(part[0], part[1]), s0, s1);
+                        return s0 + s1;
+                    };
+                    bool renew = (CODES && v_ref != v_old && i > 0) || __any_sync(0xffffffffu, valid && m == -attn_inf());
+                    float sum = 0.f;
+                    if (__builtin_expect(!renew, 1)) {
+                        sum = probabilities(Cfg::kOwnP && i > 0);
+                        renew = __any_sync(0xffffffffu, valid && !(sum <= Range::kTop));
+                    } else if (Cfg::kOwnP && i > 0) {
+                        gone = !tc_bar_wait(tc_smem(&sy.pv_done[t]), (gi - 1) & 1, abort, err);
+                        tc_fence_after();
+                    }
+                    if (__builtin_expect(renew, 0)) {
+                        float mx[4];
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) {
+                            mx[c] = fmaxf(__uint_as_float(s[c][0]), __uint_as_float(s[c][1]));
+#pragma unroll
+                            for (int k = 2; k < 32; k += 2)
+                                mx[c] = tc_max3(mx[c], __uint_as_float(s[c][k]), __uint_as_float(s[c][k + 1]));
+                        }
+                        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * ct;
+                        const float next = fmaxf(m, top - Range::kBelow);
+                        const float f = next == m ? 1.f : tc_ex2(m - next);
+                        m = next;
+                        l *= f;
+                        if (i > 0) {
+                            float fo = f;
+                            if constexpr (CODES) fo *= v_ref - v_old > 126 ? 0.f : cache_scale(127 + v_old - v_ref);
+                            for (int c = 0; c < chunks; ++c) {
+                                uint32_t o[16];
+                                tmem_ld16(o, o_at + c * 16);
+                                tmem_wait_ld();
+#pragma unroll
+                                for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * fo);
+                                tmem_st16(o_at + c * 16, o);
+                            }
+                        }
+                        sum = probabilities(false);
+                    }
+                    if (__builtin_expect(gone, 0)) return false;
+                    if constexpr (CODES) sum *= exp2f(-dv);
+                    l += sum;
+                    tmem_wait_st();
+                    tc_fence_before();
+                } else if constexpr (Cfg::kOwnP) {
+                    tc_bar_arrive_if(first, tc_smem(&sy.s_free[t]));
+                    // a warp without rows may not run a tile ahead of the others: its arrival would count for theirs
+                    if (i > 0 && !tc_bar_wait(tc_smem(&sy.pv_done[t]), (gi - 1) & 1, abort, err)) return false;
+                }
+                __syncwarp();
+                tc_bar_arrive_if(first, tc_smem(&sy.p_full[t]));
+            }
+            // ---- output ----
+            if (sg.n > 0) {
+                if (!tc_bar_wait(tc_smem(&sy.pv_done[t]), (g0 + sg.n - 1) & 1, abort, err)) return false;
+                tc_fence_after();
+            }
+            g0 += sg.n;
+            if (!__any_sync(0xffffffffu, there)) return true;
+            const bool none = l == 0.f || !valid;
+            float inv = none ? 0.f : 1.f / l;
+            if constexpr (CODES) inv *= v_ref == 0 ? 0.f : cache_scale(v_ref);
+            const float l2 = none ? -attn_inf() : m + log2f(l);
+            const long long at = (long long)sg.slot * a.tile_rows + t * rows + row;
+            for (int c = 0; c < chunks; ++c) {
+                uint32_t o[16];
+                if (sg.n > 0 && warp_on) {
+                    tmem_ld16(o, o_at + c * 16);
+                    tmem_wait_ld();
+                }
+                if (!there) continue;
+#pragma unroll
+                for (int k = 0; k < 16; ++k) o[k] = none ? 0u : __float_as_uint(__uint_as_float(o[k]) * inv);
+                if (sg.slot >= 0) {
+                    float* out = a.part_o + at * a.D + c * 16;
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) reinterpret_cast<uint4*>(out)[k] = make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+                } else {
+                    T* out = static_cast<T*>(a.out) + (((long long)u.b * a.T + tok) * a.M + h) * a.D + c * 16;
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        uint32_t v[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) v[e] = tc_pack<BF16>(__uint_as_float(o[8 * k + 2 * e]), __uint_as_float(o[8 * k + 2 * e + 1]));
+                        reinterpret_cast<uint4*>(out)[k] = make_uint4(v[0], v[1], v[2], v[3]);
+                    }
+                }
+            }
+            if (there) {
+                if (sg.slot >= 0) a.part_l2[at] = l2;
+                else a.lse[((long long)u.b * a.M + h) * a.T + tok] = l2 * kLn2;
+            }
+            tc_fence_before();
+            return true;
+        });
+        ok = !*abort;
+    } else if (warp < NQ * 4 + 4) {
+        if constexpr (Cfg::kUp > 0) tc_regs_down<Cfg::kDown>();
+        const int role = warp - NQ * 4;
+        if (role == 0) {
+            // ---- copies (all lanes: a box of rows each) ----
+            const int boxes = kTcRows / box_rows;
+            const uint32_t qbar = tc_smem(&sy.q_full);
+            int g0 = 0, r0 = 0, qs = 0;  // tiles, tiles of codes, queries so far
+            cache_segments(a, [&](const CacheSegment& sg) {
+                const CacheUnit& u = sg.u;
+                if (sg.n == 0) return true;
+                if constexpr (!OWN_Q) {
+                    if (qs > 0 && !tc_bar_wait(tc_smem(&sy.q_empty), (qs - 1) & 1, abort, err)) return false;
+                    if (lane == 0) {
+                        tc_bar_expect(qbar, NQ * NC * rows * 128);
+                        for (int t = 0; t < NQ; ++t)
+                            for (int c = 0; c < NC; ++c)
+                                tc_tma_5d(tc_smem(q_tiles) + (t * NC + c) * kTcTile, &map_q, qbar, c * 64, 0, (u.rt * NQ + t) * qpt, u.n, u.b);
+                    }
+                    ++qs;
+                }
+                auto page_of = [&](int tile) {  // of this lane's box
+                    const int token = tile * kTcRows + lane * box_rows;
+                    return lane < boxes && tile < u.cache_tiles && token < u.length ? cache_page(a.c, u.b, token) : -1;
+                };
+                int page = page_of(sg.first);
+                for (int i = 0; i < sg.n; ++i) {
+                    const int gi = g0 + i, tile = sg.first + i, mine = page;
+                    page = i + 1 < sg.n ? page_of(tile + 1) : -1;
+                    const bool tail = tile >= u.cache_tiles;
+                    if (!tail) {
+                        // a tile's words are read 8 tiles later at most: the rings are shorter
+                        const uint32_t good = __ballot_sync(0xffffffffu, mine >= 0);
+                        const int x = lane & 3;  // keys 32 x to 32 x + 31
+                        const uint32_t pages = box_rows >= 32 ? ((good >> (x * 32 / box_rows)) & 1u ? ~0u : 0u)
+                                                              : ((good >> (2 * x)) & 1u ? 0xffffu : 0u) | ((good >> (2 * x + 1)) & 1u ? 0xffff0000u : 0u);
+                        if (lane < 4) sy.words[gi & 7][x] = pages & tc_low_bits(u.length - tile * kTcRows - 32 * x);
+                        __syncwarp();
+                    }
+                    const int ring_n = CODES ? Cfg::kRaw : ST;
+                    if (tail && CODES) continue;  // the converters read them
+#pragma unroll
+                    for (int kv = 0; kv < 2; ++kv) {
+                        const int idx = 2 * (CODES ? r0 : gi) + kv, st = idx % ring_n;
+                        uint64_t* full = CODES ? sy.raw_full : sy.full;
+                        uint64_t* empty = CODES ? sy.raw_empty : sy.empty;
+                        if (idx >= ring_n && !tc_bar_wait(tc_smem(&empty[st]), (idx / ring_n - 1) & 1, abort, err)) return false;
+                        const uint32_t bar = tc_smem(&full[st]);
+                        const uint32_t dst = CODES ? tc_smem(raw) + st * Cfg::kRawBytes : tc_smem(ring) + st * Cfg::kTileBytes;
+                        if (lane == 0) tc_bar_expect(bar, CODES ? Cfg::kRawBytes : Cfg::kTileBytes);
+                        __syncwarp();
+                        if (tail) {
+                            if (lane < NC) tc_tma_4d(dst + lane * kTcTile, kv ? &map_nv : &map_nk, bar, lane * 64, u.n, (tile - u.cache_tiles) * kTcRows, u.b);
+                        } else if (lane < boxes) {
+                            const int pg = mine < 0 ? a.c.pages : mine, at = mine < 0 ? 0 : (tile * kTcRows + lane * box_rows) & (a.c.page - 1);
+                            if constexpr (CODES) {
+                                tc_tma_4d(dst + lane * box_rows * (NC * 64), kv ? &map_v : &map_k, bar, 0, u.n, at, pg);
+                            } else {
+                                for (int c = 0; c < NC; ++c)
+                                    tc_tma_4d(dst + c * kTcTile + lane * box_rows * 128, kv ? &map_v : &map_k, bar, c * 64, u.n, at, pg);
+                            }
+                        }
+                    }
+                    ++r0;
+                }
+                g0 += sg.n;
+                return true;
+            });
+        } else if (role == 1 || (NQ == 2 && role == 3)) {
+            // ---- products of row tile t ----
+            const int t = role >> 1;
+            const uint32_t on = tc_elect();
+            const uint32_t id_qk = tc_idesc(OB, false, false, 128, 128);
+            const int steps = a.D / 16;
+            const uint32_t id_pv = tc_idesc(OB, false, true, 128, steps * 16);
+            const uint32_t ring_at = tc_smem(ring);
+            const uint64_t q_desc = tc_desc(tc_smem(q_tiles) + t * Cfg::kTileBytes, 16, 1024);
+            const uint32_t s_at = tmem + t * 128, o_at = tmem + Cfg::kO + t * (NC * 64);
+            const uint32_t p_at = tmem + Cfg::kP + t * Cfg::kPStep;
+            auto product_s = [&](int st) {
+                const uint64_t k_desc = tc_desc(ring_at + st * Cfg::kTileBytes, 16, 1024);
+#pragma unroll
+                for (int k = 0; k < NC * 4; ++k) {  // 16 channels: 32 bytes further, 64: the next tile
+                    const uint64_t off = ((k >> 2) * kTcTile + (k & 3) * 32) >> 4;
+                    if (k < steps) tc_mma_ss(on, s_at, q_desc + off, k_desc + off, id_qk, k > 0);
+                }
+                tc_commit(on, tc_smem(&sy.s_full[t]));
+                tc_commit(on, tc_smem(&sy.empty[st]));
+            };
+            int g0 = 0, qs = 0;
+            uint32_t clears = 0;  // a bit a stage: which phase of its `cleared` is next
+            cache_segments(a, [&](const CacheSegment& sg) {
+                const CacheUnit& u = sg.u;
+                if (sg.n == 0) return true;
+                if (!tc_bar_wait(tc_smem(&sy.q_full), qs & 1, abort, err)) return false;
+                ++qs;
+                // K of tile gi, when S may be written
+                auto next_s = [&](int gi) {
+                    const int idx = 2 * gi, st = idx % ST;
+                    if (!tc_bar_wait(tc_smem(&sy.full[st]), (idx / ST) & 1, abort, err)) return false;
+                    if (Cfg::kOwnP && gi > 0 && !tc_bar_wait(tc_smem(&sy.s_free[t]), (gi - 1) & 1, abort, err)) return false;
+                    tc_fence_after();
+                    product_s(st);
+                    return true;
+                };
+                // P over S: the second row tile starts when the first has worked out its first P
+                if (!Cfg::kOwnP && t == 1 && g0 == 0 && !tc_bar_wait(tc_smem(&sy.turn), 0, abort, err)) return false;
+                if (!next_s(g0)) return false;
+                for (int i = 0; i < sg.n; ++i) {
+                    const int gi = g0 + i, iv = 2 * gi + 1, sv = iv % ST, tile = sg.first + i;
+                    const bool more = i + 1 < sg.n;
+                    if (Cfg::kOwnP && more && !next_s(gi + 1)) return false;
+                    if (!tc_bar_wait(tc_smem(&sy.full[sv]), (iv / ST) & 1, abort, err)) return false;
+                    if constexpr (!CODES) {
+                        const int left = tile < u.cache_tiles ? u.length - tile * kTcRows : u.count - (tile - u.cache_tiles) * kTcRows;
+                        if (left < kTcRows) {
+                            if (!tc_bar_wait(tc_smem(&sy.cleared[sv]), (clears >> sv) & 1, abort, err)) return false;
+                            clears ^= 1u << sv;
+                        }
+                    }
+                    if (!tc_bar_wait(tc_smem(&sy.p_full[t]), gi & 1, abort, err)) return false;
+                    tc_fence_after();
+                    if (!Cfg::kOwnP && NQ == 2 && t == 0 && gi == 0) tc_bar_arrive_if(on, tc_smem(&sy.turn));
+                    const uint64_t v_desc = tc_desc(ring_at + sv * Cfg::kTileBytes, kTcTile, 1024);
+#pragma unroll
+                    for (int k = 0; k < 8; ++k)  // 16 keys: two atoms further
+                        tc_mma_ts(on, o_at, p_at + k * 8, v_desc + ((k * 2048) >> 4), id_pv, i > 0 || k > 0);
+                    tc_commit(on, tc_smem(&sy.pv_done[t]));
+                    tc_commit(on, tc_smem(&sy.empty[sv]));
+                    if (!Cfg::kOwnP && more && !next_s(gi + 1)) return false;
+                }
+                if constexpr (!OWN_Q) tc_commit(on, tc_smem(&sy.q_empty));
+                g0 += sg.n;
+                return true;
+            });
+        } else if (role == 2 && !CODES) {
+            // ---- value rows behind the last ----
+            int g0 = 0;
+            cache_segments(a, [&](const CacheSegment& sg) {
+                const CacheUnit& u = sg.u;
+                for (int i = 0; i < sg.n; ++i) {
+                    const int tile = sg.first + i, idx = 2 * (g0 + i) + 1, st = idx % ST;
+                    const int left = tile < u.cache_tiles ? u.length - tile * kTcRows : u.count - (tile - u.cache_tiles) * kTcRows;
+                    if (left >= kTcRows) continue;
+                    if (!tc_bar_wait(tc_smem(&sy.full[st]), (idx / ST) & 1, abort, err)) return false;
+                    const uint32_t w[4] = {tc_low_bits(left), tc_low_bits(left - 32), tc_low_bits(left - 64), tc_low_bits(left - 96)};
+                    tc_clear_rows<NC>(ring + st * Cfg::kTileBytes, w, lane);
+                    tc_fence_async();
+                    __syncwarp();
+                    if (lane == 0) tc_bar_arrive(tc_smem(&sy.cleared[st]));
+                }
+                g0 += sg.n;
+                return true;
+            });
+        }
+        __syncwarp();
+        ok = !*abort;
+    } else if constexpr (CODES) {
+        tc_regs_down<Cfg::kConvert>();
+        // ---- codes to f16 operands: row `row` of each tile ----
+        const int cw = warp - NQ * 4 - 4, row = cw * 32 + lane;
+        int g0 = 0, r0 = 0;
+        cache_segments(a, [&](const CacheSegment& sg) {
+            const CacheUnit& u = sg.u;
+            auto page_of = [&](int i) {  // of this row at tile sg.first + i
+                const int token = (sg.first + i) * kTcRows + row;
+                return i < sg.n && sg.first + i < u.cache_tiles && token < u.length ? cache_page(a.c, u.b, token) : -1;
+            };
+            auto bytes_of = [&](int i, int page) {  // its bytes; bit 16: there is such a row
+                if (page < 0) return 0u;
+                const int place = ((sg.first + i) * kTcRows + row) & (a.c.page - 1);
+                return 0x10000u | a.c.ks[page * a.c.ks_sp + place * a.c.ks_st + u.n * a.c.ks_sh] |
+                       ((uint32_t)a.c.vs[page * a.c.vs_sp + place * a.c.vs_st + u.n * a.c.vs_sh] << 8);
+            };
+            uint32_t bytes = bytes_of(0, page_of(0));
+            int page = page_of(1);  // of the tile behind
+#pragma unroll 1
+            for (int i = 0; i < sg.n; ++i) {
+                const int gi = g0 + i, tile = sg.first + i;
+                const bool tail = tile >= u.cache_tiles;
+                const int j = (tile - u.cache_tiles) * kTcRows + row;  // new token (tail)
+                const uint32_t now = bytes;
+                bytes = bytes_of(i + 1, page);
+                page = page_of(i + 2);
+                bool there;
+                uint32_t kb, vb;  // of a new token's row: the byte that brings its largest value to 2^8 or more
+                if (!tail) {
+                    there = now >> 16, kb = now & 255u, vb = (now >> 8) & 255u;
+                } else {
+                    there = j < sg.tail_keys;
+                    kb = vb = 0;
+                    if (there) {
+                        const T* p[2] = {static_cast<const T*>(a.nk) + u.b * a.nk_sb + j * a.nk_st + u.n * a.nk_sh,
+                                         static_cast<const T*>(a.nv) + u.b * a.nv_sb + j * a.nv_st + u.n * a.nv_sh};
+#pragma unroll
+                        for (int kv = 0; kv < 2; ++kv) {
+                            uint32_t top = 0;
+                            for (int d = 0; d < a.D; d += 8) {
+                                const uint4 x = *reinterpret_cast<const uint4*>(p[kv] + d);
+                                const uint32_t mm = 0x7fff7fffu;
+                                top = __vmaxu2(top, __vmaxu2(__vmaxu2(x.x & mm, x.y & mm), __vmaxu2(x.z & mm, x.w & mm)));
+                            }
+                            top = max(top & 0xffffu, top >> 16);
+                            const float x = BF16 ? __uint_as_float(top << 16) : __half2float(__ushort_as_half((unsigned short)top));
+                            const int e = (int)(__float_as_uint(x) >> 23);
+                            const uint32_t byte = e == 255 ? 255u : (uint32_t)max(e - 8, 27);
+                            if (kv) vb = byte;
+                            else kb = byte;
+                        }
+                    }
+                }
+                // the tile's largest scales
+                const uint32_t kt = __reduce_max_sync(0xffffffffu, there && kb != 255u ? kb : 0u);
+                const uint32_t vt = __reduce_max_sync(0xffffffffu, there && vb != 255u ? vb : 0u);
+                if (lane == 0) {
+                    sy.tops[gi & 1][cw] = kt | (vt << 8);
+                    tc_bar_arrive(tc_smem(&sy.tops_full));
+                }
+                if (!tc_bar_wait(tc_smem(&sy.tops_full), gi & 1, abort, err)) return false;
+                uint32_t k_top = 0, v_top = 0;
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                    const uint32_t y = sy.tops[gi & 1][x];
+                    k_top = max(k_top, y & 255u), v_top = max(v_top, y >> 8);
+                }
+                if (row == 0) sy.k_scale[gi & 7] = cache_scale(k_top), sy.v_top[gi & 7] = v_top;
+#pragma unroll
+                for (int kv = 0; kv < 2; ++kv) {
+                    const int idx = 2 * gi + kv, st = idx % ST;
+                    const uint32_t byte = kv ? vb : kb, most = kv ? v_top : k_top;
+                    unsigned char* to = ring + st * Cfg::kTileBytes + row * 128;
+                    if (!tail) {
+                        const int ri = 2 * r0 + kv, rs = ri % Cfg::kRaw;
+                        if (!tc_bar_wait(tc_smem(&sy.raw_full[rs]), (ri / Cfg::kRaw) & 1, abort, err)) return false;
+                        if (idx >= ST && !tc_bar_wait(tc_smem(&sy.empty[st]), (idx / ST - 1) & 1, abort, err)) return false;
+                        const unsigned char* from = raw + rs * Cfg::kRawBytes + row * (NC * 64);
+                        // 2^(byte - most) in f16; a row that held no numbers: NaN; none or byte 0: zeros
+                        const float f = byte == 255u ? __uint_as_float(0x7fffffffu) : byte == 0u || byte + 126u < most ? 0.f : cache_scale(127u + byte - most);
+                        const __half2 scale = __half2half2(__float2half_rn(f));
+                        const __half2 off = __hmul2(scale, __half2half2(__ushort_as_half(0xe480)));  // -1152
+#pragma unroll 2
+                        for (int c = 0; c < NC * 4; ++c) {  // 16 codes
+                            uint32_t p[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+                            if (there && c * 16 < a.D) {
+                                const uint4 x = *reinterpret_cast<const uint4*>(from + ((NC == 2 ? c ^ (row & 7) : c ^ ((row >> 1) & 3)) << 4));
+                                const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+                                for (int k = 0; k < 4; ++k) {
+                                    if constexpr (F == kCacheE4m3) {
+                                        uint32_t lo, hi;
+                                        cache_four_f16<F>(w[k], lo, hi);
+                                        const __half2 y0 = __hmul2(*reinterpret_cast<const __half2*>(&lo), scale), y1 = __hmul2(*reinterpret_cast<const __half2*>(&hi), scale);
+                                        p[2 * k] = *reinterpret_cast<const uint32_t*>(&y0), p[2 * k + 1] = *reinterpret_cast<const uint32_t*>(&y1);
+                                    } else {  // (1024 + u) s - 1152 s, exact
+                                        const uint32_t v = w[k] ^ 0x80808080u, lo = __byte_perm(v, 0x64646464u, 0x4140), hi = __byte_perm(v, 0x64646464u, 0x4342);
+                                        const __half2 y0 = __hfma2(*reinterpret_cast<const __half2*>(&lo), scale, off), y1 = __hfma2(*reinterpret_cast<const __half2*>(&hi), scale, off);
+                                        p[2 * k] = *reinterpret_cast<const uint32_t*>(&y0), p[2 * k + 1] = *reinterpret_cast<const uint32_t*>(&y1);
+                                    }
+                                }
+                            }
+                            unsigned char* at = to + (c / 4) * kTcTile;
+                            const int ch = (c & 3) * 2;
+                            *reinterpret_cast<uint4*>(at + ((ch ^ (row & 7)) << 4)) = make_uint4(p[0], p[1], p[2], p[3]);
+                            *reinterpret_cast<uint4*>(at + (((ch + 1) ^ (row & 7)) << 4)) = make_uint4(p[4], p[5], p[6], p[7]);
+                        }
+                        tc_fence_async();
+                        __syncwarp();
+                        if (lane == 0) {
+                            tc_bar_arrive(tc_smem(&sy.raw_empty[rs]));
+                            tc_bar_arrive(tc_smem(&sy.full[st]));
+                        }
+                    } else {
+                        if (idx >= ST && !tc_bar_wait(tc_smem(&sy.empty[st]), (idx / ST - 1) & 1, abort, err)) return false;
+                        const T* p = kv ? static_cast<const T*>(a.nv) + u.b * a.nv_sb + j * a.nv_st + u.n * a.nv_sh
+                                        : static_cast<const T*>(a.nk) + u.b * a.nk_sb + j * a.nk_st + u.n * a.nk_sh;
+                        const float f = most == 0u ? 0.f : cache_scale(254u - most);
+#pragma unroll 1
+                        for (int d = 0; d < NC * 64; d += 8) {
+                            uint4 y = make_uint4(0, 0, 0, 0);
+                            if (there && d < a.D) {
+                                const uint4 x = *reinterpret_cast<const uint4*>(p + d);
+                                const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+                                uint32_t z[4];
+#pragma unroll
+                                for (int k = 0; k < 4; ++k) {
+                                    float2 v;
+                                    if constexpr (BF16) v = make_float2(__uint_as_float(w[k] << 16), __uint_as_float(w[k] & 0xffff0000u));
+                                    else v = __half22float2(*reinterpret_cast<const __half2*>(&w[k]));
+                                    z[k] = tc_pack<false>(v.x * f, v.y * f);
+                                }
+                                y = make_uint4(z[0], z[1], z[2], z[3]);
+                            }
+                            *reinterpret_cast<uint4*>(to + (d / 64) * kTcTile + ((((d / 8) & 7) ^ (row & 7)) << 4)) = y;
+                        }
+                        tc_fence_async();
+                        __syncwarp();
+                        if (lane == 0) tc_bar_arrive(tc_smem(&sy.full[st]));
+                    }
+                }
+                if (!tail) ++r0;
+            }
+            g0 += sg.n;
+            return true;
+        });
+        __syncwarp();
+        ok = !*abort;
+    }
+    if (!ok) tc_drain();
+    tc_fence_before();
+    __syncthreads();
+    if (warp == NQ * 4 + 1) tmem_dealloc(tmem, Cfg::kCols);
+}
+
+// ---- host ----
+
+namespace {
+
+using EncodeTiled = PFN_cuTensorMapEncodeTiled_v12000;
+
+// Four dimensions (channel, head, row, outer) of `es` bytes an element; boxes of 64 channels (codes: all) x 1 x box_rows x 1.
+bool map4(const void* base, int es, bool bf16, int64_t D, int inner, int64_t heads, int64_t rows, int64_t outer, int64_t sh, int64_t sr, int64_t so,
+          int box_rows, CUtensorMap* map) {
+    EncodeTiled f = reinterpret_cast<EncodeTiled>(tensor_map_encoder());
+    if (!f) return false;
+    auto bytes = [es](int64_t n, int64_t stride) { return (cuuint64_t)(n > 1 ? stride * es : 16); };
+    const cuuint64_t dims[4] = {(cuuint64_t)D, (cuuint64_t)heads, (cuuint64_t)rows, (cuuint64_t)outer};
+    const cuuint64_t strides[3] = {bytes(heads, sh), bytes(rows, sr), bytes(outer, so)};
+    const cuuint32_t box[4] = {(cuuint32_t)inner, 1u, (cuuint32_t)box_rows, 1u};
+    const cuuint32_t one[4] = {1u, 1u, 1u, 1u};
+    return f(map, es == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4,
+             const_cast<void*>(base), dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             inner * es == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+// Queries [B, T, heads, D] as (channel, head of the group, token, key head, sequence); boxes of 64 channels x G heads x `tokens`.
+bool map_queries(const CacheArgs& a, bool bf16, int tokens, CUtensorMap* map) {
+    EncodeTiled f = reinterpret_cast<EncodeTiled>(tensor_map_encoder());
+    if (!f) return false;
+    auto bytes = [](int64_t n, int64_t stride) { return (cuuint64_t)(n > 1 ? stride * 2 : 16); };
+    const cuuint64_t dims[5] = {(cuuint64_t)a.D, (cuuint64_t)a.G, (cuuint64_t)a.T, (cuuint64_t)a.N, (cuuint64_t)a.B};
+    const cuuint64_t strides[4] = {bytes(a.G, a.q_sh), bytes(a.T, a.q_st), bytes(a.N, a.G * a.q_sh), bytes(a.B, a.q_sb)};
+    const cuuint32_t box[5] = {64u, (cuuint32_t)a.G, (cuuint32_t)tokens, 1u, 1u};
+    const cuuint32_t one[5] = {1u, 1u, 1u, 1u, 1u};
+    return f(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 5, const_cast<void*>(a.q), dims, strides, box, one,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <bool BF16, int F, int NQ, int NC>
+cudaError_t tc_go(const CacheArgs& a, int grid, cudaStream_t st) {
+    using Cfg = CacheTcCfg<F, NQ, NC>;
+    const int qpt = a.tile_rows / (NQ * a.G), box_rows = a.c.page < kTcRows ? a.c.page : kTcRows;
+    const int es = F == kCacheSame ? 2 : 1, inner = F == kCacheSame ? 64 : NC * 64;
+    CUtensorMap mq, mk, mv, mnk, mnv;
+    const bool fresh = F == kCacheSame && a.nk;
+    // an empty cache: no tile of it is read
+    const bool cache = a.c.pages > 0 && a.c.longest > 0;
+    if (!map_queries(a, BF16, qpt, &mq) ||
+        (cache && (!map4(a.c.k, es, BF16, a.D, inner, a.N, a.c.page, a.c.pages, a.c.k_sh, a.c.k_st, a.c.k_sp, box_rows, &mk) ||
+                   !map4(a.c.v, es, BF16, a.D, inner, a.N, a.c.page, a.c.pages, a.c.v_sh, a.c.v_st, a.c.v_sp, box_rows, &mv))) ||
+        (fresh && (!map4(a.nk, 2, BF16, a.D, 64, a.N, a.T, a.B, a.nk_sh, a.nk_st, a.nk_sb, kTcRows, &mnk) ||
+                   !map4(a.nv, 2, BF16, a.D, 64, a.N, a.T, a.B, a.nv_sh, a.nv_st, a.nv_sb, kTcRows, &mnv))))
+        return cudaErrorInvalidValue;
+    if (!cache) mk = mv = mq;
+    if (!fresh) mnk = mnv = mq;
+    static SmemSeen seen;
+    cudaError_t e = allow_smem(reinterpret_cast<const void*>(&msda_cache_tc_kernel<BF16, F, NQ, NC>), Cfg::kSmem, seen);
+    if (e != cudaSuccess) return e;
+    msda_cache_tc_kernel<BF16, F, NQ, NC><<<grid, Cfg::kThreads, Cfg::kSmem, st>>>(a, box_rows, mq, mk, mv, mnk, mnv);
+    return cudaGetLastError();
+}
+}  // namespace
+
+template <bool BF16, int F>
+cudaError_t launch_cache_tc(const CacheArgs& a, int nq, int grid, cudaStream_t st) {
+    if (a.D > 64) return nq == 2 ? tc_go<BF16, F, 2, 2>(a, grid, st) : tc_go<BF16, F, 1, 2>(a, grid, st);
+    return nq == 2 ? tc_go<BF16, F, 2, 1>(a, grid, st) : tc_go<BF16, F, 1, 1>(a, grid, st);
+}
+
+}  // namespace msda

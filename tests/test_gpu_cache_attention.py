@@ -91,6 +91,21 @@ def test_sizes(msda, size, new, fmt, dtype):  # noqa: F811
         compare(msda, q, cache, table, lengths, key, value, mask=mask, counts=counts)
 
 
+MANY = [  # more rows a key head: heads that do not divide a tile of 128, one row more than a tile, several tiles
+    (1, 33, 300, 1, 1, 16, 16), (2, 11, 1000, 12, 4, 80, 32), (1, 43, 700, 6, 2, 64, 64), (1, 300, 513, 2, 1, 128, 128),
+    (3, 20, 2500, 16, 1, 48, 16), (1, 2, 900, 64, 1, 64, 16), (1, 1, 900, 100, 1, 128, 64), (1, 1, 600, 130, 1, 32, 16),
+    (2, 64, 5000, 8, 2, 128, 256), (9, 40, 200, 8, 8, 32, 32), (1, 129, 129, 4, 4, 112, 1024), (2, 260, 0, 2, 2, 64, 16),
+]
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("new", ["none", "chain", "tree", "ragged"])
+@pytest.mark.parametrize("size", MANY, ids=lambda s: "x".join(map(str, s)))
+def test_many_rows(msda, size, new, fmt, dtype):  # noqa: F811
+    test_sizes(msda, size, new, fmt, dtype)
+
+
 @pytest.mark.parametrize("fmt", FORMATS)
 @pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
 @pytest.mark.parametrize("T", [3, 60])
