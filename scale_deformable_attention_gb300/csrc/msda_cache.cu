@@ -661,7 +661,8 @@ msda_status msda_cache_attention(msda_dtype dt, int format, const msda_cache_pro
     a.mk_sb = p->mask_stride[0], a.mk_sq = p->mask_stride[1];
     a.B = (int)p->B, a.T = (int)p->T, a.M = (int)p->M, a.N = (int)p->N, a.D = (int)p->D, a.G = (int)(p->M / p->N);
     a.rows = (int)plan.rows, a.row_tiles = (int)plan.row_tiles, a.tile_rows = plan.shape.tile_rows;
-    a.tile_keys = plan.shape.tile_keys, a.tail_keys = plan.shape.tail_keys;
+    while ((1 << a.tile_log2) < plan.shape.tile_keys) ++a.tile_log2;
+    while ((1 << a.tail_log2) < plan.shape.tail_keys) ++a.tail_log2;
     a.c2 = (float)(scale * (double)msda::kLog2e);
     a.out = out, a.lse = lse;
     a.part_o = static_cast<float*>(workspace);  // null where no unit is shared

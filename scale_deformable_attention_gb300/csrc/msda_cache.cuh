@@ -38,7 +38,7 @@ struct CacheArgs {
     long long mk_sb, mk_sq;
     int B, T, M, N, D, G;                             // G = M / N query heads share a key head
     int rows, row_tiles, tile_rows;                   // T * G rows a key head, cut into tiles of tile_rows
-    int tile_keys, tail_keys;                         // keys a tile of work: of the cache, of the new tokens
+    int tile_log2, tail_log2;                         // keys a tile of work: 2^tile_log2 of the cache, 2^tail_log2 of the new tokens
     float c2;                                         // scale * log2(e)
     void* out;                                        // [B, T, M, D]
     float* lse;                                       // [B, M, T]
@@ -60,13 +60,16 @@ __device__ __forceinline__ int cache_count(const CachePages& c, const int* count
     atomicOr(c.err, kCacheBad);
     return n < 0 ? 0 : T;
 }
-// page number of a sequence's token, -1 (and the error bit) where the table holds none
-__device__ __forceinline__ int cache_page(const CachePages& c, int b, int token) {
-    const int p = c.table[b * c.table_sb + (token >> c.page_log2)];
-    if ((unsigned)p < (unsigned)c.pages) return p;
-    atomicOr(c.err, kCacheBad);
+// The table's entry for a sequence's token, as it stands there: read ahead of its use, so that nothing waits for it.
+constexpr int kCacheNoPage = -0x7fffffff;  // what a caller puts where there is no token; an entry of this value is no page either
+__device__ __forceinline__ int cache_entry(const CachePages& c, int b, int token) { return c.table[b * c.table_sb + (token >> c.page_log2)]; }
+// The page of an entry, -1 (and the error bit) where it is none.
+__device__ __forceinline__ int cache_page_of(const CachePages& c, int entry) {
+    if ((unsigned)entry < (unsigned)c.pages) return entry;
+    if (entry != kCacheNoPage) atomicOr(c.err, kCacheBad);
     return -1;
 }
+__device__ __forceinline__ int cache_page(const CachePages& c, int b, int token) { return cache_page_of(c, cache_entry(c, b, token)); }
 
 // ---- the plan ----
 // A unit is a tile of rows of one key head of one sequence; its work are the
@@ -75,123 +78,127 @@ __device__ __forceinline__ int cache_page(const CachePages& c, int b, int token)
 // which the blocks share out evenly: a block may end one unit and begin another,
 // so the lengths of the sequences need no balance, and a unit that several blocks
 // share is joined from their parts.  Any block finds its share from the lengths
-// alone, which every warp adds up by itself.
+// alone.
 struct CacheUnit {
     int b, n, rt;
     int length, count;   // of sequence b
     int cache_tiles, tiles;
 };
 
+// new tokens that a row tile sees at most
 __device__ __forceinline__ int cache_tail_keys(const CacheArgs& a, int rt, int count) {
     if (!a.nk) return 0;
-    const int first = rt * a.tile_rows / a.G;
-    if (first >= count) return 0;
-    if (a.mask) return count;
-    return min(count, (min(a.rows, (rt + 1) * a.tile_rows) - 1) / a.G + 1);
+    if (rt > 0 && rt * a.tile_rows / a.G >= count) return 0;
+    if (a.mask || rt == a.row_tiles - 1) return count;
+    return min(count, ((rt + 1) * a.tile_rows - 1) / a.G + 1);
 }
 __device__ __forceinline__ void cache_unit_tiles(const CacheArgs& a, CacheUnit& u) {
-    const bool any = u.rt * a.tile_rows / a.G < u.count;
-    u.cache_tiles = any ? (u.length + a.tile_keys - 1) / a.tile_keys : 0;
-    u.tiles = max(1, u.cache_tiles + (cache_tail_keys(a, u.rt, u.count) + a.tail_keys - 1) / a.tail_keys);
+    const bool any = u.rt == 0 ? u.count > 0 : u.rt * a.tile_rows / a.G < u.count;
+    u.cache_tiles = any ? (u.length + (1 << a.tile_log2) - 1) >> a.tile_log2 : 0;
+    u.tiles = max(1, u.cache_tiles + ((cache_tail_keys(a, u.rt, u.count) + (1 << a.tail_log2) - 1) >> a.tail_log2));
 }
 // tiles of all row tiles of one key head of sequence b
 __device__ __forceinline__ int cache_head_tiles(const CacheArgs& a, int b) {
     CacheUnit u;
-    u.b = b, u.n = 0;
     u.length = cache_length(a.c, a.lengths, b), u.count = cache_count(a.c, a.counts, b, a.T);
     int sum = 0;
+#pragma unroll 1
     for (u.rt = 0; u.rt < a.row_tiles; ++u.rt) {
         cache_unit_tiles(a, u);
         sum += u.tiles;
     }
     return sum;
 }
-__device__ __forceinline__ void cache_unit_at(const CacheArgs& a, int b, int n, int rt, CacheUnit& u) {
-    u.b = b, u.n = n, u.rt = rt;
-    u.length = cache_length(a.c, a.lengths, b), u.count = cache_count(a.c, a.counts, b, a.T);
-    cache_unit_tiles(a, u);
-}
 __device__ __forceinline__ void cache_next_unit(const CacheArgs& a, CacheUnit& u) {
     if (++u.rt == a.row_tiles) {
         u.rt = 0;
         if (++u.n == a.N) {
             u.n = 0, ++u.b;
-            if (u.b >= a.B) return;
             u.length = cache_length(a.c, a.lengths, u.b), u.count = cache_count(a.c, a.counts, u.b, a.T);
         }
     }
     cache_unit_tiles(a, u);
 }
 
-// Whole warp.  Tiles of all sequences.
-__device__ __forceinline__ int cache_all_tiles(const CacheArgs& a) {
-    const int lane = threadIdx.x & 31;
-    int sum = 0;
-    for (int i = lane; i < a.B; i += 32) sum += cache_head_tiles(a, i) * a.N;
-    return __reduce_add_sync(0xffffffffu, sum);
-}
-__device__ __forceinline__ int cache_share(const CacheArgs& a, int all) { return max((all + a.blocks - 1) / a.blocks, a.least); }
+// Where a block begins: its first unit, the tile within it, its tiles in all and those of each block.  One warp works it out for
+// its block (code that runs once costs about 9 cycles an instruction to fetch, and each role of a block would have its own).
+struct CacheStart {
+    CacheUnit u;
+    int tile, left, share;
+};
 
-// Whole warp.  The unit and the tile within it at place x of the line.
-__device__ __forceinline__ void cache_find(const CacheArgs& a, int x, CacheUnit& u, int* tile) {
+// Whole warp, all lanes with the same result.
+__device__ __forceinline__ CacheStart cache_start(const CacheArgs& a) {
     const int lane = threadIdx.x & 31;
-    int b = 0, head = 1;
-    for (int b0 = 0; b0 < a.B; b0 += 32) {
-        const int mine = b0 + lane < a.B ? cache_head_tiles(a, b0 + lane) : 0;
-        int upto = mine * a.N;
+    CacheStart s;
+    s.tile = s.left = s.share = 0;
+    int rt = 0;
+    if (a.whole) {
+        const int id = blockIdx.x / a.row_tiles;
+        rt = blockIdx.x - id * a.row_tiles;
+        s.u.b = id / a.N, s.u.n = id - s.u.b * a.N;
+    } else {
+        int all = 0;
+#pragma unroll 1
+        for (int i = lane; i < a.B; i += 32) all += cache_head_tiles(a, i) * a.N;
+        all = __reduce_add_sync(0xffffffffu, all);
+        s.share = max((all + a.blocks - 1) / a.blocks, a.least);
+        const long long at = (long long)blockIdx.x * s.share;
+        if (at >= all) return s;
+        int x = (int)at, head = 1;
+        s.left = min(s.share, all - x);
+        s.u.b = 0;
+#pragma unroll 1
+        for (int b0 = 0; b0 < a.B; b0 += 32) {
+            const int mine = b0 + lane < a.B ? cache_head_tiles(a, b0 + lane) : 0;
+            int upto = mine * a.N;
 #pragma unroll
-        for (int w = 1; w < 32; w <<= 1) {
-            const int o = __shfl_up_sync(0xffffffffu, upto, w);
-            if (lane >= w) upto += o;
+            for (int w = 1; w < 32; w <<= 1) {
+                const int o = __shfl_up_sync(0xffffffffu, upto, w);
+                if (lane >= w) upto += o;
+            }
+            const unsigned behind = __ballot_sync(0xffffffffu, upto > x);
+            if (behind) {
+                const int l = __ffs(behind) - 1;
+                s.u.b = b0 + l;
+                head = __shfl_sync(0xffffffffu, mine, l);
+                x -= __shfl_sync(0xffffffffu, upto, l) - head * a.N;
+                break;
+            }
+            x -= __shfl_sync(0xffffffffu, upto, 31);
         }
-        const unsigned behind = __ballot_sync(0xffffffffu, upto > x);
-        if (behind) {
-            const int l = __ffs(behind) - 1;
-            b = b0 + l;
-            head = __shfl_sync(0xffffffffu, mine, l);
-            x -= __shfl_sync(0xffffffffu, upto, l) - head * a.N;
-            break;
+        s.u.n = x / head;
+        s.tile = x - s.u.n * head;
+    }
+    s.u.rt = rt;
+    s.u.length = cache_length(a.c, a.lengths, s.u.b), s.u.count = cache_count(a.c, a.counts, s.u.b, a.T);
+    cache_unit_tiles(a, s.u);
+    if (a.whole) {
+        s.left = s.share = s.u.tiles;
+    } else {
+#pragma unroll 1
+        while (s.tile >= s.u.tiles) {
+            s.tile -= s.u.tiles;
+            ++s.u.rt;
+            cache_unit_tiles(a, s.u);
         }
-        x -= __shfl_sync(0xffffffffu, upto, 31);
     }
-    const int n = x / head;
-    x -= n * head;
-    cache_unit_at(a, b, n, 0, u);
-    while (x >= u.tiles) {
-        x -= u.tiles;
-        ++u.rt;
-        cache_unit_tiles(a, u);
-    }
-    *tile = x;
+    return s;
 }
 
 // The share of a block: calls f(unit, first tile, tiles, slot) for each unit that it has tiles of; `slot`: where the part
-// goes, -1 where the block has the whole unit.
+// goes, -1 where the block has the whole unit.  `note`: this thread writes down where the parts of a unit are.
 template <typename F>
-__device__ __forceinline__ void cache_walk(const CacheArgs& a, F f) {
-    CacheUnit u;
-    if (a.whole) {
-        int id = blockIdx.x;
-        const int rt = id % a.row_tiles;
-        id /= a.row_tiles;
-        cache_unit_at(a, id / a.N, id % a.N, rt, u);
-        f(u, 0, u.tiles, -1);
-        return;
-    }
-    const int all = cache_all_tiles(a), share = cache_share(a, all);
-    const long long at = (long long)blockIdx.x * share;
-    if (at >= all) return;
-    const int x0 = (int)at;
-    int left = min(share, all - x0);
-    int tile;
-    cache_find(a, x0, u, &tile);
+__device__ __forceinline__ void cache_walk(const CacheArgs& a, const CacheStart& s, bool note, F f) {
+    CacheUnit u = s.u;
+    int left = s.left, tile = s.tile;
     bool first = true;
+#pragma unroll 1
     while (left > 0) {
-        const int n = min(u.tiles - tile, left);
-        if (tile == 0 && threadIdx.x == 0)  // its first block says where its parts are
-            a.units[(u.b * a.N + u.n) * a.row_tiles + u.rt] =
-                make_int2(n == u.tiles ? -1 : 2 * (int)blockIdx.x + (first ? 0 : 1), 1 + (u.tiles - n + share - 1) / share);
-        f(u, tile, n, n == u.tiles ? -1 : 2 * (int)blockIdx.x + (first ? 0 : 1));
+        const int n = min(u.tiles - tile, left), slot = n == u.tiles ? -1 : 2 * (int)blockIdx.x + (first ? 0 : 1);
+        if (note && tile == 0 && !a.whole)  // its first block says where its parts are
+            a.units[(u.b * a.N + u.n) * a.row_tiles + u.rt] = make_int2(slot, 1 + (u.tiles - n + s.share - 1) / s.share);
+        f(u, tile, n, slot);
         left -= n, tile = 0, first = false;
         if (left > 0) cache_next_unit(a, u);
     }

@@ -67,7 +67,7 @@ struct CacheProduct {
     static constexpr int qp = !f32 ? 1 : F == kCacheSame ? 3 : 2, kp = f32 && F == kCacheSame ? 3 : 1, pp = qp;
     static constexpr float below = bf16 ? 0.f : 6.f;  // m below the maximum, in binary places
 };
-constexpr float kCacheAbove = 14.f;  // how far a score may pass m
+constexpr float kCacheMost = 16384.f;  // what a lane's probabilities of a row may add up to in a step before m follows
 
 template <typename T, int F, int DP, int MT>
 struct CacheRowsCfg {
@@ -159,88 +159,81 @@ struct CacheState {
     float m[MT][2], l[MT][2];
     uint32_t top;  // 8 bits: O is in units of the scale of this byte (the largest met)
 };
+constexpr float kCacheNone = -1e30f;  // m before any score
 
-// One walk over steps of KS keys: over the cache in format F, or (TAIL) over the new tokens in the queries' type.  E, EV: which
-// channels a lane has, those of the cache's format in both.
-template <typename T, int F, int DP, int MT, int E, int EV, int KS, int STAGES, bool TAIL>
+// One walk over steps of KS keys: `cached` ones over the cache in format F, then `fresh` ones over the new tokens in the queries'
+// type (one of the two is 0 where F is a format of codes).  E, EV: which channels a lane has, those of the cache's format in both.
+template <typename T, int F, int DP, int MT, int E, int EV, int KS, int STAGES>
 struct CacheWalk {
     using P = CacheProduct<T, F>;
     static constexpr int RB = DP * P::es, CH = RB / 16, EC = 16 / P::es, NT = KS / 8, GR = KS / 16, SETS = DP / (8 * EV);
     static constexpr int kStage = 2 * KS * RB;
+    static constexpr bool kCodes = F != kCacheSame;
 
     const CacheArgs& a;
     const CacheUnit& u;
     unsigned char* ring;
     const uint4* qf;      // fragments [piece][MT][DP / 16][32]
-    const float* factor;  // [MT * 16]: what scores of a row are multiplied by
-    int lane, warp, first, steps, step_keys;  // this warp's steps begin at keys first, first + step_keys, ...
-    // pages of this warp's groups of 16 keys, 32 of them at a time in the lanes, and the next 32
+    const float* factor;  // codes: [MT * 16], what scores of a row are multiplied by
+    const int* token_of;  // [MT * 16]: a row's new token
+    int lane, first, cached, first_new, fresh, step_keys;  // this warp's steps begin at keys first, first + step_keys, ...
+    // pages of this warp's groups of 16 keys, 32 of them at a time in the lanes, and entries of the next 32
     int here, next, have;
 
-    __device__ __forceinline__ int group_page(int gi) const {
+    __device__ __forceinline__ int group_entry(int gi) const {
         const int token = first + (gi / GR) * step_keys + (gi % GR) * 16;
-        return gi < steps * GR && token < u.length ? cache_page(a.c, u.b, token) : -1;
-    }
-    __device__ __forceinline__ void begin() {
-        if constexpr (!TAIL) {
-            have = 0;
-            here = group_page(lane);
-            next = group_page(32 + lane);
-        }
-    }
-    // page of group gi: asked for in ascending order
-    __device__ __forceinline__ int page_of(int gi) {
-        if (gi >= have + 32) {
-            have += 32;
-            here = next;
-            next = group_page(have + 32 + lane);
-        }
-        return __shfl_sync(0xffffffffu, here, gi & 31);
+        return gi < cached * GR && token < u.length ? cache_entry(a.c, u.b, token) : kCacheNoPage;
     }
 
     // Starts the copies of step i, and reads the bytes of its scales (lane: key); which groups of 16 keys are there.
     __device__ __forceinline__ void issue(int i, uint32_t& bytes, uint32_t& there) {
-        bytes = 0, there = 0;
         const uint32_t dst = cache_smem(ring) + (uint32_t)(i % STAGES) * kStage;
-        const int key0 = first + i * step_keys;
-        if constexpr (TAIL) {
-            const T* k = static_cast<const T*>(a.nk) + u.b * a.nk_sb + u.n * a.nk_sh;
-            const T* v = static_cast<const T*>(a.nv) + u.b * a.nv_sb + u.n * a.nv_sh;
-#pragma unroll
-            for (int x = lane; x < KS * CH; x += 32) {
-                const int row = x / CH, chunk = x % CH, j = key0 + row;
-                const bool in = j < u.count && chunk * EC < a.D;
-                const uint32_t at = dst + cache_chunk<RB>(row, chunk);
-                cache_copy16(at, in ? k + j * a.nk_st + chunk * EC : k, in ? 16 : 0);
-                cache_copy16(at + KS * RB, in ? v + j * a.nv_st + chunk * EC : v, in ? 16 : 0);
-            }
-            there = ~0u;
-        } else {
-            const char* kb = static_cast<const char*>(a.c.k) + (u.n * a.c.k_sh) * P::es;
-            const char* vb = static_cast<const char*>(a.c.v) + (u.n * a.c.v_sh) * P::es;
-#pragma unroll
-            for (int g = 0; g < GR; ++g) {
-                const int page = page_of(i * GR + g), token = key0 + g * 16, left = u.length - token;
-                if (page >= 0) there |= 1u << g;
-                const long long p = page < 0 ? 0 : page;
-                const int in_page = page < 0 ? 0 : token & (a.c.page - 1);
-                const char* k = kb + (p * a.c.k_sp + in_page * a.c.k_st) * P::es;
-                const char* v = vb + (p * a.c.v_sp + in_page * a.c.v_st) * P::es;
-#pragma unroll
-                for (int x = lane; x < 16 * CH; x += 32) {
-                    const int row = x / CH, chunk = x % CH;
-                    const bool in = page >= 0 && row < left && chunk * EC < a.D;
-                    const uint32_t at = dst + cache_chunk<RB>(g * 16 + row, chunk);
-                    cache_copy16(at, in ? k + row * a.c.k_st * P::es + chunk * 16 : k, in ? 16 : 0);
-                    cache_copy16(at + KS * RB, in ? v + row * a.c.v_st * P::es + chunk * 16 : v, in ? 16 : 0);
+        const int row0 = lane / CH, chunk = lane % CH;  // a row takes CH lanes, or each lane CH / 32 chunks of it
+#pragma unroll 1
+        for (int g = 0; g < GR; ++g) {
+            const char *k, *v;
+            long long kst, vst;
+            int left;
+            if (i < cached) {
+                const int gi = i * GR + g, token = first + i * step_keys + g * 16;
+                if (gi >= have + 32) {  // asked for in ascending order
+                    have += 32;
+                    here = cache_page_of(a.c, next);
+                    next = group_entry(have + 32 + lane);
                 }
-                if constexpr (F != kCacheSame) {
+                const int page = __shfl_sync(0xffffffffu, here, gi & 31);
+                const long long p = max(page, 0);
+                const int in_page = token & (a.c.page - 1);
+                left = page < 0 ? 0 : u.length - token;
+                if (page >= 0) there |= 1u << g;
+                k = static_cast<const char*>(a.c.k) + (p * a.c.k_sp + in_page * a.c.k_st + u.n * a.c.k_sh) * P::es;
+                v = static_cast<const char*>(a.c.v) + (p * a.c.v_sp + in_page * a.c.v_st + u.n * a.c.v_sh) * P::es;
+                kst = a.c.k_st * P::es, vst = a.c.v_st * P::es;
+                if constexpr (kCodes) {
                     const int row = lane - g * 16;
-                    if (page >= 0 && row >= 0 && row < 16 && row < left) {
+                    if ((unsigned)row < 16u && row < left) {
                         bytes = a.c.ks[p * a.c.ks_sp + (in_page + row) * a.c.ks_st + u.n * a.c.ks_sh];
                         bytes |= (uint32_t)a.c.vs[p * a.c.vs_sp + (in_page + row) * a.c.vs_st + u.n * a.c.vs_sh] << 8;
                     }
                 }
+            } else {
+                const int j = first_new + (i - cached) * step_keys + g * 16;
+                left = u.count - j;
+                const long long at = left > 0 ? j : 0;
+                k = reinterpret_cast<const char*>(static_cast<const T*>(a.nk) + u.b * a.nk_sb + at * a.nk_st + u.n * a.nk_sh);
+                v = reinterpret_cast<const char*>(static_cast<const T*>(a.nv) + u.b * a.nv_sb + at * a.nv_st + u.n * a.nv_sh);
+                kst = a.nk_st * P::es, vst = a.nv_st * P::es;
+            }
+            const char *k0 = k + row0 * kst, *v0 = v + row0 * vst;
+#pragma unroll
+            for (int x = 0; x < 16 * CH / 32; ++x) {
+                constexpr int STEP = CH < 32 ? 32 / CH : 1;
+                const int row = row0 + x * STEP;
+                const bool in = row < left && chunk * EC < a.D;
+                const uint32_t at = dst + cache_chunk<RB>(g * 16 + row, chunk);
+                cache_copy16(at, in ? k0 + chunk * 16 : k, in ? 16 : 0);
+                cache_copy16(at + KS * RB, in ? v0 + chunk * 16 : v, in ? 16 : 0);
+                k0 += STEP * kst, v0 += STEP * vst;
             }
         }
     }
@@ -397,11 +390,11 @@ struct CacheWalk {
     __device__ __forceinline__ void compute(int i, uint32_t bytes, uint32_t there, CacheState<DP, MT>& z) {
         const unsigned char* k = ring + (i % STAGES) * kStage;
         const unsigned char* v = k + KS * RB;
-        const int g = lane >> 2, c = lane & 3, key0 = first + i * step_keys;
+        const int g = lane >> 2, c = lane & 3;
         float s[MT][NT][4];
         scores(k, s);
-        float ks[NT][2], vs[NT][2];  // scales of the keys 8 j + 2 c and the next
-        if constexpr (F != kCacheSame) {
+        float vs[NT][2];  // scales of the values of the keys 8 j + 2 c and the next
+        if constexpr (kCodes) {
             const uint32_t mine = (bytes >> 8) == 255u ? 0u : bytes >> 8;
             const uint32_t top = __reduce_max_sync(0xffffffffu, mine);
             if (top > z.top) {
@@ -414,33 +407,27 @@ struct CacheWalk {
 #pragma unroll
                         for (int e = 0; e < 4; ++e) z.o[t][d][e] *= f;
             }
+            const uint32_t pair = bytes | (__shfl_down_sync(0xffffffffu, bytes, 1) << 16);
 #pragma unroll
-            for (int j = 0; j < NT; ++j)
+            for (int j = 0; j < NT; ++j) {
+                const uint32_t two = __shfl_sync(0xffffffffu, pair, j * 8 + 2 * c);
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    const uint32_t y = __shfl_sync(0xffffffffu, bytes, j * 8 + 2 * c + e), w = y >> 8;
-                    ks[j][e] = cache_scale(y & 255u);
-                    vs[j][e] = w == 255u ? cache_scale(255u) : w + 126 < z.top ? 0.f : cache_scale(127 + w - z.top);
+                    const uint32_t y = e ? two >> 16 : two & 0xffffu, w = y >> 8;
+                    const float ks = cache_scale(y & 255u);
+                    vs[j][e] = w == 255u ? cache_scale(255u) : w == 0u ? 0.f : cache_scale((uint32_t)max((int)(127 + w - z.top), 0));
+#pragma unroll
+                    for (int t = 0; t < MT; ++t) s[t][j][e] *= ks, s[t][j][2 + e] *= ks;
                 }
+            }
         }
-        float factors[MT][2];
-#pragma unroll
-        for (int t = 0; t < MT; ++t) factors[t][0] = factor[t * 16 + g], factors[t][1] = factor[t * 16 + g + 8];
-#pragma unroll
-        for (int t = 0; t < MT; ++t)
-#pragma unroll
-            for (int j = 0; j < NT; ++j)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    s[t][j][e] *= factors[t][e >> 1];
-                    if constexpr (F != kCacheSame) s[t][j][e] *= ks[j][e & 1];
-                }
-        if constexpr (TAIL) {
+        if (i >= cached) {
+            const int key0 = first_new + (i - cached) * step_keys;
 #pragma unroll
             for (int t = 0; t < MT; ++t)
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    const int q = (u.rt * a.tile_rows + t * 16 + g + 8 * h) / a.G;  // the row's token
+                    const int q = token_of[t * 16 + g + 8 * h];
                     const uint8_t* mask = a.mask ? a.mask + u.b * a.mk_sb + q * a.mk_sq : nullptr;
 #pragma unroll
                     for (int j = 0; j < NT; ++j)
@@ -451,26 +438,45 @@ struct CacheWalk {
                             if (!on) s[t][j][2 * h + e] = -attn_inf();
                         }
                 }
-        } else if (key0 + KS > u.length || there != (1u << GR) - 1) {
+        } else {
+            const int key0 = first + i * step_keys;
+            if (key0 + KS > u.length || there != (1u << GR) - 1) {
 #pragma unroll
-            for (int j = 0; j < NT; ++j)
+                for (int j = 0; j < NT; ++j)
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const bool on = key0 + j * 8 + 2 * c + e < u.length && ((there >> (j / 2)) & 1u);
+                    for (int e = 0; e < 2; ++e) {
+                        const bool on = key0 + j * 8 + 2 * c + e < u.length && ((there >> (j / 2)) & 1u);
 #pragma unroll
-                    for (int t = 0; t < MT; ++t)
-                        if (!on) s[t][j][e] = s[t][j][2 + e] = -attn_inf();
-                }
+                        for (int t = 0; t < MT; ++t)
+                            if (!on) s[t][j][e] = s[t][j][2 + e] = -attn_inf();
+                    }
+            }
         }
-        // the reference of a row follows when a score passes it by kCacheAbove
-        bool renew = false;
+        // P against the reference at hand, and once more where a sum asks for another (the first step's does)
+        float f[MT][2], p[MT][NT][4], sum[MT][2];
 #pragma unroll
         for (int t = 0; t < MT; ++t)
 #pragma unroll
-            for (int j = 0; j < NT; ++j)
+            for (int h = 0; h < 2; ++h) f[t][h] = kCodes ? factor[t * 16 + g + 8 * h] : a.c2;
+#pragma unroll 1
+        for (int pass = 0; pass < 2; ++pass) {
+            bool renew = false;
 #pragma unroll
-                for (int e = 0; e < 4; ++e) renew |= s[t][j][e] - z.m[t][e >> 1] > kCacheAbove;
-        if (__any_sync(0xffffffffu, renew)) {
+            for (int t = 0; t < MT; ++t)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    sum[t][h] = 0.f;
+#pragma unroll
+                    for (int j = 0; j < NT; ++j)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const float x = cache_ex2(fmaf(s[t][j][2 * h + e], f[t][h], -z.m[t][h]));
+                            p[t][j][2 * h + e] = x;
+                            sum[t][h] += x;
+                        }
+                    renew |= !(sum[t][h] <= kCacheMost);
+                }
+            if (pass > 0 || !__any_sync(0xffffffffu, renew)) break;
 #pragma unroll
             for (int t = 0; t < MT; ++t)
 #pragma unroll
@@ -480,69 +486,65 @@ struct CacheWalk {
                     for (int j = 0; j < NT; ++j) top = fmaxf(top, fmaxf(s[t][j][2 * h], s[t][j][2 * h + 1]));
                     top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
                     top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-                    const float next = fmaxf(z.m[t][h], top - P::below);
-                    const float f = next == z.m[t][h] ? 1.f : cache_ex2(z.m[t][h] - next);
-                    z.m[t][h] = next;
-                    z.l[t][h] *= f;
+                    const float m = fmaxf(z.m[t][h], top * f[t][h] - P::below);
+                    const float by = m == z.m[t][h] ? 1.f : cache_ex2(z.m[t][h] - m);
+                    z.m[t][h] = m;
+                    z.l[t][h] *= by;
 #pragma unroll
-                    for (int d = 0; d < DP / 8; ++d) z.o[t][d][2 * h] *= f, z.o[t][d][2 * h + 1] *= f;
+                    for (int d = 0; d < DP / 8; ++d) z.o[t][d][2 * h] *= by, z.o[t][d][2 * h + 1] *= by;
                 }
         }
 #pragma unroll
         for (int t = 0; t < MT; ++t)
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const float ref = z.m[t][h] == -attn_inf() ? 0.f : z.m[t][h];
-#pragma unroll
-                for (int j = 0; j < NT; ++j)
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const float x = cache_ex2(s[t][j][2 * h + e] - ref);
-                        z.l[t][h] += x;
-                        s[t][j][2 * h + e] = F != kCacheSame ? x * vs[j][e] : x;
-                    }
-            }
+            for (int h = 0; h < 2; ++h) z.l[t][h] += sum[t][h];
 #pragma unroll
         for (int kk = 0; kk < GR; ++kk) {
-            uint4 p[P::pp][MT];
+            uint4 pf[P::pp][MT];
 #pragma unroll
             for (int t = 0; t < MT; ++t) {
                 uint32_t x[4][P::pp];
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    cache_pieces<P::bf16, P::pp>(s[t][2 * kk + (e >> 1)][2 * (e & 1)], s[t][2 * kk + (e >> 1)][2 * (e & 1) + 1], x[e]);
+                for (int e = 0; e < 4; ++e) {
+                    float lo = p[t][2 * kk + (e >> 1)][2 * (e & 1)], hi = p[t][2 * kk + (e >> 1)][2 * (e & 1) + 1];
+                    if constexpr (kCodes) lo *= vs[2 * kk + (e >> 1)][0], hi *= vs[2 * kk + (e >> 1)][1];
+                    cache_pieces<P::bf16, P::pp>(lo, hi, x[e]);
+                }
 #pragma unroll
-                for (int i2 = 0; i2 < P::pp; ++i2) p[i2][t] = make_uint4(x[0][i2], x[1][i2], x[2][i2], x[3][i2]);
+                for (int i2 = 0; i2 < P::pp; ++i2) pf[i2][t] = make_uint4(x[0][i2], x[1][i2], x[2][i2], x[3][i2]);
             }
-            outputs(v, kk, p, z);
+            outputs(v, kk, pf, z);
         }
     }
 
     __device__ __forceinline__ void run(CacheState<DP, MT>& z) {
-        begin();
+        const int steps = cached + fresh;
+        if (cached > 0) {
+            here = group_entry(lane);
+            next = group_entry(32 + lane);
+            here = cache_page_of(a.c, here);
+            have = 0;
+        }
         uint32_t bytes[STAGES], there[STAGES];  // of the steps in flight, the nearest first
 #pragma unroll
-        for (int i = 0; i < STAGES - 1; ++i) {
-            bytes[i] = there[i] = 0;
-            if (i < steps) issue(i, bytes[i], there[i]);
-            cache_commit();
-        }
+        for (int j = 0; j < STAGES; ++j) bytes[j] = there[j] = 0;
+        // one place for the copies and one for the products, the copies STAGES - 1 steps ahead
 #pragma unroll 1
-        for (int i = 0; i < steps; ++i) {
-            if constexpr (STAGES == 1) {
+        for (int i = 1 - STAGES; i < steps; ++i) {
+            if constexpr (STAGES > 1) {
+                cache_wait<(STAGES > 1 ? STAGES - 2 : 0)>();
+                __syncwarp();  // the step's copies of all lanes are there, and the stage of step i - 1 is read
+            } else {
                 __syncwarp();
-                issue(i, bytes[0], there[0]);
-                cache_commit();
+            }
+            bytes[STAGES - 1] = there[STAGES - 1] = 0;
+            if (i + STAGES - 1 < steps) issue(i + STAGES - 1, bytes[STAGES - 1], there[STAGES - 1]);
+            cache_commit();
+            if constexpr (STAGES == 1) {
                 cache_wait<0>();
                 __syncwarp();
-            } else {
-                cache_wait<STAGES - 2>();
-                __syncwarp();  // the step's copies of all lanes are there, and the stage of step i - 1 is read
-                bytes[STAGES - 1] = there[STAGES - 1] = 0;
-                if (i + STAGES - 1 < steps) issue(i + STAGES - 1, bytes[STAGES - 1], there[STAGES - 1]);
-                cache_commit();
             }
-            compute(i, bytes[0], there[0], z);
+            if (i >= 0) compute(i, bytes[0], there[0], z);
 #pragma unroll
             for (int j = 0; j + 1 < STAGES; ++j) bytes[j] = bytes[j + 1], there[j] = there[j + 1];
         }
@@ -551,58 +553,81 @@ struct CacheWalk {
     }
 };
 
+template <typename T>
+__device__ __forceinline__ void cache_four(const T* p, float (&y)[4]) {
+    if constexpr (sizeof(T) == 4) {
+        const float4 x = *reinterpret_cast<const float4*>(p);
+        y[0] = x.x, y[1] = x.y, y[2] = x.z, y[3] = x.w;
+    } else {
+        const uint2 x = *reinterpret_cast<const uint2*>(p);
+        const float2 lo = cache_unpack<CacheType<T>::code == 2>(x.x), hi = cache_unpack<CacheType<T>::code == 2>(x.y);
+        y[0] = lo.x, y[1] = lo.y, y[2] = hi.x, y[3] = hi.y;
+    }
+}
+
 template <typename T, int F, int DP, int MT>
 __global__ void __launch_bounds__(kCacheWarps * 32, CacheRowsCfg<T, F, DP, MT>::kResident) msda_cache_rows_kernel(const CacheArgs a) {
     using Cfg = CacheRowsCfg<T, F, DP, MT>;
     using P = CacheProduct<T, F>;
     using PT = CacheProduct<T, kCacheSame>;
     using Ty = CacheType<T>;
-    constexpr int R = MT * 16, STEPS = DP / 16, OB = DP + 4;
+    constexpr int R = MT * 16, STEPS = DP / 16, OB = DP + 4, KS = Cfg::KS, KT = Cfg::kTailKeys;
+    constexpr bool CODES = F != kCacheSame;
     extern __shared__ __align__(128) unsigned char cache_smem_raw[];
-    __shared__ float factor[3][R], part_m[kCacheWarps][R], part_l[kCacheWarps][R];
+    __shared__ CacheStart start;
+    __shared__ float factor[R], up[R], part_m[kCacheWarps][R], part_l[kCacheWarps][R];
+    __shared__ int token_of[R], head_of[R];  // of a row; token T: there is none
     uint4* qf = reinterpret_cast<uint4*>(cache_smem_raw);
-    uint4* qt = F == kCacheSame ? qf : qf + P::qp * Cfg::kFragments / 16;
+    uint4* qt = CODES ? qf + P::qp * Cfg::kFragments / 16 : qf;
     unsigned char* ring = cache_smem_raw + Cfg::kQ;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, c = lane & 3;
+    if (warp == 0) {
+        const CacheStart s = cache_start(a);
+        if (lane == 0) start = s;
+    }
+    __syncthreads();
 
-    cache_walk(a, [&](const CacheUnit& u, int tile, int tiles, int slot) {
+    cache_walk(a, start, threadIdx.x == 0, [&](const CacheUnit& u, int tile, int tiles, int slot) {
         const T* query = static_cast<const T*>(a.q) + u.b * a.q_sb + (long long)u.n * a.G * a.q_sh;
-        auto row_of = [&](int r) -> const T* {  // null where there is none
-            const int x = u.rt * R + r, t = x / a.G;
-            return x < a.rows && t < u.count ? query + t * a.q_st + (x - t * a.G) * a.q_sh : nullptr;
-        };
         __syncthreads();  // the unit before is out
-        // ---- scales of the rows: with 8 bits a power of two that brings a row's largest to 2^14 or more ----
-        for (int r = warp; r < R; r += kCacheWarps) {
-            float up = 1.f;
-            if constexpr (F != kCacheSame) {
-                const T* q = row_of(r);
-                float top = 0.f;
-                if (q)
-                    for (int d = lane; d < a.D; d += 32) top = fmaxf(top, fabsf(Ty::get(q[d])));
-#pragma unroll
-                for (int w = 16; w > 0; w >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, w));
-                const int e = (int)(__float_as_uint(top) >> 23);  // 2^(e - 127) <= top
-                up = top > 0.f && e < 255 ? __uint_as_float((uint32_t)min(max(268 - e, 27), 227) << 23) : 1.f;
-            }
-            if (lane == 0) {
-                factor[0][r] = a.c2 * (1.f / up);  // a power of two: exact
-                factor[1][r] = up;
-                factor[2][r] = a.c2;
-            }
+        if (threadIdx.x < R) {
+            const int x = u.rt * R + threadIdx.x, t = x / a.G;
+            token_of[threadIdx.x] = x < a.rows ? t : a.T;
+            head_of[threadIdx.x] = x - t * a.G;
         }
         __syncthreads();
+        // ---- codes: a power of two that brings a row's largest to 2^14 or more ----
+        if constexpr (CODES) {
+#pragma unroll 1
+            for (int r = warp; r < R; r += kCacheWarps) {
+                const int t = token_of[r];
+                float top = 0.f;
+                if (t < u.count && lane * 4 < a.D) {
+                    float y[4];
+                    cache_four(query + t * a.q_st + head_of[r] * a.q_sh + lane * 4, y);
+                    top = fmaxf(fmaxf(fabsf(y[0]), fabsf(y[1])), fmaxf(fabsf(y[2]), fabsf(y[3])));
+                }
+                top = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top)));
+                const int e = (int)(__float_as_uint(top) >> 23);  // 2^(e - 127) <= top
+                const float by = e > 0 && e < 255 ? __uint_as_float((uint32_t)min(max(268 - e, 27), 227) << 23) : 1.f;
+                if (lane == 0) {
+                    up[r] = by;
+                    factor[r] = fmaxf(a.c2 * (1.f / by), 1e-37f);  // a power of two: exact; never 0, which would make NaN of what is hidden
+                }
+            }
+            __syncthreads();
+        }
         // ---- the queries' fragments: entry (tile t of 16, step s, lane) are the channels of lane % 4 at step s of rows lane / 4 and + 8 ----
+#pragma unroll 1
         for (int x = threadIdx.x; x < MT * STEPS * 32; x += kCacheWarps * 32) {
             const int ln = x & 31, s = (x >> 5) % STEPS, t = (x >> 5) / STEPS;
             const int ch = Cfg::E * ((ln & 3) + 4 * (s / (Cfg::E / 4))) + 4 * (s % (Cfg::E / 4));
             float y[2][4];
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                const int r = t * 16 + (ln >> 2) + 8 * h;
-                const T* q = row_of(r);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) y[h][e] = q && ch + e < a.D ? Ty::get(q[ch + e]) : 0.f;
+                const int r = t * 16 + (ln >> 2) + 8 * h, tok = token_of[r];
+                y[h][0] = y[h][1] = y[h][2] = y[h][3] = 0.f;
+                if (tok < u.count && ch < a.D) cache_four(query + tok * a.q_st + head_of[r] * a.q_sh + ch, y[h]);
             }
             auto put = [&](uint4* to, auto product, float up0, float up1) {
                 using Q = decltype(product);
@@ -614,8 +639,12 @@ __global__ void __launch_bounds__(kCacheWarps * 32, CacheRowsCfg<T, F, DP, MT>::
 #pragma unroll
                 for (int p = 0; p < Q::qp; ++p) to[((p * MT + t) * STEPS + s) * 32 + ln] = make_uint4(f[0][p], f[1][p], f[2][p], f[3][p]);
             };
-            put(qf, P{}, factor[1][t * 16 + (ln >> 2)], factor[1][t * 16 + (ln >> 2) + 8]);
-            if constexpr (F != kCacheSame) put(qt, PT{}, 1.f, 1.f);
+            if constexpr (CODES) {
+                put(qf, P{}, up[t * 16 + (ln >> 2)], up[t * 16 + (ln >> 2) + 8]);
+                if (a.nk) put(qt, PT{}, 1.f, 1.f);
+            } else {
+                put(qf, P{}, 1.f, 1.f);
+            }
         }
         __syncthreads();
 
@@ -624,40 +653,46 @@ __global__ void __launch_bounds__(kCacheWarps * 32, CacheRowsCfg<T, F, DP, MT>::
 #pragma unroll
         for (int t = 0; t < MT; ++t) {
 #pragma unroll
-            for (int h = 0; h < 2; ++h) z.m[t][h] = -attn_inf(), z.l[t][h] = 0.f;
+            for (int h = 0; h < 2; ++h) z.m[t][h] = kCacheNone, z.l[t][h] = 0.f;
 #pragma unroll
             for (int d = 0; d < DP / 8; ++d)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) z.o[t][d][e] = 0.f;
         }
-        const int from_cache = max(0, min(tile + tiles, u.cache_tiles) - tile);
         unsigned char* my_ring = ring + warp * Cfg::kRing;
-        if (from_cache > 0) {
-            const int first = tile * (kCacheWarps * Cfg::KS) + warp * Cfg::KS;
-            const int mine = first < u.length ? (u.length - first + kCacheWarps * Cfg::KS - 1) / (kCacheWarps * Cfg::KS) : 0;
-            CacheWalk<T, F, DP, MT, Cfg::E, Cfg::EV, Cfg::KS, Cfg::kStages, false> walk{
-                a, u, my_ring, qf, factor[0], lane, warp, first, min(from_cache, mine), kCacheWarps * Cfg::KS, 0, 0, 0};
+        // this warp's steps over the cache, and over the new tokens
+        constexpr int step = kCacheWarps * KS, step_new = kCacheWarps * KT;
+        const int last = min(tile + tiles, u.cache_tiles), first = tile * step + warp * KS;
+        const int cached = max(0, min(last - tile, (u.length - first + step - 1) / step));
+        int fresh = 0, first_new = 0;
+        if (a.nk && tile + tiles > u.cache_tiles) {
+            const int at = max(0, tile - u.cache_tiles), end = min(cache_tail_keys(a, u.rt, u.count), (tile + tiles - u.cache_tiles) * step_new);
+            first_new = at * step_new + warp * KT;
+            fresh = first_new < end ? (end - first_new + step_new - 1) / step_new : 0;
+        }
+        if constexpr (CODES) {
+            if (cached > 0) {
+                CacheWalk<T, F, DP, MT, Cfg::E, Cfg::EV, KS, Cfg::kStages> walk{a, u, my_ring, qf, factor, token_of, lane, first, cached, 0, 0, step, 0, 0, 0};
+                walk.run(z);
+                if (z.top != 0) {  // back to units of 1
+                    const float f = cache_scale(z.top);
+#pragma unroll
+                    for (int t = 0; t < MT; ++t)
+#pragma unroll
+                        for (int d = 0; d < DP / 8; ++d)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) z.o[t][d][e] *= f;
+                }
+            }
+            if (fresh > 0) {
+                CacheWalk<T, kCacheSame, DP, MT, Cfg::E, Cfg::EV, KT, Cfg::kTailStages> walk{a, u, my_ring, qt, factor, token_of, lane, 0, 0, first_new, fresh, step_new, 0, 0, 0};
+                walk.run(z);
+            }
+        } else if (cached + fresh > 0) {
+            CacheWalk<T, F, DP, MT, Cfg::E, Cfg::EV, KS, Cfg::kStages> walk{a, u, my_ring, qf, factor, token_of, lane, first, cached, first_new, fresh, step, 0, 0, 0};
             walk.run(z);
         }
-        if (F != kCacheSame && z.top != 0) {  // back to units of 1
-            const float f = cache_scale(z.top);
-#pragma unroll
-            for (int t = 0; t < MT; ++t)
-#pragma unroll
-                for (int d = 0; d < DP / 8; ++d)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) z.o[t][d][e] *= f;
-        }
-        if (tile + tiles > u.cache_tiles && a.nk) {
-            const int keys = cache_tail_keys(a, u.rt, u.count), at = max(0, tile - u.cache_tiles);
-            constexpr int KT = Cfg::kTailKeys;
-            const int first = at * (kCacheWarps * KT) + warp * KT, end = min(keys, (tile + tiles - u.cache_tiles) * (kCacheWarps * KT));
-            const int steps = first < end ? (end - first + kCacheWarps * KT - 1) / (kCacheWarps * KT) : 0;
-            CacheWalk<T, kCacheSame, DP, MT, Cfg::E, Cfg::EV, KT, Cfg::kTailStages, true> walk{
-                a, u, my_ring, qt, factor[2], lane, warp, first, steps, kCacheWarps * KT, 0, 0, 0};
-            walk.run(z);
-        }
-        __syncthreads();  // rings and factors are done with
+        __syncthreads();  // rings are done with
         // ---- the warps' parts, joined in their order ----
         float* po = reinterpret_cast<float*>(ring);
 #pragma unroll
@@ -679,23 +714,24 @@ __global__ void __launch_bounds__(kCacheWarps * 32, CacheRowsCfg<T, F, DP, MT>::
                     }
             }
         __syncthreads();
+#pragma unroll 1
         for (int x = threadIdx.x; x < R * (DP / 4); x += kCacheWarps * 32) {
-            const int r = x / (DP / 4), d = x % (DP / 4) * 4, row = u.rt * R + r;
-            if (row >= a.rows || d >= a.D) continue;
-            float top = -attn_inf();
+            const int r = x / (DP / 4), d = x % (DP / 4) * 4, t = token_of[r];
+            if (t >= a.T || d >= a.D) continue;
+            float top = kCacheNone;
 #pragma unroll
             for (int w = 0; w < kCacheWarps; ++w) top = fmaxf(top, part_m[w][r]);
             float sum = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int w = 0; w < kCacheWarps; ++w) {
-                const float f = top == -attn_inf() ? 1.f : exp2f(part_m[w][r] - top);  // none seen: zeros, or NaN scores alone
+                const float f = exp2f(part_m[w][r] - top);
                 sum += part_l[w][r] * f;
                 const float4 y = *reinterpret_cast<const float4*>(&po[(w * R + r) * OB + d]);
                 o[0] += y.x * f, o[1] += y.y * f, o[2] += y.z * f, o[3] += y.w * f;
             }
-            const int t = row / a.G, h = u.n * a.G + row - t * a.G;
+            const int h = u.n * a.G + head_of[r];
             const bool none = sum == 0.f || t >= u.count;
-            const float ref = top == -attn_inf() ? 0.f : top, l2 = none ? -attn_inf() : ref + log2f(sum), inv = none ? 0.f : 1.f / sum;
+            const float l2 = none ? -attn_inf() : top + log2f(sum), inv = none ? 0.f : 1.f / sum;
 #pragma unroll
             for (int e = 0; e < 4; ++e) o[e] = none ? 0.f : o[e] * inv;
             if (slot >= 0) {

@@ -89,9 +89,9 @@ struct CacheSegment {
 
 // Calls f(segment) for each unit of the block; false ends it.  n is 0 for rows that see nothing.
 template <typename F>
-__device__ __forceinline__ void cache_segments(const CacheArgs& a, F f) {
+__device__ __forceinline__ void cache_segments(const CacheArgs& a, const CacheStart& start, bool note, F f) {
     bool ok = true;
-    cache_walk(a, [&](const CacheUnit& u, int tile, int tiles, int slot) {
+    cache_walk(a, start, note, [&](const CacheUnit& u, int tile, int tiles, int slot) {
         if (!ok) return;
         CacheSegment s;
         s.u = u, s.first = tile, s.slot = slot;
@@ -119,6 +119,7 @@ __global__ void __launch_bounds__(CacheTcCfg<F, NQ, NC>::kThreads, 1)
     unsigned char* ring = smem + NQ * Cfg::kTileBytes;
     unsigned char* raw = ring + ST * Cfg::kTileBytes;
     __shared__ CacheTcSync sy;
+    __shared__ CacheStart start;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int qpt = a.tile_rows / (NQ * a.G), rows = qpt * a.G;  // tokens and rows of a row tile
 
@@ -145,9 +146,20 @@ __global__ void __launch_bounds__(CacheTcCfg<F, NQ, NC>::kThreads, 1)
             }
             sy.abort = 0;
             asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+            tc_prefetch_map(&map_q);
+            tc_prefetch_map(&map_k);
+            tc_prefetch_map(&map_v);
+            if (!CODES && a.nk) {
+                tc_prefetch_map(&map_nk);
+                tc_prefetch_map(&map_nv);
+            }
         }
     } else if (warp == NQ * 4 + 1) {
         tmem_alloc(tc_smem(&sy.tmem), Cfg::kCols);
+    }
+    if (warp == 0) {
+        const CacheStart s = cache_start(a);
+        if (lane == 0) start = s;
     }
     if (rows < kTcRows) {  // rows that no query fills hold zeros, not what was there
         const uint32_t words = (kTcRows - rows) * 8;
@@ -175,7 +187,7 @@ __global__ void __launch_bounds__(CacheTcCfg<F, NQ, NC>::kThreads, 1)
         const int chunks = a.D / 16;
         const uint32_t first = lane == 0;
         int g0 = 0;  // tiles before this segment
-        cache_segments(a, [&](const CacheSegment& sg) {
+        cache_segments(a, start, tid == 0, [&](const CacheSegment& sg) {
             const CacheUnit& u = sg.u;
             const int tok = u.rt * NQ * qpt + t * qpt + row / a.G, h = u.n * a.G + row % a.G;
             const bool there = row < rows && tok < a.T, valid = there && tok < u.count;
@@ -233,6 +245,7 @@ __global__ void __launch_bounds__(CacheTcCfg<F, NQ, NC>::kThreads, 1)
                         for (int c = 0; c < 4; ++c) {
                             uint32_t bits = 0;
                             if (fours) {
+#pragma unroll 1
                                 for (int k = 0; k < 32; k += 4) {
                                     const int j = c * 32 + k;
                                     uint32_t x = 0;
@@ -244,6 +257,7 @@ __global__ void __launch_bounds__(CacheTcCfg<F, NQ, NC>::kThreads, 1)
                                     for (int e = 0; e < 4; ++e) bits |= ((x >> (8 * e)) & 255u ? 1u : 0u) << (k + e);
                                 }
                             } else {
+#pragma unroll 1
                                 for (int k = 0; k < 32; ++k)
                                     if (c * 32 + k < n && mask[c * 32 + k]) bits |= 1u << k;
                             }
@@ -310,42 +324,52 @@ __global__ void __launch_bounds__(CacheTcCfg<F, NQ, NC>::kThreads, 1)
                         tc_split(tc_add2(part[0], part[1]), s0, s1);
                         return s0 + s1;
                     };
+                    // One place for the exponentials (code that is fetched first takes longer than it runs): against the reference at
+                    // hand, and once more where that is none yet or a sum asks for another.
                     bool renew = (CODES && v_ref != v_old && i > 0) || __any_sync(0xffffffffu, valid && m == -attn_inf());
+                    bool fresh = Cfg::kOwnP && i > 0;  // the last P is not known to be used up
                     float sum = 0.f;
-                    if (__builtin_expect(!renew, 1)) {
-                        sum = probabilities(Cfg::kOwnP && i > 0);
-                        renew = __any_sync(0xffffffffu, valid && !(sum <= Range::kTop));
-                    } else if (Cfg::kOwnP && i > 0) {
-                        gone = !tc_bar_wait(tc_smem(&sy.pv_done[t]), (gi - 1) & 1, abort, err);
-                        tc_fence_after();
-                    }
-                    if (__builtin_expect(renew, 0)) {
-                        float mx[4];
-#pragma unroll
-                        for (int c = 0; c < 4; ++c) {
-                            mx[c] = fmaxf(__uint_as_float(s[c][0]), __uint_as_float(s[c][1]));
-#pragma unroll
-                            for (int k = 2; k < 32; k += 2)
-                                mx[c] = tc_max3(mx[c], __uint_as_float(s[c][k]), __uint_as_float(s[c][k + 1]));
-                        }
-                        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * ct;
-                        const float next = fmaxf(m, top - Range::kBelow);
-                        const float f = next == m ? 1.f : tc_ex2(m - next);
-                        m = next;
-                        l *= f;
-                        if (i > 0) {
-                            float fo = f;
-                            if constexpr (CODES) fo *= v_ref - v_old > 126 ? 0.f : cache_scale(127 + v_old - v_ref);
-                            for (int c = 0; c < chunks; ++c) {
-                                uint32_t o[16];
-                                tmem_ld16(o, o_at + c * 16);
-                                tmem_wait_ld();
-#pragma unroll
-                                for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * fo);
-                                tmem_st16(o_at + c * 16, o);
+#pragma unroll 1
+                    for (int pass = 0; pass < 2; ++pass) {
+                        if (__builtin_expect(renew, 0)) {
+                            if (fresh) {
+                                gone = !tc_bar_wait(tc_smem(&sy.pv_done[t]), (gi - 1) & 1, abort, err);
+                                tc_fence_after();
+                                fresh = false;
                             }
+                            float mx[4];
+#pragma unroll
+                            for (int c = 0; c < 4; ++c) {
+                                mx[c] = fmaxf(__uint_as_float(s[c][0]), __uint_as_float(s[c][1]));
+#pragma unroll
+                                for (int k = 2; k < 32; k += 2)
+                                    mx[c] = tc_max3(mx[c], __uint_as_float(s[c][k]), __uint_as_float(s[c][k + 1]));
+                            }
+                            const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * ct;
+                            const float next = fmaxf(m, top - Range::kBelow);
+                            const float f = next == m ? 1.f : tc_ex2(m - next);
+                            m = next;
+                            l *= f;
+                            if (i > 0) {
+                                float fo = f;
+                                if constexpr (CODES) fo *= v_ref - v_old > 126 ? 0.f : cache_scale(127 + v_old - v_ref);
+#pragma unroll 1
+                                for (int c = 0; c < chunks; ++c) {
+                                    uint32_t o[16];
+                                    tmem_ld16(o, o_at + c * 16);
+                                    tmem_wait_ld();
+#pragma unroll
+                                    for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * fo);
+                                    tmem_st16(o_at + c * 16, o);
+                                }
+                            }
+                            if constexpr (CODES) v_old = v_ref;
+                            pass = 1;  // the reference is the tile's own: no sum can ask for another
                         }
-                        sum = probabilities(false);
+                        sum = probabilities(fresh);
+                        fresh = false;
+                        renew = __any_sync(0xffffffffu, valid && !(sum <= Range::kTop));
+                        if (!renew) break;
                     }
                     if (__builtin_expect(gone, 0)) return false;
                     if constexpr (CODES) sum *= exp2f(-dv);
@@ -372,6 +396,7 @@ __global__ void __launch_bounds__(CacheTcCfg<F, NQ, NC>::kThreads, 1)
             if constexpr (CODES) inv *= v_ref == 0 ? 0.f : cache_scale(v_ref);
             const float l2 = none ? -attn_inf() : m + log2f(l);
             const long long at = (long long)sg.slot * a.tile_rows + t * rows + row;
+#pragma unroll 1
             for (int c = 0; c < chunks; ++c) {
                 uint32_t o[16];
                 if (sg.n > 0 && warp_on) {
@@ -412,7 +437,7 @@ __global__ void __launch_bounds__(CacheTcCfg<F, NQ, NC>::kThreads, 1)
             const int boxes = kTcRows / box_rows;
             const uint32_t qbar = tc_smem(&sy.q_full);
             int g0 = 0, r0 = 0, qs = 0;  // tiles, tiles of codes, queries so far
-            cache_segments(a, [&](const CacheSegment& sg) {
+            cache_segments(a, start, false, [&](const CacheSegment& sg) {
                 const CacheUnit& u = sg.u;
                 if (sg.n == 0) return true;
                 if constexpr (!OWN_Q) {
@@ -425,14 +450,14 @@ __global__ void __launch_bounds__(CacheTcCfg<F, NQ, NC>::kThreads, 1)
                     }
                     ++qs;
                 }
-                auto page_of = [&](int tile) {  // of this lane's box
-                    const int token = tile * kTcRows + lane * box_rows;
-                    return lane < boxes && tile < u.cache_tiles && token < u.length ? cache_page(a.c, u.b, token) : -1;
+                auto entry_of = [&](int i) {  // of this lane's box at tile sg.first + i
+                    const int tile = sg.first + i, token = tile * kTcRows + lane * box_rows;
+                    return i < sg.n && lane < boxes && tile < u.cache_tiles && token < u.length ? cache_entry(a.c, u.b, token) : kCacheNoPage;
                 };
-                int page = page_of(sg.first);
+                int entry = entry_of(0), entry1 = entry_of(1);
                 for (int i = 0; i < sg.n; ++i) {
-                    const int gi = g0 + i, tile = sg.first + i, mine = page;
-                    page = i + 1 < sg.n ? page_of(tile + 1) : -1;
+                    const int gi = g0 + i, tile = sg.first + i, mine = cache_page_of(a.c, entry);
+                    entry = entry1, entry1 = entry_of(i + 2);
                     const bool tail = tile >= u.cache_tiles;
                     if (!tail) {
                         // a tile's words are read 8 tiles later at most: the rings are shorter
@@ -495,7 +520,7 @@ __global__ void __launch_bounds__(CacheTcCfg<F, NQ, NC>::kThreads, 1)
             };
             int g0 = 0, qs = 0;
             uint32_t clears = 0;  // a bit a stage: which phase of its `cleared` is next
-            cache_segments(a, [&](const CacheSegment& sg) {
+            cache_segments(a, start, false, [&](const CacheSegment& sg) {
                 const CacheUnit& u = sg.u;
                 if (sg.n == 0) return true;
                 if (!tc_bar_wait(tc_smem(&sy.q_full), qs & 1, abort, err)) return false;
@@ -542,7 +567,7 @@ __global__ void __launch_bounds__(CacheTcCfg<F, NQ, NC>::kThreads, 1)
         } else if (role == 2 && !CODES) {
             // ---- value rows behind the last ----
             int g0 = 0;
-            cache_segments(a, [&](const CacheSegment& sg) {
+            cache_segments(a, start, false, [&](const CacheSegment& sg) {
                 const CacheUnit& u = sg.u;
                 for (int i = 0; i < sg.n; ++i) {
                     const int tile = sg.first + i, idx = 2 * (g0 + i) + 1, st = idx % ST;
@@ -566,28 +591,29 @@ __global__ void __launch_bounds__(CacheTcCfg<F, NQ, NC>::kThreads, 1)
         // ---- codes to f16 operands: row `row` of each tile ----
         const int cw = warp - NQ * 4 - 4, row = cw * 32 + lane;
         int g0 = 0, r0 = 0;
-        cache_segments(a, [&](const CacheSegment& sg) {
+        cache_segments(a, start, false, [&](const CacheSegment& sg) {
             const CacheUnit& u = sg.u;
-            auto page_of = [&](int i) {  // of this row at tile sg.first + i
+            auto entry_of = [&](int i) {  // of this row at tile sg.first + i
                 const int token = (sg.first + i) * kTcRows + row;
-                return i < sg.n && sg.first + i < u.cache_tiles && token < u.length ? cache_page(a.c, u.b, token) : -1;
+                return i < sg.n && sg.first + i < u.cache_tiles && token < u.length ? cache_entry(a.c, u.b, token) : kCacheNoPage;
             };
-            auto bytes_of = [&](int i, int page) {  // its bytes; bit 16: there is such a row
+            auto bytes_of = [&](int i, int entry) {  // its bytes; bit 16: there is such a row
+                const int page = (unsigned)entry < (unsigned)a.c.pages ? entry : -1;  // the warp that copies tells of bad ones
                 if (page < 0) return 0u;
                 const int place = ((sg.first + i) * kTcRows + row) & (a.c.page - 1);
                 return 0x10000u | a.c.ks[page * a.c.ks_sp + place * a.c.ks_st + u.n * a.c.ks_sh] |
                        ((uint32_t)a.c.vs[page * a.c.vs_sp + place * a.c.vs_st + u.n * a.c.vs_sh] << 8);
             };
-            uint32_t bytes = bytes_of(0, page_of(0));
-            int page = page_of(1);  // of the tile behind
+            int entry = entry_of(0), entry1 = entry_of(1), entry2 = entry_of(2);
+            uint32_t bytes = bytes_of(0, entry);
 #pragma unroll 1
             for (int i = 0; i < sg.n; ++i) {
                 const int gi = g0 + i, tile = sg.first + i;
                 const bool tail = tile >= u.cache_tiles;
                 const int j = (tile - u.cache_tiles) * kTcRows + row;  // new token (tail)
                 const uint32_t now = bytes;
-                bytes = bytes_of(i + 1, page);
-                page = page_of(i + 2);
+                bytes = bytes_of(i + 1, entry1);
+                entry1 = entry2, entry2 = entry_of(i + 3);
                 bool there;
                 uint32_t kb, vb;  // of a new token's row: the byte that brings its largest value to 2^8 or more
                 if (!tail) {
