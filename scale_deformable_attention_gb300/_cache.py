@@ -9,7 +9,7 @@ from typing import NamedTuple, Optional, Tuple
 import torch
 
 from . import _lib
-from ._binding import DTYPE_CODE, on_device, ptr, stream, workspace_of
+from ._binding import DTYPE_CODE, stream, workspace_of
 
 # the problem struct of include/msda.h: 35 int64 members
 _problem = struct.Struct("35q").pack
@@ -45,29 +45,45 @@ def cache_create(pages: int, page: int, heads: int, channels: int, dtype: torch.
 
 
 def _pages(cache: PagedCache):
-    """(format, device, [pages, page, N, D], strides) of a cache, checked."""
+    """(format, device, [pages, page, N, D], strides, addresses) of a cache, checked."""
     key, value, ks, vs = cache
-    sh = key.shape
+    sh, dev, dt = key.shape, key.device, key.dtype
     if len(sh) != 4:
         raise ValueError(f"cache.key must be [pages, page, heads, D], got {tuple(sh)}")
-    dev, dt = key.device, key.dtype
     if dev.type != "cuda":
         raise ValueError("the operator runs on CUDA tensors only (there is no CPU implementation)")
-    if value.shape != sh or value.dtype != dt or value.device != dev:
+    if value.shape != sh or value.dtype is not dt or value.device != dev:
         raise ValueError(f"cache.value must be a {tuple(sh)} {dt} tensor on {dev}")
-    st, sv = key.stride(), value.stride()
-    if st[3] != 1 or sv[3] != 1:
+    k0, k1, k2, k3 = key.stride()
+    v0, v1, v2, v3 = value.stride()
+    if k3 != 1 or v3 != 1:
         raise ValueError("cache.key and cache.value need contiguous channels")
     if dt in CODE_FORMAT:
         for name, t in (("key_scale", ks), ("value_scale", vs)):
-            if t is None or t.shape != sh[:3] or t.dtype != torch.uint8 or t.device != dev:
+            if t is None or t.shape != sh[:3] or t.dtype is not torch.uint8 or t.device != dev:
                 raise ValueError(f"cache.{name} must be a {tuple(sh[:3])} uint8 tensor on {dev}")
-        return CODE_FORMAT[dt], dev, sh, (*st[:3], *sv[:3], *ks.stride(), *vs.stride())
+        return (CODE_FORMAT[dt], dev, sh, (k0, k1, k2, v0, v1, v2, *ks.stride(), *vs.stride()),
+                (key.data_ptr(), value.data_ptr(), ks.data_ptr(), vs.data_ptr()))
     if dt not in DTYPE_CODE:
         raise TypeError(f"unsupported cache dtype {dt}; use float32, float16, bfloat16, float8_e4m3fn or int8")
     if ks is not None or vs is not None:
         raise ValueError(f"a {dt} cache has no scales")
-    return _lib.CACHE_SAME, dev, sh, (*st[:3], *sv[:3], *_NONE3, *_NONE3)
+    return _lib.CACHE_SAME, dev, sh, (k0, k1, k2, v0, v1, v2, 0, 0, 0, 0, 0, 0), (key.data_ptr(), value.data_ptr(), None, None)
+
+
+def _call(f, dev: torch.device, *args):
+    """``f(*args, stream)`` with ``dev`` as the current device."""
+    if torch.cuda.current_device() == dev.index:
+        status = f(*args, stream(dev))
+    else:
+        with torch.cuda.device(dev):
+            status = f(*args, stream(dev))
+    if status:
+        _lib.check(status)
+
+
+def _address(t: Optional[torch.Tensor]) -> Optional[int]:
+    return None if t is None else t.data_ptr()
 
 
 def _index(name: str, t: torch.Tensor, B: int, dim: int, dev: torch.device) -> torch.Tensor:
@@ -84,6 +100,8 @@ def _index(name: str, t: torch.Tensor, B: int, dim: int, dev: torch.device) -> t
 
 def _rows(name: str, x: torch.Tensor, shape, dtype: torch.dtype, dev: torch.device) -> torch.Tensor:
     """``x`` as the kernels read it: rows that begin at multiples of 16 bytes (a copy where they do not)."""
+    if x.shape == shape and x.dtype is dtype and x.device == dev and x.is_contiguous() and not x.data_ptr() & 15:
+        return x
     if x.shape != shape:
         raise ValueError(f"{name} must be {tuple(shape)}, got {tuple(x.shape)}")
     if x.dtype != dtype:
@@ -91,8 +109,6 @@ def _rows(name: str, x: torch.Tensor, shape, dtype: torch.dtype, dev: torch.devi
     if x.device != dev:
         raise ValueError(f"{name} is on {x.device}, the cache on {dev}")
     if x.data_ptr() % 16 == 0:
-        if x.is_contiguous():
-            return x
         n, st = 16 // x.element_size(), x.stride()
         if st[3] == 1 and all(st[i] % n == 0 or shape[i] <= 1 for i in range(3)):
             return x
@@ -109,8 +125,9 @@ def _float_dtype(dtype: torch.dtype, fmt: int, cache: PagedCache) -> int:
 
 
 def _no_gradient(*tensors):
-    if torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors):
-        raise ValueError("the cache's operators have no gradient: call them under torch.no_grad() or detach the tensors")
+    for t in tensors:
+        if t is not None and t.requires_grad and torch.is_grad_enabled():
+            raise ValueError("the cache's operators have no gradient: call them under torch.no_grad() or detach the tensors")
 
 
 def cache_write(cache: PagedCache, key: torch.Tensor, value: torch.Tensor, table: torch.Tensor, start: torch.Tensor, *,
@@ -122,7 +139,7 @@ def cache_write(cache: PagedCache, key: torch.Tensor, value: torch.Tensor, table
     ``select`` [B, R] int32: row r is token select[b, r] of ``key`` and ``value``, as for the accepted ones of a drafted tree.
     A quantised cache's rows get the least power of two as scale that brings them into the codes' range.
     """
-    fmt, dev, sh, strides = _pages(cache)
+    fmt, dev, sh, strides, places = _pages(cache)
     _no_gradient(key, value)
     if key.dim() != 4:
         raise ValueError(f"key must be [B, T, heads, D], got {tuple(key.shape)}")
@@ -141,10 +158,8 @@ def cache_write(cache: PagedCache, key: torch.Tensor, value: torch.Tensor, table
     width = table.shape[1]
     p = _problem(B, R, N, N, D, T, sh[0], sh[1], width, width * sh[1], *strides, table.stride(0), *_NONE3,
                           *key.stride()[:3], *value.stride()[:3], 0, 0, 0 if select is None else select.stride(0))
-    with on_device(dev):
-        _lib.check(_lib.lib().msda_cache_write(
-            dt, fmt, p, ptr(key), ptr(value), ptr(table), ptr(start), ptr(counts), ptr(select), ptr(cache.key),
-            ptr(cache.value), ptr(cache.key_scale), ptr(cache.value_scale), stream(dev)))
+    _call(_lib.lib().msda_cache_write, dev, dt, fmt, p, key.data_ptr(), value.data_ptr(), table.data_ptr(), start.data_ptr(),
+          _address(counts), _address(select), *places)
     return cache
 
 
@@ -152,7 +167,7 @@ def cache_read(cache: PagedCache, table: torch.Tensor, lengths: torch.Tensor, ro
                dtype: Optional[torch.dtype] = None) -> Tuple[torch.Tensor, torch.Tensor]:
     """(key, value) [B, rows, N, D]: the first ``rows`` tokens of each sequence, zeros from ``lengths`` [B] (int32) on (C ABI
     ``msda_cache_read``).  ``dtype``: that of the result for a quantised cache (bfloat16 if None)."""
-    fmt, dev, sh, strides = _pages(cache)
+    fmt, dev, sh, strides, places = _pages(cache)
     if dtype is None:
         dtype = cache.key.dtype if fmt == _lib.CACHE_SAME else torch.bfloat16
     dt = _float_dtype(dtype, fmt, cache)
@@ -164,10 +179,8 @@ def cache_read(cache: PagedCache, table: torch.Tensor, lengths: torch.Tensor, ro
     value = torch.empty_like(key)
     p = _problem(B, rows, sh[2], sh[2], sh[3], rows, sh[0], sh[1], width, width * sh[1], *strides,
                           table.stride(0), *_NONE3, *_NONE3, *_NONE3, 0, 0, 0)
-    with on_device(dev):
-        _lib.check(_lib.lib().msda_cache_read(
-            dt, fmt, p, ptr(cache.key), ptr(cache.value), ptr(cache.key_scale), ptr(cache.value_scale), ptr(table),
-            ptr(lengths), ptr(key), ptr(value), stream(dev)))
+    _call(_lib.lib().msda_cache_read, dev, dt, fmt, p, *places, table.data_ptr(), lengths.data_ptr(), key.data_ptr(),
+          value.data_ptr())
     return key, value
 
 
@@ -185,7 +198,7 @@ def cache_attention(query: torch.Tensor, cache: PagedCache, table: torch.Tensor,
     and lse = -inf.  ``scale``: 1 / sqrt(D) if None.  ``longest``: a bound on the lengths that plans the launch (the table's
     width if None).
     """
-    fmt, dev, sh, strides = _pages(cache)
+    fmt, dev, sh, strides, places = _pages(cache)
     _no_gradient(query, key, value)
     if query.dim() != 4:
         raise ValueError(f"query must be [B, T, heads, D], got {tuple(query.shape)}")
@@ -227,12 +240,11 @@ def cache_attention(query: torch.Tensor, cache: PagedCache, table: torch.Tensor,
     out = torch.empty((B, T, M * D), dtype=query.dtype, device=dev)
     lse = torch.empty((B, M, T), dtype=torch.float32, device=dev)
     lib = _lib.lib()
-    workspace, n = workspace_of(lib.msda_cache_attention_workspace_size(dt, fmt, p), workspace, dev)
+    need = lib.msda_cache_attention_workspace_size(dt, fmt, p)
+    workspace, n = workspace_of(need, workspace, dev) if need or workspace is not None else (None, 0)
     if scale is None:
         scale = 1.0 / math.sqrt(D)
-    with on_device(dev):
-        _lib.check(lib.msda_cache_attention(
-            dt, fmt, p, float(scale), ptr(query), ptr(cache.key), ptr(cache.value), ptr(cache.key_scale),
-            ptr(cache.value_scale), ptr(table), ptr(lengths), ptr(key), ptr(value), ptr(mask), ptr(counts), ptr(out),
-            ptr(lse), ptr(workspace), n, stream(dev)))
+    _call(lib.msda_cache_attention, dev, dt, fmt, p, float(scale), query.data_ptr(), *places, table.data_ptr(),
+          lengths.data_ptr(), _address(key), _address(value), _address(mask), _address(counts), out.data_ptr(),
+          lse.data_ptr(), _address(workspace), n)
     return out, lse

@@ -524,17 +524,20 @@ bool tma_strides(const int64_t* st, int64_t a, int64_t b, int64_t c, int64_t es)
     return true;
 }
 
-// The tensor-core kernel's row tiles: 16-bit queries with more rows a key head than the mma.sync kernel has in a tile.
+// The tensor-core kernel's row tiles: 16-bit queries with more rows a key head than the mma.sync kernel has in a tile (32 rows there
+// took two: 8 x 16384 tokens, 4 key heads of 128: bf16 66 us against 60 here, e4m3 85 against 70; 16 rows 52 and 45).  Two row tiles a
+// block where one does not hold the rows, unquantised: keys are then read and multiplied for both.  With codes two row tiles leave too
+// few registers to convert a tile in its time (256 rows of 64 channels over 16384 tokens: 137 us against 126 as two units).
 int tc_tiles(msda_dtype dt, int format, const msda_cache_problem* p, int64_t rows) {
     const int64_t G = p->M / p->N, es = format == MSDA_CACHE_SAME ? 2 : 1;
-    if (dt == MSDA_F32 || rows <= 32 || G > msda::kTcRows) return 0;
+    if (dt == MSDA_F32 || rows <= 16 || G > msda::kTcRows) return 0;
     if (!tma_strides(p->query_stride, p->B, p->T, p->M, 2 * G) || !tma_strides(p->cache_key_stride, p->pages, p->page, p->N, es) ||
         !tma_strides(p->cache_value_stride, p->pages, p->page, p->N, es))
         return 0;
     if (format == MSDA_CACHE_SAME && p->source > 0 &&
         (!tma_strides(p->key_stride, p->B, p->source, p->N, 2) || !tma_strides(p->value_stride, p->B, p->source, p->N, 2)))
         return 0;
-    return rows > msda::kTcRows / G * G ? 2 : 1;
+    return format == MSDA_CACHE_SAME && rows > msda::kTcRows / G * G ? 2 : 1;
 }
 
 CachePlan plan_of(msda_dtype dt, int format, const msda_cache_problem* p) {

@@ -186,7 +186,8 @@ struct CacheWalk {
     }
 
     // Starts the copies of step i, and reads the bytes of its scales (lane: key); which groups of 16 keys are there.
-    __device__ __forceinline__ void issue(int i, uint32_t& bytes, uint32_t& there) {
+    // (The bytes stay untouched until their step comes: any arithmetic would wait for them here.)
+    __device__ __forceinline__ void issue(int i, uint32_t& k_byte, uint32_t& v_byte, uint32_t& there) {
         const uint32_t dst = cache_smem(ring) + (uint32_t)(i % STAGES) * kStage;
         const int row0 = lane / CH, chunk = lane % CH;  // a row takes CH lanes, or each lane CH / 32 chunks of it
 #pragma unroll 1
@@ -212,8 +213,8 @@ struct CacheWalk {
                 if constexpr (kCodes) {
                     const int row = lane - g * 16;
                     if ((unsigned)row < 16u && row < left) {
-                        bytes = a.c.ks[p * a.c.ks_sp + (in_page + row) * a.c.ks_st + u.n * a.c.ks_sh];
-                        bytes |= (uint32_t)a.c.vs[p * a.c.vs_sp + (in_page + row) * a.c.vs_st + u.n * a.c.vs_sh] << 8;
+                        k_byte = a.c.ks[p * a.c.ks_sp + (in_page + row) * a.c.ks_st + u.n * a.c.ks_sh];
+                        v_byte = a.c.vs[p * a.c.vs_sp + (in_page + row) * a.c.vs_st + u.n * a.c.vs_sh];
                     }
                 }
             } else {
@@ -387,7 +388,7 @@ struct CacheWalk {
         }
     }
 
-    __device__ __forceinline__ void compute(int i, uint32_t bytes, uint32_t there, CacheState<DP, MT>& z) {
+    __device__ __forceinline__ void compute(int i, uint32_t k_byte, uint32_t v_byte, uint32_t there, CacheState<DP, MT>& z) {
         const unsigned char* k = ring + (i % STAGES) * kStage;
         const unsigned char* v = k + KS * RB;
         const int g = lane >> 2, c = lane & 3;
@@ -395,8 +396,7 @@ struct CacheWalk {
         scores(k, s);
         float vs[NT][2];  // scales of the values of the keys 8 j + 2 c and the next
         if constexpr (kCodes) {
-            const uint32_t mine = (bytes >> 8) == 255u ? 0u : bytes >> 8;
-            const uint32_t top = __reduce_max_sync(0xffffffffu, mine);
+            const uint32_t top = __reduce_max_sync(0xffffffffu, v_byte == 255u ? 0u : v_byte);
             if (top > z.top) {
                 const float f = z.top + 126 < top ? 0.f : cache_scale(127 + z.top - top);
                 z.top = top;
@@ -407,7 +407,7 @@ struct CacheWalk {
 #pragma unroll
                         for (int e = 0; e < 4; ++e) z.o[t][d][e] *= f;
             }
-            const uint32_t pair = bytes | (__shfl_down_sync(0xffffffffu, bytes, 1) << 16);
+            const uint32_t bytes = k_byte | (v_byte << 8), pair = bytes | (__shfl_down_sync(0xffffffffu, bytes, 1) << 16);
 #pragma unroll
             for (int j = 0; j < NT; ++j) {
                 const uint32_t two = __shfl_sync(0xffffffffu, pair, j * 8 + 2 * c);
@@ -525,9 +525,9 @@ struct CacheWalk {
             here = cache_page_of(a.c, here);
             have = 0;
         }
-        uint32_t bytes[STAGES], there[STAGES];  // of the steps in flight, the nearest first
+        uint32_t kb[STAGES], vb[STAGES], there[STAGES];  // of the steps in flight, the nearest first
 #pragma unroll
-        for (int j = 0; j < STAGES; ++j) bytes[j] = there[j] = 0;
+        for (int j = 0; j < STAGES; ++j) kb[j] = vb[j] = there[j] = 0;
         // one place for the copies and one for the products, the copies STAGES - 1 steps ahead
 #pragma unroll 1
         for (int i = 1 - STAGES; i < steps; ++i) {
@@ -537,16 +537,16 @@ struct CacheWalk {
             } else {
                 __syncwarp();
             }
-            bytes[STAGES - 1] = there[STAGES - 1] = 0;
-            if (i + STAGES - 1 < steps) issue(i + STAGES - 1, bytes[STAGES - 1], there[STAGES - 1]);
+            kb[STAGES - 1] = vb[STAGES - 1] = there[STAGES - 1] = 0;
+            if (i + STAGES - 1 < steps) issue(i + STAGES - 1, kb[STAGES - 1], vb[STAGES - 1], there[STAGES - 1]);
             cache_commit();
             if constexpr (STAGES == 1) {
                 cache_wait<0>();
                 __syncwarp();
             }
-            if (i >= 0) compute(i, bytes[0], there[0], z);
+            if (i >= 0) compute(i, kb[0], vb[0], there[0], z);
 #pragma unroll
-            for (int j = 0; j + 1 < STAGES; ++j) bytes[j] = bytes[j + 1], there[j] = there[j + 1];
+            for (int j = 0; j + 1 < STAGES; ++j) kb[j] = kb[j + 1], vb[j] = vb[j + 1], there[j] = there[j + 1];
         }
         cache_wait<0>();
         __syncwarp();
@@ -763,32 +763,33 @@ static cudaError_t cache_rows_go(const CacheArgs& a, int grid, cudaStream_t st) 
     return cudaGetLastError();
 }
 
-#define MSDA_CACHE_ROWS_BY(format, D, two, f, ...)                                                               \
-    do {                                                                                                         \
-        const int key = ((format) << 2) | ((D) > 64 ? 2 : 0) | ((two) ? 1 : 0);                                  \
-        switch (key) {                                                                                           \
-            case 0: return f<T, kCacheSame, 64, 1>(__VA_ARGS__);                                                 \
-            case 1: return f<T, kCacheSame, 64, 2>(__VA_ARGS__);                                                 \
-            case 2: return f<T, kCacheSame, 128, 1>(__VA_ARGS__);                                                \
-            case 3: return f<T, kCacheSame, 128, sizeof(T) == 4 ? 1 : 2>(__VA_ARGS__);                           \
-            case 4: return f<T, kCacheE4m3, 64, 1>(__VA_ARGS__);                                                 \
-            case 5: return f<T, kCacheE4m3, 64, 2>(__VA_ARGS__);                                                 \
-            case 6: return f<T, kCacheE4m3, 128, 1>(__VA_ARGS__);                                                \
-            case 7: return f<T, kCacheE4m3, 128, sizeof(T) == 4 ? 1 : 2>(__VA_ARGS__);                           \
-            case 8: return f<T, kCacheInt8, 64, 1>(__VA_ARGS__);                                                 \
-            case 9: return f<T, kCacheInt8, 64, 2>(__VA_ARGS__);                                                 \
-            case 10: return f<T, kCacheInt8, 128, 1>(__VA_ARGS__);                                               \
-            default: return f<T, kCacheInt8, 128, sizeof(T) == 4 ? 1 : 2>(__VA_ARGS__);                          \
-        }                                                                                                        \
+// Tiles of 32 rows only in binary32 up to 64 channels: 16 bits have the tensor-core kernel there, wider rows no registers.
+#define MSDA_CACHE_ROWS_BY(format, D, rows, f, ...)                                                      \
+    do {                                                                                                 \
+        if constexpr (sizeof(T) == 4) {                                                                  \
+            if ((rows) > 16 && (D) <= 64) {                                                              \
+                if ((format) == kCacheSame) return f<T, kCacheSame, 64, 2>(__VA_ARGS__);                 \
+                if ((format) == kCacheE4m3) return f<T, kCacheE4m3, 64, 2>(__VA_ARGS__);                 \
+                return f<T, kCacheInt8, 64, 2>(__VA_ARGS__);                                             \
+            }                                                                                            \
+        }                                                                                                \
+        if ((D) <= 64) {                                                                                 \
+            if ((format) == kCacheSame) return f<T, kCacheSame, 64, 1>(__VA_ARGS__);                     \
+            if ((format) == kCacheE4m3) return f<T, kCacheE4m3, 64, 1>(__VA_ARGS__);                     \
+            return f<T, kCacheInt8, 64, 1>(__VA_ARGS__);                                                 \
+        }                                                                                                \
+        if ((format) == kCacheSame) return f<T, kCacheSame, 128, 1>(__VA_ARGS__);                        \
+        if ((format) == kCacheE4m3) return f<T, kCacheE4m3, 128, 1>(__VA_ARGS__);                        \
+        return f<T, kCacheInt8, 128, 1>(__VA_ARGS__);                                                    \
     } while (0)
 
 template <typename T>
 CacheRowsShape cache_rows_shape(int format, int D, int rows) {
-    MSDA_CACHE_ROWS_BY(format, D, rows > 16, cache_rows_shape_of);
+    MSDA_CACHE_ROWS_BY(format, D, rows, cache_rows_shape_of);
 }
 template <typename T>
 cudaError_t launch_cache_rows(const CacheArgs& a, int format, int grid, cudaStream_t st) {
-    MSDA_CACHE_ROWS_BY(format, a.D, a.rows > 16, cache_rows_go, a, grid, st);
+    MSDA_CACHE_ROWS_BY(format, a.D, a.rows, cache_rows_go, a, grid, st);
 }
 
 }  // namespace msda

@@ -45,15 +45,16 @@ struct CacheTcRange {
 template <int F, int NQ, int NC>
 struct CacheTcCfg {
     static constexpr bool kCodes = F != kCacheSame;
-    static constexpr int kStages = NC == 1 ? (kCodes ? 6 : 8) : (kCodes && NQ == 2) ? 3 : 4;  // ring of K and V operand tiles
+    static_assert(!kCodes || NQ == 1, "codes: one row tile a block");
+    static constexpr int kStages = NC == 1 ? (kCodes ? 6 : 8) : 4;  // ring of K and V operand tiles
     static constexpr int kRaw = !kCodes ? 0 : NC == 1 ? 6 : 4;                                  // ring of tiles of codes
-    static constexpr int kThreads = NQ * 128 + 128 + (kCodes ? 128 : 0);
+    static constexpr int kThreads = NQ * 128 + 128 + (kCodes ? 256 : 0);
     static constexpr uint32_t kTileBytes = NC * kTcTile, kRawBytes = NC * 64 * 128;
-    // registers of a thread of the warpgroups on the scores, of the one that issues and of the one that converts: the launch
-    // has 168 a thread with three warpgroups, 128 with four, 255 with two (no split there)
-    static constexpr int kUp = NQ == 1 ? (kCodes ? 232 : 0) : kCodes ? 192 : 208;
-    static constexpr int kDown = NQ == 1 ? 136 : kCodes ? 56 : 88, kConvert = NQ == 1 ? 136 : 72;
-    static_assert(kUp == 0 || NQ * kUp + kDown + (kCodes ? kConvert : 0) <= (kThreads == 512 ? 512 : 504), "more registers than the launch has");
+    // Registers of a thread of the warpgroups on the scores, of the one that issues and of the two that convert: with codes the launch
+    // of four warpgroups has 128 a thread, unquantised with two row tiles 168 of three; with one row tile 255, and no split.
+    static constexpr int kUp = kCodes ? 208 : NQ == 1 ? 0 : 208, kDown = kCodes ? 56 : 88, kConvert = 120;
+    static_assert(!kCodes || kUp + kDown + 2 * kConvert <= 512, "more registers than the launch has");
+    static_assert(kCodes || NQ == 1 || NQ * kUp + kDown <= 504, "more registers than the launch has");
     // tensor memory: S (128 columns a row tile), P (64), O (64 or 128); two row tiles of up to 128 channels leave no room
     // for P: it lies over S, and the next S waits until P is used up
     static constexpr bool kOwnP = NC == 1 || NQ == 1;
@@ -65,12 +66,12 @@ struct CacheTcCfg {
 
 struct CacheTcSync {
     uint64_t full[8], empty[8], raw_full[6], raw_empty[6];
-    uint64_t cleared[8], q_full, q_empty, tops_full, s_full[2], s_free[2], p_full[2], pv_done[2], turn;
+    uint64_t cleared[8], q_full, q_empty, tops_full[2], s_full[2], s_free[2], p_full[2], pv_done[2], turn;
     uint32_t tmem, abort;
     uint32_t words[8][4];    // a tile's keys that are there
     float k_scale[8];        // 8 bits: scale of a tile's K, and the byte of that of its V
     uint32_t v_top[8];
-    uint32_t tops[2][4];
+    alignas(16) uint32_t tops[2][2][4];  // of each warpgroup that converts, by turns: its warps' largest bytes
 };
 
 __device__ __forceinline__ void tc_tma_4d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int c0, int c1, int c2, int c3) {
@@ -136,9 +137,9 @@ __global__ void __launch_bounds__(CacheTcCfg<F, NQ, NC>::kThreads, 1)
             }
             tc_bar_init(tc_smem(&sy.q_full), OWN_Q ? NQ * 4 : 1);
             tc_bar_init(tc_smem(&sy.q_empty), NQ);
-            tc_bar_init(tc_smem(&sy.tops_full), 4);
             tc_bar_init(tc_smem(&sy.turn), 1);
             for (int i = 0; i < 2; ++i) {
+                tc_bar_init(tc_smem(&sy.tops_full[i]), 4);
                 tc_bar_init(tc_smem(&sy.s_full[i]), 1);
                 tc_bar_init(tc_smem(&sy.s_free[i]), 4);
                 tc_bar_init(tc_smem(&sy.p_full[i]), 4);
@@ -529,6 +530,8 @@ __global__ void __launch_bounds__(CacheTcCfg<F, NQ, NC>::kThreads, 1)
                 auto next_s = [&](int gi) {
                     const int idx = 2 * gi, st = idx % ST;
                     if (!tc_bar_wait(tc_smem(&sy.full[st]), (idx / ST) & 1, abort, err)) return false;
+                    // the scale of the tile's values, which the scores' threads read, comes from another warpgroup than that of its keys
+                    if (CODES && !tc_bar_wait(tc_smem(&sy.full[(idx + 1) % ST]), ((idx + 1) / ST) & 1, abort, err)) return false;
                     if (Cfg::kOwnP && gi > 0 && !tc_bar_wait(tc_smem(&sy.s_free[t]), (gi - 1) & 1, abort, err)) return false;
                     tc_fence_after();
                     product_s(st);
@@ -588,130 +591,126 @@ __global__ void __launch_bounds__(CacheTcCfg<F, NQ, NC>::kThreads, 1)
         ok = !*abort;
     } else if constexpr (CODES) {
         tc_regs_down<Cfg::kConvert>();
-        // ---- codes to f16 operands: row `row` of each tile ----
-        const int cw = warp - NQ * 4 - 4, row = cw * 32 + lane;
+        // ---- codes to f16 operands: row `row` of each tile, one warpgroup for K and one for V (one for both took 2.2 us a tile of 128
+        // channels, these 1.4) ----
+        const int kv = (warp - NQ * 4 - 4) >> 2, cw = (warp - NQ * 4 - 4) & 3, row = cw * 32 + lane;
         int g0 = 0, r0 = 0;
         cache_segments(a, start, false, [&](const CacheSegment& sg) {
             const CacheUnit& u = sg.u;
+            const uint8_t* scales = kv ? a.c.vs + u.n * a.c.vs_sh : a.c.ks + u.n * a.c.ks_sh;
+            const long long s_page = kv ? a.c.vs_sp : a.c.ks_sp, s_token = kv ? a.c.vs_st : a.c.ks_st;
+            const T* fresh = kv ? static_cast<const T*>(a.nv) + u.b * a.nv_sb + u.n * a.nv_sh : static_cast<const T*>(a.nk) + u.b * a.nk_sb + u.n * a.nk_sh;
+            const long long f_token = kv ? a.nv_st : a.nk_st;
             auto entry_of = [&](int i) {  // of this row at tile sg.first + i
                 const int token = (sg.first + i) * kTcRows + row;
                 return i < sg.n && sg.first + i < u.cache_tiles && token < u.length ? cache_entry(a.c, u.b, token) : kCacheNoPage;
             };
-            auto bytes_of = [&](int i, int entry) {  // its bytes; bit 16: there is such a row
-                const int page = (unsigned)entry < (unsigned)a.c.pages ? entry : -1;  // the warp that copies tells of bad ones
-                if (page < 0) return 0u;
-                const int place = ((sg.first + i) * kTcRows + row) & (a.c.page - 1);
-                return 0x10000u | a.c.ks[page * a.c.ks_sp + place * a.c.ks_st + u.n * a.c.ks_sh] |
-                       ((uint32_t)a.c.vs[page * a.c.vs_sp + place * a.c.vs_st + u.n * a.c.vs_sh] << 8);
+            // its byte, untouched until its tile comes (any arithmetic would wait for it here)
+            uint32_t ahead = 0;
+            bool here = false;
+            auto read_byte = [&](int i, int entry) {
+                here = (unsigned)entry < (unsigned)a.c.pages;  // the warp that copies tells of bad ones
+                const int page = here ? entry : 0, place = ((sg.first + i) * kTcRows + row) & (a.c.page - 1);
+                ahead = 0;
+                if (here) ahead = scales[page * s_page + place * s_token];
             };
             int entry = entry_of(0), entry1 = entry_of(1), entry2 = entry_of(2);
-            uint32_t bytes = bytes_of(0, entry);
+            read_byte(0, entry);
 #pragma unroll 1
             for (int i = 0; i < sg.n; ++i) {
                 const int gi = g0 + i, tile = sg.first + i;
                 const bool tail = tile >= u.cache_tiles;
                 const int j = (tile - u.cache_tiles) * kTcRows + row;  // new token (tail)
-                const uint32_t now = bytes;
-                bytes = bytes_of(i + 1, entry1);
+                bool there = here;
+                uint32_t byte = ahead;  // of a new token's row: the byte that brings its largest value to 2^8 or more
+                read_byte(i + 1, entry1);
                 entry1 = entry2, entry2 = entry_of(i + 3);
-                bool there;
-                uint32_t kb, vb;  // of a new token's row: the byte that brings its largest value to 2^8 or more
-                if (!tail) {
-                    there = now >> 16, kb = now & 255u, vb = (now >> 8) & 255u;
-                } else {
+                if (tail) {
                     there = j < sg.tail_keys;
-                    kb = vb = 0;
+                    uint32_t top = 0;
                     if (there) {
-                        const T* p[2] = {static_cast<const T*>(a.nk) + u.b * a.nk_sb + j * a.nk_st + u.n * a.nk_sh,
-                                         static_cast<const T*>(a.nv) + u.b * a.nv_sb + j * a.nv_st + u.n * a.nv_sh};
-#pragma unroll
-                        for (int kv = 0; kv < 2; ++kv) {
-                            uint32_t top = 0;
-                            for (int d = 0; d < a.D; d += 8) {
-                                const uint4 x = *reinterpret_cast<const uint4*>(p[kv] + d);
-                                const uint32_t mm = 0x7fff7fffu;
-                                top = __vmaxu2(top, __vmaxu2(__vmaxu2(x.x & mm, x.y & mm), __vmaxu2(x.z & mm, x.w & mm)));
-                            }
-                            top = max(top & 0xffffu, top >> 16);
-                            const float x = BF16 ? __uint_as_float(top << 16) : __half2float(__ushort_as_half((unsigned short)top));
-                            const int e = (int)(__float_as_uint(x) >> 23);
-                            const uint32_t byte = e == 255 ? 255u : (uint32_t)max(e - 8, 27);
-                            if (kv) vb = byte;
-                            else kb = byte;
+#pragma unroll 1
+                        for (int d = 0; d < a.D; d += 8) {
+                            const uint4 y = *reinterpret_cast<const uint4*>(fresh + j * f_token + d);
+                            const uint32_t mm = 0x7fff7fffu;
+                            top = __vmaxu2(top, __vmaxu2(__vmaxu2(y.x & mm, y.y & mm), __vmaxu2(y.z & mm, y.w & mm)));
                         }
                     }
+                    top = max(top & 0xffffu, top >> 16);
+                    const float y = BF16 ? __uint_as_float(top << 16) : __half2float(__ushort_as_half((unsigned short)top));
+                    const int e = (int)(__float_as_uint(y) >> 23);
+                    byte = e == 255 ? 255u : (uint32_t)max(e - 8, 27);
                 }
-                // the tile's largest scales
-                const uint32_t kt = __reduce_max_sync(0xffffffffu, there && kb != 255u ? kb : 0u);
-                const uint32_t vt = __reduce_max_sync(0xffffffffu, there && vb != 255u ? vb : 0u);
+                // the tile's largest scale, and where it is read
+                const uint32_t mine = __reduce_max_sync(0xffffffffu, there && byte != 255u ? byte : 0u);
                 if (lane == 0) {
-                    sy.tops[gi & 1][cw] = kt | (vt << 8);
-                    tc_bar_arrive(tc_smem(&sy.tops_full));
+                    sy.tops[kv][gi & 1][cw] = mine;
+                    tc_bar_arrive(tc_smem(&sy.tops_full[kv]));
                 }
-                if (!tc_bar_wait(tc_smem(&sy.tops_full), gi & 1, abort, err)) return false;
-                uint32_t k_top = 0, v_top = 0;
-#pragma unroll
-                for (int x = 0; x < 4; ++x) {
-                    const uint32_t y = sy.tops[gi & 1][x];
-                    k_top = max(k_top, y & 255u), v_top = max(v_top, y >> 8);
+                if (!tc_bar_wait(tc_smem(&sy.tops_full[kv]), gi & 1, abort, err)) return false;
+                const uint4 all = *reinterpret_cast<const uint4*>(sy.tops[kv][gi & 1]);
+                const uint32_t most = max(max(all.x, all.y), max(all.z, all.w));
+                if (row == 0) {
+                    if (kv) sy.v_top[gi & 7] = most;
+                    else sy.k_scale[gi & 7] = cache_scale(most);
                 }
-                if (row == 0) sy.k_scale[gi & 7] = cache_scale(k_top), sy.v_top[gi & 7] = v_top;
-#pragma unroll
-                for (int kv = 0; kv < 2; ++kv) {
-                    const int idx = 2 * gi + kv, st = idx % ST;
-                    const uint32_t byte = kv ? vb : kb, most = kv ? v_top : k_top;
-                    unsigned char* to = ring + st * Cfg::kTileBytes + row * 128;
+                const int idx = 2 * gi + kv, st = idx % ST;
+                unsigned char* to = ring + st * Cfg::kTileBytes + row * 128;
                     if (!tail) {
                         const int ri = 2 * r0 + kv, rs = ri % Cfg::kRaw;
                         if (!tc_bar_wait(tc_smem(&sy.raw_full[rs]), (ri / Cfg::kRaw) & 1, abort, err)) return false;
                         if (idx >= ST && !tc_bar_wait(tc_smem(&sy.empty[st]), (idx / ST - 1) & 1, abort, err)) return false;
                         const unsigned char* from = raw + rs * Cfg::kRawBytes + row * (NC * 64);
-                        // 2^(byte - most) in f16; a row that held no numbers: NaN; none or byte 0: zeros
-                        const float f = byte == 255u ? __uint_as_float(0x7fffffffu) : byte == 0u || byte + 126u < most ? 0.f : cache_scale(127u + byte - most);
+                        // 2^(byte - most) in f16; a row that held no numbers: NaN; byte 0: zeros
+                        const float f = byte == 255u ? __uint_as_float(0x7fffffffu)
+                                                        : byte == 0u || byte + 126u < most ? 0.f : cache_scale(127u + byte - most);
                         const __half2 scale = __half2half2(__float2half_rn(f));
                         const __half2 off = __hmul2(scale, __half2half2(__ushort_as_half(0xe480)));  // -1152
-#pragma unroll 2
-                        for (int c = 0; c < NC * 4; ++c) {  // 16 codes
-                            uint32_t p[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-                            if (there && c * 16 < a.D) {
-                                const uint4 x = *reinterpret_cast<const uint4*>(from + ((NC == 2 ? c ^ (row & 7) : c ^ ((row >> 1) & 3)) << 4));
-                                const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll 1
+                        for (int c0 = 0; c0 < NC * 4; c0 += 4) {  // 64 codes at a time, their loads first
+                            uint4 y[4];
+#pragma unroll
+                            for (int c = 0; c < 4; ++c)
+                                y[c] = *reinterpret_cast<const uint4*>(from + ((NC == 2 ? (c0 + c) ^ (row & 7) : c ^ ((row >> 1) & 3)) << 4));
+                            unsigned char* at = to + (c0 / 4) * kTcTile;
+#pragma unroll
+                            for (int c = 0; c < 4; ++c) {
+                                const uint32_t w[4] = {y[c].x, y[c].y, y[c].z, y[c].w};
+                                uint32_t p[8];
 #pragma unroll
                                 for (int k = 0; k < 4; ++k) {
+                                    __half2 y0, y1;
                                     if constexpr (F == kCacheE4m3) {
                                         uint32_t lo, hi;
                                         cache_four_f16<F>(w[k], lo, hi);
-                                        const __half2 y0 = __hmul2(*reinterpret_cast<const __half2*>(&lo), scale), y1 = __hmul2(*reinterpret_cast<const __half2*>(&hi), scale);
-                                        p[2 * k] = *reinterpret_cast<const uint32_t*>(&y0), p[2 * k + 1] = *reinterpret_cast<const uint32_t*>(&y1);
+                                        y0 = __hmul2(*reinterpret_cast<const __half2*>(&lo), scale), y1 = __hmul2(*reinterpret_cast<const __half2*>(&hi), scale);
                                     } else {  // (1024 + u) s - 1152 s, exact
                                         const uint32_t v = w[k] ^ 0x80808080u, lo = __byte_perm(v, 0x64646464u, 0x4140), hi = __byte_perm(v, 0x64646464u, 0x4342);
-                                        const __half2 y0 = __hfma2(*reinterpret_cast<const __half2*>(&lo), scale, off), y1 = __hfma2(*reinterpret_cast<const __half2*>(&hi), scale, off);
-                                        p[2 * k] = *reinterpret_cast<const uint32_t*>(&y0), p[2 * k + 1] = *reinterpret_cast<const uint32_t*>(&y1);
+                                        y0 = __hfma2(*reinterpret_cast<const __half2*>(&lo), scale, off), y1 = __hfma2(*reinterpret_cast<const __half2*>(&hi), scale, off);
                                     }
+                                    p[2 * k] = there ? *reinterpret_cast<const uint32_t*>(&y0) : 0u;  // behind the last row: zeros, whatever lies there
+                                    p[2 * k + 1] = there ? *reinterpret_cast<const uint32_t*>(&y1) : 0u;
                                 }
+                                *reinterpret_cast<uint4*>(at + (((2 * c) ^ (row & 7)) << 4)) = make_uint4(p[0], p[1], p[2], p[3]);
+                                *reinterpret_cast<uint4*>(at + (((2 * c + 1) ^ (row & 7)) << 4)) = make_uint4(p[4], p[5], p[6], p[7]);
                             }
-                            unsigned char* at = to + (c / 4) * kTcTile;
-                            const int ch = (c & 3) * 2;
-                            *reinterpret_cast<uint4*>(at + ((ch ^ (row & 7)) << 4)) = make_uint4(p[0], p[1], p[2], p[3]);
-                            *reinterpret_cast<uint4*>(at + (((ch + 1) ^ (row & 7)) << 4)) = make_uint4(p[4], p[5], p[6], p[7]);
                         }
                         tc_fence_async();
                         __syncwarp();
                         if (lane == 0) {
-                            tc_bar_arrive(tc_smem(&sy.raw_empty[rs]));
                             tc_bar_arrive(tc_smem(&sy.full[st]));
+                            tc_bar_arrive(tc_smem(&sy.raw_empty[rs]));
                         }
                     } else {
                         if (idx >= ST && !tc_bar_wait(tc_smem(&sy.empty[st]), (idx / ST - 1) & 1, abort, err)) return false;
-                        const T* p = kv ? static_cast<const T*>(a.nv) + u.b * a.nv_sb + j * a.nv_st + u.n * a.nv_sh
-                                        : static_cast<const T*>(a.nk) + u.b * a.nk_sb + j * a.nk_st + u.n * a.nk_sh;
+                        const T* p = fresh + j * f_token;
                         const float f = most == 0u ? 0.f : cache_scale(254u - most);
 #pragma unroll 1
                         for (int d = 0; d < NC * 64; d += 8) {
                             uint4 y = make_uint4(0, 0, 0, 0);
                             if (there && d < a.D) {
-                                const uint4 x = *reinterpret_cast<const uint4*>(p + d);
-                                const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+                                const uint4 v4 = *reinterpret_cast<const uint4*>(p + d);
+                                const uint32_t w[4] = {v4.x, v4.y, v4.z, v4.w};
                                 uint32_t z[4];
 #pragma unroll
                                 for (int k = 0; k < 4; ++k) {
@@ -728,7 +727,6 @@ __global__ void __launch_bounds__(CacheTcCfg<F, NQ, NC>::kThreads, 1)
                         __syncwarp();
                         if (lane == 0) tc_bar_arrive(tc_smem(&sy.full[st]));
                     }
-                }
                 if (!tail) ++r0;
             }
             g0 += sg.n;
@@ -805,8 +803,10 @@ cudaError_t tc_go(const CacheArgs& a, int grid, cudaStream_t st) {
 
 template <bool BF16, int F>
 cudaError_t launch_cache_tc(const CacheArgs& a, int nq, int grid, cudaStream_t st) {
-    if (a.D > 64) return nq == 2 ? tc_go<BF16, F, 2, 2>(a, grid, st) : tc_go<BF16, F, 1, 2>(a, grid, st);
-    return nq == 2 ? tc_go<BF16, F, 2, 1>(a, grid, st) : tc_go<BF16, F, 1, 1>(a, grid, st);
+    if constexpr (F == kCacheSame) {
+        if (nq == 2) return a.D > 64 ? tc_go<BF16, F, 2, 2>(a, grid, st) : tc_go<BF16, F, 2, 1>(a, grid, st);
+    }
+    return a.D > 64 ? tc_go<BF16, F, 1, 2>(a, grid, st) : tc_go<BF16, F, 1, 1>(a, grid, st);
 }
 
 }  // namespace msda
