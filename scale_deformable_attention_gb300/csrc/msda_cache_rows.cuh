@@ -517,7 +517,9 @@ struct CacheWalk {
         }
     }
 
-    __device__ __forceinline__ void run(CacheState<DP, MT>& z) {
+    // `prepare`: what the block has to do before the first products, once its first copies are on their way.
+    template <typename Prepare>
+    __device__ __forceinline__ void run(CacheState<DP, MT>& z, Prepare prepare) {
         const int steps = cached + fresh;
         if (cached > 0) {
             here = group_entry(lane);
@@ -530,7 +532,7 @@ struct CacheWalk {
         for (int j = 0; j < STAGES; ++j) kb[j] = vb[j] = there[j] = 0;
         // one place for the copies and one for the products, the copies STAGES - 1 steps ahead
 #pragma unroll 1
-        for (int i = 1 - STAGES; i < steps; ++i) {
+        for (int i = 1 - STAGES; i < max(steps, 1); ++i) {
             if constexpr (STAGES > 1) {
                 cache_wait<(STAGES > 1 ? STAGES - 2 : 0)>();
                 __syncwarp();  // the step's copies of all lanes are there, and the stage of step i - 1 is read
@@ -544,7 +546,8 @@ struct CacheWalk {
                 cache_wait<0>();
                 __syncwarp();
             }
-            if (i >= 0) compute(i, kb[0], vb[0], there[0], z);
+            if (i == 0) prepare();
+            if (i >= 0 && i < steps) compute(i, kb[0], vb[0], there[0], z);
 #pragma unroll
             for (int j = 0; j + 1 < STAGES; ++j) kb[j] = kb[j + 1], vb[j] = vb[j + 1], there[j] = there[j + 1];
         }
@@ -596,57 +599,59 @@ __global__ void __launch_bounds__(kCacheWarps * 32, CacheRowsCfg<T, F, DP, MT>::
             head_of[threadIdx.x] = x - t * a.G;
         }
         __syncthreads();
-        // ---- codes: a power of two that brings a row's largest to 2^14 or more ----
-        if constexpr (CODES) {
+        auto prepare = [&] {
+            // ---- codes: a power of two that brings a row's largest to 2^14 or more ----
+            if constexpr (CODES) {
 #pragma unroll 1
-            for (int r = warp; r < R; r += kCacheWarps) {
-                const int t = token_of[r];
-                float top = 0.f;
-                if (t < u.count && lane * 4 < a.D) {
-                    float y[4];
-                    cache_four(query + t * a.q_st + head_of[r] * a.q_sh + lane * 4, y);
-                    top = fmaxf(fmaxf(fabsf(y[0]), fabsf(y[1])), fmaxf(fabsf(y[2]), fabsf(y[3])));
+                for (int r = warp; r < R; r += kCacheWarps) {
+                    const int t = token_of[r];
+                    float top = 0.f;
+                    if (t < u.count && lane * 4 < a.D) {
+                        float y[4];
+                        cache_four(query + t * a.q_st + head_of[r] * a.q_sh + lane * 4, y);
+                        top = fmaxf(fmaxf(fabsf(y[0]), fabsf(y[1])), fmaxf(fabsf(y[2]), fabsf(y[3])));
+                    }
+                    top = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top)));
+                    const int e = (int)(__float_as_uint(top) >> 23);  // 2^(e - 127) <= top
+                    const float by = e > 0 && e < 255 ? __uint_as_float((uint32_t)min(max(268 - e, 27), 227) << 23) : 1.f;
+                    if (lane == 0) {
+                        up[r] = by;
+                        factor[r] = fmaxf(a.c2 * (1.f / by), 1e-37f);  // a power of two: exact; never 0, which would make NaN of what is hidden
+                    }
                 }
-                top = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top)));
-                const int e = (int)(__float_as_uint(top) >> 23);  // 2^(e - 127) <= top
-                const float by = e > 0 && e < 255 ? __uint_as_float((uint32_t)min(max(268 - e, 27), 227) << 23) : 1.f;
-                if (lane == 0) {
-                    up[r] = by;
-                    factor[r] = fmaxf(a.c2 * (1.f / by), 1e-37f);  // a power of two: exact; never 0, which would make NaN of what is hidden
+                __syncthreads();
+            }
+            // ---- the queries' fragments: entry (tile t of 16, step s, lane) are the channels of lane % 4 at step s of rows lane / 4 and + 8 ----
+#pragma unroll 1
+            for (int x = threadIdx.x; x < MT * STEPS * 32; x += kCacheWarps * 32) {
+                const int ln = x & 31, s = (x >> 5) % STEPS, t = (x >> 5) / STEPS;
+                const int ch = Cfg::E * ((ln & 3) + 4 * (s / (Cfg::E / 4))) + 4 * (s % (Cfg::E / 4));
+                float y[2][4];
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int r = t * 16 + (ln >> 2) + 8 * h, tok = token_of[r];
+                    y[h][0] = y[h][1] = y[h][2] = y[h][3] = 0.f;
+                    if (tok < u.count && ch < a.D) cache_four(query + tok * a.q_st + head_of[r] * a.q_sh + ch, y[h]);
+                }
+                auto put = [&](uint4* to, auto product, float up0, float up1) {
+                    using Q = decltype(product);
+                    uint32_t f[4][Q::qp];
+                    cache_pieces<Q::bf16, Q::qp>(y[0][0] * up0, y[0][1] * up0, f[0]);
+                    cache_pieces<Q::bf16, Q::qp>(y[1][0] * up1, y[1][1] * up1, f[1]);
+                    cache_pieces<Q::bf16, Q::qp>(y[0][2] * up0, y[0][3] * up0, f[2]);
+                    cache_pieces<Q::bf16, Q::qp>(y[1][2] * up1, y[1][3] * up1, f[3]);
+#pragma unroll
+                    for (int p = 0; p < Q::qp; ++p) to[((p * MT + t) * STEPS + s) * 32 + ln] = make_uint4(f[0][p], f[1][p], f[2][p], f[3][p]);
+                };
+                if constexpr (CODES) {
+                    put(qf, P{}, up[t * 16 + (ln >> 2)], up[t * 16 + (ln >> 2) + 8]);
+                    if (a.nk) put(qt, PT{}, 1.f, 1.f);
+                } else {
+                    put(qf, P{}, 1.f, 1.f);
                 }
             }
             __syncthreads();
-        }
-        // ---- the queries' fragments: entry (tile t of 16, step s, lane) are the channels of lane % 4 at step s of rows lane / 4 and + 8 ----
-#pragma unroll 1
-        for (int x = threadIdx.x; x < MT * STEPS * 32; x += kCacheWarps * 32) {
-            const int ln = x & 31, s = (x >> 5) % STEPS, t = (x >> 5) / STEPS;
-            const int ch = Cfg::E * ((ln & 3) + 4 * (s / (Cfg::E / 4))) + 4 * (s % (Cfg::E / 4));
-            float y[2][4];
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int r = t * 16 + (ln >> 2) + 8 * h, tok = token_of[r];
-                y[h][0] = y[h][1] = y[h][2] = y[h][3] = 0.f;
-                if (tok < u.count && ch < a.D) cache_four(query + tok * a.q_st + head_of[r] * a.q_sh + ch, y[h]);
-            }
-            auto put = [&](uint4* to, auto product, float up0, float up1) {
-                using Q = decltype(product);
-                uint32_t f[4][Q::qp];
-                cache_pieces<Q::bf16, Q::qp>(y[0][0] * up0, y[0][1] * up0, f[0]);
-                cache_pieces<Q::bf16, Q::qp>(y[1][0] * up1, y[1][1] * up1, f[1]);
-                cache_pieces<Q::bf16, Q::qp>(y[0][2] * up0, y[0][3] * up0, f[2]);
-                cache_pieces<Q::bf16, Q::qp>(y[1][2] * up1, y[1][3] * up1, f[3]);
-#pragma unroll
-                for (int p = 0; p < Q::qp; ++p) to[((p * MT + t) * STEPS + s) * 32 + ln] = make_uint4(f[0][p], f[1][p], f[2][p], f[3][p]);
-            };
-            if constexpr (CODES) {
-                put(qf, P{}, up[t * 16 + (ln >> 2)], up[t * 16 + (ln >> 2) + 8]);
-                if (a.nk) put(qt, PT{}, 1.f, 1.f);
-            } else {
-                put(qf, P{}, 1.f, 1.f);
-            }
-        }
-        __syncthreads();
+        };
 
         CacheState<DP, MT> z;
         z.top = 0;
@@ -671,26 +676,24 @@ __global__ void __launch_bounds__(kCacheWarps * 32, CacheRowsCfg<T, F, DP, MT>::
             fresh = first_new < end ? (end - first_new + step_new - 1) / step_new : 0;
         }
         if constexpr (CODES) {
-            if (cached > 0) {
-                CacheWalk<T, F, DP, MT, Cfg::E, Cfg::EV, KS, Cfg::kStages> walk{a, u, my_ring, qf, factor, token_of, lane, first, cached, 0, 0, step, 0, 0, 0};
-                walk.run(z);
-                if (z.top != 0) {  // back to units of 1
-                    const float f = cache_scale(z.top);
+            CacheWalk<T, F, DP, MT, Cfg::E, Cfg::EV, KS, Cfg::kStages> walk{a, u, my_ring, qf, factor, token_of, lane, first, cached, 0, 0, step, 0, 0, 0};
+            walk.run(z, prepare);
+            if (z.top != 0) {  // back to units of 1
+                const float f = cache_scale(z.top);
 #pragma unroll
-                    for (int t = 0; t < MT; ++t)
+                for (int t = 0; t < MT; ++t)
 #pragma unroll
-                        for (int d = 0; d < DP / 8; ++d)
+                    for (int d = 0; d < DP / 8; ++d)
 #pragma unroll
-                            for (int e = 0; e < 4; ++e) z.o[t][d][e] *= f;
-                }
+                        for (int e = 0; e < 4; ++e) z.o[t][d][e] *= f;
             }
             if (fresh > 0) {
                 CacheWalk<T, kCacheSame, DP, MT, Cfg::E, Cfg::EV, KT, Cfg::kTailStages> walk{a, u, my_ring, qt, factor, token_of, lane, 0, 0, first_new, fresh, step_new, 0, 0, 0};
-                walk.run(z);
+                walk.run(z, [] {});
             }
-        } else if (cached + fresh > 0) {
+        } else {
             CacheWalk<T, F, DP, MT, Cfg::E, Cfg::EV, KS, Cfg::kStages> walk{a, u, my_ring, qf, factor, token_of, lane, first, cached, first_new, fresh, step, 0, 0, 0};
-            walk.run(z);
+            walk.run(z, prepare);
         }
         __syncthreads();  // rings are done with
         // ---- the warps' parts, joined in their order ----

@@ -196,32 +196,30 @@ __global__ void __launch_bounds__(CacheTcCfg<F, NQ, NC>::kThreads, 1)
             float c2 = a.c2;
             if constexpr (OWN_Q) {
                 if (sg.n > 0) {
-                    // the row in f16, its largest brought to 2^14 or more
+                    // the row in f16, its largest brought to 2^14 or more (all of it in registers: its loads wait for one another no more)
                     const T* q = static_cast<const T*>(a.q) + u.b * a.q_sb + tok * a.q_st + h * a.q_sh;
+                    uint4 x[NC * 8];
                     uint32_t top = 0;
-                    if (valid)
-                        for (int d = 0; d < a.D; d += 8) {
-                            const uint4 x = *reinterpret_cast<const uint4*>(q + d);
-                            const uint32_t m = 0x7fff7fffu;
-                            top = __vmaxu2(top, __vmaxu2(__vmaxu2(x.x & m, x.y & m), __vmaxu2(x.z & m, x.w & m)));
-                        }
+#pragma unroll
+                    for (int k = 0; k < NC * 8; ++k) x[k] = valid && k * 8 < a.D ? *reinterpret_cast<const uint4*>(q + k * 8) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+                    for (int k = 0; k < NC * 8; ++k) {
+                        const uint32_t mm = 0x7fff7fffu;
+                        top = __vmaxu2(top, __vmaxu2(__vmaxu2(x[k].x & mm, x[k].y & mm), __vmaxu2(x[k].z & mm, x[k].w & mm)));
+                    }
                     const int e = (int)(max(top & 0xffffu, top >> 16) >> 7);
                     const float up = e > 0 && e < 255 ? __uint_as_float((uint32_t)min(max(268 - e, 27), 227) << 23) : 1.f;
                     c2 = a.c2 * (1.f / up);
-                    if (row < rows)
-                        for (int d = 0; d < NC * 64; d += 8) {
-                            uint4 y = make_uint4(0, 0, 0, 0);
-                            if (valid && d < a.D) {
-                                const uint4 x = *reinterpret_cast<const uint4*>(q + d);
-                                const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-                                uint32_t p[4];
+                    if (row < rows) {
 #pragma unroll
-                                for (int k = 0; k < 4; ++k)
-                                    p[k] = tc_pack<false>(__uint_as_float(w[k] << 16) * up, __uint_as_float(w[k] & 0xffff0000u) * up);
-                                y = make_uint4(p[0], p[1], p[2], p[3]);
-                            }
-                            *reinterpret_cast<uint4*>(q_tiles + (t * NC + d / 64) * kTcTile + row * 128 + ((((d / 8) & 7) ^ (row & 7)) << 4)) = y;
+                        for (int k = 0; k < NC * 8; ++k) {
+                            const uint32_t w[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
+                            uint32_t p[4];
+#pragma unroll
+                            for (int v = 0; v < 4; ++v) p[v] = tc_pack<false>(__uint_as_float(w[v] << 16) * up, __uint_as_float(w[v] & 0xffff0000u) * up);
+                            *reinterpret_cast<uint4*>(q_tiles + (t * NC + k / 8) * kTcTile + row * 128 + (((k & 7) ^ (row & 7)) << 4)) = make_uint4(p[0], p[1], p[2], p[3]);
                         }
+                    }
                     tc_fence_async();
                     __syncwarp();
                     tc_bar_arrive_if(first, tc_smem(&sy.q_full));
@@ -629,7 +627,7 @@ __global__ void __launch_bounds__(CacheTcCfg<F, NQ, NC>::kThreads, 1)
                     there = j < sg.tail_keys;
                     uint32_t top = 0;
                     if (there) {
-#pragma unroll 1
+#pragma unroll 4
                         for (int d = 0; d < a.D; d += 8) {
                             const uint4 y = *reinterpret_cast<const uint4*>(fresh + j * f_token + d);
                             const uint32_t mm = 0x7fff7fffu;
@@ -705,7 +703,7 @@ __global__ void __launch_bounds__(CacheTcCfg<F, NQ, NC>::kThreads, 1)
                         if (idx >= ST && !tc_bar_wait(tc_smem(&sy.empty[st]), (idx / ST - 1) & 1, abort, err)) return false;
                         const T* p = fresh + j * f_token;
                         const float f = most == 0u ? 0.f : cache_scale(254u - most);
-#pragma unroll 1
+#pragma unroll 2
                         for (int d = 0; d < NC * 64; d += 8) {
                             uint4 y = make_uint4(0, 0, 0, 0);
                             if (there && d < a.D) {

@@ -94,7 +94,7 @@ def test_sizes(msda, size, new, fmt, dtype):  # noqa: F811
 MANY = [  # more rows a key head: heads that do not divide a tile of 128, one row more than a tile, several tiles
     (1, 33, 300, 1, 1, 16, 16), (2, 11, 1000, 12, 4, 80, 32), (1, 43, 700, 6, 2, 64, 64), (1, 300, 513, 2, 1, 128, 128),
     (3, 20, 2500, 16, 1, 48, 16), (1, 2, 900, 64, 1, 64, 16), (1, 1, 900, 100, 1, 128, 64), (1, 1, 600, 130, 1, 32, 16),
-    (2, 64, 5000, 8, 2, 128, 256), (9, 40, 200, 8, 8, 32, 32), (1, 129, 129, 4, 4, 112, 1024), (2, 260, 0, 2, 2, 64, 16),
+    (2, 64, 5000, 8, 2, 128, 256), (37, 18, 150, 1, 1, 32, 16), (9, 40, 200, 8, 8, 32, 32), (1, 129, 129, 4, 4, 112, 1024), (2, 260, 0, 2, 2, 64, 16),
 ]
 
 
