@@ -150,7 +150,7 @@ __device__ __forceinline__ float cache_top_value(uint32_t top) {
 
 // U rows of K and of V at a time a lane.
 template <typename T, int F>
-__global__ void __launch_bounds__(kMoveThreads) msda_cache_write_kernel(const CacheMoveArgs a) {
+__global__ void __launch_bounds__(kMoveThreads, sizeof(T) == 4 ? 3 : 4) msda_cache_write_kernel(const CacheMoveArgs a) {
     constexpr int E = CacheVec<T>::n, U = 2, ES = F == kCacheSame ? (int)sizeof(T) : 1;
     const int lane = threadIdx.x & 31, at = lane & ((1 << a.lanes_log2) - 1), row0 = lane >> a.lanes_log2, rows = 32 >> a.lanes_log2;
     const bool in = at * E < a.D;
@@ -232,7 +232,7 @@ __global__ void __launch_bounds__(kMoveThreads) msda_cache_write_kernel(const Ca
 }
 
 template <typename T, int F>
-__global__ void __launch_bounds__(kMoveThreads) msda_cache_read_kernel(const CacheMoveArgs a) {
+__global__ void __launch_bounds__(kMoveThreads, sizeof(T) == 4 ? 3 : 4) msda_cache_read_kernel(const CacheMoveArgs a) {
     constexpr int E = CacheVec<T>::n, U = 4, ES = F == kCacheSame ? (int)sizeof(T) : 1;
     const int lane = threadIdx.x & 31, at = lane & ((1 << a.lanes_log2) - 1), row0 = lane >> a.lanes_log2, rows = 32 >> a.lanes_log2;
     const bool in = at * E < a.D;

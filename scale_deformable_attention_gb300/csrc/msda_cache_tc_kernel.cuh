@@ -43,7 +43,7 @@ struct CacheTcRange {
 };
 
 template <int F, int NQ, int NC>
-struct CacheTcCfg {
+struct CacheTcCfg {  // stages are even in number: K has the even ones, V the odd ones
     static constexpr bool kCodes = F != kCacheSame;
     static_assert(!kCodes || NQ == 1, "codes: one row tile a block");
     static constexpr int kStages = NC == 1 ? (kCodes ? 6 : 8) : 4;  // ring of K and V operand tiles
@@ -128,7 +128,7 @@ __global__ void __launch_bounds__(CacheTcCfg<F, NQ, NC>::kThreads, 1)
         if (lane == 0) {
             for (int i = 0; i < 8; ++i) {
                 tc_bar_init(tc_smem(&sy.full[i]), CODES ? 4 : 1);
-                tc_bar_init(tc_smem(&sy.empty[i]), NQ);
+                tc_bar_init(tc_smem(&sy.empty[i]), NQ + (!CODES && (i & 1) ? 1 : 0));  // values lie in the odd stages: the warp that clears lets them go too
                 tc_bar_init(tc_smem(&sy.cleared[i]), 1);
             }
             for (int i = 0; i < 6; ++i) {
@@ -187,7 +187,7 @@ __global__ void __launch_bounds__(CacheTcCfg<F, NQ, NC>::kThreads, 1)
         const uint32_t p_at = tmem + Cfg::kP + t * Cfg::kPStep + lanes;
         const int chunks = a.D / 16;
         const uint32_t first = lane == 0;
-        int g0 = 0;  // tiles before this segment
+        int g0 = 0, p0 = 0;  // tiles before this segment, tiles of the cache so far
         cache_segments(a, start, tid == 0, [&](const CacheSegment& sg) {
             const CacheUnit& u = sg.u;
             const int tok = u.rt * NQ * qpt + t * qpt + row / a.G, h = u.n * a.G + row % a.G;
@@ -278,7 +278,7 @@ __global__ void __launch_bounds__(CacheTcCfg<F, NQ, NC>::kThreads, 1)
                     }
                     if (!tail) {
 #pragma unroll
-                        for (int c = 0; c < 4; ++c) w[c] = sy.words[gi & 7][c];
+                        for (int c = 0; c < 4; ++c) w[c] = sy.words[p0 & 7][c];
                     }
                     if (__builtin_expect(__any_sync(0xffffffffu, (w[0] & w[1] & w[2] & w[3]) != 0xffffffffu), 0)) {
 #pragma unroll
@@ -380,6 +380,7 @@ __global__ void __launch_bounds__(CacheTcCfg<F, NQ, NC>::kThreads, 1)
                     // a warp without rows may not run a tile ahead of the others: its arrival would count for theirs
                     if (i > 0 && !tc_bar_wait(tc_smem(&sy.pv_done[t]), (gi - 1) & 1, abort, err)) return false;
                 }
+                p0 += tail ? 0 : 1;
                 __syncwarp();
                 tc_bar_arrive_if(first, tc_smem(&sy.p_full[t]));
             }
@@ -435,7 +436,7 @@ __global__ void __launch_bounds__(CacheTcCfg<F, NQ, NC>::kThreads, 1)
             // ---- copies (all lanes: a box of rows each) ----
             const int boxes = kTcRows / box_rows;
             const uint32_t qbar = tc_smem(&sy.q_full);
-            int g0 = 0, r0 = 0, qs = 0;  // tiles, tiles of codes, queries so far
+            int g0 = 0, p0 = 0, qs = 0;  // tiles, tiles of the cache, queries so far
             cache_segments(a, start, false, [&](const CacheSegment& sg) {
                 const CacheUnit& u = sg.u;
                 if (sg.n == 0) return true;
@@ -459,19 +460,20 @@ __global__ void __launch_bounds__(CacheTcCfg<F, NQ, NC>::kThreads, 1)
                     entry = entry1, entry1 = entry_of(i + 2);
                     const bool tail = tile >= u.cache_tiles;
                     if (!tail) {
-                        // a tile's words are read 8 tiles later at most: the rings are shorter
+                        // eight places by turns, counted in tiles of the cache: those ahead are in the rings (tiles of new tokens pass
+                        // this warp by where the cache holds codes, any number of them)
                         const uint32_t good = __ballot_sync(0xffffffffu, mine >= 0);
                         const int x = lane & 3;  // keys 32 x to 32 x + 31
                         const uint32_t pages = box_rows >= 32 ? ((good >> (x * 32 / box_rows)) & 1u ? ~0u : 0u)
                                                               : ((good >> (2 * x)) & 1u ? 0xffffu : 0u) | ((good >> (2 * x + 1)) & 1u ? 0xffff0000u : 0u);
-                        if (lane < 4) sy.words[gi & 7][x] = pages & tc_low_bits(u.length - tile * kTcRows - 32 * x);
+                        if (lane < 4) sy.words[p0 & 7][x] = pages & tc_low_bits(u.length - tile * kTcRows - 32 * x);
                         __syncwarp();
                     }
                     const int ring_n = CODES ? Cfg::kRaw : ST;
                     if (tail && CODES) continue;  // the converters read them
 #pragma unroll
                     for (int kv = 0; kv < 2; ++kv) {
-                        const int idx = 2 * (CODES ? r0 : gi) + kv, st = idx % ring_n;
+                        const int idx = 2 * (CODES ? p0 : gi) + kv, st = idx % ring_n;
                         uint64_t* full = CODES ? sy.raw_full : sy.full;
                         uint64_t* empty = CODES ? sy.raw_empty : sy.empty;
                         if (idx >= ring_n && !tc_bar_wait(tc_smem(&empty[st]), (idx / ring_n - 1) & 1, abort, err)) return false;
@@ -491,7 +493,7 @@ __global__ void __launch_bounds__(CacheTcCfg<F, NQ, NC>::kThreads, 1)
                             }
                         }
                     }
-                    ++r0;
+                    p0 += tail ? 0 : 1;
                 }
                 g0 += sg.n;
                 return true;
@@ -571,15 +573,19 @@ __global__ void __launch_bounds__(CacheTcCfg<F, NQ, NC>::kThreads, 1)
             cache_segments(a, start, false, [&](const CacheSegment& sg) {
                 const CacheUnit& u = sg.u;
                 for (int i = 0; i < sg.n; ++i) {
+                    // every tile is waited for, in its turn: a barrier tells only the last phase from the one under way
                     const int tile = sg.first + i, idx = 2 * (g0 + i) + 1, st = idx % ST;
                     const int left = tile < u.cache_tiles ? u.length - tile * kTcRows : u.count - (tile - u.cache_tiles) * kTcRows;
-                    if (left >= kTcRows) continue;
                     if (!tc_bar_wait(tc_smem(&sy.full[st]), (idx / ST) & 1, abort, err)) return false;
-                    const uint32_t w[4] = {tc_low_bits(left), tc_low_bits(left - 32), tc_low_bits(left - 64), tc_low_bits(left - 96)};
-                    tc_clear_rows<NC>(ring + st * Cfg::kTileBytes, w, lane);
-                    tc_fence_async();
+                    if (left < kTcRows) {
+                        const uint32_t w[4] = {tc_low_bits(left), tc_low_bits(left - 32), tc_low_bits(left - 64), tc_low_bits(left - 96)};
+                        tc_clear_rows<NC>(ring + st * Cfg::kTileBytes, w, lane);
+                        tc_fence_async();
+                        __syncwarp();
+                        if (lane == 0) tc_bar_arrive(tc_smem(&sy.cleared[st]));
+                    }
                     __syncwarp();
-                    if (lane == 0) tc_bar_arrive(tc_smem(&sy.cleared[st]));
+                    if (lane == 0) tc_bar_arrive(tc_smem(&sy.empty[st]));
                 }
                 g0 += sg.n;
                 return true;

@@ -106,6 +106,21 @@ def test_many_rows(msda, size, new, fmt, dtype):  # noqa: F811
     test_sizes(msda, size, new, fmt, dtype)
 
 
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("T", [1, 20, 64])
+def test_long_shares(msda, T, fmt, D):  # noqa: F811
+    """Blocks that walk many tiles over the ends of several sequences, whose last tiles hold rows that are not theirs (NaN)."""
+    lengths = [11999, 9000, 12001, 130, 7777, 10113, 5, 11000, 8191, 6401]
+    g, cache, table, lengths = made(msda, 24, "bf16", fmt, 10, 12001, 4, D, 64, lengths)
+    q, key, value = (normal(g, (10, T, n, D), torch.bfloat16) for n in (16, 4, 4))
+    counts = torch.randint(1, T + 1, (10,), generator=g, device=DEV).int()
+    for x in (q, key, value):
+        x[torch.arange(T, device=DEV)[None] >= counts[:, None]] = math.nan
+    for _ in range(2):
+        compare(msda, q, cache, table, lengths, key, value, counts=counts)
+
+
 @pytest.mark.parametrize("fmt", FORMATS)
 @pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
 @pytest.mark.parametrize("T", [3, 60])
@@ -262,6 +277,46 @@ def test_prompt_drafts_and_tokens_together(msda, fmt, dtype):  # noqa: F811
         compare(msda, q, cache, table, lengths, k, v)
         msda.cache_write(cache, k, v, table, lengths)
         lengths = lengths + 1
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("T", [1, 40])
+def test_padding_without_new_keys(msda, fmt, T):  # noqa: F811
+    """counts alone: padded queries, NaN in them, over the cache."""
+    g, cache, table, lengths = made(msda, 21, "f16", fmt, 3, 300, 2, 48, 32, [300, 0, 17])
+    q = normal(g, (3, T, 4, 48), torch.float16)
+    counts = ints(T, T, 0)
+    q[2] = math.nan
+    out, lse = compare(msda, q, cache, table, lengths, counts=counts)
+    assert not out[1:].any() and (lse[1:] == -math.inf).all()
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_two_calls_at_once(msda, fmt):  # noqa: F811
+    """Calls on two streams over one cache, each with parts to join: the results of one after the other."""
+    g, cache, table, lengths = made(msda, 22, "bf16", fmt, 2, 9000, 2, 128, 64)
+    q = [normal(g, (2, T, 8, 128), torch.bfloat16) for T in (1, 40)]
+    want = [msda.cache_attention(x, cache, table, lengths) for x in q]
+    streams = [torch.cuda.Stream() for _ in q]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        got = []
+        for s, x in zip(streams, q):
+            with torch.cuda.stream(s):
+                got.append(msda.cache_attention(x, cache, table, lengths))
+        torch.cuda.synchronize()
+        for a, b in zip(got, want):
+            assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+def test_a_workspace_of_ones_own(msda):  # noqa: F811
+    g, cache, table, lengths = made(msda, 23, "bf16", "int8", 2, 9000, 2, 64, 64)
+    q = normal(g, (2, 3, 8, 64), torch.bfloat16)
+    want = msda.cache_attention(q, cache, table, lengths)
+    ws = torch.full((64 << 20,), 255, dtype=torch.uint8, device=DEV)
+    for _ in range(2):
+        got = msda.cache_attention(q, cache, table, lengths, workspace=ws)
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
 
 
 def test_against_dense_attention(msda):  # noqa: F811
