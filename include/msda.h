@@ -517,10 +517,13 @@ msda_status msda_cache_read(msda_dtype dt, int format, const msda_cache_problem*
  *
  * Sums, statistics and products accumulate in fp32.  Probabilities are rounded
  * to 16 bits for their product: those of fp16 and of quantised caches to fp16
- * (half a step, or 2^-30 of a row's largest), bf16 over a bf16 cache to bf16; fp32
+ * (half a step, or 2^-33 of a row's largest), bf16 over a bf16 cache to bf16; fp32
  * runs in two fp16 pieces (quantised) or three bf16 pieces a value, products
- * below 2^-22 of a value left out.  fp16 pieces: a quantised value below 2^-24
- * of the largest value that its warp meets loses bits.  No atomics take part in a sum: equal
+ * below 2^-22 of a value left out.  In a quantised cache this goes for a
+ * probability times its value's scale, against the largest of both that a warp or
+ * tile meets; bf16 queries and new tokens there become fp16 times a power of two a
+ * row or tile, elements below 2^-22 of its largest losing bits.
+ * No atomics take part in a sum: equal
  * calls give equal bits; the order depends on the sizes and lengths.
  *
  * `longest` plans the launch; a smaller bound on the lengths than the table's

@@ -3,7 +3,6 @@ attention of new tokens over it (C ABI ``msda_cache_write`` / ``_read`` / ``_att
 from __future__ import annotations
 
 import math
-import struct
 from typing import NamedTuple, Optional, Tuple
 
 import torch
@@ -11,8 +10,6 @@ import torch
 from . import _lib
 from ._binding import DTYPE_CODE, stream, workspace_of
 
-# the problem struct of include/msda.h: 35 int64 members
-_problem = struct.Struct("35q").pack
 CODE_FORMAT = {torch.float8_e4m3fn: _lib.CACHE_E4M3, torch.int8: _lib.CACHE_INT8}
 _NONE3 = (0, 0, 0)
 
@@ -156,7 +153,7 @@ def cache_write(cache: PagedCache, key: torch.Tensor, value: torch.Tensor, table
     if counts is not None:
         counts = _index("counts", counts, B, 1, dev)
     width = table.shape[1]
-    p = _problem(B, R, N, N, D, T, sh[0], sh[1], width, width * sh[1], *strides, table.stride(0), *_NONE3,
+    p = _lib.cache_problem(B, R, N, N, D, T, sh[0], sh[1], width, width * sh[1], *strides, table.stride(0), *_NONE3,
                           *key.stride()[:3], *value.stride()[:3], 0, 0, 0 if select is None else select.stride(0))
     _call(_lib.lib().msda_cache_write, dev, dt, fmt, p, key.data_ptr(), value.data_ptr(), table.data_ptr(), start.data_ptr(),
           _address(counts), _address(select), *places)
@@ -177,7 +174,7 @@ def cache_read(cache: PagedCache, table: torch.Tensor, lengths: torch.Tensor, ro
     table, lengths = _index("table", table, B, 2, dev), _index("lengths", lengths, B, 1, dev)
     key = torch.empty((B, rows, *sh[2:]), dtype=dtype, device=dev)
     value = torch.empty_like(key)
-    p = _problem(B, rows, sh[2], sh[2], sh[3], rows, sh[0], sh[1], width, width * sh[1], *strides,
+    p = _lib.cache_problem(B, rows, sh[2], sh[2], sh[3], rows, sh[0], sh[1], width, width * sh[1], *strides,
                           table.stride(0), *_NONE3, *_NONE3, *_NONE3, 0, 0, 0)
     _call(_lib.lib().msda_cache_read, dev, dt, fmt, p, *places, table.data_ptr(), lengths.data_ptr(), key.data_ptr(),
           value.data_ptr())
@@ -235,7 +232,7 @@ def cache_attention(query: torch.Tensor, cache: PagedCache, table: torch.Tensor,
         ms0, ms1 = 0 if mask.shape[0] == 1 else mask.stride(0), mask.stride(1)
     if counts is not None:
         counts = _index("counts", counts, B, 1, dev)
-    p = _problem(B, T, M, N, D, 0 if key is None else T, sh[0], sh[1], width, longest, *strides, table.stride(0),
+    p = _lib.cache_problem(B, T, M, N, D, 0 if key is None else T, sh[0], sh[1], width, longest, *strides, table.stride(0),
                           *query.stride()[:3], *ks, *vs, ms0, ms1, 0)
     out = torch.empty((B, T, M * D), dtype=query.dtype, device=dev)
     lse = torch.empty((B, M, T), dtype=torch.float32, device=dev)

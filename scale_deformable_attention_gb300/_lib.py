@@ -7,6 +7,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 import threading
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -34,7 +35,8 @@ CACHE_SAME, CACHE_E4M3, CACHE_INT8 = 0, 1, 2
 # the problem structs of include/msda.h: nothing but int64 members, so a flat array lays them out
 RotaryProblem = ctypes.c_int64 * 18
 AttentionProblem = ctypes.c_int64 * 19
-CacheProblem = ctypes.c_int64 * 35
+# (packed as bytes, which takes a tenth of the time of an array of so many)
+cache_problem = struct.Struct("35q").pack
 
 
 class MsdaError(RuntimeError):

@@ -8,7 +8,9 @@
 // tokens of a head, so that pages, places and scales are looked up once for them
 // by one lane each and handed on by shuffles; a block's warps take the heads of the
 // same tokens.  The cache's side (head by head) is then read or written in runs of
-// 16 rows, the other side in whole tokens.
+// 16 rows, the other side in whole tokens.  8 x 22223 tokens of 8 heads of 64, e4m3 to bf16: 88 us, 85 % of the copy rate;
+// lookups in every lane took 132 us (ALU 51 % busy with addresses).  Four blocks an SM in 16 bits (three: 97 us), three in
+// binary32 (four: 29 us against 27 for 4 x 8191 tokens of 8 heads of 48).
 #include <cuda_runtime.h>
 
 #include <cstdint>
@@ -301,49 +303,49 @@ __global__ void __launch_bounds__(kMoveThreads, sizeof(T) == 4 ? 3 : 4) msda_cac
     }
 }
 
-// A block a row (of a unit): the parts of the blocks that shared the unit.  Four groups of 32 lanes take every fourth part, a lane
-// four channels; the groups are joined in their order.
+// Parts of the blocks that shared a unit: a block of 16 warps takes 16 rows of it, as many warps a row as there are (16 for one row, one
+// for 16), each every so many-th part, a lane four channels; the warps of a row are joined in their order.  (Blocks cost more than
+// what they do: one a row took 15 us, cold, for 8192 rows of two or three parts of 128 channels; four rows one after the other by four
+// warps 5 us more for 16 units of 29 parts.)
+constexpr int kJoinWarps = 16;
 template <typename T>
-__global__ void __launch_bounds__(128) msda_cache_join_kernel(const CacheArgs a) {
-    __shared__ float4 part[4][32];
-    __shared__ float tops[4], sums[4];
+__global__ void __launch_bounds__(kJoinWarps * 32) msda_cache_join_kernel(const CacheArgs a) {
+    __shared__ float4 part[kJoinWarps][32];
+    __shared__ float tops[kJoinWarps], sums[kJoinWarps];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    int id = blockIdx.x;
-    const int rt = id % a.row_tiles, r = blockIdx.y, row = rt * a.tile_rows + r;
-    id /= a.row_tiles;
-    const int n = id % a.N, b = id / a.N;
     asm volatile("griddepcontrol.wait;" ::: "memory");  // launched as a programmatic dependent of the kernel that makes the parts
-    if (row >= a.rows) return;
     const int2 parts = a.units[blockIdx.x];
     if (parts.x < 0) return;
+    int id = blockIdx.x;
+    const int rt = id % a.row_tiles;
+    id /= a.row_tiles;
+    const int n = id % a.N, b = id / a.N, r0 = blockIdx.y * kJoinWarps;
+    const int rows = min(kJoinWarps, min(a.tile_rows, a.rows - rt * a.tile_rows) - r0);  // of this block
+    int each_log2 = 4;                                                                  // warps a row: a power of two
+    while (each_log2 > 0 && (rows << each_log2) > kJoinWarps) --each_log2;
+    const int each = 1 << each_log2, r = r0 + (warp >> each_log2), row = rt * a.tile_rows + r, mine = warp & (each - 1);
+    const bool there = r - r0 < rows;
     float top = -attn_inf(), sum = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
+    // joins (l2, s, y) to (top, sum, o); NaN statistics make the row NaN
+    auto join = [&](float l2, float s, const float4& y) {
+        const float next = fmaxf(top, l2), ref = next == -attn_inf() ? 0.f : next, f = exp2f(top - ref), w = exp2f(l2 - ref);
+        top = next, sum = sum * f + w * s;
+        o[0] = o[0] * f + w * y.x, o[1] = o[1] * f + w * y.y, o[2] = o[2] * f + w * y.z, o[3] = o[3] * f + w * y.w;
+    };
 #pragma unroll 4
-    for (int i = warp; i < parts.y; i += 4) {
+    for (int i = there ? mine : parts.y; i < parts.y; i += each) {
         // the first block's slot, then the first slots of the blocks behind it
         const long long at = (long long)(i == 0 ? parts.x : 2 * ((parts.x >> 1) + i)) * a.tile_rows + r;
         const float l2 = a.part_l2[at];
         float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
         if (lane * 4 < a.D) y = *reinterpret_cast<const float4*>(a.part_o + at * a.D + lane * 4);
-        // NaN: a part whose statistics are NaN makes the row NaN
-        const float next = fmaxf(top, l2), ref = next == -attn_inf() ? 0.f : next;
-        const float f = exp2f(top - ref), w = exp2f(l2 - ref);
-        top = next, sum = sum * f + w;
-        o[0] = o[0] * f + w * y.x, o[1] = o[1] * f + w * y.y, o[2] = o[2] * f + w * y.z, o[3] = o[3] * f + w * y.w;
+        join(l2, 1.f, y);
     }
     part[warp][lane] = make_float4(o[0], o[1], o[2], o[3]);
     if (lane == 0) tops[warp] = top, sums[warp] = sum;
     __syncthreads();
-    if (warp != 0) return;
-    top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
-    const float ref = top == -attn_inf() ? 0.f : top;
-    sum = o[0] = o[1] = o[2] = o[3] = 0.f;
-#pragma unroll
-    for (int w = 0; w < 4; ++w) {
-        const float f = exp2f(tops[w] - ref);
-        const float4 y = part[w][lane];
-        sum += sums[w] * f;
-        o[0] += y.x * f, o[1] += y.y * f, o[2] += y.z * f, o[3] += y.w * f;
-    }
+    if (!there || mine != 0) return;
+    for (int w = 1; w < each; ++w) join(tops[warp + w], sums[warp + w], part[warp + w][lane]);
     const int t = row / a.G, h = n * a.G + row - t * a.G;
     const float inv = sum == 0.f ? 0.f : 1.f / sum;
     if (lane * 4 < a.D) {
@@ -356,14 +358,14 @@ __global__ void __launch_bounds__(128) msda_cache_join_kernel(const CacheArgs a)
             else out[e] = __float2bfloat16_rn(y);
         }
     }
-    if (lane == 0) a.lse[((long long)b * a.M + h) * a.T + t] = sum == 0.f ? -attn_inf() : (ref + log2f(sum)) * kLn2;
+    if (lane == 0) a.lse[((long long)b * a.M + h) * a.T + t] = sum == 0.f ? -attn_inf() : ((top == -attn_inf() ? 0.f : top) + log2f(sum)) * kLn2;
 }
 
 template <typename T>
 static cudaError_t join_go(const CacheArgs& a, bool early, cudaStream_t st) {
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)((long long)a.B * a.N * a.row_tiles), (unsigned)(a.rows < a.tile_rows ? a.rows : a.tile_rows));
-    cfg.blockDim = dim3(128);
+    cfg.gridDim = dim3((unsigned)((long long)a.B * a.N * a.row_tiles), (unsigned)(((a.rows < a.tile_rows ? a.rows : a.tile_rows) + kJoinWarps - 1) / kJoinWarps));
+    cfg.blockDim = dim3(kJoinWarps * 32);
     cfg.stream = st;
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

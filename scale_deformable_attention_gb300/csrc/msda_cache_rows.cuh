@@ -18,6 +18,11 @@
 // register brings next to each other: no transposing load.  16-byte chunks of a
 // row are swizzled by the row so that both reads are free of bank conflicts.
 //
+// Measured, one new token of 16 heads on 4 of 128 channels: 8 x 65536 tokens bf16 168 us (6.4 TB/s), e4m3 129 us (4.2 TB/s:
+// half the bytes, the same products and exponentials); 8 x 16384: 51 and 45 us.  About 8 us of each pass before a
+// block's first product: code that runs once costs some 9 cycles an instruction to fetch (plan 2.5 us, first
+// copies 2.5, queries 1.2), so copies, products and exponentials stand in one place of the code each.
+//
 // Types.  16 bits: as they are.  8 bits: codes are whole f16 values, so the
 // product is of f16 whatever the queries are; these are scaled by a power of two
 // a row (bf16 has fewer bits than f16, binary32 takes two pieces), the scales of
@@ -25,9 +30,9 @@
 // largest that the warp has met.  binary32: three bf16 pieces a value, six
 // products, the small ones first, summed anew each step (a tensor core cuts its
 // sums off).  P is rounded to 16 bits for its product (binary32: 2 pieces of f16
-// or 3 of bf16).  f16 P: m lies 2^6 below the row's maximum when it was looked
-// for, and is looked for again when a score passes 2^14 of it: a P is off by half a
-// step or 2^-31 of the row's largest.
+// or 3 of bf16).  f16 P: m lies 2^8 below the row's maximum when it was looked
+// for, and is looked for again when a lane's P of a row add up to more than 2^14:
+// a P is off by half a step or 2^-33 of the row's largest.
 #pragma once
 
 #include "msda_cache.cuh"
@@ -42,19 +47,16 @@ struct CacheType;
 template <>
 struct CacheType<float> {
     static constexpr int code = 0;
-    static __device__ __forceinline__ float get(float x) { return x; }
     static __device__ __forceinline__ float put(float x) { return x; }
 };
 template <>
 struct CacheType<__half> {
     static constexpr int code = 1;
-    static __device__ __forceinline__ float get(__half x) { return __half2float(x); }
     static __device__ __forceinline__ __half put(float x) { return __float2half_rn(x); }
 };
 template <>
 struct CacheType<__nv_bfloat16> {
     static constexpr int code = 2;
-    static __device__ __forceinline__ float get(__nv_bfloat16 x) { return __bfloat162float(x); }
     static __device__ __forceinline__ __nv_bfloat16 put(float x) { return __float2bfloat16_rn(x); }
 };
 
@@ -65,7 +67,7 @@ struct CacheProduct {
     static constexpr bool bf16 = F == kCacheSame && CacheType<T>::code != 1;
     static constexpr int es = F == kCacheSame ? (int)sizeof(T) : 1;
     static constexpr int qp = !f32 ? 1 : F == kCacheSame ? 3 : 2, kp = f32 && F == kCacheSame ? 3 : 1, pp = qp;
-    static constexpr float below = bf16 ? 0.f : 6.f;  // m below the maximum, in binary places
+    static constexpr float below = bf16 ? 0.f : 8.f;  // m below the maximum, in binary places
 };
 constexpr float kCacheMost = 16384.f;  // what a lane's probabilities of a row may add up to in a step before m follows
 

@@ -16,12 +16,12 @@ def lib():
 
 def problem(B=2, T=3, M=4, N=2, D=32, source=3, pages=9, page=16, width=4, longest=64, ck=None, cv=None, ks=None, vs=None,
             ts=None, q=None, k=None, v=None, ms=(0, 0), ss=0):
-    from scale_deformable_attention_gb300._lib import CacheProblem
+    from scale_deformable_attention_gb300._lib import cache_problem
 
     pool = (N * page * D, D, page * D)
     scales = (N * page, 1, page)
     rows = lambda heads: (T * heads * D, heads * D, D)              # noqa: E731
-    return CacheProblem(B, T, M, N, D, source, pages, page, width, longest, *(ck or pool), *(cv or pool), *(ks or scales),
+    return cache_problem(B, T, M, N, D, source, pages, page, width, longest, *(ck or pool), *(cv or pool), *(ks or scales),
                         *(vs or scales), width if ts is None else ts, *(q or rows(M)), *(k or rows(N)), *(v or rows(N)), *ms, ss)
 
 
