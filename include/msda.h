@@ -455,7 +455,8 @@ msda_status msda_attention_backward(msda_dtype dt, unsigned flags, const msda_at
  * and are checked there: a sequence's length or count outside its range is
  * brought into it, a token whose page number, place or selection lies outside is
  * neither written nor read (read: zeros; attention: not seen), and each raises
- * bit 3 of msda_device_errors().
+ * bit 3 of msda_device_errors().  A cache of no pages holds no tokens: its
+ * pointers and the table may be NULL, and every length is brought to 0.
  */
 typedef struct {
     int64_t B, T, M, N, D;      /* sequences, tokens of each in this call, query heads, key heads, channels */

@@ -390,6 +390,10 @@ constexpr int64_t kMost = 1ll << 30;
 
 bool positive(const int64_t* s) { return s[0] >= 0 && s[1] >= 0 && s[2] >= 0; }
 
+// Tokens that a sequence has at most: none where there are no pages, whatever its length says (the kernels bring lengths into this
+// range, raise the error bit and look at no table).
+int64_t longest_of(const msda_cache_problem* p) { return p->pages > 0 ? p->longest : 0; }
+
 // Sizes that all three calls share.
 msda_status check(msda_dtype dt, int format, const msda_cache_problem* p) {
     if (dt != MSDA_F32 && dt != MSDA_F16 && dt != MSDA_BF16) return failf(MSDA_ERR_INVALID_ARG, "unknown dtype %d", (int)dt);
@@ -449,7 +453,7 @@ msda::CachePages pages_of(const msda_cache_problem* p, const void* key, const vo
     three(p->key_scale_stride, c.ks_sp, c.ks_st, c.ks_sh);
     three(p->value_scale_stride, c.vs_sp, c.vs_st, c.vs_sh);
     c.table = table, c.table_sb = p->table_stride;
-    c.pages = (int)p->pages, c.page = (int)p->page, c.longest = (int)p->longest;
+    c.pages = (int)p->pages, c.page = (int)p->page, c.longest = (int)longest_of(p);
     while ((1 << c.page_log2) < c.page) ++c.page_log2;
     return c;
 }
@@ -500,7 +504,7 @@ msda_status check_attention(msda_dtype dt, int format, const msda_cache_problem*
     if (p->M > 65535) return failf(MSDA_ERR_UNSUPPORTED, "M=%lld too large", (long long)p->M);
     const int64_t G = p->M / p->N;
     // the line of all tiles (16 rows, 64 keys at least) is counted in 32 bits
-    const int64_t tiles = (p->longest + 63) / 64 + (p->source + 63) / 64 + 1, rows = (p->T * G + 15) / 16;
+    const int64_t tiles = (longest_of(p) + 63) / 64 + (p->source + 63) / 64 + 1, rows = (p->T * G + 15) / 16;
     int64_t all;
     if (p->T * G > kMost || !msda::mul_fits(p->B * p->N, rows, &all) || !msda::mul_fits(all, tiles, &all) || all > 0x7fffffffll / 2)
         return failf(MSDA_ERR_UNSUPPORTED, "B=%lld sequences of T=%lld tokens and M=%lld heads over %lld tokens are too many for one call", (long long)p->B,
@@ -533,8 +537,9 @@ bool tma_strides(const int64_t* st, int64_t a, int64_t b, int64_t c, int64_t es)
 int tc_tiles(msda_dtype dt, int format, const msda_cache_problem* p, int64_t rows) {
     const int64_t G = p->M / p->N, es = format == MSDA_CACHE_SAME ? 2 : 1;
     if (dt == MSDA_F32 || rows <= 16 || G > msda::kTcRows) return 0;
-    if (!tma_strides(p->query_stride, p->B, p->T, p->M, 2 * G) || !tma_strides(p->cache_key_stride, p->pages, p->page, p->N, es) ||
-        !tma_strides(p->cache_value_stride, p->pages, p->page, p->N, es))
+    if (!tma_strides(p->query_stride, p->B, p->T, p->M, 2 * G)) return 0;
+    if (longest_of(p) > 0 && (!tma_strides(p->cache_key_stride, p->pages, p->page, p->N, es) ||
+                              !tma_strides(p->cache_value_stride, p->pages, p->page, p->N, es)))
         return 0;
     if (format == MSDA_CACHE_SAME && p->source > 0 &&
         (!tma_strides(p->key_stride, p->B, p->source, p->N, 2) || !tma_strides(p->value_stride, p->B, p->source, p->N, 2)))
@@ -553,7 +558,7 @@ CachePlan plan_of(msda_dtype dt, int format, const msda_cache_problem* p) {
                                : msda::cache_rows_shape<__nv_bfloat16>(format, (int)p->D, (int)c.rows);
     c.row_tiles = (c.rows + c.shape.tile_rows - 1) / c.shape.tile_rows;
     c.units = p->B * p->N * c.row_tiles;
-    c.most_tiles = (p->longest + c.shape.tile_keys - 1) / c.shape.tile_keys + (p->source + c.shape.tail_keys - 1) / c.shape.tail_keys;
+    c.most_tiles = (longest_of(p) + c.shape.tile_keys - 1) / c.shape.tile_keys + (p->source + c.shape.tail_keys - 1) / c.shape.tail_keys;
     if (c.most_tiles < 1) c.most_tiles = 1;
     c.least = c.nq ? 2 : 4;
     c.whole = c.most_tiles <= 2 * c.least;
@@ -649,7 +654,7 @@ msda_status msda_cache_attention(msda_dtype dt, int format, const msda_cache_pro
         (s = vectors(value, p->value_stride, p->B, p->source, p->N, es, fresh, "value")) || (s = msda::need_ptr(lengths, rows, 4, "lengths")) ||
         (s = msda::need_ptr(counts, counts != nullptr, 4, "counts")) || (s = msda::need_ptr(out, rows, 16, "out")) ||
         (s = msda::need_ptr(lse, rows, 4, "lse")) ||
-        (s = cache_ok(dt, format, p, cache_key, cache_value, key_scale, value_scale, table, rows && p->pages > 0 && p->longest > 0)))
+        (s = cache_ok(dt, format, p, cache_key, cache_value, key_scale, value_scale, table, rows && longest_of(p) > 0)))
         return s;
     if (!rows) return MSDA_OK;
     const CachePlan plan = plan_of(dt, format, p);

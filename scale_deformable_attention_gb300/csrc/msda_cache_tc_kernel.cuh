@@ -792,8 +792,7 @@ cudaError_t tc_go(const CacheArgs& a, int grid, cudaStream_t st) {
     const int es = F == kCacheSame ? 2 : 1, inner = F == kCacheSame ? 64 : NC * 64;
     CUtensorMap mq, mk, mv, mnk, mnv;
     const bool fresh = F == kCacheSame && a.nk;
-    // an empty cache: no tile of it is read
-    const bool cache = a.c.pages > 0 && a.c.longest > 0;
+    const bool cache = a.c.longest > 0;  // else every length is 0: there are no tiles of the cache, and its maps are not used
     if (!map_queries(a, BF16, qpt, &mq) ||
         (cache && (!map4(a.c.k, es, BF16, a.D, inner, a.N, a.c.page, a.c.pages, a.c.k_sh, a.c.k_st, a.c.k_sp, box_rows, &mk) ||
                    !map4(a.c.v, es, BF16, a.D, inner, a.N, a.c.page, a.c.pages, a.c.v_sh, a.c.v_st, a.c.v_sp, box_rows, &mv))) ||
