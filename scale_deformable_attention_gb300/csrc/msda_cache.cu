@@ -13,7 +13,9 @@
 // binary32 (four: 29 us against 27 for 4 x 8191 tokens of 8 heads of 48).
 #include <cuda_runtime.h>
 
+#include <cmath>
 #include <cstdint>
+#include <limits>
 #include <type_traits>
 
 #include "msda_attention_tc.cuh"
@@ -673,7 +675,8 @@ msda_status msda_cache_attention(msda_dtype dt, int format, const msda_cache_pro
     a.rows = (int)plan.rows, a.row_tiles = (int)plan.row_tiles, a.tile_rows = plan.shape.tile_rows;
     while ((1 << a.tile_log2) < plan.shape.tile_keys) ++a.tile_log2;
     while ((1 << a.tail_log2) < plan.shape.tail_keys) ++a.tail_log2;
-    a.c2 = (float)(scale * (double)msda::kLog2e);
+    // never 0, by which the -inf of a hidden token would become NaN (a score is then off by 2^-149 |q k|, below 2^-20)
+    a.c2 = std::fmax((float)(scale * (double)msda::kLog2e), std::numeric_limits<float>::denorm_min());
     a.out = out, a.lse = lse;
     a.part_o = static_cast<float*>(workspace);  // null where no unit is shared
     a.part_l2 = reinterpret_cast<float*>(static_cast<unsigned char*>(workspace) + plan.part_l2);
