@@ -516,7 +516,11 @@ msda_status msda_cache_read(msda_dtype dt, int format, const msda_cache_problem*
  *       behind lengths[b].  A NaN or infinity in a value that some query of a
  *       sequence sees reaches those that do not (0 * NaN), as in the matrix form.
  *
- * Sums, statistics and products accumulate in fp32.  Probabilities are rounded
+ * Sums, statistics and products accumulate in fp32.  The tensor cores cut their
+ * sums off, towards zero, where others round to nearest: of positive values a
+ * 16-bit output over 67200 tokens is low by 2^-11 (tcgen05, a block a sequence)
+ * or 2^-13.5 (up to 16 rows a key head), in proportion to the tokens; fp32 adds
+ * up outputs of 16 tokens at a time, rounded.  Probabilities are rounded
  * to 16 bits for their product: those of fp16 and of quantised caches to fp16
  * (half a step, or 2^-33 of a row's largest), bf16 over a bf16 cache to bf16; fp32
  * runs in two fp16 pieces (quantised) or three bf16 pieces a value, products
