@@ -527,7 +527,9 @@ msda_status msda_cache_read(msda_dtype dt, int format, const msda_cache_problem*
  * below 2^-22 of a value left out.  In a quantised cache this goes for a
  * probability times its value's scale, against the largest of both that a warp or
  * tile meets; bf16 queries and new tokens there become fp16 times a power of two a
- * row or tile, elements below 2^-22 of its largest losing bits.
+ * row or, for values, tile, elements below 2^-22 of its largest losing bits (a new key
+ * more than 2^8 below its tile's largest: 2^-14 of its own).  Cached keys are exact,
+ * at whatever scales; a cached value's code is cut below 2^-24 of its tile's largest scale.
  * No atomics take part in a sum: equal
  * calls give equal bits; the order depends on the sizes and lengths.
  *

@@ -14,9 +14,13 @@
 //     a row tile its products;
 //   - unquantised: one clears the value rows that lie behind a sequence's last;
 //   - 8 bits: a warpgroup turns the codes of a tile, a row a thread, into f16 rows
-//     of the operands (whole values, exact), brought to the scale of the tile's
-//     largest row: the scores of the tile are multiplied by that scale of K, its
-//     P by that of V over the largest met.  New tokens' rows go the same way.
+//     of the operands, brought to the scale of the tile's largest row: the scores
+//     of the tile are multiplied by that scale of K, its P by that of V over the
+//     largest met.  New tokens' rows go the same way.  Codes 2^15 (e4m3) or 2^24
+//     (int8) below are still exact.  A key whose scale lies further below, as next
+//     to one of nothing but a large channel, goes in at its own scale, and its
+//     column of scores is multiplied by that (such scores were 0 from 2^25 on
+//     otherwise); values of P V share a sum and lose bits there.
 // bf16 queries of a quantised cache become f16 with a power of two a row.
 //
 // Measured, 16 heads on 4 of 128 channels over 8 x 65536 tokens: 64 rows a key head bf16 180 us (6.0 TB/s: memory), e4m3
@@ -67,6 +71,9 @@ struct CacheTcCfg {  // stages are even in number: K has the even ones, V the od
     static constexpr uint32_t kO = kOwnP ? NQ * 192 : NQ * 128;
     static constexpr uint32_t kCols = NQ == 2 || NC == 2 ? 512 : 256;
     static constexpr size_t kSmem = (size_t)(NQ + kStages) * kTileBytes + (size_t)kRaw * kRawBytes + 1024;
+    // binary places that a key may lie below the tile's largest and share its scale: codes stay exact in f16 (e4m3: 2^-9 2^-15, int8:
+    // 1 2^-24); new tokens, whose rows begin at 2^8, keep 2^-14 of their own largest in full
+    static constexpr int kApart = F == kCacheE4m3 ? 15 : 24, kApartNew = 8;
 };
 
 struct CacheTcSync {
@@ -76,14 +83,33 @@ struct CacheTcSync {
     uint32_t words[8][4];    // a tile's keys that are there
     float k_scale[8];        // 8 bits: scale of a tile's K, and the byte of that of its V
     uint32_t v_top[8];
+    int k_far[8];            // tile i + 1: some of its keys have scales of their own
     alignas(16) uint32_t tops[2][2][4];  // of each warpgroup that converts, by turns: its warps' largest bytes
 };
+
+static_assert(CacheTcCfg<kCacheE4m3, 1, 2>::kSmem + sizeof(CacheTcSync) + sizeof(CacheStart) <= 227 * 1024, "more shared memory than a block has");
 
 __device__ __forceinline__ void tc_tma_4d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int c0, int c1, int c2, int c3) {
     asm volatile(
         "cp.async.bulk.tensor.4d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(dst),
         "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
         : "memory");
+}
+
+// Of a new token's row: the byte of the power of two that brings its largest value to 2^8 or more; 255 where it holds an infinity or a NaN.
+template <bool BF16, typename T>
+__device__ __forceinline__ uint32_t cache_new_byte(const T* row, int D) {
+    uint32_t top = 0;
+#pragma unroll 4
+    for (int d = 0; d < D; d += 8) {
+        const uint4 y = *reinterpret_cast<const uint4*>(row + d);
+        const uint32_t mm = 0x7fff7fffu;
+        top = __vmaxu2(top, __vmaxu2(__vmaxu2(y.x & mm, y.y & mm), __vmaxu2(y.z & mm, y.w & mm)));
+    }
+    top = max(top & 0xffffu, top >> 16);
+    const float y = BF16 ? __uint_as_float(top << 16) : __half2float(__ushort_as_half((unsigned short)top));
+    const int e = (int)(__float_as_uint(y) >> 23);
+    return e == 255 ? 255u : (uint32_t)max(e - 8, 27);
 }
 
 // A unit's tiles of a block: cache tiles first, then those of the new tokens.
@@ -107,11 +133,46 @@ __device__ __forceinline__ void cache_segments(const CacheArgs& a, const CacheSt
     });
 }
 
+// Scores of a tile (at s_at in tensor memory) some of whose keys are at scales of their own: columns times these over 2^(most - 127).
+// Worked out anew and outside of the loop, so that the way that most tiles take holds next to nothing of it (a table from the
+// converting warps cost every tile 8 %; this 2 to 4: int8 92.9 -> 97.1 us for a tree of 16 over 16 x 16641 tokens).
+template <bool BF16, int F>
+__device__ __noinline__ void cache_tc_own_scales(const CacheArgs& a, const CacheSegment& sg, int tile, uint32_t most, uint32_t s_at) {
+    using Cfg = CacheTcCfg<F, 1, 1>;
+    using T = typename std::conditional<BF16, __nv_bfloat16, __half>::type;
+    const int lane = threadIdx.x & 31;
+    const CacheUnit& u = sg.u;
+    const bool tail = tile >= u.cache_tiles;
+#pragma unroll 1
+    for (int c = 0; c < 128; c += 32) {
+        const int key = tile * kTcRows + c + lane, j = key - u.cache_tiles * kTcRows;
+        uint32_t byte = 0;
+        if (tail) {
+            if (j < sg.tail_keys) byte = cache_new_byte<BF16>(static_cast<const T*>(a.nk) + u.b * a.nk_sb + j * a.nk_st + u.n * a.nk_sh, a.D);
+        } else if (key < u.length) {
+            const int page = cache_entry(a.c, u.b, key);
+            if ((unsigned)page < (unsigned)a.c.pages) byte = a.c.ks[page * a.c.ks_sp + (key & (a.c.page - 1)) * a.c.ks_st + u.n * a.c.ks_sh];
+        }
+        const int below = (int)(most - byte);
+        const float own = byte == 0u || below <= (tail ? Cfg::kApartNew : Cfg::kApart) ? 1.f : below > 126 ? 0.f : cache_scale(127 - below);
+#pragma unroll 1
+        for (int half = 0; half < 32; half += 16) {
+            uint32_t x[16];
+            tmem_ld16(x, s_at + c + half);
+            tmem_wait_ld();
+#pragma unroll
+            for (int k = 0; k < 16; ++k) x[k] = __float_as_uint(__uint_as_float(x[k]) * __shfl_sync(0xffffffffu, own, half + k));
+            tmem_st16(s_at + c + half, x);
+        }
+    }
+    tmem_wait_st();
+}
+
 }  // namespace
 
 template <bool BF16, int F, int NQ, int NC>
 __global__ void __launch_bounds__(CacheTcCfg<F, NQ, NC>::kThreads, 1)
-    msda_cache_tc_kernel(const CacheArgs a, const int box_rows, const __grid_constant__ CUtensorMap map_q,
+    msda_cache_tc_kernel(const __grid_constant__ CacheArgs a, const int box_rows, const __grid_constant__ CUtensorMap map_q,
                          const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
                          const __grid_constant__ CUtensorMap map_nk, const __grid_constant__ CUtensorMap map_nv) {
     using Cfg = CacheTcCfg<F, NQ, NC>;
@@ -150,6 +211,7 @@ __global__ void __launch_bounds__(CacheTcCfg<F, NQ, NC>::kThreads, 1)
                 tc_bar_init(tc_smem(&sy.p_full[i]), 4);
                 tc_bar_init(tc_smem(&sy.pv_done[i]), 1);
             }
+            for (int i = 0; i < 8; ++i) sy.k_far[i] = 0;
             sy.abort = 0;
             asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
             tc_prefetch_map(&map_q);
@@ -273,6 +335,10 @@ __global__ void __launch_bounds__(CacheTcCfg<F, NQ, NC>::kThreads, 1)
                 if (!tc_bar_wait(tc_smem(&sy.s_full[t]), gi & 1, abort, err)) return false;
                 tc_fence_after();
                 if (warp_on) {
+                    if constexpr (CODES) {
+                        if (__builtin_expect(sy.k_far[gi & 7] == gi + 1, 0))
+                            cache_tc_own_scales<BF16, F>(a, sg, tile, __float_as_uint(sy.k_scale[gi & 7]) >> 23, s_at);
+                    }
                     uint32_t s[4][32];
 #pragma unroll
                     for (int c = 0; c < 4; ++c) tmem_ld32(s[c], s_at + c * 32);
@@ -610,6 +676,7 @@ __global__ void __launch_bounds__(CacheTcCfg<F, NQ, NC>::kThreads, 1)
             const long long s_page = kv ? a.c.vs_sp : a.c.ks_sp, s_token = kv ? a.c.vs_st : a.c.ks_st;
             const T* fresh = kv ? static_cast<const T*>(a.nv) + u.b * a.nv_sb + u.n * a.nv_sh : static_cast<const T*>(a.nk) + u.b * a.nk_sb + u.n * a.nk_sh;
             const long long f_token = kv ? a.nv_st : a.nk_st;
+            const int apart = kv ? 300 : Cfg::kApart;  // values share a sum: no scales of their own
             auto entry_of = [&](int i) {  // of this row at tile sg.first + i
                 const int token = (sg.first + i) * kTcRows + row;
                 return i < sg.n && sg.first + i < u.cache_tiles && token < u.length ? cache_entry(a.c, u.b, token) : kCacheNoPage;
@@ -636,19 +703,7 @@ __global__ void __launch_bounds__(CacheTcCfg<F, NQ, NC>::kThreads, 1)
                 entry1 = entry2, entry2 = entry_of(i + 3);
                 if (tail) {
                     there = j < sg.tail_keys;
-                    uint32_t top = 0;
-                    if (there) {
-#pragma unroll 4
-                        for (int d = 0; d < a.D; d += 8) {
-                            const uint4 y = *reinterpret_cast<const uint4*>(fresh + j * f_token + d);
-                            const uint32_t mm = 0x7fff7fffu;
-                            top = __vmaxu2(top, __vmaxu2(__vmaxu2(y.x & mm, y.y & mm), __vmaxu2(y.z & mm, y.w & mm)));
-                        }
-                    }
-                    top = max(top & 0xffffu, top >> 16);
-                    const float y = BF16 ? __uint_as_float(top << 16) : __half2float(__ushort_as_half((unsigned short)top));
-                    const int e = (int)(__float_as_uint(y) >> 23);
-                    byte = e == 255 ? 255u : (uint32_t)max(e - 8, 27);
+                    byte = there ? cache_new_byte<BF16>(fresh + j * f_token, a.D) : 27u;
                 }
                 // the tile's largest scale, and where it is read
                 const uint32_t mine = __reduce_max_sync(0xffffffffu, there && byte != 255u ? byte : 0u);
@@ -671,8 +726,9 @@ __global__ void __launch_bounds__(CacheTcCfg<F, NQ, NC>::kThreads, 1)
                         if (idx >= ST && !tc_bar_wait(tc_smem(&sy.empty[st]), (idx / ST - 1) & 1, abort, err)) return false;
                         const unsigned char* from = raw + rs * Cfg::kRawBytes + row * (NC * 64);
                         // 2^(byte - most) in f16; a row that held no numbers: NaN; byte 0: zeros
-                        const float f = byte == 255u ? __uint_as_float(0x7fffffffu)
-                                                        : byte == 0u || byte + 126u < most ? 0.f : cache_scale(127u + byte - most);
+                        const int below = (int)(most - byte);
+                        const bool far = below > apart && byte != 0u;  // goes in at its own scale
+                        const float f = byte == 255u ? __uint_as_float(0x7fffffffu) : far ? 1.f : byte == 0u || below > 126 ? 0.f : cache_scale(127 - below);
                         const __half2 scale = __half2half2(__float2half_rn(f));
                         const __half2 off = __hmul2(scale, __half2half2(__ushort_as_half(0xe480)));  // -1152
 #pragma unroll 1
@@ -706,6 +762,8 @@ __global__ void __launch_bounds__(CacheTcCfg<F, NQ, NC>::kThreads, 1)
                         }
                         tc_fence_async();
                         __syncwarp();
+                        if (far) sy.k_far[gi & 7] = gi + 1;
+                        __syncwarp();
                         if (lane == 0) {
                             tc_bar_arrive(tc_smem(&sy.full[st]));
                             tc_bar_arrive(tc_smem(&sy.raw_empty[rs]));
@@ -713,7 +771,8 @@ __global__ void __launch_bounds__(CacheTcCfg<F, NQ, NC>::kThreads, 1)
                     } else {
                         if (idx >= ST && !tc_bar_wait(tc_smem(&sy.empty[st]), (idx / ST - 1) & 1, abort, err)) return false;
                         const T* p = fresh + j * f_token;
-                        const float f = most == 0u ? 0.f : cache_scale(254u - most);
+                        const bool far = kv == 0 && there && byte + Cfg::kApartNew < most;
+                        const float f = most == 0u ? 0.f : cache_scale(254u - (far ? byte : most));
 #pragma unroll 2
                         for (int d = 0; d < NC * 64; d += 8) {
                             uint4 y = make_uint4(0, 0, 0, 0);
@@ -733,6 +792,7 @@ __global__ void __launch_bounds__(CacheTcCfg<F, NQ, NC>::kThreads, 1)
                             *reinterpret_cast<uint4*>(to + (d / 64) * kTcTile + ((((d / 8) & 7) ^ (row & 7)) << 4)) = y;
                         }
                         tc_fence_async();
+                        if (far) sy.k_far[gi & 7] = gi + 1;
                         __syncwarp();
                         if (lane == 0) tc_bar_arrive(tc_smem(&sy.full[st]));
                     }
