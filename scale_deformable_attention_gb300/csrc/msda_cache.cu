@@ -283,7 +283,7 @@ __global__ void __launch_bounds__(kMoveThreads, sizeof(T) == 4 ? 3 : 4) msda_cac
                     uint4 y = x[i][w];
                     if constexpr (F != kCacheSame) {
                         const uint32_t byte = __shfl_sync(0xffffffffu, bytes, (r & 15) + 16 * w), c[2] = {y.x, y.y};
-                        const float s = byte == 255u ? __uint_as_float(0x7fffffffu) : cache_scale(byte);
+                        const float s = cache_row_scale(byte);
                         float v[E];
 #pragma unroll
                         for (int e = 0; e < E / 4; ++e) {

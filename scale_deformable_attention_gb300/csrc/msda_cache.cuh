@@ -206,7 +206,8 @@ __device__ __forceinline__ void cache_walk(const CacheArgs& a, const CacheStart&
 
 // ---- codes ----
 
-__device__ __forceinline__ float cache_scale(uint32_t byte) { return __uint_as_float(byte << 23); }  // 255: infinite, and with codes of 0 NaN
+__device__ __forceinline__ float cache_scale(uint32_t byte) { return __uint_as_float(byte << 23); }  // of bytes below 255
+__device__ __forceinline__ float cache_row_scale(uint32_t byte) { return byte == 255u ? __uint_as_float(0x7fffffffu) : cache_scale(byte); }  // 255: NaN
 
 // two codes (the low 16 bits) as f16, exactly
 __device__ __forceinline__ uint32_t cache_e4m3_f16(uint32_t two) {

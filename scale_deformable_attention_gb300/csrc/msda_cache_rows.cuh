@@ -420,18 +420,32 @@ struct CacheWalk {
 #pragma unroll
                         for (int e = 0; e < 4; ++e) z.o[t][d][e] *= f;
             }
-            const uint32_t bytes = k_byte | (v_byte << 8), pair = bytes | (__shfl_down_sync(0xffffffffu, bytes, 1) << 16);
+            const uint32_t below = v_byte == 0u ? 0u : (uint32_t)max((int)(127u + v_byte - z.top), 0) & 255u;  // this lane's key
+            const uint32_t bytes = k_byte | (below << 8), pair = bytes | (__shfl_down_sync(0xffffffffu, bytes, 1) << 16);
 #pragma unroll
             for (int j = 0; j < NT; ++j) {
                 const uint32_t two = __shfl_sync(0xffffffffu, pair, j * 8 + 2 * c);
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    const uint32_t y = e ? two >> 16 : two & 0xffffu, w = y >> 8;
+                    const uint32_t y = e ? two >> 16 : two & 0xffffu;
                     const float ks = cache_scale(y & 255u);
-                    vs[j][e] = w == 255u ? cache_scale(255u) : w == 0u ? 0.f : cache_scale((uint32_t)max((int)(127 + w - z.top), 0));
+                    vs[j][e] = cache_scale(y >> 8);
 #pragma unroll
                     for (int t = 0; t < MT; ++t) s[t][j][e] *= ks, s[t][j][2 + e] *= ks;
                 }
+            }
+            if (__builtin_expect(__any_sync(0xffffffffu, k_byte == 255u || v_byte == 255u), 0)) {  // rows that are NaN, whatever their codes
+#pragma unroll
+                for (int j = 0; j < NT; ++j)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const uint32_t kb = __shfl_sync(0xffffffffu, k_byte, j * 8 + 2 * c + e), vb = __shfl_sync(0xffffffffu, v_byte, j * 8 + 2 * c + e);
+                        vs[j][e] = vb == 255u ? cache_row_scale(255u) : vs[j][e];
+#pragma unroll
+                        for (int t = 0; t < MT; ++t)
+#pragma unroll
+                            for (int h = 0; h < 2; ++h) s[t][j][2 * h + e] = kb == 255u ? cache_row_scale(255u) : s[t][j][2 * h + e];
+                    }
             }
         }
         if (i >= cached) {
