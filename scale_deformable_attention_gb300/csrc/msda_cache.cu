@@ -152,6 +152,13 @@ __device__ __forceinline__ float cache_top_value(uint32_t top) {
     }
 }
 
+// x brought into -most..most; NaN stays NaN (a code of another program's may be one).
+__device__ __forceinline__ float cache_clamp(float x, float most) {
+    asm("max.NaN.f32 %0, %0, %1;" : "+f"(x) : "f"(-most));
+    asm("min.NaN.f32 %0, %0, %1;" : "+f"(x) : "f"(most));
+    return x;
+}
+
 // U rows of K and of V at a time a lane.
 template <typename T, int F>
 __global__ void __launch_bounds__(kMoveThreads, sizeof(T) == 4 ? 3 : 4) msda_cache_write_kernel(const CacheMoveArgs a) {
@@ -294,7 +301,7 @@ __global__ void __launch_bounds__(kMoveThreads, sizeof(T) == 4 ? 3 : 4) msda_cac
                         }
                         if (s * 512.f > CacheVec<T>::most()) {  // a code may be rounded up past the type's range: finite rows stay finite
 #pragma unroll
-                            for (int e = 0; e < E; ++e) v[e] = fminf(fmaxf(v[e], -CacheVec<T>::most()), CacheVec<T>::most());
+                            for (int e = 0; e < E; ++e) v[e] = cache_clamp(v[e], CacheVec<T>::most());
                         }
                         y = CacheVec<T>::put(v);
                     }
