@@ -640,7 +640,7 @@ __global__ void __launch_bounds__(kCacheWarps * 32, CacheRowsCfg<T, F, DP, MT>::
                     }
                     top = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top)));
                     const int e = (int)(__float_as_uint(top) >> 23);  // 2^(e - 127) <= top
-                    const float by = e > 0 && e < 255 ? __uint_as_float((uint32_t)min(max(268 - e, 27), 227) << 23) : 1.f;
+                    const float by = e > 0 && e < 255 ? __uint_as_float((uint32_t)min(268 - e, 227) << 23) : 1.f;
                     if (lane == 0) {
                         up[r] = by;
                         factor[r] = fmaxf(a.c2 * (1.f / by), 1e-37f);  // a power of two: exact; never 0, which would make NaN of what is hidden

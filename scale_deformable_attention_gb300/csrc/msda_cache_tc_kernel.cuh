@@ -275,7 +275,7 @@ __global__ void __launch_bounds__(CacheTcCfg<F, NQ, NC>::kThreads, 1)
                         top = __vmaxu2(top, __vmaxu2(__vmaxu2(x[k].x & mm, x[k].y & mm), __vmaxu2(x[k].z & mm, x[k].w & mm)));
                     }
                     const int e = (int)(max(top & 0xffffu, top >> 16) >> 7);
-                    const float up = e > 0 && e < 255 ? __uint_as_float((uint32_t)min(max(268 - e, 27), 227) << 23) : 1.f;
+                    const float up = e > 0 && e < 255 ? __uint_as_float((uint32_t)min(268 - e, 227) << 23) : 1.f;
                     c2 = a.c2 * (1.f / up);
                     if (row < rows) {
 #pragma unroll
