@@ -137,7 +137,7 @@ def cache_write(cache: PagedCache, key: torch.Tensor, value: torch.Tensor, table
     A quantised cache's rows get the least power of two as scale that brings them into the codes' range.
     """
     fmt, dev, sh, strides, places = _pages(cache)
-    _no_gradient(key, value)
+    _no_gradient(cache.key, cache.value, key, value)
     if key.dim() != 4:
         raise ValueError(f"key must be [B, T, heads, D], got {tuple(key.shape)}")
     B, T, N, D = key.shape
@@ -165,6 +165,7 @@ def cache_read(cache: PagedCache, table: torch.Tensor, lengths: torch.Tensor, ro
     """(key, value) [B, rows, N, D]: the first ``rows`` tokens of each sequence, zeros from ``lengths`` [B] (int32) on (C ABI
     ``msda_cache_read``).  ``dtype``: that of the result for a quantised cache (bfloat16 if None)."""
     fmt, dev, sh, strides, places = _pages(cache)
+    _no_gradient(cache.key, cache.value)
     if dtype is None:
         dtype = cache.key.dtype if fmt == _lib.CACHE_SAME else torch.bfloat16
     dt = _float_dtype(dtype, fmt, cache)
@@ -196,7 +197,7 @@ def cache_attention(query: torch.Tensor, cache: PagedCache, table: torch.Tensor,
     width if None).
     """
     fmt, dev, sh, strides, places = _pages(cache)
-    _no_gradient(query, key, value)
+    _no_gradient(cache.key, cache.value, query, key, value)
     if query.dim() != 4:
         raise ValueError(f"query must be [B, T, heads, D], got {tuple(query.shape)}")
     B, T, M, D = query.shape
