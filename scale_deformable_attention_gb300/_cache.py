@@ -6,6 +6,7 @@ import math
 from typing import NamedTuple, Optional, Tuple
 
 import torch
+from torch.autograd import forward_ad
 
 from . import _lib
 from ._binding import DTYPE_CODE, stream, workspace_of
@@ -122,8 +123,11 @@ def _float_dtype(dtype: torch.dtype, fmt: int, cache: PagedCache) -> int:
 
 
 def _no_gradient(*tensors):
+    reverse, forward = torch.is_grad_enabled(), forward_ad._current_level >= 0
+    if not (reverse or forward):
+        return
     for t in tensors:
-        if t is not None and t.requires_grad and torch.is_grad_enabled():
+        if t is not None and (reverse and t.requires_grad or forward and forward_ad.unpack_dual(t).tangent is not None):
             raise ValueError("the cache's operators have no gradient: call them under torch.no_grad() or detach the tensors")
 
 
