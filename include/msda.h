@@ -522,7 +522,9 @@ msda_status msda_cache_read(msda_dtype dt, int format, const msda_cache_problem*
  * or 2^-13.5 (up to 16 rows a key head), in proportion to the tokens; fp32 adds
  * up outputs of 16 tokens at a time, rounded.  Probabilities are rounded
  * to 16 bits for their product: those of fp16 and of quantised caches to fp16
- * (half a step, or 2^-33 of a row's largest), bf16 over a bf16 cache to bf16; fp32
+ * (half a step, or 2^-33 of the largest in a row's tile, 2^-37 up to 16 rows a key
+ * head; a row of which one key has all but 1/128 keeps what its other tiles hold),
+ * bf16 over a bf16 cache to bf16; fp32
  * runs in two fp16 pieces (quantised) or three bf16 pieces a value, products
  * below 2^-22 of a value left out.  In a quantised cache this goes for a
  * probability times its value's scale, against the largest of both that a warp or

@@ -32,9 +32,11 @@
 // the outputs of 16 keys are summed anew and added in binary32 (480 sequences of
 // 67200 tokens, e4m3, positive values: low by 5e-5 without that); scores run
 // through the D / 16 products of a key in one sum.  P is rounded to 16 bits for its product (binary32: 2 pieces of f16
-// or 3 of bf16).  f16 P: m lies 2^8 below the row's maximum when it was looked
-// for, and is looked for again when a lane's P of a row add up to more than 2^14:
-// a P is off by half a step or 2^-33 of the row's largest.
+// or 3 of bf16).  f16 P: m lies 2^12 below the row's maximum when it was looked
+// for, and is looked for again when a lane's P of a row add up to more than 1.5 2^15:
+// a P is off by half a step or 2^-37 of the row's largest.  That loses a row's
+// output where one key outweighs the others while its value is small; rows of
+// which one key has all but 1/128 take a lower m for steps that fall far below.
 #pragma once
 
 #include "msda_cache.cuh"
@@ -69,9 +71,15 @@ struct CacheProduct {
     static constexpr bool bf16 = F == kCacheSame && CacheType<T>::code != 1;
     static constexpr int es = F == kCacheSame ? (int)sizeof(T) : 1;
     static constexpr int qp = !f32 ? 1 : F == kCacheSame ? 3 : 2, kp = f32 && F == kCacheSame ? 3 : 1, pp = qp;
-    static constexpr float below = bf16 ? 0.f : 8.f;  // m below the maximum, in binary places
+    // m below the maximum, in binary places, and what a lane's probabilities of a row may add up to in a step before m follows: f16 holds
+    // 65504, eight equal ones at the maximum are 2^15
+    static constexpr float below = bf16 ? 0.f : 12.f, most = bf16 ? 16384.f : 49152.f;
+    // f16, rows that one key outweighs (all but `alone` of the sum): the smallest sum of a lane's keys, how far a step's maximum lies
+    // below m before m goes down for it, m below it then (binary32 over codes: two pieces, that is 2^-24 of a sum of 4 or more), and what
+    // keeps O under 2^127: l before, m's way
+    static constexpr float low = f32 ? 4.f : 0x1p-7f, drop = f32 ? 0.f : 6.f, below_low = f32 ? 8.f : 3.f;
+    static constexpr float most_l = 0x1p40f, way = 56.f, alone = 0x1p-7f;
 };
-constexpr float kCacheMost = 16384.f;  // what a lane's probabilities of a row may add up to in a step before m follows
 
 template <typename T, int F, int DP, int MT>
 struct CacheRowsCfg {
@@ -161,6 +169,7 @@ template <int DP, int MT>
 struct CacheState {
     float o[MT][DP / 8][4];
     float m[MT][2], l[MT][2];
+    float low[MT][2], alone[MT][2];  // f16: a lane's sum that asks for a lower m (0: none), the largest key's part of the row's sum
     uint32_t top;  // 8 bits: O is in units of the scale of this byte (the largest met)
 };
 constexpr float kCacheNone = -1e30f;  // m before any score
@@ -501,9 +510,23 @@ struct CacheWalk {
                             p[t][j][2 * h + e] = x;
                             sum[t][h] += x;
                         }
-                    renew |= !(sum[t][h] <= kCacheMost);
+                    renew |= !(sum[t][h] <= P::most && (P::bf16 || sum[t][h] >= z.low[t][h]));
                 }
-            if (pass > 0 || !__any_sync(0xffffffffu, renew)) break;
+            if (pass > 0) {
+                if constexpr (!P::bf16) {
+#pragma unroll
+                    for (int t = 0; t < MT; ++t)
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            float all = z.l[t][h] + sum[t][h];
+                            all += __shfl_xor_sync(0xffffffffu, all, 1);
+                            all += __shfl_xor_sync(0xffffffffu, all, 2);
+                            z.low[t][h] = all - z.alone[t][h] < z.alone[t][h] * P::alone && all < P::most_l ? P::low : 0.f;
+                        }
+                }
+                break;
+            }
+            if (!__any_sync(0xffffffffu, renew)) break;
 #pragma unroll
             for (int t = 0; t < MT; ++t)
 #pragma unroll
@@ -513,8 +536,14 @@ struct CacheWalk {
                     for (int j = 0; j < NT; ++j) top = fmaxf(top, fmaxf(s[t][j][2 * h], s[t][j][2 * h + 1]));
                     top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
                     top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-                    const float m = fmaxf(z.m[t][h], top * f[t][h] - P::below);
+                    top *= f[t][h];
+                    float m = fmaxf(z.m[t][h], top - P::below);
+                    if constexpr (!P::bf16) {
+                        if (m > z.m[t][h]) z.alone[t][h] = exp2f(P::below);
+                        if (z.low[t][h] > 0.f && top < z.m[t][h] - P::drop && top > z.m[t][h] - P::way) m = top - P::below_low;
+                    }
                     const float by = m == z.m[t][h] ? 1.f : cache_ex2(z.m[t][h] - m);
+                    if (!P::bf16 && m < z.m[t][h]) z.alone[t][h] *= by;
                     z.m[t][h] = m;
                     z.l[t][h] *= by;
 #pragma unroll
@@ -685,7 +714,7 @@ __global__ void __launch_bounds__(kCacheWarps * 32, CacheRowsCfg<T, F, DP, MT>::
 #pragma unroll
         for (int t = 0; t < MT; ++t) {
 #pragma unroll
-            for (int h = 0; h < 2; ++h) z.m[t][h] = kCacheNone, z.l[t][h] = 0.f;
+            for (int h = 0; h < 2; ++h) z.m[t][h] = kCacheNone, z.l[t][h] = z.low[t][h] = z.alone[t][h] = 0.f;
 #pragma unroll
             for (int d = 0; d < DP / 8; ++d)
 #pragma unroll

@@ -30,7 +30,10 @@
 //
 // The reference m follows when a row's sum over a tile passes a limit, as in the
 // dense forward: P is in f16 at most 49152 and m 2^8 below the maximum when it is
-// looked for, in bf16 2^14.
+// looked for, in bf16 2^14.  f16 loses what lies 2^33 below the reference, and a
+// row's output with it where one key outweighs the others while its value is
+// small.  Such rows, one key with all but 1/128 of the sum so far, have a lower
+// limit too: a tile below it gets an m of its own, O and l going up.
 #pragma once
 
 #include <cuda.h>
@@ -49,6 +52,9 @@ template <bool OB>
 struct CacheTcRange {
     static constexpr float kTop = OB ? 16384.f : 49152.f;  // the largest sum of a row over a tile; f16 holds 65504
     static constexpr float kBelow = OB ? 0.f : 8.f;        // m below the maximum: 128 equal ones add up to 2^15
+    // f16, rows that one key outweighs (all but kAlone of the sum), as in the dense forward: the smallest sum of a tile, m below its
+    // maximum when it goes down for one, and what keeps O under 2^127: l before, m's way
+    static constexpr float kLow = 0x1p-7f, kBelowLow = 3.f, kMostL = 0x1p40f, kWay = 56.f, kAlone = 0x1p-7f;
 };
 
 template <int F, int NQ, int NC>
@@ -60,8 +66,10 @@ struct CacheTcCfg {  // stages are even in number: K has the even ones, V the od
     static constexpr int kThreads = NQ * 128 + 128 + (kCodes ? 256 : 0);
     static constexpr uint32_t kTileBytes = NC * kTcTile, kRawBytes = NC * 64 * 128;
     // Registers of a thread of the warpgroups on the scores, of the one that issues and of the two that convert: with codes the launch
-    // of four warpgroups has 128 a thread, unquantised with two row tiles 168 of three; with one row tile 255, and no split.
-    static constexpr int kUp = kCodes ? 208 : NQ == 1 ? 0 : 208, kDown = kCodes ? 56 : 88, kConvert = 120;
+    // of four warpgroups has 128 a thread, unquantised with two row tiles 168 of three; with one row tile 255, and no split.  (Codes at
+    // 208/56/120, 224/48/120, 232/56/112, us: e4m3 piece of 1100 over 2 x 8191 of 64 channels 137.5, 130.5, 131.4; int8 tree of 16
+    // over 16 x 16641 of 128 channels 101.6, 99.8, 101.9.)
+    static constexpr int kUp = kCodes ? 224 : NQ == 1 ? 0 : 208, kDown = kCodes ? 48 : 88, kConvert = 120;
     static_assert(!kCodes || kUp + kDown + 2 * kConvert <= 512, "more registers than the launch has");
     static_assert(kCodes || NQ == 1 || NQ * kUp + kDown <= 504, "more registers than the launch has");
     // tensor memory: S (128 columns a row tile), P (64), O (64 or 128); two row tiles of up to 128 channels leave no room
@@ -292,7 +300,8 @@ __global__ void __launch_bounds__(CacheTcCfg<F, NQ, NC>::kThreads, 1)
                     tc_bar_arrive_if(first, tc_smem(&sy.q_full));
                 }
             }
-            float m = -attn_inf(), l = 0.f;
+            // reference, sum; f16: the sum of a tile that asks for a lower reference (0: none), the largest key's part of l
+            float m = -attn_inf(), l = 0.f, low = 0.f, alone = 0.f;
             uint32_t v_ref = 0;
 #pragma unroll 1
             for (int i = 0; i < sg.n; ++i) {
@@ -416,8 +425,13 @@ __global__ void __launch_bounds__(CacheTcCfg<F, NQ, NC>::kThreads, 1)
                                     mx[c] = tc_max3(mx[c], __uint_as_float(s[c][k]), __uint_as_float(s[c][k + 1]));
                             }
                             const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * ct;
-                            const float next = fmaxf(m, top - Range::kBelow);
+                            float next = fmaxf(m, top - Range::kBelow);
+                            if constexpr (!OB) {
+                                if (next > m) alone = exp2f(Range::kBelow);
+                                if (low > 0.f && top < m - 6.f && top > m - Range::kWay) next = top - Range::kBelowLow;
+                            }
                             const float f = next == m ? 1.f : tc_ex2(m - next);
+                            if (!OB && next < m) alone *= f;
                             m = next;
                             l *= f;
                             if (i > 0) {
@@ -438,11 +452,15 @@ __global__ void __launch_bounds__(CacheTcCfg<F, NQ, NC>::kThreads, 1)
                         }
                         sum = probabilities(fresh);
                         fresh = false;
-                        renew = __any_sync(0xffffffffu, valid && !(sum <= Range::kTop));
+                        const bool fits = sum <= Range::kTop;
+                        if constexpr (CODES) sum *= exp2f(-dv);
+                        if constexpr (!OB) {
+                            if (renew) low = l + sum - alone < alone * Range::kAlone && l < Range::kMostL ? Range::kLow : 0.f;
+                        }
+                        renew = __any_sync(0xffffffffu, valid && !(fits && (OB || sum >= low)));
                         if (!renew) break;
                     }
                     if (__builtin_expect(gone, 0)) return false;
-                    if constexpr (CODES) sum *= exp2f(-dv);
                     l += sum;
                     tmem_wait_st();
                     tc_fence_before();
