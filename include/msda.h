@@ -484,7 +484,10 @@ enum { MSDA_CACHE_SAME = 0, MSDA_CACHE_E4M3 = 1, MSDA_CACHE_INT8 = 2 };
  * code, 2^-4 of it (e4m3, down to 2^-6 s) or s / 2 (int8).  A power of two
  * costs e4m3 nothing (its steps follow the value) and makes every code times its
  * scale a value that 16 bits hold.
- * Two sequences that write the same place in one call leave either's row.
+ * A place that two rows of one call go to (of two sequences, or of one whose table
+ * names a page twice), or whose memory another place shares, holds parts of either
+ * in any mixture, codes of one under the scale of another among them.  key and
+ * value may not overlap the cache.
  */
 msda_status msda_cache_write(msda_dtype dt, int format, const msda_cache_problem* problem, const void* key,
                              const void* value, const int32_t* table, const int32_t* start, const int32_t* counts,

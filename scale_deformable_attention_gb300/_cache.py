@@ -138,7 +138,8 @@ def cache_write(cache: PagedCache, key: torch.Tensor, value: torch.Tensor, table
     ``key``, ``value`` [B, T, N, D]; ``table`` [B, width] int32, the page numbers of each sequence; ``start`` [B] int32:
     token r of sequence b becomes its token start[b] + r.  ``counts`` [B] int32: how many tokens of each (all if None).
     ``select`` [B, R] int32: row r is token select[b, r] of ``key`` and ``value``, as for the accepted ones of a drafted tree.
-    A quantised cache's rows get the least power of two as scale that brings them into the codes' range.
+    A quantised cache's rows get the least power of two as scale that brings them into the codes' range.  A place that two
+    rows of one call go to holds parts of either in any mixture.
     """
     fmt, dev, sh, strides, places = _pages(cache)
     _no_gradient(cache.key, cache.value, key, value)
