@@ -516,25 +516,34 @@ msda_status msda_cache_read(msda_dtype dt, int format, const msda_cache_problem*
  *   mask [B or 1, T, T] bytes; counts [B] or NULL: rows t >= counts[b] are
  *       padding and give zeros and lse = -inf, as does a row that sees nothing.
  *       Padding may hold anything, NaN included, and so may what the cache holds
- *       behind lengths[b].  A NaN or infinity in a value that some query of a
- *       sequence sees reaches those that do not (0 * NaN), as in the matrix form.
+ *       behind lengths[b].  A NaN or infinity in a value of a sequence's tokens
+ *       (below lengths[b] in the cache, below counts[b] of the new ones) can reach
+ *       that channel of every query of the sequence, of those that do not see the
+ *       token too (0 * NaN), as in the matrix form.
  *
  * Sums, statistics and products accumulate in fp32.  The tensor cores cut their
  * sums off, towards zero, where others round to nearest: of positive values a
- * 16-bit output over 67200 tokens is low by 2^-11 (tcgen05, a block a sequence)
- * or 2^-13.5 (up to 16 rows a key head), in proportion to the tokens; fp32 adds
- * up outputs of 16 tokens at a time, rounded.  Probabilities are rounded
- * to 16 bits for their product: those of fp16 and of quantised caches to fp16
- * (half a step, or 2^-33 of the largest in a row's tile, 2^-37 up to 16 rows a key
- * head; a row of which one key has all but 1/128 keeps what its other tiles hold),
- * bf16 over a bf16 cache to bf16; fp32
- * runs in two fp16 pieces (quantised) or three bf16 pieces a value, products
- * below 2^-22 of a value left out.  In a quantised cache this goes for a
- * probability times its value's scale, against the largest of both that a warp or
- * tile meets; bf16 queries and new tokens there become fp16 times a power of two a
- * row or, for values, tile, elements below 2^-22 of its largest losing bits (a new key
- * more than 2^8 below its tile's largest: 2^-14 of its own).  Cached keys are exact,
- * at whatever scales; a cached value's code is cut below 2^-24 of its tile's largest scale.
+ * 16-bit output over 67200 tokens is low by 2^-11 (more than 16 rows, T M / N, a
+ * key head; a block walks the sequence alone) or 2^-13.5 (up to 16), in proportion
+ * to the tokens; fp32 adds up the outputs of 16 tokens at a time, rounded.
+ *   bf16 over a bf16 cache: probabilities are rounded to bf16 for their product.
+ *   fp16, and quantised caches: to fp16, half a step or 2^-33 of the largest in a
+ *       row's tile (2^-37 up to 16 rows a key head); a row of which one key has all
+ *       but 1/128 keeps what its other tiles hold.
+ *   Quantised caches: cached keys are exact, at whatever scales.  A probability is
+ *       held times its value's scale over the largest that a warp or tile meets, and
+ *       what that makes of it is rounded; with more than 16 rows a key head a code of
+ *       a value is cut below 2^-24 of its tile's largest scale.  bf16 queries become
+ *       fp16 times a power of two a row, new tokens fp16 times one a tile: elements
+ *       below 2^-22 of the largest lose bits (a new key more than 2^8 below its
+ *       tile's largest has one of its own: below 2^-14 of its largest).
+ *   fp32 over codes: queries and probabilities in two fp16 pieces.
+ *   fp32 over fp32, and its new tokens: three bf16 pieces a value, products below
+ *       2^-22 of a value left out.  A key, value or query there that is above bf16's
+ *       largest value, 3.39e38, counts as NaN, infinities among them (the dense form
+ *       takes infinities as such).
+ * Unquantised values of 2^112 and more can overflow fp32 before the division by
+ * the sum.
  * No atomics take part in a sum: equal
  * calls give equal bits; the order depends on the sizes and lengths.
  *
