@@ -734,14 +734,18 @@ __global__ void __launch_bounds__(kCacheWarps * 32, CacheRowsCfg<T, F, DP, MT>::
         if constexpr (CODES) {
             CacheWalk<T, F, DP, MT, Cfg::E, Cfg::EV, KS, Cfg::kStages> walk{a, u, my_ring, qf, factor, token_of, lane, first, cached, 0, 0, step, 0, 0, 0};
             walk.run(z, prepare);
-            if (z.top != 0) {  // back to units of 1
+            if (z.top != 0) {  // back to units of 1, with m where the largest key asks for it: a lower one makes large values infinite
                 const float f = cache_scale(z.top);
 #pragma unroll
                 for (int t = 0; t < MT; ++t)
 #pragma unroll
-                    for (int d = 0; d < DP / 8; ++d)
+                    for (int h = 0; h < 2; ++h) {
+                        const int e = max((int)(__float_as_uint(z.alone[t][h]) >> 23) - 127 - (int)P::below, 0);  // places that m went down
+                        const float by = cache_scale(127 - e);
+                        z.m[t][h] += e, z.l[t][h] *= by, z.alone[t][h] *= by;
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) z.o[t][d][e] *= f;
+                        for (int d = 0; d < DP / 8; ++d) z.o[t][d][2 * h] = z.o[t][d][2 * h] * by * f, z.o[t][d][2 * h + 1] = z.o[t][d][2 * h + 1] * by * f;
+                    }
             }
             if (fresh > 0) {
                 CacheWalk<T, kCacheSame, DP, MT, Cfg::E, Cfg::EV, KT, Cfg::kTailStages> walk{a, u, my_ring, qt, factor, token_of, lane, 0, 0, first_new, fresh, step_new, 0, 0, 0};

@@ -481,8 +481,7 @@ __global__ void __launch_bounds__(CacheTcCfg<F, NQ, NC>::kThreads, 1)
             g0 += sg.n;
             if (!__any_sync(0xffffffffu, there)) return true;
             const bool none = l == 0.f || !valid;
-            float inv = none ? 0.f : 1.f / l;
-            if constexpr (CODES) inv *= v_ref == 0 ? 0.f : cache_scale(v_ref);
+            const float inv = none ? 0.f : 1.f / l, unit = CODES ? cache_scale(v_ref) : 1.f;  // one after the other: their product may be below binary32
             const float l2 = none ? -attn_inf() : m + log2f(l);
             const long long at = (long long)sg.slot * a.tile_rows + t * rows + row;
 #pragma unroll 1
@@ -494,7 +493,7 @@ __global__ void __launch_bounds__(CacheTcCfg<F, NQ, NC>::kThreads, 1)
                 }
                 if (!there) continue;
 #pragma unroll
-                for (int k = 0; k < 16; ++k) o[k] = none ? 0u : __float_as_uint(__uint_as_float(o[k]) * inv);
+                for (int k = 0; k < 16; ++k) o[k] = none ? 0u : __float_as_uint(__uint_as_float(o[k]) * inv * unit);
                 if (sg.slot >= 0) {
                     float* out = a.part_o + at * a.D + c * 16;
 #pragma unroll
