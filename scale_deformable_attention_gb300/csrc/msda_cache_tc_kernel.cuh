@@ -737,82 +737,82 @@ __global__ void __launch_bounds__(CacheTcCfg<F, NQ, NC>::kThreads, 1)
                 }
                 const int idx = 2 * gi + kv, st = idx % ST;
                 unsigned char* to = ring + st * Cfg::kTileBytes + row * 128;
-                    if (!tail) {
-                        const int ri = 2 * r0 + kv, rs = ri % Cfg::kRaw;
-                        if (!tc_bar_wait(tc_smem(&sy.raw_full[rs]), (ri / Cfg::kRaw) & 1, abort, err)) return false;
-                        if (idx >= ST && !tc_bar_wait(tc_smem(&sy.empty[st]), (idx / ST - 1) & 1, abort, err)) return false;
-                        const unsigned char* from = raw + rs * Cfg::kRawBytes + row * (NC * 64);
-                        // 2^(byte - most) in f16; a row that held no numbers: NaN; byte 0: zeros
-                        const int below = (int)(most - byte);
-                        const bool far = below > apart && byte != 0u;  // goes in at its own scale
-                        const float f = byte == 255u ? __uint_as_float(0x7fffffffu) : far ? 1.f : byte == 0u || below > 126 ? 0.f : cache_scale(127 - below);
-                        const __half2 scale = __half2half2(__float2half_rn(f));
-                        const __half2 off = __hmul2(scale, __half2half2(__ushort_as_half(0xe480)));  // -1152
+                if (!tail) {
+                    const int ri = 2 * r0 + kv, rs = ri % Cfg::kRaw;
+                    if (!tc_bar_wait(tc_smem(&sy.raw_full[rs]), (ri / Cfg::kRaw) & 1, abort, err)) return false;
+                    if (idx >= ST && !tc_bar_wait(tc_smem(&sy.empty[st]), (idx / ST - 1) & 1, abort, err)) return false;
+                    const unsigned char* from = raw + rs * Cfg::kRawBytes + row * (NC * 64);
+                    // 2^(byte - most) in f16; a row that held no numbers: NaN; byte 0: zeros
+                    const int below = (int)(most - byte);
+                    const bool far = below > apart && byte != 0u;  // goes in at its own scale
+                    const float f = byte == 255u ? __uint_as_float(0x7fffffffu) : far ? 1.f : byte == 0u || below > 126 ? 0.f : cache_scale(127 - below);
+                    const __half2 scale = __half2half2(__float2half_rn(f));
+                    const __half2 off = __hmul2(scale, __half2half2(__ushort_as_half(0xe480)));  // -1152
 #pragma unroll 1
-                        for (int c0 = 0; c0 < NC * 4; c0 += 4) {  // 64 codes at a time, their loads first
-                            uint4 y[4];
+                    for (int c0 = 0; c0 < NC * 4; c0 += 4) {  // 64 codes at a time, their loads first
+                        uint4 y[4];
 #pragma unroll
-                            for (int c = 0; c < 4; ++c)
-                                y[c] = *reinterpret_cast<const uint4*>(from + ((NC == 2 ? (c0 + c) ^ (row & 7) : c ^ ((row >> 1) & 3)) << 4));
-                            unsigned char* at = to + (c0 / 4) * kTcTile;
+                        for (int c = 0; c < 4; ++c)
+                            y[c] = *reinterpret_cast<const uint4*>(from + ((NC == 2 ? (c0 + c) ^ (row & 7) : c ^ ((row >> 1) & 3)) << 4));
+                        unsigned char* at = to + (c0 / 4) * kTcTile;
 #pragma unroll
-                            for (int c = 0; c < 4; ++c) {
-                                const uint32_t w[4] = {y[c].x, y[c].y, y[c].z, y[c].w};
-                                uint32_t p[8];
+                        for (int c = 0; c < 4; ++c) {
+                            const uint32_t w[4] = {y[c].x, y[c].y, y[c].z, y[c].w};
+                            uint32_t p[8];
 #pragma unroll
-                                for (int k = 0; k < 4; ++k) {
-                                    __half2 y0, y1;
-                                    if constexpr (F == kCacheE4m3) {
-                                        uint32_t lo, hi;
-                                        cache_four_f16<F>(w[k], lo, hi);
-                                        y0 = __hmul2(*reinterpret_cast<const __half2*>(&lo), scale), y1 = __hmul2(*reinterpret_cast<const __half2*>(&hi), scale);
-                                    } else {  // (1024 + u) s - 1152 s, exact
-                                        const uint32_t v = w[k] ^ 0x80808080u, lo = __byte_perm(v, 0x64646464u, 0x4140), hi = __byte_perm(v, 0x64646464u, 0x4342);
-                                        y0 = __hfma2(*reinterpret_cast<const __half2*>(&lo), scale, off), y1 = __hfma2(*reinterpret_cast<const __half2*>(&hi), scale, off);
-                                    }
-                                    p[2 * k] = there ? *reinterpret_cast<const uint32_t*>(&y0) : 0u;  // behind the last row: zeros, whatever lies there
-                                    p[2 * k + 1] = there ? *reinterpret_cast<const uint32_t*>(&y1) : 0u;
+                            for (int k = 0; k < 4; ++k) {
+                                __half2 y0, y1;
+                                if constexpr (F == kCacheE4m3) {
+                                    uint32_t lo, hi;
+                                    cache_four_f16<F>(w[k], lo, hi);
+                                    y0 = __hmul2(*reinterpret_cast<const __half2*>(&lo), scale), y1 = __hmul2(*reinterpret_cast<const __half2*>(&hi), scale);
+                                } else {  // (1024 + u) s - 1152 s, exact
+                                    const uint32_t v = w[k] ^ 0x80808080u, lo = __byte_perm(v, 0x64646464u, 0x4140), hi = __byte_perm(v, 0x64646464u, 0x4342);
+                                    y0 = __hfma2(*reinterpret_cast<const __half2*>(&lo), scale, off), y1 = __hfma2(*reinterpret_cast<const __half2*>(&hi), scale, off);
                                 }
-                                *reinterpret_cast<uint4*>(at + (((2 * c) ^ (row & 7)) << 4)) = make_uint4(p[0], p[1], p[2], p[3]);
-                                *reinterpret_cast<uint4*>(at + (((2 * c + 1) ^ (row & 7)) << 4)) = make_uint4(p[4], p[5], p[6], p[7]);
+                                p[2 * k] = there ? *reinterpret_cast<const uint32_t*>(&y0) : 0u;  // behind the last row: zeros, whatever lies there
+                                p[2 * k + 1] = there ? *reinterpret_cast<const uint32_t*>(&y1) : 0u;
                             }
+                            *reinterpret_cast<uint4*>(at + (((2 * c) ^ (row & 7)) << 4)) = make_uint4(p[0], p[1], p[2], p[3]);
+                            *reinterpret_cast<uint4*>(at + (((2 * c + 1) ^ (row & 7)) << 4)) = make_uint4(p[4], p[5], p[6], p[7]);
                         }
-                        tc_fence_async();
-                        __syncwarp();
-                        if (far) sy.k_far[gi & 7] = gi + 1;
-                        __syncwarp();
-                        if (lane == 0) {
-                            tc_bar_arrive(tc_smem(&sy.full[st]));
-                            tc_bar_arrive(tc_smem(&sy.raw_empty[rs]));
-                        }
-                    } else {
-                        if (idx >= ST && !tc_bar_wait(tc_smem(&sy.empty[st]), (idx / ST - 1) & 1, abort, err)) return false;
-                        const T* p = fresh + j * f_token;
-                        const bool far = kv == 0 && there && byte + Cfg::kApartNew < most;
-                        const float f = most == 0u ? 0.f : cache_scale(254u - (far ? byte : most));
-#pragma unroll 2
-                        for (int d = 0; d < NC * 64; d += 8) {
-                            uint4 y = make_uint4(0, 0, 0, 0);
-                            if (there && d < a.D) {
-                                const uint4 v4 = *reinterpret_cast<const uint4*>(p + d);
-                                const uint32_t w[4] = {v4.x, v4.y, v4.z, v4.w};
-                                uint32_t z[4];
-#pragma unroll
-                                for (int k = 0; k < 4; ++k) {
-                                    float2 v;
-                                    if constexpr (BF16) v = make_float2(__uint_as_float(w[k] << 16), __uint_as_float(w[k] & 0xffff0000u));
-                                    else v = __half22float2(*reinterpret_cast<const __half2*>(&w[k]));
-                                    z[k] = tc_pack<false>(v.x * f, v.y * f);
-                                }
-                                y = make_uint4(z[0], z[1], z[2], z[3]);
-                            }
-                            *reinterpret_cast<uint4*>(to + (d / 64) * kTcTile + ((((d / 8) & 7) ^ (row & 7)) << 4)) = y;
-                        }
-                        tc_fence_async();
-                        if (far) sy.k_far[gi & 7] = gi + 1;
-                        __syncwarp();
-                        if (lane == 0) tc_bar_arrive(tc_smem(&sy.full[st]));
                     }
+                    tc_fence_async();
+                    __syncwarp();
+                    if (far) sy.k_far[gi & 7] = gi + 1;
+                    __syncwarp();
+                    if (lane == 0) {
+                        tc_bar_arrive(tc_smem(&sy.full[st]));
+                        tc_bar_arrive(tc_smem(&sy.raw_empty[rs]));
+                    }
+                } else {
+                    if (idx >= ST && !tc_bar_wait(tc_smem(&sy.empty[st]), (idx / ST - 1) & 1, abort, err)) return false;
+                    const T* p = fresh + j * f_token;
+                    const bool far = kv == 0 && there && byte + Cfg::kApartNew < most;
+                    const float f = most == 0u ? 0.f : cache_scale(254u - (far ? byte : most));
+#pragma unroll 2
+                    for (int d = 0; d < NC * 64; d += 8) {
+                        uint4 y = make_uint4(0, 0, 0, 0);
+                        if (there && d < a.D) {
+                            const uint4 v4 = *reinterpret_cast<const uint4*>(p + d);
+                            const uint32_t w[4] = {v4.x, v4.y, v4.z, v4.w};
+                            uint32_t z[4];
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) {
+                                float2 v;
+                                if constexpr (BF16) v = make_float2(__uint_as_float(w[k] << 16), __uint_as_float(w[k] & 0xffff0000u));
+                                else v = __half22float2(*reinterpret_cast<const __half2*>(&w[k]));
+                                z[k] = tc_pack<false>(v.x * f, v.y * f);
+                            }
+                            y = make_uint4(z[0], z[1], z[2], z[3]);
+                        }
+                        *reinterpret_cast<uint4*>(to + (d / 64) * kTcTile + ((((d / 8) & 7) ^ (row & 7)) << 4)) = y;
+                    }
+                    tc_fence_async();
+                    if (far) sy.k_far[gi & 7] = gi + 1;
+                    __syncwarp();
+                    if (lane == 0) tc_bar_arrive(tc_smem(&sy.full[st]));
+                }
                 if (!tail) ++r0;
             }
             g0 += sg.n;
