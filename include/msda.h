@@ -543,7 +543,8 @@ msda_status msda_cache_read(msda_dtype dt, int format, const msda_cache_problem*
  *       largest value, 3.39e38, counts as NaN, infinities among them (the dense form
  *       takes infinities as such).
  * Unquantised values of 2^112 and more can overflow fp32 before the division by
- * the sum.
+ * the sum; over codes, scores of keys of 2^100 and more can, and query rows whose
+ * largest element is below 2^-86 lose bits.
  * No atomics take part in a sum: equal
  * calls give equal bits; the order depends on the sizes and lengths.
  *

@@ -2,15 +2,16 @@
 // msda_cache_write / _read / _attention, the kernels that write and read rows,
 // and the one that joins the parts of units which several blocks shared.
 //
-// Writing and reading are bound by memory: a row of D channels lies in the lanes
+// Reading is bound by memory, a quantised write by its arithmetic: a row of D channels lies in the lanes
 // that 16 bytes of the unquantised type each make, so its largest magnitude takes
 // log2(lanes) exchanges and every access is a whole vector.  A warp takes 16
 // tokens of a head, so that pages, places and scales are looked up once for them
 // by one lane each and handed on by shuffles; a block's warps take the heads of the
 // same tokens.  The cache's side (head by head) is then read or written in runs of
-// 16 rows, the other side in whole tokens.  8 x 22223 tokens of 8 heads of 64, e4m3 to bf16: 88 us, 85 % of the copy rate;
-// lookups in every lane took 132 us (ALU 51 % busy with addresses).  Four blocks an SM in 16 bits (three: 97 us), three in
-// binary32 (four: 29 us against 27 for 4 x 8191 tokens of 8 heads of 48).
+// 16 rows, the other side in whole tokens.  8 x 22223 tokens of 8 heads of 64, e4m3 to bf16: 86 us, 88 % of the copy rate,
+// bf16 97 us, 99 %; lookups in every lane took 132 us (ALU 51 % busy with addresses).  Prompts of 8 x up to 16641 tokens of 4
+// heads of 128 written: bf16 47 us, 91 %; to e4m3 55 us, 59 % (ALU 52 %: largest of a row, scale, codes).  Four blocks an SM in
+// 16 bits (three: 97 us), three in binary32 (four: 29 us against 27 for 4 x 8191 tokens of 8 heads of 48).
 #include <cuda_runtime.h>
 
 #include <cmath>
@@ -540,7 +541,7 @@ bool tma_strides(const int64_t* st, int64_t a, int64_t b, int64_t c, int64_t es)
 }
 
 // The tensor-core kernel's row tiles: 16-bit queries with more rows a key head than the mma.sync kernel has in a tile (32 rows there
-// took two: 8 x 16384 tokens, 4 key heads of 128: bf16 66 us against 60 here, e4m3 85 against 70; 16 rows 52 and 45).  Two row tiles a
+// take two: 8 x 16384 tokens, 4 key heads of 128: bf16 95 us against 61 here, e4m3 75 against 67; 16 rows 61 and 52).  Two row tiles a
 // block where one does not hold the rows, unquantised: keys are then read and multiplied for both.  With codes two row tiles leave too
 // few registers to convert a tile in its time (256 rows of 64 channels over 16384 tokens: 137 us against 126 as two units).
 int tc_tiles(msda_dtype dt, int format, const msda_cache_problem* p, int64_t rows) {
@@ -569,6 +570,10 @@ CachePlan plan_of(msda_dtype dt, int format, const msda_cache_problem* p) {
     c.units = p->B * p->N * c.row_tiles;
     c.most_tiles = (longest_of(p) + c.shape.tile_keys - 1) / c.shape.tile_keys + (p->source + c.shape.tail_keys - 1) / c.shape.tail_keys;
     if (c.most_tiles < 1) c.most_tiles = 1;
+    // A block takes `least` tiles at least, and units of up to twice that run whole: a second launch and the parts cost about 6 us (2 x 256
+    // tokens 7.5 whole, 13.1 with blocks of 4 tiles).  One token of 16 heads on 4 of 128 channels, bf16, with `least` at half, this, twice,
+    // us: 2 x 512 tokens 12.1, 13.0, 15.9, 2 x 4096 15.6, 14.8, 16.4; trees of 16 over 2 x 512 12.7, 15.4, 17.2, over 8 x 4096 25.8
+    // each; a binary32 tree of 25 over 8 x 900 22.7, 24.3, 26.5.  Whole up to four times `least`: 2 x 512 10.2, but that tree 31.5.
     c.least = c.nq ? 2 : 4;
     c.whole = c.most_tiles <= 2 * c.least;
     const int64_t most = msda::kPlanSms * c.shape.resident, want = (c.units * c.most_tiles + c.least - 1) / c.least;

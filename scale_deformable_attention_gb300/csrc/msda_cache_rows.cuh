@@ -18,8 +18,8 @@
 // register brings next to each other: no transposing load.  16-byte chunks of a
 // row are swizzled by the row so that both reads are free of bank conflicts.
 //
-// Measured, one new token of 16 heads on 4 of 128 channels: 8 x 65536 tokens bf16 168 us (6.4 TB/s), e4m3 129 us (4.2 TB/s:
-// half the bytes, the same products and exponentials); 8 x 16384: 51 and 45 us.  About 8 us of each pass before a
+// Measured, one new token of 16 heads on 4 of 128 channels: 8 x 65536 tokens bf16 169 us (6.3 TB/s), e4m3 119 us (4.6 TB/s:
+// half the bytes, the same products and exponentials); 8 x 16384: 53 and 44 us, binary32 114 and, over e4m3, 69.  About 8 us of each pass before a
 // block's first product: code that runs once costs some 9 cycles an instruction to fetch (plan 2.5 us, first
 // copies 2.5, queries 1.2), so copies, products and exponentials stand in one place of the code each.
 //

@@ -24,8 +24,8 @@
 // bf16 queries of a quantised cache become f16 with a power of two a row.
 //
 // Measured, 16 heads on 4 of 128 channels over 8 x 65536 tokens: 64 rows a key head bf16 180 us (6.0 TB/s: memory), e4m3
-// 183 us (a tile of 128 keys takes 2800 cycles: the scores' threads, one a scheduler, follow their own latencies); 256 rows
-// bf16 245 us (1120 TFLOP/s, 3700 cycles a tile of two row tiles).  8 x 16384 tokens: 60, 70 and 84 us, of which 8 pass
+// 180 us (a tile of 128 keys takes 2800 cycles: the scores' threads, one a scheduler, follow their own latencies); 256 rows
+// bf16 255 us (1080 TFLOP/s, 3700 cycles a tile of two row tiles).  8 x 16384 tokens: 61, 69 and 90 us, of which 8 pass
 // before the first product (code fetched, plan, queries) and 3 in the parts' writing.
 //
 // The reference m follows when a row's sum over a tile passes a limit, as in the
