@@ -532,11 +532,11 @@ msda_status msda_cache_read(msda_dtype dt, int format, const msda_cache_problem*
  *       but 1/128 keeps what its other tiles hold.
  *   Quantised caches: cached keys are exact, at whatever scales.  A probability is
  *       held times its value's scale over the largest that a warp or tile meets, and
- *       what that makes of it is rounded; with more than 16 rows a key head a code of
- *       a value is cut below 2^-24 of its tile's largest scale.  bf16 queries become
- *       fp16 times a power of two a row, new tokens fp16 times one a tile: elements
- *       below 2^-22 of the largest lose bits (a new key more than 2^8 below its
- *       tile's largest has one of its own: below 2^-14 of its largest).
+ *       what that makes of it is rounded; with more than 16 rows a key head codes of
+ *       values are cut at 2^-31 (e4m3) or 2^-29 (int8) of their tile's largest scale,
+ *       and scales below that are 0.  bf16 queries become fp16 times a power of two
+ *       a row, new tokens fp16 times one a tile: elements below 2^-27 of the largest
+ *       lose bits (of a new key only those below 2^-14 of its own largest).
  *   fp32 over codes: queries and probabilities in two fp16 pieces.
  *   fp32 over fp32, and its new tokens: three bf16 pieces a value, products below
  *       2^-22 of a value left out.  A key, value or query there that is above bf16's

@@ -14,13 +14,14 @@
 //     a row tile its products;
 //   - unquantised: one clears the value rows that lie behind a sequence's last;
 //   - 8 bits: a warpgroup turns the codes of a tile, a row a thread, into f16 rows
-//     of the operands, brought to the scale of the tile's largest row: the scores
-//     of the tile are multiplied by that scale of K, its P by that of V over the
-//     largest met.  New tokens' rows go the same way.  Codes 2^15 (e4m3) or 2^24
-//     (int8) below are still exact.  A key whose scale lies further below, as next
+//     of the operands, the tile's largest scale being 2^7 (e4m3) or 2^5 (int8) of
+//     theirs: the scores of the tile are multiplied by that scale of K, its P by
+//     that of V over the largest met.  New tokens' rows go the same way.  Codes
+//     2^22 or 2^29 below are still exact.  A key whose scale lies further below, as next
 //     to one of nothing but a large channel, goes in at its own scale, and its
 //     column of scores is multiplied by that (such scores were 0 from 2^25 on
-//     otherwise); values of P V share a sum and lose bits there.
+//     otherwise); values of P V share a sum: codes are cut at 2^-31 (2^-29) of the
+//     largest scale, scales below that are 0.
 // bf16 queries of a quantised cache become f16 with a power of two a row.
 //
 // Measured, 16 heads on 4 of 128 channels over 8 x 65536 tokens: 64 rows a key head bf16 180 us (6.0 TB/s: memory), e4m3
@@ -79,9 +80,11 @@ struct CacheTcCfg {  // stages are even in number: K has the even ones, V the od
     static constexpr uint32_t kO = kOwnP ? NQ * 192 : NQ * 128;
     static constexpr uint32_t kCols = NQ == 2 || NC == 2 ? 512 : 256;
     static constexpr size_t kSmem = (size_t)(NQ + kStages) * kTileBytes + (size_t)kRaw * kRawBytes + 1024;
-    // binary places that a key may lie below the tile's largest and share its scale: codes stay exact in f16 (e4m3: 2^-9 2^-15, int8:
-    // 1 2^-24); new tokens, whose rows begin at 2^8, keep 2^-14 of their own largest in full
-    static constexpr int kApart = F == kCacheE4m3 ? 15 : 24, kApartNew = 8;
+    // The tile's largest scale in the operands' f16: 448 2^7 (new tokens: 65504) and 127 2^5 are within it, and so is the 1152 that
+    // int8 codes pass by.  Binary places that a key may lie below and share it: codes stay exact (e4m3: 2^-9 2^(7 - 22), int8: 2^(5 - 29));
+    // new tokens, whose rows then begin at 1, keep 2^-14 of their own largest in full.
+    static constexpr int kLift = F == kCacheE4m3 ? 7 : 5;
+    static constexpr int kApart = kLift + (F == kCacheE4m3 ? 15 : 24), kApartNew = kLift + 8;
 };
 
 struct CacheTcSync {
@@ -346,7 +349,7 @@ __global__ void __launch_bounds__(CacheTcCfg<F, NQ, NC>::kThreads, 1)
                 if (warp_on) {
                     if constexpr (CODES) {
                         if (__builtin_expect(sy.k_far[gi & 7] == gi + 1, 0))
-                            cache_tc_own_scales<BF16, F>(a, sg, tile, __float_as_uint(sy.k_scale[gi & 7]) >> 23, s_at);
+                            cache_tc_own_scales<BF16, F>(a, sg, tile, (__float_as_uint(sy.k_scale[gi & 7]) >> 23) + Cfg::kLift, s_at);
                     }
                     uint32_t s[4][32];
 #pragma unroll
@@ -481,7 +484,7 @@ __global__ void __launch_bounds__(CacheTcCfg<F, NQ, NC>::kThreads, 1)
             g0 += sg.n;
             if (!__any_sync(0xffffffffu, there)) return true;
             const bool none = l == 0.f || !valid;
-            const float inv = none ? 0.f : 1.f / l, unit = CODES ? cache_scale(v_ref) : 1.f;  // one after the other: their product may be below binary32
+            const float inv = none ? 0.f : 1.f / l, unit = !CODES ? 1.f : v_ref > Cfg::kLift ? cache_scale(v_ref - Cfg::kLift) : 0.f;  // one after the other: their product may be below binary32
             const float l2 = none ? -attn_inf() : m + log2f(l);
             const long long at = (long long)sg.slot * a.tile_rows + t * rows + row;
 #pragma unroll 1
@@ -733,7 +736,7 @@ __global__ void __launch_bounds__(CacheTcCfg<F, NQ, NC>::kThreads, 1)
                 const uint32_t most = max(max(all.x, all.y), max(all.z, all.w));
                 if (row == 0) {
                     if (kv) sy.v_top[gi & 7] = most;
-                    else sy.k_scale[gi & 7] = cache_scale(most);
+                    else sy.k_scale[gi & 7] = most > Cfg::kLift ? cache_scale(most - Cfg::kLift) : 0.f;
                 }
                 const int idx = 2 * gi + kv, st = idx % ST;
                 unsigned char* to = ring + st * Cfg::kTileBytes + row * 128;
@@ -742,10 +745,10 @@ __global__ void __launch_bounds__(CacheTcCfg<F, NQ, NC>::kThreads, 1)
                     if (!tc_bar_wait(tc_smem(&sy.raw_full[rs]), (ri / Cfg::kRaw) & 1, abort, err)) return false;
                     if (idx >= ST && !tc_bar_wait(tc_smem(&sy.empty[st]), (idx / ST - 1) & 1, abort, err)) return false;
                     const unsigned char* from = raw + rs * Cfg::kRawBytes + row * (NC * 64);
-                    // 2^(byte - most) in f16; a row that held no numbers: NaN; byte 0: zeros
+                    // 2^(byte - most + lift) in f16; a row that held no numbers: NaN; byte 0: zeros
                     const int below = (int)(most - byte);
                     const bool far = below > apart && byte != 0u;  // goes in at its own scale
-                    const float f = byte == 255u ? __uint_as_float(0x7fffffffu) : far ? 1.f : byte == 0u || below > 126 ? 0.f : cache_scale(127 - below);
+                    const float f = byte == 255u ? __uint_as_float(0x7fffffffu) : far ? cache_scale(127 + Cfg::kLift) : byte == 0u || below > 126 ? 0.f : cache_scale(127 + Cfg::kLift - below);
                     const __half2 scale = __half2half2(__float2half_rn(f));
                     const __half2 off = __hmul2(scale, __half2half2(__ushort_as_half(0xe480)));  // -1152
 #pragma unroll 1
@@ -789,7 +792,7 @@ __global__ void __launch_bounds__(CacheTcCfg<F, NQ, NC>::kThreads, 1)
                     if (idx >= ST && !tc_bar_wait(tc_smem(&sy.empty[st]), (idx / ST - 1) & 1, abort, err)) return false;
                     const T* p = fresh + j * f_token;
                     const bool far = kv == 0 && there && byte + Cfg::kApartNew < most;
-                    const float f = most == 0u ? 0.f : cache_scale(254u - (far ? byte : most));
+                    const float f = most == 0u ? 0.f : cache_scale(254u + Cfg::kLift - (far ? byte : most));
 #pragma unroll 2
                     for (int d = 0; d < NC * 64; d += 8) {
                         uint4 y = make_uint4(0, 0, 0, 0);
