@@ -10,8 +10,8 @@ pytestmark = pytest.mark.gpu
 
 
 def keys(g, shape, dtype, far):
-    """Every third row (at random) has one channel of 2^far, which the queries do not have, and nothing else; the others
-    are normal in channels 16 to 31, a few of them 2^-far / 2 of that."""
+    """Three rows in ten (at random) have one channel of 2^far, which the queries do not have, and nothing else; the others are
+    normal in channels 16 to 31."""
     B, S, N, D = shape
     k = torch.zeros(shape, device=DEV)
     k[..., 16:32] = torch.randn((B, S, N, 16), generator=g, device=DEV)
@@ -43,7 +43,7 @@ def test_scales_within_a_tile(msda, far, T, fmt, dtype):  # noqa: F811
     q = q.to(C.DT[dtype])
     lengths = ints(S, 333)
     out, lse = compare(msda, q, cache, table, lengths)
-    assert (out.float().std(1).min() > 0) if T > 1 else True
+    assert T == 1 or out.float().std(1).min() > 0
     key = (keys(g, (B, T, N, D), "f32", far) / up).to(C.DT[dtype])
     value = normal(g, (B, T, N, D), C.DT[dtype])
     compare(msda, q, cache, table, lengths, key, value)

@@ -1,6 +1,4 @@
 """Rows in which one key of the paged cache outweighs every other and the others still make the output."""
-import math
-
 import pytest
 
 import dense_reference as R
@@ -83,4 +81,3 @@ def test_scores_that_fall_and_rise(msda, T, fmt, dtype):  # noqa: F811
     table = table_of(g, B, 125, 260)
     msda.cache_write(cache, k.to(C.DT[dtype]), v.to(C.DT[dtype]), table, ints(0, 0))
     check(msda, q.to(C.DT[dtype]), cache, table, ints(S, 1999), dtype, fmt)
-    assert math.isfinite(float(v.sum()))
